@@ -11,6 +11,8 @@ The same names as the C ABI:
     gemm_f8e4m3_tn_dscale(M, N, K, A, lda, B, ldb, C, ldc, scale_a_ptr, scale_b_ptr, stream=None)
     gemm_quantize_e4m3(x, x_type, rows, cols, ldx, q, ldq, scale_ptr, stream=None)
     gemm_f16_tn_softmax_stats(M, N, K, A, lda, B, ldb, C, ldc, scale, row_max, row_sum, stream=None)
+    gemm_tn_grouped / gemm_tn_grouped_grad_b / gemm_tn_grouped_grad_a / gemm_i8_tn / gemm_i8_tn_grouped /
+        gemm_quantize_i8_rows: products grouped by expert with their gradients, 8-bit integer products, row quantiser
     gemm_poll_device_status(stream=None)
 
 A, B and C are device pointers given as ints or as CUDA torch tensors (their
@@ -27,6 +29,9 @@ status other than GEMM_OK raises GemmError.
 Convenience wrappers over torch tensors in TN storage:
     f16_tn(A (M,K) fp16, Bt (N,K) fp16, C=None) -> C^T as an (N, M) fp16 tensor
     f8e4m3_tn(A (M,K) uint8/float8_e4m3fn, Bt (N,K), scale_a, scale_b, C=None) -> (N, M) bf16
+    tn_grouped(A (E,M,K), Bt (T,K), offsets (E+1,) int32, C=None) -> (T, M); tn_grouped_grad_b, tn_grouped_grad_a
+    i8_tn(A (M,K) int8, Bt (N,K) int8, scale_a (M,), scale_b (N,), C=None) -> (N, M); i8_tn_grouped
+    quantize_i8_rows(x (rows, cols)) -> (int8 codes, scale (rows,))
 The (N, M) row-major result IS the column-major M x N matrix C with ldc = M.
 """
 from __future__ import annotations
@@ -54,11 +59,18 @@ EXPORTS = (
     "gemm_debug_set_skinny_mode",
     "gemm_debug_set_clock_probe",
     "gemm_f8e4m3_tn_dscale", "gemm_quantize_e4m3", "gemm_f16_tn_softmax_stats",
+    "gemm_grouped_workspace", "gemm_tn_grouped", "gemm_tn_grouped_grad_b", "gemm_tn_grouped_grad_a",
+    "gemm_i8_tn", "gemm_i8_tn_grouped", "gemm_quantize_i8_rows",
 )
 
 GEMM_IN_F32 = 0
 GEMM_IN_F16 = 1
 GEMM_IN_BF16 = 2
+
+GEMM_GROUPED_PRODUCT = 0
+GEMM_GROUPED_GRAD_B = 1
+GEMM_GROUPED_GRAD_A = 2
+GEMM_GROUPED_I8 = 3
 
 
 class GemmError(RuntimeError):
@@ -87,6 +99,20 @@ def _load() -> ctypes.CDLL:
     lib.gemm_quantize_e4m3.restype = st
     lib.gemm_f16_tn_noalloc.argtypes = [i64, i64, i64, vp, i64, vp, i64, vp, i64, vp]
     lib.gemm_f16_tn_noalloc.restype = st
+    lib.gemm_grouped_workspace.argtypes = [st, i64, i64, i64, i64, vp, i64, i64, vp, i64]
+    lib.gemm_grouped_workspace.restype = i64
+    lib.gemm_tn_grouped.argtypes = [st, i64, i64, i64, i64, vp, i64, i64, vp, i64, vp, vp, i64, vp, i64, vp]
+    lib.gemm_tn_grouped.restype = st
+    lib.gemm_tn_grouped_grad_b.argtypes = [st, i64, i64, i64, i64, vp, i64, i64, vp, i64, vp, vp, i64, vp, i64, vp]
+    lib.gemm_tn_grouped_grad_b.restype = st
+    lib.gemm_tn_grouped_grad_a.argtypes = [st, i64, i64, i64, i64, vp, i64, vp, i64, vp, vp, i64, i64, vp, i64, vp]
+    lib.gemm_tn_grouped_grad_a.restype = st
+    lib.gemm_i8_tn.argtypes = [st, i64, i64, i64, vp, i64, vp, vp, i64, vp, vp, i64, vp, i64, vp]
+    lib.gemm_i8_tn.restype = st
+    lib.gemm_i8_tn_grouped.argtypes = [st, i64, i64, i64, i64, vp, i64, i64, vp, vp, i64, vp, vp, vp, i64, vp, i64, vp]
+    lib.gemm_i8_tn_grouped.restype = st
+    lib.gemm_quantize_i8_rows.argtypes = [vp, st, i64, i64, i64, vp, i64, vp, vp]
+    lib.gemm_quantize_i8_rows.restype = st
     lib.gemm_status_string.argtypes = [st]
     lib.gemm_status_string.restype = ctypes.c_char_p
     lib.gemm_last_error.argtypes = []
@@ -204,6 +230,53 @@ def gemm_quantize_e4m3(x, x_type, rows, cols, ldx, q, ldq, scale, stream=None) -
     """Per-tensor E4M3 quantisation on the device: codes into q, amax / 448 into *scale."""
     return _check(calls.gemm_quantize_e4m3(_ptr(x), int(x_type), rows, cols, ldx, _ptr(q), ldq, _ptr(scale),
                                            _stream(stream)))
+
+
+def gemm_grouped_workspace(op, E, M, K, T, X, ldx, stride_x, Y, ldy) -> int:
+    """Workspace bytes that a grouped or 8-bit product with these operands needs."""
+    n = calls.gemm_grouped_workspace(int(op), E, M, K, T, _ptr(X), ldx, stride_x, _ptr(Y), ldy)
+    if n < 0:
+        raise ValueError("gemm_grouped_workspace: argument out of range")
+    return n
+
+
+def gemm_tn_grouped(type, E, M, K, T, A, lda, stride_a, B, ldb, offsets, C, ldc, workspace=None, workspace_bytes=0,
+                    stream=None) -> int:
+    return _check(calls.gemm_tn_grouped(int(type), E, M, K, T, _ptr(A), lda, stride_a, _ptr(B), ldb, _ptr(offsets),
+                                        _ptr(C), ldc, _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def gemm_tn_grouped_grad_b(type, E, M, K, T, A, lda, stride_a, dC, lddc, offsets, dB, lddb, workspace=None,
+                           workspace_bytes=0, stream=None) -> int:
+    return _check(calls.gemm_tn_grouped_grad_b(int(type), E, M, K, T, _ptr(A), lda, stride_a, _ptr(dC), lddc,
+                                               _ptr(offsets), _ptr(dB), lddb, _ptr(workspace), workspace_bytes,
+                                               _stream(stream)))
+
+
+def gemm_tn_grouped_grad_a(type, E, M, K, T, dC, lddc, B, ldb, offsets, dA, ldda, stride_da, workspace=None,
+                           workspace_bytes=0, stream=None) -> int:
+    return _check(calls.gemm_tn_grouped_grad_a(int(type), E, M, K, T, _ptr(dC), lddc, _ptr(B), ldb, _ptr(offsets),
+                                               _ptr(dA), ldda, stride_da, _ptr(workspace), workspace_bytes,
+                                               _stream(stream)))
+
+
+def gemm_i8_tn(out_type, M, N, K, A, lda, scale_a, B, ldb, scale_b, C, ldc, workspace=None, workspace_bytes=0,
+               stream=None) -> int:
+    return _check(calls.gemm_i8_tn(int(out_type), M, N, K, _ptr(A), lda, _ptr(scale_a), _ptr(B), ldb, _ptr(scale_b),
+                                   _ptr(C), ldc, _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def gemm_i8_tn_grouped(out_type, E, M, K, T, A, lda, stride_a, scale_a, B, ldb, scale_b, offsets, C, ldc,
+                       workspace=None, workspace_bytes=0, stream=None) -> int:
+    return _check(calls.gemm_i8_tn_grouped(int(out_type), E, M, K, T, _ptr(A), lda, stride_a, _ptr(scale_a), _ptr(B),
+                                           ldb, _ptr(scale_b), _ptr(offsets), _ptr(C), ldc, _ptr(workspace),
+                                           workspace_bytes, _stream(stream)))
+
+
+def gemm_quantize_i8_rows(x, x_type, rows, cols, ldx, q, ldq, scale, stream=None) -> int:
+    """8-bit quantisation with a scale per row: codes into q, amax / 127 of each row into scale."""
+    return _check(calls.gemm_quantize_i8_rows(_ptr(x), int(x_type), rows, cols, ldx, _ptr(q), ldq, _ptr(scale),
+                                              _stream(stream)))
 
 
 def gemm_f16_tn_noalloc(M, N, K, A, lda, B, ldb, C, ldc, stream=None) -> int:
@@ -411,3 +484,188 @@ def f8e4m3_tn(A, Bt, scale_a, scale_b, C=None, stream=None):
     with _on(A.device):
         gemm_f8e4m3_tn(M, N, K, A, lda, Bt, ldb, C, ldc, float(scale_a), float(scale_b), stream)
     return C
+
+
+# ---------------------------------------------------------------- grouped and 8-bit products
+def _half_type(dtype, name):
+    import torch
+    if dtype == torch.bfloat16:
+        return GEMM_IN_BF16
+    if dtype == torch.float16:
+        return GEMM_IN_F16
+    raise ValueError(f"{name} must be torch.float16 or torch.bfloat16, not {dtype}")
+
+
+def _experts(t, dtype, name, shape=None):
+    """(row stride, expert stride) of a 3-D tensor (E, rows, inner) with contiguous rows."""
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dim() != 3:
+        raise ValueError(f"{name} must be a 3-D torch tensor (experts, rows, columns)")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    E, R, I = t.shape
+    if shape is not None and (E, R, I) != shape:
+        raise ValueError(f"{name} must have shape {shape}, not {(E, R, I)}")
+    s0, s1, s2 = t.stride()
+    if I > 1 and s2 != 1 and t.numel() > 0:
+        raise ValueError(f"{name} must have unit stride along its last dimension")
+    return (s1 if R > 1 else max(I, 1)), (s0 if E > 1 else 0)
+
+
+def _vector(t, dtype, n, name):
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape ({n},)")
+
+
+def _same_device(device, tensors):
+    if device.type != "cuda":
+        raise ValueError("the tensors must be CUDA tensors")
+    for name, t in tensors.items():
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
+def _call(device, stream, op, sizes, X, ldx, stride_x, Y, ldy, launch):
+    """launch(workspace, bytes, stream) on `device`, with a workspace from torch's
+    allocator that belongs to the stream (so that it is used again only after
+    this call's kernels)."""
+    import torch
+    if torch.cuda.current_device() != device.index:
+        with torch.cuda.device(device):
+            return _call(device, stream, op, sizes, X, ldx, stride_x, Y, ldy, launch)
+    n = gemm_grouped_workspace(op, *sizes, X, ldx, stride_x, Y, ldy)
+    if n == 0:
+        return launch(None, 0, stream)
+    if stream is None:
+        return launch(torch.empty(n, dtype=torch.uint8, device=device), n, None)
+    own = stream if not isinstance(stream, int) else torch.cuda.ExternalStream(stream, device=device)
+    with torch.cuda.stream(own):
+        workspace = torch.empty(n, dtype=torch.uint8, device=device)
+    return launch(workspace, n, stream)
+
+
+def _offsets(offsets, E):
+    import torch
+    _vector(offsets, torch.int32, E + 1, "offsets")
+
+
+def tn_grouped(A, Bt, offsets, C=None, stream=None):
+    """C^T[t] = A[e] Bt[t] for the rows offsets[e] <= t < offsets[e + 1] of every
+    expert e: A (E, M, K), Bt (T, K), offsets (E + 1,) int32, all on one GPU;
+    A, Bt and C (T, M) are all fp16 or all bf16, their rows contiguous.  Rows of
+    no expert are not written."""
+    import torch
+    kind = _half_type(A.dtype, "A")
+    lda, stride_a = _experts(A, A.dtype, "A")
+    E, M, K = A.shape
+    ldb = _rows(Bt, A.dtype, "Bt", (Bt.shape[0], K) if isinstance(Bt, torch.Tensor) and Bt.dim() == 2 else None, cuda=False)
+    T = Bt.shape[0]
+    _offsets(offsets, E)
+    _same_device(A.device, {"A": A, "Bt": Bt, "offsets": offsets})
+    C, ldc = _output(C, M, T, A.dtype, A.device)
+    _call(A.device, stream, GEMM_GROUPED_PRODUCT, (E, M, K, T), A, lda, stride_a, Bt, ldb,
+          lambda ws, n, s: gemm_tn_grouped(kind, E, M, K, T, A, lda, stride_a, Bt, ldb, offsets, C, ldc, ws, n, s))
+    return C
+
+
+def tn_grouped_grad_b(A, dCt, offsets, dBt=None, stream=None):
+    """The gradient of tn_grouped for Bt: dBt[t] = A[e]^T dC^T[t], with dCt (T, M)
+    -> (T, K).  Rows of no expert are not written."""
+    import torch
+    kind = _half_type(A.dtype, "A")
+    lda, stride_a = _experts(A, A.dtype, "A")
+    E, M, K = A.shape
+    ldd = _rows(dCt, A.dtype, "dCt", (dCt.shape[0], M) if isinstance(dCt, torch.Tensor) and dCt.dim() == 2 else None, cuda=False)
+    T = dCt.shape[0]
+    _offsets(offsets, E)
+    _same_device(A.device, {"A": A, "dCt": dCt, "offsets": offsets})
+    if dBt is None:
+        dBt = torch.empty((T, K), dtype=A.dtype, device=A.device)
+    ldb = _rows(dBt, A.dtype, "dBt", (T, K))
+    _same_device(A.device, {"dBt": dBt})
+    _call(A.device, stream, GEMM_GROUPED_GRAD_B, (E, M, K, T), A, lda, stride_a, dCt, ldd,
+          lambda ws, n, s: gemm_tn_grouped_grad_b(kind, E, M, K, T, A, lda, stride_a, dCt, ldd, offsets, dBt, ldb, ws,
+                                                  n, s))
+    return dBt
+
+
+def tn_grouped_grad_a(dCt, Bt, offsets, dA=None, stream=None):
+    """The gradient of tn_grouped for A: dA[e] = sum over e's rows t of the outer
+    products dC^T[t] Bt[t], with dCt (T, M) and Bt (T, K) -> (E, M, K); zeros for
+    an expert without rows."""
+    import torch
+    if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.shape[0] < 1:
+        raise ValueError("offsets must be a 1-D tensor of experts + 1 rows")
+    kind = _half_type(dCt.dtype, "dCt")
+    ldd = _rows(dCt, dCt.dtype, "dCt", cuda=False)
+    T, M = dCt.shape
+    ldb = _rows(Bt, dCt.dtype, "Bt", (T, Bt.shape[1]) if isinstance(Bt, torch.Tensor) and Bt.dim() == 2 else None, cuda=False)
+    K, E = Bt.shape[1], offsets.shape[0] - 1
+    _offsets(offsets, E)
+    _same_device(dCt.device, {"dCt": dCt, "Bt": Bt, "offsets": offsets})
+    if dA is None:
+        dA = torch.empty((E, M, K), dtype=dCt.dtype, device=dCt.device)
+    ldda, stride_da = _experts(dA, dCt.dtype, "dA", (E, M, K))
+    _same_device(dCt.device, {"dA": dA})
+    _call(dCt.device, stream, GEMM_GROUPED_GRAD_A, (E, M, K, T), dCt, ldd, 0, Bt, ldb,
+          lambda ws, n, s: gemm_tn_grouped_grad_a(kind, E, M, K, T, dCt, ldd, Bt, ldb, offsets, dA, ldda, stride_da, ws,
+                                                  n, s))
+    return dA
+
+
+def i8_tn(A, Bt, scale_a, scale_b, C=None, dtype=None, stream=None):
+    """C^T[n, m] = scale_a[m] scale_b[n] sum_k A[m, k] Bt[n, k]: A (M, K) and Bt
+    (N, K) int8, scale_a (M,) and scale_b (N,) fp32 -> (N, M) of `dtype`
+    (torch.float16 unless C or dtype says torch.bfloat16)."""
+    import torch
+    M, N, K, lda, ldb = _operands(A, Bt, torch.int8)
+    _vector(scale_a, torch.float32, M, "scale_a")
+    _vector(scale_b, torch.float32, N, "scale_b")
+    dtype = dtype or (torch.float16 if C is None else C.dtype)
+    kind = _half_type(dtype, "dtype")
+    _same_device(A.device, {"scale_a": scale_a, "scale_b": scale_b})
+    C, ldc = _output(C, M, N, dtype, A.device)
+    _call(A.device, stream, GEMM_GROUPED_I8, (1, M, K, N), A, lda, 0, Bt, ldb,
+          lambda ws, n, s: gemm_i8_tn(kind, M, N, K, A, lda, scale_a, Bt, ldb, scale_b, C, ldc, ws, n, s))
+    return C
+
+
+def i8_tn_grouped(A, Bt, scale_a, scale_b, offsets, C=None, dtype=None, stream=None):
+    """i8_tn grouped by expert as in tn_grouped: A (E, M, K) and Bt (T, K) int8,
+    scale_a (E, M) and scale_b (T,) fp32 -> (T, M) of `dtype`."""
+    import torch
+    lda, stride_a = _experts(A, torch.int8, "A")
+    E, M, K = A.shape
+    ldb = _rows(Bt, torch.int8, "Bt", (Bt.shape[0], K) if isinstance(Bt, torch.Tensor) and Bt.dim() == 2 else None, cuda=False)
+    T = Bt.shape[0]
+    if not isinstance(scale_a, torch.Tensor) or scale_a.shape != (E, M):
+        raise ValueError(f"scale_a must have shape {(E, M)}")
+    _vector(scale_a.reshape(-1) if scale_a.is_contiguous() else scale_a, torch.float32, E * M, "scale_a")
+    _vector(scale_b, torch.float32, T, "scale_b")
+    _offsets(offsets, E)
+    _same_device(A.device, {"Bt": Bt, "scale_a": scale_a, "scale_b": scale_b, "offsets": offsets})
+    dtype = dtype or (torch.float16 if C is None else C.dtype)
+    kind = _half_type(dtype, "dtype")
+    C, ldc = _output(C, M, T, dtype, A.device)
+    _call(A.device, stream, GEMM_GROUPED_I8, (E, M, K, T), A, lda, stride_a, Bt, ldb,
+          lambda ws, n, s: gemm_i8_tn_grouped(kind, E, M, K, T, A, lda, stride_a, scale_a, Bt, ldb, scale_b, offsets, C,
+                                              ldc, ws, n, s))
+    return C
+
+
+def quantize_i8_rows(x, stream=None):
+    """x: a 2-D float32 / float16 / bfloat16 CUDA tensor with unit column stride.
+    Returns (int8 codes of x's shape, scale as a float32 tensor of its rows): the
+    operands of i8_tn, for activations (tokens) and weights (channels) alike."""
+    import torch
+    types = {torch.float32: GEMM_IN_F32, torch.float16: GEMM_IN_F16, torch.bfloat16: GEMM_IN_BF16}
+    if not isinstance(x, torch.Tensor) or x.dtype not in types or x.dim() != 2:
+        raise ValueError("x must be a 2-D float32/float16/bfloat16 tensor")
+    ldx = _rows(x, x.dtype, "x")
+    rows, cols = x.shape
+    q = torch.empty((rows, cols), dtype=torch.int8, device=x.device)
+    scale = torch.empty(rows, dtype=torch.float32, device=x.device)
+    with _on(x.device):
+        gemm_quantize_i8_rows(x, types[x.dtype], rows, cols, ldx, q, max(cols, 1), scale, stream)
+    return q, scale

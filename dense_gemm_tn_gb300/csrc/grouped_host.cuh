@@ -1,0 +1,403 @@
+// Host side of the products grouped by expert, the 8-bit integer products and
+// the row quantiser (included by tn_gemm.cu, inside its anonymous namespace).
+//
+// These calls keep nothing in the library: operand copies and grad_a's tensor
+// maps go into a workspace that the caller passes, so calls on any streams,
+// from any threads, and graphs captured from them share no buffer unless the
+// caller gives them the same one.
+
+struct GroupedCall {
+    const char *name;
+    int op;                       // gemm_grouped_op_t
+    int type, out_type;           // operands (16-bit ones) and result
+    int64_t E, M, K, T;
+    const void *X;                // A, or grad_a's dC
+    int64_t ldx, stride_x;
+    const void *Y;                // B, or grad_b's dC
+    int64_t ldy;
+    const int32_t *offsets;
+    void *out;
+    int64_t ldo, stride_o;
+    const float *scale_a, *scale_b;
+    void *workspace;
+    int64_t workspace_bytes;
+    cudaStream_t stream;
+    bool needs_offsets = false;
+};
+
+// An operand as `blocks` matrices of rows x inner elements, and whether it is
+// copied first: the 8-bit ones always (widened to f16), the 16-bit ones when
+// the TMA cannot address them in place -- base, row stride or block stride not
+// a multiple of 16 bytes, or the sum's index contiguous and its extent not one
+// (a row that ends inside a 16-byte unit is not clipped element by element) --
+// or when the blocks interleave or repeat (a block stride below a row's).
+struct GroupedOperand {
+    const void *base;
+    int64_t rows, blocks, inner, ld, stride;
+    bool copy;
+    int64_t copy_ld;              // elements
+    size_t copy_bytes;
+};
+
+GroupedOperand grouped_operand(const void *base, int64_t rows, int64_t blocks, int64_t inner, int64_t ld,
+                               int64_t stride, bool inner_is_sum, bool i8)
+{
+    GroupedOperand o{base, rows, blocks, inner, ld, stride, i8, 0, 0};
+    if (!i8)
+        o.copy = reinterpret_cast<uintptr_t>(base) % 16 || ld % 8 || (blocks > 1 && (stride % 8 || stride < ld)) ||
+                 (inner_is_sum && inner % 8);
+    if (o.copy) {
+        o.copy_ld = (inner + 63) / 64 * 64;
+        o.copy_bytes = size_t(rows) * size_t(blocks) * size_t(o.copy_ld) * 2;
+        o.copy_bytes = (o.copy_bytes + 255) & ~size_t(255);
+    }
+    return o;
+}
+
+struct GroupedPlan {
+    GroupedOperand x, y;
+    size_t map_bytes;             // grad_a: two tensor maps per expert
+    size_t bytes() const { return x.copy_bytes + y.copy_bytes + map_bytes; }
+};
+
+bool grouped_sizes_fit(int64_t E, int64_t M, int64_t K, int64_t T, int64_t ldx, int64_t ldy, int64_t stride)
+{
+    return E <= tn::kGrMaxExperts && M <= kMaxDim && K <= kMaxDim && T <= kMaxDim && ldx <= kMaxDim && ldy <= kMaxDim &&
+           stride <= (int64_t(1) << 38);
+}
+
+// Nothing to read: the sum, or the result, is empty.
+bool grouped_idle(int64_t E, int64_t M, int64_t K, int64_t T) { return E == 0 || M == 0 || K == 0 || T == 0; }
+
+GroupedPlan grouped_plan(int op, int64_t E, int64_t M, int64_t K, int64_t T, const void *X, int64_t ldx,
+                         int64_t stride_x, const void *Y, int64_t ldy)
+{
+    GroupedPlan g{};
+    if (grouped_idle(E, M, K, T)) return g;
+    const bool i8 = op == GEMM_GROUPED_I8;
+    if (op == GEMM_GROUPED_GRAD_A) {
+        g.x = grouped_operand(X, T, 1, M, ldx, 0, false, false);
+        g.y = grouped_operand(Y, T, 1, K, ldy, 0, false, false);
+        g.map_bytes = size_t(E) * 2 * sizeof(CUtensorMap);
+    } else {
+        const bool grad_b = op == GEMM_GROUPED_GRAD_B;
+        g.x = grouped_operand(X, M, E, K, ldx, stride_x, !grad_b, i8);
+        g.y = grouped_operand(Y, T, 1, grad_b ? M : K, ldy, 0, true, i8);
+    }
+    return g;
+}
+
+int64_t grouped_workspace(int op, int64_t E, int64_t M, int64_t K, int64_t T, const void *X, int64_t ldx,
+                          int64_t stride_x, const void *Y, int64_t ldy)
+{
+    if (op < GEMM_GROUPED_PRODUCT || op > GEMM_GROUPED_I8 || E < 0 || M < 0 || K < 0 || T < 0 || ldx < 0 || ldy < 0 ||
+        stride_x < 0 || !grouped_sizes_fit(E, M, K, T, ldx, ldy, stride_x))
+        return -1;
+    return static_cast<int64_t>(grouped_plan(op, E, M, K, T, X, ldx, stride_x, Y, ldy).bytes());
+}
+
+template <typename Src>
+gemm_status_t launch_widen(const char *name, DeviceState &dev, const GroupedOperand &o, uint16_t *dst,
+                           cudaStream_t stream)
+{
+    const tn::WidenJob<Src> j{static_cast<const Src *>(o.base), o.ld,       o.stride, dst, o.copy_ld, o.rows,
+                              o.rows * o.blocks,                o.inner};
+    int64_t blocks = (j.rows * (j.ld_dst / 8) + tn::kWidenThreads - 1) / tn::kWidenThreads;
+    if (blocks > int64_t(dev.sms) * 64) blocks = int64_t(dev.sms) * 64;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
+    cfg.blockDim = dim3(tn::kWidenThreads, 1, 1);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, tn::widen_rows_kernel<Src>, j);
+    if (e != cudaSuccess) return fail(GEMM_ERR_CUDA, "%s: launch (operand copy): %s", name, cudaGetErrorString(e));
+    return GEMM_OK;
+}
+
+template <int kOp, int kGroup, int kRows>
+gemm_status_t launch_grouped(const GroupedCall &c, DeviceState &dev, tn::GroupedParams &prm, int variant)
+{
+    using Cfg = tn::GroupedCfg<kGroup, kRows>;
+    auto kernel = tn::tn_grouped_kernel<kOp, kGroup, kRows>;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = kGroup;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.blockDim = dim3(tn::kThreads, 1, 1);
+    cfg.dynamicSmemBytes = Cfg::kSmemBytes;
+    int slots;
+    {
+        std::lock_guard<std::mutex> lock(g_mutex);
+        int &n = dev.grouped_slots[kOp][variant];
+        if (n == 0) {
+            cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmemBytes);
+            if (e != cudaSuccess) return fail(GEMM_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+            int found = dev.sms;
+            if (kGroup == 2) {
+                cfg.attrs = attr + 1;
+                cfg.numAttrs = 1;
+                cfg.gridDim = dim3(kGroup * (dev.sms / kGroup), 1, 1);
+                e = cudaOccupancyMaxActiveClusters(&found, kernel, &cfg);
+                if (e != cudaSuccess || found <= 0) {
+                    cudaGetLastError();
+                    found = dev.sms / kGroup;
+                }
+            }
+            n = found;
+        }
+        slots = n;
+    }
+    const int64_t l_tiles = (int64_t(prm.l_extent) + Cfg::kTileL - 1) / Cfg::kTileL;
+    const int64_t r_tiles = kOp == tn::kGrGradA ? c.E * ((c.M + kRows - 1) / kRows)
+                                                : c.T / kRows + (c.E < c.T ? c.E : c.T);   // an upper bound
+    if (r_tiles > (int64_t(1) << 30) / l_tiles) return fail(GEMM_ERR_UNSUPPORTED, "%s: too many output tiles", c.name);
+    const int64_t tiles = r_tiles * l_tiles;
+    const int grid = static_cast<int>(tiles < slots ? tiles : slots) * kGroup;
+    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+    cfg.stream = c.stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = kGroup == 2 ? 2 : 1;
+    t_rec = LaunchRecord{};
+    t_rec.name = c.name;
+    t_rec.grouped = 1;
+    t_rec.cluster = kGroup;
+    t_rec.grid = grid;
+    t_rec.slots = slots;
+    t_rec.tiles = static_cast<int>(tiles);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, prm);
+    if (e != cudaSuccess) return fail(GEMM_ERR_CUDA, "%s: launch: %s", c.name, cudaGetErrorString(e));
+    return GEMM_OK;
+}
+
+template <int kOp>
+gemm_status_t launch_grouped_op(const GroupedCall &c, DeviceState &dev, tn::GroupedParams &prm,
+                                const void *x, const void *y, int64_t ldx, int64_t stride_x, int64_t ldy,
+                                int64_t inner_x, int64_t inner_y)
+{
+    // Few rows per expert: bound by the read of the weights, on single CTAs of
+    // 128 x 64 tiles (twice as many of them, and a deeper ring); else CTA pairs.
+    const bool few = kOp != tn::kGrGradA && c.T <= 64 * c.E;
+    const uint32_t rows_r = few ? 64 : 128;
+    gemm_status_t st;
+    if (prm.red > 0) {
+        const CUtensorMapDataType type =
+            prm.fmt ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+        if constexpr (kOp == tn::kGrGradA) {
+            tn::GroupedMapsParams m;
+            memset(&m, 0, sizeof(m));
+            if ((st = encode_2d(&m.dc, type, x, inner_x, c.T, ldx * 2, 64, tn::kGrBlock, "dC")) != GEMM_OK) return st;
+            if ((st = encode_2d(&m.b, type, y, inner_y, c.T, ldy * 2, 64, tn::kGrBlock, "B")) != GEMM_OK) return st;
+            m.maps = const_cast<CUtensorMap *>(prm.group_maps);
+            m.offsets = prm.offsets;
+            m.dc_base = static_cast<const uint8_t *>(x);
+            m.b_base = static_cast<const uint8_t *>(y);
+            m.dc_row_bytes = ldx * 2;
+            m.b_row_bytes = ldy * 2;
+            m.E = prm.E;
+            m.T = prm.T;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            attr[0].val.programmaticStreamSerializationAllowed = 1;
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(static_cast<unsigned>(2 * c.E), 1, 1);
+            cfg.blockDim = dim3(32, 1, 1);
+            cfg.stream = c.stream;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            cudaError_t e = cudaLaunchKernelEx(&cfg, tn::grouped_maps_kernel, m);
+            if (e != cudaSuccess) return fail(GEMM_ERR_CUDA, "%s: launch (tensor maps): %s", c.name, cudaGetErrorString(e));
+        } else {
+            const uint32_t box_l = kOp == tn::kGrProduct ? 128 : 64;
+            const uint64_t apart = c.E > 1 ? uint64_t(stride_x) * 2 : uint64_t(16);
+            if ((st = encode_map(&prm.tmap_l, type, x, inner_x, c.M, ldx * 2, c.E, apart, 64, box_l, "A")) != GEMM_OK)
+                return st;
+            if ((st = encode_2d(&prm.tmap_r, type, y, inner_y, c.T, ldy * 2, 64, rows_r, "rows")) != GEMM_OK) return st;
+            if ((st = encode_2d(&prm.tmap_r16, type, y, inner_y, c.T, ldy * 2, 64, 16, "rows")) != GEMM_OK) return st;
+        }
+    }
+    if constexpr (kOp != tn::kGrGradA) {
+        if (few) return launch_grouped<kOp, 1, 64>(c, dev, prm, 0);
+    }
+    return launch_grouped<kOp, 2, 256>(c, dev, prm, 1);
+}
+
+gemm_status_t run_grouped(const GroupedCall &c)
+{
+    const char *name = c.name;
+    const bool i8 = c.op == GEMM_GROUPED_I8, grad_a = c.op == GEMM_GROUPED_GRAD_A, grad_b = c.op == GEMM_GROUPED_GRAD_B;
+    for (int t : {c.type, c.out_type})
+        if (t != GEMM_IN_F16 && t != GEMM_IN_BF16)
+            return fail(GEMM_ERR_INVALID_ARG, "%s: unknown or unsupported type %d (GEMM_IN_F16 or GEMM_IN_BF16)", name, t);
+    if (c.E < 0 || c.M < 0 || c.K < 0 || c.T < 0)
+        return fail(GEMM_ERR_INVALID_ARG, "%s: negative size (E=%lld M=%lld K=%lld rows=%lld)", name, (long long)c.E,
+                    (long long)c.M, (long long)c.K, (long long)c.T);
+    auto at_least = [](int64_t v) { return v > 1 ? v : int64_t(1); };
+    const int64_t inner_x = grad_a ? c.M : c.K, inner_y = grad_b ? c.M : c.K;
+    const int64_t inner_o = grad_a || grad_b ? c.K : c.M;
+    if (c.ldx < at_least(inner_x) || c.ldy < at_least(inner_y) || c.ldo < at_least(inner_o))
+        return fail(GEMM_ERR_INVALID_ARG, "%s: a leading dimension is below its row's length", name);
+    if (c.stride_x < 0 || c.stride_o < 0) return fail(GEMM_ERR_INVALID_ARG, "%s: negative stride", name);
+    if (!grouped_sizes_fit(c.E, c.M, c.K, c.T, c.ldx, c.ldy, c.stride_x > c.stride_o ? c.stride_x : c.stride_o) ||
+        c.ldo > kMaxDim)
+        return fail(GEMM_ERR_UNSUPPORTED, "%s: more than %d experts, or a size, leading dimension or stride too large", name,
+                    tn::kGrMaxExperts);
+    // the result is empty, or has no row that any expert could own
+    if (c.E == 0 || inner_o == 0 || (grad_a ? c.M == 0 : c.T == 0)) return GEMM_OK;
+    const int64_t red = grad_a ? c.T : (grad_b ? c.M : c.K);
+    if (!c.out) return fail(GEMM_ERR_INVALID_ARG, "%s: the result is NULL", name);
+    if (reinterpret_cast<uintptr_t>(c.out) % 2) return fail(GEMM_ERR_INVALID_ARG, "%s: the result is not 2-byte aligned", name);
+    if (grad_a && c.E > 1 && c.stride_o < (c.M - 1) * c.ldo + c.K && c.ldo < (c.E - 1) * c.stride_o + c.K)
+        return fail(GEMM_ERR_INVALID_ARG, "%s: the experts' results overlap", name);
+    const uintptr_t misfit = i8 ? 0 : 1;
+    if (red > 0) {
+        if (!c.X || !c.Y) return fail(GEMM_ERR_INVALID_ARG, "%s: an operand is NULL", name);
+        if ((reinterpret_cast<uintptr_t>(c.X) | reinterpret_cast<uintptr_t>(c.Y)) & misfit)
+            return fail(GEMM_ERR_INVALID_ARG, "%s: an operand is not aligned to its element size", name);
+    }
+    const bool dense = i8 && !c.needs_offsets;
+    if (!dense) {
+        if (!c.offsets) return fail(GEMM_ERR_INVALID_ARG, "%s: offsets is NULL", name);
+        if (reinterpret_cast<uintptr_t>(c.offsets) % 4)
+            return fail(GEMM_ERR_INVALID_ARG, "%s: offsets is not 4-byte aligned", name);
+    }
+    if (i8) {
+        if (!c.scale_a || !c.scale_b) return fail(GEMM_ERR_INVALID_ARG, "%s: a scale pointer is NULL", name);
+        if ((reinterpret_cast<uintptr_t>(c.scale_a) | reinterpret_cast<uintptr_t>(c.scale_b)) % 4)
+            return fail(GEMM_ERR_INVALID_ARG, "%s: a scale pointer is not 4-byte aligned", name);
+    }
+    const GroupedPlan plan = grouped_plan(c.op, c.E, c.M, c.K, c.T, c.X, c.ldx, c.stride_x, c.Y, c.ldy);
+    if (plan.bytes() > 0) {
+        if (!c.workspace || c.workspace_bytes < static_cast<int64_t>(plan.bytes()))
+            return fail(GEMM_ERR_INVALID_ARG, "%s: the workspace has %lld bytes, %zu are needed (gemm_grouped_workspace)", name,
+                        (long long)(c.workspace ? c.workspace_bytes : 0), plan.bytes());
+        if (reinterpret_cast<uintptr_t>(c.workspace) % 256)
+            return fail(GEMM_ERR_INVALID_ARG, "%s: the workspace is not 256-byte aligned", name);
+    }
+    DeviceState *dev = nullptr;
+    gemm_status_t st = device_state(&dev, nullptr);
+    if (st != GEMM_OK) return st;
+
+    uint8_t *ws = static_cast<uint8_t *>(c.workspace);
+    const void *x = c.X, *y = c.Y;
+    int64_t ldx = c.ldx, stride_x = c.stride_x, ldy = c.ldy, in_x = inner_x, in_y = inner_y;
+    int copied = 0;
+    auto copy = [&](const GroupedOperand &o) {
+        uint16_t *dst = reinterpret_cast<uint16_t *>(ws);
+        ws += o.copy_bytes;
+        return i8 ? launch_widen<int8_t>(name, *dev, o, dst, c.stream) : launch_widen<uint16_t>(name, *dev, o, dst, c.stream);
+    };
+    if (plan.x.copy) {
+        x = ws;
+        if ((st = copy(plan.x)) != GEMM_OK) return st;
+        ldx = in_x = plan.x.copy_ld;
+        stride_x = plan.x.rows * ldx;
+        copied |= 1;
+    }
+    if (plan.y.copy) {
+        y = ws;
+        if ((st = copy(plan.y)) != GEMM_OK) return st;
+        ldy = in_y = plan.y.copy_ld;
+        copied |= 2;
+    }
+    tn::GroupedParams prm;
+    memset(&prm, 0, sizeof(prm));
+    prm.group_maps = reinterpret_cast<const CUtensorMap *>(ws);
+    prm.offsets = dense ? nullptr : c.offsets;
+    prm.out = static_cast<uint16_t *>(c.out);
+    prm.out_ld = c.ldo;
+    prm.out_stride = grad_a ? c.stride_o : 0;
+    prm.E = static_cast<int32_t>(c.E);
+    prm.T = static_cast<int32_t>(c.T);
+    prm.l_extent = static_cast<int32_t>(inner_o);
+    prm.r_extent = grad_a ? static_cast<int32_t>(c.M) : 0;
+    prm.red = static_cast<int32_t>(red);
+    prm.fmt = c.type == GEMM_IN_BF16 ? 1u : 0u;
+    prm.out_fmt = c.out_type == GEMM_IN_BF16 ? 1u : 0u;
+    prm.scale_l = c.scale_a;
+    prm.scale_r = c.scale_b;
+    prm.flags = stall_flags(g_inject_stall.load());
+    prm.wait_limit_ns = g_wait_limit_ns.load();
+    if (grad_a)
+        st = launch_grouped_op<tn::kGrGradA>(c, *dev, prm, x, y, ldx, stride_x, ldy, in_x, in_y);
+    else if (grad_b)
+        st = launch_grouped_op<tn::kGrGradB>(c, *dev, prm, x, y, ldx, stride_x, ldy, in_x, in_y);
+    else
+        st = launch_grouped_op<tn::kGrProduct>(c, *dev, prm, x, y, ldx, stride_x, ldy, in_x, in_y);
+    t_rec.copied = copied;
+    return st;
+}
+
+template <int kIn>
+gemm_status_t launch_quant_rows(DeviceState &dev, const qz::QuantRowsParams &prm, cudaStream_t stream)
+{
+    auto kernel = qz::quant_rows_kernel<kIn>;
+    int per_sm;
+    {
+        std::lock_guard<std::mutex> lock(g_mutex);
+        if (dev.quant_rows_blocks[kIn] == 0) {
+            int n = 0;
+            cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, qz::kRowThreads, 0);
+            if (e != cudaSuccess || n <= 0)
+                return fail(GEMM_ERR_CUDA, "gemm_quantize_i8_rows: occupancy query: %s", cudaGetErrorString(e));
+            dev.quant_rows_blocks[kIn] = n;
+        }
+        per_sm = dev.quant_rows_blocks[kIn];
+    }
+    int64_t grid = int64_t(per_sm) * dev.sms;
+    if (grid > prm.rows) grid = prm.rows;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+    cfg.blockDim = dim3(qz::kRowThreads, 1, 1);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    t_rec = LaunchRecord{};
+    t_rec.name = "gemm_quantize_i8_rows";
+    t_rec.quant = true;
+    t_rec.qgrid = grid;
+    t_rec.qunits = prm.rows;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, prm);
+    if (e != cudaSuccess) return fail(GEMM_ERR_CUDA, "gemm_quantize_i8_rows: launch: %s", cudaGetErrorString(e));
+    return GEMM_OK;
+}
+
+gemm_status_t run_quant_rows(const void *x, int x_type, int64_t rows, int64_t cols, int64_t ldx, int8_t *q, int64_t ldq,
+                             float *scale, cudaStream_t stream)
+{
+    const char *name = "gemm_quantize_i8_rows";
+    if (x_type < qz::kInF32 || x_type > qz::kInBF16)
+        return fail(GEMM_ERR_INVALID_ARG, "%s: unknown input type %d", name, x_type);
+    const int64_t esz = x_type == qz::kInF32 ? 4 : 2;
+    if (rows < 0 || cols < 0) return fail(GEMM_ERR_INVALID_ARG, "%s: negative size", name);
+    const int64_t cmin = cols > 1 ? cols : 1;
+    if (ldx < cmin || ldq < cmin) return fail(GEMM_ERR_INVALID_ARG, "%s: ldx or ldq < max(1, cols)", name);
+    if (rows == 0) return GEMM_OK;
+    if (!scale) return fail(GEMM_ERR_INVALID_ARG, "%s: scale is NULL", name);
+    if (reinterpret_cast<uintptr_t>(scale) % 4) return fail(GEMM_ERR_INVALID_ARG, "%s: scale is not 4-byte aligned", name);
+    if (cols > 0) {
+        if (!x || !q) return fail(GEMM_ERR_INVALID_ARG, "%s: x or q is NULL", name);
+        if (reinterpret_cast<uintptr_t>(x) % esz)
+            return fail(GEMM_ERR_INVALID_ARG, "%s: x is not aligned to its element size", name);
+    }
+    if (rows > (int64_t(1) << 40) / cmin) return fail(GEMM_ERR_UNSUPPORTED, "%s: more than 2^40 elements", name);
+    DeviceState *dev = nullptr;
+    gemm_status_t st = device_state(&dev, nullptr);
+    if (st != GEMM_OK) return st;
+    const qz::QuantRowsParams prm{x, q, scale, ldx, ldq, rows, cols};
+    switch (x_type) {
+    case qz::kInF32: return launch_quant_rows<qz::kInF32>(*dev, prm, stream);
+    case qz::kInF16: return launch_quant_rows<qz::kInF16>(*dev, prm, stream);
+    default: return launch_quant_rows<qz::kInBF16>(*dev, prm, stream);
+    }
+}

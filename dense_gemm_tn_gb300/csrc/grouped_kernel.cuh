@@ -1,0 +1,674 @@
+// tn_grouped_kernel: matrix products grouped by expert, ragged row ranges
+// given by offsets in device memory, with both gradients, and the 8-bit
+// integer product, which is the same kernel on operands widened to f16.
+//
+// Rows t of expert e are the ones with offsets[e] <= t < offsets[e + 1].
+//     product  C[t, m]     = sum_k A[e, m, k] B[t, k]
+//     grad_b   dB[t, k]    = sum_m dC[t, m] A[e, m, k]
+//     grad_a   dA[e, m, k] = sum_{t of e} dC[t, m] B[t, k]
+// (C, dB and dA row-major; sums in FP32 in tensor memory, rounded once.)
+//
+// One structure for the three.  The MMA's M side ("L", TMEM lanes) runs over
+// the result's contiguous index (m, k, k) and its N side ("R", TMEM columns)
+// over the result's rows (t, t, m).  The N side of a tcgen05.mma takes any
+// multiple of 16 (32 for a CTA pair), so a group's last tile, or a group of a
+// few rows, costs MMAs of its own size, not of a whole tile's; a group's rows
+// are cut into tiles of equal height.  Which index of an operand is the sum's
+// decides its layout in shared memory: contiguous along the sum, it is K-major
+// (rows of 128 bytes along the sum); contiguous across it, MN-major (rows of
+// 64 elements across, one for each term).  The TMA writes both with the same
+// 128-byte swizzle, and the tensor core reads both.
+//              L                         R
+//   product    A   (K-major)             B   (K-major)
+//   grad_b     A   (MN-major)            dC  (K-major)
+//   grad_a     B   (MN-major)            dC  (MN-major)
+//
+// Ragged ends: a row of another group that a box of the N side takes along
+// only reaches accumulator columns that are not stored.  In grad_a the rows
+// are the sum, so there the tensor maps of each group (made on the device by
+// grouped_maps_kernel) end where the group ends, and the TMA fills with zeros.
+//
+// Roles, barriers, bounded waits and the programmatic-dependent-launch
+// protocol are the general kernel's (tn_gemm_kernel.cuh): warp 0 loads, one
+// thread of warp 1 issues the MMAs, warps 2-5 read the accumulator and store.
+#pragma once
+
+#include "tn_gemm_kernel.cuh"
+
+namespace tn {
+
+constexpr int kGrMaxExperts = 1024;
+constexpr int kGrBlock = 64;                 // terms of the sum per stage: 128 bytes of 16-bit elements
+constexpr int kGrRaster = 8;                 // R tiles per raster group
+
+enum GroupedOp : int { kGrProduct = 0, kGrGradB = 1, kGrGradA = 2 };
+
+// kGroup CTAs compute a tile of 128 * kGroup (L) x kRows (R).
+template <int kGroup, int kRows>
+struct GroupedCfg {
+    static constexpr int kRowsL = 128;                       // per CTA
+    static constexpr int kRowsR = kRows / kGroup;            // per CTA
+    static constexpr int kTileL = kRowsL * kGroup;
+    static constexpr int kLBytes = kRowsL * 128;
+    static constexpr int kRBytes = kRowsR * 128;
+    static constexpr int kStageBytes = kLBytes + kRBytes;
+    static constexpr int kStages = 196608 / kStageBytes;
+    static constexpr int kGran = 16 * kGroup;                // the MMA's N is a multiple of it
+    static constexpr uint32_t kAccCols = kRows;
+    static constexpr uint32_t kTmemCols = 2 * kAccCols;      // two accumulators: an epilogue overlaps the next tile
+    // full[S], empty[S], accfull[2], accempty[2], drain, never
+    static constexpr int kNumBarriers = 2 * kStages + 6;
+    static constexpr int kTables = 2 * (kGrMaxExperts + 8) * 4;   // group starts, units before each group
+    static constexpr int kSmemBytes =
+        1024 /* alignment slack */ + kStages * kStageBytes + kNumBarriers * 8 + 32 + kStages * 4 + kTables;
+    static_assert(kSmemBytes <= 232448, "exceeds the 227 KiB shared memory of one CTA");
+};
+
+struct GroupedParams {
+    // product: L {K, M, E} box {64, 128, 1}, R {K, T} boxes {64, kRowsR} and {64, 16};
+    // grad_b:  L {K, M, E} box {64, 64, 1},  R {M, T} boxes {64, kRowsR} and {64, 16}
+    CUtensorMap tmap_l, tmap_r, tmap_r16;
+    const CUtensorMap *group_maps;   // grad_a: [E][2], R {M, T_e} and L {K, T_e}, boxes {64, 64}
+    const int32_t *offsets;          // E + 1 row starts, or NULL: one group of all T rows
+    uint16_t *out;                   // row r of group e's range at out + e * out_stride + r * out_ld
+    int64_t out_ld, out_stride;
+    int32_t E, T;
+    int32_t l_extent;                // the result's contiguous extent
+    int32_t r_extent;                // grad_a: the result's rows per expert (M)
+    int32_t red;                     // terms of the sum (grad_a: the group's rows instead)
+    uint32_t fmt, out_fmt;           // operands and result: 0 f16, 1 bf16
+    const float *scale_l;            // 8-bit product: [E][l_extent] and [T] (else NULL)
+    const float *scale_r;
+    uint32_t flags;                  // kFlagStall* (test hooks)
+    uint64_t wait_limit_ns;
+};
+
+// ------------------------------------------------------------------ schedule
+// Rows [start[e], start[e + 1]) belong to group e.  Offsets are read as if each
+// were at least the ones before it and at most T, so a table that is not
+// ascending, or that passes T, never leads outside the operands.
+struct GroupedTile {
+    int32_t e, l0, r0;      // group, first index of the L side, first row within the group's range
+    int32_t rows;           // rows of the result in this tile
+    int32_t n_mma;          // MMA N
+    int32_t red;            // terms of the sum
+};
+
+__host__ __device__ __forceinline__ int32_t grouped_tile_rows(int32_t rows, int32_t tiles, int32_t gran)
+{
+    return ((rows + tiles - 1) / tiles + gran - 1) / gran * gran;
+}
+
+template <int kOp, int kRows, int kTileL, int kGran>
+struct GroupedWalk {
+    const int32_t *start, *before;      // shared memory
+    int32_t l_tiles, r_extent, red;
+    int32_t e;
+
+    // Tile u (u never decreases over the calls).
+    __device__ __forceinline__ GroupedTile at(int32_t u)
+    {
+        while (before[e + 1] <= u) ++e;
+        GroupedTile t;
+        const int32_t group_rows = start[e + 1] - start[e];
+        const int32_t rows = kOp == kGrGradA ? r_extent : group_rows;
+        const int32_t tiles = (rows + kRows - 1) / kRows;
+        const int32_t h = grouped_tile_rows(rows, tiles, kGran);
+        int64_t tr, tl;
+        tile_coord(u - before[e], tiles, l_tiles, kGrRaster, tr, tl);
+        t.e = e;
+        t.l0 = static_cast<int32_t>(tl) * kTileL;
+        t.r0 = static_cast<int32_t>(tr) * h;
+        t.rows = rows - t.r0 < h ? rows - t.r0 : h;
+        t.n_mma = (t.rows + kGran - 1) / kGran * kGran;
+        t.red = kOp == kGrGradA ? group_rows : red;
+        return t;
+    }
+};
+
+// Descriptor of an MN-major operand with the 128-byte swizzle: each term's 64
+// elements are a row of 128 bytes, 8 terms 1024 bytes further on (the stride
+// offset), the next 64 elements across a block of kGrBlock terms further on
+// (the leading offset).
+__device__ __forceinline__ uint64_t desc_mnmajor_sw128(uint32_t saddr)
+{
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>((kGrBlock * 128) >> 4) << 16;
+    d |= static_cast<uint64_t>(1024 >> 4) << 32;
+    d |= static_cast<uint64_t>(1) << 46;
+    d |= static_cast<uint64_t>(2) << 61;
+    return d;
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int32_t x, int32_t y,
+                                            int32_t z)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::
+            "r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap *map, uint32_t bar, int32_t x,
+                                                 int32_t y, int32_t z)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+
+// Makes a tensor map that another kernel wrote usable by this thread's TMA
+// instructions.
+__device__ __forceinline__ void acquire_tensormap(const CUtensorMap *map)
+{
+    asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(reinterpret_cast<uint64_t>(map))
+                 : "memory");
+}
+
+// The group tables in shared memory, by all threads of the CTA.
+template <int kOp, int kRows>
+__device__ __forceinline__ void grouped_tables(const GroupedParams &p, int32_t l_tiles, int32_t *start, int32_t *before)
+{
+    const int32_t E = p.E, T = p.T;
+    for (int32_t i = threadIdx.x; i <= E; i += kThreads) {
+        const int32_t o = p.offsets ? p.offsets[i] : (i == 0 ? 0 : T);
+        start[i] = o < 0 ? 0 : (o > T ? T : o);
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        // each lane a run of entries: the running maximum of the starts, then the
+        // running sum of the groups' tiles
+        const int lane = threadIdx.x;
+        const int32_t per = (E + 1 + 31) / 32;
+        const int32_t i0 = lane * per < E + 1 ? lane * per : E + 1;
+        const int32_t i1 = i0 + per < E + 1 ? i0 + per : E + 1;
+        int32_t top = 0;
+        for (int32_t i = i0; i < i1; ++i) top = start[i] > top ? start[i] : top;
+        int32_t run = top;
+        for (int d = 1; d < 32; d *= 2) {
+            const int32_t o = __shfl_up_sync(0xffffffffu, run, d);
+            if (lane >= d && o > run) run = o;
+        }
+        int32_t m = __shfl_up_sync(0xffffffffu, run, 1);
+        if (lane == 0) m = 0;
+        for (int32_t i = i0; i < i1; ++i) {
+            m = start[i] > m ? start[i] : m;
+            start[i] = m;
+        }
+        __syncwarp();
+        int32_t sum = 0;
+        for (int32_t i = i0; i < i1 && i < E; ++i) {
+            const int32_t rows = kOp == kGrGradA ? p.r_extent : start[i + 1] - start[i];
+            sum += (rows + kRows - 1) / kRows * l_tiles;
+        }
+        int32_t acc = sum;
+        for (int d = 1; d < 32; d *= 2) {
+            const int32_t o = __shfl_up_sync(0xffffffffu, acc, d);
+            if (lane >= d) acc += o;
+        }
+        acc -= sum;
+        for (int32_t i = i0; i < i1; ++i) {
+            before[i] = acc;
+            if (i < E) {
+                const int32_t rows = kOp == kGrGradA ? p.r_extent : start[i + 1] - start[i];
+                acc += (rows + kRows - 1) / kRows * l_tiles;
+            }
+        }
+    }
+    __syncthreads();
+}
+
+template <int kOp, int kGroup, int kRows>
+__global__ void __launch_bounds__(kThreads, 1) tn_grouped_kernel(const __grid_constant__ GroupedParams p)
+{
+    using Cfg = GroupedCfg<kGroup, kRows>;
+    constexpr int kStages = Cfg::kStages;
+    constexpr bool kLMajorK = kOp == kGrProduct, kRMajorK = kOp != kGrGradA;
+
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t s_ring = ptx::smem_addr(smem);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kStages * Cfg::kStageBytes);
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + Cfg::kNumBarriers);
+    volatile uint32_t *abort_flag = tmem_holder + 1;
+    volatile uint32_t *issued_count = tmem_holder + 2;    // fills this CTA's producer issued
+    volatile uint32_t *producer_done = tmem_holder + 3;   // set once this CTA's producer issues no more
+    volatile uint32_t *fill_bytes = tmem_holder + 8;      // [kStages]: this CTA's bytes of the stage's last fill
+    int32_t *start = reinterpret_cast<int32_t *>(tmem_holder + 8 + kStages);
+    int32_t *before = start + kGrMaxExperts + 8;
+    const uint32_t abort_addr = ptx::smem_addr(const_cast<uint32_t *>(abort_flag));
+    const uint32_t count_addr = ptx::smem_addr(const_cast<uint32_t *>(issued_count));
+    const uint32_t done_addr = ptx::smem_addr(const_cast<uint32_t *>(producer_done));
+    const uint32_t fill_addr = ptx::smem_addr(const_cast<uint32_t *>(fill_bytes));
+    const uint32_t bar0 = ptx::smem_addr(bars);
+    auto full_bar = [&](int s) { return bar0 + 8u * s; };
+    auto empty_bar = [&](int s) { return bar0 + 8u * (kStages + s); };
+    auto accfull_bar = [&](int b) { return bar0 + 8u * (2 * kStages + b); };
+    auto accempty_bar = [&](int b) { return bar0 + 8u * (2 * kStages + 2 + b); };
+    const uint32_t drain_bar = bar0 + 8u * (2 * kStages + 4);
+    const uint32_t never_bar = bar0 + 8u * (2 * kStages + 5);   // nothing ever arrives (test stalls)
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t pos = kGroup == 2 ? ptx::cluster_ctarank() : 0u;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            ptx::mbar_init(full_bar(s), 1);
+            ptx::mbar_init(empty_bar(s), 1);
+            fill_bytes[s] = 0u;
+        }
+        for (int b = 0; b < 2; ++b) {
+            ptx::mbar_init(accfull_bar(b), 1);
+            ptx::mbar_init(accempty_bar(b), kEpiWarps * kGroup);
+        }
+        ptx::mbar_init(drain_bar, 1);
+        ptx::mbar_init(never_bar, 1);
+        *abort_flag = 0u;
+        *issued_count = 0u;
+        *producer_done = 0u;
+        ptx::fence_mbar_init();
+        ptx::fence_proxy_async_smem();
+    }
+    if (kOp != kGrGradA && threadIdx.x == 32 && p.red > 0) {
+        ptx::prefetch_tensormap(&p.tmap_l);
+        ptx::prefetch_tensormap(&p.tmap_r);
+        ptx::prefetch_tensormap(&p.tmap_r16);
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc<kGroup>(ptx::smem_addr(tmem_holder), Cfg::kTmemCols);
+        ptx::tmem_relinquish_alloc_permit<kGroup>();
+    }
+    ptx::tc_fence_before_sync();
+    if constexpr (kGroup == 2)
+        ptx::cluster_sync();
+    else
+        __syncthreads();
+    ptx::tc_fence_after_sync();
+    const uint32_t tmem_base = *tmem_holder;
+    const Waiter w{abort_flag, abort_addr, pos, static_cast<uint32_t>(kGroup), p.wait_limit_ns};
+
+    // Every thread's first global access is behind this wait: the offsets, and
+    // in grad_a the maps, may be the previous kernel's.
+    ptx::griddep_wait();
+    const int32_t l_tiles = (p.l_extent + Cfg::kTileL - 1) / Cfg::kTileL;
+    grouped_tables<kOp, kRows>(p, l_tiles, start, before);
+    const int32_t total = before[p.E];
+    const int32_t slot = static_cast<int32_t>(blockIdx.x) / kGroup, slots = static_cast<int32_t>(gridDim.x) / kGroup;
+    GroupedWalk<kOp, kRows, Cfg::kTileL, Cfg::kGran> walk{start, before, l_tiles, p.r_extent, p.red, 0};
+    auto blocks_of = [](int32_t red) { return (red + kGrBlock - 1) / kGrBlock; };
+
+    if (warp == 0) {
+        // ------------------------------------------------ TMA producer (every CTA)
+        // A pair's loads all complete on the even CTA's full[s], which its own
+        // producer arms with both CTAs' bytes.
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0, n_issued = 0;
+            bool ok = true;
+            if (p.flags & (pos == 0 ? kFlagStallProducer0 : kFlagStallProducer1)) ok = w.wait(never_bar, 0u, kSiteStall);
+            int32_t mapped = -1;
+            for (int32_t u = slot; ok && u < total; u += slots) {
+                const GroupedTile t = walk.at(u);
+                const int32_t cols = t.n_mma / kGroup;        // R elements of this CTA
+                const int32_t l0 = t.l0 + static_cast<int32_t>(pos) * Cfg::kRowsL;
+                const int32_t r0 = (kOp == kGrGradA ? 0 : start[t.e]) + t.r0 + static_cast<int32_t>(pos) * cols;
+                const uint32_t r_bytes =
+                    kRMajorK ? cols * 128u : static_cast<uint32_t>((cols + 63) / 64) * (kGrBlock * 128u);
+                const uint32_t fill = Cfg::kLBytes + r_bytes;
+                const CUtensorMap *map_l = &p.tmap_l, *map_r = &p.tmap_r;
+                if constexpr (kOp == kGrGradA) {
+                    map_r = p.group_maps + 2 * t.e;
+                    map_l = map_r + 1;
+                    if (t.e != mapped && t.red > 0) {
+                        acquire_tensormap(map_r);
+                        acquire_tensormap(map_l);
+                        mapped = t.e;
+                    }
+                }
+                const int32_t blocks = blocks_of(t.red);
+                for (int32_t i = 0; i < blocks; ++i) {
+                    if (!w.wait(empty_bar(stage), phase ^ 1u, kSiteEmpty)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t s_l = s_ring + stage * Cfg::kStageBytes, s_r = s_l + Cfg::kLBytes;
+                    const int32_t k0 = i * kGrBlock;
+                    uint32_t bar = full_bar(stage);
+                    fill_bytes[stage] = fill;
+                    if (pos == 0) ptx::mbar_arrive_expect_tx(bar, kGroup * fill);
+                    if constexpr (kGroup == 2) bar = ptx::mapa_shared(bar, 0);
+                    auto load2 = [&](uint32_t dst, const CUtensorMap *map, int32_t x, int32_t y) {
+                        if constexpr (kGroup == 2)
+                            ptx::tma_load_2d_pair(dst, map, bar, x, y);
+                        else
+                            ptx::tma_load_2d(dst, map, bar, x, y);
+                    };
+                    auto load3 = [&](uint32_t dst, const CUtensorMap *map, int32_t x, int32_t y, int32_t z) {
+                        if constexpr (kGroup == 2)
+                            tma_load_3d_pair(dst, map, bar, x, y, z);
+                        else
+                            tma_load_3d(dst, map, bar, x, y, z);
+                    };
+                    if constexpr (kOp == kGrProduct) {
+                        load3(s_l, map_l, k0, l0, t.e);
+                    } else if constexpr (kOp == kGrGradB) {
+                        load3(s_l, map_l, l0, k0, t.e);
+                        load3(s_l + kGrBlock * 128, map_l, l0 + 64, k0, t.e);
+                    } else {
+                        load2(s_l, map_l, l0, k0);
+                        load2(s_l + kGrBlock * 128, map_l, l0 + 64, k0);
+                    }
+                    if constexpr (kRMajorK) {
+                        if (cols == Cfg::kRowsR) {
+                            load2(s_r, map_r, k0, r0);
+                        } else {
+                            for (int32_t c = 0; c < cols; c += 16) load2(s_r + c * 128, &p.tmap_r16, k0, r0 + c);
+                        }
+                    } else {
+                        load2(s_r, map_r, r0, k0);
+                        if (cols > 64) load2(s_r + kGrBlock * 128, map_r, r0 + 64, k0);
+                    }
+                    *issued_count = ++n_issued;
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            // no more loads from this CTA: the next kernel may start its setup
+            ptx::griddep_launch_dependents();
+            if constexpr (kGroup == 2) {
+                ptx::st_release_cluster_u32(ptx::mapa_shared(done_addr, pos), 1u);
+                if (pos == 0) {
+                    // Both producers have stopped (or the limit ran out): let every load that
+                    // was issued land before the pair can exit.  Loads go round the stages in
+                    // order, and a stage is refilled only after the pair's MMAs read its
+                    // previous fill, so the two producers are at most one fill of a stage
+                    // apart.  On the normal path both issued every fill; after an abort the
+                    // bytes that will not come are taken off the last fill, or the fill that
+                    // this CTA did not arm is armed for the bytes that will.
+                    uint32_t peer = n_issued;
+                    const uint64_t t0 = ptx::globaltimer();
+                    bool stopped = true;
+                    while (ptx::ld_acquire_cluster_u32(ptx::mapa_shared(done_addr, 1)) == 0u) {
+                        if (ptx::globaltimer() - t0 > w.limit) {
+                            atomicCAS(&g_tn_status, 0, 4 | (kSitePeerDone << 8));
+                            stopped = false;
+                            break;
+                        }
+                    }
+                    if (stopped) peer = ptx::ld_relaxed_cluster_u32(ptx::mapa_shared(count_addr, 1));
+                    for (int s = 0; s < kStages; ++s) {
+                        auto fills = [&](uint32_t n) { return n / kStages + (static_cast<uint32_t>(s) < n % kStages); };
+                        const uint32_t mine = fills(n_issued), theirs = fills(peer);
+                        const uint32_t last = mine > theirs ? mine : theirs;
+                        if (last == 0) continue;
+                        if (mine > theirs + 1 || theirs > mine + 1) {      // cannot happen; never guess
+                            atomicCAS(&g_tn_status, 0, 4 | (kSiteReconcile << 8));
+                            continue;
+                        }
+                        if (mine > theirs)
+                            ptx::mbar_complete_tx(full_bar(s), fill_bytes[s]);
+                        else if (theirs > mine)
+                            ptx::mbar_arrive_expect_tx(
+                                full_bar(s), ptx::ld_relaxed_cluster_u32(ptx::mapa_shared(fill_addr + 4u * s, 1)));
+                        w.drain(full_bar(s), (last - 1) & 1u);
+                    }
+                }
+            } else {
+                for (int s = 0; s < kStages; ++s) {
+                    const uint32_t passes = n_issued / kStages + (static_cast<uint32_t>(s) < n_issued % kStages ? 1u : 0u);
+                    if (passes) w.drain(full_bar(s), (passes - 1) & 1u);
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && pos == 0) {
+            // ------------------------------------------------ MMA issuer (even CTA of a pair)
+            int stage = 0, acc = 0;
+            uint32_t phase = 0, acc_phase = 0;
+            bool ok = true, issued_any = false;
+            constexpr uint16_t kMask = kGroup == 2 ? 3 : 1;
+            constexpr uint32_t kStepL = kLMajorK ? 2 : 128, kStepR = kRMajorK ? 2 : 128;   // 16 terms on, in 16-byte units
+            if (p.flags & kFlagStallMma) ok = w.wait(never_bar, 0u, kSiteStall);
+            for (int32_t u = slot; ok && u < total; u += slots) {
+                const GroupedTile t = walk.at(u);
+                if (t.red == 0) continue;
+                const uint32_t idesc = ptx::idesc_f32acc(Cfg::kTileL, static_cast<uint32_t>(t.n_mma), p.fmt, p.fmt) |
+                                       (kLMajorK ? 0u : 1u << 15) | (kRMajorK ? 0u : 1u << 16);
+                if (!w.wait(accempty_bar(acc), acc_phase ^ 1u, kSiteAccEmpty)) break;
+                ptx::tc_fence_after_sync();
+                const uint32_t d_tmem = tmem_base + acc * Cfg::kAccCols;
+                const int32_t blocks = blocks_of(t.red);
+                for (int32_t i = 0; i < blocks; ++i) {
+                    if (!w.wait(full_bar(stage), phase, kSiteLoaded)) {
+                        ok = false;
+                        break;
+                    }
+                    ptx::tc_fence_after_sync();
+                    const uint32_t s_l = s_ring + stage * Cfg::kStageBytes, s_r = s_l + Cfg::kLBytes;
+                    const uint64_t desc_l = kLMajorK ? ptx::desc_kmajor_sw128(s_l) : desc_mnmajor_sw128(s_l);
+                    const uint64_t desc_r = kRMajorK ? ptx::desc_kmajor_sw128(s_r) : desc_mnmajor_sw128(s_r);
+                    // terms past the end of the sum are zeros: whole steps of them are left out
+                    const int32_t left = t.red - i * kGrBlock;
+                    const int steps = left >= kGrBlock ? kGrBlock / 16 : (left + 15) / 16;
+#pragma unroll
+                    for (int j = 0; j < kGrBlock / 16; ++j)
+                        if (j < steps)
+                            ptx::mma_f16<kGroup>(d_tmem, desc_l + kStepL * j, desc_r + kStepR * j, idesc,
+                                                 (i | j) != 0 ? 1u : 0u);
+                    issued_any = true;
+                    ptx::mma_commit<kGroup>(empty_bar(stage), kMask);
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!ok) break;
+                ptx::mma_commit<kGroup>(accfull_bar(acc), kMask);
+                if (++acc == 2) {
+                    acc = 0;
+                    acc_phase ^= 1u;
+                }
+            }
+            // every MMA this thread issued completes before TMEM is freed
+            if (issued_any) {
+                ptx::mma_commit<kGroup>(drain_bar, 1);
+                w.drain(drain_bar, 0u);
+            }
+        }
+    } else {
+        // ------------------------------------------------ epilogue (warps 2..5, every CTA)
+        const int quarter = warp & 3;             // TMEM lanes 32*quarter .. +31 are this warp's
+        int acc = 0;
+        uint32_t acc_phase = 0;
+        const bool out_bf16 = p.out_fmt != 0;
+        for (int32_t u = slot; u < total; u += slots) {
+            const GroupedTile t = walk.at(u);
+            const int32_t l = t.l0 + static_cast<int32_t>(pos) * Cfg::kRowsL + 32 * quarter + lane;
+            const bool live = l < p.l_extent;
+            const int64_t row0 = static_cast<int64_t>(kOp == kGrGradA ? 0 : start[t.e]) + t.r0;
+            uint16_t *out = p.out + t.e * p.out_stride + row0 * p.out_ld + l;
+            if (t.red == 0) {                     // an empty sum
+                if (live)
+                    for (int32_t r = 0; r < t.rows; ++r) out[r * p.out_ld] = 0;
+                continue;
+            }
+            const float scale_l = p.scale_l && live ? __ldg(p.scale_l + static_cast<int64_t>(t.e) * p.l_extent + l) : 1.0f;
+            if (!__all_sync(0xffffffffu, w.wait(accfull_bar(acc), acc_phase, kSiteAccFull))) break;
+            ptx::tc_fence_after_sync();
+            const uint32_t t_row = tmem_base + (static_cast<uint32_t>(32 * quarter) << 16) + acc * Cfg::kAccCols;
+            for (int32_t c = 0; c < t.n_mma; c += 32) {
+                uint32_t v[32];
+                ptx::tmem_ld_32x32b_x32(t_row + c, v);
+                ptx::tmem_ld_wait(v);
+                if (c + 32 >= t.n_mma) {          // the accumulator is read: hand it back
+                    ptx::tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if constexpr (kGroup == 2)
+                            ptx::mbar_arrive_remote(ptx::mapa_shared(accempty_bar(acc), 0));
+                        else
+                            ptx::mbar_arrive(accempty_bar(acc));
+                    }
+                }
+                if (live) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        if (c + j >= t.rows) break;
+                        float x = __uint_as_float(v[j]);
+                        if (p.scale_l) x = x * scale_l * __ldg(p.scale_r + row0 + c + j);
+                        const uint32_t h = out_bf16 ? ptx::pack_bf16x2(x, x) : ptx::pack_f16x2(x, x);
+                        out[(c + j) * p.out_ld] = static_cast<uint16_t>(h & 0xFFFFu);
+                    }
+                }
+                __syncwarp();
+            }
+            if (++acc == 2) {
+                acc = 0;
+                acc_phase ^= 1u;
+            }
+        }
+    }
+
+    __syncwarp();                // .aligned barriers below need converged warps
+    ptx::tc_fence_before_sync();
+    if constexpr (kGroup == 2)
+        ptx::cluster_sync();     // no CTA leaves while the other may still touch its shared memory
+    else
+        __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        ptx::tc_fence_after_sync();
+        ptx::tmem_dealloc<kGroup>(tmem_base, Cfg::kTmemCols);
+    }
+}
+
+// ------------------------------------------------------------------ grad_a's tensor maps
+// maps[2 e] and maps[2 e + 1]: the rows of group e of dC and of B, as copies of
+// two templates with the group's first row as base and its rows as extent.  One
+// warp per group and map.
+struct GroupedMapsParams {
+    CUtensorMap dc, b;
+    CUtensorMap *maps;
+    const int32_t *offsets;
+    const uint8_t *dc_base, *b_base;
+    int64_t dc_row_bytes, b_row_bytes;
+    int32_t E, T;
+};
+
+__global__ void __launch_bounds__(32) grouped_maps_kernel(const __grid_constant__ GroupedMapsParams p)
+{
+    __shared__ __align__(128) CUtensorMap map;
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    const int32_t e = static_cast<int32_t>(blockIdx.x) >> 1, lane = threadIdx.x;
+    const bool second = blockIdx.x & 1;
+    // the group's rows, from offsets read as the product's kernel reads them
+    auto clamped = [&](int32_t i) {
+        const int32_t o = p.offsets[i];
+        return o < 0 ? 0 : (o > p.T ? p.T : o);
+    };
+    int32_t top = 0;
+    for (int32_t i = lane; i <= e; i += 32) {
+        const int32_t o = clamped(i);
+        top = o > top ? o : top;
+    }
+    const int32_t first = __reduce_max_sync(0xffffffffu, top);
+    const int32_t end = max(first, clamped(e + 1));
+    if (first == end) return;                     // no rows: the map is not used
+    const uint32_t *src = reinterpret_cast<const uint32_t *>(second ? &p.b : &p.dc);
+    reinterpret_cast<uint32_t *>(&map)[lane] = src[lane];
+    __syncwarp();
+    const uint32_t s_map = ptx::smem_addr(&map);
+    if (lane == 0) {
+        const uint64_t base = reinterpret_cast<uint64_t>(second ? p.b_base + first * p.b_row_bytes
+                                                                : p.dc_base + first * p.dc_row_bytes);
+        asm volatile("tensormap.replace.tile.global_address.shared::cta.b1024.b64 [%0], %1;" ::"r"(s_map), "l"(base)
+                     : "memory");
+        asm volatile("tensormap.replace.tile.global_dim.shared::cta.b1024.b32 [%0], 1, %1;" ::"r"(s_map),
+                     "r"(static_cast<uint32_t>(end - first))
+                     : "memory");
+    }
+    __syncwarp();
+    asm volatile("tensormap.cp_fenceproxy.global.shared::cta.tensormap::generic.release.gpu.sync.aligned [%0], [%1], 128;" ::
+                     "l"(reinterpret_cast<uint64_t>(p.maps + 2 * e + second)),
+                 "r"(s_map)
+                 : "memory");
+}
+
+// ------------------------------------------------------------------ copies
+// Rows that the TMA cannot address in place, or 8-bit integers, copied to f16
+// (or as they are, 16 bits wide) rows that start on 128-byte boundaries, the
+// padding zeroed: row r of the copy is row r % rows_per of block r / rows_per.
+template <typename Src>
+struct WidenJob {
+    const Src *src;
+    int64_t ld, stride;
+    uint16_t *dst;
+    int64_t ld_dst;      // a multiple of 64
+    int64_t rows_per, rows, cols;
+};
+
+// Four 8-bit integers to four halves: x + 128 in the low bits of 1024's
+// mantissa is 1152 + x, exactly.
+__device__ __forceinline__ uint2 i8x4_to_f16x4(uint32_t w)
+{
+    const uint32_t u = w ^ 0x80808080u;
+    uint2 r;
+    asm("{\n\t.reg .b32 a;\n\tprmt.b32 a, %1, 0x64646464, 0x4140;\n\tsub.rn.f16x2 %0, a, %2;\n\t}"
+        : "=r"(r.x) : "r"(u), "r"(0x64806480u));
+    asm("{\n\t.reg .b32 a;\n\tprmt.b32 a, %1, 0x64646464, 0x4342;\n\tsub.rn.f16x2 %0, a, %2;\n\t}"
+        : "=r"(r.y) : "r"(u), "r"(0x64806480u));
+    return r;
+}
+
+constexpr int kWidenThreads = 256;
+
+// One thread per 8 elements (16 bytes) of the copy.
+template <typename Src>
+__global__ void __launch_bounds__(kWidenThreads) widen_rows_kernel(const WidenJob<Src> j)
+{
+    ptx::griddep_wait();
+    const int64_t chunks = j.ld_dst / 8, total = j.rows * chunks;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kWidenThreads;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kWidenThreads + threadIdx.x; i < total; i += step) {
+        const int64_t r = i / chunks, c = (i - r * chunks) * 8;
+        const int64_t e = r / j.rows_per;
+        const Src *src = j.src + e * j.stride + (r - e * j.rows_per) * j.ld + c;
+        uint4 o = make_uint4(0, 0, 0, 0);
+        if (c + 8 <= j.cols && reinterpret_cast<uintptr_t>(src) % (8 * sizeof(Src)) == 0) {
+            if constexpr (sizeof(Src) == 1) {
+                const uint2 w = __ldg(reinterpret_cast<const uint2 *>(src));
+                const uint2 lo = i8x4_to_f16x4(w.x), hi = i8x4_to_f16x4(w.y);
+                o = make_uint4(lo.x, lo.y, hi.x, hi.y);
+            } else {
+                o = __ldg(reinterpret_cast<const uint4 *>(src));
+            }
+        } else {
+            union {
+                Src v[8];
+                uint2 w;
+                uint4 u;
+            } in;
+            in.u = make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                if (c + q < j.cols) in.v[q] = src[q];
+            if constexpr (sizeof(Src) == 1) {
+                const uint2 lo = i8x4_to_f16x4(in.w.x), hi = i8x4_to_f16x4(in.w.y);
+                o = make_uint4(lo.x, lo.y, hi.x, hi.y);
+            } else {
+                o = in.u;
+            }
+        }
+        reinterpret_cast<uint4 *>(j.dst + r * j.ld_dst)[c / 8] = o;
+    }
+}
+
+}  // namespace tn

@@ -13,6 +13,8 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
+#include <string.h>
+
 #include "tn_gemm.h"
 
 /* Reads args[i] as a 64-bit int; returns 0 and sets an exception on failure. */
@@ -154,6 +156,102 @@ static PyObject *py_gemm_quantize_e4m3(PyObject *self, PyObject *const *args, Py
         (long)gemm_quantize_e4m3(x, dtype, rows, cols, ldx, q, ldq, (float *)scale, stream));
 }
 
+/* The calls with many arguments: `form` has one letter per argument, 'i' a C
+ * int, 'l' a 64-bit int, 'p' a pointer; the values are left in v[]. */
+typedef union {
+    int i;
+    int64_t l;
+    void *p;
+} arg_value;
+
+static int read_args(const char *name, const char *form, PyObject *const *args, Py_ssize_t nargs, arg_value *v)
+{
+    const Py_ssize_t want = (Py_ssize_t)strlen(form);
+    if (!check_nargs(name, nargs, want)) return 0;
+    for (Py_ssize_t k = 0; k < want; ++k) {
+        const int ok = form[k] == 'i' ? arg_int(args, k, &v[k].i)
+                       : form[k] == 'l' ? arg_i64(args, k, &v[k].l) : arg_ptr(args, k, &v[k].p);
+        if (!ok) return 0;
+    }
+    return 1;
+}
+
+/* (op, E, M, K, T, X, ldx, stride_x, Y, ldy) -> bytes */
+static PyObject *py_gemm_grouped_workspace(PyObject *self, PyObject *const *args, Py_ssize_t nargs)
+{
+    (void)self;
+    arg_value v[10];
+    if (!read_args("gemm_grouped_workspace", "illllpllpl", args, nargs, v)) return NULL;
+    return PyLong_FromLongLong(gemm_grouped_workspace(v[0].i, v[1].l, v[2].l, v[3].l, v[4].l, v[5].p, v[6].l, v[7].l,
+                                                      v[8].p, v[9].l));
+}
+
+/* (type, E, M, K, T, A, lda, stride_a, B, ldb, offsets, C, ldc, workspace, workspace_bytes, stream) */
+static PyObject *py_gemm_tn_grouped(PyObject *self, PyObject *const *args, Py_ssize_t nargs)
+{
+    (void)self;
+    arg_value v[16];
+    if (!read_args("gemm_tn_grouped", "illllpllplpplplp", args, nargs, v)) return NULL;
+    return PyLong_FromLong((long)gemm_tn_grouped(v[0].i, v[1].l, v[2].l, v[3].l, v[4].l, v[5].p, v[6].l, v[7].l, v[8].p,
+                                                 v[9].l, (const int32_t *)v[10].p, v[11].p, v[12].l, v[13].p, v[14].l,
+                                                 v[15].p));
+}
+
+/* (type, E, M, K, T, A, lda, stride_a, dC, lddc, offsets, dB, lddb, workspace, workspace_bytes, stream) */
+static PyObject *py_gemm_tn_grouped_grad_b(PyObject *self, PyObject *const *args, Py_ssize_t nargs)
+{
+    (void)self;
+    arg_value v[16];
+    if (!read_args("gemm_tn_grouped_grad_b", "illllpllplpplplp", args, nargs, v)) return NULL;
+    return PyLong_FromLong((long)gemm_tn_grouped_grad_b(v[0].i, v[1].l, v[2].l, v[3].l, v[4].l, v[5].p, v[6].l, v[7].l,
+                                                        v[8].p, v[9].l, (const int32_t *)v[10].p, v[11].p, v[12].l,
+                                                        v[13].p, v[14].l, v[15].p));
+}
+
+/* (type, E, M, K, T, dC, lddc, B, ldb, offsets, dA, ldda, stride_da, workspace, workspace_bytes, stream) */
+static PyObject *py_gemm_tn_grouped_grad_a(PyObject *self, PyObject *const *args, Py_ssize_t nargs)
+{
+    (void)self;
+    arg_value v[16];
+    if (!read_args("gemm_tn_grouped_grad_a", "illllplplppllplp", args, nargs, v)) return NULL;
+    return PyLong_FromLong((long)gemm_tn_grouped_grad_a(v[0].i, v[1].l, v[2].l, v[3].l, v[4].l, v[5].p, v[6].l, v[7].p,
+                                                        v[8].l, (const int32_t *)v[9].p, v[10].p, v[11].l, v[12].l,
+                                                        v[13].p, v[14].l, v[15].p));
+}
+
+/* (out_type, M, N, K, A, lda, scale_a, B, ldb, scale_b, C, ldc, workspace, workspace_bytes, stream) */
+static PyObject *py_gemm_i8_tn(PyObject *self, PyObject *const *args, Py_ssize_t nargs)
+{
+    (void)self;
+    arg_value v[15];
+    if (!read_args("gemm_i8_tn", "illlplpplpplplp", args, nargs, v)) return NULL;
+    return PyLong_FromLong((long)gemm_i8_tn(v[0].i, v[1].l, v[2].l, v[3].l, (const int8_t *)v[4].p, v[5].l,
+                                            (const float *)v[6].p, (const int8_t *)v[7].p, v[8].l,
+                                            (const float *)v[9].p, v[10].p, v[11].l, v[12].p, v[13].l, v[14].p));
+}
+
+/* (out_type, E, M, K, T, A, lda, stride_a, scale_a, B, ldb, scale_b, offsets, C, ldc, workspace, workspace_bytes, stream) */
+static PyObject *py_gemm_i8_tn_grouped(PyObject *self, PyObject *const *args, Py_ssize_t nargs)
+{
+    (void)self;
+    arg_value v[18];
+    if (!read_args("gemm_i8_tn_grouped", "illllpllpplppplplp", args, nargs, v)) return NULL;
+    return PyLong_FromLong((long)gemm_i8_tn_grouped(
+        v[0].i, v[1].l, v[2].l, v[3].l, v[4].l, (const int8_t *)v[5].p, v[6].l, v[7].l, (const float *)v[8].p,
+        (const int8_t *)v[9].p, v[10].l, (const float *)v[11].p, (const int32_t *)v[12].p, v[13].p, v[14].l, v[15].p,
+        v[16].l, v[17].p));
+}
+
+/* (x, x_type, rows, cols, ldx, q, ldq, scale, stream) */
+static PyObject *py_gemm_quantize_i8_rows(PyObject *self, PyObject *const *args, Py_ssize_t nargs)
+{
+    (void)self;
+    arg_value v[9];
+    if (!read_args("gemm_quantize_i8_rows", "pilllplpp", args, nargs, v)) return NULL;
+    return PyLong_FromLong((long)gemm_quantize_i8_rows(v[0].p, v[1].i, v[2].l, v[3].l, v[4].l, (int8_t *)v[5].p, v[6].l,
+                                                       (float *)v[7].p, v[8].p));
+}
+
 static PyMethodDef methods[] = {
     {"gemm_f16_tn", (PyCFunction)(void (*)(void))py_gemm_f16_tn, METH_FASTCALL,
      "gemm_f16_tn(M, N, K, A, lda, B, ldb, C, ldc, stream) -> status"},
@@ -167,6 +265,25 @@ static PyMethodDef methods[] = {
      "gemm_f16_tn_softmax_stats(M, N, K, A, lda, B, ldb, C, ldc, scale, row_max, row_sum, stream) -> status"},
     {"gemm_quantize_e4m3", (PyCFunction)(void (*)(void))py_gemm_quantize_e4m3, METH_FASTCALL,
      "gemm_quantize_e4m3(x, dtype, rows, cols, ldx, q, ldq, scale_out, stream) -> status"},
+    {"gemm_grouped_workspace", (PyCFunction)(void (*)(void))py_gemm_grouped_workspace, METH_FASTCALL,
+     "gemm_grouped_workspace(op, E, M, K, T, X, ldx, stride_x, Y, ldy) -> bytes"},
+    {"gemm_tn_grouped", (PyCFunction)(void (*)(void))py_gemm_tn_grouped, METH_FASTCALL,
+     "gemm_tn_grouped(type, E, M, K, T, A, lda, stride_a, B, ldb, offsets, C, ldc, workspace, workspace_bytes, stream) "
+     "-> status"},
+    {"gemm_tn_grouped_grad_b", (PyCFunction)(void (*)(void))py_gemm_tn_grouped_grad_b, METH_FASTCALL,
+     "gemm_tn_grouped_grad_b(type, E, M, K, T, A, lda, stride_a, dC, lddc, offsets, dB, lddb, workspace, "
+     "workspace_bytes, stream) -> status"},
+    {"gemm_tn_grouped_grad_a", (PyCFunction)(void (*)(void))py_gemm_tn_grouped_grad_a, METH_FASTCALL,
+     "gemm_tn_grouped_grad_a(type, E, M, K, T, dC, lddc, B, ldb, offsets, dA, ldda, stride_da, workspace, "
+     "workspace_bytes, stream) -> status"},
+    {"gemm_i8_tn", (PyCFunction)(void (*)(void))py_gemm_i8_tn, METH_FASTCALL,
+     "gemm_i8_tn(out_type, M, N, K, A, lda, scale_a, B, ldb, scale_b, C, ldc, workspace, workspace_bytes, stream) -> "
+     "status"},
+    {"gemm_i8_tn_grouped", (PyCFunction)(void (*)(void))py_gemm_i8_tn_grouped, METH_FASTCALL,
+     "gemm_i8_tn_grouped(out_type, E, M, K, T, A, lda, stride_a, scale_a, B, ldb, scale_b, offsets, C, ldc, workspace, "
+     "workspace_bytes, stream) -> status"},
+    {"gemm_quantize_i8_rows", (PyCFunction)(void (*)(void))py_gemm_quantize_i8_rows, METH_FASTCALL,
+     "gemm_quantize_i8_rows(x, x_type, rows, cols, ldx, q, ldq, scale, stream) -> status"},
     {NULL, NULL, 0, NULL},
 };
 

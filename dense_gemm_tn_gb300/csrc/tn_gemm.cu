@@ -24,6 +24,8 @@
 #include "aux_kernels.cuh"
 #include "repack_kernel.cuh"
 #include "quant_e4m3_kernel.cuh"
+#include "grouped_kernel.cuh"
+#include "quant_i8_kernel.cuh"
 
 namespace {
 
@@ -93,6 +95,8 @@ struct DeviceState {
     std::unordered_map<cudaStream_t, Split> stats;
     int quant_blocks[3] = {};         // co-resident quantiser CTAs per SM, by input type (0 = not queried)
     bool skinny_attr[2] = {};         // tn_skinny_kernel's shared-memory attribute set, by kind
+    int grouped_slots[3][3] = {};     // co-resident tn_grouped_kernel CTAs or pairs, by operation and variant (0 = not queried)
+    int quant_rows_blocks[3] = {};    // co-resident CTAs of the row quantiser per SM, by input type (0 = not queried)
     // One lock per stream, held by a call from its first buffer lookup through
     // its last launch: a call is several launches (row copy, GEMM, reduce),
     // and two host threads' calls on one stream must not interleave them.
@@ -127,6 +131,7 @@ struct LaunchRecord {
     int G = 0, wide = 0, grid = 0, clusters = 0, slots = 0;
     int tiles = 0, units = 0, tail_start = 0, tail_mode = 0, split_parts = 0, vec = 0, cluster = 0, lean = 0;
     int skinny = 0;
+    int grouped = 0, copied = 0;    // a product grouped by expert (tiles: an upper bound); operands copied (1: first, 2: second)
     long long qgrid = 0, qunits = 0;
 };
 thread_local LaunchRecord t_rec;
@@ -278,10 +283,12 @@ struct MapKey {
     uint64_t inner, outer, row_bytes;
     uint32_t box_inner, box_outer;
     int type;
+    uint64_t depth, depth_bytes;      // third dimension; depth 0: a 2-D map
     bool operator==(const MapKey &o) const
     {
         return base == o.base && inner == o.inner && outer == o.outer && row_bytes == o.row_bytes &&
-               box_inner == o.box_inner && box_outer == o.box_outer && type == o.type;
+               box_inner == o.box_inner && box_outer == o.box_outer && type == o.type && depth == o.depth &&
+               depth_bytes == o.depth_bytes;
     }
 };
 
@@ -290,9 +297,9 @@ struct MapKeyHash {
     {
         // 64-bit multiplicative mixing of the fields
         uint64_t h = 0x9E3779B97F4A7C15ull;
-        const uint64_t f[6] = {static_cast<uint64_t>(k.base), k.inner, k.outer, k.row_bytes,
+        const uint64_t f[7] = {static_cast<uint64_t>(k.base), k.inner, k.outer, k.row_bytes,
                                (static_cast<uint64_t>(k.box_inner) << 32) | k.box_outer,
-                               static_cast<uint64_t>(static_cast<uint32_t>(k.type))};
+                               static_cast<uint64_t>(static_cast<uint32_t>(k.type)) | (k.depth << 32), k.depth_bytes};
         for (uint64_t x : f) {
             h ^= x + 0x9E3779B97F4A7C15ull + (h << 6) + (h >> 2);
             h *= 0xBF58476D1CE4E5B9ull;
@@ -313,12 +320,14 @@ struct MapCache {
 };
 MapCache g_maps;
 
-gemm_status_t encode_2d(CUtensorMap *map, CUtensorMapDataType type, const void *base, uint64_t inner,
-                        uint64_t outer, uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer,
-                        const char *what)
+// depth > 0: a 3-D map of `depth` such matrices, depth_bytes apart, with boxes
+// of one matrix.
+gemm_status_t encode_map(CUtensorMap *map, CUtensorMapDataType type, const void *base, uint64_t inner,
+                         uint64_t outer, uint64_t row_bytes, uint64_t depth, uint64_t depth_bytes,
+                         uint32_t box_inner, uint32_t box_outer, const char *what)
 {
     const MapKey key{reinterpret_cast<uintptr_t>(base), inner, outer, row_bytes, box_inner, box_outer,
-                     static_cast<int>(type)};
+                     static_cast<int>(type), depth, depth_bytes};
     {
         std::lock_guard<std::mutex> lock(g_maps.mutex);
         auto it = g_maps.entries.find(key);
@@ -330,11 +339,11 @@ gemm_status_t encode_2d(CUtensorMap *map, CUtensorMapDataType type, const void *
     }
     EncodeTiledFn fn = encode_fn();
     if (!fn) return fail(GEMM_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
-    const cuuint64_t dims[2] = {inner, outer};
-    const cuuint64_t strides[1] = {row_bytes};
-    const cuuint32_t box[2] = {box_inner, box_outer};
-    const cuuint32_t elem_strides[2] = {1, 1};
-    CUresult r = fn(map, type, 2, const_cast<void *>(base), dims, strides, box, elem_strides,
+    const cuuint64_t dims[3] = {inner, outer, depth};
+    const cuuint64_t strides[2] = {row_bytes, depth_bytes};
+    const cuuint32_t box[3] = {box_inner, box_outer, 1};
+    const cuuint32_t elem_strides[3] = {1, 1, 1};
+    CUresult r = fn(map, type, depth ? 3 : 2, const_cast<void *>(base), dims, strides, box, elem_strides,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(GEMM_ERR_CUDA, "cuTensorMapEncodeTiled(%s) failed with %d", what, (int)r);
@@ -350,6 +359,13 @@ gemm_status_t encode_2d(CUtensorMap *map, CUtensorMapDataType type, const void *
     }
     g_maps.entries[key] = MapCache::Entry{*map, ++g_maps.clock};
     return GEMM_OK;
+}
+
+gemm_status_t encode_2d(CUtensorMap *map, CUtensorMapDataType type, const void *base, uint64_t inner,
+                        uint64_t outer, uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer,
+                        const char *what)
+{
+    return encode_map(map, type, base, inner, outer, row_bytes, 0, 0, box_inner, box_outer, what);
 }
 
 // gemm_debug_inject_stall modes -> kernel flags.
@@ -1115,6 +1131,8 @@ gemm_status_t run_quant(const void *x, int x_type, int64_t rows, int64_t cols, i
     }
 }
 
+#include "grouped_host.cuh"
+
 }  // namespace
 
 extern "C" {
@@ -1170,6 +1188,72 @@ gemm_status_t gemm_quantize_e4m3(const void *x, int x_type, int64_t rows, int64_
 {
     t_last_error[0] = '\0';
     return run_quant(x, x_type, rows, cols, ldx, q, ldq, scale, static_cast<cudaStream_t>(stream));
+}
+
+int64_t gemm_grouped_workspace(int op, int64_t E, int64_t M, int64_t K, int64_t T, const void *X, int64_t ldx,
+                               int64_t stride_x, const void *Y, int64_t ldy)
+{
+    return grouped_workspace(op, E, M, K, T, X, ldx, stride_x, Y, ldy);
+}
+
+gemm_status_t gemm_tn_grouped(int type, int64_t E, int64_t M, int64_t K, int64_t T, const void *A, int64_t lda,
+                              int64_t stride_a, const void *B, int64_t ldb, const int32_t *offsets, void *C,
+                              int64_t ldc, void *workspace, int64_t workspace_bytes, void *stream)
+{
+    t_last_error[0] = '\0';
+    GroupedCall c{"gemm_tn_grouped", GEMM_GROUPED_PRODUCT, type, type, E, M, K, T, A, lda, stride_a, B, ldb, offsets, C, ldc, 0,
+                  nullptr, nullptr, workspace, workspace_bytes, static_cast<cudaStream_t>(stream)};
+    return run_grouped(c);
+}
+
+gemm_status_t gemm_tn_grouped_grad_b(int type, int64_t E, int64_t M, int64_t K, int64_t T, const void *A, int64_t lda,
+                                     int64_t stride_a, const void *dC, int64_t lddc, const int32_t *offsets, void *dB,
+                                     int64_t lddb, void *workspace, int64_t workspace_bytes, void *stream)
+{
+    t_last_error[0] = '\0';
+    GroupedCall c{"gemm_tn_grouped_grad_b", GEMM_GROUPED_GRAD_B, type, type, E, M, K, T, A, lda, stride_a, dC, lddc, offsets, dB,
+                  lddb, 0, nullptr, nullptr, workspace, workspace_bytes, static_cast<cudaStream_t>(stream)};
+    return run_grouped(c);
+}
+
+gemm_status_t gemm_tn_grouped_grad_a(int type, int64_t E, int64_t M, int64_t K, int64_t T, const void *dC,
+                                     int64_t lddc, const void *B, int64_t ldb, const int32_t *offsets, void *dA,
+                                     int64_t ldda, int64_t stride_da, void *workspace, int64_t workspace_bytes,
+                                     void *stream)
+{
+    t_last_error[0] = '\0';
+    GroupedCall c{"gemm_tn_grouped_grad_a", GEMM_GROUPED_GRAD_A, type, type, E, M, K, T, dC, lddc, 0, B, ldb, offsets, dA, ldda,
+                  stride_da, nullptr, nullptr, workspace, workspace_bytes, static_cast<cudaStream_t>(stream)};
+    return run_grouped(c);
+}
+
+gemm_status_t gemm_i8_tn(int out_type, int64_t M, int64_t N, int64_t K, const int8_t *A, int64_t lda,
+                         const float *scale_a, const int8_t *B, int64_t ldb, const float *scale_b, void *C,
+                         int64_t ldc, void *workspace, int64_t workspace_bytes, void *stream)
+{
+    t_last_error[0] = '\0';
+    GroupedCall c{"gemm_i8_tn", GEMM_GROUPED_I8, GEMM_IN_F16, out_type, 1, M, K, N, A, lda, 0, B, ldb, nullptr, C, ldc, 0,
+                  scale_a, scale_b, workspace, workspace_bytes, static_cast<cudaStream_t>(stream)};
+    return run_grouped(c);
+}
+
+gemm_status_t gemm_i8_tn_grouped(int out_type, int64_t E, int64_t M, int64_t K, int64_t T, const int8_t *A,
+                                 int64_t lda, int64_t stride_a, const float *scale_a, const int8_t *B, int64_t ldb,
+                                 const float *scale_b, const int32_t *offsets, void *C, int64_t ldc, void *workspace,
+                                 int64_t workspace_bytes, void *stream)
+{
+    t_last_error[0] = '\0';
+    GroupedCall c{"gemm_i8_tn_grouped", GEMM_GROUPED_I8, GEMM_IN_F16, out_type, E, M, K, T, A, lda, stride_a, B, ldb, offsets, C,
+                  ldc, 0, scale_a, scale_b, workspace, workspace_bytes, static_cast<cudaStream_t>(stream)};
+    c.needs_offsets = true;
+    return run_grouped(c);
+}
+
+gemm_status_t gemm_quantize_i8_rows(const void *x, int x_type, int64_t rows, int64_t cols, int64_t ldx, int8_t *q,
+                                    int64_t ldq, float *scale, void *stream)
+{
+    t_last_error[0] = '\0';
+    return run_quant_rows(x, x_type, rows, cols, ldx, q, ldq, scale, static_cast<cudaStream_t>(stream));
 }
 
 const char *gemm_status_string(gemm_status_t s)
@@ -1302,6 +1386,10 @@ const char *gemm_debug_last_launch(void)
     const LaunchRecord &r = t_rec;
     if (!r.name)
         t_last_launch[0] = '\0';
+    else if (r.grouped)
+        snprintf(t_last_launch, sizeof(t_last_launch),
+                 "%s: ctas_per_cluster=%d grid=%d slots=%d tiles<=%d copied=%d", r.name, r.cluster, r.grid, r.slots,
+                 r.tiles, r.copied);
     else if (r.quant)
         snprintf(t_last_launch, sizeof(t_last_launch), "%s: grid=%lld units=%lld vec=%d", r.name, r.qgrid, r.qunits,
                  r.vec);

@@ -158,7 +158,7 @@ gemm_status_t gemm_f16_tn_softmax_stats(int64_t M, int64_t N, int64_t K,
                                         float *row_max, float *row_sum,
                                         void *stream);
 
-/* Element types gemm_quantize_e4m3 reads. */
+/* Element types of the quantisers' inputs, and of the grouped products. */
 typedef enum {
     GEMM_IN_F32 = 0,    /* IEEE binary32 */
     GEMM_IN_F16 = 1,    /* IEEE binary16 */
@@ -237,6 +237,122 @@ gemm_status_t gemm_f16_tn_noalloc(int64_t M, int64_t N, int64_t K,
                                   const void *B, int64_t ldb,
                                   void *C, int64_t ldc,
                                   void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Products grouped by expert.
+ *
+ * E experts hold one M x K matrix A_e each; T rows of B (T x K, row-major: the
+ * columns of the TN product's B, one per token) are sorted by expert.  Expert
+ * e's rows are those with offsets[e] <= t < offsets[e+1], offsets being E + 1
+ * ascending 32-bit row numbers in DEVICE memory (read when the kernels run, so
+ * an earlier kernel on the stream may write them):
+ *
+ *     gemm_tn_grouped         C[t,m]    = sum_k A_e[m,k] B[t,k]        (t of e)
+ *     gemm_tn_grouped_grad_b  dB[t,k]   = sum_m dC[t,m] A_e[m,k]       (t of e)
+ *     gemm_tn_grouped_grad_a  dA_e[m,k] = sum_{t of e} dC[t,m] B[t,k]
+ *
+ * A_e's element (m,k) is at A[e*stride_a + m*lda + k]; B, C and dC are T rows
+ * with leading dimensions ldb, ldc and lddc (C row t is column t of the
+ * column-major product, as in gemm_f16_tn).  `type` is GEMM_IN_F16 or
+ * GEMM_IN_BF16, the type of every operand and of the result.  Sums are FP32
+ * (their order does not depend on timing) and rounded once.
+ *
+ * An expert may have no rows: its dA is written as zeros.  Rows before
+ * offsets[0] and from offsets[E] on belong to no expert: they are not read, and
+ * their rows of C and dB are left as they were.  Values of one expert's rows
+ * never reach another's results, infinities and NaNs included.  Offsets that
+ * descend, are negative or pass T are read as if each were at least the ones
+ * before it and at most T.  K == 0 (M == 0 for grad_b) writes zeros to the
+ * experts' rows.  At most 1024 experts.
+ *
+ * Workspace: an operand that the TMA cannot address in place (base, row stride
+ * or expert stride not a multiple of 16 bytes, or a row along the sum whose
+ * length is not one) is first copied into the workspace, and grad_a keeps two
+ * tensor maps per expert there.  gemm_grouped_workspace returns the bytes a
+ * call with the same arguments needs (often 0: NULL will do).  The caller owns
+ * the workspace (256-byte aligned); it may be used again, or freed in stream
+ * order, once the call's kernels have run.  These calls keep no buffer of the
+ * library's: calls and captured graphs that overlap need workspaces of their
+ * own and nothing else.
+ *
+ * Errors: GEMM_ERR_INVALID_ARG for an unknown type, a negative size or stride,
+ * a leading dimension below its row's length, overlapping dA_e, NULL or
+ * misaligned pointers with work to do, or a workspace that is too small;
+ * GEMM_ERR_UNSUPPORTED off sm_103, for more than 1024 experts, sizes beyond
+ * 2^31 - 256 or 2^30 result tiles; GEMM_ERR_CUDA on a failed launch.
+ */
+typedef enum {
+    GEMM_GROUPED_PRODUCT = 0,   /* X = A,  Y = B */
+    GEMM_GROUPED_GRAD_B = 1,    /* X = A,  Y = dC */
+    GEMM_GROUPED_GRAD_A = 2,    /* X = dC, Y = B (stride_x is not used) */
+    GEMM_GROUPED_I8 = 3         /* X = A,  Y = B; gemm_i8_tn has E = 1 */
+} gemm_grouped_op_t;
+
+/* Workspace bytes of a call, -1 for arguments that it would refuse. */
+int64_t gemm_grouped_workspace(int op, int64_t E, int64_t M, int64_t K, int64_t T,
+                               const void *X, int64_t ldx, int64_t stride_x,
+                               const void *Y, int64_t ldy);
+
+gemm_status_t gemm_tn_grouped(int type, int64_t E, int64_t M, int64_t K, int64_t T,
+                              const void *A, int64_t lda, int64_t stride_a,
+                              const void *B, int64_t ldb, const int32_t *offsets,
+                              void *C, int64_t ldc,
+                              void *workspace, int64_t workspace_bytes, void *stream);
+
+gemm_status_t gemm_tn_grouped_grad_b(int type, int64_t E, int64_t M, int64_t K, int64_t T,
+                                     const void *A, int64_t lda, int64_t stride_a,
+                                     const void *dC, int64_t lddc, const int32_t *offsets,
+                                     void *dB, int64_t lddb,
+                                     void *workspace, int64_t workspace_bytes, void *stream);
+
+gemm_status_t gemm_tn_grouped_grad_a(int type, int64_t E, int64_t M, int64_t K, int64_t T,
+                                     const void *dC, int64_t lddc,
+                                     const void *B, int64_t ldb, const int32_t *offsets,
+                                     void *dA, int64_t ldda, int64_t stride_da,
+                                     void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * Products of 8-bit integers with a scale for each channel m and each token:
+ *
+ *     gemm_i8_tn          C[n,m] = out((S * scale_a[m]) * scale_b[n]),     S = sum_k A[m,k] B[n,k]
+ *     gemm_i8_tn_grouped  the same for every expert's rows, scale_a being E x M
+ *
+ * A, B: signed 8-bit integers, all 256 values; C: N (or T) rows of M, out_type
+ * GEMM_IN_F16 or GEMM_IN_BF16.  scale_a, scale_b: fp32 in device memory, 4-byte
+ * aligned.  GB300's tensor cores multiply 8-bit integers far below their FP16
+ * rate, so the integers are widened to FP16, which holds each of them exactly;
+ * products are exact and S is an FP32 sum, exact while it stays below 2^24.
+ * The result is rounded once.  Everything else (offsets, rows of no expert,
+ * workspace with op GEMM_GROUPED_I8, errors) is as for gemm_tn_grouped.
+ */
+gemm_status_t gemm_i8_tn(int out_type, int64_t M, int64_t N, int64_t K,
+                         const int8_t *A, int64_t lda, const float *scale_a,
+                         const int8_t *B, int64_t ldb, const float *scale_b,
+                         void *C, int64_t ldc,
+                         void *workspace, int64_t workspace_bytes, void *stream);
+
+gemm_status_t gemm_i8_tn_grouped(int out_type, int64_t E, int64_t M, int64_t K, int64_t T,
+                                 const int8_t *A, int64_t lda, int64_t stride_a, const float *scale_a,
+                                 const int8_t *B, int64_t ldb, const float *scale_b, const int32_t *offsets,
+                                 void *C, int64_t ldc,
+                                 void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * 8-bit integer quantisation with one scale per row (a token of activations, or
+ * a channel of weights):
+ *
+ *     amax     = max_c |x[r,c]|
+ *     scale[r] = amax / 127                        fp32
+ *     q[r,c]   = round(127 x[r,c] / amax)          of the exact quotient, ties to even
+ *
+ * x, x_type, ldx as for gemm_quantize_e4m3; q: rows x cols, q[r*ldq + c]; scale:
+ * `rows` floats.  A row of zeros, or cols == 0, has scale 0 (and codes 0).  A
+ * row with an infinity or a NaN has scale NaN and codes 0: a product with it is
+ * NaN in that row only.  rows == 0 writes nothing.  One launch, no buffer.
+ * Errors as for gemm_quantize_e4m3.
+ */
+gemm_status_t gemm_quantize_i8_rows(const void *x, int x_type, int64_t rows, int64_t cols, int64_t ldx,
+                                    int8_t *q, int64_t ldq, float *scale, void *stream);
 
 /* Human-readable name of a status code (static storage). */
 const char *gemm_status_string(gemm_status_t status);
