@@ -514,11 +514,19 @@ def _experts(t, dtype, name, shape=None):
 
 def _vector(t, dtype, n, name):
     import torch
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != (n,) or not t.is_contiguous():
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape ({n},)")
 
 
-def _same_device(device, tensors):
+def _tokens(t, dtype, cols, name):
+    """Row stride of a 2-D tensor of `cols` columns (rows contiguous)."""
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.shape[1] != cols:
+        raise ValueError(f"{name} must be a 2-D torch tensor with {cols} columns")
+    return _rows(t, dtype, name, cuda=False)
+
+
+def _same_device(device, **tensors):
     if device.type != "cuda":
         raise ValueError("the tensors must be CUDA tensors")
     for name, t in tensors.items():
@@ -526,28 +534,35 @@ def _same_device(device, tensors):
             raise ValueError(f"{name} is on {t.device}, not on {device}")
 
 
-def _call(device, stream, op, sizes, X, ldx, stride_x, Y, ldy, launch):
-    """launch(workspace, bytes, stream) on `device`, with a workspace from torch's
-    allocator that belongs to the stream (so that it is used again only after
-    this call's kernels)."""
+def _launch_stream(device, stream):
+    """The stream's handle (None: torch's current stream of `device`)."""
     import torch
-    if torch.cuda.current_device() != device.index:
-        with torch.cuda.device(device):
-            return _call(device, stream, op, sizes, X, ldx, stride_x, Y, ldy, launch)
-    n = gemm_grouped_workspace(op, *sizes, X, ldx, stride_x, Y, ldy)
-    if n == 0:
-        return launch(None, 0, stream)
     if stream is None:
-        return launch(torch.empty(n, dtype=torch.uint8, device=device), n, None)
-    own = stream if not isinstance(stream, int) else torch.cuda.ExternalStream(stream, device=device)
-    with torch.cuda.stream(own):
-        workspace = torch.empty(n, dtype=torch.uint8, device=device)
-    return launch(workspace, n, stream)
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return stream if isinstance(stream, int) else int(stream.cuda_stream)
 
 
-def _offsets(offsets, E):
+def _workspace(device, stream, op, sizes, X, ldx, stride_x, Y, ldy):
+    """(address, bytes) of a workspace and the tensor that holds it.  It comes from
+    torch's allocator and belongs to the call's stream, so it is used again only
+    after the call's kernels."""
     import torch
-    _vector(offsets, torch.int32, E + 1, "offsets")
+    n = calls.gemm_grouped_workspace(op, *sizes, X, ldx, stride_x, Y, ldy)
+    if n <= 0:                      # (refused arguments are refused, with their reason, by the call itself)
+        return None, 0, None
+    if stream is None:
+        held = torch.empty(n, dtype=torch.uint8, device=device)
+    else:
+        own = stream if not isinstance(stream, int) else torch.cuda.ExternalStream(stream, device=device)
+        with torch.cuda.stream(own):
+            held = torch.empty(n, dtype=torch.uint8, device=device)
+    return held.data_ptr(), n, held
+
+
+def _elsewhere(device):
+    """Whether `device` is not the calling thread's current one (which the C ABI works on)."""
+    import torch
+    return torch.cuda.current_device() != device.index
 
 
 def tn_grouped(A, Bt, offsets, C=None, stream=None):
@@ -556,16 +571,20 @@ def tn_grouped(A, Bt, offsets, C=None, stream=None):
     A, Bt and C (T, M) are all fp16 or all bf16, their rows contiguous.  Rows of
     no expert are not written."""
     import torch
-    kind = _half_type(A.dtype, "A")
     lda, stride_a = _experts(A, A.dtype, "A")
+    kind, device = _half_type(A.dtype, "A"), A.device
     E, M, K = A.shape
-    ldb = _rows(Bt, A.dtype, "Bt", (Bt.shape[0], K) if isinstance(Bt, torch.Tensor) and Bt.dim() == 2 else None, cuda=False)
-    T = Bt.shape[0]
-    _offsets(offsets, E)
-    _same_device(A.device, {"A": A, "Bt": Bt, "offsets": offsets})
-    C, ldc = _output(C, M, T, A.dtype, A.device)
-    _call(A.device, stream, GEMM_GROUPED_PRODUCT, (E, M, K, T), A, lda, stride_a, Bt, ldb,
-          lambda ws, n, s: gemm_tn_grouped(kind, E, M, K, T, A, lda, stride_a, Bt, ldb, offsets, C, ldc, ws, n, s))
+    ldb, T = _tokens(Bt, A.dtype, K, "Bt"), Bt.shape[0]
+    _vector(offsets, torch.int32, E + 1, "offsets")
+    _same_device(device, Bt=Bt, offsets=offsets)
+    if _elsewhere(device):
+        with torch.cuda.device(device):
+            return tn_grouped(A, Bt, offsets, C, stream)
+    C, ldc = _output(C, M, T, A.dtype, device)
+    a, b = A.data_ptr(), Bt.data_ptr()
+    ws, n, held = _workspace(device, stream, GEMM_GROUPED_PRODUCT, (E, M, K, T), a, lda, stride_a, b, ldb)
+    _check(calls.gemm_tn_grouped(kind, E, M, K, T, a, lda, stride_a, b, ldb, offsets.data_ptr(), C.data_ptr(), ldc, ws,
+                                 n, _launch_stream(device, stream)))
     return C
 
 
@@ -573,20 +592,20 @@ def tn_grouped_grad_b(A, dCt, offsets, dBt=None, stream=None):
     """The gradient of tn_grouped for Bt: dBt[t] = A[e]^T dC^T[t], with dCt (T, M)
     -> (T, K).  Rows of no expert are not written."""
     import torch
-    kind = _half_type(A.dtype, "A")
     lda, stride_a = _experts(A, A.dtype, "A")
+    kind, device = _half_type(A.dtype, "A"), A.device
     E, M, K = A.shape
-    ldd = _rows(dCt, A.dtype, "dCt", (dCt.shape[0], M) if isinstance(dCt, torch.Tensor) and dCt.dim() == 2 else None, cuda=False)
-    T = dCt.shape[0]
-    _offsets(offsets, E)
-    _same_device(A.device, {"A": A, "dCt": dCt, "offsets": offsets})
-    if dBt is None:
-        dBt = torch.empty((T, K), dtype=A.dtype, device=A.device)
-    ldb = _rows(dBt, A.dtype, "dBt", (T, K))
-    _same_device(A.device, {"dBt": dBt})
-    _call(A.device, stream, GEMM_GROUPED_GRAD_B, (E, M, K, T), A, lda, stride_a, dCt, ldd,
-          lambda ws, n, s: gemm_tn_grouped_grad_b(kind, E, M, K, T, A, lda, stride_a, dCt, ldd, offsets, dBt, ldb, ws,
-                                                  n, s))
+    ldd, T = _tokens(dCt, A.dtype, M, "dCt"), dCt.shape[0]
+    _vector(offsets, torch.int32, E + 1, "offsets")
+    _same_device(device, dCt=dCt, offsets=offsets)
+    if _elsewhere(device):
+        with torch.cuda.device(device):
+            return tn_grouped_grad_b(A, dCt, offsets, dBt, stream)
+    dBt, ldb = _output(dBt, K, T, A.dtype, device)
+    a, d = A.data_ptr(), dCt.data_ptr()
+    ws, n, held = _workspace(device, stream, GEMM_GROUPED_GRAD_B, (E, M, K, T), a, lda, stride_a, d, ldd)
+    _check(calls.gemm_tn_grouped_grad_b(kind, E, M, K, T, a, lda, stride_a, d, ldd, offsets.data_ptr(), dBt.data_ptr(),
+                                        ldb, ws, n, _launch_stream(device, stream)))
     return dBt
 
 
@@ -596,38 +615,49 @@ def tn_grouped_grad_a(dCt, Bt, offsets, dA=None, stream=None):
     an expert without rows."""
     import torch
     if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.shape[0] < 1:
-        raise ValueError("offsets must be a 1-D tensor of experts + 1 rows")
+        raise ValueError("offsets must be a 1-D tensor of experts + 1 row numbers")
+    if not isinstance(dCt, torch.Tensor) or dCt.dim() != 2 or not isinstance(Bt, torch.Tensor) or Bt.dim() != 2:
+        raise ValueError("dCt and Bt must be 2-D torch tensors")
+    E, device, (T, M), K = offsets.shape[0] - 1, dCt.device, dCt.shape, Bt.shape[1]
     kind = _half_type(dCt.dtype, "dCt")
-    ldd = _rows(dCt, dCt.dtype, "dCt", cuda=False)
-    T, M = dCt.shape
-    ldb = _rows(Bt, dCt.dtype, "Bt", (T, Bt.shape[1]) if isinstance(Bt, torch.Tensor) and Bt.dim() == 2 else None, cuda=False)
-    K, E = Bt.shape[1], offsets.shape[0] - 1
-    _offsets(offsets, E)
-    _same_device(dCt.device, {"dCt": dCt, "Bt": Bt, "offsets": offsets})
+    ldd, ldb = _tokens(dCt, dCt.dtype, M, "dCt"), _tokens(Bt, dCt.dtype, K, "Bt")
+    if Bt.shape[0] != T:
+        raise ValueError(f"dCt has {T} rows and Bt {Bt.shape[0]}")
+    _vector(offsets, torch.int32, E + 1, "offsets")
+    _same_device(device, Bt=Bt, offsets=offsets)
+    if _elsewhere(device):
+        with torch.cuda.device(device):
+            return tn_grouped_grad_a(dCt, Bt, offsets, dA, stream)
     if dA is None:
-        dA = torch.empty((E, M, K), dtype=dCt.dtype, device=dCt.device)
+        dA = torch.empty((E, M, K), dtype=dCt.dtype, device=device)
     ldda, stride_da = _experts(dA, dCt.dtype, "dA", (E, M, K))
-    _same_device(dCt.device, {"dA": dA})
-    _call(dCt.device, stream, GEMM_GROUPED_GRAD_A, (E, M, K, T), dCt, ldd, 0, Bt, ldb,
-          lambda ws, n, s: gemm_tn_grouped_grad_a(kind, E, M, K, T, dCt, ldd, Bt, ldb, offsets, dA, ldda, stride_da, ws,
-                                                  n, s))
+    _same_device(device, dA=dA)
+    d, b = dCt.data_ptr(), Bt.data_ptr()
+    ws, n, held = _workspace(device, stream, GEMM_GROUPED_GRAD_A, (E, M, K, T), d, ldd, 0, b, ldb)
+    _check(calls.gemm_tn_grouped_grad_a(kind, E, M, K, T, d, ldd, b, ldb, offsets.data_ptr(), dA.data_ptr(), ldda,
+                                        stride_da, ws, n, _launch_stream(device, stream)))
     return dA
 
 
 def i8_tn(A, Bt, scale_a, scale_b, C=None, dtype=None, stream=None):
     """C^T[n, m] = scale_a[m] scale_b[n] sum_k A[m, k] Bt[n, k]: A (M, K) and Bt
     (N, K) int8, scale_a (M,) and scale_b (N,) fp32 -> (N, M) of `dtype`
-    (torch.float16 unless C or dtype says torch.bfloat16)."""
+    (torch.float16, unless C or dtype says torch.bfloat16)."""
     import torch
     M, N, K, lda, ldb = _operands(A, Bt, torch.int8)
     _vector(scale_a, torch.float32, M, "scale_a")
     _vector(scale_b, torch.float32, N, "scale_b")
-    dtype = dtype or (torch.float16 if C is None else C.dtype)
+    dtype, device = dtype or (torch.float16 if C is None else C.dtype), A.device
     kind = _half_type(dtype, "dtype")
-    _same_device(A.device, {"scale_a": scale_a, "scale_b": scale_b})
-    C, ldc = _output(C, M, N, dtype, A.device)
-    _call(A.device, stream, GEMM_GROUPED_I8, (1, M, K, N), A, lda, 0, Bt, ldb,
-          lambda ws, n, s: gemm_i8_tn(kind, M, N, K, A, lda, scale_a, Bt, ldb, scale_b, C, ldc, ws, n, s))
+    _same_device(device, scale_a=scale_a, scale_b=scale_b)
+    if _elsewhere(device):
+        with torch.cuda.device(device):
+            return i8_tn(A, Bt, scale_a, scale_b, C, dtype, stream)
+    C, ldc = _output(C, M, N, dtype, device)
+    a, b = A.data_ptr(), Bt.data_ptr()
+    ws, n, held = _workspace(device, stream, GEMM_GROUPED_I8, (1, M, K, N), a, lda, 0, b, ldb)
+    _check(calls.gemm_i8_tn(kind, M, N, K, a, lda, scale_a.data_ptr(), b, ldb, scale_b.data_ptr(), C.data_ptr(), ldc, ws,
+                            n, _launch_stream(device, stream)))
     return C
 
 
@@ -637,20 +667,23 @@ def i8_tn_grouped(A, Bt, scale_a, scale_b, offsets, C=None, dtype=None, stream=N
     import torch
     lda, stride_a = _experts(A, torch.int8, "A")
     E, M, K = A.shape
-    ldb = _rows(Bt, torch.int8, "Bt", (Bt.shape[0], K) if isinstance(Bt, torch.Tensor) and Bt.dim() == 2 else None, cuda=False)
-    T = Bt.shape[0]
-    if not isinstance(scale_a, torch.Tensor) or scale_a.shape != (E, M):
-        raise ValueError(f"scale_a must have shape {(E, M)}")
-    _vector(scale_a.reshape(-1) if scale_a.is_contiguous() else scale_a, torch.float32, E * M, "scale_a")
+    ldb, T = _tokens(Bt, torch.int8, K, "Bt"), Bt.shape[0]
+    if (not isinstance(scale_a, torch.Tensor) or scale_a.dtype != torch.float32 or tuple(scale_a.shape) != (E, M)
+            or not scale_a.is_contiguous()):
+        raise ValueError(f"scale_a must be a contiguous torch.float32 tensor of shape {(E, M)}")
     _vector(scale_b, torch.float32, T, "scale_b")
-    _offsets(offsets, E)
-    _same_device(A.device, {"Bt": Bt, "scale_a": scale_a, "scale_b": scale_b, "offsets": offsets})
-    dtype = dtype or (torch.float16 if C is None else C.dtype)
+    _vector(offsets, torch.int32, E + 1, "offsets")
+    dtype, device = dtype or (torch.float16 if C is None else C.dtype), A.device
     kind = _half_type(dtype, "dtype")
-    C, ldc = _output(C, M, T, dtype, A.device)
-    _call(A.device, stream, GEMM_GROUPED_I8, (E, M, K, T), A, lda, stride_a, Bt, ldb,
-          lambda ws, n, s: gemm_i8_tn_grouped(kind, E, M, K, T, A, lda, stride_a, scale_a, Bt, ldb, scale_b, offsets, C,
-                                              ldc, ws, n, s))
+    _same_device(device, Bt=Bt, scale_a=scale_a, scale_b=scale_b, offsets=offsets)
+    if _elsewhere(device):
+        with torch.cuda.device(device):
+            return i8_tn_grouped(A, Bt, scale_a, scale_b, offsets, C, dtype, stream)
+    C, ldc = _output(C, M, T, dtype, device)
+    a, b = A.data_ptr(), Bt.data_ptr()
+    ws, n, held = _workspace(device, stream, GEMM_GROUPED_I8, (E, M, K, T), a, lda, stride_a, b, ldb)
+    _check(calls.gemm_i8_tn_grouped(kind, E, M, K, T, a, lda, stride_a, scale_a.data_ptr(), b, ldb, scale_b.data_ptr(),
+                                    offsets.data_ptr(), C.data_ptr(), ldc, ws, n, _launch_stream(device, stream)))
     return C
 
 
@@ -662,10 +695,13 @@ def quantize_i8_rows(x, stream=None):
     types = {torch.float32: GEMM_IN_F32, torch.float16: GEMM_IN_F16, torch.bfloat16: GEMM_IN_BF16}
     if not isinstance(x, torch.Tensor) or x.dtype not in types or x.dim() != 2:
         raise ValueError("x must be a 2-D float32/float16/bfloat16 tensor")
-    ldx = _rows(x, x.dtype, "x")
+    ldx, device = _rows(x, x.dtype, "x"), x.device
+    if _elsewhere(device):
+        with torch.cuda.device(device):
+            return quantize_i8_rows(x, stream)
     rows, cols = x.shape
-    q = torch.empty((rows, cols), dtype=torch.int8, device=x.device)
-    scale = torch.empty(rows, dtype=torch.float32, device=x.device)
-    with _on(x.device):
-        gemm_quantize_i8_rows(x, types[x.dtype], rows, cols, ldx, q, max(cols, 1), scale, stream)
+    q = torch.empty((rows, cols), dtype=torch.int8, device=device)
+    scale = torch.empty(rows, dtype=torch.float32, device=device)
+    _check(calls.gemm_quantize_i8_rows(x.data_ptr(), types[x.dtype], rows, cols, ldx, q.data_ptr(), max(cols, 1),
+                                       scale.data_ptr(), _launch_stream(device, stream)))
     return q, scale

@@ -185,7 +185,6 @@ gemm_status_t launch_grouped_op(const GroupedCall &c, DeviceState &dev, tn::Grou
     // Few rows per expert: bound by the read of the weights, on single CTAs of
     // 128 x 64 tiles (twice as many of them, and a deeper ring); else CTA pairs.
     const bool few = kOp != tn::kGrGradA && c.T <= 64 * c.E;
-    const uint32_t rows_r = few ? 64 : 128;
     gemm_status_t st;
     if (prm.red > 0) {
         const CUtensorMapDataType type =
@@ -219,8 +218,9 @@ gemm_status_t launch_grouped_op(const GroupedCall &c, DeviceState &dev, tn::Grou
             const uint64_t apart = c.E > 1 ? uint64_t(stride_x) * 2 : uint64_t(16);
             if ((st = encode_map(&prm.tmap_l, type, x, inner_x, c.M, ldx * 2, c.E, apart, 64, box_l, "A")) != GEMM_OK)
                 return st;
-            if ((st = encode_2d(&prm.tmap_r, type, y, inner_y, c.T, ldy * 2, 64, rows_r, "rows")) != GEMM_OK) return st;
-            if ((st = encode_2d(&prm.tmap_r16, type, y, inner_y, c.T, ldy * 2, 64, 16, "rows")) != GEMM_OK) return st;
+            for (int i = 0; i < (few ? 3 : 4); ++i)
+                if ((st = encode_2d(&prm.tmap_r[i], type, y, inner_y, c.T, ldy * 2, 64, 16u << i, "rows")) != GEMM_OK)
+                    return st;
         }
     }
     if constexpr (kOp != tn::kGrGradA) {
@@ -321,6 +321,7 @@ gemm_status_t run_grouped(const GroupedCall &c)
     prm.red = static_cast<int32_t>(red);
     prm.fmt = c.type == GEMM_IN_BF16 ? 1u : 0u;
     prm.out_fmt = c.out_type == GEMM_IN_BF16 ? 1u : 0u;
+    prm.out_vec = reinterpret_cast<uintptr_t>(c.out) % 16 == 0 && c.ldo % 8 == 0 && (!grad_a || c.stride_o % 8 == 0);
     prm.scale_l = c.scale_a;
     prm.scale_r = c.scale_b;
     prm.flags = stall_flags(g_inject_stall.load());
@@ -335,30 +336,43 @@ gemm_status_t run_grouped(const GroupedCall &c)
     return st;
 }
 
+// Launches the row quantiser: a warp per row up to 8 windows of 16 bytes a lane
+// (4 KiB of x), unless the rows are too few to fill the SMs that way; then a
+// CTA of 256 or 512 threads with up to 8 windows a thread (32 and 64 KiB);
+// beyond that the kernel that reads x twice.
 template <int kIn>
 gemm_status_t launch_quant_rows(DeviceState &dev, const qz::QuantRowsParams &prm, cudaStream_t stream)
 {
-    auto kernel = qz::quant_rows_kernel<kIn>;
-    int per_sm;
-    {
-        std::lock_guard<std::mutex> lock(g_mutex);
-        if (dev.quant_rows_blocks[kIn] == 0) {
-            int n = 0;
-            cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, qz::kRowThreads, 0);
-            if (e != cudaSuccess || n <= 0)
-                return fail(GEMM_ERR_CUDA, "gemm_quantize_i8_rows: occupancy query: %s", cudaGetErrorString(e));
-            dev.quant_rows_blocks[kIn] = n;
-        }
-        per_sm = dev.quant_rows_blocks[kIn];
+    constexpr int64_t kElem = qz::elem_bytes(kIn), kVec = 16 / kElem;
+    const bool aligned = reinterpret_cast<uintptr_t>(prm.x) % 16 == 0 && reinterpret_cast<uintptr_t>(prm.q) % kVec == 0 &&
+                         (prm.rows == 1 || ((prm.ldx * kElem) % 16 == 0 && prm.ldq % kVec == 0));
+    const int64_t windows = (prm.cols + kVec - 1) / kVec + (aligned ? 0 : 1);
+    void (*kernel)(qz::QuantRowsParams);
+    int threads = qz::kRowThreads, rows_per_cta = 1;
+    const bool long_rows = windows > 512 * 8;
+    if (windows <= 32 * 8 && prm.rows > 8 * dev.sms) {
+        kernel = aligned ? qz::quant_rows_kernel<kIn, 32, 8, true> : qz::quant_rows_kernel<kIn, 32, 8, false>;
+        rows_per_cta = qz::kRowThreads / 32;
+    } else if (windows <= 256 * 4) {
+        kernel = aligned ? qz::quant_rows_kernel<kIn, 256, 4, true> : qz::quant_rows_kernel<kIn, 256, 4, false>;
+    } else if (windows <= 256 * 8) {
+        kernel = aligned ? qz::quant_rows_kernel<kIn, 256, 8, true> : qz::quant_rows_kernel<kIn, 256, 8, false>;
+    } else if (!long_rows) {
+        kernel = aligned ? qz::quant_rows_kernel<kIn, 512, 8, true> : qz::quant_rows_kernel<kIn, 512, 8, false>;
+        threads = 512;
+    } else {
+        kernel = qz::quant_long_rows_kernel<kIn>;
+        threads = qz::kLongThreads;
     }
-    int64_t grid = int64_t(per_sm) * dev.sms;
-    if (grid > prm.rows) grid = prm.rows;
+    int64_t grid = (prm.rows + rows_per_cta - 1) / rows_per_cta;
+    if (long_rows && grid > int64_t(dev.sms) * 4) grid = int64_t(dev.sms) * 4;
+    if (grid > INT32_MAX) return fail(GEMM_ERR_UNSUPPORTED, "gemm_quantize_i8_rows: too many rows");
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
-    cfg.blockDim = dim3(qz::kRowThreads, 1, 1);
+    cfg.blockDim = dim3(threads, 1, 1);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
@@ -367,6 +381,7 @@ gemm_status_t launch_quant_rows(DeviceState &dev, const qz::QuantRowsParams &prm
     t_rec.quant = true;
     t_rec.qgrid = grid;
     t_rec.qunits = prm.rows;
+    t_rec.vec = aligned;
     cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, prm);
     if (e != cudaSuccess) return fail(GEMM_ERR_CUDA, "gemm_quantize_i8_rows: launch: %s", cudaGetErrorString(e));
     return GEMM_OK;

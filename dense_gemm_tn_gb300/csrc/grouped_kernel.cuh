@@ -38,8 +38,10 @@
 namespace tn {
 
 constexpr int kGrMaxExperts = 1024;
-constexpr int kGrBlock = 64;                 // terms of the sum per stage: 128 bytes of 16-bit elements
+constexpr int kGrBlock = 64;                 // terms of the sum per block: 128 bytes of 16-bit elements
 constexpr int kGrRaster = 8;                 // R tiles per raster group
+constexpr int kGrChunk = 32;                 // accumulator columns per epilogue step
+constexpr int kGrStageBytes = kGrChunk * 64; // one epilogue warp's staging: 32 rows of 32 16-bit results
 
 enum GroupedOp : int { kGrProduct = 0, kGrGradB = 1, kGrGradA = 2 };
 
@@ -51,23 +53,28 @@ struct GroupedCfg {
     static constexpr int kTileL = kRowsL * kGroup;
     static constexpr int kLBytes = kRowsL * 128;
     static constexpr int kRBytes = kRowsR * 128;
-    static constexpr int kStageBytes = kLBytes + kRBytes;
+    static constexpr int kBlockBytes = kLBytes + kRBytes;
+    // Blocks per stage, each with a barrier of its own that its loads complete on;
+    // the stage is given back as a whole.  Pairs: two (see TileCfg on long stages).
+    static constexpr int kAtoms = kGroup;
+    static constexpr int kStageBytes = kAtoms * kBlockBytes;
     static constexpr int kStages = 196608 / kStageBytes;
     static constexpr int kGran = 16 * kGroup;                // the MMA's N is a multiple of it
     static constexpr uint32_t kAccCols = kRows;
     static constexpr uint32_t kTmemCols = 2 * kAccCols;      // two accumulators: an epilogue overlaps the next tile
-    // full[S], empty[S], accfull[2], accempty[2], drain, never
-    static constexpr int kNumBarriers = 2 * kStages + 6;
+    // full[S][atoms], empty[S], accfull[2], accempty[2], drain, never
+    static constexpr int kNumBarriers = (kAtoms + 1) * kStages + 6;
     static constexpr int kTables = 2 * (kGrMaxExperts + 8) * 4;   // group starts, units before each group
-    static constexpr int kSmemBytes =
-        1024 /* alignment slack */ + kStages * kStageBytes + kNumBarriers * 8 + 32 + kStages * 4 + kTables;
+    static constexpr int kStaging = kEpiWarps * kGrStageBytes;
+    static constexpr int kSmemBytes = 1024 /* alignment slack */ + kStages * kStageBytes + kStaging + kNumBarriers * 8 +
+                                      32 + kStages * kAtoms * 4 + kTables;
     static_assert(kSmemBytes <= 232448, "exceeds the 227 KiB shared memory of one CTA");
 };
 
 struct GroupedParams {
-    // product: L {K, M, E} box {64, 128, 1}, R {K, T} boxes {64, kRowsR} and {64, 16};
-    // grad_b:  L {K, M, E} box {64, 64, 1},  R {M, T} boxes {64, kRowsR} and {64, 16}
-    CUtensorMap tmap_l, tmap_r, tmap_r16;
+    // product: L {K, M, E} box {64, 128, 1}, R {K, T} boxes {64, 16 << i};
+    // grad_b:  L {K, M, E} box {64, 64, 1},  R {M, T} boxes {64, 16 << i}
+    CUtensorMap tmap_l, tmap_r[4];
     const CUtensorMap *group_maps;   // grad_a: [E][2], R {M, T_e} and L {K, T_e}, boxes {64, 64}
     const int32_t *offsets;          // E + 1 row starts, or NULL: one group of all T rows
     uint16_t *out;                   // row r of group e's range at out + e * out_stride + r * out_ld
@@ -77,6 +84,7 @@ struct GroupedParams {
     int32_t r_extent;                // grad_a: the result's rows per expert (M)
     int32_t red;                     // terms of the sum (grad_a: the group's rows instead)
     uint32_t fmt, out_fmt;           // operands and result: 0 f16, 1 bf16
+    uint32_t out_vec;                // every row of the result starts on a 16-byte boundary
     const float *scale_l;            // 8-bit product: [E][l_extent] and [T] (else NULL)
     const float *scale_r;
     uint32_t flags;                  // kFlagStall* (test hooks)
@@ -226,31 +234,34 @@ template <int kOp, int kGroup, int kRows>
 __global__ void __launch_bounds__(kThreads, 1) tn_grouped_kernel(const __grid_constant__ GroupedParams p)
 {
     using Cfg = GroupedCfg<kGroup, kRows>;
-    constexpr int kStages = Cfg::kStages;
+    constexpr int kStages = Cfg::kStages, kAtoms = Cfg::kAtoms;
     constexpr bool kLMajorK = kOp == kGrProduct, kRMajorK = kOp != kGrGradA;
 
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t s_ring = ptx::smem_addr(smem);
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kStages * Cfg::kStageBytes);
+    const uint32_t s_staging = s_ring + kStages * Cfg::kStageBytes;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kStages * Cfg::kStageBytes + Cfg::kStaging);
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + Cfg::kNumBarriers);
     volatile uint32_t *abort_flag = tmem_holder + 1;
     volatile uint32_t *issued_count = tmem_holder + 2;    // fills this CTA's producer issued
     volatile uint32_t *producer_done = tmem_holder + 3;   // set once this CTA's producer issues no more
-    volatile uint32_t *fill_bytes = tmem_holder + 8;      // [kStages]: this CTA's bytes of the stage's last fill
-    int32_t *start = reinterpret_cast<int32_t *>(tmem_holder + 8 + kStages);
+    // [kStages][kAtoms]: this CTA's bytes of the block in the stage's last fill
+    volatile uint32_t *fill_bytes = tmem_holder + 8;
+    int32_t *start = reinterpret_cast<int32_t *>(tmem_holder + 8 + kStages * kAtoms);
     int32_t *before = start + kGrMaxExperts + 8;
     const uint32_t abort_addr = ptx::smem_addr(const_cast<uint32_t *>(abort_flag));
     const uint32_t count_addr = ptx::smem_addr(const_cast<uint32_t *>(issued_count));
     const uint32_t done_addr = ptx::smem_addr(const_cast<uint32_t *>(producer_done));
     const uint32_t fill_addr = ptx::smem_addr(const_cast<uint32_t *>(fill_bytes));
     const uint32_t bar0 = ptx::smem_addr(bars);
-    auto full_bar = [&](int s) { return bar0 + 8u * s; };
-    auto empty_bar = [&](int s) { return bar0 + 8u * (kStages + s); };
-    auto accfull_bar = [&](int b) { return bar0 + 8u * (2 * kStages + b); };
-    auto accempty_bar = [&](int b) { return bar0 + 8u * (2 * kStages + 2 + b); };
-    const uint32_t drain_bar = bar0 + 8u * (2 * kStages + 4);
-    const uint32_t never_bar = bar0 + 8u * (2 * kStages + 5);   // nothing ever arrives (test stalls)
+    constexpr int kEmpty0 = kStages * kAtoms, kAcc0 = kEmpty0 + kStages;
+    auto full_bar = [&](int s, int a) { return bar0 + 8u * (s * kAtoms + a); };
+    auto empty_bar = [&](int s) { return bar0 + 8u * (kEmpty0 + s); };
+    auto accfull_bar = [&](int b) { return bar0 + 8u * (kAcc0 + b); };
+    auto accempty_bar = [&](int b) { return bar0 + 8u * (kAcc0 + 2 + b); };
+    const uint32_t drain_bar = bar0 + 8u * (kAcc0 + 4);
+    const uint32_t never_bar = bar0 + 8u * (kAcc0 + 5);   // nothing ever arrives (test stalls)
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -258,9 +269,11 @@ __global__ void __launch_bounds__(kThreads, 1) tn_grouped_kernel(const __grid_co
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
-            ptx::mbar_init(full_bar(s), 1);
+            for (int a = 0; a < kAtoms; ++a) {
+                ptx::mbar_init(full_bar(s, a), 1);
+                fill_bytes[s * kAtoms + a] = 0u;
+            }
             ptx::mbar_init(empty_bar(s), 1);
-            fill_bytes[s] = 0u;
         }
         for (int b = 0; b < 2; ++b) {
             ptx::mbar_init(accfull_bar(b), 1);
@@ -276,8 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1) tn_grouped_kernel(const __grid_co
     }
     if (kOp != kGrGradA && threadIdx.x == 32 && p.red > 0) {
         ptx::prefetch_tensormap(&p.tmap_l);
-        ptx::prefetch_tensormap(&p.tmap_r);
-        ptx::prefetch_tensormap(&p.tmap_r16);
+        for (int i = 0; (16 << i) <= Cfg::kRowsR; ++i) ptx::prefetch_tensormap(&p.tmap_r[i]);
     }
     if (warp == 1) {
         ptx::tmem_alloc<kGroup>(ptx::smem_addr(tmem_holder), Cfg::kTmemCols);
@@ -304,8 +316,9 @@ __global__ void __launch_bounds__(kThreads, 1) tn_grouped_kernel(const __grid_co
 
     if (warp == 0) {
         // ------------------------------------------------ TMA producer (every CTA)
-        // A pair's loads all complete on the even CTA's full[s], which its own
-        // producer arms with both CTAs' bytes.
+        // A pair's loads all complete on the even CTA's full[s][a], which its own
+        // producer arms with both CTAs' bytes.  A block past the end of the sum
+        // (the last stage's second) is armed with no bytes.
         if (lane == 0) {
             int stage = 0;
             uint32_t phase = 0, n_issued = 0;
@@ -317,10 +330,12 @@ __global__ void __launch_bounds__(kThreads, 1) tn_grouped_kernel(const __grid_co
                 const int32_t cols = t.n_mma / kGroup;        // R elements of this CTA
                 const int32_t l0 = t.l0 + static_cast<int32_t>(pos) * Cfg::kRowsL;
                 const int32_t r0 = (kOp == kGrGradA ? 0 : start[t.e]) + t.r0 + static_cast<int32_t>(pos) * cols;
+                int box = 0;
+                while (kRMajorK && (16 << box) < cols) ++box;
                 const uint32_t r_bytes =
-                    kRMajorK ? cols * 128u : static_cast<uint32_t>((cols + 63) / 64) * (kGrBlock * 128u);
+                    kRMajorK ? (16u << box) * 128u : static_cast<uint32_t>((cols + 63) / 64) * (kGrBlock * 128u);
                 const uint32_t fill = Cfg::kLBytes + r_bytes;
-                const CUtensorMap *map_l = &p.tmap_l, *map_r = &p.tmap_r;
+                const CUtensorMap *map_l = &p.tmap_l, *map_r = p.tmap_r;
                 if constexpr (kOp == kGrGradA) {
                     map_r = p.group_maps + 2 * t.e;
                     map_l = map_r + 1;
@@ -331,47 +346,52 @@ __global__ void __launch_bounds__(kThreads, 1) tn_grouped_kernel(const __grid_co
                     }
                 }
                 const int32_t blocks = blocks_of(t.red);
-                for (int32_t i = 0; i < blocks; ++i) {
+                for (int32_t i = 0; i < blocks; i += kAtoms) {
                     if (!w.wait(empty_bar(stage), phase ^ 1u, kSiteEmpty)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t s_l = s_ring + stage * Cfg::kStageBytes, s_r = s_l + Cfg::kLBytes;
-                    const int32_t k0 = i * kGrBlock;
-                    uint32_t bar = full_bar(stage);
-                    fill_bytes[stage] = fill;
-                    if (pos == 0) ptx::mbar_arrive_expect_tx(bar, kGroup * fill);
-                    if constexpr (kGroup == 2) bar = ptx::mapa_shared(bar, 0);
-                    auto load2 = [&](uint32_t dst, const CUtensorMap *map, int32_t x, int32_t y) {
-                        if constexpr (kGroup == 2)
-                            ptx::tma_load_2d_pair(dst, map, bar, x, y);
-                        else
-                            ptx::tma_load_2d(dst, map, bar, x, y);
-                    };
-                    auto load3 = [&](uint32_t dst, const CUtensorMap *map, int32_t x, int32_t y, int32_t z) {
-                        if constexpr (kGroup == 2)
-                            tma_load_3d_pair(dst, map, bar, x, y, z);
-                        else
-                            tma_load_3d(dst, map, bar, x, y, z);
-                    };
-                    if constexpr (kOp == kGrProduct) {
-                        load3(s_l, map_l, k0, l0, t.e);
-                    } else if constexpr (kOp == kGrGradB) {
-                        load3(s_l, map_l, l0, k0, t.e);
-                        load3(s_l + kGrBlock * 128, map_l, l0 + 64, k0, t.e);
-                    } else {
-                        load2(s_l, map_l, l0, k0);
-                        load2(s_l + kGrBlock * 128, map_l, l0 + 64, k0);
-                    }
-                    if constexpr (kRMajorK) {
-                        if (cols == Cfg::kRowsR) {
-                            load2(s_r, map_r, k0, r0);
+#pragma unroll
+                    for (int a = 0; a < kAtoms; ++a) {
+                        const uint32_t s_l = s_ring + stage * Cfg::kStageBytes + a * Cfg::kBlockBytes;
+                        const uint32_t s_r = s_l + Cfg::kLBytes;
+                        const int32_t k0 = (i + a) * kGrBlock;
+                        const bool past = i + a >= blocks;
+                        uint32_t bar = full_bar(stage, a);
+                        fill_bytes[stage * kAtoms + a] = past ? 0u : fill;
+                        if (pos == 0) ptx::mbar_arrive_expect_tx(bar, past ? 0u : kGroup * fill);
+                        if (past) continue;
+                        if constexpr (kGroup == 2) bar = ptx::mapa_shared(bar, 0);
+                        auto load2 = [&](uint32_t dst, const CUtensorMap *map, int32_t x, int32_t y) {
+                            if constexpr (kGroup == 2)
+                                ptx::tma_load_2d_pair(dst, map, bar, x, y);
+                            else
+                                ptx::tma_load_2d(dst, map, bar, x, y);
+                        };
+                        auto load3 = [&](uint32_t dst, const CUtensorMap *map, int32_t x, int32_t y, int32_t z) {
+                            if constexpr (kGroup == 2)
+                                tma_load_3d_pair(dst, map, bar, x, y, z);
+                            else
+                                tma_load_3d(dst, map, bar, x, y, z);
+                        };
+                        if constexpr (kOp == kGrProduct) {
+                            load3(s_l, map_l, k0, l0, t.e);
+                        } else if constexpr (kOp == kGrGradB) {
+                            load3(s_l, map_l, l0, k0, t.e);
+                            load3(s_l + kGrBlock * 128, map_l, l0 + 64, k0, t.e);
                         } else {
-                            for (int32_t c = 0; c < cols; c += 16) load2(s_r + c * 128, &p.tmap_r16, k0, r0 + c);
+                            load2(s_l, map_l, l0, k0);
+                            load2(s_l + kGrBlock * 128, map_l, l0 + 64, k0);
                         }
-                    } else {
-                        load2(s_r, map_r, r0, k0);
-                        if (cols > 64) load2(s_r + kGrBlock * 128, map_r, r0 + 64, k0);
+                        if constexpr (kRMajorK) {
+                            // one box of the next power of two of rows (its other rows meet no
+                            // stored column): boxes of 16 rows alone made a tile of 224 rows take
+                            // twice a full one's time, and exact sums of boxes 10 % longer than this
+                            load2(s_r, map_r + box, k0, r0);
+                        } else {
+                            load2(s_r, map_r, r0, k0);
+                            if (cols > 64) load2(s_r + kGrBlock * 128, map_r, r0 + 64, k0);
+                        }
                     }
                     *issued_count = ++n_issued;
                     if (++stage == kStages) {
@@ -412,18 +432,21 @@ __global__ void __launch_bounds__(kThreads, 1) tn_grouped_kernel(const __grid_co
                             atomicCAS(&g_tn_status, 0, 4 | (kSiteReconcile << 8));
                             continue;
                         }
-                        if (mine > theirs)
-                            ptx::mbar_complete_tx(full_bar(s), fill_bytes[s]);
-                        else if (theirs > mine)
-                            ptx::mbar_arrive_expect_tx(
-                                full_bar(s), ptx::ld_relaxed_cluster_u32(ptx::mapa_shared(fill_addr + 4u * s, 1)));
-                        w.drain(full_bar(s), (last - 1) & 1u);
+                        for (int a = 0; a < kAtoms; ++a) {
+                            const int b = s * kAtoms + a;
+                            if (mine > theirs && fill_bytes[b])
+                                ptx::mbar_complete_tx(full_bar(s, a), fill_bytes[b]);
+                            else if (theirs > mine)
+                                ptx::mbar_arrive_expect_tx(
+                                    full_bar(s, a), ptx::ld_relaxed_cluster_u32(ptx::mapa_shared(fill_addr + 4u * b, 1)));
+                            w.drain(full_bar(s, a), (last - 1) & 1u);
+                        }
                     }
                 }
             } else {
                 for (int s = 0; s < kStages; ++s) {
                     const uint32_t passes = n_issued / kStages + (static_cast<uint32_t>(s) < n_issued % kStages ? 1u : 0u);
-                    if (passes) w.drain(full_bar(s), (passes - 1) & 1u);
+                    for (int a = 0; a < kAtoms && passes; ++a) w.drain(full_bar(s, a), (passes - 1) & 1u);
                 }
             }
         }
@@ -445,24 +468,28 @@ __global__ void __launch_bounds__(kThreads, 1) tn_grouped_kernel(const __grid_co
                 ptx::tc_fence_after_sync();
                 const uint32_t d_tmem = tmem_base + acc * Cfg::kAccCols;
                 const int32_t blocks = blocks_of(t.red);
-                for (int32_t i = 0; i < blocks; ++i) {
-                    if (!w.wait(full_bar(stage), phase, kSiteLoaded)) {
-                        ok = false;
-                        break;
-                    }
-                    ptx::tc_fence_after_sync();
-                    const uint32_t s_l = s_ring + stage * Cfg::kStageBytes, s_r = s_l + Cfg::kLBytes;
-                    const uint64_t desc_l = kLMajorK ? ptx::desc_kmajor_sw128(s_l) : desc_mnmajor_sw128(s_l);
-                    const uint64_t desc_r = kRMajorK ? ptx::desc_kmajor_sw128(s_r) : desc_mnmajor_sw128(s_r);
-                    // terms past the end of the sum are zeros: whole steps of them are left out
-                    const int32_t left = t.red - i * kGrBlock;
-                    const int steps = left >= kGrBlock ? kGrBlock / 16 : (left + 15) / 16;
+                for (int32_t i = 0; ok && i < blocks; i += kAtoms) {
 #pragma unroll
-                    for (int j = 0; j < kGrBlock / 16; ++j)
-                        if (j < steps)
-                            ptx::mma_f16<kGroup>(d_tmem, desc_l + kStepL * j, desc_r + kStepR * j, idesc,
-                                                 (i | j) != 0 ? 1u : 0u);
-                    issued_any = true;
+                    for (int a = 0; a < kAtoms; ++a) {
+                        if (!w.wait(full_bar(stage, a), phase, kSiteLoaded)) {
+                            ok = false;
+                            break;
+                        }
+                        ptx::tc_fence_after_sync();
+                        const uint32_t s_l = s_ring + stage * Cfg::kStageBytes + a * Cfg::kBlockBytes;
+                        const uint32_t s_r = s_l + Cfg::kLBytes;
+                        const uint64_t desc_l = kLMajorK ? ptx::desc_kmajor_sw128(s_l) : desc_mnmajor_sw128(s_l);
+                        const uint64_t desc_r = kRMajorK ? ptx::desc_kmajor_sw128(s_r) : desc_mnmajor_sw128(s_r);
+                        // terms past the end of the sum are zeros: whole steps of them are left out
+                        const int32_t left = t.red - (i + a) * kGrBlock;
+#pragma unroll
+                        for (int j = 0; j < kGrBlock / 16; ++j)
+                            if (left > 16 * j)
+                                ptx::mma_f16<kGroup>(d_tmem, desc_l + kStepL * j, desc_r + kStepR * j, idesc,
+                                                     (i | a | j) != 0 ? 1u : 0u);
+                        issued_any = true;
+                    }
+                    if (!ok) break;
                     ptx::mma_commit<kGroup>(empty_bar(stage), kMask);
                     if (++stage == kStages) {
                         stage = 0;
@@ -484,30 +511,47 @@ __global__ void __launch_bounds__(kThreads, 1) tn_grouped_kernel(const __grid_co
         }
     } else {
         // ------------------------------------------------ epilogue (warps 2..5, every CTA)
+        // The accumulator holds the result transposed (its lanes are the result's
+        // contiguous index).  A warp takes its 32 lanes by 32 columns as 8 x 8
+        // fragments, stores them transposed to its staging rows of 64 bytes, and
+        // writes those out 16 bytes a lane, whole 32-byte sectors.  The 16-byte
+        // pieces of two rows share a 128-byte line and are permuted within it, so
+        // that neither side meets a bank twice.
         const int quarter = warp & 3;             // TMEM lanes 32*quarter .. +31 are this warp's
+        const uint32_t s_mine = s_staging + (warp - 2) * kGrStageBytes;
+        auto piece = [&](int row, int c) {        // address of 16-byte piece c (0 .. 3) of a staging row
+            return s_mine + (row >> 1) * 128 + (((((row & 1) << 2) | c) ^ ((row >> 1) & 3)) << 4);
+        };
         int acc = 0;
         uint32_t acc_phase = 0;
-        const bool out_bf16 = p.out_fmt != 0;
+        const bool out_bf16 = p.out_fmt != 0, vec = p.out_vec != 0, scaled = p.scale_l != nullptr;
         for (int32_t u = slot; u < total; u += slots) {
             const GroupedTile t = walk.at(u);
-            const int32_t l = t.l0 + static_cast<int32_t>(pos) * Cfg::kRowsL + 32 * quarter + lane;
-            const bool live = l < p.l_extent;
+            const int32_t l0 = t.l0 + static_cast<int32_t>(pos) * Cfg::kRowsL + 32 * quarter;   // this warp's 32
             const int64_t row0 = static_cast<int64_t>(kOp == kGrGradA ? 0 : start[t.e]) + t.r0;
-            uint16_t *out = p.out + t.e * p.out_stride + row0 * p.out_ld + l;
+            uint16_t *out = p.out + t.e * p.out_stride + row0 * p.out_ld + l0;
+            const int32_t wide = p.l_extent - l0 < 32 ? p.l_extent - l0 : 32;   // of them inside the result
             if (t.red == 0) {                     // an empty sum
-                if (live)
-                    for (int32_t r = 0; r < t.rows; ++r) out[r * p.out_ld] = 0;
+                if (lane < wide)
+                    for (int32_t r = 0; r < t.rows; ++r) out[r * p.out_ld + lane] = 0;
                 continue;
             }
-            const float scale_l = p.scale_l && live ? __ldg(p.scale_l + static_cast<int64_t>(t.e) * p.l_extent + l) : 1.0f;
+            float scale_l[4] = {1.0f, 1.0f, 1.0f, 1.0f};      // of lanes l0 + 8 i + lane / 4
+            if (scaled) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (8 * i + (lane >> 2) < wide)
+                        scale_l[i] = __ldg(p.scale_l + static_cast<int64_t>(t.e) * p.l_extent + l0 + 8 * i + (lane >> 2));
+            }
             if (!__all_sync(0xffffffffu, w.wait(accfull_bar(acc), acc_phase, kSiteAccFull))) break;
             ptx::tc_fence_after_sync();
             const uint32_t t_row = tmem_base + (static_cast<uint32_t>(32 * quarter) << 16) + acc * Cfg::kAccCols;
-            for (int32_t c = 0; c < t.n_mma; c += 32) {
-                uint32_t v[32];
-                ptx::tmem_ld_32x32b_x32(t_row + c, v);
-                ptx::tmem_ld_wait(v);
-                if (c + 32 >= t.n_mma) {          // the accumulator is read: hand it back
+            for (int32_t c = 0; c < t.n_mma; c += kGrChunk) {
+                uint32_t v[2][16];
+                ptx::tmem_ld_16x256b_x4(t_row + c, v[0]);
+                ptx::tmem_ld_16x256b_x4(t_row + (16u << 16) + c, v[1]);
+                ptx::tmem_ld_wait(v[0], v[1]);
+                if (c + kGrChunk >= t.n_mma) {    // the accumulator is read: hand it back
                     ptx::tc_fence_before_sync();
                     __syncwarp();
                     if (lane == 0) {
@@ -517,17 +561,49 @@ __global__ void __launch_bounds__(kThreads, 1) tn_grouped_kernel(const __grid_co
                             ptx::mbar_arrive(accempty_bar(acc));
                     }
                 }
-                if (live) {
+                uint32_t h[2][4][2];              // [half of the lanes][8 columns][8 lanes]
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        if (c + j >= t.rows) break;
-                        float x = __uint_as_float(v[j]);
-                        if (p.scale_l) x = x * scale_l * __ldg(p.scale_r + row0 + c + j);
-                        const uint32_t h = out_bf16 ? ptx::pack_bf16x2(x, x) : ptx::pack_f16x2(x, x);
-                        out[(c + j) * p.out_ld] = static_cast<uint16_t>(h & 0xFFFFu);
+                for (int i = 0; i < 4; ++i) {
+                    float s0 = 1.0f, s1 = 1.0f;
+                    if (scaled) {
+                        const int32_t r = c + 8 * i + 2 * (lane & 3);
+                        if (r < t.rows) s0 = __ldg(p.scale_r + row0 + r);
+                        if (r + 1 < t.rows) s1 = __ldg(p.scale_r + row0 + r + 1);
+                    }
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        float x0 = __uint_as_float(v[q >> 1][4 * i + 2 * (q & 1)]);
+                        float x1 = __uint_as_float(v[q >> 1][4 * i + 2 * (q & 1) + 1]);
+                        if (scaled) {
+                            x0 = x0 * scale_l[q] * s0;
+                            x1 = x1 * scale_l[q] * s1;
+                        }
+                        h[q >> 1][i][q & 1] = out_bf16 ? ptx::pack_bf16x2(x0, x1) : ptx::pack_f16x2(x0, x1);
                     }
                 }
+                __syncwarp();                     // the last step's pieces have been read
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+#pragma unroll
+                    for (int i = 0; i < 4; i += 2)
+                        ptx::stmatrix_x4_trans(piece(8 * (i + (lane >> 4)) + (lane & 7), 2 * half + ((lane >> 3) & 1)),
+                                               h[half][i][0], h[half][i][1], h[half][i + 1][0], h[half][i + 1][1]);
                 __syncwarp();
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int row = 8 * q + (lane >> 2), col = 8 * (lane & 3);
+                    if (c + row >= t.rows || col >= wide) continue;
+                    const uint4 x = ptx::ld_shared_v4(piece(row, lane & 3));
+                    uint16_t *dst = out + (c + row) * p.out_ld + col;
+                    if (vec && col + 8 <= wide) {
+                        *reinterpret_cast<uint4 *>(dst) = x;
+                    } else {
+                        const uint32_t words[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                        for (int b = 0; b < 8; ++b)
+                            if (col + b < wide) dst[b] = static_cast<uint16_t>(words[b >> 1] >> (16 * (b & 1)));
+                    }
+                }
             }
             if (++acc == 2) {
                 acc = 0;

@@ -96,7 +96,6 @@ struct DeviceState {
     int quant_blocks[3] = {};         // co-resident quantiser CTAs per SM, by input type (0 = not queried)
     bool skinny_attr[2] = {};         // tn_skinny_kernel's shared-memory attribute set, by kind
     int grouped_slots[3][3] = {};     // co-resident tn_grouped_kernel CTAs or pairs, by operation and variant (0 = not queried)
-    int quant_rows_blocks[3] = {};    // co-resident CTAs of the row quantiser per SM, by input type (0 = not queried)
     // One lock per stream, held by a call from its first buffer lookup through
     // its last launch: a call is several launches (row copy, GEMM, reduce),
     // and two host threads' calls on one stream must not interleave them.
