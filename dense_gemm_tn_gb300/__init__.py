@@ -487,6 +487,10 @@ def f8e4m3_tn(A, Bt, scale_a, scale_b, C=None, stream=None):
 
 
 # ---------------------------------------------------------------- grouped and 8-bit products
+# Each helper checks its arguments in full, except that operands which are all
+# contiguous on the current device (the common case, and the one where a call is
+# short enough for the host's time to count) take a shorter way through the same
+# checks of types and shapes: measured on a GB300's host, 24 -> 14 us a call.
 def _half_type(dtype, name):
     import torch
     if dtype == torch.bfloat16:
@@ -534,35 +538,39 @@ def _same_device(device, **tensors):
             raise ValueError(f"{name} is on {t.device}, not on {device}")
 
 
-def _launch_stream(device, stream):
-    """The stream's handle (None: torch's current stream of `device`)."""
-    import torch
+def _launch_stream(index, stream):
+    """The stream's handle (None: torch's current stream of that device)."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device.index)
+        import torch
+        return torch._C._cuda_getCurrentRawStream(index)
     return stream if isinstance(stream, int) else int(stream.cuda_stream)
 
 
-def _workspace(device, stream, op, sizes, X, ldx, stride_x, Y, ldy):
-    """(address, bytes) of a workspace and the tensor that holds it.  It comes from
-    torch's allocator and belongs to the call's stream, so it is used again only
-    after the call's kernels."""
+def _workspace(device, stream, n):
+    """n bytes from torch's allocator that belong to the call's stream, so that
+    they are used again only after the call's kernels."""
     import torch
-    n = calls.gemm_grouped_workspace(op, *sizes, X, ldx, stride_x, Y, ldy)
-    if n <= 0:                      # (refused arguments are refused, with their reason, by the call itself)
-        return None, 0, None
     if stream is None:
-        held = torch.empty(n, dtype=torch.uint8, device=device)
-    else:
-        own = stream if not isinstance(stream, int) else torch.cuda.ExternalStream(stream, device=device)
-        with torch.cuda.stream(own):
-            held = torch.empty(n, dtype=torch.uint8, device=device)
-    return held.data_ptr(), n, held
+        return torch.empty(n, dtype=torch.uint8, device=device)
+    own = stream if not isinstance(stream, int) else torch.cuda.ExternalStream(stream, device=device)
+    with torch.cuda.stream(own):
+        return torch.empty(n, dtype=torch.uint8, device=device)
 
 
-def _elsewhere(device):
-    """Whether `device` is not the calling thread's current one (which the C ABI works on)."""
+def _plain(index, *tensors):
+    """Whether the tensors are contiguous on device `index`, the current one: their
+    strides are their shapes', and nothing is left to check but types and shapes."""
     import torch
-    return torch.cuda.current_device() != device.index
+    for t in tensors:
+        if not t.is_contiguous() or t.get_device() != index:
+            return False
+    return index is not None and torch._C._cuda_getDevice() == index
+
+
+def _elsewhere(index):
+    """Whether device `index` is not the calling thread's current one (which the C ABI works on)."""
+    import torch
+    return torch.cuda.current_device() != index
 
 
 def tn_grouped(A, Bt, offsets, C=None, stream=None):
@@ -571,20 +579,31 @@ def tn_grouped(A, Bt, offsets, C=None, stream=None):
     A, Bt and C (T, M) are all fp16 or all bf16, their rows contiguous.  Rows of
     no expert are not written."""
     import torch
-    lda, stride_a = _experts(A, A.dtype, "A")
-    kind, device = _half_type(A.dtype, "A"), A.device
-    E, M, K = A.shape
-    ldb, T = _tokens(Bt, A.dtype, K, "Bt"), Bt.shape[0]
-    _vector(offsets, torch.int32, E + 1, "offsets")
-    _same_device(device, Bt=Bt, offsets=offsets)
-    if _elsewhere(device):
-        with torch.cuda.device(device):
-            return tn_grouped(A, Bt, offsets, C, stream)
-    C, ldc = _output(C, M, T, A.dtype, device)
+    dtype, device = A.dtype, A.device
+    kind = _half_type(dtype, "A")
+    if (C is None and Bt.dtype is dtype and offsets.dtype is torch.int32 and A.dim() == 3 and Bt.dim() == 2
+            and offsets.dim() == 1 and _plain(device.index, A, Bt, offsets)
+            and A.shape[2] == Bt.shape[1] > 0 and offsets.shape[0] == A.shape[0] + 1):
+        (E, M, K), T = A.shape, Bt.shape[0]
+        lda = ldb = K
+        stride_a = M * K
+        C, ldc = torch.empty((T, M), dtype=dtype, device=device), max(M, 1)
+    else:
+        lda, stride_a = _experts(A, dtype, "A")
+        E, M, K = A.shape
+        ldb, T = _tokens(Bt, dtype, K, "Bt"), Bt.shape[0]
+        _vector(offsets, torch.int32, E + 1, "offsets")
+        _same_device(device, Bt=Bt, offsets=offsets)
+        if _elsewhere(device.index):
+            with torch.cuda.device(device):
+                return tn_grouped(A, Bt, offsets, C, stream)
+        C, ldc = _output(C, M, T, dtype, device)
     a, b = A.data_ptr(), Bt.data_ptr()
-    ws, n, held = _workspace(device, stream, GEMM_GROUPED_PRODUCT, (E, M, K, T), a, lda, stride_a, b, ldb)
+    n = calls.gemm_grouped_workspace(GEMM_GROUPED_PRODUCT, E, M, K, T, a, lda, stride_a, b, ldb)
+    held = _workspace(device, stream, n) if n > 0 else None
+    ws = held.data_ptr() if n > 0 else None
     _check(calls.gemm_tn_grouped(kind, E, M, K, T, a, lda, stride_a, b, ldb, offsets.data_ptr(), C.data_ptr(), ldc, ws,
-                                 n, _launch_stream(device, stream)))
+                                 n, _launch_stream(device.index, stream)))
     return C
 
 
@@ -598,14 +617,16 @@ def tn_grouped_grad_b(A, dCt, offsets, dBt=None, stream=None):
     ldd, T = _tokens(dCt, A.dtype, M, "dCt"), dCt.shape[0]
     _vector(offsets, torch.int32, E + 1, "offsets")
     _same_device(device, dCt=dCt, offsets=offsets)
-    if _elsewhere(device):
+    if _elsewhere(device.index):
         with torch.cuda.device(device):
             return tn_grouped_grad_b(A, dCt, offsets, dBt, stream)
     dBt, ldb = _output(dBt, K, T, A.dtype, device)
     a, d = A.data_ptr(), dCt.data_ptr()
-    ws, n, held = _workspace(device, stream, GEMM_GROUPED_GRAD_B, (E, M, K, T), a, lda, stride_a, d, ldd)
+    n = calls.gemm_grouped_workspace(GEMM_GROUPED_GRAD_B, E, M, K, T, a, lda, stride_a, d, ldd)
+    held = _workspace(device, stream, n) if n > 0 else None
+    ws = held.data_ptr() if n > 0 else None
     _check(calls.gemm_tn_grouped_grad_b(kind, E, M, K, T, a, lda, stride_a, d, ldd, offsets.data_ptr(), dBt.data_ptr(),
-                                        ldb, ws, n, _launch_stream(device, stream)))
+                                        ldb, ws, n, _launch_stream(device.index, stream)))
     return dBt
 
 
@@ -625,7 +646,7 @@ def tn_grouped_grad_a(dCt, Bt, offsets, dA=None, stream=None):
         raise ValueError(f"dCt has {T} rows and Bt {Bt.shape[0]}")
     _vector(offsets, torch.int32, E + 1, "offsets")
     _same_device(device, Bt=Bt, offsets=offsets)
-    if _elsewhere(device):
+    if _elsewhere(device.index):
         with torch.cuda.device(device):
             return tn_grouped_grad_a(dCt, Bt, offsets, dA, stream)
     if dA is None:
@@ -633,9 +654,11 @@ def tn_grouped_grad_a(dCt, Bt, offsets, dA=None, stream=None):
     ldda, stride_da = _experts(dA, dCt.dtype, "dA", (E, M, K))
     _same_device(device, dA=dA)
     d, b = dCt.data_ptr(), Bt.data_ptr()
-    ws, n, held = _workspace(device, stream, GEMM_GROUPED_GRAD_A, (E, M, K, T), d, ldd, 0, b, ldb)
+    n = calls.gemm_grouped_workspace(GEMM_GROUPED_GRAD_A, E, M, K, T, d, ldd, 0, b, ldb)
+    held = _workspace(device, stream, n) if n > 0 else None
+    ws = held.data_ptr() if n > 0 else None
     _check(calls.gemm_tn_grouped_grad_a(kind, E, M, K, T, d, ldd, b, ldb, offsets.data_ptr(), dA.data_ptr(), ldda,
-                                        stride_da, ws, n, _launch_stream(device, stream)))
+                                        stride_da, ws, n, _launch_stream(device.index, stream)))
     return dA
 
 
@@ -644,20 +667,29 @@ def i8_tn(A, Bt, scale_a, scale_b, C=None, dtype=None, stream=None):
     (N, K) int8, scale_a (M,) and scale_b (N,) fp32 -> (N, M) of `dtype`
     (torch.float16, unless C or dtype says torch.bfloat16)."""
     import torch
-    M, N, K, lda, ldb = _operands(A, Bt, torch.int8)
-    _vector(scale_a, torch.float32, M, "scale_a")
-    _vector(scale_b, torch.float32, N, "scale_b")
     dtype, device = dtype or (torch.float16 if C is None else C.dtype), A.device
     kind = _half_type(dtype, "dtype")
-    _same_device(device, scale_a=scale_a, scale_b=scale_b)
-    if _elsewhere(device):
-        with torch.cuda.device(device):
-            return i8_tn(A, Bt, scale_a, scale_b, C, dtype, stream)
-    C, ldc = _output(C, M, N, dtype, device)
+    if (C is None and A.dtype is torch.int8 is Bt.dtype and scale_a.dtype is torch.float32 is scale_b.dtype
+            and A.dim() == 2 == Bt.dim() and _plain(device.index, A, Bt, scale_a, scale_b)
+            and A.shape[1] == Bt.shape[1] > 0 and scale_a.shape == A.shape[:1] and scale_b.shape == Bt.shape[:1]):
+        (M, K), N = A.shape, Bt.shape[0]
+        lda = ldb = K
+        C, ldc = torch.empty((N, M), dtype=dtype, device=device), max(M, 1)
+    else:
+        M, N, K, lda, ldb = _operands(A, Bt, torch.int8)
+        _vector(scale_a, torch.float32, M, "scale_a")
+        _vector(scale_b, torch.float32, N, "scale_b")
+        _same_device(device, scale_a=scale_a, scale_b=scale_b)
+        if _elsewhere(device.index):
+            with torch.cuda.device(device):
+                return i8_tn(A, Bt, scale_a, scale_b, C, dtype, stream)
+        C, ldc = _output(C, M, N, dtype, device)
     a, b = A.data_ptr(), Bt.data_ptr()
-    ws, n, held = _workspace(device, stream, GEMM_GROUPED_I8, (1, M, K, N), a, lda, 0, b, ldb)
+    n = calls.gemm_grouped_workspace(GEMM_GROUPED_I8, 1, M, K, N, a, lda, 0, b, ldb)
+    held = _workspace(device, stream, n) if n > 0 else None
+    ws = held.data_ptr() if n > 0 else None
     _check(calls.gemm_i8_tn(kind, M, N, K, a, lda, scale_a.data_ptr(), b, ldb, scale_b.data_ptr(), C.data_ptr(), ldc, ws,
-                            n, _launch_stream(device, stream)))
+                            n, _launch_stream(device.index, stream)))
     return C
 
 
@@ -676,14 +708,16 @@ def i8_tn_grouped(A, Bt, scale_a, scale_b, offsets, C=None, dtype=None, stream=N
     dtype, device = dtype or (torch.float16 if C is None else C.dtype), A.device
     kind = _half_type(dtype, "dtype")
     _same_device(device, Bt=Bt, scale_a=scale_a, scale_b=scale_b, offsets=offsets)
-    if _elsewhere(device):
+    if _elsewhere(device.index):
         with torch.cuda.device(device):
             return i8_tn_grouped(A, Bt, scale_a, scale_b, offsets, C, dtype, stream)
     C, ldc = _output(C, M, T, dtype, device)
     a, b = A.data_ptr(), Bt.data_ptr()
-    ws, n, held = _workspace(device, stream, GEMM_GROUPED_I8, (E, M, K, T), a, lda, stride_a, b, ldb)
+    n = calls.gemm_grouped_workspace(GEMM_GROUPED_I8, E, M, K, T, a, lda, stride_a, b, ldb)
+    held = _workspace(device, stream, n) if n > 0 else None
+    ws = held.data_ptr() if n > 0 else None
     _check(calls.gemm_i8_tn_grouped(kind, E, M, K, T, a, lda, stride_a, scale_a.data_ptr(), b, ldb, scale_b.data_ptr(),
-                                    offsets.data_ptr(), C.data_ptr(), ldc, ws, n, _launch_stream(device, stream)))
+                                    offsets.data_ptr(), C.data_ptr(), ldc, ws, n, _launch_stream(device.index, stream)))
     return C
 
 
@@ -692,16 +726,24 @@ def quantize_i8_rows(x, stream=None):
     Returns (int8 codes of x's shape, scale as a float32 tensor of its rows): the
     operands of i8_tn, for activations (tokens) and weights (channels) alike."""
     import torch
-    types = {torch.float32: GEMM_IN_F32, torch.float16: GEMM_IN_F16, torch.bfloat16: GEMM_IN_BF16}
-    if not isinstance(x, torch.Tensor) or x.dtype not in types or x.dim() != 2:
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise ValueError("x must be a 2-D float32/float16/bfloat16 tensor")
-    ldx, device = _rows(x, x.dtype, "x"), x.device
-    if _elsewhere(device):
-        with torch.cuda.device(device):
-            return quantize_i8_rows(x, stream)
-    rows, cols = x.shape
-    q = torch.empty((rows, cols), dtype=torch.int8, device=device)
+    dtype, device = x.dtype, x.device
+    kind = (GEMM_IN_BF16 if dtype is torch.bfloat16 else GEMM_IN_F16 if dtype is torch.float16 else
+            GEMM_IN_F32 if dtype is torch.float32 else None)
+    if kind is None:
+        raise ValueError("x must be a 2-D float32/float16/bfloat16 tensor")
+    shape = x.shape
+    rows, cols = shape
+    if cols > 0 and _plain(device.index, x):
+        ldx = cols
+    else:
+        ldx = _rows(x, dtype, "x")
+        if _elsewhere(device.index):
+            with torch.cuda.device(device):
+                return quantize_i8_rows(x, stream)
+    q = torch.empty(shape, dtype=torch.int8, device=device)
     scale = torch.empty(rows, dtype=torch.float32, device=device)
-    _check(calls.gemm_quantize_i8_rows(x.data_ptr(), types[x.dtype], rows, cols, ldx, q.data_ptr(), max(cols, 1),
-                                       scale.data_ptr(), _launch_stream(device, stream)))
+    _check(calls.gemm_quantize_i8_rows(x.data_ptr(), kind, rows, cols, ldx, q.data_ptr(), max(cols, 1), scale.data_ptr(),
+                                       _launch_stream(device.index, stream)))
     return q, scale

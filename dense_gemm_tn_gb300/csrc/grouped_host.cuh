@@ -25,8 +25,13 @@ struct GroupedCall {
     bool needs_offsets = false;
 };
 
+// Rows per expert up to which the 8-bit product widens its operands on the way
+// to the tensor core (tn_i8_kernel) instead of first.
+constexpr int64_t kI8DirectRows = 512;
+
 // An operand as `blocks` matrices of rows x inner elements, and whether it is
-// copied first: the 8-bit ones always (widened to f16), the 16-bit ones when
+// copied first: the 8-bit ones for many rows per expert (widened to f16), and
+// all of them when
 // the TMA cannot address them in place -- base, row stride or block stride not
 // a multiple of 16 bytes, or the sum's index contiguous and its extent not one
 // (a row that ends inside a 16-byte unit is not clipped element by element) --
@@ -42,16 +47,23 @@ struct GroupedOperand {
 GroupedOperand grouped_operand(const void *base, int64_t rows, int64_t blocks, int64_t inner, int64_t ld,
                                int64_t stride, bool inner_is_sum, bool i8)
 {
-    GroupedOperand o{base, rows, blocks, inner, ld, stride, i8, 0, 0};
-    if (!i8)
-        o.copy = reinterpret_cast<uintptr_t>(base) % 16 || ld % 8 || (blocks > 1 && (stride % 8 || stride < ld)) ||
-                 (inner_is_sum && inner % 8);
+    const int64_t vec = i8 ? 16 : 8;              // elements of 16 bytes
+    GroupedOperand o{base, rows, blocks, inner, ld, stride, false, 0, 0};
+    o.copy = reinterpret_cast<uintptr_t>(base) % 16 || ld % vec || (blocks > 1 && (stride % vec || stride < ld)) ||
+             (inner_is_sum && inner % vec);
+    return o;
+}
+
+// Decides on the copy and sizes it.
+void grouped_copy(GroupedOperand &o, bool copy)
+{
+    o.copy = copy;
     if (o.copy) {
+        const int64_t rows = o.rows, blocks = o.blocks, inner = o.inner;
         o.copy_ld = (inner + 63) / 64 * 64;
         o.copy_bytes = size_t(rows) * size_t(blocks) * size_t(o.copy_ld) * 2;
         o.copy_bytes = (o.copy_bytes + 255) & ~size_t(255);
     }
-    return o;
 }
 
 struct GroupedPlan {
@@ -79,10 +91,15 @@ GroupedPlan grouped_plan(int op, int64_t E, int64_t M, int64_t K, int64_t T, con
         g.x = grouped_operand(X, T, 1, M, ldx, 0, false, false);
         g.y = grouped_operand(Y, T, 1, K, ldy, 0, false, false);
         g.map_bytes = size_t(E) * 2 * sizeof(CUtensorMap);
+        grouped_copy(g.x, g.x.copy);
+        grouped_copy(g.y, g.y.copy);
     } else {
         const bool grad_b = op == GEMM_GROUPED_GRAD_B;
         g.x = grouped_operand(X, M, E, K, ldx, stride_x, !grad_b, i8);
         g.y = grouped_operand(Y, T, 1, grad_b ? M : K, ldy, 0, true, i8);
+        const bool widen = i8 && (T > kI8DirectRows * E || g.x.copy || g.y.copy);     // both or neither
+        grouped_copy(g.x, widen || g.x.copy);
+        grouped_copy(g.y, widen || g.y.copy);
     }
     return g;
 }
@@ -131,7 +148,7 @@ gemm_status_t launch_grouped(const GroupedCall &c, DeviceState &dev, tn::Grouped
     attr[1].val.clusterDim.x = kGroup;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
-    cfg.blockDim = dim3(tn::kThreads, 1, 1);
+    cfg.blockDim = dim3(tn::kGrThreads, 1, 1);
     cfg.dynamicSmemBytes = Cfg::kSmemBytes;
     int slots;
     {
@@ -177,6 +194,55 @@ gemm_status_t launch_grouped(const GroupedCall &c, DeviceState &dev, tn::Grouped
     return GEMM_OK;
 }
 
+gemm_status_t launch_i8(const GroupedCall &c, DeviceState &dev, tn::GroupedParams &prm)
+{
+    gemm_status_t st;
+    const uint64_t apart = c.E > 1 ? uint64_t(c.stride_x) : uint64_t(16);
+    if (prm.red > 0) {
+        if ((st = encode_map(&prm.tmap_l, CU_TENSOR_MAP_DATA_TYPE_UINT8, c.X, c.K, c.M, c.ldx, c.E, apart, tn::kI8Block,
+                             tn::kI8RowsL, "A")) != GEMM_OK)
+            return st;
+        for (uint32_t i = 0; i < tn::kI8Rows / 16; ++i)
+            if ((st = encode_2d(&prm.tmap_r[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, c.Y, c.K, c.T, c.ldy, tn::kI8Block,
+                                16 * (i + 1), "rows")) != GEMM_OK)
+                return st;
+    }
+    auto kernel = tn::tn_i8_kernel;
+    {
+        std::lock_guard<std::mutex> lock(g_mutex);
+        if (!dev.i8_attr) {
+            cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, tn::kI8SmemBytes);
+            if (e != cudaSuccess) return fail(GEMM_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+            dev.i8_attr = true;
+        }
+    }
+    const int64_t l_tiles = (c.M + tn::kI8RowsL - 1) / tn::kI8RowsL;
+    const int64_t r_tiles = c.T / tn::kI8Rows + (c.E < c.T ? c.E : c.T);       // an upper bound
+    if (r_tiles > (int64_t(1) << 30) / l_tiles) return fail(GEMM_ERR_UNSUPPORTED, "%s: too many output tiles", c.name);
+    const int64_t tiles = r_tiles * l_tiles;
+    const int grid = static_cast<int>(tiles < dev.sms ? tiles : dev.sms);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+    cfg.blockDim = dim3(tn::kI8Threads, 1, 1);
+    cfg.dynamicSmemBytes = tn::kI8SmemBytes;
+    cfg.stream = c.stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    t_rec = LaunchRecord{};
+    t_rec.name = c.name;
+    t_rec.grouped = 1;
+    t_rec.cluster = 1;
+    t_rec.grid = grid;
+    t_rec.slots = dev.sms;
+    t_rec.tiles = static_cast<int>(tiles);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, prm);
+    if (e != cudaSuccess) return fail(GEMM_ERR_CUDA, "%s: launch: %s", c.name, cudaGetErrorString(e));
+    return GEMM_OK;
+}
+
 template <int kOp>
 gemm_status_t launch_grouped_op(const GroupedCall &c, DeviceState &dev, tn::GroupedParams &prm,
                                 const void *x, const void *y, int64_t ldx, int64_t stride_x, int64_t ldy,
@@ -214,17 +280,23 @@ gemm_status_t launch_grouped_op(const GroupedCall &c, DeviceState &dev, tn::Grou
             cudaError_t e = cudaLaunchKernelEx(&cfg, tn::grouped_maps_kernel, m);
             if (e != cudaSuccess) return fail(GEMM_ERR_CUDA, "%s: launch (tensor maps): %s", c.name, cudaGetErrorString(e));
         } else {
-            const uint32_t box_l = kOp == tn::kGrProduct ? 128 : 64;
+            const uint32_t box_l = kOp == tn::kGrGradB ? 64 : 128;
             const uint64_t apart = c.E > 1 ? uint64_t(stride_x) * 2 : uint64_t(16);
             if ((st = encode_map(&prm.tmap_l, type, x, inner_x, c.M, ldx * 2, c.E, apart, 64, box_l, "A")) != GEMM_OK)
                 return st;
-            for (int i = 0; i < (few ? 3 : 4); ++i)
-                if ((st = encode_2d(&prm.tmap_r[i], type, y, inner_y, c.T, ldy * 2, 64, 16u << i, "rows")) != GEMM_OK)
+            for (uint32_t i = 0; i < (few ? 4 : 8); ++i)
+                if ((st = encode_2d(&prm.tmap_r[i], type, y, inner_y, c.T, ldy * 2, 64, 16 * (i + 1), "rows")) != GEMM_OK)
                     return st;
         }
     }
     if constexpr (kOp != tn::kGrGradA) {
         if (few) return launch_grouped<kOp, 1, 64>(c, dev, prm, 0);
+    } else {
+        // Short sums are bound by what surrounds them and by the stores: tiles of two
+        // halves, half as many.  Measured on GB300, 256 -> 512 rows: 32 experts of 1024 x 2048
+        // and 3008 rows 51.6 -> 44.5 us; but 8 of 8192 x 4096 and 8192 rows 324 -> 340 us, of
+        // 4096 x 4096 and 16384 rows 342 -> 343.
+        if (c.M >= 512 && c.T <= 256 * c.E) return launch_grouped<kOp, 2, 512>(c, dev, prm, 2);
     }
     return launch_grouped<kOp, 2, 256>(c, dev, prm, 1);
 }
@@ -326,10 +398,14 @@ gemm_status_t run_grouped(const GroupedCall &c)
     prm.scale_r = c.scale_b;
     prm.flags = stall_flags(g_inject_stall.load());
     prm.wait_limit_ns = g_wait_limit_ns.load();
-    if (grad_a)
+    if (i8 && !copied)
+        st = launch_i8(c, *dev, prm);
+    else if (grad_a)
         st = launch_grouped_op<tn::kGrGradA>(c, *dev, prm, x, y, ldx, stride_x, ldy, in_x, in_y);
     else if (grad_b)
         st = launch_grouped_op<tn::kGrGradB>(c, *dev, prm, x, y, ldx, stride_x, ldy, in_x, in_y);
+    else if (i8)
+        st = launch_grouped_op<tn::kGrI8>(c, *dev, prm, x, y, ldx, stride_x, ldy, in_x, in_y);
     else
         st = launch_grouped_op<tn::kGrProduct>(c, *dev, prm, x, y, ldx, stride_x, ldy, in_x, in_y);
     t_rec.copied = copied;

@@ -29,8 +29,8 @@
 // grouped_maps_kernel) end where the group ends, and the TMA fills with zeros.
 //
 // Roles, barriers, bounded waits and the programmatic-dependent-launch
-// protocol are the general kernel's (tn_gemm_kernel.cuh): warp 0 loads, one
-// thread of warp 1 issues the MMAs, warps 2-5 read the accumulator and store.
+// protocol are the general kernel's (tn_gemm_kernel.cuh): warp 0 loads, warp 1
+// issues the MMAs, warps 2-9 read the accumulator and store.
 #pragma once
 
 #include "tn_gemm_kernel.cuh"
@@ -43,38 +43,50 @@ constexpr int kGrRaster = 8;                 // R tiles per raster group
 constexpr int kGrChunk = 32;                 // accumulator columns per epilogue step
 constexpr int kGrStageBytes = kGrChunk * 64; // one epilogue warp's staging: 32 rows of 32 16-bit results
 
-enum GroupedOp : int { kGrProduct = 0, kGrGradB = 1, kGrGradA = 2 };
+// (kGrI8: the product with the 8-bit form's scales.)
+enum GroupedOp : int { kGrProduct = 0, kGrGradB = 1, kGrGradA = 2, kGrI8 = 3 };
 
-// kGroup CTAs compute a tile of 128 * kGroup (L) x kRows (R).
+constexpr int kGrEpiWarps = 8;               // epilogue warps: two per quarter of the TMEM lanes
+constexpr int kGrThreads = 64 + 32 * kGrEpiWarps;
+
+// kGroup CTAs compute a tile of 128 * kGroup (L) x kRows (R).  Its rows are one
+// MMA N side up to 256, or (kRows = 512) two halves that share the L operand,
+// the first of 256 rows: a quarter fewer bytes per MMA out of L2.  A half's
+// accumulator is one of two TMEM buffers, which the halves of all tiles use in
+// turn, so the epilogue of one overlaps the MMAs of the next.
 template <int kGroup, int kRows>
 struct GroupedCfg {
+    static constexpr int kHalfRows = kRows < 256 ? kRows : 256;
+    static constexpr int kHalves = kRows / kHalfRows;
     static constexpr int kRowsL = 128;                       // per CTA
-    static constexpr int kRowsR = kRows / kGroup;            // per CTA
+    static constexpr int kRowsR = kHalfRows / kGroup;        // per CTA and half
     static constexpr int kTileL = kRowsL * kGroup;
     static constexpr int kLBytes = kRowsL * 128;
     static constexpr int kRBytes = kRowsR * 128;
-    static constexpr int kBlockBytes = kLBytes + kRBytes;
+    static constexpr int kBlockBytes = kLBytes + kHalves * kRBytes;
     // Blocks per stage, each with a barrier of its own that its loads complete on;
-    // the stage is given back as a whole.  Pairs: two (see TileCfg on long stages).
-    static constexpr int kAtoms = kGroup;
+    // the stage is given back as a whole.  Two, where they fit: what a stage costs
+    // beside its bytes (a wait, an election and a commit or an arming on either
+    // side, some 350 cycles) is then paid half as often.
+    static constexpr int kAtoms = kHalves == 1 ? 2 : 1;
     static constexpr int kStageBytes = kAtoms * kBlockBytes;
     static constexpr int kStages = 196608 / kStageBytes;
     static constexpr int kGran = 16 * kGroup;                // the MMA's N is a multiple of it
-    static constexpr uint32_t kAccCols = kRows;
+    static constexpr uint32_t kAccCols = kHalfRows;
     static constexpr uint32_t kTmemCols = 2 * kAccCols;      // two accumulators: an epilogue overlaps the next tile
     // full[S][atoms], empty[S], accfull[2], accempty[2], drain, never
     static constexpr int kNumBarriers = (kAtoms + 1) * kStages + 6;
     static constexpr int kTables = 2 * (kGrMaxExperts + 8) * 4;   // group starts, units before each group
-    static constexpr int kStaging = kEpiWarps * kGrStageBytes;
+    static constexpr int kStaging = kGrEpiWarps * kGrStageBytes;
     static constexpr int kSmemBytes = 1024 /* alignment slack */ + kStages * kStageBytes + kStaging + kNumBarriers * 8 +
                                       32 + kStages * kAtoms * 4 + kTables;
     static_assert(kSmemBytes <= 232448, "exceeds the 227 KiB shared memory of one CTA");
 };
 
 struct GroupedParams {
-    // product: L {K, M, E} box {64, 128, 1}, R {K, T} boxes {64, 16 << i};
-    // grad_b:  L {K, M, E} box {64, 64, 1},  R {M, T} boxes {64, 16 << i}
-    CUtensorMap tmap_l, tmap_r[4];
+    // product: L {K, M, E} box {64, 128, 1}, R {K, T} boxes {64, 16 (i + 1)};
+    // grad_b:  L {K, M, E} box {64, 64, 1},  R {M, T} boxes {64, 16 (i + 1)}
+    CUtensorMap tmap_l, tmap_r[8];
     const CUtensorMap *group_maps;   // grad_a: [E][2], R {M, T_e} and L {K, T_e}, boxes {64, 64}
     const int32_t *offsets;          // E + 1 row starts, or NULL: one group of all T rows
     uint16_t *out;                   // row r of group e's range at out + e * out_stride + r * out_ld
@@ -91,6 +103,22 @@ struct GroupedParams {
     uint64_t wait_limit_ns;
 };
 
+// Waiter::wait by a converged warp, with one answer for all its lanes.
+__device__ __forceinline__ bool wait_warp(const Waiter &w, uint32_t bar, uint32_t parity, int site)
+{
+    if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
+    const uint64_t t0 = ptx::globaltimer();
+    while (true) {
+        if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
+        if (__any_sync(0xffffffffu, *w.abort_flag != 0u)) return false;
+        if (__any_sync(0xffffffffu, ptx::globaltimer() - t0 > w.limit)) {
+            if (ptx::elect_one()) w.raise(site);
+            __syncwarp();
+            return false;
+        }
+    }
+}
+
 // ------------------------------------------------------------------ schedule
 // Rows [start[e], start[e + 1]) belong to group e.  Offsets are read as if each
 // were at least the ones before it and at most T, so a table that is not
@@ -98,16 +126,11 @@ struct GroupedParams {
 struct GroupedTile {
     int32_t e, l0, r0;      // group, first index of the L side, first row within the group's range
     int32_t rows;           // rows of the result in this tile
-    int32_t n_mma;          // MMA N
+    int32_t n_mma[2];       // MMA N of either half (0: no second half)
     int32_t red;            // terms of the sum
 };
 
-__host__ __device__ __forceinline__ int32_t grouped_tile_rows(int32_t rows, int32_t tiles, int32_t gran)
-{
-    return ((rows + tiles - 1) / tiles + gran - 1) / gran * gran;
-}
-
-template <int kOp, int kRows, int kTileL, int kGran>
+template <int kOp, int kRows, int kHalfRows, int kTileL, int kGran>
 struct GroupedWalk {
     const int32_t *start, *before;      // shared memory
     int32_t l_tiles, r_extent, red;
@@ -121,14 +144,18 @@ struct GroupedWalk {
         const int32_t group_rows = start[e + 1] - start[e];
         const int32_t rows = kOp == kGrGradA ? r_extent : group_rows;
         const int32_t tiles = (rows + kRows - 1) / kRows;
-        const int32_t h = grouped_tile_rows(rows, tiles, kGran);
+        // the rows in steps of kGran, spread evenly: the first `more` tiles have one more
+        const int32_t steps = (rows + kGran - 1) / kGran, each = steps / tiles, more = steps - each * tiles;
         int64_t tr, tl;
         tile_coord(u - before[e], tiles, l_tiles, kGrRaster, tr, tl);
         t.e = e;
         t.l0 = static_cast<int32_t>(tl) * kTileL;
-        t.r0 = static_cast<int32_t>(tr) * h;
-        t.rows = rows - t.r0 < h ? rows - t.r0 : h;
-        t.n_mma = (t.rows + kGran - 1) / kGran * kGran;
+        const int32_t r = static_cast<int32_t>(tr);
+        t.r0 = (r * each + (r < more ? r : more)) * kGran;
+        const int32_t padded = (each + (r < more ? 1 : 0)) * kGran;
+        t.rows = rows - t.r0 < padded ? rows - t.r0 : padded;
+        t.n_mma[0] = padded < kHalfRows ? padded : kHalfRows;
+        t.n_mma[1] = padded - t.n_mma[0];
         t.red = kOp == kGrGradA ? group_rows : red;
         return t;
     }
@@ -178,11 +205,11 @@ __device__ __forceinline__ void acquire_tensormap(const CUtensorMap *map)
 }
 
 // The group tables in shared memory, by all threads of the CTA.
-template <int kOp, int kRows>
+template <int kOp, int kRows, int kCtaThreads = kGrThreads>
 __device__ __forceinline__ void grouped_tables(const GroupedParams &p, int32_t l_tiles, int32_t *start, int32_t *before)
 {
     const int32_t E = p.E, T = p.T;
-    for (int32_t i = threadIdx.x; i <= E; i += kThreads) {
+    for (int32_t i = threadIdx.x; i <= E; i += kCtaThreads) {
         const int32_t o = p.offsets ? p.offsets[i] : (i == 0 ? 0 : T);
         start[i] = o < 0 ? 0 : (o > T ? T : o);
     }
@@ -230,12 +257,146 @@ __device__ __forceinline__ void grouped_tables(const GroupedParams &p, int32_t l
     __syncthreads();
 }
 
+// ------------------------------------------------------------------ epilogue
+// The accumulator holds the result transposed (its lanes are the result's
+// contiguous index).  A warp takes its 32 lanes by 32 columns as 8 x 8
+// fragments, stores them transposed to its staging rows of 64 bytes, and
+// writes those out 16 bytes a lane, whole 32-byte sectors.  The 16-byte pieces
+// of two staging rows share a 128-byte line and are permuted within it, so that
+// neither side meets a bank twice.  One warp runs this with little to overlap,
+// so what counts is instructions: about 60 a step.
+struct GroupedStore {
+    uint32_t st0, ld0;        // this lane's first staging addresses (others are fixed offsets from them)
+    int lane;
+    int32_t wide;             // of this warp's 32 lanes, those inside the result
+    bool vec;                 // 16-byte stores: all 32 lanes, on 16-byte boundaries
+    int64_t ld;               // the result's row stride, elements
+    float scale_l[4];         // 8-bit product: of lanes 8 i + lane / 4
+
+    __device__ __forceinline__ void init(uint32_t s_mine, int lane_)
+    {
+        lane = lane_;
+        auto piece = [&](int row, int c) {        // address of 16-byte piece c (0 .. 3) of a staging row
+            return s_mine + (row >> 1) * 128 + (((((row & 1) << 2) | c) ^ ((row >> 1) & 3)) << 4);
+        };
+        st0 = piece(8 * (lane >> 4) + (lane & 7), (lane >> 3) & 1);
+        ld0 = piece(lane >> 2, lane & 3);
+    }
+
+    // Columns v of one step, the result's rows from out on (this warp's first
+    // element of the step's first row), `rows` of them to store; scale_r: the
+    // scale of the step's first row.
+    template <bool kBf16, bool kScaled>
+    __device__ __forceinline__ void step(const uint32_t (&v)[2][16], uint16_t *out, int32_t rows,
+                                         const float *scale_r) const
+    {
+        uint32_t h[2][4][2];                      // [half of the lanes][8 columns][8 lanes]
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float s0 = 1.0f, s1 = 1.0f;
+            if constexpr (kScaled) {
+                const int32_t r = 8 * i + 2 * (lane & 3);
+                if (r < rows) s0 = __ldg(scale_r + r);
+                if (r + 1 < rows) s1 = __ldg(scale_r + r + 1);
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                float x0 = __uint_as_float(v[q >> 1][4 * i + 2 * (q & 1)]);
+                float x1 = __uint_as_float(v[q >> 1][4 * i + 2 * (q & 1) + 1]);
+                if constexpr (kScaled) {
+                    x0 = x0 * scale_l[q] * s0;
+                    x1 = x1 * scale_l[q] * s1;
+                }
+                h[q >> 1][i][q & 1] = kBf16 ? ptx::pack_bf16x2(x0, x1) : ptx::pack_f16x2(x0, x1);
+            }
+        }
+        __syncwarp();                             // the last step's pieces have been read
+#pragma unroll
+        for (int q = 0; q < 2; ++q)               // lanes 16 q .. : pieces 2 q, 2 q + 1
+#pragma unroll
+            for (int i = 0; i < 4; i += 2)
+                ptx::stmatrix_x4_trans((st0 ^ (32u * q)) + 512u * i, h[q][i][0], h[q][i][1], h[q][i + 1][0],
+                                       h[q][i + 1][1]);
+        __syncwarp();
+        uint16_t *dst = out + (lane >> 2) * ld + 8 * (lane & 3);
+        if (vec && rows >= kGrChunk) {
+            uint4 x[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) x[q] = ptx::ld_shared_v4(ld0 + 512u * q);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4 *>(dst + 8 * q * ld) = x[q];
+        } else {
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q, dst += 8 * ld) {
+                if (8 * q + (lane >> 2) >= rows) continue;
+                const uint4 x = ptx::ld_shared_v4(ld0 + 512u * q);
+                if (vec) {
+                    *reinterpret_cast<uint4 *>(dst) = x;
+                } else {
+                    const uint32_t words[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                    for (int b = 0; b < 8; ++b)
+                        if (8 * (lane & 3) + b < wide) dst[b] = static_cast<uint16_t>(words[b >> 1] >> (16 * (b & 1)));
+                }
+            }
+        }
+    }
+
+    // The steps first, first + 2, ... of a half's columns (from TMEM address
+    // t_row on; out, rows and scale_r as for step 0), the next one's columns on
+    // their way while one is stored; read_all() once all have been read.
+    template <bool kBf16, bool kScaled, class ReadAll>
+    __device__ __forceinline__ void half(uint32_t t_row, int32_t first, int32_t steps, uint16_t *out, int32_t rows,
+                                         const float *scale_r, ReadAll read_all) const
+    {
+        auto load = [&](int32_t s, uint32_t (&v)[2][16]) {
+            ptx::tmem_ld_16x256b_x4(t_row + s * kGrChunk, v[0]);
+            ptx::tmem_ld_16x256b_x4(t_row + (16u << 16) + s * kGrChunk, v[1]);
+        };
+        auto landed = [&](uint32_t (&v)[2][16]) {
+            ptx::tmem_ld_wait_all();
+            ptx::reg_dependency(v[0]);
+            ptx::reg_dependency(v[1]);
+        };
+        auto store = [&](int32_t s, const uint32_t (&v)[2][16]) {
+            const int32_t c = s * kGrChunk;
+            step<kBf16, kScaled>(v, out + c * ld, rows - c, kScaled ? scale_r + c : nullptr);
+        };
+        uint32_t va[2][16], vb[2][16];
+        int32_t s = first;
+        if (s < steps) {
+            load(s, va);
+            landed(va);
+        }
+        while (true) {
+            if (s + 2 >= steps) {
+                read_all();
+                if (s < steps) store(s, va);
+                return;
+            }
+            load(s + 2, vb);
+            store(s, va);
+            landed(vb);
+            s += 2;
+            if (s + 2 >= steps) {
+                read_all();
+                store(s, vb);
+                return;
+            }
+            load(s + 2, va);
+            store(s, vb);
+            landed(va);
+            s += 2;
+        }
+    }
+};
+
 template <int kOp, int kGroup, int kRows>
-__global__ void __launch_bounds__(kThreads, 1) tn_grouped_kernel(const __grid_constant__ GroupedParams p)
+__global__ void __launch_bounds__(kGrThreads, 1) tn_grouped_kernel(const __grid_constant__ GroupedParams p)
 {
     using Cfg = GroupedCfg<kGroup, kRows>;
     constexpr int kStages = Cfg::kStages, kAtoms = Cfg::kAtoms;
-    constexpr bool kLMajorK = kOp == kGrProduct, kRMajorK = kOp != kGrGradA;
+    constexpr bool kLMajorK = kOp == kGrProduct || kOp == kGrI8, kRMajorK = kOp != kGrGradA;
 
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -277,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1) tn_grouped_kernel(const __grid_co
         }
         for (int b = 0; b < 2; ++b) {
             ptx::mbar_init(accfull_bar(b), 1);
-            ptx::mbar_init(accempty_bar(b), kEpiWarps * kGroup);
+            ptx::mbar_init(accempty_bar(b), kGrEpiWarps * kGroup);
         }
         ptx::mbar_init(drain_bar, 1);
         ptx::mbar_init(never_bar, 1);
@@ -289,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1) tn_grouped_kernel(const __grid_co
     }
     if (kOp != kGrGradA && threadIdx.x == 32 && p.red > 0) {
         ptx::prefetch_tensormap(&p.tmap_l);
-        for (int i = 0; (16 << i) <= Cfg::kRowsR; ++i) ptx::prefetch_tensormap(&p.tmap_r[i]);
+        ptx::prefetch_tensormap(&p.tmap_r[Cfg::kRowsR / 16 - 1]);
     }
     if (warp == 1) {
         ptx::tmem_alloc<kGroup>(ptx::smem_addr(tmem_holder), Cfg::kTmemCols);
@@ -311,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1) tn_grouped_kernel(const __grid_co
     grouped_tables<kOp, kRows>(p, l_tiles, start, before);
     const int32_t total = before[p.E];
     const int32_t slot = static_cast<int32_t>(blockIdx.x) / kGroup, slots = static_cast<int32_t>(gridDim.x) / kGroup;
-    GroupedWalk<kOp, kRows, Cfg::kTileL, Cfg::kGran> walk{start, before, l_tiles, p.r_extent, p.red, 0};
+    GroupedWalk<kOp, kRows, Cfg::kHalfRows, Cfg::kTileL, Cfg::kGran> walk{start, before, l_tiles, p.r_extent, p.red, 0};
     auto blocks_of = [](int32_t red) { return (red + kGrBlock - 1) / kGrBlock; };
 
     if (warp == 0) {
@@ -319,38 +480,48 @@ __global__ void __launch_bounds__(kThreads, 1) tn_grouped_kernel(const __grid_co
         // A pair's loads all complete on the even CTA's full[s][a], which its own
         // producer arms with both CTAs' bytes.  A block past the end of the sum
         // (the last stage's second) is armed with no bytes.
-        if (lane == 0) {
+        {
             int stage = 0;
             uint32_t phase = 0, n_issued = 0;
             bool ok = true;
-            if (p.flags & (pos == 0 ? kFlagStallProducer0 : kFlagStallProducer1)) ok = w.wait(never_bar, 0u, kSiteStall);
+            if (p.flags & (pos == 0 ? kFlagStallProducer0 : kFlagStallProducer1))
+                ok = wait_warp(w, never_bar, 0u, kSiteStall);
             int32_t mapped = -1;
             for (int32_t u = slot; ok && u < total; u += slots) {
                 const GroupedTile t = walk.at(u);
-                const int32_t cols = t.n_mma / kGroup;        // R elements of this CTA
                 const int32_t l0 = t.l0 + static_cast<int32_t>(pos) * Cfg::kRowsL;
-                const int32_t r0 = (kOp == kGrGradA ? 0 : start[t.e]) + t.r0 + static_cast<int32_t>(pos) * cols;
-                int box = 0;
-                while (kRMajorK && (16 << box) < cols) ++box;
-                const uint32_t r_bytes =
-                    kRMajorK ? (16u << box) * 128u : static_cast<uint32_t>((cols + 63) / 64) * (kGrBlock * 128u);
+                int32_t cols[2], r0[2];       // this CTA's R elements of either half, and the first
+                uint32_t r_bytes = 0;
+#pragma unroll
+                for (int h = 0; h < Cfg::kHalves; ++h) {
+                    cols[h] = t.n_mma[h] / kGroup;
+                    r0[h] = (kOp == kGrGradA ? 0 : start[t.e]) + t.r0 + h * Cfg::kHalfRows +
+                            static_cast<int32_t>(pos) * cols[h];
+                    r_bytes += kRMajorK ? cols[h] * 128u
+                                        : static_cast<uint32_t>((cols[h] + 63) / 64) * (kGrBlock * 128u);
+                }
                 const uint32_t fill = Cfg::kLBytes + r_bytes;
                 const CUtensorMap *map_l = &p.tmap_l, *map_r = p.tmap_r;
                 if constexpr (kOp == kGrGradA) {
                     map_r = p.group_maps + 2 * t.e;
                     map_l = map_r + 1;
                     if (t.e != mapped && t.red > 0) {
-                        acquire_tensormap(map_r);
-                        acquire_tensormap(map_l);
+                        if (ptx::elect_one()) {       // (the lane that issues the loads)
+                            acquire_tensormap(map_r);
+                            acquire_tensormap(map_l);
+                        }
+                        __syncwarp();
                         mapped = t.e;
                     }
                 }
                 const int32_t blocks = blocks_of(t.red);
                 for (int32_t i = 0; i < blocks; i += kAtoms) {
-                    if (!w.wait(empty_bar(stage), phase ^ 1u, kSiteEmpty)) {
+                    if (!wait_warp(w, empty_bar(stage), phase ^ 1u, kSiteEmpty)) {
                         ok = false;
                         break;
                     }
+                    ++n_issued;
+                    if (ptx::elect_one()) {
 #pragma unroll
                     for (int a = 0; a < kAtoms; ++a) {
                         const uint32_t s_l = s_ring + stage * Cfg::kStageBytes + a * Cfg::kBlockBytes;
@@ -374,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1) tn_grouped_kernel(const __grid_co
                             else
                                 tma_load_3d(dst, map, bar, x, y, z);
                         };
-                        if constexpr (kOp == kGrProduct) {
+                        if constexpr (kLMajorK) {
                             load3(s_l, map_l, k0, l0, t.e);
                         } else if constexpr (kOp == kGrGradB) {
                             load3(s_l, map_l, l0, k0, t.e);
@@ -383,17 +554,24 @@ __global__ void __launch_bounds__(kThreads, 1) tn_grouped_kernel(const __grid_co
                             load2(s_l, map_l, l0, k0);
                             load2(s_l + kGrBlock * 128, map_l, l0 + 64, k0);
                         }
-                        if constexpr (kRMajorK) {
-                            // one box of the next power of two of rows (its other rows meet no
-                            // stored column): boxes of 16 rows alone made a tile of 224 rows take
-                            // twice a full one's time, and exact sums of boxes 10 % longer than this
-                            load2(s_r, map_r + box, k0, r0);
-                        } else {
-                            load2(s_r, map_r, r0, k0);
-                            if (cols > 64) load2(s_r + kGrBlock * 128, map_r, r0 + 64, k0);
+#pragma unroll
+                        for (int h = 0; h < Cfg::kHalves; ++h) {
+                            if (h > 0 && cols[h] == 0) break;
+                            const uint32_t dst = s_r + h * Cfg::kRBytes;
+                            if constexpr (kRMajorK) {
+                                // one box of just these rows: with boxes of 16 rows a tile of 224 took
+                                // twice a full one's time, with one of 128 (the next power of two a CTA)
+                                // no less than a full one's
+                                load2(dst, map_r + cols[h] / 16 - 1, k0, r0[h]);
+                            } else {
+                                load2(dst, map_r, r0[h], k0);
+                                if (cols[h] > 64) load2(dst + kGrBlock * 128, map_r, r0[h] + 64, k0);
+                            }
                         }
                     }
-                    *issued_count = ++n_issued;
+                    *issued_count = n_issued;
+                    }
+                    __syncwarp();
                     if (++stage == kStages) {
                         stage = 0;
                         phase ^= 1u;
@@ -401,10 +579,12 @@ __global__ void __launch_bounds__(kThreads, 1) tn_grouped_kernel(const __grid_co
                 }
             }
             // no more loads from this CTA: the next kernel may start its setup
-            ptx::griddep_launch_dependents();
+            if (lane == 0) ptx::griddep_launch_dependents();
             if constexpr (kGroup == 2) {
-                ptx::st_release_cluster_u32(ptx::mapa_shared(done_addr, pos), 1u);
-                if (pos == 0) {
+                // (one lane from here on: the counts below are its own stores or released to it)
+                const bool one = ptx::elect_one();
+                if (one) ptx::st_release_cluster_u32(ptx::mapa_shared(done_addr, pos), 1u);
+                if (one && pos == 0) {
                     // Both producers have stopped (or the limit ran out): let every load that
                     // was issued land before the pair can exit.  Loads go round the stages in
                     // order, and a stage is refilled only after the pair's MMAs read its
@@ -443,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, 1) tn_grouped_kernel(const __grid_co
                         }
                     }
                 }
-            } else {
+            } else if (ptx::elect_one()) {
                 for (int s = 0; s < kStages; ++s) {
                     const uint32_t passes = n_issued / kStages + (static_cast<uint32_t>(s) < n_issued % kStages ? 1u : 0u);
                     for (int a = 0; a < kAtoms && passes; ++a) w.drain(full_bar(s, a), (passes - 1) & 1u);
@@ -451,163 +631,178 @@ __global__ void __launch_bounds__(kThreads, 1) tn_grouped_kernel(const __grid_co
             }
         }
     } else if (warp == 1) {
-        if (lane == 0 && pos == 0) {
+        if (pos == 0) {
             // ------------------------------------------------ MMA issuer (even CTA of a pair)
-            int stage = 0, acc = 0;
-            uint32_t phase = 0, acc_phase = 0;
+            int stage = 0;
+            uint32_t phase = 0, sub = 0;      // sub: halves so far; half `sub` uses accumulator sub % 2
             bool ok = true, issued_any = false;
             constexpr uint16_t kMask = kGroup == 2 ? 3 : 1;
             constexpr uint32_t kStepL = kLMajorK ? 2 : 128, kStepR = kRMajorK ? 2 : 128;   // 16 terms on, in 16-byte units
-            if (p.flags & kFlagStallMma) ok = w.wait(never_bar, 0u, kSiteStall);
+            if (p.flags & kFlagStallMma) ok = wait_warp(w, never_bar, 0u, kSiteStall);
             for (int32_t u = slot; ok && u < total; u += slots) {
                 const GroupedTile t = walk.at(u);
                 if (t.red == 0) continue;
-                const uint32_t idesc = ptx::idesc_f32acc(Cfg::kTileL, static_cast<uint32_t>(t.n_mma), p.fmt, p.fmt) |
-                                       (kLMajorK ? 0u : 1u << 15) | (kRMajorK ? 0u : 1u << 16);
-                if (!w.wait(accempty_bar(acc), acc_phase ^ 1u, kSiteAccEmpty)) break;
+                const int halves = Cfg::kHalves == 2 && t.n_mma[1] > 0 ? 2 : 1;
+                uint32_t idesc[2], d_tmem[2];
+#pragma unroll
+                for (int h = 0; h < Cfg::kHalves; ++h) {
+                    idesc[h] = ptx::idesc_f32acc(Cfg::kTileL, static_cast<uint32_t>(t.n_mma[h]), p.fmt, p.fmt) |
+                               (kLMajorK ? 0u : 1u << 15) | (kRMajorK ? 0u : 1u << 16);
+                    d_tmem[h] = tmem_base + ((sub + h) & 1u) * Cfg::kAccCols;
+                }
+                if (!wait_warp(w, accempty_bar(sub & 1u), ((sub >> 1) & 1u) ^ 1u, kSiteAccEmpty)) break;
                 ptx::tc_fence_after_sync();
-                const uint32_t d_tmem = tmem_base + acc * Cfg::kAccCols;
                 const int32_t blocks = blocks_of(t.red);
+                // The MMAs of block i, in atom a of stage s, for half h.  Terms past the end
+                // of the sum are zeros: whole steps of them are left out.
+                auto issue = [&](int s, int a, int32_t i, int h) {
+                    const uint32_t s_l = s_ring + s * Cfg::kStageBytes + a * Cfg::kBlockBytes;
+                    const uint32_t s_r = s_l + Cfg::kLBytes + h * Cfg::kRBytes;
+                    const uint64_t desc_l = kLMajorK ? ptx::desc_kmajor_sw128(s_l) : desc_mnmajor_sw128(s_l);
+                    const uint64_t desc_r = kRMajorK ? ptx::desc_kmajor_sw128(s_r) : desc_mnmajor_sw128(s_r);
+                    const int32_t left = t.red - i * kGrBlock;
+#pragma unroll
+                    for (int j = 0; j < kGrBlock / 16; ++j)
+                        if (left > 16 * j)
+                            ptx::mma_f16<kGroup>(d_tmem[h], desc_l + kStepL * j, desc_r + kStepR * j, idesc[h],
+                                                 (i | j) != 0 ? 1u : 0u);
+                };
+                // A tile's second half may have to wait for the epilogue to read its
+                // accumulator.  Until then stages are held with only their first half's MMAs
+                // issued, at most kStages - 1 of them, so that the producer always has one to
+                // fill; the held stages' second halves follow in order.
+                const uint32_t bar1 = accempty_bar((sub + 1) & 1u), phase1 = (((sub + 1) >> 1) & 1u) ^ 1u;
+                bool free1 = halves == 1;
+                int held = 0, held_stage = 0;
+                int32_t held_block = 0;
+                auto flush = [&]() {
+                    ptx::tc_fence_after_sync();
+                    for (; held > 0; --held, ++held_block) {
+                        if (ptx::elect_one()) {
+                            issue(held_stage, 0, held_block, Cfg::kHalves - 1);
+                            ptx::mma_commit<kGroup>(empty_bar(held_stage), kMask);
+                        }
+                        __syncwarp();
+                        if (++held_stage == kStages) held_stage = 0;
+                    }
+                };
                 for (int32_t i = 0; ok && i < blocks; i += kAtoms) {
 #pragma unroll
                     for (int a = 0; a < kAtoms; ++a) {
-                        if (!w.wait(full_bar(stage, a), phase, kSiteLoaded)) {
+                        if (!wait_warp(w, full_bar(stage, a), phase, kSiteLoaded)) {
                             ok = false;
                             break;
                         }
                         ptx::tc_fence_after_sync();
-                        const uint32_t s_l = s_ring + stage * Cfg::kStageBytes + a * Cfg::kBlockBytes;
-                        const uint32_t s_r = s_l + Cfg::kLBytes;
-                        const uint64_t desc_l = kLMajorK ? ptx::desc_kmajor_sw128(s_l) : desc_mnmajor_sw128(s_l);
-                        const uint64_t desc_r = kRMajorK ? ptx::desc_kmajor_sw128(s_r) : desc_mnmajor_sw128(s_r);
-                        // terms past the end of the sum are zeros: whole steps of them are left out
-                        const int32_t left = t.red - (i + a) * kGrBlock;
-#pragma unroll
-                        for (int j = 0; j < kGrBlock / 16; ++j)
-                            if (left > 16 * j)
-                                ptx::mma_f16<kGroup>(d_tmem, desc_l + kStepL * j, desc_r + kStepR * j, idesc,
-                                                     (i | a | j) != 0 ? 1u : 0u);
+                        if (ptx::elect_one()) {
+                            issue(stage, a, i + a, 0);
+                            // (a tile's last block of one half: the stage is free behind its MMAs)
+                            if (Cfg::kHalves == 1 && a == kAtoms - 1) ptx::mma_commit<kGroup>(empty_bar(stage), kMask);
+                        }
+                        __syncwarp();
                         issued_any = true;
                     }
                     if (!ok) break;
-                    ptx::mma_commit<kGroup>(empty_bar(stage), kMask);
+                    if constexpr (Cfg::kHalves == 2) {
+                        if (!free1) free1 = __all_sync(0xffffffffu, ptx::mbar_test_wait(bar1, phase1));
+                        if (!free1 && held + 1 < kStages && i + 1 < blocks) {
+                            if (held == 0) {
+                                held_stage = stage;
+                                held_block = i;
+                            }
+                            ++held;
+                            if (++stage == kStages) {
+                                stage = 0;
+                                phase ^= 1u;
+                            }
+                            continue;
+                        }
+                        if (!free1 && !(free1 = wait_warp(w, bar1, phase1, kSiteAccEmpty))) {
+                            ok = false;
+                            break;
+                        }
+                        if (halves == 2) flush();
+                        if (ptx::elect_one()) {
+                            if (halves == 2) issue(stage, 0, i, 1);
+                            ptx::mma_commit<kGroup>(empty_bar(stage), kMask);
+                        }
+                        __syncwarp();
+                    }
                     if (++stage == kStages) {
                         stage = 0;
                         phase ^= 1u;
                     }
                 }
                 if (!ok) break;
-                ptx::mma_commit<kGroup>(accfull_bar(acc), kMask);
-                if (++acc == 2) {
-                    acc = 0;
-                    acc_phase ^= 1u;
+                for (int h = 0; h < halves; ++h, ++sub) {
+                    if (ptx::elect_one()) ptx::mma_commit<kGroup>(accfull_bar(sub & 1u), kMask);
+                    __syncwarp();
                 }
             }
             // every MMA this thread issued completes before TMEM is freed
-            if (issued_any) {
+            if (issued_any && ptx::elect_one()) {
                 ptx::mma_commit<kGroup>(drain_bar, 1);
                 w.drain(drain_bar, 0u);
             }
         }
     } else {
-        // ------------------------------------------------ epilogue (warps 2..5, every CTA)
-        // The accumulator holds the result transposed (its lanes are the result's
-        // contiguous index).  A warp takes its 32 lanes by 32 columns as 8 x 8
-        // fragments, stores them transposed to its staging rows of 64 bytes, and
-        // writes those out 16 bytes a lane, whole 32-byte sectors.  The 16-byte
-        // pieces of two rows share a 128-byte line and are permuted within it, so
-        // that neither side meets a bank twice.
+        // ------------------------------------------------ epilogue (warps 2..9, every CTA)
         const int quarter = warp & 3;             // TMEM lanes 32*quarter .. +31 are this warp's
-        const uint32_t s_mine = s_staging + (warp - 2) * kGrStageBytes;
-        auto piece = [&](int row, int c) {        // address of 16-byte piece c (0 .. 3) of a staging row
-            return s_mine + (row >> 1) * 128 + (((((row & 1) << 2) | c) ^ ((row >> 1) & 3)) << 4);
-        };
-        int acc = 0;
-        uint32_t acc_phase = 0;
-        const bool out_bf16 = p.out_fmt != 0, vec = p.out_vec != 0, scaled = p.scale_l != nullptr;
-        for (int32_t u = slot; u < total; u += slots) {
+        const int turn = (warp - 2) >> 2;         // of the columns' steps, the quarter's two warps take every other one
+        GroupedStore store;
+        store.init(s_staging + (warp - 2) * kGrStageBytes, lane);
+        store.ld = p.out_ld;
+        uint32_t sub = 0;                         // halves so far
+        bool ok = true;
+        const bool out_bf16 = p.out_fmt != 0;
+        for (int32_t u = slot; ok && u < total; u += slots) {
             const GroupedTile t = walk.at(u);
             const int32_t l0 = t.l0 + static_cast<int32_t>(pos) * Cfg::kRowsL + 32 * quarter;   // this warp's 32
             const int64_t row0 = static_cast<int64_t>(kOp == kGrGradA ? 0 : start[t.e]) + t.r0;
             uint16_t *out = p.out + t.e * p.out_stride + row0 * p.out_ld + l0;
-            const int32_t wide = p.l_extent - l0 < 32 ? p.l_extent - l0 : 32;   // of them inside the result
+            store.wide = p.l_extent - l0 < 32 ? p.l_extent - l0 : 32;
+            store.vec = p.out_vec != 0 && store.wide == 32;
             if (t.red == 0) {                     // an empty sum
-                if (lane < wide)
-                    for (int32_t r = 0; r < t.rows; ++r) out[r * p.out_ld + lane] = 0;
+                if (lane < store.wide)
+                    for (int32_t r = turn; r < t.rows; r += 2) out[r * p.out_ld + lane] = 0;
                 continue;
             }
-            float scale_l[4] = {1.0f, 1.0f, 1.0f, 1.0f};      // of lanes l0 + 8 i + lane / 4
-            if (scaled) {
+            if constexpr (kOp == kGrI8) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    if (8 * i + (lane >> 2) < wide)
-                        scale_l[i] = __ldg(p.scale_l + static_cast<int64_t>(t.e) * p.l_extent + l0 + 8 * i + (lane >> 2));
+                    store.scale_l[i] = 8 * i + (lane >> 2) < store.wide
+                                           ? __ldg(p.scale_l + static_cast<int64_t>(t.e) * p.l_extent + l0 + 8 * i + (lane >> 2))
+                                           : 0.0f;
             }
-            if (!__all_sync(0xffffffffu, w.wait(accfull_bar(acc), acc_phase, kSiteAccFull))) break;
-            ptx::tc_fence_after_sync();
-            const uint32_t t_row = tmem_base + (static_cast<uint32_t>(32 * quarter) << 16) + acc * Cfg::kAccCols;
-            for (int32_t c = 0; c < t.n_mma; c += kGrChunk) {
-                uint32_t v[2][16];
-                ptx::tmem_ld_16x256b_x4(t_row + c, v[0]);
-                ptx::tmem_ld_16x256b_x4(t_row + (16u << 16) + c, v[1]);
-                ptx::tmem_ld_wait(v[0], v[1]);
-                if (c + kGrChunk >= t.n_mma) {    // the accumulator is read: hand it back
+#pragma unroll 1
+            for (int half = 0; half < Cfg::kHalves; ++half) {
+                const int32_t first = half * Cfg::kHalfRows;       // the half's first row within the tile
+                const int32_t n_mma = half == 0 ? t.n_mma[0] : t.n_mma[1];
+                if (half > 0 && n_mma == 0) break;
+                ok = wait_warp(w, accfull_bar(sub & 1u), (sub >> 1) & 1u, kSiteAccFull);
+                if (!ok) break;
+                ptx::tc_fence_after_sync();
+                const uint32_t t_row =
+                    tmem_base + (static_cast<uint32_t>(32 * quarter) << 16) + (sub & 1u) * Cfg::kAccCols;
+                const int32_t steps = (n_mma + kGrChunk - 1) / kGrChunk;
+                auto hand_back = [&]() {          // this warp has read its part of the accumulator
                     ptx::tc_fence_before_sync();
                     __syncwarp();
                     if (lane == 0) {
                         if constexpr (kGroup == 2)
-                            ptx::mbar_arrive_remote(ptx::mapa_shared(accempty_bar(acc), 0));
+                            ptx::mbar_arrive_remote(ptx::mapa_shared(accempty_bar(sub & 1u), 0));
                         else
-                            ptx::mbar_arrive(accempty_bar(acc));
+                            ptx::mbar_arrive(accempty_bar(sub & 1u));
                     }
-                }
-                uint32_t h[2][4][2];              // [half of the lanes][8 columns][8 lanes]
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float s0 = 1.0f, s1 = 1.0f;
-                    if (scaled) {
-                        const int32_t r = c + 8 * i + 2 * (lane & 3);
-                        if (r < t.rows) s0 = __ldg(p.scale_r + row0 + r);
-                        if (r + 1 < t.rows) s1 = __ldg(p.scale_r + row0 + r + 1);
-                    }
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        float x0 = __uint_as_float(v[q >> 1][4 * i + 2 * (q & 1)]);
-                        float x1 = __uint_as_float(v[q >> 1][4 * i + 2 * (q & 1) + 1]);
-                        if (scaled) {
-                            x0 = x0 * scale_l[q] * s0;
-                            x1 = x1 * scale_l[q] * s1;
-                        }
-                        h[q >> 1][i][q & 1] = out_bf16 ? ptx::pack_bf16x2(x0, x1) : ptx::pack_f16x2(x0, x1);
-                    }
-                }
-                __syncwarp();                     // the last step's pieces have been read
-#pragma unroll
-                for (int half = 0; half < 2; ++half)
-#pragma unroll
-                    for (int i = 0; i < 4; i += 2)
-                        ptx::stmatrix_x4_trans(piece(8 * (i + (lane >> 4)) + (lane & 7), 2 * half + ((lane >> 3) & 1)),
-                                               h[half][i][0], h[half][i][1], h[half][i + 1][0], h[half][i + 1][1]);
-                __syncwarp();
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int row = 8 * q + (lane >> 2), col = 8 * (lane & 3);
-                    if (c + row >= t.rows || col >= wide) continue;
-                    const uint4 x = ptx::ld_shared_v4(piece(row, lane & 3));
-                    uint16_t *dst = out + (c + row) * p.out_ld + col;
-                    if (vec && col + 8 <= wide) {
-                        *reinterpret_cast<uint4 *>(dst) = x;
-                    } else {
-                        const uint32_t words[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                        for (int b = 0; b < 8; ++b)
-                            if (col + b < wide) dst[b] = static_cast<uint16_t>(words[b >> 1] >> (16 * (b & 1)));
-                    }
-                }
-            }
-            if (++acc == 2) {
-                acc = 0;
-                acc_phase ^= 1u;
+                };
+                uint16_t *dst = out + first * p.out_ld;
+                const int32_t rows = t.rows - first;
+                const float *scale_r = kOp == kGrI8 ? p.scale_r + row0 + first : nullptr;
+                if (out_bf16)
+                    store.half<true, kOp == kGrI8>(t_row, turn, steps, dst, rows, scale_r, hand_back);
+                else
+                    store.half<false, kOp == kGrI8>(t_row, turn, steps, dst, rows, scale_r, hand_back);
+                ++sub;
             }
         }
     }
@@ -693,15 +888,18 @@ struct WidenJob {
 
 // Four 8-bit integers to four halves: x + 128 in the low bits of 1024's
 // mantissa is 1152 + x, exactly.
+__device__ __forceinline__ uint32_t f16x2_minus_1152(uint32_t v)
+{
+    uint32_t r;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(0x64806480u));
+    return r;
+}
+
 __device__ __forceinline__ uint2 i8x4_to_f16x4(uint32_t w)
 {
     const uint32_t u = w ^ 0x80808080u;
-    uint2 r;
-    asm("{\n\t.reg .b32 a;\n\tprmt.b32 a, %1, 0x64646464, 0x4140;\n\tsub.rn.f16x2 %0, a, %2;\n\t}"
-        : "=r"(r.x) : "r"(u), "r"(0x64806480u));
-    asm("{\n\t.reg .b32 a;\n\tprmt.b32 a, %1, 0x64646464, 0x4342;\n\tsub.rn.f16x2 %0, a, %2;\n\t}"
-        : "=r"(r.y) : "r"(u), "r"(0x64806480u));
-    return r;
+    return make_uint2(f16x2_minus_1152(__byte_perm(u, 0x64646464u, 0x4140)),
+                      f16x2_minus_1152(__byte_perm(u, 0x64646464u, 0x4342)));
 }
 
 constexpr int kWidenThreads = 256;

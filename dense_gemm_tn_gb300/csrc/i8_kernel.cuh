@@ -1,0 +1,373 @@
+// tn_i8_kernel: the 8-bit integer product (dense, or grouped by expert) for few
+// rows per expert, where the read of the weights is what counts.
+//
+//     C[t, m] = (sum_k A[e, m, k] B[t, k]) scale_a[e, m] scale_b[t]
+//
+// The weights are read once, as the 8-bit integers they are, and widened to f16
+// (exactly) on the way to the tensor core: GB300 multiplies f16 an order of
+// magnitude faster than 8-bit integers.  Widening them in a kernel of its own,
+// as for more rows, moves five bytes per weight instead of one.
+//
+// Per CTA: 128 weights' rows (MMA M) by up to 64 tokens (MMA N), single CTAs.
+// Warp 0 loads 8-bit tiles of 128 terms by TMA; warps 6-13 widen the weights
+// into tensor memory, from where the MMAs of warp 1 take their A operand, and
+// the tokens into shared memory (two K-major 128B-swizzled blocks of 64 terms);
+// warps 2-5 scale and store.  With the weights widened into shared memory as
+// well, a stage's 108 KiB of shared-memory traffic (load, read, write, the
+// MMAs' reads) bound it: 820 cycles a stage, against 44 KiB this way.
+// Schedule, ragged ends, bounded waits and the epilogue's steps are the grouped
+// kernel's.
+#pragma once
+
+#include "grouped_kernel.cuh"
+
+namespace tn {
+
+constexpr int kI8EpiWarps = 4;
+constexpr int kI8WidenWarps = 8;                             // two teams, which take stages in turn
+constexpr int kI8TeamWarps = kI8WidenWarps / 2;
+constexpr int kI8Threads = 32 * (2 + kI8EpiWarps + kI8WidenWarps);
+constexpr int kI8Block = 128;                                // terms per 8-bit stage: 128 bytes
+
+constexpr int kI8RowsL = 128, kI8Rows = 64;
+constexpr int kI8Stage8Bytes = (kI8RowsL + kI8Rows) * 128;   // 8-bit stage: L, then R
+constexpr int kI8Stages8 = 6;
+constexpr int kI8HalfBytes = kI8Rows * 128;                  // 64 terms of R as f16
+constexpr int kI8Stage16Bytes = 2 * kI8HalfBytes;
+constexpr int kI8Stages16 = 2;                               // one per team
+// TMEM columns: two accumulators, then the two f16 stages of L (two terms a column)
+constexpr uint32_t kI8ACol0 = 2 * kI8Rows, kI8ACols = kI8Block / 2;
+constexpr uint32_t kI8TmemCols = kI8ACol0 + kI8Stages16 * kI8ACols;
+static_assert(kI8TmemCols == 256, "a power of two");
+// full8[S8], empty8[S8], full16[S16], empty16[S16], accfull[2], accempty[2], drain, never
+constexpr int kI8Barriers = 2 * kI8Stages8 + 2 * kI8Stages16 + 6;
+constexpr int kI8SmemBytes = 1024 /* alignment slack */ + kI8Stages8 * kI8Stage8Bytes + kI8Stages16 * kI8Stage16Bytes +
+                             kI8EpiWarps * kGrStageBytes + kI8Barriers * 8 + 32 + 2 * (kGrMaxExperts + 8) * 4;
+static_assert(kI8SmemBytes <= 232448, "exceeds the 227 KiB shared memory of one CTA");
+
+// Four 8-bit terms to f16, in the order 0, 2, 1, 3: what bounds the widening is
+// the integer pipe, and a mask is cheaper than byte permutations.  L's and R's
+// are widened alike, so each product still pairs a term with its own.
+__device__ __forceinline__ uint2 widen_word(uint32_t w)
+{
+    // x ^ 0x80 = x + 128 in the low bits of 1024's mantissa is 1152 + x
+    uint32_t a, b;
+    asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(a) : "r"(w), "r"(0x00FF00FFu), "r"(0x64806480u));
+    asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(b) : "r"(w >> 8), "r"(0x00FF00FFu), "r"(0x64806480u));
+    return make_uint2(f16x2_minus_1152(a), f16x2_minus_1152(b));
+}
+
+// A lane's part of widening eight rows (r0 .. r0 + 7) of a swizzled 8-bit tile
+// into the two swizzled f16 blocks: 16 terms of each 64-term half, two 16-byte
+// loads and four 16-byte stores.  An odd row does half 1 first, so that the two
+// rows of a shared-memory pass meet no bank twice, in the loads or the stores.
+struct WidenRows {
+    uint32_t ld[2], st[2];        // offsets of the piece done first and second: its load, its first store
+
+    __device__ __forceinline__ explicit WidenRows(int lane)
+    {
+        const int row = lane >> 2, c = lane & 3;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int half = (row & 1) ^ i;
+            ld[i] = row * 128 + (((4 * half + c) ^ row) << 4);
+            st[i] = half * kI8HalfBytes + row * 128 + (((2 * c) ^ row) << 4);
+        }
+    }
+    __device__ __forceinline__ void store(uint32_t dst, int i, const uint4 &w) const
+    {
+        const uint2 a = widen_word(w.x), b = widen_word(w.y), d = widen_word(w.z), e = widen_word(w.w);
+        ptx::st_shared_v4(dst + st[i], a.x, a.y, b.x, b.y);
+        ptx::st_shared_v4(dst + (st[i] ^ 16u), d.x, d.y, e.x, e.y);
+    }
+};
+
+__global__ void __launch_bounds__(kI8Threads, 1) tn_i8_kernel(const __grid_constant__ GroupedParams p)
+{
+    constexpr int kS8 = kI8Stages8, kS16 = kI8Stages16;
+
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t s_ring8 = ptx::smem_addr(smem), s_ring16 = s_ring8 + kS8 * kI8Stage8Bytes;
+    const uint32_t s_staging = s_ring16 + kS16 * kI8Stage16Bytes;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kS8 * kI8Stage8Bytes + kS16 * kI8Stage16Bytes + kI8EpiWarps * kGrStageBytes);
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + kI8Barriers);
+    volatile uint32_t *abort_flag = tmem_holder + 1;
+    int32_t *start = reinterpret_cast<int32_t *>(tmem_holder + 8);
+    int32_t *before = start + kGrMaxExperts + 8;
+    const uint32_t abort_addr = ptx::smem_addr(const_cast<uint32_t *>(abort_flag));
+    const uint32_t bar0 = ptx::smem_addr(bars);
+    auto full8_bar = [&](int s) { return bar0 + 8u * s; };
+    auto empty8_bar = [&](int s) { return bar0 + 8u * (kS8 + s); };
+    auto full16_bar = [&](int s) { return bar0 + 8u * (2 * kS8 + s); };
+    auto empty16_bar = [&](int s) { return bar0 + 8u * (2 * kS8 + kS16 + s); };
+    constexpr int kAcc0 = 2 * kS8 + 2 * kS16;
+    auto accfull_bar = [&](int b) { return bar0 + 8u * (kAcc0 + b); };
+    auto accempty_bar = [&](int b) { return bar0 + 8u * (kAcc0 + 2 + b); };
+    const uint32_t drain_bar = bar0 + 8u * (kAcc0 + 4);
+    const uint32_t never_bar = bar0 + 8u * (kAcc0 + 5);   // nothing ever arrives (test stalls)
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kS8; ++s) {
+            ptx::mbar_init(full8_bar(s), 1);
+            ptx::mbar_init(empty8_bar(s), kI8TeamWarps);
+        }
+        for (int s = 0; s < kS16; ++s) {
+            ptx::mbar_init(full16_bar(s), kI8TeamWarps);
+            ptx::mbar_init(empty16_bar(s), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            ptx::mbar_init(accfull_bar(b), 1);
+            ptx::mbar_init(accempty_bar(b), kI8EpiWarps);
+        }
+        ptx::mbar_init(drain_bar, 1);
+        ptx::mbar_init(never_bar, 1);
+        *abort_flag = 0u;
+        ptx::fence_mbar_init();
+        ptx::fence_proxy_async_smem();
+    }
+    if (threadIdx.x == 32 && p.red > 0) {
+        ptx::prefetch_tensormap(&p.tmap_l);
+        ptx::prefetch_tensormap(&p.tmap_r[0]);
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc<1>(ptx::smem_addr(tmem_holder), kI8TmemCols);
+        ptx::tmem_relinquish_alloc_permit<1>();
+    }
+    ptx::tc_fence_before_sync();
+    __syncthreads();
+    ptx::tc_fence_after_sync();
+    const uint32_t tmem_base = *tmem_holder;
+    const Waiter w{abort_flag, abort_addr, 0u, 1u, p.wait_limit_ns};
+
+    ptx::griddep_wait();                      // every thread's first global access is behind this wait
+    const int32_t l_tiles = (p.l_extent + kI8RowsL - 1) / kI8RowsL;
+    grouped_tables<kGrI8, kI8Rows, kI8Threads>(p, l_tiles, start, before);
+    const int32_t total = before[p.E];
+    const int32_t slot = static_cast<int32_t>(blockIdx.x), slots = static_cast<int32_t>(gridDim.x);
+    GroupedWalk<kGrI8, kI8Rows, kI8Rows, kI8RowsL, 16> walk{start, before, l_tiles, 0, p.red, 0};
+    const int32_t blocks = (p.red + kI8Block - 1) / kI8Block;       // 8-bit stages of a tile
+
+    if (warp == 0) {
+        // ------------------------------------------------ TMA producer
+        int stage = 0;
+        uint32_t phase = 0, n_issued = 0;
+        bool ok = true;
+        if (p.flags & kFlagStallProducer0) ok = wait_warp(w, never_bar, 0u, kSiteStall);
+        for (int32_t u = slot; ok && u < total; u += slots) {
+            const GroupedTile t = walk.at(u);
+            const CUtensorMap *map_r = p.tmap_r + t.n_mma[0] / 16 - 1;
+            const int32_t r0 = start[t.e] + t.r0;
+            const uint32_t fill = static_cast<uint32_t>(kI8RowsL + t.n_mma[0]) * 128u;
+            for (int32_t i = 0; i < blocks; ++i) {
+                if (!wait_warp(w, empty8_bar(stage), phase ^ 1u, kSiteEmpty)) {
+                    ok = false;
+                    break;
+                }
+                if (ptx::elect_one()) {
+                    const uint32_t s_l = s_ring8 + stage * kI8Stage8Bytes;
+                    ptx::mbar_arrive_expect_tx(full8_bar(stage), fill);
+                    tma_load_3d(s_l, &p.tmap_l, full8_bar(stage), i * kI8Block, t.l0, t.e);
+                    ptx::tma_load_2d(s_l + kI8RowsL * 128, map_r, full8_bar(stage), i * kI8Block, r0);
+                }
+                __syncwarp();
+                ++n_issued;
+                if (++stage == kS8) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+        if (lane == 0) ptx::griddep_launch_dependents();
+        if (ptx::elect_one())
+            for (int s = 0; s < kS8; ++s) {       // every issued load lands before the CTA can exit
+                const uint32_t passes = n_issued / kS8 + (static_cast<uint32_t>(s) < n_issued % kS8 ? 1u : 0u);
+                if (passes) w.drain(full8_bar(s), (passes - 1) & 1u);
+            }
+    } else if (warp == 1) {
+        // ------------------------------------------------ MMA issuer
+        int stage = 0;
+        uint32_t phase = 0, sub = 0;
+        bool ok = true, issued_any = false;
+        if (p.flags & kFlagStallMma) ok = wait_warp(w, never_bar, 0u, kSiteStall);
+        for (int32_t u = slot; ok && p.red > 0 && u < total; u += slots, ++sub) {
+            const GroupedTile t = walk.at(u);
+            const uint32_t idesc = ptx::idesc_f32acc(kI8RowsL, static_cast<uint32_t>(t.n_mma[0]), 0u, 0u);
+            const uint32_t d_tmem = tmem_base + (sub & 1u) * kI8Rows;
+            if (!wait_warp(w, accempty_bar(sub & 1u), ((sub >> 1) & 1u) ^ 1u, kSiteAccEmpty)) break;
+            ptx::tc_fence_after_sync();
+            for (int32_t i = 0; i < blocks; ++i) {
+                if (!wait_warp(w, full16_bar(stage), phase, kSiteLoaded)) {
+                    ok = false;
+                    break;
+                }
+                ptx::tc_fence_after_sync();
+                const int32_t left = p.red - i * kI8Block;
+                if (ptx::elect_one()) {
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const uint64_t desc_r =
+                            ptx::desc_kmajor_sw128(s_ring16 + stage * kI8Stage16Bytes + half * kI8HalfBytes);
+                        const uint32_t a_tmem = tmem_base + kI8ACol0 + stage * kI8ACols + half * (kI8ACols / 2);
+#pragma unroll
+                        for (int j = 0; j < kGrBlock / 16; ++j)
+                            if (left > half * kGrBlock + 16 * j)
+                                ptx::mma_f16_ts(d_tmem, a_tmem + 8 * j, desc_r + 2u * j, idesc,
+                                                (i | half | j) != 0 ? 1u : 0u);
+                    }
+                    ptx::mma_commit<1>(empty16_bar(stage));
+                    if (i + 1 == blocks) ptx::mma_commit<1>(accfull_bar(sub & 1u));
+                }
+                __syncwarp();
+                issued_any = true;
+                if (++stage == kS16) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+            if (!ok) break;
+        }
+        if (issued_any && ptx::elect_one()) {     // every MMA issued completes before TMEM is freed
+            ptx::mma_commit<1>(drain_bar);
+            w.drain(drain_bar, 0u);
+        }
+    } else if (warp < 2 + kI8EpiWarps) {
+        // ------------------------------------------------ epilogue (warps 2..5)
+        const int quarter = warp & 3;
+        GroupedStore store;
+        store.init(s_staging + (warp - 2) * kGrStageBytes, lane);
+        store.ld = p.out_ld;
+        uint32_t sub = 0;
+        for (int32_t u = slot; u < total; u += slots) {
+            const GroupedTile t = walk.at(u);
+            const int32_t l0 = t.l0 + 32 * quarter;
+            const int64_t row0 = static_cast<int64_t>(start[t.e]) + t.r0;
+            uint16_t *out = p.out + row0 * p.out_ld + l0;
+            store.wide = p.l_extent - l0 < 32 ? p.l_extent - l0 : 32;
+            store.vec = p.out_vec != 0 && store.wide == 32;
+            if (p.red == 0) {                     // an empty sum
+                if (lane < store.wide)
+                    for (int32_t r = 0; r < t.rows; ++r) out[r * p.out_ld + lane] = 0;
+                continue;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                store.scale_l[i] = 8 * i + (lane >> 2) < store.wide
+                                       ? __ldg(p.scale_l + static_cast<int64_t>(t.e) * p.l_extent + l0 + 8 * i + (lane >> 2))
+                                       : 0.0f;
+            if (!wait_warp(w, accfull_bar(sub & 1u), (sub >> 1) & 1u, kSiteAccFull)) break;
+            ptx::tc_fence_after_sync();
+            const uint32_t t_row = tmem_base + (static_cast<uint32_t>(32 * quarter) << 16) + (sub & 1u) * kI8Rows;
+            for (int32_t c = 0; c < t.n_mma[0]; c += kGrChunk) {
+                uint32_t v[2][16];
+                ptx::tmem_ld_16x256b_x4(t_row + c, v[0]);
+                ptx::tmem_ld_16x256b_x4(t_row + (16u << 16) + c, v[1]);
+                ptx::tmem_ld_wait_all();
+                ptx::reg_dependency(v[0]);
+                ptx::reg_dependency(v[1]);
+                if (c + kGrChunk >= t.n_mma[0]) {
+                    ptx::tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(accempty_bar(sub & 1u));
+                }
+                if (p.out_fmt != 0)
+                    store.step<true, true>(v, out + c * p.out_ld, t.rows - c, p.scale_r + row0 + c);
+                else
+                    store.step<false, true>(v, out + c * p.out_ld, t.rows - c, p.scale_r + row0 + c);
+            }
+            ++sub;
+        }
+    } else {
+        // ------------------------------------------------ widening (warps 6..13)
+        // Two teams of four warps take the stages in turn, each into an f16 stage of
+        // its own: while one waits, loads or stores, the other has the integer pipe.
+        // A warp widens the 32 rows of L that are its quarter of the TMEM lanes, a row
+        // a lane, and its share of R's groups of eight rows.
+        const int team = (warp - 2 - kI8EpiWarps) / kI8TeamWarps, mine = (warp - 2 - kI8EpiWarps) % kI8TeamWarps;
+        static_assert(kS16 == 2 && kS8 % 2 == 0, "a team's stages are every other one");
+        const int quarter = warp & 3;
+        const WidenRows widen(lane);
+        const uint32_t row_l = static_cast<uint32_t>(32 * quarter + lane) * 128u;
+        const uint32_t t_a = tmem_base + (static_cast<uint32_t>(32 * quarter) << 16) + kI8ACol0 + team * kI8ACols;
+        const uint32_t dst = s_ring16 + team * kI8Stage16Bytes + mine * 1024;
+        constexpr int kOwnR = kI8Rows / 8 / kI8TeamWarps;     // groups of R a warp has at most
+        bool ok = true;
+        int stage8 = team;
+        uint32_t phase8 = 0, phase16 = 0, n = 0;              // n: stages so far
+        for (int32_t u = slot; ok && p.red > 0 && u < total; u += slots) {
+            const int32_t groups_r = walk.at(u).n_mma[0] / 8;
+            for (int32_t i = 0; i < blocks; ++i, ++n) {
+                if ((n & 1u) != static_cast<uint32_t>(team)) continue;
+                ok = wait_warp(w, full8_bar(stage8), phase8, kSiteLoaded);
+                if (!ok) break;
+                const uint32_t src = s_ring8 + stage8 * kI8Stage8Bytes;
+                uint4 v[4], r[kOwnR][2];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) v[c] = ptx::ld_shared_v4(src + row_l + ((c ^ (lane & 7)) << 4));
+#pragma unroll
+                for (int g = 0; g < kOwnR; ++g)
+                    if (mine + g * kI8TeamWarps < groups_r) {
+                        const uint32_t at = src + (kI8RowsL + 8 * (mine + g * kI8TeamWarps)) * 128;
+                        r[g][0] = ptx::ld_shared_v4(at + widen.ld[0]);
+                        r[g][1] = ptx::ld_shared_v4(at + widen.ld[1]);
+                    }
+                ok = wait_warp(w, empty16_bar(team), phase16 ^ 1u, kSiteEmpty);
+                if (!ok) break;
+                ptx::tc_fence_after_sync();                   // the MMAs that read this stage are done
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t f[32];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const uint32_t words[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const uint2 x = widen_word(words[q]);
+                            f[8 * c + 2 * q] = x.x;
+                            f[8 * c + 2 * q + 1] = x.y;
+                        }
+                    }
+                    if (half == 0) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) v[c] = ptx::ld_shared_v4(src + row_l + (((4 + c) ^ (lane & 7)) << 4));
+                    }
+                    ptx::tmem_st_32x32b_x32(t_a + half * (kI8ACols / 2), f);
+                }
+#pragma unroll
+                for (int g = 0; g < kOwnR; ++g)
+                    if (mine + g * kI8TeamWarps < groups_r) {
+                        widen.store(dst + g * kI8TeamWarps * 1024, 0, r[g][0]);
+                        widen.store(dst + g * kI8TeamWarps * 1024, 1, r[g][1]);
+                    }
+                ptx::fence_proxy_async_smem();                // the MMAs read what was stored
+                ptx::tmem_st_wait();
+                ptx::tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    ptx::mbar_arrive(full16_bar(team));
+                    ptx::mbar_arrive(empty8_bar(stage8));
+                }
+                phase16 ^= 1u;
+                stage8 += 2;
+                if (stage8 >= kS8) {
+                    stage8 -= kS8;
+                    phase8 ^= 1u;
+                }
+            }
+        }
+    }
+
+    __syncwarp();                // .aligned barriers below need converged warps
+    ptx::tc_fence_before_sync();
+    __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        ptx::tc_fence_after_sync();
+        ptx::tmem_dealloc<1>(tmem_base, kI8TmemCols);
+    }
+}
+
+}  // namespace tn

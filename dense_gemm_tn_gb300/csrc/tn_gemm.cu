@@ -25,6 +25,7 @@
 #include "repack_kernel.cuh"
 #include "quant_e4m3_kernel.cuh"
 #include "grouped_kernel.cuh"
+#include "i8_kernel.cuh"
 #include "quant_i8_kernel.cuh"
 
 namespace {
@@ -95,7 +96,8 @@ struct DeviceState {
     std::unordered_map<cudaStream_t, Split> stats;
     int quant_blocks[3] = {};         // co-resident quantiser CTAs per SM, by input type (0 = not queried)
     bool skinny_attr[2] = {};         // tn_skinny_kernel's shared-memory attribute set, by kind
-    int grouped_slots[3][3] = {};     // co-resident tn_grouped_kernel CTAs or pairs, by operation and variant (0 = not queried)
+    int grouped_slots[4][3] = {};     // co-resident tn_grouped_kernel CTAs or pairs, by operation and variant (0 = not queried)
+    bool i8_attr = false;             // tn_i8_kernel's shared-memory attribute set
     // One lock per stream, held by a call from its first buffer lookup through
     // its last launch: a call is several launches (row copy, GEMM, reduce),
     // and two host threads' calls on one stream must not interleave them.

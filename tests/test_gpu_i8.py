@@ -35,7 +35,8 @@ def assert_scaled(got, sums, sa, sb, terms, dtype):
 
 @pytest.mark.parametrize("dtype", TYPES, ids=["f16", "bf16"])
 @pytest.mark.parametrize("M,N,K", [(1, 1, 1), (8, 1, 16), (128, 16, 128), (257, 3, 80), (64, 65, 63), (130, 300, 1000),
-                                   (512, 64, 2048), (1000, 513, 333), (33, 100, 5)])
+                                   (512, 64, 2048), (1000, 513, 333), (33, 100, 5), (300, 17, 144), (129, 128, 400),
+                                   (2000, 100, 1040), (128, 129, 256), (40, 1, 4096), (640, 112, 16), (20000, 33, 128)])
 def test_i8_product(M, N, K, dtype):
     A, Bt, sa, sb = codes(M, K, seed=1), codes(N, K, seed=2), scales(M, seed=3), scales(N, seed=4)
     C = g.i8_tn(A, Bt, sa, sb, dtype=dtype)
@@ -44,7 +45,8 @@ def test_i8_product(M, N, K, dtype):
     assert_scaled(C, Bt.double() @ A.double().t(), sa[None, :], sb[:, None], K, dtype)
 
 
-@pytest.mark.parametrize("counts,M,K", [([1], 16, 16), ([0, 3, 0, 1], 128, 64), ([70, 0, 300], 200, 208), ([5, 6], 31, 33)])
+@pytest.mark.parametrize("counts,M,K", [([1], 16, 16), ([0, 3, 0, 1], 128, 64), ([70, 0, 300], 200, 208), ([5, 6], 31, 33),
+                                        ([1] * 40, 384, 272), ([64, 0, 65, 3], 130, 128), ([200, 10, 100], 136, 112)])
 def test_i8_grouped(counts, M, K):
     E, T = len(counts), sum(counts)
     off = offsets_of(counts)

@@ -68,7 +68,7 @@ INVALID = [
     (grad_a, dict(ws=None)), (grad_a, dict(n=256)), (grad_a, dict(stride_da=8, ldda=8)), (grad_a, dict(stride_da=-1)),
     (grad_a, dict(dA=None)), (grad_a, dict(type=g.GEMM_IN_F32)), (grad_a, dict(ldda=7)), (grad_a, dict(lddc=15)),
     (i8, dict(type=g.GEMM_IN_F32)), (i8, dict(sa=None)), (i8, dict(sb=None)), (i8, dict(sa=P + 2)), (i8, dict(lda=15)),
-    (i8, dict(ldc=15)), (i8, dict(N=-1)), (i8, dict(C=5 * P + 1)), (i8, dict(n=0)), (i8, dict(ws=None)),
+    (i8, dict(ldc=15)), (i8, dict(N=-1)), (i8, dict(C=5 * P + 1)), (i8, dict(lda=17, n=0)), (i8, dict(lda=17, ws=None)), (i8, dict(N=600, n=0)),
     (i8_grouped, dict(offsets=None)), (i8_grouped, dict(sb=None)), (i8_grouped, dict(ldb=15)), (i8_grouped, dict(T=-1)),
     (quant, dict(type=9)), (quant, dict(rows=-1)), (quant, dict(cols=-1)), (quant, dict(ldx=7)), (quant, dict(ldq=7)),
     (quant, dict(x=None)), (quant, dict(q=None)), (quant, dict(scale=None)), (quant, dict(scale=P + 2)),
@@ -158,11 +158,15 @@ def test_helpers_refuse_shapes_types_and_places():
         g.quantize_i8_rows(torch.zeros(4, 4, dtype=torch.float16))
 
 
-def test_rows_are_cut_into_equal_tiles_that_cover_them():
-    """The kernel's cut of a group's rows, restated: every tile has a row, none is
-    taller than the largest, and together they are the group's rows."""
-    for largest, step in ((256, 32), (64, 16)):
+def test_rows_are_cut_into_even_tiles_that_cover_them():
+    """The kernel's cut of a group's rows, restated: steps of the MMA's N side spread
+    evenly over the fewest tiles; every tile has a row, none is taller than the
+    largest, and together they are the group's rows."""
+    for largest, step in ((512, 32), (256, 32), (64, 16)):
         for rows in list(range(1, 3000)) + [16383, 16384, 16385, 10 ** 6 + 1]:
-            tiles = -(-rows // largest)
-            h = -(-(-(-rows // tiles)) // step) * step
-            assert h <= largest and (tiles - 1) * h < rows <= tiles * h
+            tiles, steps = -(-rows // largest), -(-rows // step)
+            each, more = divmod(steps, tiles)
+            heights = [(each + (r < more)) * step for r in range(tiles)]
+            starts = [(r * each + min(r, more)) * step for r in range(tiles)]
+            assert max(heights) <= largest and starts[-1] < rows <= starts[-1] + heights[-1]
+            assert all(a + h == b for a, h, b in zip(starts, heights, starts[1:]))
