@@ -249,8 +249,12 @@ gemm_status_t launch_grouped_op(const GroupedCall &c, DeviceState &dev, tn::Grou
                                 int64_t inner_x, int64_t inner_y)
 {
     // Few rows per expert: bound by the read of the weights, on single CTAs of
-    // 128 x 64 tiles (twice as many of them, and a deeper ring); else CTA pairs.
-    const bool few = kOp != tn::kGrGradA && c.T <= 64 * c.E;
+    // 128 x 64 tiles (twice as many of them, and no pair to set up), as long as an
+    // expert's rows mostly fit one tile.  Measured on GB300, single CTAs / pairs: 16
+    // experts of 4096 x 1024 with 1 row on average 16.5 / 17.3 us, 32 rows 27.6 /
+    // 28.6; 8 of 2048 x 4096 with 32 rows 26.2 / 28.2, but with 48 (some over 64)
+    // 35.8 / 28.6.
+    const bool few = kOp != tn::kGrGradA && c.T <= 32 * c.E;
     gemm_status_t st;
     if (prm.red > 0) {
         const CUtensorMapDataType type =
@@ -414,10 +418,10 @@ gemm_status_t run_grouped(const GroupedCall &c)
 
 // Launches the row quantiser: a warp per row up to 8 windows of 16 bytes a lane
 // (4 KiB of x), unless the rows are too few to fill the SMs that way; then a
-// CTA of 256 or 512 threads with up to 8 windows a thread (32 and 64 KiB);
-// beyond that the kernel that reads x twice.
+// CTA of 256, 512 or 1024 threads with up to 8 windows a thread (32, 64 and 128
+// KiB); beyond that the kernel that reads x twice.
 template <int kIn>
-gemm_status_t launch_quant_rows(DeviceState &dev, const qz::QuantRowsParams &prm, cudaStream_t stream)
+gemm_status_t launch_quant_rows(DeviceState &dev, qz::QuantRowsParams &prm, cudaStream_t stream)
 {
     constexpr int64_t kElem = qz::elem_bytes(kIn), kVec = 16 / kElem;
     const bool aligned = reinterpret_cast<uintptr_t>(prm.x) % 16 == 0 && reinterpret_cast<uintptr_t>(prm.q) % kVec == 0 &&
@@ -425,20 +429,30 @@ gemm_status_t launch_quant_rows(DeviceState &dev, const qz::QuantRowsParams &prm
     const int64_t windows = (prm.cols + kVec - 1) / kVec + (aligned ? 0 : 1);
     void (*kernel)(qz::QuantRowsParams);
     int threads = qz::kRowThreads, rows_per_cta = 1;
-    const bool long_rows = windows > 512 * 8;
-    if (windows <= 32 * 8 && prm.rows > 8 * dev.sms) {
+    // a row's codes are staged in shared memory where rows are not aligned (more
+    // than 48 KiB of them: the kernel for long rows, which does not stage)
+    const int64_t staging = aligned ? 0 : (windows * kVec + 4 + 15) / 16 * 16;
+    const bool long_rows = windows > 1024 * 8 || staging > 49152;
+    prm.staging_bytes = long_rows ? 0 : static_cast<int32_t>(staging);
+    if (long_rows) {
+        kernel = qz::quant_long_rows_kernel<kIn>;
+        threads = qz::kLongThreads;
+    } else if (windows <= 32 * 2 && prm.rows > 8 * dev.sms) {
+        kernel = aligned ? qz::quant_rows_kernel<kIn, 32, 2, true> : qz::quant_rows_kernel<kIn, 32, 2, false>;
+        rows_per_cta = qz::kRowThreads / 32;
+    } else if (windows <= 32 * 8 && prm.rows > 8 * dev.sms) {
         kernel = aligned ? qz::quant_rows_kernel<kIn, 32, 8, true> : qz::quant_rows_kernel<kIn, 32, 8, false>;
         rows_per_cta = qz::kRowThreads / 32;
-    } else if (windows <= 256 * 4) {
-        kernel = aligned ? qz::quant_rows_kernel<kIn, 256, 4, true> : qz::quant_rows_kernel<kIn, 256, 4, false>;
+    } else if (windows <= 256 * (aligned ? 4 : 5)) {      // (a row off its alignment has a window more)
+        kernel = aligned ? qz::quant_rows_kernel<kIn, 256, 4, true> : qz::quant_rows_kernel<kIn, 256, 5, false>;
     } else if (windows <= 256 * 8) {
         kernel = aligned ? qz::quant_rows_kernel<kIn, 256, 8, true> : qz::quant_rows_kernel<kIn, 256, 8, false>;
-    } else if (!long_rows) {
+    } else if (windows <= 512 * 8) {
         kernel = aligned ? qz::quant_rows_kernel<kIn, 512, 8, true> : qz::quant_rows_kernel<kIn, 512, 8, false>;
         threads = 512;
     } else {
-        kernel = qz::quant_long_rows_kernel<kIn>;
-        threads = qz::kLongThreads;
+        kernel = aligned ? qz::quant_rows_kernel<kIn, 1024, 8, true> : qz::quant_rows_kernel<kIn, 1024, 8, false>;
+        threads = 1024;
     }
     int64_t grid = (prm.rows + rows_per_cta - 1) / rows_per_cta;
     if (long_rows && grid > int64_t(dev.sms) * 4) grid = int64_t(dev.sms) * 4;
@@ -449,6 +463,7 @@ gemm_status_t launch_quant_rows(DeviceState &dev, const qz::QuantRowsParams &prm
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
     cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>(rows_per_cta) * prm.staging_bytes;
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
@@ -485,7 +500,7 @@ gemm_status_t run_quant_rows(const void *x, int x_type, int64_t rows, int64_t co
     DeviceState *dev = nullptr;
     gemm_status_t st = device_state(&dev, nullptr);
     if (st != GEMM_OK) return st;
-    const qz::QuantRowsParams prm{x, q, scale, ldx, ldq, rows, cols};
+    qz::QuantRowsParams prm{x, q, scale, ldx, ldq, rows, cols, 0};
     switch (x_type) {
     case qz::kInF32: return launch_quant_rows<qz::kInF32>(*dev, prm, stream);
     case qz::kInF16: return launch_quant_rows<qz::kInF16>(*dev, prm, stream);

@@ -27,6 +27,7 @@ struct QuantRowsParams {
     int8_t *q;                // rows x cols codes, row stride ldq
     float *scale;             // rows
     int64_t ldx, ldq, rows, cols;
+    int32_t staging_bytes;    // shared memory for one row's codes
 };
 
 // The code of an fp32 x next to the border n + 1/2 of two codes, n = floor(127 |x| / a):
@@ -110,14 +111,12 @@ __device__ __forceinline__ uint2 window_codes(const uint4 &w, float lift, float 
     return make_uint2(packed[0], packed[1]);
 }
 
-// Window `i` of a row: 16 bytes of x from column i * kVec - skew on, the columns
-// outside the row 0 (and not read).
+// The 16 bytes of x from column c on, the columns outside the row 0 (and not
+// read): a window that reaches past an end of the row.
 template <int kIn>
-__device__ __forceinline__ uint4 load_window(const uint8_t *row, int32_t skew, int32_t cols, int32_t i)
+__device__ __noinline__ uint4 part_window(const uint8_t *row, int32_t c, int32_t cols)
 {
     constexpr int kVec = In<kIn>::kVec, kElem = elem_bytes(kIn);
-    const int32_t c = i * kVec - skew;
-    if (c >= 0 && c + kVec <= cols) return __ldcs(reinterpret_cast<const uint4 *>(row - skew * kElem) + i);
     union {
         uint16_t h[8];
         uint32_t f[4];
@@ -158,20 +157,28 @@ __device__ __forceinline__ uint32_t window_top(uint32_t acc)
     return __float_as_uint(In<kIn>::amax(acc)) & 0x7FFFFFFFu;
 }
 
+// CTAs per SM that the registers leave room for: what hides the loads' latency
+// and the steps of a row is other rows.
+__host__ __device__ constexpr int quant_min_blocks(int team, int windows)
+{
+    return windows == 2 ? 6 : team <= 256 ? (windows <= 5 ? 5 : 4) : team == 512 ? 2 : 1;
+}
+
 // kTeam threads per row (a warp, or a whole CTA), which keep the row's 16-byte
 // windows in registers, kWindows each: one read of x, one write of q.  kAligned:
 // rows of x start on 16-byte boundaries and rows of q where a window's codes
 // can be stored at once.  Otherwise the windows are those of the aligned
 // addresses that the row lies in; the first and last are read element by
-// element, and the codes are put into a row of shared memory at the row's own
-// misalignment, from where they are written in aligned 16-byte pieces.
+// element, and the codes are staged in a row of shared memory, from where they
+// are written in aligned words (with byte stores at the row's own misalignment
+// 16384 x 8191 bf16 took 136 us).
 template <int kIn, int kTeam, int kWindows, bool kAligned>
-__global__ void __launch_bounds__(kTeam == 32 ? kRowThreads : kTeam) quant_rows_kernel(const QuantRowsParams p)
+__global__ void __launch_bounds__(kTeam == 32 ? kRowThreads : kTeam, quant_min_blocks(kTeam, kWindows)) quant_rows_kernel(const QuantRowsParams p)
 {
     constexpr int kVec = In<kIn>::kVec, kElem = elem_bytes(kIn);
     constexpr int kTeams = kTeam == 32 ? kRowThreads / 32 : 1, kTeamWarps = kTeam / 32;
     __shared__ uint32_t warp_top[kTeamWarps];
-    __shared__ __align__(16) uint8_t staged[kAligned ? 16 : kTeams * (kTeam * kWindows * kVec + 16)];
+    extern __shared__ __align__(16) uint8_t staged[];        // !kAligned: staging_bytes a team
     tn::ptx::griddep_wait();
     const int t = kTeam == 32 ? threadIdx.x & 31 : threadIdx.x, team = kTeam == 32 ? threadIdx.x >> 5 : 0;
     const int64_t r = static_cast<int64_t>(blockIdx.x) * kTeams + team;
@@ -181,10 +188,18 @@ __global__ void __launch_bounds__(kTeam == 32 ? kRowThreads : kTeam) quant_rows_
     const int32_t skew = kAligned ? 0 : static_cast<int32_t>((reinterpret_cast<uintptr_t>(row) & 15u) / kElem);
     uint4 w[kWindows];
     uint32_t top = 0;
+    // whole windows first, all of their loads in flight; then the row's ends
 #pragma unroll
-    for (int i = 0; i < kWindows; ++i)
-        w[i] = in && (t + i * kTeam) * kVec - skew < cols ? load_window<kIn>(row, skew, cols, t + i * kTeam)
-                                                          : make_uint4(0u, 0u, 0u, 0u);
+    for (int i = 0; i < kWindows; ++i) {
+        const int32_t c = (t + i * kTeam) * kVec - skew;
+        w[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (in && c >= 0 && c + kVec <= cols) w[i] = __ldcs(reinterpret_cast<const uint4 *>(row + c * kElem));
+    }
+#pragma unroll
+    for (int i = 0; i < kWindows; ++i) {
+        const int32_t c = (t + i * kTeam) * kVec - skew;
+        if (in && c < cols && (c < 0 || c + kVec > cols)) w[i] = part_window<kIn>(row, c, cols);
+    }
 #pragma unroll
     for (int i = 0; i < kWindows; ++i) top = In<kIn>::acc_chunk(top, w[i]);
     top = __reduce_max_sync(0xffffffffu, window_top<kIn>(top));
@@ -195,29 +210,23 @@ __global__ void __launch_bounds__(kTeam == 32 ? kRowThreads : kTeam) quant_rows_
     }
     const RowScale rs(top, in && t == 0 ? p.scale + r : nullptr);
     int8_t *q = p.q + (in ? r : 0) * p.ldq;
-    uint8_t *mine = staged + team * (kTeam * kWindows * kVec + 16);
-    const int32_t q_skew = kAligned ? 0 : static_cast<int32_t>(reinterpret_cast<uintptr_t>(q) & 15u);
+    uint8_t *mine = staged + team * p.staging_bytes;
 #pragma unroll
     for (int i = 0; i < kWindows; ++i) {
         const int32_t c = (t + i * kTeam) * kVec - skew;
         if (!in || c >= cols) continue;
         const uint2 k = rs.codes ? window_codes<kIn>(w[i], rs.lift, rs.a, rs.inv) : make_uint2(0u, 0u);
-        if constexpr (kAligned) {
-            if (c + kVec <= cols) {
-                if constexpr (kVec == 8)
-                    __stcs(reinterpret_cast<uint2 *>(q + c), k);
-                else
-                    __stcs(reinterpret_cast<uint32_t *>(q + c), k.x);
-            } else {
-#pragma unroll
-                for (int j = 0; j < kVec; ++j)
-                    if (c + j < cols) q[c + j] = static_cast<int8_t>((j < 4 ? k.x : k.y) >> (8 * (j & 3)));
-            }
+        if (!kAligned || c + kVec <= cols) {
+            // (staged: column c at byte skew + c)
+            void *to = kAligned ? static_cast<void *>(q + c) : static_cast<void *>(mine + (t + i * kTeam) * kVec);
+            if constexpr (kVec == 8)
+                *static_cast<uint2 *>(to) = k;
+            else
+                *static_cast<uint32_t *>(to) = k.x;
         } else {
 #pragma unroll
             for (int j = 0; j < kVec; ++j)
-                if (c + j >= 0 && c + j < cols)
-                    mine[q_skew + c + j] = static_cast<uint8_t>((j < 4 ? k.x : k.y) >> (8 * (j & 3)));
+                if (c + j < cols) q[c + j] = static_cast<int8_t>((j < 4 ? k.x : k.y) >> (8 * (j & 3)));
         }
     }
     if constexpr (!kAligned) {
@@ -226,12 +235,17 @@ __global__ void __launch_bounds__(kTeam == 32 ? kRowThreads : kTeam) quant_rows_
         else
             __syncthreads();
         if (!in) return;
-        for (int32_t b = t * 16; b < q_skew + cols; b += kTeam * 16) {
-            if (b >= q_skew && b + 16 <= q_skew + cols) {
-                *reinterpret_cast<uint4 *>(q - q_skew + b) = *reinterpret_cast<const uint4 *>(mine + b);
+        // aligned words of q, each cut out of two staged ones
+        const int32_t q_skew = static_cast<int32_t>(reinterpret_cast<uintptr_t>(q) & 3u);
+        for (int32_t b = t * 4 - q_skew; b < cols; b += kTeam * 4) {
+            const int32_t at = b + skew;
+            if (b >= 0 && b + 4 <= cols) {
+                const uint32_t *words = reinterpret_cast<const uint32_t *>(mine) + (at >> 2);
+                *reinterpret_cast<uint32_t *>(q + b) = __funnelshift_r(words[0], words[1], 8u * (at & 3));
             } else {
-                for (int j = 0; j < 16; ++j)
-                    if (b + j >= q_skew && b + j < q_skew + cols) q[b + j - q_skew] = static_cast<int8_t>(mine[b + j]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (b + j >= 0 && b + j < cols) q[b + j] = static_cast<int8_t>(mine[at + j]);
             }
         }
     }
@@ -251,11 +265,12 @@ __global__ void __launch_bounds__(kLongThreads) quant_long_rows_kernel(const Qua
         // columns are counted in 64 bits here: a row may have more than 2^31
         const int64_t windows = (p.cols + skew + kVec - 1) / kVec;
         auto window = [&](int64_t i) {
-            // from a window's own start, so that the 32-bit arithmetic of load_window fits
-            const int64_t left = p.cols + skew - i * kVec;
-            const int32_t here = static_cast<int32_t>(left < kVec ? left : kVec);
-            return i == 0 ? load_window<kIn>(row, skew, here - skew, 0)
-                          : load_window<kIn>(row + (i * kVec - skew) * kElem, 0, here, 0);
+            // (a part window is read from its own start, so that 32 bits count its columns)
+            const int64_t c = i * kVec - skew;
+            const uint8_t *from = row + c * kElem;
+            if (c >= 0 && c + kVec <= p.cols) return __ldcs(reinterpret_cast<const uint4 *>(from));
+            if (c < 0) return part_window<kIn>(row, -skew, static_cast<int32_t>(p.cols < kVec ? p.cols : kVec));
+            return part_window<kIn>(from, 0, static_cast<int32_t>(p.cols - c));
         };
         uint32_t acc = 0;
 #pragma unroll 4

@@ -66,7 +66,7 @@ def rows64(x):
 
 
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16, torch.float32], ids=["f16", "bf16", "f32"])
-@pytest.mark.parametrize("rows,cols", [(1, 1), (1, 7), (3, 16), (5, 2048), (17, 1000), (300, 513), (2, 40000)])
+@pytest.mark.parametrize("rows,cols", [(1, 1), (1, 7), (3, 16), (5, 2048), (17, 1000), (300, 513), (2, 40000), (2, 70001), (3, 66000), (2000, 37), (1300, 200), (1301, 2049), (1500, 4097), (5, 16385), (3, 9000), (4, 32768), (2, 32770)])
 def test_quantise_rows(rows, cols, dtype):
     gen = torch.Generator(device="cuda").manual_seed(rows * 131 + cols)
     x = (torch.randn(rows, cols, generator=gen, device="cuda") * 3).to(dtype)
