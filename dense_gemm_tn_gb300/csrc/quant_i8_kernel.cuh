@@ -50,8 +50,13 @@ __device__ __forceinline__ float border_code(float x, float a, float n)
 constexpr float kNearBorder = 0x1p-15f;
 
 // Rows whose largest value is below 2^-100 are scaled by 2^100 (exactly, and
-// also out of the subnormals) so that 127 / amax stays finite.
-__device__ __forceinline__ float row_lift(float amax) { return amax < 0x1p-100f ? 0x1p100f : 1.0f; }
+// also out of the subnormals) so that 127 / amax stays finite, and those above
+// 2^100 by 2^-100 so that 254 x does (what that takes into the subnormals has
+// code 0 either way).
+__device__ __forceinline__ float row_lift(float amax)
+{
+    return amax < 0x1p-100f ? 0x1p100f : (amax > 0x1p100f ? 0x1p-100f : 1.0f);
+}
 
 // 1.5 * 2^23: added to a value of at most 2^22, it leaves the value rounded to
 // an integer (ties to even) in the low bits.
@@ -73,7 +78,7 @@ __device__ __forceinline__ uint2 window_codes(const uint4 &w, float lift, float 
         else
             x[i] = f16_bits_to_f32(words[i >> 1] >> (16 * (i & 1)) & 0xFFFFu);
     }
-    if (kIn != kInF16 && lift != 1.0f) {                 // (a half's amax is never that small)
+    if (kIn != kInF16 && lift != 1.0f) {                 // (a half is never that small or large)
 #pragma unroll
         for (int i = 0; i < kVec; ++i) x[i] *= lift;
     }

@@ -59,6 +59,160 @@ def test_i8_grouped(counts, M, K):
         assert_scaled(C[r], Bt[r].double() @ A[e].double().t(), sa[e][None, :], sb[r][:, None], K, torch.bfloat16)
 
 
+def grouped_sums(A, Bt, b):
+    return torch.cat([Bt[b[e]:b[e + 1]].double() @ A[e].double().t() for e in range(A.shape[0])])
+
+
+def test_extreme_codes_and_long_sums():
+    """Sums past 2^24: of equal products they are exact in FP32 anyway, of mixed ones
+    within the FP32 sum's bound."""
+    for N in (3, 600):                              # widened on the way, and widened first
+        for K in (1024, 16384):
+            A = torch.full((130, K), -128, dtype=torch.int8, device="cuda")
+            Bt = torch.full((N, K), -128, dtype=torch.int8, device="cuda")
+            one = torch.ones(130, device="cuda")
+            C = g.i8_tn(A, Bt, one * 2.0 ** -20, torch.ones(N, device="cuda"))
+            assert bool((C == K * 2.0 ** -6).all())
+            A, Bt = codes(130, K, seed=5).clamp_(min=100), codes(N, K, seed=6)
+            sa, sb = scales(130, seed=7) * 2.0 ** -6, scales(N, seed=8)
+            C = g.i8_tn(A, Bt, sa, sb, dtype=torch.bfloat16)
+            assert_scaled(C, Bt.double() @ A.double().t(), sa[None, :], sb[:, None], K, torch.bfloat16)
+
+
+@pytest.mark.parametrize("N", [5, 64, 600])
+def test_every_code_widens_exactly(N):
+    """A's rows hold all 256 values, Bt picks one term per row."""
+    K = 256
+    A = torch.arange(-128, 128, device="cuda").to(torch.int8).repeat(16, 1)
+    Bt = torch.zeros(N, K, dtype=torch.int8, device="cuda")
+    at = (torch.arange(N, device="cuda") * 37) % K
+    Bt[torch.arange(N, device="cuda"), at] = 1
+    C = g.i8_tn(A, Bt, torch.ones(16, device="cuda"), torch.ones(N, device="cuda"))
+    assert torch.equal(C, A[0, at].half()[:, None].expand(N, 16))
+    C = g.i8_tn(Bt, A, torch.ones(N, device="cuda"), torch.ones(16, device="cuda"))
+    assert torch.equal(C, A[0, at].half()[None, :].expand(16, N))
+
+
+@pytest.mark.parametrize("M,N,K,pad", [(200, 17, 144, 16), (200, 17, 144, 1), (130, 600, 48, 32), (65, 3, 33, 0)])
+def test_i8_strides(M, N, K, pad):
+    A, Bt = padded(codes(M, K, seed=1), K + pad, 99), padded(codes(N, K, seed=2), K + pad, -77)
+    sa, sb = scales(M, seed=3), scales(N, seed=4)
+    C = padded(torch.full((N, M), 5.5, dtype=torch.float16, device="cuda"), M + pad, 5.5)
+    g.i8_tn(A, Bt, sa, sb, C=C)
+    assert_scaled(C, Bt.double() @ A.double().t(), sa[None, :], sb[:, None], K, torch.float16)
+    assert bool((C.as_strided((N, M + pad), (M + pad, 1))[:, M:] == 5.5).all())
+
+
+def test_i8_rows_of_no_expert_and_bad_offsets():
+    M, K, T = 136, 80, 90
+    A, Bt, sa, sb = codes(3, M, K, seed=1), codes(T, K, seed=2), scales(3, M, seed=3), scales(T, seed=4)
+    for table in ([10, 30, 30, 80], [-4, 50, 20, 70], [0, 200, 0, 0]):
+        b, top = [], 0
+        for o in table:
+            top = max(top, min(max(o, 0), T))
+            b.append(top)
+        C = torch.full((T, M), 5.5, dtype=torch.bfloat16, device="cuda")
+        g.i8_tn_grouped(A, Bt, sa, sb, torch.tensor(table, dtype=torch.int32, device="cuda"), C=C)
+        rows = slice(b[0], b[3])
+        sa_rows = torch.cat([sa[e].expand(b[e + 1] - b[e], M) for e in range(3)])
+        assert_scaled(C[rows], grouped_sums(A, Bt, b), sa_rows, sb[rows][:, None], K, torch.bfloat16)
+        assert bool((C[:b[0]] == 5.5).all()) and bool((C[b[3]:] == 5.5).all())
+
+
+def test_i8_scales_of_zero_nan_and_infinity_stay_in_their_row_and_column():
+    M, N, K = 140, 70, 64
+    A, Bt, sa, sb = codes(M, K, seed=1), codes(N, K, seed=2), scales(M, seed=3), scales(N, seed=4)
+    clean = g.i8_tn(A, Bt, sa, sb)
+    sa[3], sa[130], sb[5], sb[69] = 0, float("nan"), float("nan"), 0
+    C = g.i8_tn(A, Bt, sa, sb)
+    assert bool(C[5].isnan().all()) and bool(C[:, 130].isnan().all())
+    keep_n, keep_m = torch.ones(N, dtype=torch.bool), torch.ones(M, dtype=torch.bool)
+    keep_n[[5, 69]] = False
+    keep_m[[3, 130]] = False
+    assert torch.equal(C[keep_n][:, keep_m], clean[keep_n][:, keep_m])
+    assert bool((C[69][keep_m] == 0).all()) and bool((C[keep_n, 3] == 0).all())
+
+
+def test_i8_empty_sums():
+    i8 = dict(dtype=torch.int8, device="cuda")
+    C = torch.full((5, 40), 9.0, dtype=torch.float16, device="cuda")
+    g.i8_tn(torch.zeros(40, 0, **i8), torch.zeros(5, 0, **i8), torch.ones(40, device="cuda"), torch.ones(5, device="cuda"), C=C)
+    assert bool((C == 0).all())
+
+
+def test_i8_captured_on_two_streams():
+    cases = [(codes(3, 200, 144, seed=i), codes(150, 144, seed=i + 1), scales(3, 200, seed=i + 2), scales(150, seed=i + 3),
+              offsets_of([100, 0, 50])) for i in (1, 20)]
+    wide = [(codes(96, 80, seed=i), codes(700, 80, seed=i + 1), scales(96, seed=i + 2), scales(700, seed=i + 3)) for i in (40, 60)]
+    run = [lambda c=c, w=w: (g.i8_tn_grouped(*c), g.i8_tn(*w)) for c, w in zip(cases, wide)]
+    want = [r() for r in run]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for r in run:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(r())
+        graphs.append(graph)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(20):
+        for graph, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                graph.replay()
+    torch.cuda.synchronize()
+    for out, w in zip(outs, want):
+        assert all(torch.equal(x, y) for x, y in zip(out, w))
+    g.gemm_poll_device_status()
+
+
+@pytest.mark.parametrize("mode", [1, 2])
+def test_i8_stalled_role_reports_a_timeout(mode):
+    args = codes(300, 1024, seed=1), codes(20, 1024, seed=2), scales(300, seed=3), scales(20, seed=4)
+    want = g.i8_tn(*args)
+    g.gemm_poll_device_status()
+    g.gemm_set_wait_limit_ns(20_000_000)
+    g.gemm_debug_inject_stall(mode)
+    try:
+        g.i8_tn(*args)
+        with pytest.raises(g.GemmError) as e:
+            g.gemm_poll_device_status()
+        assert e.value.status == g.GEMM_ERR_TIMEOUT
+    finally:
+        g.gemm_debug_inject_stall(0)
+        g.gemm_set_wait_limit_ns(0)
+    assert torch.equal(g.i8_tn(*args), want)
+    g.gemm_poll_device_status()
+
+
+def test_past_2_31_elements():
+    M, K, E = 4096, 4096, 130
+    A = torch.zeros(E, M, K, dtype=torch.int8, device="cuda")
+    A[E - 1] = codes(M, K, seed=1)
+    Bt, sa, sb = codes(40, K, seed=2), torch.zeros(E, M, device="cuda"), scales(40, seed=3)
+    sa[E - 1] = scales(M, seed=4)
+    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    off[E] = 40
+    C = g.i8_tn_grouped(A, Bt, sa, sb, off)
+    assert_scaled(C, Bt.double() @ A[E - 1].double().t(), sa[E - 1][None, :], sb[:, None], K, torch.float16)
+
+
+def test_quantised_layer_together():
+    """Weights by channel and tokens by row to 8 bits, then the product: near the
+    unquantised one by the two quantisations' half steps."""
+    T, M, K = 37, 300, 512
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    x, w = (torch.randn(*s, generator=gen, device="cuda").bfloat16() for s in ((T, K), (M, K)))
+    qx, sx = g.quantize_i8_rows(x)
+    qw, sw = g.quantize_i8_rows(w)
+    y = g.i8_tn(qw, qx, sw, sx, dtype=torch.bfloat16)
+    g.gemm_poll_device_status()
+    # |x - q s| <= s / 2 for either operand
+    x64, w64 = x.double(), w.double()
+    bound = (sx.double()[:, None] / 2 * w64.abs().sum(1) + x64.abs().sum(1, keepdim=True) * sw.double() / 2
+             + K * sx.double()[:, None] * sw.double() / 4)
+    ref = x64 @ w64.t()
+    assert bool(((y.double() - ref).abs() <= bound * 1.001 + (ref.abs() + bound) * 2.0 ** -8).all())
+
+
 def rows64(x):
     top = x.double().abs().amax(1, keepdim=True) if x.shape[1] else torch.zeros(x.shape[0], 1, device=x.device).double()
     q = torch.where(top > 0, (x.double() * 127 / top).round(), torch.zeros_like(x.double()))
@@ -75,3 +229,84 @@ def test_quantise_rows(rows, cols, dtype):
     want, scale = rows64(x)
     assert torch.equal(q.double(), want)
     assert torch.equal(s, scale.float())
+
+
+def exact_codes(row):
+    """round(127 x / amax), ties to even, in rational arithmetic."""
+    from fractions import Fraction
+    x = [Fraction(float(v)) for v in row]
+    top = max(abs(v) for v in x)
+    return [round(127 * v / top) if top else 0 for v in x]        # (Fraction rounds ties to even)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16, torch.float32], ids=["f16", "bf16", "f32"])
+def test_quantise_borders_and_ties(dtype):
+    """Values on and either side of every border of two codes, for row maxima with odd
+    and even mantissas."""
+    rows = []
+    for top in (1.0, 127.0, 254.0, 1.5, 3.1415, 0.8203125, 100.375):
+        top = float(torch.tensor(top, dtype=dtype))
+        row = torch.tensor([(n + 0.5) * top / 127 for n in range(127)], dtype=torch.float64).to(dtype)
+        up = torch.nextafter(row.float(), torch.full_like(row.float(), 1e9)) if dtype == torch.float32 else (row.view(torch.int16) + 1).view(dtype)
+        down = torch.nextafter(row.float(), torch.zeros_like(row.float())) if dtype == torch.float32 else (row.view(torch.int16) - 1).view(dtype)
+        rows.append(torch.cat([torch.tensor([top], dtype=dtype), row, -row, up.to(dtype), -down.to(dtype), down.to(dtype)]).clamp(-top, top))
+    x = torch.stack(rows)
+    q, s = g.quantize_i8_rows(x.cuda())
+    for r in range(x.shape[0]):
+        assert q[r].cpu().tolist() == exact_codes(x[r].double().tolist()), r
+    assert torch.equal(s.cpu(), (x.double().abs().amax(1) / 127).float())
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16, torch.float32], ids=["f16", "bf16", "f32"])
+@pytest.mark.parametrize("cols", [5, 64, 100, 2049, 9000])
+def test_quantise_extreme_rows(cols, dtype):
+    info = torch.finfo(dtype)
+    gen = torch.Generator(device="cuda").manual_seed(cols)
+    base = torch.rand(6, cols, generator=gen, device="cuda", dtype=torch.float64) * 2 - 1
+    tiny = info.smallest_normal
+    x = torch.stack([base[0] * info.max, base[1] * tiny * 0.9, base[2] * tiny * 300, base[3] * 0, base[4], base[5] * info.max]).to(dtype)
+    x[3] = -0.0
+    x[4, -1] = float("nan")
+    x[5, cols // 2] = float("-inf")
+    q, s = g.quantize_i8_rows(x)
+    want, scale = rows64(x[:4])
+    assert torch.equal(q[:4].double(), want)
+    assert torch.equal(s[:4], scale.float())
+    assert bool(s[4:].isnan().all()) and bool((q[4:] == 0).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16, torch.float32], ids=["f16", "bf16", "f32"])
+@pytest.mark.parametrize("rows,cols,ld,base", [(4, 100, 104, 0), (4, 100, 103, 0), (7, 33, 40, 1), (3, 1, 9, 3), (1400, 50, 57, 5),
+                                               (9, 2100, 2107, 2), (3, 17000, 17001, 1), (2, 50001, 50003, 3)])
+def test_quantise_strides_and_bases(rows, cols, ld, base, dtype):
+    gen = torch.Generator(device="cuda").manual_seed(rows + cols)
+    room = torch.randn(base + rows * ld, generator=gen, device="cuda").mul_(50).to(dtype)
+    x = room[base:].as_strided((rows, cols), (ld, 1))
+    for q_base, q_ld in ((0, cols), (0, cols + 5), (3, cols + 8), (8, cols // 16 * 16 + 16)):
+        out = torch.full((q_base + rows * q_ld + 16,), 55, dtype=torch.int8, device="cuda")
+        scale = torch.zeros(rows, device="cuda")
+        g.gemm_quantize_i8_rows(x, {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}[dtype], rows, cols, ld,
+                                out.data_ptr() + q_base, q_ld, scale)
+        q = out[q_base:].as_strided((rows, cols), (q_ld, 1))
+        want, s = rows64(x)
+        assert torch.equal(q.double(), want) and torch.equal(scale, s.float())
+        q.fill_(55)
+        assert bool((out == 55).all())               # nothing beside the codes was written
+
+
+def test_quantise_empty_and_dependent_launches():
+    q, s = g.quantize_i8_rows(torch.zeros(5, 0, device="cuda"))
+    assert q.shape == (5, 0) and bool((s == 0).all())
+    q, s = g.quantize_i8_rows(torch.zeros(0, 7, device="cuda"))
+    assert q.shape == (0, 7) and s.shape == (0,)
+    x = torch.zeros(40, 300, device="cuda", dtype=torch.bfloat16)
+    src = torch.randn(40, 300, device="cuda").bfloat16()
+    w, sw = codes(64, 300, seed=1), scales(64, seed=2)
+    want_q, want_s = g.quantize_i8_rows(src)
+    want = g.i8_tn(w, want_q, sw, want_s)
+    for _ in range(30):
+        x.zero_()
+        x.copy_(src)
+        q, s = g.quantize_i8_rows(x)
+        assert torch.equal(g.i8_tn(w, q, sw, s), want)
+    assert torch.equal(q, want_q)
