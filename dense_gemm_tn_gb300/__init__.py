@@ -557,6 +557,13 @@ def _workspace(device, stream, n):
         return torch.empty(n, dtype=torch.uint8, device=device)
 
 
+def _tensors(*operands):
+    import torch
+    for t in operands:
+        if not isinstance(t, torch.Tensor):
+            raise ValueError(f"the operands must be torch tensors, not {type(t).__name__}")
+
+
 def _plain(index, *tensors):
     """Whether the tensors are contiguous on device `index`, the current one: their
     strides are their shapes', and nothing is left to check but types and shapes."""
@@ -579,6 +586,7 @@ def tn_grouped(A, Bt, offsets, C=None, stream=None):
     A, Bt and C (T, M) are all fp16 or all bf16, their rows contiguous.  Rows of
     no expert are not written."""
     import torch
+    _tensors(A, Bt, offsets)
     dtype, device = A.dtype, A.device
     kind = _half_type(dtype, "A")
     if (C is None and Bt.dtype is dtype and offsets.dtype is torch.int32 and A.dim() == 3 and Bt.dim() == 2
@@ -611,16 +619,25 @@ def tn_grouped_grad_b(A, dCt, offsets, dBt=None, stream=None):
     """The gradient of tn_grouped for Bt: dBt[t] = A[e]^T dC^T[t], with dCt (T, M)
     -> (T, K).  Rows of no expert are not written."""
     import torch
-    lda, stride_a = _experts(A, A.dtype, "A")
-    kind, device = _half_type(A.dtype, "A"), A.device
-    E, M, K = A.shape
-    ldd, T = _tokens(dCt, A.dtype, M, "dCt"), dCt.shape[0]
-    _vector(offsets, torch.int32, E + 1, "offsets")
-    _same_device(device, dCt=dCt, offsets=offsets)
-    if _elsewhere(device.index):
-        with torch.cuda.device(device):
-            return tn_grouped_grad_b(A, dCt, offsets, dBt, stream)
-    dBt, ldb = _output(dBt, K, T, A.dtype, device)
+    _tensors(A, dCt, offsets)
+    dtype, device = A.dtype, A.device
+    kind = _half_type(dtype, "A")
+    if (dBt is None and dCt.dtype is dtype and offsets.dtype is torch.int32 and A.dim() == 3 and dCt.dim() == 2
+            and offsets.dim() == 1 and _plain(device.index, A, dCt, offsets)
+            and A.shape[1] == dCt.shape[1] > 0 < A.shape[2] and offsets.shape[0] == A.shape[0] + 1):
+        (E, M, K), T = A.shape, dCt.shape[0]
+        lda, stride_a, ldd = K, M * K, M
+        dBt, ldb = torch.empty((T, K), dtype=dtype, device=device), K
+    else:
+        lda, stride_a = _experts(A, dtype, "A")
+        E, M, K = A.shape
+        ldd, T = _tokens(dCt, dtype, M, "dCt"), dCt.shape[0]
+        _vector(offsets, torch.int32, E + 1, "offsets")
+        _same_device(device, dCt=dCt, offsets=offsets)
+        if _elsewhere(device.index):
+            with torch.cuda.device(device):
+                return tn_grouped_grad_b(A, dCt, offsets, dBt, stream)
+        dBt, ldb = _output(dBt, K, T, dtype, device)
     a, d = A.data_ptr(), dCt.data_ptr()
     n = calls.gemm_grouped_workspace(GEMM_GROUPED_GRAD_B, E, M, K, T, a, lda, stride_a, d, ldd)
     held = _workspace(device, stream, n) if n > 0 else None
@@ -635,9 +652,10 @@ def tn_grouped_grad_a(dCt, Bt, offsets, dA=None, stream=None):
     products dC^T[t] Bt[t], with dCt (T, M) and Bt (T, K) -> (E, M, K); zeros for
     an expert without rows."""
     import torch
-    if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.shape[0] < 1:
+    _tensors(dCt, Bt, offsets)
+    if offsets.dim() != 1 or offsets.shape[0] < 1:
         raise ValueError("offsets must be a 1-D tensor of experts + 1 row numbers")
-    if not isinstance(dCt, torch.Tensor) or dCt.dim() != 2 or not isinstance(Bt, torch.Tensor) or Bt.dim() != 2:
+    if dCt.dim() != 2 or Bt.dim() != 2:
         raise ValueError("dCt and Bt must be 2-D torch tensors")
     E, device, (T, M), K = offsets.shape[0] - 1, dCt.device, dCt.shape, Bt.shape[1]
     kind = _half_type(dCt.dtype, "dCt")
@@ -667,6 +685,7 @@ def i8_tn(A, Bt, scale_a, scale_b, C=None, dtype=None, stream=None):
     (N, K) int8, scale_a (M,) and scale_b (N,) fp32 -> (N, M) of `dtype`
     (torch.float16, unless C or dtype says torch.bfloat16)."""
     import torch
+    _tensors(A, Bt, scale_a, scale_b)
     dtype, device = dtype or (torch.float16 if C is None else C.dtype), A.device
     kind = _half_type(dtype, "dtype")
     if (C is None and A.dtype is torch.int8 is Bt.dtype and scale_a.dtype is torch.float32 is scale_b.dtype
@@ -693,9 +712,8 @@ def i8_tn(A, Bt, scale_a, scale_b, C=None, dtype=None, stream=None):
     return C
 
 
-def i8_tn_grouped(A, Bt, scale_a, scale_b, offsets, C=None, dtype=None, stream=None):
-    """i8_tn grouped by expert as in tn_grouped: A (E, M, K) and Bt (T, K) int8,
-    scale_a (E, M) and scale_b (T,) fp32 -> (T, M) of `dtype`."""
+def _i8_grouped_operands(A, Bt, scale_a, scale_b, offsets, C, dtype):
+    """(lda, stride_a, ldb, ldc, C) of i8_tn_grouped's operands, all checked."""
     import torch
     lda, stride_a = _experts(A, torch.int8, "A")
     E, M, K = A.shape
@@ -705,13 +723,32 @@ def i8_tn_grouped(A, Bt, scale_a, scale_b, offsets, C=None, dtype=None, stream=N
         raise ValueError(f"scale_a must be a contiguous torch.float32 tensor of shape {(E, M)}")
     _vector(scale_b, torch.float32, T, "scale_b")
     _vector(offsets, torch.int32, E + 1, "offsets")
+    _same_device(A.device, Bt=Bt, scale_a=scale_a, scale_b=scale_b, offsets=offsets)
+    C, ldc = _output(C, M, T, dtype, A.device)
+    return lda, stride_a, ldb, ldc, C
+
+
+def i8_tn_grouped(A, Bt, scale_a, scale_b, offsets, C=None, dtype=None, stream=None):
+    """i8_tn grouped by expert as in tn_grouped: A (E, M, K) and Bt (T, K) int8,
+    scale_a (E, M) and scale_b (T,) fp32 -> (T, M) of `dtype`."""
+    import torch
+    _tensors(A, Bt, scale_a, scale_b, offsets)
     dtype, device = dtype or (torch.float16 if C is None else C.dtype), A.device
     kind = _half_type(dtype, "dtype")
-    _same_device(device, Bt=Bt, scale_a=scale_a, scale_b=scale_b, offsets=offsets)
-    if _elsewhere(device.index):
-        with torch.cuda.device(device):
-            return i8_tn_grouped(A, Bt, scale_a, scale_b, offsets, C, dtype, stream)
-    C, ldc = _output(C, M, T, dtype, device)
+    if (C is None and A.dtype is torch.int8 is Bt.dtype and scale_a.dtype is torch.float32 is scale_b.dtype
+            and offsets.dtype is torch.int32 and A.dim() == 3 and Bt.dim() == 2 and offsets.dim() == 1
+            and _plain(device.index, A, Bt, scale_a, scale_b, offsets) and A.shape[2] == Bt.shape[1] > 0 < A.shape[1]
+            and scale_a.shape == A.shape[:2] and scale_b.shape == Bt.shape[:1] and offsets.shape[0] == A.shape[0] + 1):
+        (E, M, K), T = A.shape, Bt.shape[0]
+        lda = ldb = K
+        stride_a = M * K
+        C, ldc = torch.empty((T, M), dtype=dtype, device=device), M
+    else:
+        lda, stride_a, ldb, ldc, C = _i8_grouped_operands(A, Bt, scale_a, scale_b, offsets, C, dtype)
+        (E, M, K), T = A.shape, Bt.shape[0]
+        if _elsewhere(device.index):
+            with torch.cuda.device(device):
+                return i8_tn_grouped(A, Bt, scale_a, scale_b, offsets, C, dtype, stream)
     a, b = A.data_ptr(), Bt.data_ptr()
     n = calls.gemm_grouped_workspace(GEMM_GROUPED_I8, E, M, K, T, a, lda, stride_a, b, ldb)
     held = _workspace(device, stream, n) if n > 0 else None

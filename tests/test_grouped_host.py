@@ -147,6 +147,10 @@ def test_helpers_refuse_shapes_types_and_places():
         g.tn_grouped_grad_b(A, Bt, off)
     with pytest.raises(ValueError, match="Bt"):
         g.tn_grouped_grad_a(torch.zeros(5, 16, **f16), Bt, off)
+    for call in (lambda: g.tn_grouped([1], Bt, off), lambda: g.tn_grouped_grad_b(A, None, off),
+                 lambda: g.tn_grouped_grad_a(Bt, Bt, [0, 4]), lambda: g.i8_tn(1, Bt, off, off), lambda: g.quantize_i8_rows(3)):
+        with pytest.raises(ValueError):
+            call()
     i8 = dict(dtype=torch.int8)
     with pytest.raises(ValueError, match="CUDA"):
         g.i8_tn(torch.zeros(16, 8, **i8), torch.zeros(4, 8, **i8), torch.zeros(16), torch.zeros(4))
