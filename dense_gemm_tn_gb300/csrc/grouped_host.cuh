@@ -25,13 +25,14 @@ struct GroupedCall {
     bool needs_offsets = false;
 };
 
-// Rows per expert up to which the 8-bit product widens its operands on the way
-// to the tensor core (tn_i8_kernel) instead of first.
-constexpr int64_t kI8DirectRows = 512;
+// Rows per expert up to which the 8-bit product widens both operands on the way
+// to the tensor core, on single CTAs (tn_i8_kernel); with more, the tokens are
+// widened first and CTA pairs widen the weights (tn_i8_pair_kernel).
+constexpr int64_t kI8DirectRows = 128;
 
 // An operand as `blocks` matrices of rows x inner elements, and whether it is
-// copied first: the 8-bit ones for many rows per expert (widened to f16), and
-// all of them when
+// copied first: 8-bit tokens for many rows per expert (widened to f16), and all
+// operands when
 // the TMA cannot address them in place -- base, row stride or block stride not
 // a multiple of 16 bytes, or the sum's index contiguous and its extent not one
 // (a row that ends inside a 16-byte unit is not clipped element by element) --
@@ -97,9 +98,8 @@ GroupedPlan grouped_plan(int op, int64_t E, int64_t M, int64_t K, int64_t T, con
         const bool grad_b = op == GEMM_GROUPED_GRAD_B;
         g.x = grouped_operand(X, M, E, K, ldx, stride_x, !grad_b, i8);
         g.y = grouped_operand(Y, T, 1, grad_b ? M : K, ldy, 0, true, i8);
-        const bool widen = i8 && (T > kI8DirectRows * E || g.x.copy || g.y.copy);     // both or neither
-        grouped_copy(g.x, widen || g.x.copy);
-        grouped_copy(g.y, widen || g.y.copy);
+        grouped_copy(g.x, g.x.copy);
+        grouped_copy(g.y, g.y.copy || (i8 && (T > kI8DirectRows * E || g.x.copy)));
     }
     return g;
 }
@@ -237,6 +237,73 @@ gemm_status_t launch_i8(const GroupedCall &c, DeviceState &dev, tn::GroupedParam
     t_rec.cluster = 1;
     t_rec.grid = grid;
     t_rec.slots = dev.sms;
+    t_rec.tiles = static_cast<int>(tiles);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, prm);
+    if (e != cudaSuccess) return fail(GEMM_ERR_CUDA, "%s: launch: %s", c.name, cudaGetErrorString(e));
+    return GEMM_OK;
+}
+
+// tokens: the widened copy, ld elements a row.
+gemm_status_t launch_i8_pair(const GroupedCall &c, DeviceState &dev, tn::GroupedParams &prm, const void *tokens,
+                             int64_t ld)
+{
+    gemm_status_t st;
+    const uint64_t apart = c.E > 1 ? uint64_t(c.stride_x) : uint64_t(16);
+    if (prm.red > 0) {
+        if ((st = encode_map(&prm.tmap_l, CU_TENSOR_MAP_DATA_TYPE_UINT8, c.X, c.K, c.M, c.ldx, c.E, apart, tn::kI8Block,
+                             128, "A")) != GEMM_OK)
+            return st;
+        for (uint32_t i = 0; i < tn::kIpRowsR / 16; ++i)
+            if ((st = encode_2d(&prm.tmap_r[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, tokens, ld, c.T, ld * 2, tn::kGrBlock,
+                                16 * (i + 1), "rows")) != GEMM_OK)
+                return st;
+    }
+    auto kernel = tn::tn_i8_pair_kernel;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.blockDim = dim3(tn::kI8Threads, 1, 1);
+    cfg.dynamicSmemBytes = tn::kIpSmemBytes;
+    int slots;
+    {
+        std::lock_guard<std::mutex> lock(g_mutex);
+        int &n = dev.i8_pair_slots;
+        if (n == 0) {
+            cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, tn::kIpSmemBytes);
+            if (e != cudaSuccess) return fail(GEMM_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+            int found = 0;
+            cfg.attrs = attr + 1;
+            cfg.numAttrs = 1;
+            cfg.gridDim = dim3(2 * (dev.sms / 2), 1, 1);
+            e = cudaOccupancyMaxActiveClusters(&found, kernel, &cfg);
+            if (e != cudaSuccess || found <= 0) {
+                cudaGetLastError();
+                found = dev.sms / 2;
+            }
+            n = found;
+        }
+        slots = n;
+    }
+    const int64_t l_tiles = (c.M + 255) / 256;
+    const int64_t r_tiles = c.T / tn::kIpRows + (c.E < c.T ? c.E : c.T);       // an upper bound
+    if (r_tiles > (int64_t(1) << 30) / l_tiles) return fail(GEMM_ERR_UNSUPPORTED, "%s: too many output tiles", c.name);
+    const int64_t tiles = r_tiles * l_tiles;
+    const int grid = 2 * static_cast<int>(tiles < slots ? tiles : slots);
+    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+    cfg.stream = c.stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    t_rec = LaunchRecord{};
+    t_rec.name = c.name;
+    t_rec.grouped = 1;
+    t_rec.cluster = 2;
+    t_rec.grid = grid;
+    t_rec.slots = slots;
     t_rec.tiles = static_cast<int>(tiles);
     cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, prm);
     if (e != cudaSuccess) return fail(GEMM_ERR_CUDA, "%s: launch: %s", c.name, cudaGetErrorString(e));
@@ -404,6 +471,8 @@ gemm_status_t run_grouped(const GroupedCall &c)
     prm.wait_limit_ns = g_wait_limit_ns.load();
     if (i8 && !copied)
         st = launch_i8(c, *dev, prm);
+    else if (i8 && copied == 2)
+        st = launch_i8_pair(c, *dev, prm, y, ldy);
     else if (grad_a)
         st = launch_grouped_op<tn::kGrGradA>(c, *dev, prm, x, y, ldx, stride_x, ldy, in_x, in_y);
     else if (grad_b)

@@ -45,16 +45,29 @@ constexpr int kI8SmemBytes = 1024 /* alignment slack */ + kI8Stages8 * kI8Stage8
                              kI8EpiWarps * kGrStageBytes + kI8Barriers * 8 + 32 + 2 * (kGrMaxExperts + 8) * 4;
 static_assert(kI8SmemBytes <= 232448, "exceeds the 227 KiB shared memory of one CTA");
 
-// Four 8-bit terms to f16, in the order 0, 2, 1, 3: what bounds the widening is
-// the integer pipe, and a mask is cheaper than byte permutations.  L's and R's
-// are widened alike, so each product still pairs a term with its own.
-__device__ __forceinline__ uint2 widen_word(uint32_t w)
+// A lane's row of L, 128 8-bit terms of a swizzled tile, to its TMEM lane's 64
+// columns at t_a; v: its first four 16-byte pieces, loaded before.
+__device__ __forceinline__ void widen_row_to_tmem(uint32_t row_addr, int lane, uint4 (&v)[4], uint32_t t_a)
 {
-    // x ^ 0x80 = x + 128 in the low bits of 1024's mantissa is 1152 + x
-    uint32_t a, b;
-    asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(a) : "r"(w), "r"(0x00FF00FFu), "r"(0x64806480u));
-    asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(b) : "r"(w >> 8), "r"(0x00FF00FFu), "r"(0x64806480u));
-    return make_uint2(f16x2_minus_1152(a), f16x2_minus_1152(b));
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        uint32_t f[32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const uint32_t words[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const uint2 x = i8x4_to_f16x4(words[q]);
+                f[8 * c + 2 * q] = x.x;
+                f[8 * c + 2 * q + 1] = x.y;
+            }
+        }
+        if (half == 0) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) v[c] = ptx::ld_shared_v4(row_addr + (((4 + c) ^ (lane & 7)) << 4));
+        }
+        ptx::tmem_st_32x32b_x32(t_a + 32 * half, f);
+    }
 }
 
 // A lane's part of widening eight rows (r0 .. r0 + 7) of a swizzled 8-bit tile
@@ -76,7 +89,7 @@ struct WidenRows {
     }
     __device__ __forceinline__ void store(uint32_t dst, int i, const uint4 &w) const
     {
-        const uint2 a = widen_word(w.x), b = widen_word(w.y), d = widen_word(w.z), e = widen_word(w.w);
+        const uint2 a = i8x4_to_f16x4(w.x), b = i8x4_to_f16x4(w.y), d = i8x4_to_f16x4(w.z), e = i8x4_to_f16x4(w.w);
         ptx::st_shared_v4(dst + st[i], a.x, a.y, b.x, b.y);
         ptx::st_shared_v4(dst + (st[i] ^ 16u), d.x, d.y, e.x, e.y);
     }
@@ -215,7 +228,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) tn_i8_kernel(const __grid_const
 #pragma unroll
                         for (int j = 0; j < kGrBlock / 16; ++j)
                             if (left > half * kGrBlock + 16 * j)
-                                ptx::mma_f16_ts(d_tmem, a_tmem + 8 * j, desc_r + 2u * j, idesc,
+                                ptx::mma_f16_ts<1>(d_tmem, a_tmem + 8 * j, desc_r + 2u * j, idesc,
                                                 (i | half | j) != 0 ? 1u : 0u);
                     }
                     ptx::mma_commit<1>(empty16_bar(stage));
@@ -317,25 +330,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) tn_i8_kernel(const __grid_const
                 ok = wait_warp(w, empty16_bar(team), phase16 ^ 1u, kSiteEmpty);
                 if (!ok) break;
                 ptx::tc_fence_after_sync();                   // the MMAs that read this stage are done
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t f[32];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const uint32_t words[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const uint2 x = widen_word(words[q]);
-                            f[8 * c + 2 * q] = x.x;
-                            f[8 * c + 2 * q + 1] = x.y;
-                        }
-                    }
-                    if (half == 0) {
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) v[c] = ptx::ld_shared_v4(src + row_l + (((4 + c) ^ (lane & 7)) << 4));
-                    }
-                    ptx::tmem_st_32x32b_x32(t_a + half * (kI8ACols / 2), f);
-                }
+                widen_row_to_tmem(src + row_l, lane, v, t_a);
 #pragma unroll
                 for (int g = 0; g < kOwnR; ++g)
                     if (mine + g * kI8TeamWarps < groups_r) {
@@ -367,6 +362,331 @@ __global__ void __launch_bounds__(kI8Threads, 1) tn_i8_kernel(const __grid_const
         __syncwarp();
         ptx::tc_fence_after_sync();
         ptx::tmem_dealloc<1>(tmem_base, kI8TmemCols);
+    }
+}
+
+// ------------------------------------------------------------------ many rows
+// tn_i8_pair_kernel: the same product on CTA pairs, for many rows per expert.
+// The weights are again widened on the way, each CTA's 128 rows into its own
+// tensor memory; the tokens come widened to f16 (widen_rows_kernel; T x K, where
+// widening the weights as well would move five bytes for each of them first).
+//
+// Tiles of 256 (L) x up to 192 (R) rows: two accumulators of 192 columns and two
+// stages of widened weights of 64 fill the 512 TMEM columns.  A stage is 128
+// terms: 16 KiB of 8-bit weights, which the CTA's own barrier announces to its
+// widening warps, and two swizzled blocks of its half of the tokens, announced to
+// the even CTA's issuing warp.  The widening warps of both CTAs arrive on the
+// even CTA's barrier of the TMEM stage.
+constexpr int kIpRows = 192, kIpRowsR = kIpRows / 2;         // per tile, per CTA
+constexpr int kIpLBytes = 128 * 128;
+constexpr int kIpAtomBytes = kIpRowsR * 128;                 // 64 terms of a CTA's tokens
+constexpr int kIpStageBytes = kIpLBytes + 2 * kIpAtomBytes;
+constexpr int kIpStages = 4;                                 // (an even number: a team's stages are every other one)
+constexpr uint32_t kIpACol0 = 2 * kIpRows;
+constexpr uint32_t kIpTmemCols = 512;
+static_assert(kIpACol0 + 2 * kI8ACols == kIpTmemCols, "the TMEM columns are all used");
+static_assert(kIpAtomBytes % 1024 == 0, "blocks start on the swizzle's 1024 bytes");
+// full8[S], fullr[S], empty[S], fulla[2], emptya[2], accfull[2], accempty[2], drain, never
+constexpr int kIpBarriers = 3 * kIpStages + 10;
+constexpr int kIpSmemBytes = 1024 /* alignment slack */ + kIpStages * kIpStageBytes + kI8EpiWarps * kGrStageBytes +
+                             kIpBarriers * 8 + 32 + kIpStages * 4 + 2 * (kGrMaxExperts + 8) * 4;
+static_assert(kIpSmemBytes <= 232448, "exceeds the 227 KiB shared memory of one CTA");
+
+__global__ void __launch_bounds__(kI8Threads, 1) tn_i8_pair_kernel(const __grid_constant__ GroupedParams p)
+{
+    constexpr int kS = kIpStages;
+
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t s_ring = ptx::smem_addr(smem), s_staging = s_ring + kS * kIpStageBytes;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kS * kIpStageBytes + kI8EpiWarps * kGrStageBytes);
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + kIpBarriers);
+    volatile uint32_t *abort_flag = tmem_holder + 1;
+    volatile uint32_t *issued_count = tmem_holder + 2;    // fills this CTA's producer issued
+    volatile uint32_t *producer_done = tmem_holder + 3;   // set once this CTA's producer issues no more
+    volatile uint32_t *fill_bytes = tmem_holder + 8;      // [kS]: this CTA's token bytes of the stage's last fill
+    int32_t *start = reinterpret_cast<int32_t *>(tmem_holder + 8 + kS);
+    int32_t *before = start + kGrMaxExperts + 8;
+    const uint32_t abort_addr = ptx::smem_addr(const_cast<uint32_t *>(abort_flag));
+    const uint32_t count_addr = ptx::smem_addr(const_cast<uint32_t *>(issued_count));
+    const uint32_t done_addr = ptx::smem_addr(const_cast<uint32_t *>(producer_done));
+    const uint32_t fill_addr = ptx::smem_addr(const_cast<uint32_t *>(fill_bytes));
+    const uint32_t bar0 = ptx::smem_addr(bars);
+    auto full8_bar = [&](int s) { return bar0 + 8u * s; };
+    auto fullr_bar = [&](int s) { return bar0 + 8u * (kS + s); };
+    auto empty_bar = [&](int s) { return bar0 + 8u * (2 * kS + s); };
+    auto fulla_bar = [&](int t) { return bar0 + 8u * (3 * kS + t); };
+    auto emptya_bar = [&](int t) { return bar0 + 8u * (3 * kS + 2 + t); };
+    auto accfull_bar = [&](int b) { return bar0 + 8u * (3 * kS + 4 + b); };
+    auto accempty_bar = [&](int b) { return bar0 + 8u * (3 * kS + 6 + b); };
+    const uint32_t drain_bar = bar0 + 8u * (3 * kS + 8);
+    const uint32_t never_bar = bar0 + 8u * (3 * kS + 9);   // nothing ever arrives (test stalls)
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t pos = ptx::cluster_ctarank();
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kS; ++s) {
+            ptx::mbar_init(full8_bar(s), 1);
+            ptx::mbar_init(fullr_bar(s), 1);
+            ptx::mbar_init(empty_bar(s), kI8TeamWarps + 1);      // the weights are read, and the tokens
+            fill_bytes[s] = 0u;
+        }
+        for (int b = 0; b < 2; ++b) {
+            ptx::mbar_init(fulla_bar(b), 2 * kI8TeamWarps);
+            ptx::mbar_init(emptya_bar(b), 1);
+            ptx::mbar_init(accfull_bar(b), 1);
+            ptx::mbar_init(accempty_bar(b), 2 * kI8EpiWarps);
+        }
+        ptx::mbar_init(drain_bar, 1);
+        ptx::mbar_init(never_bar, 1);
+        *abort_flag = 0u;
+        *issued_count = 0u;
+        *producer_done = 0u;
+        ptx::fence_mbar_init();
+        ptx::fence_proxy_async_smem();
+    }
+    if (threadIdx.x == 32 && p.red > 0) {
+        ptx::prefetch_tensormap(&p.tmap_l);
+        ptx::prefetch_tensormap(&p.tmap_r[kIpRowsR / 16 - 1]);
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc<2>(ptx::smem_addr(tmem_holder), kIpTmemCols);
+        ptx::tmem_relinquish_alloc_permit<2>();
+    }
+    ptx::tc_fence_before_sync();
+    ptx::cluster_sync();
+    ptx::tc_fence_after_sync();
+    const uint32_t tmem_base = *tmem_holder;
+    const Waiter w{abort_flag, abort_addr, pos, 2u, p.wait_limit_ns};
+
+    ptx::griddep_wait();                      // every thread's first global access is behind this wait
+    const int32_t l_tiles = (p.l_extent + 255) / 256;
+    grouped_tables<kGrI8, kIpRows, kI8Threads>(p, l_tiles, start, before);
+    const int32_t total = before[p.E];
+    const int32_t slot = static_cast<int32_t>(blockIdx.x) / 2, slots = static_cast<int32_t>(gridDim.x) / 2;
+    GroupedWalk<kGrI8, kIpRows, kIpRows, 256, 32> walk{start, before, l_tiles, 0, p.red, 0};
+    const int32_t blocks = (p.red + kI8Block - 1) / kI8Block;       // stages of a tile
+
+    if (warp == 0) {
+        // ------------------------------------------------ TMA producer (both CTAs)
+        int stage = 0;
+        uint32_t phase = 0, n_issued = 0;
+        bool ok = true;
+        if (p.flags & (pos == 0 ? kFlagStallProducer0 : kFlagStallProducer1)) ok = wait_warp(w, never_bar, 0u, kSiteStall);
+        for (int32_t u = slot; ok && u < total; u += slots) {
+            const GroupedTile t = walk.at(u);
+            const int32_t cols = t.n_mma[0] / 2;                 // this CTA's tokens
+            const CUtensorMap *map_r = p.tmap_r + cols / 16 - 1;
+            const int32_t l0 = t.l0 + static_cast<int32_t>(pos) * 128;
+            const int32_t r0 = start[t.e] + t.r0 + static_cast<int32_t>(pos) * cols;
+            for (int32_t i = 0; i < blocks; ++i) {
+                if (!wait_warp(w, empty_bar(stage), phase ^ 1u, kSiteEmpty)) {
+                    ok = false;
+                    break;
+                }
+                ++n_issued;
+                if (ptx::elect_one()) {
+                    const uint32_t s_l = s_ring + stage * kIpStageBytes, s_r = s_l + kIpLBytes;
+                    const uint32_t bar_r = ptx::mapa_shared(fullr_bar(stage), 0);
+                    const uint32_t bytes = 2u * cols * 128u;
+                    fill_bytes[stage] = bytes;
+                    ptx::mbar_arrive_expect_tx(full8_bar(stage), kIpLBytes);
+                    tma_load_3d(s_l, &p.tmap_l, full8_bar(stage), i * kI8Block, l0, t.e);
+                    if (pos == 0) ptx::mbar_arrive_expect_tx(fullr_bar(stage), 2 * bytes);
+                    ptx::tma_load_2d_pair(s_r, map_r, bar_r, i * kI8Block, r0);
+                    ptx::tma_load_2d_pair(s_r + kIpAtomBytes, map_r, bar_r, i * kI8Block + kGrBlock, r0);
+                    *issued_count = n_issued;
+                }
+                __syncwarp();
+                if (++stage == kS) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+        if (lane == 0) ptx::griddep_launch_dependents();
+        if (ptx::elect_one()) {
+            auto fills = [](uint32_t n, int s) { return n / kS + (static_cast<uint32_t>(s) < n % kS ? 1u : 0u); };
+            // this CTA's weights: every issued load lands before the CTA can exit
+            for (int s = 0; s < kS; ++s)
+                if (const uint32_t passes = fills(n_issued, s)) w.drain(full8_bar(s), (passes - 1) & 1u);
+            ptx::st_release_cluster_u32(ptx::mapa_shared(done_addr, pos), 1u);
+            if (pos == 0) {
+                // the pair's tokens, as in tn_grouped_kernel
+                uint32_t peer = n_issued;
+                const uint64_t t0 = ptx::globaltimer();
+                bool stopped = true;
+                while (ptx::ld_acquire_cluster_u32(ptx::mapa_shared(done_addr, 1)) == 0u) {
+                    if (ptx::globaltimer() - t0 > w.limit) {
+                        atomicCAS(&g_tn_status, 0, 4 | (kSitePeerDone << 8));
+                        stopped = false;
+                        break;
+                    }
+                }
+                if (stopped) peer = ptx::ld_relaxed_cluster_u32(ptx::mapa_shared(count_addr, 1));
+                for (int s = 0; s < kS; ++s) {
+                    const uint32_t mine = fills(n_issued, s), theirs = fills(peer, s);
+                    const uint32_t last = mine > theirs ? mine : theirs;
+                    if (last == 0) continue;
+                    if (mine > theirs + 1 || theirs > mine + 1) {      // cannot happen; never guess
+                        atomicCAS(&g_tn_status, 0, 4 | (kSiteReconcile << 8));
+                        continue;
+                    }
+                    if (mine > theirs)
+                        ptx::mbar_complete_tx(fullr_bar(s), fill_bytes[s]);
+                    else if (theirs > mine)
+                        ptx::mbar_arrive_expect_tx(fullr_bar(s),
+                                                   ptx::ld_relaxed_cluster_u32(ptx::mapa_shared(fill_addr + 4u * s, 1)));
+                    w.drain(fullr_bar(s), (last - 1) & 1u);
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (pos == 0) {
+            // ------------------------------------------------ MMA issuer (even CTA)
+            int stage = 0;
+            uint32_t phase = 0, sub = 0, n = 0;               // n: stages so far
+            bool ok = true, issued_any = false;
+            if (p.flags & kFlagStallMma) ok = wait_warp(w, never_bar, 0u, kSiteStall);
+            for (int32_t u = slot; ok && p.red > 0 && u < total; u += slots, ++sub) {
+                const GroupedTile t = walk.at(u);
+                const uint32_t idesc = ptx::idesc_f32acc(256, static_cast<uint32_t>(t.n_mma[0]), 0u, 0u);
+                const uint32_t d_tmem = tmem_base + (sub & 1u) * kIpRows;
+                if (!wait_warp(w, accempty_bar(sub & 1u), ((sub >> 1) & 1u) ^ 1u, kSiteAccEmpty)) break;
+                for (int32_t i = 0; i < blocks; ++i, ++n) {
+                    const uint32_t team = n & 1u;
+                    if (!wait_warp(w, fullr_bar(stage), phase, kSiteLoaded) ||
+                        !wait_warp(w, fulla_bar(team), (n >> 1) & 1u, kSiteLoaded)) {
+                        ok = false;
+                        break;
+                    }
+                    ptx::tc_fence_after_sync();
+                    const int32_t left = p.red - i * kI8Block;
+                    if (ptx::elect_one()) {
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            const uint64_t desc_r = ptx::desc_kmajor_sw128(s_ring + stage * kIpStageBytes + kIpLBytes +
+                                                                           half * kIpAtomBytes);
+                            const uint32_t a_tmem = tmem_base + kIpACol0 + team * kI8ACols + half * (kI8ACols / 2);
+#pragma unroll
+                            for (int j = 0; j < kGrBlock / 16; ++j)
+                                if (left > half * kGrBlock + 16 * j)
+                                    ptx::mma_f16_ts<2>(d_tmem, a_tmem + 8 * j, desc_r + 2u * j, idesc,
+                                                       (i | half | j) != 0 ? 1u : 0u);
+                        }
+                        ptx::mma_commit<2>(emptya_bar(team), 3);
+                        ptx::mma_commit<2>(empty_bar(stage), 3);
+                        if (i + 1 == blocks) ptx::mma_commit<2>(accfull_bar(sub & 1u), 3);
+                    }
+                    __syncwarp();
+                    issued_any = true;
+                    if (++stage == kS) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            if (issued_any && ptx::elect_one()) {             // every MMA issued completes before TMEM is freed
+                ptx::mma_commit<2>(drain_bar, 1);
+                w.drain(drain_bar, 0u);
+            }
+        }
+    } else if (warp < 2 + kI8EpiWarps) {
+        // ------------------------------------------------ epilogue (warps 2..5, both CTAs)
+        const int quarter = warp & 3;
+        GroupedStore store;
+        store.init(s_staging + (warp - 2) * kGrStageBytes, lane);
+        store.ld = p.out_ld;
+        uint32_t sub = 0;
+        for (int32_t u = slot; u < total; u += slots) {
+            const GroupedTile t = walk.at(u);
+            const int32_t l0 = t.l0 + static_cast<int32_t>(pos) * 128 + 32 * quarter;
+            const int64_t row0 = static_cast<int64_t>(start[t.e]) + t.r0;
+            uint16_t *out = p.out + row0 * p.out_ld + l0;
+            store.wide = p.l_extent - l0 < 32 ? p.l_extent - l0 : 32;
+            store.vec = p.out_vec != 0 && store.wide == 32;
+            if (p.red == 0) {                     // an empty sum
+                if (lane < store.wide)
+                    for (int32_t r = 0; r < t.rows; ++r) out[r * p.out_ld + lane] = 0;
+                continue;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                store.scale_l[i] = 8 * i + (lane >> 2) < store.wide
+                                       ? __ldg(p.scale_l + static_cast<int64_t>(t.e) * p.l_extent + l0 + 8 * i + (lane >> 2))
+                                       : 0.0f;
+            if (!wait_warp(w, accfull_bar(sub & 1u), (sub >> 1) & 1u, kSiteAccFull)) break;
+            ptx::tc_fence_after_sync();
+            const uint32_t t_row = tmem_base + (static_cast<uint32_t>(32 * quarter) << 16) + (sub & 1u) * kIpRows;
+            for (int32_t c = 0; c < t.n_mma[0]; c += kGrChunk) {
+                uint32_t v[2][16];
+                ptx::tmem_ld_16x256b_x4(t_row + c, v[0]);
+                ptx::tmem_ld_16x256b_x4(t_row + (16u << 16) + c, v[1]);
+                ptx::tmem_ld_wait_all();
+                ptx::reg_dependency(v[0]);
+                ptx::reg_dependency(v[1]);
+                if (c + kGrChunk >= t.n_mma[0]) {
+                    ptx::tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive_remote(ptx::mapa_shared(accempty_bar(sub & 1u), 0));
+                }
+                if (p.out_fmt != 0)
+                    store.step<true, true>(v, out + c * p.out_ld, t.rows - c, p.scale_r + row0 + c);
+                else
+                    store.step<false, true>(v, out + c * p.out_ld, t.rows - c, p.scale_r + row0 + c);
+            }
+            ++sub;
+        }
+    } else {
+        // ------------------------------------------------ widening (warps 6..13, both CTAs)
+        const int team = (warp - 2 - kI8EpiWarps) / kI8TeamWarps;
+        static_assert(kS % 2 == 0, "a team's stages are every other one");
+        const int quarter = warp & 3;
+        const uint32_t row_l = static_cast<uint32_t>(32 * quarter + lane) * 128u;
+        const uint32_t t_a = tmem_base + (static_cast<uint32_t>(32 * quarter) << 16) + kIpACol0 + team * kI8ACols;
+        const uint32_t fulla = ptx::mapa_shared(fulla_bar(team), 0);
+        bool ok = true;
+        int stage = team;
+        uint32_t phase = 0, phase_a = 0, n = 0;               // n: stages so far
+        for (int32_t u = slot; ok && p.red > 0 && u < total; u += slots) {
+            for (int32_t i = 0; i < blocks; ++i, ++n) {
+                if ((n & 1u) != static_cast<uint32_t>(team)) continue;
+                ok = wait_warp(w, full8_bar(stage), phase, kSiteLoaded);
+                if (!ok) break;
+                const uint32_t src = s_ring + stage * kIpStageBytes + row_l;
+                uint4 v[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) v[c] = ptx::ld_shared_v4(src + ((c ^ (lane & 7)) << 4));
+                ok = wait_warp(w, emptya_bar(team), phase_a ^ 1u, kSiteEmpty);
+                if (!ok) break;
+                ptx::tc_fence_after_sync();                   // the MMAs that read this TMEM stage are done
+                widen_row_to_tmem(src, lane, v, t_a);
+                ptx::tmem_st_wait();
+                ptx::tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    ptx::mbar_arrive_remote(fulla);
+                    ptx::mbar_arrive(empty_bar(stage));
+                }
+                phase_a ^= 1u;
+                stage += 2;
+                if (stage >= kS) {
+                    stage -= kS;
+                    phase ^= 1u;
+                }
+            }
+        }
+    }
+
+    __syncwarp();                // .aligned barriers below need converged warps
+    ptx::tc_fence_before_sync();
+    ptx::cluster_sync();         // no CTA leaves while the other may still touch its shared memory
+    if (warp == 1) {
+        __syncwarp();
+        ptx::tc_fence_after_sync();
+        ptx::tmem_dealloc<2>(tmem_base, kIpTmemCols);
     }
 }
 

@@ -98,6 +98,7 @@ struct DeviceState {
     bool skinny_attr[2] = {};         // tn_skinny_kernel's shared-memory attribute set, by kind
     int grouped_slots[4][3] = {};     // co-resident tn_grouped_kernel CTAs or pairs, by operation and variant (0 = not queried)
     bool i8_attr = false;             // tn_i8_kernel's shared-memory attribute set
+    int i8_pair_slots = 0;            // co-resident pairs of tn_i8_pair_kernel (0 = not queried)
     // One lock per stream, held by a call from its first buffer lookup through
     // its last launch: a call is several launches (row copy, GEMM, reduce),
     // and two host threads' calls on one stream must not interleave them.
@@ -666,6 +667,7 @@ gemm_status_t launch(const char *name, tn::KernelParams &prm, DeviceState &dev, 
     }
     t_rec.name = name;
     t_rec.quant = false;
+    t_rec.grouped = 0;
     t_rec.lean = lean;
     t_rec.skinny = 0;
     t_rec.G = G;
@@ -1050,6 +1052,7 @@ gemm_status_t launch_quant(DeviceState &dev, qz::QuantParams &prm, cudaStream_t 
     if (st != GEMM_OK) return st;
     prm.slots = reinterpret_cast<float *>(slots + zeroed);
     t_rec.name = "gemm_quantize_e4m3";
+    t_rec.grouped = 0;
     t_rec.quant = true;
     t_rec.qgrid = grid;
     t_rec.qunits = prm.num_units;

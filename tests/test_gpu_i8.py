@@ -36,7 +36,8 @@ def assert_scaled(got, sums, sa, sb, terms, dtype):
 @pytest.mark.parametrize("dtype", TYPES, ids=["f16", "bf16"])
 @pytest.mark.parametrize("M,N,K", [(1, 1, 1), (8, 1, 16), (128, 16, 128), (257, 3, 80), (64, 65, 63), (130, 300, 1000),
                                    (512, 64, 2048), (1000, 513, 333), (33, 100, 5), (300, 17, 144), (129, 128, 400),
-                                   (2000, 100, 1040), (128, 129, 256), (40, 1, 4096), (640, 112, 16), (20000, 33, 128)])
+                                   (2000, 100, 1040), (128, 129, 256), (40, 1, 4096), (640, 112, 16), (20000, 33, 128),
+                                   (256, 257, 128), (300, 300, 144), (1000, 700, 400), (512, 1025, 2064), (77, 5000, 64), (8, 600, 16)])
 def test_i8_product(M, N, K, dtype):
     A, Bt, sa, sb = codes(M, K, seed=1), codes(N, K, seed=2), scales(M, seed=3), scales(N, seed=4)
     C = g.i8_tn(A, Bt, sa, sb, dtype=dtype)
@@ -46,7 +47,8 @@ def test_i8_product(M, N, K, dtype):
 
 
 @pytest.mark.parametrize("counts,M,K", [([1], 16, 16), ([0, 3, 0, 1], 128, 64), ([70, 0, 300], 200, 208), ([5, 6], 31, 33),
-                                        ([1] * 40, 384, 272), ([64, 0, 65, 3], 130, 128), ([200, 10, 100], 136, 112)])
+                                        ([1] * 40, 384, 272), ([64, 0, 65, 3], 130, 128), ([200, 10, 100], 136, 112),
+                                        ([300, 0, 600], 264, 272), ([193, 192, 1000, 2], 520, 1040)])
 def test_i8_grouped(counts, M, K):
     E, T = len(counts), sum(counts)
     off = offsets_of(counts)
@@ -164,9 +166,10 @@ def test_i8_captured_on_two_streams():
     g.gemm_poll_device_status()
 
 
-@pytest.mark.parametrize("mode", [1, 2])
-def test_i8_stalled_role_reports_a_timeout(mode):
-    args = codes(300, 1024, seed=1), codes(20, 1024, seed=2), scales(300, seed=3), scales(20, seed=4)
+@pytest.mark.parametrize("N,mode", [(20, 1), (20, 2), (700, 1), (700, 2), (700, 3)])
+def test_i8_stalled_role_reports_a_timeout(N, mode):
+    """20 rows: single CTAs; 700: CTA pairs (mode 3: the odd CTA's producer)."""
+    args = codes(600, 2048, seed=1), codes(N, 2048, seed=2), scales(600, seed=3), scales(N, seed=4)
     want = g.i8_tn(*args)
     g.gemm_poll_device_status()
     g.gemm_set_wait_limit_ns(20_000_000)
