@@ -113,14 +113,27 @@ int64_t grouped_workspace(int op, int64_t E, int64_t M, int64_t K, int64_t T, co
     return static_cast<int64_t>(grouped_plan(op, E, M, K, T, X, ldx, stride_x, Y, ldy).bytes());
 }
 
+// Copies the operands that the plan says into the workspace, in one launch.
 template <typename Src>
-gemm_status_t launch_widen(const char *name, DeviceState &dev, const GroupedOperand &o, uint16_t *dst,
+gemm_status_t launch_widen(const char *name, DeviceState &dev, const GroupedPlan &plan, void *x, void *y,
                            cudaStream_t stream)
 {
-    const tn::WidenJob<Src> j{static_cast<const Src *>(o.base), o.ld,       o.stride, dst, o.copy_ld, o.rows,
-                              o.rows * o.blocks,                o.inner};
-    int64_t blocks = (j.rows * (j.ld_dst / 8) + tn::kWidenThreads - 1) / tn::kWidenThreads;
-    if (blocks > int64_t(dev.sms) * 64) blocks = int64_t(dev.sms) * 64;
+    constexpr int64_t kElems = 16 / sizeof(Src);
+    auto job = [](const GroupedOperand &o, void *dst) {
+        tn::WidenJob<Src> j{static_cast<const Src *>(o.base), o.ld, o.stride, static_cast<uint16_t *>(dst), o.copy_ld, o.rows,
+                            o.copy ? o.rows * o.blocks : 0, o.inner, 0, 1, 0, nullptr};
+        const int64_t units = o.copy_ld / kElems;
+        if (o.copy)
+            j.end = reinterpret_cast<const char *>(j.src + (o.blocks - 1) * o.stride + (o.rows - 1) * o.ld + o.inner);
+        while (j.shift < 5 && (int64_t(1) << j.shift) < units) ++j.shift;
+        j.segs = (units + tn::kWidenSeg - 1) / tn::kWidenSeg;
+        j.work = ((j.rows + (int64_t(32) >> j.shift) - 1) >> (5 - j.shift)) * j.segs;
+        return j;
+    };
+    const tn::WidenJob<Src> jx = job(plan.x, x), jy = job(plan.y, y);
+    const int64_t warps = jx.work + jy.work, per = tn::kWidenThreads / 32;
+    int64_t blocks = (warps + per - 1) / per;
+    if (blocks > int64_t(dev.sms) * 32) blocks = int64_t(dev.sms) * 32;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -130,7 +143,7 @@ gemm_status_t launch_widen(const char *name, DeviceState &dev, const GroupedOper
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, tn::widen_rows_kernel<Src>, j);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, tn::widen_rows_kernel<Src>, jx, jy);
     if (e != cudaSuccess) return fail(GEMM_ERR_CUDA, "%s: launch (operand copy): %s", name, cudaGetErrorString(e));
     return GEMM_OK;
 }
@@ -432,23 +445,23 @@ gemm_status_t run_grouped(const GroupedCall &c)
     const void *x = c.X, *y = c.Y;
     int64_t ldx = c.ldx, stride_x = c.stride_x, ldy = c.ldy, in_x = inner_x, in_y = inner_y;
     int copied = 0;
-    auto copy = [&](const GroupedOperand &o) {
-        uint16_t *dst = reinterpret_cast<uint16_t *>(ws);
-        ws += o.copy_bytes;
-        return i8 ? launch_widen<int8_t>(name, *dev, o, dst, c.stream) : launch_widen<uint16_t>(name, *dev, o, dst, c.stream);
-    };
     if (plan.x.copy) {
         x = ws;
-        if ((st = copy(plan.x)) != GEMM_OK) return st;
+        ws += plan.x.copy_bytes;
         ldx = in_x = plan.x.copy_ld;
         stride_x = plan.x.rows * ldx;
         copied |= 1;
     }
     if (plan.y.copy) {
         y = ws;
-        if ((st = copy(plan.y)) != GEMM_OK) return st;
+        ws += plan.y.copy_bytes;
         ldy = in_y = plan.y.copy_ld;
         copied |= 2;
+    }
+    if (copied) {
+        st = i8 ? launch_widen<int8_t>(name, *dev, plan, const_cast<void *>(x), const_cast<void *>(y), c.stream)
+                : launch_widen<uint16_t>(name, *dev, plan, const_cast<void *>(x), const_cast<void *>(y), c.stream);
+        if (st != GEMM_OK) return st;
     }
     tn::GroupedParams prm;
     memset(&prm, 0, sizeof(prm));

@@ -33,6 +33,7 @@
 // issues the MMAs, warps 2-9 read the accumulator and store.
 #pragma once
 
+#include "repack_kernel.cuh"
 #include "tn_gemm_kernel.cuh"
 
 namespace tn {
@@ -266,6 +267,7 @@ __device__ __forceinline__ void grouped_tables(const GroupedParams &p, int32_t l
 // neither side meets a bank twice.  One warp runs this with little to overlap,
 // so what counts is instructions: about 60 a step.
 struct GroupedStore {
+    uint32_t base;            // the warp's staging rows
     uint32_t st0, ld0;        // this lane's first staging addresses (others are fixed offsets from them)
     int lane;
     int32_t wide;             // of this warp's 32 lanes, those inside the result
@@ -275,6 +277,7 @@ struct GroupedStore {
 
     __device__ __forceinline__ void init(uint32_t s_mine, int lane_)
     {
+        base = s_mine;
         lane = lane_;
         auto piece = [&](int row, int c) {        // address of 16-byte piece c (0 .. 3) of a staging row
             return s_mine + (row >> 1) * 128 + (((((row & 1) << 2) | c) ^ ((row >> 1) & 3)) << 4);
@@ -318,26 +321,28 @@ struct GroupedStore {
                 ptx::stmatrix_x4_trans((st0 ^ (32u * q)) + 512u * i, h[q][i][0], h[q][i][1], h[q][i + 1][0],
                                        h[q][i + 1][1]);
         __syncwarp();
-        uint16_t *dst = out + (lane >> 2) * ld + 8 * (lane & 3);
-        if (vec && rows >= kGrChunk) {
-            uint4 x[4];
+        if (vec) {
+            uint16_t *dst = out + (lane >> 2) * ld + 8 * (lane & 3);
+            if (rows >= kGrChunk) {
+                uint4 x[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) x[q] = ptx::ld_shared_v4(ld0 + 512u * q);
+                for (int q = 0; q < 4; ++q) x[q] = ptx::ld_shared_v4(ld0 + 512u * q);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4 *>(dst + 8 * q * ld) = x[q];
-        } else {
+                for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4 *>(dst + 8 * q * ld) = x[q];
+            } else {
 #pragma unroll 1
-            for (int q = 0; q < 4; ++q, dst += 8 * ld) {
-                if (8 * q + (lane >> 2) >= rows) continue;
-                const uint4 x = ptx::ld_shared_v4(ld0 + 512u * q);
-                if (vec) {
-                    *reinterpret_cast<uint4 *>(dst) = x;
-                } else {
-                    const uint32_t words[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                    for (int b = 0; b < 8; ++b)
-                        if (8 * (lane & 3) + b < wide) dst[b] = static_cast<uint16_t>(words[b >> 1] >> (16 * (b & 1)));
-                }
+                for (int q = 0; 8 * q + (lane >> 2) < rows; ++q, dst += 8 * ld)
+                    *reinterpret_cast<uint4 *>(dst) = ptx::ld_shared_v4(ld0 + 512u * q);
+            }
+        } else if (lane < wide) {
+            // rows that are not aligned, or end inside this warp's 32: an element a lane,
+            // so that a warp's store is one stretch of a row
+            uint16_t *dst = out + lane;
+            const int32_t n = rows < kGrChunk ? rows : kGrChunk;
+#pragma unroll 8
+            for (int32_t r = 0; r < n; ++r) {
+                dst[r * ld] = ptx::ld_shared_u16(base + (r >> 1) * 128 +
+                                                 (((((r & 1) << 2) | (lane >> 3)) ^ ((r >> 1) & 3)) << 4) + 2 * (lane & 7));
             }
         }
     }
@@ -884,6 +889,9 @@ struct WidenJob {
     uint16_t *dst;
     int64_t ld_dst;      // a multiple of 64
     int64_t rows_per, rows, cols;
+    int32_t shift;       // 1 << shift lanes of a warp to a row
+    int64_t segs, work;  // segments (kWidenSeg units) of a row; warps' shares in all
+    const char *end;     // one past the last row's last element
 };
 
 // Four 8-bit integers to four halves, exactly.
@@ -907,45 +915,98 @@ __device__ __forceinline__ uint2 i8x4_to_f16x4(uint32_t w)
 }
 
 constexpr int kWidenThreads = 256;
+constexpr int kWidenSeg = 256;                   // units (16 source bytes) of a warp's share of a row at most
 
-// One thread per 8 elements (16 bytes) of the copy.
+// Both operands in one launch (either may have no rows).  A warp's share is up to
+// 256 units of one row, or several short rows side by side; what is worked out
+// for a row is worked out once for all of them.  A row starts wherever its
+// elements do, so a unit is cut out of two aligned 16-byte loads, and what it
+// took along past the row's end is masked.  Units whose loads would leave the
+// operand (its first and last ones) are gathered element by element: none reads
+// a byte before its first or after its last element.
 template <typename Src>
-__global__ void __launch_bounds__(kWidenThreads) widen_rows_kernel(const WidenJob<Src> j)
+__global__ void __launch_bounds__(kWidenThreads, 5) widen_rows_kernel(const __grid_constant__ WidenJob<Src> j0,
+                                                                      const __grid_constant__ WidenJob<Src> j1)
 {
+    constexpr int kElems = 16 / sizeof(Src);     // of a unit
     ptx::griddep_wait();
-    const int64_t chunks = j.ld_dst / 8, total = j.rows * chunks;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * kWidenThreads;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kWidenThreads + threadIdx.x; i < total; i += step) {
-        const int64_t r = i / chunks, c = (i - r * chunks) * 8;
-        const int64_t e = r / j.rows_per;
-        const Src *src = j.src + e * j.stride + (r - e * j.rows_per) * j.ld + c;
-        uint4 o = make_uint4(0, 0, 0, 0);
-        if (c + 8 <= j.cols && reinterpret_cast<uintptr_t>(src) % (8 * sizeof(Src)) == 0) {
-            if constexpr (sizeof(Src) == 1) {
-                const uint2 w = __ldg(reinterpret_cast<const uint2 *>(src));
-                const uint2 lo = i8x4_to_f16x4(w.x), hi = i8x4_to_f16x4(w.y);
-                o = make_uint4(lo.x, lo.y, hi.x, hi.y);
-            } else {
-                o = __ldg(reinterpret_cast<const uint4 *>(src));
-            }
-        } else {
-            union {
-                Src v[8];
-                uint2 w;
-                uint4 u;
-            } in;
-            in.u = make_uint4(0, 0, 0, 0);
+    const int lane = threadIdx.x & 31;
+    const int64_t work = j0.work + j1.work, step = static_cast<int64_t>(gridDim.x) * (kWidenThreads / 32);
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * (kWidenThreads / 32) + (threadIdx.x >> 5); i < work; i += step) {
+        const WidenJob<Src> &j = i < j0.work ? j0 : j1;
+        const int64_t n = i < j0.work ? i : i - j0.work;
+        int64_t first = n, seg = 0;              // the warp's first row (shift 5: the row), its segment
+        if (j.segs > 1) {
+            first = j.work <= 0xFFFFFFFFll ? static_cast<uint32_t>(n) / static_cast<uint32_t>(j.segs) : n / j.segs;
+            seg = n - first * j.segs;
+        }
+        const int64_t r = (first << (5 - j.shift)) + (lane >> j.shift);
+        if (r >= j.rows) continue;
+        int64_t e = 0;
+        if (j.rows != j.rows_per)                // several blocks
+            e = j.rows <= 0xFFFFFFFFll ? static_cast<uint32_t>(r) / static_cast<uint32_t>(j.rows_per) : r / j.rows_per;
+        const int64_t u0 = seg * kWidenSeg;      // the share's first unit of its row(s)
+        const Src *src = j.src + e * j.stride + (r - e * j.rows_per) * j.ld + u0 * kElems;
+        uint16_t *dst = j.dst + r * j.ld_dst + u0 * kElems;
+        // within the share 32 bits count elements and units
+        const int64_t left = j.cols - u0 * kElems, room = j.ld_dst / kElems - u0;
+        const int32_t cols = static_cast<int32_t>(left < kWidenSeg * kElems ? (left > 0 ? left : 0) : kWidenSeg * kElems);
+        const int32_t units = static_cast<int32_t>(room < kWidenSeg ? room : kWidenSeg);
+        const int32_t s = static_cast<int32_t>(reinterpret_cast<uintptr_t>(src) & 15u);
+        const uint4 *aligned = reinterpret_cast<const uint4 *>(reinterpret_cast<const char *>(src) - s);
+        const int32_t bytes = cols * static_cast<int32_t>(sizeof(Src)), lanes = 1 << j.shift;
+        const uint32_t sh = 8u * (s & 3);
+        // units whose aligned loads stay inside the operand: from lo on, below hi
+        const char *begin = reinterpret_cast<const char *>(j.src);
+        const int32_t lo = reinterpret_cast<const char *>(aligned) < begin ? 1 : 0;
+        const int64_t whole = (j.end - reinterpret_cast<const char *>(aligned)) / 16 - (s == 0 ? 0 : 1);
+        const int32_t hi = static_cast<int32_t>(whole < units ? whole : units);
+#pragma unroll 2
+        for (int32_t c = lane & (lanes - 1); c < units; c += lanes) {
+            const int32_t valid = bytes - 16 * c;            // of this unit's bytes
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (valid > 0 && c >= lo && c < hi) {
+                x = __ldg(aligned + c);
+                if (s != 0) {
+                    const uint4 y = __ldg(aligned + c + 1);
+                    const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+                    switch (s >> 2) {
+                    case 0: x = window16<0>(w, sh); break;
+                    case 1: x = window16<1>(w, sh); break;
+                    case 2: x = window16<2>(w, sh); break;
+                    default: x = window16<3>(w, sh); break;
+                    }
+                }
+                if (valid < 16) {
+                    auto keep = [valid](int32_t first) {     // mask of the word from byte `first` on
+                        const int32_t n = valid - first;
+                        return n >= 4 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << (8 * n)) - 1u;
+                    };
+                    x.x &= keep(0);
+                    x.y &= keep(4);
+                    x.z &= keep(8);
+                    x.w &= keep(12);
+                }
+            } else if (valid > 0) {
+                union {
+                    Src v[kElems];
+                    uint4 u4;
+                } part;
+                part.u4 = x;
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
-                if (c + q < j.cols) in.v[q] = src[q];
+                for (int q = 0; q < kElems; ++q)
+                    if (c * kElems + q < cols) part.v[q] = src[c * kElems + q];
+                x = part.u4;
+            }
+            uint4 *to = reinterpret_cast<uint4 *>(dst + c * kElems);
             if constexpr (sizeof(Src) == 1) {
-                const uint2 lo = i8x4_to_f16x4(in.w.x), hi = i8x4_to_f16x4(in.w.y);
-                o = make_uint4(lo.x, lo.y, hi.x, hi.y);
+                const uint2 a = i8x4_to_f16x4(x.x), b = i8x4_to_f16x4(x.y), d = i8x4_to_f16x4(x.z), f = i8x4_to_f16x4(x.w);
+                to[0] = make_uint4(a.x, a.y, b.x, b.y);
+                to[1] = make_uint4(d.x, d.y, f.x, f.y);
             } else {
-                o = in.u;
+                to[0] = x;
             }
         }
-        reinterpret_cast<uint4 *>(j.dst + r * j.ld_dst)[c / 8] = o;
     }
 }
 
