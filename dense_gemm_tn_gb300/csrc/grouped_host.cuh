@@ -116,12 +116,12 @@ int64_t grouped_workspace(int op, int64_t E, int64_t M, int64_t K, int64_t T, co
 // Copies the operands that the plan says into the workspace, in one launch.
 template <typename Src>
 gemm_status_t launch_widen(const char *name, DeviceState &dev, const GroupedPlan &plan, void *x, void *y,
-                           cudaStream_t stream)
+                           const int32_t *offsets, cudaStream_t stream)
 {
     constexpr int64_t kElems = 16 / sizeof(Src);
     auto job = [](const GroupedOperand &o, void *dst) {
         tn::WidenJob<Src> j{static_cast<const Src *>(o.base), o.ld, o.stride, static_cast<uint16_t *>(dst), o.copy_ld, o.rows,
-                            o.copy ? o.rows * o.blocks : 0, o.inner, 0, 1, 0, nullptr};
+                            o.copy ? o.rows * o.blocks : 0, o.inner, 0, 1, 0, nullptr, nullptr};
         const int64_t units = o.copy_ld / kElems;
         if (o.copy)
             j.end = reinterpret_cast<const char *>(j.src + (o.blocks - 1) * o.stride + (o.rows - 1) * o.ld + o.inner);
@@ -130,7 +130,9 @@ gemm_status_t launch_widen(const char *name, DeviceState &dev, const GroupedPlan
         j.work = ((j.rows + (int64_t(32) >> j.shift) - 1) >> (5 - j.shift)) * j.segs;
         return j;
     };
-    const tn::WidenJob<Src> jx = job(plan.x, x), jy = job(plan.y, y);
+    tn::WidenJob<Src> jx = job(plan.x, x);
+    const tn::WidenJob<Src> jy = job(plan.y, y);
+    jx.offsets = offsets;
     const int64_t warps = jx.work + jy.work, per = tn::kWidenThreads / 32;
     int64_t blocks = (warps + per - 1) / per;
     if (blocks > int64_t(dev.sms) * 32) blocks = int64_t(dev.sms) * 32;
@@ -459,8 +461,9 @@ gemm_status_t run_grouped(const GroupedCall &c)
         copied |= 2;
     }
     if (copied) {
-        st = i8 ? launch_widen<int8_t>(name, *dev, plan, const_cast<void *>(x), const_cast<void *>(y), c.stream)
-                : launch_widen<uint16_t>(name, *dev, plan, const_cast<void *>(x), const_cast<void *>(y), c.stream);
+        const int32_t *per_expert = grad_a || dense ? nullptr : c.offsets;     // x is the experts' weights
+        st = i8 ? launch_widen<int8_t>(name, *dev, plan, const_cast<void *>(x), const_cast<void *>(y), per_expert, c.stream)
+                : launch_widen<uint16_t>(name, *dev, plan, const_cast<void *>(x), const_cast<void *>(y), per_expert, c.stream);
         if (st != GEMM_OK) return st;
     }
     tn::GroupedParams prm;

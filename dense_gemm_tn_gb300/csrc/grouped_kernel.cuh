@@ -892,6 +892,7 @@ struct WidenJob {
     int32_t shift;       // 1 << shift lanes of a warp to a row
     int64_t segs, work;  // segments (kWidenSeg units) of a row; warps' shares in all
     const char *end;     // one past the last row's last element
+    const int32_t *offsets;   // blocks are the experts' and only those with rows are read; or NULL
 };
 
 // Four 8-bit integers to four halves, exactly.
@@ -945,6 +946,10 @@ __global__ void __launch_bounds__(kWidenThreads, 5) widen_rows_kernel(const __gr
         int64_t e = 0;
         if (j.rows != j.rows_per)                // several blocks
             e = j.rows <= 0xFFFFFFFFll ? static_cast<uint32_t>(r) / static_cast<uint32_t>(j.rows_per) : r / j.rows_per;
+        // Rows of expert e run from the largest offset up to its own to the next one,
+        // if that is larger: it has none where the next is not above its own.
+        // Nothing reads that part of the copy.
+        if (j.offsets && max(j.offsets[e + 1], 0) <= max(j.offsets[e], 0)) continue;
         const int64_t u0 = seg * kWidenSeg;      // the share's first unit of its row(s)
         const Src *src = j.src + e * j.stride + (r - e * j.rows_per) * j.ld + u0 * kElems;
         uint16_t *dst = j.dst + r * j.ld_dst + u0 * kElems;

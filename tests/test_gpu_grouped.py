@@ -195,6 +195,32 @@ def test_offsets_out_of_order_or_range_stay_inside(table):
     assert torch.equal(dA, grad_a64(dCt, Bt, b).to(dtype))
 
 
+@pytest.mark.parametrize("table", [[0, 0, 30, 30, 10, 64, 64], [-5, -9, 20, 90, 80, 70, 64], [64, 3, 50, 63, 64, 65, 9],
+                                   [0, 30, 10, 20, 31, 31, 64]])
+@pytest.mark.parametrize("M,K", [(65, 63), (300, 137)])
+def test_copied_weights_of_experts_without_rows(table, M, K):
+    """Weights that have to be copied are so for experts with rows alone: the others' may
+    hold anything, and no expert with rows is left out whatever the order of the offsets."""
+    dtype, T, E = torch.bfloat16, 64, 6
+    off = torch.tensor(table, dtype=torch.int32, device="cuda")
+    b, top = [], 0
+    for o in table:
+        top = max(top, min(max(o, 0), T))
+        b.append(top)
+    A, Bt, dCt = (small_ints(*s, seed=i, dtype=dtype) for i, s in enumerate([(E, M, K), (T, K), (T, M)], 1))
+    for e in range(E):
+        if b[e] == b[e + 1]:
+            A[e] = float("nan")
+    junk = torch.full((1 << 22,), float("nan"), device="cuda")           # what the workspace may be made of
+    del junk
+    C, dB = (torch.full((T, n), 3.5, dtype=dtype, device="cuda") for n in (M, K))
+    g.tn_grouped(A, Bt, off, C=C)
+    g.tn_grouped_grad_b(A, dCt, off, dBt=dB)
+    g.gemm_poll_device_status()
+    for got, ref in ((C, product64(A, Bt, b)), (dB, grad_b64(A, dCt, b))):
+        assert torch.equal(got, torch.where(ref.isnan(), torch.full_like(ref, 3.5), ref).to(dtype))
+
+
 def test_empty_sums_and_sizes():
     off = offsets_of([3, 0, 5])
     f16 = dict(dtype=torch.float16, device="cuda")
