@@ -31,17 +31,17 @@ struct GroupedCall {
 constexpr int64_t kI8DirectRows = 128;
 
 // An operand as `blocks` matrices of rows x inner elements, and whether it is
-// copied first: 8-bit tokens for many rows per expert (widened to f16), and all
-// operands when
-// the TMA cannot address them in place -- base, row stride or block stride not
-// a multiple of 16 bytes, or the sum's index contiguous and its extent not one
-// (a row that ends inside a 16-byte unit is not clipped element by element) --
-// or when the blocks interleave or repeat (a block stride below a row's).
+// copied first: when the TMA cannot address it in place -- base, row stride or
+// block stride not a multiple of 16 bytes, or the sum's index contiguous and its
+// extent not one (a row that ends inside a 16-byte unit is not clipped element by
+// element) -- or when the blocks interleave or repeat (a block stride below a
+// row's); and 8-bit tokens for many rows per expert, to be widened to f16.
 struct GroupedOperand {
     const void *base;
     int64_t rows, blocks, inner, ld, stride;
     bool copy;
     int64_t copy_ld;              // elements
+    bool widen;                   // 8-bit integers to f16; else the copy is of the operand's type
     size_t copy_bytes;
 };
 
@@ -49,20 +49,21 @@ GroupedOperand grouped_operand(const void *base, int64_t rows, int64_t blocks, i
                                int64_t stride, bool inner_is_sum, bool i8)
 {
     const int64_t vec = i8 ? 16 : 8;              // elements of 16 bytes
-    GroupedOperand o{base, rows, blocks, inner, ld, stride, false, 0, 0};
+    GroupedOperand o{base, rows, blocks, inner, ld, stride, false, 0, false, 0};
     o.copy = reinterpret_cast<uintptr_t>(base) % 16 || ld % vec || (blocks > 1 && (stride % vec || stride < ld)) ||
              (inner_is_sum && inner % vec);
     return o;
 }
 
-// Decides on the copy and sizes it.
-void grouped_copy(GroupedOperand &o, bool copy)
+// Sizes the copy, if there is one.
+void grouped_copy(GroupedOperand &o, bool i8, bool widen)
 {
-    o.copy = copy;
+    o.widen = widen;
+    o.copy |= widen;
     if (o.copy) {
         const int64_t rows = o.rows, blocks = o.blocks, inner = o.inner;
         o.copy_ld = (inner + 63) / 64 * 64;
-        o.copy_bytes = size_t(rows) * size_t(blocks) * size_t(o.copy_ld) * 2;
+        o.copy_bytes = size_t(rows) * size_t(blocks) * size_t(o.copy_ld) * (i8 && !widen ? 1 : 2);
         o.copy_bytes = (o.copy_bytes + 255) & ~size_t(255);
     }
 }
@@ -92,15 +93,13 @@ GroupedPlan grouped_plan(int op, int64_t E, int64_t M, int64_t K, int64_t T, con
         g.x = grouped_operand(X, T, 1, M, ldx, 0, false, false);
         g.y = grouped_operand(Y, T, 1, K, ldy, 0, false, false);
         g.map_bytes = size_t(E) * 2 * sizeof(CUtensorMap);
-        grouped_copy(g.x, g.x.copy);
-        grouped_copy(g.y, g.y.copy);
     } else {
         const bool grad_b = op == GEMM_GROUPED_GRAD_B;
         g.x = grouped_operand(X, M, E, K, ldx, stride_x, !grad_b, i8);
         g.y = grouped_operand(Y, T, 1, grad_b ? M : K, ldy, 0, true, i8);
-        grouped_copy(g.x, g.x.copy);
-        grouped_copy(g.y, g.y.copy || (i8 && (T > kI8DirectRows * E || g.x.copy)));
     }
+    grouped_copy(g.x, i8, false);
+    grouped_copy(g.y, i8, i8 && T > kI8DirectRows * E);
     return g;
 }
 
@@ -120,13 +119,12 @@ gemm_status_t launch_widen(const char *name, DeviceState &dev, const GroupedPlan
 {
     constexpr int64_t kElems = 16 / sizeof(Src);
     auto job = [](const GroupedOperand &o, void *dst) {
-        tn::WidenJob<Src> j{static_cast<const Src *>(o.base), o.ld, o.stride, static_cast<uint16_t *>(dst), o.copy_ld, o.rows,
-                            o.copy ? o.rows * o.blocks : 0, o.inner, 0, 1, 0, nullptr, nullptr};
-        const int64_t units = o.copy_ld / kElems;
+        tn::WidenJob<Src> j{static_cast<const Src *>(o.base), o.ld, o.stride, static_cast<uint8_t *>(dst), o.copy_ld / kElems,
+                            o.widen ? 32 : 16, o.rows, o.copy ? o.rows * o.blocks : 0, o.inner, 0, 1, 0, nullptr, nullptr};
         if (o.copy)
             j.end = reinterpret_cast<const char *>(j.src + (o.blocks - 1) * o.stride + (o.rows - 1) * o.ld + o.inner);
-        while (j.shift < 5 && (int64_t(1) << j.shift) < units) ++j.shift;
-        j.segs = (units + tn::kWidenSeg - 1) / tn::kWidenSeg;
+        while (j.shift < 5 && (int64_t(1) << j.shift) < j.units) ++j.shift;
+        j.segs = (j.units + tn::kWidenSeg - 1) / tn::kWidenSeg;
         j.work = ((j.rows + (int64_t(32) >> j.shift) - 1) >> (5 - j.shift)) * j.segs;
         return j;
     };
@@ -209,16 +207,18 @@ gemm_status_t launch_grouped(const GroupedCall &c, DeviceState &dev, tn::Grouped
     return GEMM_OK;
 }
 
-gemm_status_t launch_i8(const GroupedCall &c, DeviceState &dev, tn::GroupedParams &prm)
+// x, y: the weights and the tokens, 8-bit integers that the TMA can address.
+gemm_status_t launch_i8(const GroupedCall &c, DeviceState &dev, tn::GroupedParams &prm, const void *x, const void *y,
+                        int64_t ldx, int64_t stride_x, int64_t ldy, int64_t inner_x, int64_t inner_y)
 {
     gemm_status_t st;
-    const uint64_t apart = c.E > 1 ? uint64_t(c.stride_x) : uint64_t(16);
+    const uint64_t apart = c.E > 1 ? uint64_t(stride_x) : uint64_t(16);
     if (prm.red > 0) {
-        if ((st = encode_map(&prm.tmap_l, CU_TENSOR_MAP_DATA_TYPE_UINT8, c.X, c.K, c.M, c.ldx, c.E, apart, tn::kI8Block,
+        if ((st = encode_map(&prm.tmap_l, CU_TENSOR_MAP_DATA_TYPE_UINT8, x, inner_x, c.M, ldx, c.E, apart, tn::kI8Block,
                              tn::kI8RowsL, "A")) != GEMM_OK)
             return st;
         for (uint32_t i = 0; i < tn::kI8Rows / 16; ++i)
-            if ((st = encode_2d(&prm.tmap_r[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, c.Y, c.K, c.T, c.ldy, tn::kI8Block,
+            if ((st = encode_2d(&prm.tmap_r[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, y, inner_y, c.T, ldy, tn::kI8Block,
                                 16 * (i + 1), "rows")) != GEMM_OK)
                 return st;
     }
@@ -258,18 +258,19 @@ gemm_status_t launch_i8(const GroupedCall &c, DeviceState &dev, tn::GroupedParam
     return GEMM_OK;
 }
 
-// tokens: the widened copy, ld elements a row.
-gemm_status_t launch_i8_pair(const GroupedCall &c, DeviceState &dev, tn::GroupedParams &prm, const void *tokens,
-                             int64_t ld)
+// x as for launch_i8; tokens: the widened copy, ld_tokens elements a row.
+gemm_status_t launch_i8_pair(const GroupedCall &c, DeviceState &dev, tn::GroupedParams &prm, const void *x, int64_t ldx,
+                             int64_t stride_x, int64_t inner_x, const void *tokens, int64_t ld_tokens)
 {
     gemm_status_t st;
-    const uint64_t apart = c.E > 1 ? uint64_t(c.stride_x) : uint64_t(16);
+    const uint64_t apart = c.E > 1 ? uint64_t(stride_x) : uint64_t(16);
     if (prm.red > 0) {
-        if ((st = encode_map(&prm.tmap_l, CU_TENSOR_MAP_DATA_TYPE_UINT8, c.X, c.K, c.M, c.ldx, c.E, apart, tn::kI8Block,
+        if ((st = encode_map(&prm.tmap_l, CU_TENSOR_MAP_DATA_TYPE_UINT8, x, inner_x, c.M, ldx, c.E, apart, tn::kI8Block,
                              128, "A")) != GEMM_OK)
             return st;
         for (uint32_t i = 0; i < tn::kIpRowsR / 16; ++i)
-            if ((st = encode_2d(&prm.tmap_r[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, tokens, ld, c.T, ld * 2, tn::kGrBlock,
+            if ((st = encode_2d(&prm.tmap_r[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, tokens, ld_tokens, c.T, ld_tokens * 2,
+                                tn::kGrBlock,
                                 16 * (i + 1), "rows")) != GEMM_OK)
                 return st;
     }
@@ -485,16 +486,14 @@ gemm_status_t run_grouped(const GroupedCall &c)
     prm.scale_r = c.scale_b;
     prm.flags = stall_flags(g_inject_stall.load());
     prm.wait_limit_ns = g_wait_limit_ns.load();
-    if (i8 && !copied)
-        st = launch_i8(c, *dev, prm);
-    else if (i8 && copied == 2)
-        st = launch_i8_pair(c, *dev, prm, y, ldy);
+    if (i8 && plan.y.widen)
+        st = launch_i8_pair(c, *dev, prm, x, ldx, stride_x, in_x, y, ldy);
+    else if (i8)
+        st = launch_i8(c, *dev, prm, x, y, ldx, stride_x, ldy, in_x, in_y);
     else if (grad_a)
         st = launch_grouped_op<tn::kGrGradA>(c, *dev, prm, x, y, ldx, stride_x, ldy, in_x, in_y);
     else if (grad_b)
         st = launch_grouped_op<tn::kGrGradB>(c, *dev, prm, x, y, ldx, stride_x, ldy, in_x, in_y);
-    else if (i8)
-        st = launch_grouped_op<tn::kGrI8>(c, *dev, prm, x, y, ldx, stride_x, ldy, in_x, in_y);
     else
         st = launch_grouped_op<tn::kGrProduct>(c, *dev, prm, x, y, ldx, stride_x, ldy, in_x, in_y);
     t_rec.copied = copied;

@@ -44,7 +44,7 @@ constexpr int kGrRaster = 8;                 // R tiles per raster group
 constexpr int kGrChunk = 32;                 // accumulator columns per epilogue step
 constexpr int kGrStageBytes = kGrChunk * 64; // one epilogue warp's staging: 32 rows of 32 16-bit results
 
-// (kGrI8: the product with the 8-bit form's scales.)
+// (kGrI8: the 8-bit kernels' product; tn_grouped_kernel has no such form.)
 enum GroupedOp : int { kGrProduct = 0, kGrGradB = 1, kGrGradA = 2, kGrI8 = 3 };
 
 constexpr int kGrEpiWarps = 8;               // epilogue warps: two per quarter of the TMEM lanes
@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(kGrThreads, 1) tn_grouped_kernel(const __grid_
 {
     using Cfg = GroupedCfg<kGroup, kRows>;
     constexpr int kStages = Cfg::kStages, kAtoms = Cfg::kAtoms;
-    constexpr bool kLMajorK = kOp == kGrProduct || kOp == kGrI8, kRMajorK = kOp != kGrGradA;
+    constexpr bool kLMajorK = kOp == kGrProduct, kRMajorK = kOp != kGrGradA;
 
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -772,13 +772,6 @@ __global__ void __launch_bounds__(kGrThreads, 1) tn_grouped_kernel(const __grid_
                     for (int32_t r = turn; r < t.rows; r += 2) out[r * p.out_ld + lane] = 0;
                 continue;
             }
-            if constexpr (kOp == kGrI8) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    store.scale_l[i] = 8 * i + (lane >> 2) < store.wide
-                                           ? __ldg(p.scale_l + static_cast<int64_t>(t.e) * p.l_extent + l0 + 8 * i + (lane >> 2))
-                                           : 0.0f;
-            }
 #pragma unroll 1
             for (int half = 0; half < Cfg::kHalves; ++half) {
                 const int32_t first = half * Cfg::kHalfRows;       // the half's first row within the tile
@@ -802,11 +795,10 @@ __global__ void __launch_bounds__(kGrThreads, 1) tn_grouped_kernel(const __grid_
                 };
                 uint16_t *dst = out + first * p.out_ld;
                 const int32_t rows = t.rows - first;
-                const float *scale_r = kOp == kGrI8 ? p.scale_r + row0 + first : nullptr;
                 if (out_bf16)
-                    store.half<true, kOp == kGrI8>(t_row, turn, steps, dst, rows, scale_r, hand_back);
+                    store.half<true, false>(t_row, turn, steps, dst, rows, nullptr, hand_back);
                 else
-                    store.half<false, kOp == kGrI8>(t_row, turn, steps, dst, rows, scale_r, hand_back);
+                    store.half<false, false>(t_row, turn, steps, dst, rows, nullptr, hand_back);
                 ++sub;
             }
         }
@@ -879,15 +871,15 @@ __global__ void __launch_bounds__(32) grouped_maps_kernel(const __grid_constant_
 }
 
 // ------------------------------------------------------------------ copies
-// Rows that the TMA cannot address in place, or 8-bit integers, copied to f16
-// (or as they are, 16 bits wide) rows that start on 128-byte boundaries, the
-// padding zeroed: row r of the copy is row r % rows_per of block r / rows_per.
+// Rows that the TMA cannot address in place, copied to rows that start on 64-byte
+// boundaries, the padding zeroed, and 8-bit tokens widened to f16 on the way where the
+// kernel wants them so: row r of the copy is row r % rows_per of block r / rows_per.
 template <typename Src>
 struct WidenJob {
     const Src *src;
     int64_t ld, stride;
-    uint16_t *dst;
-    int64_t ld_dst;      // a multiple of 64
+    uint8_t *dst;
+    int64_t units, unit_bytes;   // 16-byte source units of a row, padding included; bytes of one in the copy
     int64_t rows_per, rows, cols;
     int32_t shift;       // 1 << shift lanes of a warp to a row
     int64_t segs, work;  // segments (kWidenSeg units) of a row; warps' shares in all
@@ -952,9 +944,9 @@ __global__ void __launch_bounds__(kWidenThreads, 5) widen_rows_kernel(const __gr
         if (j.offsets && max(j.offsets[e + 1], 0) <= max(j.offsets[e], 0)) continue;
         const int64_t u0 = seg * kWidenSeg;      // the share's first unit of its row(s)
         const Src *src = j.src + e * j.stride + (r - e * j.rows_per) * j.ld + u0 * kElems;
-        uint16_t *dst = j.dst + r * j.ld_dst + u0 * kElems;
+        uint8_t *dst = j.dst + (r * j.units + u0) * j.unit_bytes;
         // within the share 32 bits count elements and units
-        const int64_t left = j.cols - u0 * kElems, room = j.ld_dst / kElems - u0;
+        const int64_t left = j.cols - u0 * kElems, room = j.units - u0;
         const int32_t cols = static_cast<int32_t>(left < kWidenSeg * kElems ? (left > 0 ? left : 0) : kWidenSeg * kElems);
         const int32_t units = static_cast<int32_t>(room < kWidenSeg ? room : kWidenSeg);
         const int32_t s = static_cast<int32_t>(reinterpret_cast<uintptr_t>(src) & 15u);
@@ -1003,8 +995,8 @@ __global__ void __launch_bounds__(kWidenThreads, 5) widen_rows_kernel(const __gr
                     if (c * kElems + q < cols) part.v[q] = src[c * kElems + q];
                 x = part.u4;
             }
-            uint4 *to = reinterpret_cast<uint4 *>(dst + c * kElems);
-            if constexpr (sizeof(Src) == 1) {
+            uint4 *to = reinterpret_cast<uint4 *>(dst + c * static_cast<int32_t>(j.unit_bytes));
+            if (sizeof(Src) == 1 && j.unit_bytes == 32) {    // to f16
                 const uint2 a = i8x4_to_f16x4(x.x), b = i8x4_to_f16x4(x.y), d = i8x4_to_f16x4(x.z), f = i8x4_to_f16x4(x.w);
                 to[0] = make_uint4(a.x, a.y, b.x, b.y);
                 to[1] = make_uint4(d.x, d.y, f.x, f.y);
