@@ -923,6 +923,7 @@ __global__ void __launch_bounds__(kWidenThreads, 5) widen_rows_kernel(const __gr
 {
     constexpr int kElems = 16 / sizeof(Src);     // of a unit
     ptx::griddep_wait();
+    ptx::griddep_launch_dependents();            // they start once the last of these CTAs has
     const int lane = threadIdx.x & 31;
     const int64_t work = j0.work + j1.work, step = static_cast<int64_t>(gridDim.x) * (kWidenThreads / 32);
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * (kWidenThreads / 32) + (threadIdx.x >> 5); i < work; i += step) {
