@@ -25,10 +25,27 @@ struct GroupedCall {
     bool needs_offsets = false;
 };
 
-// Rows per expert up to which the 8-bit product widens both operands on the way
-// to the tensor core, on single CTAs (tn_i8_kernel); with more, the tokens are
-// widened first and CTA pairs widen the weights (tn_i8_pair_kernel).
-constexpr int64_t kI8DirectRows = 128;
+// Tiles of l x up to r rows that T rows of E experts make, at most: the counts
+// are known on the device only.
+int64_t grouped_tiles(int64_t l_extent, int64_t l, int64_t T, int64_t E, int64_t r)
+{
+    return (l_extent + l - 1) / l * (T / r + (E < T ? E : T));
+}
+
+// The 8-bit product widens both operands on the way to the tensor core, on single
+// CTAs (tn_i8_kernel), for few rows per expert and where its tiles make up to one
+// and a half waves of the 152 SMs; else the tokens are widened first and CTA pairs
+// widen the weights (tn_i8_pair_kernel).  The rule is the workspace query's too,
+// so it asks no device.  Measured on GB300, single CTAs / pairs: 1024 x 200 x 4096
+// (32 tiles) 11.9 / 19.7 us, 1024 x 1024 x 1024 (136) 8.7 / 11.9, 320 x 4178 x 2560
+// (198) 21.0 / 25.2, 4096 x 512 x 4096 (288) 30.3 / 24.8, 2048 x 2048 x 2048 (528)
+// 31.2 / 24.0.
+constexpr int64_t kI8DirectRows = 128, kI8DirectTiles = 228;
+
+bool i8_direct(int64_t M, int64_t T, int64_t E)
+{
+    return T <= kI8DirectRows * E || grouped_tiles(M, tn::kI8RowsL, T, E, tn::kI8Rows) <= kI8DirectTiles;
+}
 
 // An operand as `blocks` matrices of rows x inner elements, and whether it is
 // copied first: when the TMA cannot address it in place -- base, row stride or
@@ -99,7 +116,7 @@ GroupedPlan grouped_plan(int op, int64_t E, int64_t M, int64_t K, int64_t T, con
         g.y = grouped_operand(Y, T, 1, grad_b ? M : K, ldy, 0, true, i8);
     }
     grouped_copy(g.x, i8, false);
-    grouped_copy(g.y, i8, i8 && T > kI8DirectRows * E);
+    grouped_copy(g.y, i8, i8 && !i8_direct(M, T, E));
     return g;
 }
 
@@ -148,6 +165,50 @@ gemm_status_t launch_widen(const char *name, DeviceState &dev, const GroupedPlan
     return GEMM_OK;
 }
 
+// Clusters of this launch that fit the device at once.
+int co_resident(const void *kernel, const cudaLaunchConfig_t &cfg, int fallback)
+{
+    int found = 0;
+    if (cudaOccupancyMaxActiveClusters(&found, kernel, &cfg) != cudaSuccess || found <= 0) {
+        cudaGetLastError();
+        found = fallback;
+    }
+    return found;
+}
+
+// How many single CTAs share each tile's sum of `stages` ring stages: 1, 2, 4 or
+// 8, while every tile's cluster is resident at once and each CTA has four stages at
+// least; but one CTA below twelve stages, where what the join costs (1.5 us) is not
+// won back.  slots: the device's co-resident clusters of 2, 4 and 8 (0 = not queried).
+// Measured on GB300, whole sums -> split: 1024 x 16 x 8192 in 8 bits (8 tiles)
+// 22.3 -> 10.3 us, 4096 x 16 x 4096 (32 tiles) 13.4 -> 9.7, 2048 x 16 x 1536 7.8 -> 7.5,
+// 2048 x 16 x 1024 6.8 -> 7.0; weight gradient of 8 experts of 8192 x 512 with 256 rows
+// 28.2 -> 19.1; and with more clusters of 8 than are resident, 2048 x 16 x 4096 14.0 -> 17.6.
+int grouped_split(const void *kernel, int threads, int smem, int64_t tiles, int64_t stages, int sms, int (&slots)[3])
+{
+    int split = 1;
+    if (stages < 12) return split;
+    for (int i = 0; i < 3 && stages >= 8 * split && tiles * split * 2 <= sms; ++i, split *= 2) {
+        std::lock_guard<std::mutex> lock(g_mutex);
+        if (slots[i] == 0) {
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = split * 2;
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(static_cast<unsigned>(sms / (split * 2) * (split * 2)), 1, 1);
+            cfg.blockDim = dim3(threads, 1, 1);
+            cfg.dynamicSmemBytes = smem;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            slots[i] = co_resident(kernel, cfg, 1);
+        }
+        if (tiles > slots[i]) break;
+    }
+    return split;
+}
+
 template <int kOp, int kGroup, int kRows>
 gemm_status_t launch_grouped(const GroupedCall &c, DeviceState &dev, tn::GroupedParams &prm, int variant)
 {
@@ -175,11 +236,7 @@ gemm_status_t launch_grouped(const GroupedCall &c, DeviceState &dev, tn::Grouped
                 cfg.attrs = attr + 1;
                 cfg.numAttrs = 1;
                 cfg.gridDim = dim3(kGroup * (dev.sms / kGroup), 1, 1);
-                e = cudaOccupancyMaxActiveClusters(&found, kernel, &cfg);
-                if (e != cudaSuccess || found <= 0) {
-                    cudaGetLastError();
-                    found = dev.sms / kGroup;
-                }
+                found = co_resident(reinterpret_cast<const void *>(kernel), cfg, dev.sms / kGroup);
             }
             n = found;
         }
@@ -190,15 +247,21 @@ gemm_status_t launch_grouped(const GroupedCall &c, DeviceState &dev, tn::Grouped
                                                 : c.T / kRows + (c.E < c.T ? c.E : c.T);   // an upper bound
     if (r_tiles > (int64_t(1) << 30) / l_tiles) return fail(GEMM_ERR_UNSUPPORTED, "%s: too many output tiles", c.name);
     const int64_t tiles = r_tiles * l_tiles;
-    const int grid = static_cast<int>(tiles < slots ? tiles : slots) * kGroup;
+    constexpr int64_t kStageTerms = Cfg::kAtoms * tn::kGrBlock;
+    if constexpr (kGroup == 1)
+        prm.split = grouped_split(reinterpret_cast<const void *>(kernel), tn::kGrThreads, Cfg::kSmemBytes, tiles,
+                                  (int64_t(prm.red) + kStageTerms - 1) / kStageTerms, dev.sms, dev.split_slots[kOp]);
+    const int cluster = kGroup * prm.split;
+    const int grid = static_cast<int>(tiles < slots ? tiles : slots) * cluster;
+    attr[1].val.clusterDim.x = cluster;
     cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
     cfg.stream = c.stream;
     cfg.attrs = attr;
-    cfg.numAttrs = kGroup == 2 ? 2 : 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     t_rec = LaunchRecord{};
     t_rec.name = c.name;
     t_rec.grouped = 1;
-    t_rec.cluster = kGroup;
+    t_rec.cluster = cluster;
     t_rec.grid = grid;
     t_rec.slots = slots;
     t_rec.tiles = static_cast<int>(tiles);
@@ -231,25 +294,29 @@ gemm_status_t launch_i8(const GroupedCall &c, DeviceState &dev, tn::GroupedParam
             dev.i8_attr = true;
         }
     }
-    const int64_t l_tiles = (c.M + tn::kI8RowsL - 1) / tn::kI8RowsL;
-    const int64_t r_tiles = c.T / tn::kI8Rows + (c.E < c.T ? c.E : c.T);       // an upper bound
-    if (r_tiles > (int64_t(1) << 30) / l_tiles) return fail(GEMM_ERR_UNSUPPORTED, "%s: too many output tiles", c.name);
-    const int64_t tiles = r_tiles * l_tiles;
-    const int grid = static_cast<int>(tiles < dev.sms ? tiles : dev.sms);
-    cudaLaunchAttribute attr[1];
+    const int64_t tiles = grouped_tiles(c.M, tn::kI8RowsL, c.T, c.E, tn::kI8Rows);
+    if (tiles > int64_t(1) << 30) return fail(GEMM_ERR_UNSUPPORTED, "%s: too many output tiles", c.name);
+    prm.split = grouped_split(reinterpret_cast<const void *>(kernel), tn::kI8Threads, tn::kI8SmemBytes, tiles,
+                              (int64_t(prm.red) + tn::kI8Block - 1) / tn::kI8Block, dev.sms, dev.split_slots[2]);
+    const int grid = static_cast<int>(tiles < dev.sms ? tiles : dev.sms) * prm.split;
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = prm.split;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
     cfg.blockDim = dim3(tn::kI8Threads, 1, 1);
     cfg.dynamicSmemBytes = tn::kI8SmemBytes;
     cfg.stream = c.stream;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = prm.split > 1 ? 2 : 1;
     t_rec = LaunchRecord{};
     t_rec.name = c.name;
     t_rec.grouped = 1;
-    t_rec.cluster = 1;
+    t_rec.cluster = prm.split;
     t_rec.grid = grid;
     t_rec.slots = dev.sms;
     t_rec.tiles = static_cast<int>(tiles);
@@ -292,23 +359,15 @@ gemm_status_t launch_i8_pair(const GroupedCall &c, DeviceState &dev, tn::Grouped
         if (n == 0) {
             cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, tn::kIpSmemBytes);
             if (e != cudaSuccess) return fail(GEMM_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
-            int found = 0;
             cfg.attrs = attr + 1;
             cfg.numAttrs = 1;
             cfg.gridDim = dim3(2 * (dev.sms / 2), 1, 1);
-            e = cudaOccupancyMaxActiveClusters(&found, kernel, &cfg);
-            if (e != cudaSuccess || found <= 0) {
-                cudaGetLastError();
-                found = dev.sms / 2;
-            }
-            n = found;
+            n = co_resident(reinterpret_cast<const void *>(kernel), cfg, dev.sms / 2);
         }
         slots = n;
     }
-    const int64_t l_tiles = (c.M + 255) / 256;
-    const int64_t r_tiles = c.T / tn::kIpRows + (c.E < c.T ? c.E : c.T);       // an upper bound
-    if (r_tiles > (int64_t(1) << 30) / l_tiles) return fail(GEMM_ERR_UNSUPPORTED, "%s: too many output tiles", c.name);
-    const int64_t tiles = r_tiles * l_tiles;
+    const int64_t tiles = grouped_tiles(c.M, 256, c.T, c.E, tn::kIpRows);
+    if (tiles > int64_t(1) << 30) return fail(GEMM_ERR_UNSUPPORTED, "%s: too many output tiles", c.name);
     const int grid = 2 * static_cast<int>(tiles < slots ? tiles : slots);
     cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
     cfg.stream = c.stream;
@@ -331,13 +390,17 @@ gemm_status_t launch_grouped_op(const GroupedCall &c, DeviceState &dev, tn::Grou
                                 const void *x, const void *y, int64_t ldx, int64_t stride_x, int64_t ldy,
                                 int64_t inner_x, int64_t inner_y)
 {
-    // Few rows per expert: bound by the read of the weights, on single CTAs of
-    // 128 x 64 tiles (twice as many of them, and no pair to set up), as long as an
-    // expert's rows mostly fit one tile.  Measured on GB300, single CTAs / pairs: 16
-    // experts of 4096 x 1024 with 1 row on average 16.5 / 17.3 us, 32 rows 27.6 /
-    // 28.6; 8 of 2048 x 4096 with 32 rows 26.2 / 28.2, but with 48 (some over 64)
-    // 35.8 / 28.6.
-    const bool few = kOp != tn::kGrGradA && c.T <= 32 * c.E;
+    // Single CTAs of 128 x 64 tiles (four times as many of them, and no pair to set
+    // up) for few rows per expert, where the read of the weights is what counts, as
+    // long as an expert's rows mostly fit one tile; and where their tiles make no more
+    // than one wave, so that pairs leave SMs idle.  Measured on GB300, single CTAs /
+    // pairs: 16 experts of 4096 x 1024 with 1 row on average 16.5 / 17.3 us, 32 rows
+    // 27.6 / 28.6; 8 of 2048 x 4096 with 32 rows 26.2 / 28.2, but with 48 (some over 64)
+    // 35.8 / 28.6.  By tiles: 8 of 1024 x 4096 with 512 rows in all (128) 18.1 / 20.8,
+    // 5 of 200 x 5240 with 2020 (72, the sum split) 17.8 / 34.9; 4 of 2048 x 2048 with
+    // 400 (160) 10.8 / 10.4, 8 of 1024 x 1024 with 1024 (192) 11.2 / 8.6.
+    const bool few = kOp != tn::kGrGradA &&
+                     (c.T <= 32 * c.E || grouped_tiles(prm.l_extent, 128, c.T, c.E, 64) <= dev.sms);
     gemm_status_t st;
     if (prm.red > 0) {
         const CUtensorMapDataType type =
@@ -482,6 +545,7 @@ gemm_status_t run_grouped(const GroupedCall &c)
     prm.fmt = c.type == GEMM_IN_BF16 ? 1u : 0u;
     prm.out_fmt = c.out_type == GEMM_IN_BF16 ? 1u : 0u;
     prm.out_vec = reinterpret_cast<uintptr_t>(c.out) % 16 == 0 && c.ldo % 8 == 0 && (!grad_a || c.stride_o % 8 == 0);
+    prm.split = 1;
     prm.scale_l = c.scale_a;
     prm.scale_r = c.scale_b;
     prm.flags = stall_flags(g_inject_stall.load());

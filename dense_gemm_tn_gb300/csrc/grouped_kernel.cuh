@@ -97,6 +97,7 @@ struct GroupedParams {
     int32_t r_extent;                // grad_a: the result's rows per expert (M)
     int32_t red;                     // terms of the sum (grad_a: the group's rows instead)
     uint32_t fmt, out_fmt;           // operands and result: 0 f16, 1 bf16
+    int32_t split;                   // single CTAs: a cluster of this many shares a tile's sum (1, 2, 4 or 8)
     uint32_t out_vec;                // every row of the result starts on a 16-byte boundary
     const float *scale_l;            // 8-bit product: [E][l_extent] and [T] (else NULL)
     const float *scale_r;
@@ -396,6 +397,83 @@ struct GroupedStore {
     }
 };
 
+// ------------------------------------------------------------------ split sums
+// Few tiles with long sums leave most SMs idle.  Then a cluster of 2, 4 or 8
+// single CTAs takes a tile (and just one: the host asks for no more tiles than
+// clusters), each CTA a part of the sum.  The tile's 32 x 32 pieces of the
+// accumulator are shared out over the CTAs: each leaves the others' pieces of its
+// own partial sum, as the registers that they are read into, in its ring, whose
+// loads and MMAs are all done, and adds up its own out of the others' rings, in
+// the order of the ranks, so that a result never depends on timing.
+struct SplitSum {
+    uint32_t ring;            // shared address, the same in every CTA
+    int32_t split, rank;      // CTAs of the cluster (a power of two), this one's rank
+
+    // Piece (quarter of the lanes, step of the columns).
+    __device__ __forceinline__ bool mine(int quarter, int step) const { return ((quarter + 4 * step) & (split - 1)) == rank; }
+    __device__ __forceinline__ uint32_t at(int quarter, int step, int lane) const
+    {
+        return ring + static_cast<uint32_t>(quarter + 4 * step) * 4096u + lane * 16u;
+    }
+    __device__ __forceinline__ void leave(uint32_t addr, const uint32_t (&v)[2][16]) const
+    {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                ptx::st_shared_v4(addr + (4 * h + i) * 512u, v[h][4 * i], v[h][4 * i + 1], v[h][4 * i + 2], v[h][4 * i + 3]);
+    }
+    // v: this CTA's own part of the piece, then the sum.
+    __device__ __forceinline__ void add_others(uint32_t addr, uint32_t (&v)[2][16]) const
+    {
+        float sum[2][16];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) sum[h][i] = 0.0f;
+#pragma unroll 1
+        for (int32_t q = 0; q < split; ++q) {
+            const uint32_t from = ptx::mapa_shared(addr, q);
+            uint4 x[2][4];
+            if (q != rank) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[h][i] = ptx::ld_cluster_v4(from + (4 * h + i) * 512u);
+            } else {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        x[h][i] = make_uint4(v[h][4 * i], v[h][4 * i + 1], v[h][4 * i + 2], v[h][4 * i + 3]);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    sum[h][4 * i] += __uint_as_float(x[h][i].x);
+                    sum[h][4 * i + 1] += __uint_as_float(x[h][i].y);
+                    sum[h][4 * i + 2] += __uint_as_float(x[h][i].z);
+                    sum[h][4 * i + 3] += __uint_as_float(x[h][i].w);
+                }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[h][i] = __float_as_uint(sum[h][i]);
+    }
+};
+
+// A piece's columns out of TMEM.
+__device__ __forceinline__ void load_piece(uint32_t t_addr, uint32_t (&v)[2][16])
+{
+    ptx::tmem_ld_16x256b_x4(t_addr, v[0]);
+    ptx::tmem_ld_16x256b_x4(t_addr + (16u << 16), v[1]);
+    ptx::tmem_ld_wait_all();
+    ptx::reg_dependency(v[0]);
+    ptx::reg_dependency(v[1]);
+}
+
 template <int kOp, int kGroup, int kRows>
 __global__ void __launch_bounds__(kGrThreads, 1) tn_grouped_kernel(const __grid_constant__ GroupedParams p)
 {
@@ -476,10 +554,23 @@ __global__ void __launch_bounds__(kGrThreads, 1) tn_grouped_kernel(const __grid_
     const int32_t l_tiles = (p.l_extent + Cfg::kTileL - 1) / Cfg::kTileL;
     grouped_tables<kOp, kRows>(p, l_tiles, start, before);
     const int32_t total = before[p.E];
-    const int32_t slot = static_cast<int32_t>(blockIdx.x) / kGroup, slots = static_cast<int32_t>(gridDim.x) / kGroup;
+    // (grad_a's sums are the groups' own rows: not split)
+    constexpr bool kMaySplit = kGroup == 1 && kOp != kGrGradA;
+    static_assert(!kMaySplit || kRows <= 2 * kGrChunk, "the pieces of a split sum are four by two at most");
+    const int32_t split = kMaySplit ? p.split : 1;
+    const int32_t ctas = kGroup * split;
+    const int32_t slot = static_cast<int32_t>(blockIdx.x) / ctas, slots = static_cast<int32_t>(gridDim.x) / ctas;
+    const SplitSum parts{s_ring, split, split > 1 ? static_cast<int32_t>(ptx::cluster_ctarank()) : 0};
+    // the blocks of a sum of `blocks` that are this CTA's: whole stages
+    auto part = [&](int32_t blocks, int32_t rank) {
+        if (!kMaySplit) return rank == 0 ? 0 : blocks;
+        const int32_t stages = (blocks + kAtoms - 1) / kAtoms, to = stages * rank / split * kAtoms;
+        return to < blocks ? to : blocks;
+    };
     GroupedWalk<kOp, kRows, Cfg::kHalfRows, Cfg::kTileL, Cfg::kGran> walk{start, before, l_tiles, p.r_extent, p.red, 0};
     auto blocks_of = [](int32_t red) { return (red + kGrBlock - 1) / kGrBlock; };
 
+    bool joins = false;                           // an epilogue warp whose tile's split sum is complete here
     if (warp == 0) {
         // ------------------------------------------------ TMA producer (every CTA)
         // A pair's loads all complete on the even CTA's full[s][a], which its own
@@ -489,7 +580,7 @@ __global__ void __launch_bounds__(kGrThreads, 1) tn_grouped_kernel(const __grid_
             int stage = 0;
             uint32_t phase = 0, n_issued = 0;
             bool ok = true;
-            if (p.flags & (pos == 0 ? kFlagStallProducer0 : kFlagStallProducer1))
+            if (p.flags & (pos == 0 && parts.rank == 0 ? kFlagStallProducer0 : kFlagStallProducer1))
                 ok = wait_warp(w, never_bar, 0u, kSiteStall);
             int32_t mapped = -1;
             for (int32_t u = slot; ok && u < total; u += slots) {
@@ -519,8 +610,9 @@ __global__ void __launch_bounds__(kGrThreads, 1) tn_grouped_kernel(const __grid_
                         mapped = t.e;
                     }
                 }
-                const int32_t blocks = blocks_of(t.red);
-                for (int32_t i = 0; i < blocks; i += kAtoms) {
+                const int32_t sum_blocks = blocks_of(t.red);
+                const int32_t begin = part(sum_blocks, parts.rank), blocks = part(sum_blocks, parts.rank + 1);
+                for (int32_t i = begin; i < blocks; i += kAtoms) {
                     if (!wait_warp(w, empty_bar(stage), phase ^ 1u, kSiteEmpty)) {
                         ok = false;
                         break;
@@ -657,7 +749,8 @@ __global__ void __launch_bounds__(kGrThreads, 1) tn_grouped_kernel(const __grid_
                 }
                 if (!wait_warp(w, accempty_bar(sub & 1u), ((sub >> 1) & 1u) ^ 1u, kSiteAccEmpty)) break;
                 ptx::tc_fence_after_sync();
-                const int32_t blocks = blocks_of(t.red);
+                const int32_t sum_blocks = blocks_of(t.red);
+                const int32_t begin = part(sum_blocks, parts.rank), blocks = part(sum_blocks, parts.rank + 1);
                 // The MMAs of block i, in atom a of stage s, for half h.  Terms past the end
                 // of the sum are zeros: whole steps of them are left out.
                 auto issue = [&](int s, int a, int32_t i, int h) {
@@ -670,7 +763,7 @@ __global__ void __launch_bounds__(kGrThreads, 1) tn_grouped_kernel(const __grid_
                     for (int j = 0; j < kGrBlock / 16; ++j)
                         if (left > 16 * j)
                             ptx::mma_f16<kGroup>(d_tmem[h], desc_l + kStepL * j, desc_r + kStepR * j, idesc[h],
-                                                 (i | j) != 0 ? 1u : 0u);
+                                                 (i - begin) | j ? 1u : 0u);
                 };
                 // A tile's second half may have to wait for the epilogue to read its
                 // accumulator.  Until then stages are held with only their first half's MMAs
@@ -691,7 +784,7 @@ __global__ void __launch_bounds__(kGrThreads, 1) tn_grouped_kernel(const __grid_
                         if (++held_stage == kStages) held_stage = 0;
                     }
                 };
-                for (int32_t i = 0; ok && i < blocks; i += kAtoms) {
+                for (int32_t i = begin; ok && i < blocks; i += kAtoms) {
 #pragma unroll
                     for (int a = 0; a < kAtoms; ++a) {
                         if (!wait_warp(w, full_bar(stage, a), phase, kSiteLoaded)) {
@@ -762,6 +855,18 @@ __global__ void __launch_bounds__(kGrThreads, 1) tn_grouped_kernel(const __grid_
         const bool out_bf16 = p.out_fmt != 0;
         for (int32_t u = slot; ok && u < total; u += slots) {
             const GroupedTile t = walk.at(u);
+            if (split > 1) {                      // the cluster's one tile, stored further down
+                ok = joins = wait_warp(w, accfull_bar(0), 0u, kSiteAccFull);
+                if (!ok) break;
+                ptx::tc_fence_after_sync();
+                for (int s = turn; s * kGrChunk < t.n_mma[0]; s += 2) {
+                    if (parts.mine(quarter, s)) continue;
+                    uint32_t v[2][16];
+                    load_piece(tmem_base + (static_cast<uint32_t>(32 * quarter) << 16) + s * kGrChunk, v);
+                    parts.leave(parts.at(quarter, s, lane), v);
+                }
+                break;
+            }
             const int32_t l0 = t.l0 + static_cast<int32_t>(pos) * Cfg::kRowsL + 32 * quarter;   // this warp's 32
             const int64_t row0 = static_cast<int64_t>(kOp == kGrGradA ? 0 : start[t.e]) + t.r0;
             uint16_t *out = p.out + t.e * p.out_stride + row0 * p.out_ld + l0;
@@ -805,9 +910,37 @@ __global__ void __launch_bounds__(kGrThreads, 1) tn_grouped_kernel(const __grid_
     }
 
     __syncwarp();                // .aligned barriers below need converged warps
+    if constexpr (kMaySplit) {
+        if (split > 1) {
+            ptx::cluster_sync();                  // every CTA's pieces are in its ring
+            if (joins) {
+                const int quarter = warp & 3;
+                const GroupedTile t = walk.at(slot);
+                const int32_t l0 = t.l0 + 32 * quarter;
+                GroupedStore store;
+                store.init(s_staging + (warp - 2) * kGrStageBytes, lane);
+                store.ld = p.out_ld;
+                store.wide = p.l_extent - l0 < 32 ? p.l_extent - l0 : 32;
+                store.vec = p.out_vec != 0 && store.wide == 32;
+                uint16_t *out = p.out + (static_cast<int64_t>(start[t.e]) + t.r0) * p.out_ld + l0;
+                for (int s = (warp - 2) >> 2; s * kGrChunk < t.n_mma[0]; s += 2) {
+                    if (!parts.mine(quarter, s)) continue;
+                    uint32_t v[2][16];
+                    load_piece(tmem_base + (static_cast<uint32_t>(32 * quarter) << 16) + s * kGrChunk, v);
+                    parts.add_others(parts.at(quarter, s, lane), v);
+                    const int32_t c = s * kGrChunk;
+                    if (p.out_fmt != 0)
+                        store.step<true, false>(v, out + c * p.out_ld, t.rows - c, nullptr);
+                    else
+                        store.step<false, false>(v, out + c * p.out_ld, t.rows - c, nullptr);
+                }
+            }
+            __syncwarp();
+        }
+    }
     ptx::tc_fence_before_sync();
-    if constexpr (kGroup == 2)
-        ptx::cluster_sync();     // no CTA leaves while the other may still touch its shared memory
+    if (kGroup == 2 || split > 1)
+        ptx::cluster_sync();     // no CTA leaves while another may still touch its shared memory
     else
         __syncthreads();
     if (warp == 1) {

@@ -160,22 +160,44 @@ __global__ void __launch_bounds__(kI8Threads, 1) tn_i8_kernel(const __grid_const
     const int32_t l_tiles = (p.l_extent + kI8RowsL - 1) / kI8RowsL;
     grouped_tables<kGrI8, kI8Rows, kI8Threads>(p, l_tiles, start, before);
     const int32_t total = before[p.E];
-    const int32_t slot = static_cast<int32_t>(blockIdx.x), slots = static_cast<int32_t>(gridDim.x);
+    const int32_t split = p.split;
+    const int32_t slot = static_cast<int32_t>(blockIdx.x) / split, slots = static_cast<int32_t>(gridDim.x) / split;
+    const SplitSum parts{s_ring8, split, split > 1 ? static_cast<int32_t>(ptx::cluster_ctarank()) : 0};
     GroupedWalk<kGrI8, kI8Rows, kI8Rows, kI8RowsL, 16> walk{start, before, l_tiles, 0, p.red, 0};
-    const int32_t blocks = (p.red + kI8Block - 1) / kI8Block;       // 8-bit stages of a tile
+    // 8-bit stages of a tile, this CTA's being those from begin on, below blocks
+    const int32_t sum_blocks = (p.red + kI8Block - 1) / kI8Block;
+    const int32_t begin = sum_blocks * parts.rank / split, blocks = sum_blocks * (parts.rank + 1) / split;
+    bool joins = false;                       // an epilogue warp whose tile's split sum is complete here
+
+    GroupedStore store;
+    // an epilogue warp's part of the result, with its scales
+    auto aim = [&](const GroupedTile &t, int quarter) {
+        const int32_t l0 = t.l0 + 32 * quarter;
+        store.init(s_staging + (warp - 2) * kGrStageBytes, lane);
+        store.ld = p.out_ld;
+        store.wide = p.l_extent - l0 < 32 ? p.l_extent - l0 : 32;
+        store.vec = p.out_vec != 0 && store.wide == 32;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            store.scale_l[i] = 8 * i + (lane >> 2) < store.wide
+                                   ? __ldg(p.scale_l + static_cast<int64_t>(t.e) * p.l_extent + l0 + 8 * i + (lane >> 2))
+                                   : 0.0f;
+        return p.out + (static_cast<int64_t>(start[t.e]) + t.r0) * p.out_ld + l0;
+    };
 
     if (warp == 0) {
         // ------------------------------------------------ TMA producer
         int stage = 0;
         uint32_t phase = 0, n_issued = 0;
         bool ok = true;
-        if (p.flags & kFlagStallProducer0) ok = wait_warp(w, never_bar, 0u, kSiteStall);
+        if (p.flags & (parts.rank == 0 ? kFlagStallProducer0 : kFlagStallProducer1))
+            ok = wait_warp(w, never_bar, 0u, kSiteStall);
         for (int32_t u = slot; ok && u < total; u += slots) {
             const GroupedTile t = walk.at(u);
             const CUtensorMap *map_r = p.tmap_r + t.n_mma[0] / 16 - 1;
             const int32_t r0 = start[t.e] + t.r0;
             const uint32_t fill = static_cast<uint32_t>(kI8RowsL + t.n_mma[0]) * 128u;
-            for (int32_t i = 0; i < blocks; ++i) {
+            for (int32_t i = begin; i < blocks; ++i) {
                 if (!wait_warp(w, empty8_bar(stage), phase ^ 1u, kSiteEmpty)) {
                     ok = false;
                     break;
@@ -212,7 +234,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) tn_i8_kernel(const __grid_const
             const uint32_t d_tmem = tmem_base + (sub & 1u) * kI8Rows;
             if (!wait_warp(w, accempty_bar(sub & 1u), ((sub >> 1) & 1u) ^ 1u, kSiteAccEmpty)) break;
             ptx::tc_fence_after_sync();
-            for (int32_t i = 0; i < blocks; ++i) {
+            for (int32_t i = begin; i < blocks; ++i) {
                 if (!wait_warp(w, full16_bar(stage), phase, kSiteLoaded)) {
                     ok = false;
                     break;
@@ -229,7 +251,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) tn_i8_kernel(const __grid_const
                         for (int j = 0; j < kGrBlock / 16; ++j)
                             if (left > half * kGrBlock + 16 * j)
                                 ptx::mma_f16_ts<1>(d_tmem, a_tmem + 8 * j, desc_r + 2u * j, idesc,
-                                                (i | half | j) != 0 ? 1u : 0u);
+                                                (i - begin) | half | j ? 1u : 0u);
                     }
                     ptx::mma_commit<1>(empty16_bar(stage));
                     if (i + 1 == blocks) ptx::mma_commit<1>(accfull_bar(sub & 1u));
@@ -250,37 +272,32 @@ __global__ void __launch_bounds__(kI8Threads, 1) tn_i8_kernel(const __grid_const
     } else if (warp < 2 + kI8EpiWarps) {
         // ------------------------------------------------ epilogue (warps 2..5)
         const int quarter = warp & 3;
-        GroupedStore store;
-        store.init(s_staging + (warp - 2) * kGrStageBytes, lane);
-        store.ld = p.out_ld;
         uint32_t sub = 0;
         for (int32_t u = slot; u < total; u += slots) {
             const GroupedTile t = walk.at(u);
-            const int32_t l0 = t.l0 + 32 * quarter;
             const int64_t row0 = static_cast<int64_t>(start[t.e]) + t.r0;
-            uint16_t *out = p.out + row0 * p.out_ld + l0;
-            store.wide = p.l_extent - l0 < 32 ? p.l_extent - l0 : 32;
-            store.vec = p.out_vec != 0 && store.wide == 32;
+            uint16_t *out = aim(t, quarter);
             if (p.red == 0) {                     // an empty sum
                 if (lane < store.wide)
                     for (int32_t r = 0; r < t.rows; ++r) out[r * p.out_ld + lane] = 0;
                 continue;
             }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                store.scale_l[i] = 8 * i + (lane >> 2) < store.wide
-                                       ? __ldg(p.scale_l + static_cast<int64_t>(t.e) * p.l_extent + l0 + 8 * i + (lane >> 2))
-                                       : 0.0f;
             if (!wait_warp(w, accfull_bar(sub & 1u), (sub >> 1) & 1u, kSiteAccFull)) break;
             ptx::tc_fence_after_sync();
             const uint32_t t_row = tmem_base + (static_cast<uint32_t>(32 * quarter) << 16) + (sub & 1u) * kI8Rows;
+            if (split > 1) {                      // the cluster's one tile, stored further down
+                for (int s = 0; s * kGrChunk < t.n_mma[0]; ++s) {
+                    if (parts.mine(quarter, s)) continue;
+                    uint32_t v[2][16];
+                    load_piece(t_row + s * kGrChunk, v);
+                    parts.leave(parts.at(quarter, s, lane), v);
+                }
+                joins = true;
+                break;
+            }
             for (int32_t c = 0; c < t.n_mma[0]; c += kGrChunk) {
                 uint32_t v[2][16];
-                ptx::tmem_ld_16x256b_x4(t_row + c, v[0]);
-                ptx::tmem_ld_16x256b_x4(t_row + (16u << 16) + c, v[1]);
-                ptx::tmem_ld_wait_all();
-                ptx::reg_dependency(v[0]);
-                ptx::reg_dependency(v[1]);
+                load_piece(t_row + c, v);
                 if (c + kGrChunk >= t.n_mma[0]) {
                     ptx::tc_fence_before_sync();
                     __syncwarp();
@@ -312,7 +329,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) tn_i8_kernel(const __grid_const
         uint32_t phase8 = 0, phase16 = 0, n = 0;              // n: stages so far
         for (int32_t u = slot; ok && p.red > 0 && u < total; u += slots) {
             const int32_t groups_r = walk.at(u).n_mma[0] / 8;
-            for (int32_t i = 0; i < blocks; ++i, ++n) {
+            for (int32_t i = begin; i < blocks; ++i, ++n) {
                 if ((n & 1u) != static_cast<uint32_t>(team)) continue;
                 ok = wait_warp(w, full8_bar(stage8), phase8, kSiteLoaded);
                 if (!ok) break;
@@ -356,8 +373,32 @@ __global__ void __launch_bounds__(kI8Threads, 1) tn_i8_kernel(const __grid_const
     }
 
     __syncwarp();                // .aligned barriers below need converged warps
+    if (split > 1) {
+        ptx::cluster_sync();                  // every CTA's pieces are in its ring
+        if (joins) {
+            const int quarter = warp & 3;
+            const GroupedTile t = walk.at(slot);
+            const int64_t row0 = static_cast<int64_t>(start[t.e]) + t.r0;
+            uint16_t *out = aim(t, quarter);
+            for (int s = 0; s * kGrChunk < t.n_mma[0]; ++s) {
+                if (!parts.mine(quarter, s)) continue;
+                const int32_t c = s * kGrChunk;
+                uint32_t v[2][16];
+                load_piece(tmem_base + (static_cast<uint32_t>(32 * quarter) << 16) + c, v);
+                parts.add_others(parts.at(quarter, s, lane), v);
+                if (p.out_fmt != 0)
+                    store.step<true, true>(v, out + c * p.out_ld, t.rows - c, p.scale_r + row0 + c);
+                else
+                    store.step<false, true>(v, out + c * p.out_ld, t.rows - c, p.scale_r + row0 + c);
+            }
+        }
+        __syncwarp();
+    }
     ptx::tc_fence_before_sync();
-    __syncthreads();
+    if (split > 1)
+        ptx::cluster_sync();     // no CTA leaves while another reads its ring
+    else
+        __syncthreads();
     if (warp == 1) {
         __syncwarp();
         ptx::tc_fence_after_sync();

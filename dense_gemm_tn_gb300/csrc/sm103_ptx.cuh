@@ -527,6 +527,17 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr)
     return v;
 }
 
+// The same from another CTA of the cluster (shared::cluster address).
+__device__ __forceinline__ uint4 ld_cluster_v4(uint32_t cluster_addr)
+{
+    uint4 v;
+    asm volatile("ld.shared::cluster.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(cluster_addr)
+                 : "memory");
+    return v;
+}
+
 // Orders later uses of a second register block after a preceding wait.
 __device__ __forceinline__ void reg_dependency(uint32_t (&r)[32])
 {

@@ -38,6 +38,21 @@ SHAPES = [
     ([2000], 1544, 512),
     ([2] * 70, 200, 136),
     ([31, 33, 32, 1], 256, 4096),
+    # more tiles than one wave of single CTAs: CTA pairs
+    ([257, 0, 31, 5000], 520, 264),
+    ([513, 7, 4025], 384, 640),
+    ([3000, 200], 1000, 392),
+    ([300, 4900], 129, 127),
+    ([10000, 3], 99, 255),
+    ([20000], 1, 1),
+    ([40] * 30, 700, 520),
+    # few tiles with long sums, of the product or the gradient: split over clusters
+    ([5], 128, 1536),
+    ([3, 0, 64, 65], 200, 4104),
+    ([1], 8, 20000),
+    ([700], 136, 3333),
+    ([2, 31], 9001, 72),
+    ([90, 0, 1], 2064, 260),
 ]
 
 
@@ -62,7 +77,8 @@ def test_product_and_gradients_bit_exact(counts, M, K, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=["f16", "bf16"])
-@pytest.mark.parametrize("counts,M,K", [([3, 5], 256, 2048), ([200, 77, 300], 520, 1000), ([700, 900], 640, 1536)])
+@pytest.mark.parametrize("counts,M,K", [([3, 5], 256, 2048), ([200, 77, 300], 520, 1000), ([700, 900], 640, 1536),
+                                        ([5000, 3333], 640, 1536), ([9, 0, 70], 136, 9000), ([20, 3], 7000, 264)])
 def test_normal_values_within_the_derived_bound(counts, M, K, dtype):
     E, T = len(counts), sum(counts)
     off = offsets_of(counts)
@@ -74,11 +90,11 @@ def test_normal_values_within_the_derived_bound(counts, M, K, dtype):
                 dtype, "grad_a")
 
 
-def test_repeats_bit_for_bit():
-    counts = [130, 0, 700, 41]
-    off = offsets_of(counts)
+@pytest.mark.parametrize("counts,M,K", [([130, 0, 700, 41], 392, 520), ([1300, 0, 7000, 41], 392, 520), ([13, 0, 70, 4], 2056, 4104)])
+def test_repeats_bit_for_bit(counts, M, K):
+    off, T = offsets_of(counts), sum(counts)
     A, Bt, dCt = (normals(*s, seed=i, dtype=torch.bfloat16)
-                  for i, s in enumerate([(4, 392, 520), (871, 520), (871, 392)], 1))
+                  for i, s in enumerate([(4, M, K), (T, K), (T, M)], 1))
     calls = (lambda: g.tn_grouped(A, Bt, off), lambda: g.tn_grouped_grad_b(A, dCt, off),
              lambda: g.tn_grouped_grad_a(dCt, Bt, off))
     for call in calls:
@@ -90,7 +106,9 @@ def test_repeats_bit_for_bit():
 # (rows per expert, M, K, padding of A's, Bt's and the results' rows, of the expert blocks): strides that the
 # TMA takes in place and strides it does not; the padding holds NaN and must not be read, and not be written
 STRIDES = [([40, 7], 72, 136, 8, 0), ([40, 7], 72, 136, 1, 0), ([300, 0, 90], 264, 200, 24, 64),
-           ([300, 0, 90], 264, 200, 3, 5), ([20, 30], 65, 33, 7, 0), ([1, 70], 129, 1, 9, 1)]
+           ([300, 0, 90], 264, 200, 3, 5), ([20, 30], 65, 33, 7, 0), ([1, 70], 129, 1, 9, 1),
+           ([3000, 0, 4090], 264, 200, 24, 64), ([3000, 0, 4090], 264, 200, 3, 5), ([9000, 90], 65, 33, 7, 0),
+           ([20, 0, 3], 72, 2056, 8, 0), ([20, 0, 3], 72, 2051, 1, 3)]
 
 
 @pytest.mark.parametrize("counts,M,K,pad,block_pad", STRIDES)
@@ -395,9 +413,31 @@ def test_offsets_and_inputs_written_just_before_the_call():
 
 
 @pytest.mark.parametrize("mode", [1, 2, 3])
-@pytest.mark.parametrize("rows", [8, 300])
+def test_a_stalled_part_of_a_split_sum_reports_a_timeout(mode):
+    """Mode 1 stalls the MMAs, mode 2 the producer of a cluster's first CTA, mode 3 the others'."""
+    off = offsets_of([5, 9])
+    A, Bt, dCt = (small_ints(*s, seed=i, dtype=torch.float16) for i, s in enumerate([(2, 2056, 4104), (14, 4104), (14, 2056)], 1))
+    for call in (lambda: g.tn_grouped(A[:, :128], Bt, off), lambda: g.tn_grouped_grad_b(A[..., :128], dCt, off)):
+        want = call()
+        g.gemm_poll_device_status()
+        g.gemm_set_wait_limit_ns(20_000_000)
+        g.gemm_debug_inject_stall(mode)
+        try:
+            call()
+            with pytest.raises(g.GemmError) as e:
+                g.gemm_poll_device_status()
+            assert e.value.status == g.GEMM_ERR_TIMEOUT
+        finally:
+            g.gemm_debug_inject_stall(0)
+            g.gemm_set_wait_limit_ns(0)
+        assert torch.equal(call(), want)
+        g.gemm_poll_device_status()
+
+
+@pytest.mark.parametrize("mode", [1, 2, 3])
+@pytest.mark.parametrize("rows", [8, 3000])
 def test_a_stalled_role_reports_a_timeout_and_leaves_the_context_usable(mode, rows):
-    """rows 8: single CTAs; 300: CTA pairs.  (Mode 3, the odd CTA's producer, has
+    """rows 8: single CTAs; 3000: CTA pairs.  (Mode 3, the odd CTA's producer, has
     nothing to stall in a single CTA.)"""
     off = offsets_of([rows, rows])
     A, Bt, dCt = (small_ints(*s, seed=i, dtype=torch.float16)

@@ -37,7 +37,13 @@ def assert_scaled(got, sums, sa, sb, terms, dtype):
 @pytest.mark.parametrize("M,N,K", [(1, 1, 1), (8, 1, 16), (128, 16, 128), (257, 3, 80), (64, 65, 63), (130, 300, 1000),
                                    (512, 64, 2048), (1000, 513, 333), (33, 100, 5), (300, 17, 144), (129, 128, 400),
                                    (2000, 100, 1040), (128, 129, 256), (40, 1, 4096), (640, 112, 16), (20000, 33, 128),
-                                   (256, 257, 128), (300, 300, 144), (1000, 700, 400), (512, 1025, 2064), (77, 5000, 64), (8, 600, 16)])
+                                   (256, 257, 128), (300, 300, 144), (1000, 700, 400), (512, 1025, 2064), (77, 5000, 64), (8, 600, 16)]
+                         # CTA pairs: tiles past one and a half waves of single CTAs
+                         + [(2000, 1000, 400), (1290, 1537, 333), (1000, 4000, 48), (4096, 1025, 144), (520, 4097, 2064),
+                            (33, 16000, 16), (300, 5000, 5), (129, 8000, 1040)]
+                         # few tiles with long sums: split over clusters of 2, 4 and 8
+                         + [(128, 16, 1536), (100, 5, 16384), (128, 64, 3100), (257, 33, 8191), (2000, 17, 2064),
+                            (8192, 9, 2048), (1, 1, 100000), (2300, 65, 6000), (300, 200, 12300)])
 def test_i8_product(M, N, K, dtype):
     A, Bt, sa, sb = codes(M, K, seed=1), codes(N, K, seed=2), scales(M, seed=3), scales(N, seed=4)
     C = g.i8_tn(A, Bt, sa, sb, dtype=dtype)
@@ -48,7 +54,9 @@ def test_i8_product(M, N, K, dtype):
 
 @pytest.mark.parametrize("counts,M,K", [([1], 16, 16), ([0, 3, 0, 1], 128, 64), ([70, 0, 300], 200, 208), ([5, 6], 31, 33),
                                         ([1] * 40, 384, 272), ([64, 0, 65, 3], 130, 128), ([200, 10, 100], 136, 112),
-                                        ([300, 0, 600], 264, 272), ([193, 192, 1000, 2], 520, 1040)])
+                                        ([300, 0, 600], 264, 272), ([193, 192, 1000, 2], 520, 1040),
+                                        ([3000, 0, 2600, 193], 520, 272), ([2192, 1930, 1000, 2], 520, 1040), ([9000, 100], 264, 33),
+                                        ([3, 0, 70, 1], 200, 5000), ([1], 96, 20000), ([200, 9], 129, 2049)])
 def test_i8_grouped(counts, M, K):
     E, T = len(counts), sum(counts)
     off = offsets_of(counts)
@@ -81,7 +89,7 @@ def test_extreme_codes_and_long_sums():
             assert_scaled(C, Bt.double() @ A.double().t(), sa[None, :], sb[:, None], K, torch.bfloat16)
 
 
-@pytest.mark.parametrize("N", [5, 64, 600])
+@pytest.mark.parametrize("N", [5, 64, 600, 20000])
 def test_every_code_widens_exactly(N):
     """A's rows hold all 256 values, Bt picks one term per row."""
     K = 256
@@ -95,7 +103,8 @@ def test_every_code_widens_exactly(N):
     assert torch.equal(C, A[0, at].half()[None, :].expand(16, N))
 
 
-@pytest.mark.parametrize("M,N,K,pad", [(200, 17, 144, 16), (200, 17, 144, 1), (130, 600, 48, 32), (65, 3, 33, 0)])
+@pytest.mark.parametrize("M,N,K,pad", [(200, 17, 144, 16), (200, 17, 144, 1), (130, 600, 48, 32), (65, 3, 33, 0),
+                                       (130, 9000, 48, 32), (130, 9000, 48, 1), (65, 3, 4001, 3), (200, 70, 2064, 16)])
 def test_i8_strides(M, N, K, pad):
     A, Bt = padded(codes(M, K, seed=1), K + pad, 99), padded(codes(N, K, seed=2), K + pad, -77)
     sa, sb = scales(M, seed=3), scales(N, seed=4)
@@ -142,10 +151,11 @@ def test_i8_empty_sums():
     assert bool((C == 0).all())
 
 
-def test_i8_captured_on_two_streams():
+@pytest.mark.parametrize("rows", [700, 15000])
+def test_i8_captured_on_two_streams(rows):
     cases = [(codes(3, 200, 144, seed=i), codes(150, 144, seed=i + 1), scales(3, 200, seed=i + 2), scales(150, seed=i + 3),
               offsets_of([100, 0, 50])) for i in (1, 20)]
-    wide = [(codes(96, 80, seed=i), codes(700, 80, seed=i + 1), scales(96, seed=i + 2), scales(700, seed=i + 3)) for i in (40, 60)]
+    wide = [(codes(96, 80, seed=i), codes(rows, 80, seed=i + 1), scales(96, seed=i + 2), scales(rows, seed=i + 3)) for i in (40, 60)]
     run = [lambda c=c, w=w: (g.i8_tn_grouped(*c), g.i8_tn(*w)) for c, w in zip(cases, wide)]
     want = [r() for r in run]
     torch.cuda.synchronize()
@@ -166,9 +176,10 @@ def test_i8_captured_on_two_streams():
     g.gemm_poll_device_status()
 
 
-@pytest.mark.parametrize("N,mode", [(20, 1), (20, 2), (700, 1), (700, 2), (700, 3)])
+@pytest.mark.parametrize("N,mode", [(20, 1), (20, 2), (20, 3), (700, 1), (700, 2), (3000, 1), (3000, 2), (3000, 3)])
 def test_i8_stalled_role_reports_a_timeout(N, mode):
-    """20 rows: single CTAs; 700: CTA pairs (mode 3: the odd CTA's producer)."""
+    """20 and 700 rows: single CTAs, with 20 in clusters that share a tile's sum; 3000:
+    CTA pairs (mode 3: the producers of all but a cluster's first CTA)."""
     args = codes(600, 2048, seed=1), codes(N, 2048, seed=2), scales(600, seed=3), scales(N, seed=4)
     want = g.i8_tn(*args)
     g.gemm_poll_device_status()
@@ -184,6 +195,28 @@ def test_i8_stalled_role_reports_a_timeout(N, mode):
         g.gemm_set_wait_limit_ns(0)
     assert torch.equal(g.i8_tn(*args), want)
     g.gemm_poll_device_status()
+
+
+@pytest.mark.parametrize("M,N,K", [(832, 32, 12160), (2048, 16, 4096), (100, 130, 9000)])
+def test_i8_split_sums_repeat_bit_for_bit_beside_others(M, N, K):
+    """Parts of a sum are joined in one order, whatever else runs."""
+    args = codes(M, K, seed=1), codes(N, K, seed=2), scales(M, seed=3), scales(N, seed=4)
+    other = codes(512, 640, seed=5), codes(900, 640, seed=6), scales(512, seed=7), scales(900, seed=8)
+    want = g.i8_tn(*args)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = g.i8_tn(*args)
+    s = torch.cuda.Stream()
+    got = []
+    for _ in range(10):
+        with torch.cuda.stream(s):
+            g.i8_tn(*other)
+            got.append(g.i8_tn(*args))
+        graph.replay()
+    torch.cuda.synchronize()
+    g.gemm_poll_device_status()
+    assert all(torch.equal(x, want) for x in got + [out])
 
 
 def test_past_2_31_elements():

@@ -68,7 +68,7 @@ INVALID = [
     (grad_a, dict(ws=None)), (grad_a, dict(n=256)), (grad_a, dict(stride_da=8, ldda=8)), (grad_a, dict(stride_da=-1)),
     (grad_a, dict(dA=None)), (grad_a, dict(type=g.GEMM_IN_F32)), (grad_a, dict(ldda=7)), (grad_a, dict(lddc=15)),
     (i8, dict(type=g.GEMM_IN_F32)), (i8, dict(sa=None)), (i8, dict(sb=None)), (i8, dict(sa=P + 2)), (i8, dict(lda=15)),
-    (i8, dict(ldc=15)), (i8, dict(N=-1)), (i8, dict(C=5 * P + 1)), (i8, dict(lda=17, n=0)), (i8, dict(lda=17, ws=None)), (i8, dict(N=300, n=0)),
+    (i8, dict(ldc=15)), (i8, dict(N=-1)), (i8, dict(C=5 * P + 1)), (i8, dict(lda=17, n=0)), (i8, dict(lda=17, ws=None)), (i8, dict(N=20000, n=0)),
     (i8_grouped, dict(offsets=None)), (i8_grouped, dict(sb=None)), (i8_grouped, dict(ldb=15)), (i8_grouped, dict(T=-1)),
     (quant, dict(type=9)), (quant, dict(rows=-1)), (quant, dict(cols=-1)), (quant, dict(ldx=7)), (quant, dict(ldq=7)),
     (quant, dict(x=None)), (quant, dict(q=None)), (quant, dict(scale=None)), (quant, dict(scale=P + 2)),
