@@ -141,6 +141,13 @@ gemm_status_t launch_widen(const char *name, DeviceState &dev, const GroupedPlan
         if (o.copy)
             j.end = reinterpret_cast<const char *>(j.src + (o.blocks - 1) * o.stride + (o.rows - 1) * o.ld + o.inner);
         while (j.shift < 5 && (int64_t(1) << j.shift) < j.units) ++j.shift;
+        // A short row: of 32, 16 and 8 lanes the most that leave the fewest idle in its
+        // last turn.  Measured on GB300, 32 lanes -> this: 447360 rows of 40 units 143 -> 97
+        // us; but 850 rows of 712 with the gradient behind them 36 -> 52 us.
+        for (int t = j.shift - 1; j.units <= 64 && t >= 3; --t) {
+            auto idle = [&j](int n) { return (int64_t(1) << n) - 1 - (j.units - 1) % (int64_t(1) << n); };
+            if (idle(t) < idle(j.shift)) j.shift = t;
+        }
         j.segs = (j.units + tn::kWidenSeg - 1) / tn::kWidenSeg;
         j.work = ((j.rows + (int64_t(32) >> j.shift) - 1) >> (5 - j.shift)) * j.segs;
         return j;
