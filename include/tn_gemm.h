@@ -408,6 +408,8 @@ void gemm_set_wait_limit_ns(uint64_t limit_ns);
  *   1  the MMA-issuing thread;
  *   2  the TMA producer of the even CTA of each pair (or of each CTA);
  *   3  the TMA producer of the odd CTA of each pair.
+ * Where a grouped or 8-bit product splits its sums over clusters, 2 means the
+ * first CTA of each and 3 all the others.
  * 0 turns the hook off.
  */
 void gemm_debug_inject_stall(int mode);

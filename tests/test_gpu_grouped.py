@@ -282,6 +282,35 @@ def test_gradients_against_differences():
     assert float(by_a) == float((g.tn_grouped_grad_a(dCt, Bt, off).double() * dir_a.double()).sum())
 
 
+@pytest.mark.parametrize("table", [[5, 8, 8, 50], [0, 30, 10, 64], [-5, 20, 20, 90], [50, 40, 30, 20], [64, 64, 64, 64]])
+def test_split_sums_with_rows_of_no_expert_and_infinities(table):
+    """Sums long enough to be split over clusters (K of the product, M of the gradient):
+    tables as above, one expert's values infinite or NaN, strided and unaligned results."""
+    M, K, T, dtype = 2064, 2056, 64, torch.bfloat16
+    off = torch.tensor(table, dtype=torch.int32, device="cuda")
+    b, top = [], 0
+    for o in table:
+        top = max(top, min(max(o, 0), T))
+        b.append(top)
+    A, Bt, dCt = (small_ints(*s, seed=i, dtype=dtype) for i, s in enumerate([(3, M, K), (T, K), (T, M)], 1))
+    A[1], Bt[:b[0]], Bt[b[3]:], dCt[:b[0]], dCt[b[3]:] = (float("nan"),) * 5
+    Bt[b[2]:b[3]][:1, 7] = float("inf")
+    narrow = A[:, :130], dCt[:, :130]                      # the product's A (a part of its rows), the gradient's by its columns
+    for call, A_, R, pad in ((g.tn_grouped, narrow[0], Bt, 3), (g.tn_grouped_grad_b, A[..., :136], dCt, 8)):
+        ref = (product64 if call is g.tn_grouped else grad_b64)(A_, R, b)
+        room = torch.full((T, ref.shape[1] + pad), 3.5, dtype=dtype, device="cuda")
+        out = room[:, : ref.shape[1]]
+        call(A_, R, off, **{"C" if call is g.tn_grouped else "dBt": out})
+        g.gemm_poll_device_status()
+        assert bool((room[:, ref.shape[1]:] == 3.5).all())
+        owned = torch.zeros(T, dtype=torch.bool, device="cuda")
+        owned[b[0]:b[3]] = True
+        assert bool((out[~owned] == 3.5).all())
+        assert torch.equal(out[owned].isnan(), ref[owned].to(dtype).isnan())
+        finite = ~ref[owned].isnan()
+        assert torch.equal(out[owned][finite], ref[owned].to(dtype)[finite])
+
+
 def test_past_2_31_elements():
     """Weights, tokens and results of more than 2^31 elements: offsets in 64 bits."""
     M, K, E = 4096, 4096, 130                      # 2.18e9 weights
