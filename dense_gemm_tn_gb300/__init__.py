@@ -490,13 +490,24 @@ def f8e4m3_tn(A, Bt, scale_a, scale_b, C=None, stream=None):
 # Each helper checks its arguments in full, except that operands which are all
 # contiguous on the current device (the common case, and the one where a call is
 # short enough for the host's time to count) take a shorter way through the same
-# checks of types and shapes: measured on a GB300's host, 24 -> 14 us a call.
-def _half_type(dtype, name):
+# checks of types and shapes.  Measured on a GB300's host (a plain torch.add takes 7.9 us
+# there): tn_grouped_grad_a 24.9 -> 14.1 us a call.
+_torch = None          # the module, from the first helper call on
+_half_kinds = {}       # {dtype: GEMM_IN_...} of the 16-bit types
+
+
+def _load_torch():
+    global _torch
     import torch
-    if dtype == torch.bfloat16:
-        return GEMM_IN_BF16
-    if dtype == torch.float16:
-        return GEMM_IN_F16
+    _half_kinds.update({torch.float16: GEMM_IN_F16, torch.bfloat16: GEMM_IN_BF16})
+    _torch = torch
+    return torch
+
+
+def _half_type(dtype, name):
+    kind = _half_kinds.get(dtype)
+    if kind is not None:
+        return kind
     raise ValueError(f"{name} must be torch.float16 or torch.bfloat16, not {dtype}")
 
 
@@ -541,15 +552,14 @@ def _same_device(device, **tensors):
 def _launch_stream(index, stream):
     """The stream's handle (None: torch's current stream of that device)."""
     if stream is None:
-        import torch
-        return torch._C._cuda_getCurrentRawStream(index)
+        return _torch._C._cuda_getCurrentRawStream(index)
     return stream if isinstance(stream, int) else int(stream.cuda_stream)
 
 
 def _workspace(device, stream, n):
     """n bytes from torch's allocator that belong to the call's stream, so that
     they are used again only after the call's kernels."""
-    import torch
+    torch = _torch
     if stream is None:
         return torch.empty(n, dtype=torch.uint8, device=device)
     own = stream if not isinstance(stream, int) else torch.cuda.ExternalStream(stream, device=device)
@@ -557,21 +567,20 @@ def _workspace(device, stream, n):
         return torch.empty(n, dtype=torch.uint8, device=device)
 
 
-def _tensors(*operands):
-    import torch
+def _tensors(torch, *operands):
     for t in operands:
         if not isinstance(t, torch.Tensor):
             raise ValueError(f"the operands must be torch tensors, not {type(t).__name__}")
 
 
-def _plain(index, *tensors):
-    """Whether the tensors are contiguous on device `index`, the current one: their
-    strides are their shapes', and nothing is left to check but types and shapes."""
-    import torch
+def _plain(torch, *tensors):
+    """Whether the tensors are contiguous on the current device: their strides are
+    their shapes', and nothing is left to check but types and shapes."""
+    index = tensors[0].get_device()
     for t in tensors:
         if not t.is_contiguous() or t.get_device() != index:
             return False
-    return index is not None and torch._C._cuda_getDevice() == index
+    return index >= 0 and torch._C._cuda_getDevice() == index
 
 
 def _elsewhere(index):
@@ -585,14 +594,13 @@ def tn_grouped(A, Bt, offsets, C=None, stream=None):
     expert e: A (E, M, K), Bt (T, K), offsets (E + 1,) int32, all on one GPU;
     A, Bt and C (T, M) are all fp16 or all bf16, their rows contiguous.  Rows of
     no expert are not written."""
-    import torch
-    _tensors(A, Bt, offsets)
-    dtype, device = A.dtype, A.device
+    torch = _torch or _load_torch()
+    _tensors(torch, A, Bt, offsets)
+    dtype, device, sa, sb, so = A.dtype, A.device, A.shape, Bt.shape, offsets.shape
     kind = _half_type(dtype, "A")
-    if (C is None and Bt.dtype is dtype and offsets.dtype is torch.int32 and A.dim() == 3 and Bt.dim() == 2
-            and offsets.dim() == 1 and _plain(device.index, A, Bt, offsets)
-            and A.shape[2] == Bt.shape[1] > 0 and offsets.shape[0] == A.shape[0] + 1):
-        (E, M, K), T = A.shape, Bt.shape[0]
+    if (C is None and Bt.dtype is dtype and offsets.dtype is torch.int32 and len(sa) == 3 and len(sb) == 2
+            and len(so) == 1 and sa[2] == sb[1] > 0 and so[0] == sa[0] + 1 and _plain(torch, A, Bt, offsets)):
+        (E, M, K), T = sa, sb[0]
         lda = ldb = K
         stride_a = M * K
         C, ldc = torch.empty((T, M), dtype=dtype, device=device), max(M, 1)
@@ -618,14 +626,13 @@ def tn_grouped(A, Bt, offsets, C=None, stream=None):
 def tn_grouped_grad_b(A, dCt, offsets, dBt=None, stream=None):
     """The gradient of tn_grouped for Bt: dBt[t] = A[e]^T dC^T[t], with dCt (T, M)
     -> (T, K).  Rows of no expert are not written."""
-    import torch
-    _tensors(A, dCt, offsets)
-    dtype, device = A.dtype, A.device
+    torch = _torch or _load_torch()
+    _tensors(torch, A, dCt, offsets)
+    dtype, device, sa, sd, so = A.dtype, A.device, A.shape, dCt.shape, offsets.shape
     kind = _half_type(dtype, "A")
-    if (dBt is None and dCt.dtype is dtype and offsets.dtype is torch.int32 and A.dim() == 3 and dCt.dim() == 2
-            and offsets.dim() == 1 and _plain(device.index, A, dCt, offsets)
-            and A.shape[1] == dCt.shape[1] > 0 < A.shape[2] and offsets.shape[0] == A.shape[0] + 1):
-        (E, M, K), T = A.shape, dCt.shape[0]
+    if (dBt is None and dCt.dtype is dtype and offsets.dtype is torch.int32 and len(sa) == 3 and len(sd) == 2
+            and len(so) == 1 and sa[1] == sd[1] > 0 < sa[2] and so[0] == sa[0] + 1 and _plain(torch, A, dCt, offsets)):
+        (E, M, K), T = sa, sd[0]
         lda, stride_a, ldd = K, M * K, M
         dBt, ldb = torch.empty((T, K), dtype=dtype, device=device), K
     else:
@@ -651,26 +658,32 @@ def tn_grouped_grad_a(dCt, Bt, offsets, dA=None, stream=None):
     """The gradient of tn_grouped for A: dA[e] = sum over e's rows t of the outer
     products dC^T[t] Bt[t], with dCt (T, M) and Bt (T, K) -> (E, M, K); zeros for
     an expert without rows."""
-    import torch
-    _tensors(dCt, Bt, offsets)
-    if offsets.dim() != 1 or offsets.shape[0] < 1:
+    torch = _torch or _load_torch()
+    _tensors(torch, dCt, Bt, offsets)
+    dtype, device, sd, sb, so = dCt.dtype, dCt.device, dCt.shape, Bt.shape, offsets.shape
+    if len(so) != 1 or so[0] < 1:
         raise ValueError("offsets must be a 1-D tensor of experts + 1 row numbers")
-    if dCt.dim() != 2 or Bt.dim() != 2:
+    if len(sd) != 2 or len(sb) != 2:
         raise ValueError("dCt and Bt must be 2-D torch tensors")
-    E, device, (T, M), K = offsets.shape[0] - 1, dCt.device, dCt.shape, Bt.shape[1]
-    kind = _half_type(dCt.dtype, "dCt")
-    ldd, ldb = _tokens(dCt, dCt.dtype, M, "dCt"), _tokens(Bt, dCt.dtype, K, "Bt")
-    if Bt.shape[0] != T:
-        raise ValueError(f"dCt has {T} rows and Bt {Bt.shape[0]}")
-    _vector(offsets, torch.int32, E + 1, "offsets")
-    _same_device(device, Bt=Bt, offsets=offsets)
-    if _elsewhere(device.index):
-        with torch.cuda.device(device):
-            return tn_grouped_grad_a(dCt, Bt, offsets, dA, stream)
-    if dA is None:
-        dA = torch.empty((E, M, K), dtype=dCt.dtype, device=device)
-    ldda, stride_da = _experts(dA, dCt.dtype, "dA", (E, M, K))
-    _same_device(device, dA=dA)
+    E, (T, M), K = so[0] - 1, sd, sb[1]
+    kind = _half_type(dtype, "dCt")
+    if (dA is None and Bt.dtype is dtype and offsets.dtype is torch.int32 and sb[0] == T and M > 0 < K
+            and _plain(torch, dCt, Bt, offsets)):
+        ldd, ldb, ldda, stride_da = M, K, K, M * K
+        dA = torch.empty((E, M, K), dtype=dtype, device=device)
+    else:
+        ldd, ldb = _tokens(dCt, dtype, M, "dCt"), _tokens(Bt, dtype, K, "Bt")
+        if sb[0] != T:
+            raise ValueError(f"dCt has {T} rows and Bt {sb[0]}")
+        _vector(offsets, torch.int32, E + 1, "offsets")
+        _same_device(device, Bt=Bt, offsets=offsets)
+        if _elsewhere(device.index):
+            with torch.cuda.device(device):
+                return tn_grouped_grad_a(dCt, Bt, offsets, dA, stream)
+        if dA is None:
+            dA = torch.empty((E, M, K), dtype=dtype, device=device)
+        ldda, stride_da = _experts(dA, dtype, "dA", (E, M, K))
+        _same_device(device, dA=dA)
     d, b = dCt.data_ptr(), Bt.data_ptr()
     n = calls.gemm_grouped_workspace(GEMM_GROUPED_GRAD_A, E, M, K, T, d, ldd, 0, b, ldb)
     held = _workspace(device, stream, n) if n > 0 else None
@@ -684,14 +697,14 @@ def i8_tn(A, Bt, scale_a, scale_b, C=None, dtype=None, stream=None):
     """C^T[n, m] = scale_a[m] scale_b[n] sum_k A[m, k] Bt[n, k]: A (M, K) and Bt
     (N, K) int8, scale_a (M,) and scale_b (N,) fp32 -> (N, M) of `dtype`
     (torch.float16, unless C or dtype says torch.bfloat16)."""
-    import torch
-    _tensors(A, Bt, scale_a, scale_b)
-    dtype, device = dtype or (torch.float16 if C is None else C.dtype), A.device
+    torch = _torch or _load_torch()
+    _tensors(torch, A, Bt, scale_a, scale_b)
+    dtype, device, sa, sb = dtype or (torch.float16 if C is None else C.dtype), A.device, A.shape, Bt.shape
     kind = _half_type(dtype, "dtype")
     if (C is None and A.dtype is torch.int8 is Bt.dtype and scale_a.dtype is torch.float32 is scale_b.dtype
-            and A.dim() == 2 == Bt.dim() and _plain(device.index, A, Bt, scale_a, scale_b)
-            and A.shape[1] == Bt.shape[1] > 0 and scale_a.shape == A.shape[:1] and scale_b.shape == Bt.shape[:1]):
-        (M, K), N = A.shape, Bt.shape[0]
+            and len(sa) == 2 == len(sb) and sa[1] == sb[1] > 0 and scale_a.shape == (sa[0],) and scale_b.shape == (sb[0],)
+            and _plain(torch, A, Bt, scale_a, scale_b)):
+        (M, K), N = sa, sb[0]
         lda = ldb = K
         C, ldc = torch.empty((N, M), dtype=dtype, device=device), max(M, 1)
     else:
@@ -731,15 +744,15 @@ def _i8_grouped_operands(A, Bt, scale_a, scale_b, offsets, C, dtype):
 def i8_tn_grouped(A, Bt, scale_a, scale_b, offsets, C=None, dtype=None, stream=None):
     """i8_tn grouped by expert as in tn_grouped: A (E, M, K) and Bt (T, K) int8,
     scale_a (E, M) and scale_b (T,) fp32 -> (T, M) of `dtype`."""
-    import torch
-    _tensors(A, Bt, scale_a, scale_b, offsets)
-    dtype, device = dtype or (torch.float16 if C is None else C.dtype), A.device
+    torch = _torch or _load_torch()
+    _tensors(torch, A, Bt, scale_a, scale_b, offsets)
+    dtype, device, sa, sb = dtype or (torch.float16 if C is None else C.dtype), A.device, A.shape, Bt.shape
     kind = _half_type(dtype, "dtype")
     if (C is None and A.dtype is torch.int8 is Bt.dtype and scale_a.dtype is torch.float32 is scale_b.dtype
-            and offsets.dtype is torch.int32 and A.dim() == 3 and Bt.dim() == 2 and offsets.dim() == 1
-            and _plain(device.index, A, Bt, scale_a, scale_b, offsets) and A.shape[2] == Bt.shape[1] > 0 < A.shape[1]
-            and scale_a.shape == A.shape[:2] and scale_b.shape == Bt.shape[:1] and offsets.shape[0] == A.shape[0] + 1):
-        (E, M, K), T = A.shape, Bt.shape[0]
+            and offsets.dtype is torch.int32 and len(sa) == 3 and len(sb) == 2 and sa[2] == sb[1] > 0 < sa[1]
+            and scale_a.shape == sa[:2] and scale_b.shape == (sb[0],) and offsets.shape == (sa[0] + 1,)
+            and _plain(torch, A, Bt, scale_a, scale_b, offsets)):
+        (E, M, K), T = sa, sb[0]
         lda = ldb = K
         stride_a = M * K
         C, ldc = torch.empty((T, M), dtype=dtype, device=device), M
@@ -762,17 +775,16 @@ def quantize_i8_rows(x, stream=None):
     """x: a 2-D float32 / float16 / bfloat16 CUDA tensor with unit column stride.
     Returns (int8 codes of x's shape, scale as a float32 tensor of its rows): the
     operands of i8_tn, for activations (tokens) and weights (channels) alike."""
-    import torch
+    torch = _torch or _load_torch()
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise ValueError("x must be a 2-D float32/float16/bfloat16 tensor")
     dtype, device = x.dtype, x.device
-    kind = (GEMM_IN_BF16 if dtype is torch.bfloat16 else GEMM_IN_F16 if dtype is torch.float16 else
-            GEMM_IN_F32 if dtype is torch.float32 else None)
+    kind = GEMM_IN_F32 if dtype is torch.float32 else _half_kinds.get(dtype)
     if kind is None:
         raise ValueError("x must be a 2-D float32/float16/bfloat16 tensor")
     shape = x.shape
     rows, cols = shape
-    if cols > 0 and _plain(device.index, x):
+    if cols > 0 and _plain(torch, x):
         ldx = cols
     else:
         ldx = _rows(x, dtype, "x")

@@ -20,7 +20,7 @@
 //
 // Measured on GB300: 16 experts of 4096 x 2048, 515 rows 32.0 us (4.4 TB/s; 512 tiles are
 // 3.4 waves and take the time of 4); 8192 x 16 x 2048 9.0 us replayed from a graph, where
-// start, epilogue and the join of two half sums are some 6 of them (11.1 us called from
+// start, epilogue and the join of two half sums are some 6 of them (11.0 us called from
 // Python, whose host time bounds it); 1024 x 16 x 8192 10.3 us on 64 CTAs.
 #pragma once
 
