@@ -141,6 +141,11 @@ struct GroupedTile {
     int32_t red;            // terms of the sum
 };
 
+// Tiles of up to r rows that `rows` rows make.  (rows + r - 1 may pass 2^31 - 1.)
+__host__ __device__ constexpr int32_t row_tiles(int32_t rows, int32_t r) { return rows > 0 ? (rows - 1) / r + 1 : 0; }
+static_assert(row_tiles(0x7FFFFF00, 512) == 0x400000 && row_tiles(512, 512) == 1 && row_tiles(0, 512) == 0,
+              "up to 2^31 - 256 rows, the most that a call may have");
+
 template <int kOp, int kRows, int kHalfRows, int kTileL, int kGran>
 struct GroupedWalk {
     const int32_t *start, *before;      // shared memory
@@ -154,7 +159,7 @@ struct GroupedWalk {
         GroupedTile t;
         const int32_t group_rows = start[e + 1] - start[e];
         const int32_t rows = kOp == kGrGradA ? r_extent : group_rows;
-        const int32_t tiles = (rows + kRows - 1) / kRows;
+        const int32_t tiles = row_tiles(rows, kRows);
         // the rows in steps of kGran, spread evenly: the first `more` tiles have one more
         const int32_t steps = (rows + kGran - 1) / kGran, each = steps / tiles, more = steps - each * tiles;
         int64_t tr, tl;
@@ -249,7 +254,7 @@ __device__ __forceinline__ void grouped_tables(const GroupedParams &p, int32_t l
         int32_t sum = 0;
         for (int32_t i = i0; i < i1 && i < E; ++i) {
             const int32_t rows = kOp == kGrGradA ? p.r_extent : start[i + 1] - start[i];
-            sum += (rows + kRows - 1) / kRows * l_tiles;
+            sum += row_tiles(rows, kRows) * l_tiles;
         }
         int32_t acc = sum;
         for (int d = 1; d < 32; d *= 2) {
@@ -261,7 +266,7 @@ __device__ __forceinline__ void grouped_tables(const GroupedParams &p, int32_t l
             before[i] = acc;
             if (i < E) {
                 const int32_t rows = kOp == kGrGradA ? p.r_extent : start[i + 1] - start[i];
-                acc += (rows + kRows - 1) / kRows * l_tiles;
+                acc += row_tiles(rows, kRows) * l_tiles;
             }
         }
     }

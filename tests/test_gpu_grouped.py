@@ -332,6 +332,17 @@ def test_past_2_31_elements():
     assert torch.equal(dA[E - 1], (want.double().t() @ Bt[-300:].double()).half()) and float(dA[E - 2].abs().max()) == 0
 
 
+@pytest.mark.parametrize("M", [2 ** 31 - 256, 2 ** 31 - 512])
+def test_weight_gradient_of_the_most_rows(M):
+    """As many rows of dA as a call may have: their number of tiles in 32 bits."""
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    dCt = torch.randint(-3, 4, (1, M), generator=gen, device="cuda", dtype=torch.int8).half()
+    dA = torch.full((1, M, 1), 9.0, dtype=torch.float16, device="cuda")
+    g.tn_grouped_grad_a(dCt, torch.full((1, 1), 2.0, dtype=torch.float16, device="cuda"), offsets_of([1]), dA=dA)
+    g.gemm_poll_device_status()
+    assert torch.equal(dA.view(-1), dCt.view(-1) * 2)
+
+
 # ------------------------------------------------------------------ streams, graphs, threads
 def small_case(seed, dtype=torch.bfloat16):
     counts = [40, 0, 130, 9]
