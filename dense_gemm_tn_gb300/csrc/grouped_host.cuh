@@ -585,9 +585,9 @@ gemm_status_t launch_quant_rows(DeviceState &dev, qz::QuantRowsParams &prm, cuda
     void (*kernel)(qz::QuantRowsParams);
     int threads = qz::kRowThreads, rows_per_cta = 1;
     // a row's codes are staged in shared memory where rows are not aligned (more
-    // than 48 KiB of them: the kernel for long rows, which does not stage)
+    // than it has room for: the kernel for long rows, which does not stage)
     const int64_t staging = aligned ? 0 : (windows * kVec + 4 + 15) / 16 * 16;
-    const bool long_rows = windows > 1024 * 8 || staging > 49152;
+    const bool long_rows = windows > 1024 * 8 || staging > qz::kMaxStaging;
     prm.staging_bytes = long_rows ? 0 : static_cast<int32_t>(staging);
     if (long_rows) {
         kernel = qz::quant_long_rows_kernel<kIn>;

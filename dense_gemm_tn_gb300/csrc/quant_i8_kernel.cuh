@@ -27,6 +27,9 @@ namespace qz {
 
 constexpr int kRowThreads = 256;
 constexpr int kLongThreads = 512;
+// Shared memory that a launch has without asking for more, less the row kernels'
+// own (the largest team's 32 maxima): what is left to stage a row's codes in.
+constexpr int kMaxStaging = 49152 - 32 * 4;
 
 struct QuantRowsParams {
     const void *x;            // rows x cols, row stride ldx elements

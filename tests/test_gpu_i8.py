@@ -330,6 +330,19 @@ def test_quantise_strides_and_bases(rows, cols, ld, base, dtype):
         assert bool((out == 55).all())               # nothing beside the codes was written
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16, torch.float32], ids=["f16", "bf16", "f32"])
+@pytest.mark.parametrize("cols", [16383, 32765, 49000, 49001, 49007, 49008, 49009, 49100, 49135, 49136, 49137, 49153, 65535])
+def test_quantise_unaligned_rows_about_the_most_that_is_staged(cols, dtype):
+    """Rows that start on no 16-byte boundary, either side of the lengths where the
+    staged codes outgrow shared memory and one kernel follows another."""
+    gen = torch.Generator(device="cuda").manual_seed(cols)
+    room = torch.randn(3 * (cols + 1), generator=gen, device="cuda").to(dtype)
+    for x in (room[1:].as_strided((3, cols), (cols + 1, 1)), room[:2 * cols].view(2, cols), room[1:1 + cols].view(1, cols)):
+        q, s = g.quantize_i8_rows(x)
+        want, scale = rows64(x)
+        assert torch.equal(q.double(), want) and torch.equal(s, scale.float())
+
+
 def test_quantise_empty_and_dependent_launches():
     q, s = g.quantize_i8_rows(torch.zeros(5, 0, device="cuda"))
     assert q.shape == (5, 0) and bool((s == 0).all())
