@@ -483,7 +483,9 @@ gemm_status_t run_grouped(const GroupedCall &c)
     const int64_t red = grad_a ? c.T : (grad_b ? c.M : c.K);
     if (!c.out) return fail(GEMM_ERR_INVALID_ARG, "%s: the result is NULL", name);
     if (reinterpret_cast<uintptr_t>(c.out) % 2) return fail(GEMM_ERR_INVALID_ARG, "%s: the result is not 2-byte aligned", name);
-    if (grad_a && c.E > 1 && c.stride_o < (c.M - 1) * c.ldo + c.K && c.ldo < (c.E - 1) * c.stride_o + c.K)
+    // the experts' matrices lie one after the other, or row by row beside each other
+    if (grad_a && c.E > 1 && c.stride_o < (c.M - 1) * c.ldo + c.K &&
+        (c.stride_o < c.K || c.ldo < (c.E - 1) * c.stride_o + c.K))
         return fail(GEMM_ERR_INVALID_ARG, "%s: the experts' results overlap", name);
     const uintptr_t misfit = i8 ? 0 : 1;
     if (red > 0) {

@@ -174,3 +174,22 @@ def test_rows_are_cut_into_even_tiles_that_cover_them():
             starts = [(r * each + min(r, more)) * step for r in range(tiles)]
             assert max(heights) <= largest and starts[-1] < rows <= starts[-1] + heights[-1]
             assert all(a + h == b for a, h, b in zip(starts, heights, starts[1:]))
+
+
+@pytest.mark.parametrize("lib", BINDINGS, ids=lambda b: getattr(b, "__name__", "ctypes"))
+@pytest.mark.parametrize("E,M,K,ldda,stride,fits", [
+    (2, 16, 8, 8, 128, True), (2, 16, 8, 8, 127, False), (3, 16, 8, 24, 8, True), (3, 16, 8, 23, 8, False),
+    (2, 16, 8, 8, 0, False), (2, 16, 8, 4096, 0, False), (2, 16, 8, 4096, 4, False), (2, 16, 8, 4096, 7, False),
+    (2, 1, 8, 8, 8, True), (2, 1, 8, 8, 7, False), (2, 1, 8, 8, 0, False), (2, 1, 8, 4096, 0, False),
+    (1, 16, 8, 8, 0, True)])
+def test_weight_gradients_that_overlap_are_refused(lib, E, M, K, ldda, stride, fits):
+    """Two experts' dA may alternate row by row, but no element may belong to both."""
+    at = {(e * stride + m * ldda + k) for e in range(E) for m in range(M) for k in range(K)}
+    assert (len(at) == E * M * K) == fits
+    if fits and torch.cuda.is_available():
+        return                                     # (no pointer here may reach a kernel)
+    status = grad_a(lib, E=E, M=M, K=K, lddc=max(M, 1), ldda=ldda, stride_da=stride, ws=5 * P, n=1 << 20)
+    if fits:
+        assert status == g.GEMM_ERR_CUDA           # (past the checks: there is no device)
+    else:
+        assert status == g.GEMM_ERR_INVALID_ARG and "overlap" in g.last_error()
