@@ -556,14 +556,22 @@ def _launch_stream(index, stream):
     return stream if isinstance(stream, int) else int(stream.cuda_stream)
 
 
+def _torch_stream(device, stream):
+    """The torch stream of a `stream` argument (not None).  Handle 0 is the default
+    stream: torch.cuda.ExternalStream would make it one of torch's pool."""
+    import torch
+    if not isinstance(stream, int):
+        return stream
+    return torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
+
+
 def _workspace(device, stream, n):
     """n bytes from torch's allocator that belong to the call's stream, so that
     they are used again only after the call's kernels."""
     torch = _torch
     if stream is None:
         return torch.empty(n, dtype=torch.uint8, device=device)
-    own = stream if not isinstance(stream, int) else torch.cuda.ExternalStream(stream, device=device)
-    with torch.cuda.stream(own):
+    with torch.cuda.stream(_torch_stream(device, stream)):
         return torch.empty(n, dtype=torch.uint8, device=device)
 
 

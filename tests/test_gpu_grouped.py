@@ -382,6 +382,25 @@ def test_other_streams(as_int):
     assert all(torch.equal(x, y) for x, y in zip(inside, want))
 
 
+@pytest.mark.parametrize("kind", ["none", "object", "handle", "default_object", "default_handle"])
+def test_the_workspace_belongs_to_the_calls_stream(kind):
+    """A freed block is handed out again to its own stream alone, so the workspace's
+    comes back for that stream.  (The default stream's handle is 0.)"""
+    g.quantize_i8_rows(torch.zeros(1, 1, device="cuda"))          # (the helpers' torch is looked up by their first call)
+    device, side, default = torch.device("cuda", 0), torch.cuda.Stream(), torch.cuda.default_stream()
+    stream, own = {"none": (None, default), "object": (side, side), "handle": (side.cuda_stream, side),
+                   "default_object": (default, default), "default_handle": (default.cuda_stream, default)}[kind]
+    n = 3 << 20
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    ws = g._workspace(device, stream, n)
+    at = ws.data_ptr()
+    del ws
+    with torch.cuda.stream(own):
+        again = torch.empty(n, dtype=torch.uint8, device=device)
+    assert again.data_ptr() == at
+
+
 def test_captured_replayed_and_two_graphs_at_once():
     cases = [small_case(1), small_case(50)]
     for c in cases:
