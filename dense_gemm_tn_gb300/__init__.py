@@ -33,6 +33,7 @@ Convenience wrappers over torch tensors in TN storage:
     i8_tn(A (M,K) int8, Bt (N,K) int8, scale_a (M,), scale_b (N,), C=None) -> (N, M); i8_tn_grouped
     quantize_i8_rows(x (rows, cols)) -> (int8 codes, scale (rows,))
 The (N, M) row-major result IS the column-major M x N matrix C with ldc = M.
+With a `stream`, new results are that stream's memory, as under torch.cuda.stream.
 """
 from __future__ import annotations
 
@@ -394,10 +395,32 @@ def _operands(A, Bt, dtype):
     return M, N, K, lda, ldb
 
 
-def _output(C, M, N, dtype, device):
+def _torch_stream(device, stream):
+    """The torch stream of a `stream` argument (not None).  Handle 0 is the default
+    stream: torch.cuda.ExternalStream would make it one of torch's pool."""
     import torch
+    if not isinstance(stream, int):
+        return stream
+    return torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
+
+
+def _empty(shape, dtype, device, stream):
+    """A result's tensor.  On a stream of the caller's its memory is that stream's, as
+    under torch.cuda.stream(stream): the current stream may still have kernels in hand
+    that use what its own freed blocks held.  Once released it waits for the current
+    stream as well, whose kernels may read the result."""
+    torch = _torch or _load_torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(_torch_stream(device, stream)):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
+def _output(C, M, N, dtype, device, stream=None):
     if C is None:
-        C = torch.empty((N, M), dtype=dtype, device=device)
+        C = _empty((N, M), dtype, device, stream)
     ldc = _rows(C, dtype, "C", (N, M))
     if C.device != device:
         raise ValueError(f"C is on {C.device}, the operands on {device}")
@@ -416,7 +439,7 @@ def f16_tn(A, Bt, C=None, stream=None):
     A, Bt (and C) are fp16 CUDA tensors whose rows are contiguous."""
     import torch
     M, N, K, lda, ldb = _operands(A, Bt, torch.float16)
-    C, ldc = _output(C, M, N, torch.float16, A.device)
+    C, ldc = _output(C, M, N, torch.float16, A.device, stream)
     with _on(A.device):
         gemm_f16_tn(M, N, K, A, lda, Bt, ldb, C, ldc, stream)
     return C
@@ -427,9 +450,8 @@ def f16_tn_softmax_stats(Q, Kmat, scale, C=None, stream=None):
     tensor, row_max (M,), row_sum (M,)): S = scale * Q Kmat^T."""
     import torch
     M, N, K, lda, ldb = _operands(Q, Kmat, torch.float16)
-    C, ldc = _output(C, M, N, torch.float16, Q.device)
-    row_max = torch.empty(M, dtype=torch.float32, device=Q.device)
-    row_sum = torch.empty(M, dtype=torch.float32, device=Q.device)
+    C, ldc = _output(C, M, N, torch.float16, Q.device, stream)
+    row_max, row_sum = (_empty((M,), torch.float32, Q.device, stream) for _ in range(2))
     with _on(Q.device):
         gemm_f16_tn_softmax_stats(M, N, K, Q, lda, Kmat, ldb, C, ldc, scale, row_max, row_sum, stream)
     return C, row_max, row_sum
@@ -446,8 +468,8 @@ def quantize_e4m3(x, stream=None):
     if not x.is_cuda:
         raise ValueError("x must be a CUDA tensor")
     rows, cols = x.shape
-    q = torch.empty((rows, cols), dtype=torch.uint8, device=x.device)
-    scale = torch.empty(1, dtype=torch.float32, device=x.device)
+    q = _empty((rows, cols), torch.uint8, x.device, stream)
+    scale = _empty((1,), torch.float32, x.device, stream)
     ld = max(cols, 1)
     with _on(x.device):
         gemm_quantize_e4m3(x, types[x.dtype], rows, cols, x.stride(0) if rows > 1 else ld, q, ld, scale, stream)
@@ -469,7 +491,7 @@ def f8e4m3_tn_dscale(A, Bt, scale_a, scale_b, C=None, stream=None):
     _scale_tensor(scale_b, "scale_b")
     if scale_a.device != A.device or scale_b.device != A.device:
         raise ValueError("scale_a and scale_b must be on the operands' device")
-    C, ldc = _output(C, M, N, torch.bfloat16, A.device)
+    C, ldc = _output(C, M, N, torch.bfloat16, A.device, stream)
     with _on(A.device):
         gemm_f8e4m3_tn_dscale(M, N, K, A, lda, Bt, ldb, C, ldc, scale_a, scale_b, stream)
     return C
@@ -480,7 +502,7 @@ def f8e4m3_tn(A, Bt, scale_a, scale_b, C=None, stream=None):
     (M, K) and Bt (N, K); the scales are Python floats."""
     import torch
     M, N, K, lda, ldb = _operands(A, Bt, torch.uint8)
-    C, ldc = _output(C, M, N, torch.bfloat16, A.device)
+    C, ldc = _output(C, M, N, torch.bfloat16, A.device, stream)
     with _on(A.device):
         gemm_f8e4m3_tn(M, N, K, A, lda, Bt, ldb, C, ldc, float(scale_a), float(scale_b), stream)
     return C
@@ -556,15 +578,6 @@ def _launch_stream(index, stream):
     return stream if isinstance(stream, int) else int(stream.cuda_stream)
 
 
-def _torch_stream(device, stream):
-    """The torch stream of a `stream` argument (not None).  Handle 0 is the default
-    stream: torch.cuda.ExternalStream would make it one of torch's pool."""
-    import torch
-    if not isinstance(stream, int):
-        return stream
-    return torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
-
-
 def _workspace(device, stream, n):
     """n bytes from torch's allocator that belong to the call's stream, so that
     they are used again only after the call's kernels."""
@@ -611,7 +624,7 @@ def tn_grouped(A, Bt, offsets, C=None, stream=None):
         (E, M, K), T = sa, sb[0]
         lda = ldb = K
         stride_a = M * K
-        C, ldc = torch.empty((T, M), dtype=dtype, device=device), max(M, 1)
+        C, ldc = _empty((T, M), dtype, device, stream), max(M, 1)
     else:
         lda, stride_a = _experts(A, dtype, "A")
         E, M, K = A.shape
@@ -621,7 +634,7 @@ def tn_grouped(A, Bt, offsets, C=None, stream=None):
         if _elsewhere(device.index):
             with torch.cuda.device(device):
                 return tn_grouped(A, Bt, offsets, C, stream)
-        C, ldc = _output(C, M, T, dtype, device)
+        C, ldc = _output(C, M, T, dtype, device, stream)
     a, b = A.data_ptr(), Bt.data_ptr()
     n = calls.gemm_grouped_workspace(GEMM_GROUPED_PRODUCT, E, M, K, T, a, lda, stride_a, b, ldb)
     held = _workspace(device, stream, n) if n > 0 else None
@@ -642,7 +655,7 @@ def tn_grouped_grad_b(A, dCt, offsets, dBt=None, stream=None):
             and len(so) == 1 and sa[1] == sd[1] > 0 < sa[2] and so[0] == sa[0] + 1 and _plain(torch, A, dCt, offsets)):
         (E, M, K), T = sa, sd[0]
         lda, stride_a, ldd = K, M * K, M
-        dBt, ldb = torch.empty((T, K), dtype=dtype, device=device), K
+        dBt, ldb = _empty((T, K), dtype, device, stream), K
     else:
         lda, stride_a = _experts(A, dtype, "A")
         E, M, K = A.shape
@@ -652,7 +665,7 @@ def tn_grouped_grad_b(A, dCt, offsets, dBt=None, stream=None):
         if _elsewhere(device.index):
             with torch.cuda.device(device):
                 return tn_grouped_grad_b(A, dCt, offsets, dBt, stream)
-        dBt, ldb = _output(dBt, K, T, dtype, device)
+        dBt, ldb = _output(dBt, K, T, dtype, device, stream)
     a, d = A.data_ptr(), dCt.data_ptr()
     n = calls.gemm_grouped_workspace(GEMM_GROUPED_GRAD_B, E, M, K, T, a, lda, stride_a, d, ldd)
     held = _workspace(device, stream, n) if n > 0 else None
@@ -678,7 +691,7 @@ def tn_grouped_grad_a(dCt, Bt, offsets, dA=None, stream=None):
     if (dA is None and Bt.dtype is dtype and offsets.dtype is torch.int32 and sb[0] == T and M > 0 < K
             and _plain(torch, dCt, Bt, offsets)):
         ldd, ldb, ldda, stride_da = M, K, K, M * K
-        dA = torch.empty((E, M, K), dtype=dtype, device=device)
+        dA = _empty((E, M, K), dtype, device, stream)
     else:
         ldd, ldb = _tokens(dCt, dtype, M, "dCt"), _tokens(Bt, dtype, K, "Bt")
         if sb[0] != T:
@@ -689,7 +702,7 @@ def tn_grouped_grad_a(dCt, Bt, offsets, dA=None, stream=None):
             with torch.cuda.device(device):
                 return tn_grouped_grad_a(dCt, Bt, offsets, dA, stream)
         if dA is None:
-            dA = torch.empty((E, M, K), dtype=dtype, device=device)
+            dA = _empty((E, M, K), dtype, device, stream)
         ldda, stride_da = _experts(dA, dtype, "dA", (E, M, K))
         _same_device(device, dA=dA)
     d, b = dCt.data_ptr(), Bt.data_ptr()
@@ -714,7 +727,7 @@ def i8_tn(A, Bt, scale_a, scale_b, C=None, dtype=None, stream=None):
             and _plain(torch, A, Bt, scale_a, scale_b)):
         (M, K), N = sa, sb[0]
         lda = ldb = K
-        C, ldc = torch.empty((N, M), dtype=dtype, device=device), max(M, 1)
+        C, ldc = _empty((N, M), dtype, device, stream), max(M, 1)
     else:
         M, N, K, lda, ldb = _operands(A, Bt, torch.int8)
         _vector(scale_a, torch.float32, M, "scale_a")
@@ -723,7 +736,7 @@ def i8_tn(A, Bt, scale_a, scale_b, C=None, dtype=None, stream=None):
         if _elsewhere(device.index):
             with torch.cuda.device(device):
                 return i8_tn(A, Bt, scale_a, scale_b, C, dtype, stream)
-        C, ldc = _output(C, M, N, dtype, device)
+        C, ldc = _output(C, M, N, dtype, device, stream)
     a, b = A.data_ptr(), Bt.data_ptr()
     n = calls.gemm_grouped_workspace(GEMM_GROUPED_I8, 1, M, K, N, a, lda, 0, b, ldb)
     held = _workspace(device, stream, n) if n > 0 else None
@@ -733,7 +746,7 @@ def i8_tn(A, Bt, scale_a, scale_b, C=None, dtype=None, stream=None):
     return C
 
 
-def _i8_grouped_operands(A, Bt, scale_a, scale_b, offsets, C, dtype):
+def _i8_grouped_operands(A, Bt, scale_a, scale_b, offsets, C, dtype, stream):
     """(lda, stride_a, ldb, ldc, C) of i8_tn_grouped's operands, all checked."""
     import torch
     lda, stride_a = _experts(A, torch.int8, "A")
@@ -745,7 +758,7 @@ def _i8_grouped_operands(A, Bt, scale_a, scale_b, offsets, C, dtype):
     _vector(scale_b, torch.float32, T, "scale_b")
     _vector(offsets, torch.int32, E + 1, "offsets")
     _same_device(A.device, Bt=Bt, scale_a=scale_a, scale_b=scale_b, offsets=offsets)
-    C, ldc = _output(C, M, T, dtype, A.device)
+    C, ldc = _output(C, M, T, dtype, A.device, stream)
     return lda, stride_a, ldb, ldc, C
 
 
@@ -763,9 +776,9 @@ def i8_tn_grouped(A, Bt, scale_a, scale_b, offsets, C=None, dtype=None, stream=N
         (E, M, K), T = sa, sb[0]
         lda = ldb = K
         stride_a = M * K
-        C, ldc = torch.empty((T, M), dtype=dtype, device=device), M
+        C, ldc = _empty((T, M), dtype, device, stream), M
     else:
-        lda, stride_a, ldb, ldc, C = _i8_grouped_operands(A, Bt, scale_a, scale_b, offsets, C, dtype)
+        lda, stride_a, ldb, ldc, C = _i8_grouped_operands(A, Bt, scale_a, scale_b, offsets, C, dtype, stream)
         (E, M, K), T = A.shape, Bt.shape[0]
         if _elsewhere(device.index):
             with torch.cuda.device(device):
@@ -799,8 +812,8 @@ def quantize_i8_rows(x, stream=None):
         if _elsewhere(device.index):
             with torch.cuda.device(device):
                 return quantize_i8_rows(x, stream)
-    q = torch.empty(shape, dtype=torch.int8, device=device)
-    scale = torch.empty(rows, dtype=torch.float32, device=device)
+    q = _empty(shape, torch.int8, device, stream)
+    scale = _empty((rows,), torch.float32, device, stream)
     _check(calls.gemm_quantize_i8_rows(x.data_ptr(), kind, rows, cols, ldx, q.data_ptr(), max(cols, 1), scale.data_ptr(),
                                        _launch_stream(device.index, stream)))
     return q, scale
