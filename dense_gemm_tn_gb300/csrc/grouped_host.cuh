@@ -357,7 +357,7 @@ gemm_status_t launch_i8_pair(const GroupedCall &c, DeviceState &dev, tn::Grouped
     attr[1].val.clusterDim.x = 2;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
-    cfg.blockDim = dim3(tn::kI8Threads, 1, 1);
+    cfg.blockDim = dim3(tn::kIpThreads, 1, 1);
     cfg.dynamicSmemBytes = tn::kIpSmemBytes;
     int slots;
     {
@@ -366,6 +366,11 @@ gemm_status_t launch_i8_pair(const GroupedCall &c, DeviceState &dev, tn::Grouped
         if (n == 0) {
             cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, tn::kIpSmemBytes);
             if (e != cudaSuccess) return fail(GEMM_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+            // (with fewer registers its epilogue would wait for more than there are)
+            cudaFuncAttributes fa;
+            e = cudaFuncGetAttributes(&fa, kernel);
+            if (e != cudaSuccess || fa.numRegs < tn::kIpLaunchRegs)
+                return fail(GEMM_ERR_CUDA, "%s: the kernel was compiled for fewer registers than it shares out", c.name);
             cfg.attrs = attr + 1;
             cfg.numAttrs = 1;
             cfg.gridDim = dim3(2 * (dev.sms / 2), 1, 1);

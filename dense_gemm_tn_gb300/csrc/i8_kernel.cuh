@@ -40,38 +40,127 @@ constexpr int kI8Stages8 = 6;
 constexpr int kI8HalfBytes = kI8Rows * 128;                  // 64 terms of R as f16
 constexpr int kI8Stage16Bytes = 2 * kI8HalfBytes;
 constexpr int kI8Stages16 = 2;                               // one per team
-// TMEM columns: two accumulators, then the two f16 stages of L (two terms a column)
+// TMEM columns: two accumulators, the two f16 stages of L (two terms a column), and
+// the sums of runs
 constexpr uint32_t kI8ACol0 = 2 * kI8Rows, kI8ACols = kI8Block / 2;
-constexpr uint32_t kI8TmemCols = kI8ACol0 + kI8Stages16 * kI8ACols;
-static_assert(kI8TmemCols == 256, "a power of two");
+constexpr uint32_t kI8SumCol0 = kI8ACol0 + kI8Stages16 * kI8ACols;
+constexpr uint32_t kI8TmemCols = 512;
+static_assert(kI8SumCol0 + kI8Rows <= kI8TmemCols, "the TMEM columns of an SM");
 // full8[S8], empty8[S8], full16[S16], empty16[S16], accfull[2], accempty[2], drain, never
 constexpr int kI8Barriers = 2 * kI8Stages8 + 2 * kI8Stages16 + 6;
 constexpr int kI8SmemBytes = 1024 /* alignment slack */ + kI8Stages8 * kI8Stage8Bytes + kI8Stages16 * kI8Stage16Bytes +
                              kI8EpiWarps * kGrStageBytes + kI8Barriers * 8 + 32 + 2 * (kGrMaxExperts + 8) * 4;
 static_assert(kI8SmemBytes <= 232448, "exceeds the 227 KiB shared memory of one CTA");
 
+// A tensor core's FP32 sum of 8-bit products is exact while it stays within 2^24,
+// which 1024 terms of at most 2^14 each do not leave.  So an accumulator takes a run
+// of that many terms and no more: the epilogue adds it to the tile's sum, an integer,
+// while the MMAs of the next run go on in the other accumulator.  kI8MaxExact terms
+// stay in 32 bits.  The runs of a longer sum are rounded to whole units of 2^s, s > 0,
+// so that it does, 2^s being less than a 32768th of the number of terms.
+//
+// Measured on GB300 against one accumulator for the whole sum, which was off by hundreds
+// where large parts cancel: single CTAs 8192 x 16 x 2048 and 1024 x 16 x 8192 no
+// difference, 4096 x 192 x 8192 29.8 -> 30.9 us; pairs 8192 x 4096 x 8192 312 -> 323,
+// 8 experts of 4096 x 2048 with 4096 rows 57.4 -> 62.2, sums of one run (K = 1024)
+// 51.1 -> 53.2.  What it costs there is the widening warps' share of the SM, which
+// have no time to spare.  (Sums kept in floats until one comes to 2^24, read with
+// 32-lane loads, or held by twelve warps instead of eight were all slower.)
+constexpr int kI8Run = 1024 / kI8Block;                      // stages
+constexpr int32_t kI8MaxExact = 131071;                      // * 2^14 < 2^31
+
+// 2^-s for a sum of `red` terms.
+__device__ __forceinline__ float sum_unit(int32_t red)
+{
+    int s = 0;
+    if (red > kI8MaxExact)
+        while (red >> s > 65536) ++s;
+    return __uint_as_float(static_cast<uint32_t>(127 - s) << 23);
+}
+
+// A piece of a run's sums (floats) as integers, and of a tile's sum as floats.
+__device__ __forceinline__ void piece_to_ints(uint32_t (&v)[2][16], float unit)
+{
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[h][i] = static_cast<uint32_t>(__float2int_rn(__uint_as_float(v[h][i]) * unit));
+}
+
+__device__ __forceinline__ void piece_to_floats(uint32_t (&v)[2][16], float unit)
+{
+    const float back = 1.0f / unit;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[h][i] = __float_as_uint(__int2float_rn(static_cast<int32_t>(v[h][i])) * back);
+}
+
+// What the CTAs of a cluster left of their parts of a piece at `addr` of their rings,
+// added up.
+__device__ __forceinline__ void join_piece(const SplitSum &parts, uint32_t addr, uint32_t (&v)[2][16])
+{
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[h][i] = 0u;
+#pragma unroll 1
+    for (int32_t q = 0; q < parts.split; ++q) {
+        const uint32_t from = ptx::mapa_shared(addr, q);
+        uint4 x[2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[h][i] = ptx::ld_cluster_v4(from + (4 * h + i) * 512u);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[h][4 * i] += x[h][i].x;
+                v[h][4 * i + 1] += x[h][i].y;
+                v[h][4 * i + 2] += x[h][i].z;
+                v[h][4 * i + 3] += x[h][i].w;
+            }
+    }
+}
+
+// A piece's columns to TMEM, from where this warp alone takes them back.
+__device__ __forceinline__ void store_piece(uint32_t t_addr, const uint32_t (&v)[2][16])
+{
+    ptx::tmem_st_16x256b_x4(t_addr, v[0]);
+    ptx::tmem_st_16x256b_x4(t_addr + (16u << 16), v[1]);
+    ptx::tmem_st_wait();
+}
+
 // A lane's row of L, 128 8-bit terms of a swizzled tile, to its TMEM lane's 64
 // columns at t_a; v: its first four 16-byte pieces, loaded before.
+template <int kPieces = 4>
 __device__ __forceinline__ void widen_row_to_tmem(uint32_t row_addr, int lane, uint4 (&v)[4], uint32_t t_a)
 {
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-        uint32_t f[32];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const uint32_t words[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+        for (int part = 0; part < 4; part += kPieces) {
+            uint32_t f[8 * kPieces];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const uint2 x = i8x4_to_f16x4(words[q]);
-                f[8 * c + 2 * q] = x.x;
-                f[8 * c + 2 * q + 1] = x.y;
+            for (int c = 0; c < kPieces; ++c) {
+                const uint32_t words[4] = {v[part + c].x, v[part + c].y, v[part + c].z, v[part + c].w};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const uint2 x = i8x4_to_f16x4(words[q]);
+                    f[8 * c + 2 * q] = x.x;
+                    f[8 * c + 2 * q + 1] = x.y;
+                }
             }
-        }
-        if (half == 0) {
+            if (half == 0) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) v[c] = ptx::ld_shared_v4(row_addr + (((4 + c) ^ (lane & 7)) << 4));
+                for (int c = part; c < part + kPieces; ++c) v[c] = ptx::ld_shared_v4(row_addr + (((4 + c) ^ (lane & 7)) << 4));
+            }
+            if constexpr (kPieces == 4)
+                ptx::tmem_st_32x32b_x32(t_a + 32 * half, f);
+            else
+                ptx::tmem_st_32x32b_x16(t_a + 32 * half + 8 * part, f);
         }
-        ptx::tmem_st_32x32b_x32(t_a + 32 * half, f);
     }
 }
 
@@ -172,6 +261,8 @@ __global__ void __launch_bounds__(kI8Threads, 1) tn_i8_kernel(const __grid_const
     // 8-bit stages of a tile, this CTA's being those from begin on, below blocks
     const int32_t sum_blocks = (p.red + kI8Block - 1) / kI8Block;
     const int32_t begin = sum_blocks * parts.rank / split, blocks = sum_blocks * (parts.rank + 1) / split;
+    const bool sums = sum_blocks > kI8Run;    // sums of several runs, as integers
+    const float unit = sum_unit(p.red);
     bool joins = false;                       // an epilogue warp whose tile's split sum is complete here
 
     GroupedStore store;
@@ -230,22 +321,22 @@ __global__ void __launch_bounds__(kI8Threads, 1) tn_i8_kernel(const __grid_const
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer
         int stage = 0;
-        uint32_t phase = 0, sub = 0;
+        uint32_t phase = 0, sub = 0;              // sub: runs so far; run `sub` uses accumulator sub % 2
         bool ok = true, issued_any = false;
         if (p.flags & kFlagStallMma) ok = wait_warp(w, never_bar, 0u, kSiteStall);
-        for (int32_t u = slot; ok && p.red > 0 && u < total; u += slots, ++sub) {
+        for (int32_t u = slot; ok && p.red > 0 && u < total; u += slots) {
             const GroupedTile t = walk.at(u);
             const uint32_t idesc = ptx::idesc_f32acc(kI8RowsL, static_cast<uint32_t>(t.n_mma[0]), 0u, 0u);
-            const uint32_t d_tmem = tmem_base + (sub & 1u) * kI8Rows;
-            if (!wait_warp(w, accempty_bar(sub & 1u), ((sub >> 1) & 1u) ^ 1u, kSiteAccEmpty)) break;
-            ptx::tc_fence_after_sync();
-            for (int32_t i = begin; i < blocks; ++i) {
-                if (!wait_warp(w, full16_bar(stage), phase, kSiteLoaded)) {
+            for (int32_t i = begin, run = 0; i < blocks; ++i) {      // run: stages of the run so far
+                const uint32_t d_tmem = tmem_base + (sub & 1u) * kI8Rows;
+                if ((run == 0 && !wait_warp(w, accempty_bar(sub & 1u), ((sub >> 1) & 1u) ^ 1u, kSiteAccEmpty)) ||
+                    !wait_warp(w, full16_bar(stage), phase, kSiteLoaded)) {
                     ok = false;
                     break;
                 }
                 ptx::tc_fence_after_sync();
                 const int32_t left = p.red - i * kI8Block;
+                const bool last = i + 1 == blocks || run + 1 == kI8Run;
                 if (ptx::elect_one()) {
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
@@ -256,13 +347,18 @@ __global__ void __launch_bounds__(kI8Threads, 1) tn_i8_kernel(const __grid_const
                         for (int j = 0; j < kGrBlock / 16; ++j)
                             if (left > half * kGrBlock + 16 * j)
                                 ptx::mma_f16_ts<1>(d_tmem, a_tmem + 8 * j, desc_r + 2u * j, idesc,
-                                                (i - begin) | half | j ? 1u : 0u);
+                                                (run | half | j) != 0 ? 1u : 0u);
                     }
                     ptx::mma_commit<1>(empty16_bar(stage));
-                    if (i + 1 == blocks) ptx::mma_commit<1>(accfull_bar(sub & 1u));
+                    if (last) ptx::mma_commit<1>(accfull_bar(sub & 1u));
                 }
                 __syncwarp();
                 issued_any = true;
+                ++run;
+                if (last) {
+                    run = 0;
+                    ++sub;
+                }
                 if (++stage == kS16) {
                     stage = 0;
                     phase ^= 1u;
@@ -287,33 +383,51 @@ __global__ void __launch_bounds__(kI8Threads, 1) tn_i8_kernel(const __grid_const
                     for (int32_t r = 0; r < t.rows; ++r) out[r * p.out_ld + lane] = 0;
                 continue;
             }
-            if (!wait_warp(w, accfull_bar(sub & 1u), (sub >> 1) & 1u, kSiteAccFull)) break;
-            ptx::tc_fence_after_sync();
-            const uint32_t t_row = tmem_base + (static_cast<uint32_t>(32 * quarter) << 16) + (sub & 1u) * kI8Rows;
-            if (split > 1) {                      // the cluster's one tile, stored further down
-                for (int s = 0; s * kGrChunk < t.n_mma[0]; ++s) {
-                    if (parts.mine(quarter, s)) continue;
+            const uint32_t t_lanes = tmem_base + (static_cast<uint32_t>(32 * quarter) << 16);
+            bool ok = true;
+            for (int32_t i = begin; i < blocks; i += kI8Run, ++sub) {
+                const bool last = i + kI8Run >= blocks;
+                ok = wait_warp(w, accfull_bar(sub & 1u), (sub >> 1) & 1u, kSiteAccFull);
+                if (!ok) break;
+                ptx::tc_fence_after_sync();
+#pragma unroll 1
+                for (int32_t c = 0; c < t.n_mma[0]; c += kGrChunk) {
                     uint32_t v[2][16];
-                    load_piece(t_row + s * kGrChunk, v);
-                    parts.leave(parts.at(quarter, s, lane), v);
+                    load_piece(t_lanes + (sub & 1u) * kI8Rows + c, v);
+                    if (c + kGrChunk >= t.n_mma[0]) {
+                        ptx::tc_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(accempty_bar(sub & 1u));
+                    }
+                    if (sums) {
+                        piece_to_ints(v, unit);
+                        if (i > begin) {
+                            uint32_t so_far[2][16];
+                            load_piece(t_lanes + kI8SumCol0 + c, so_far);
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                                for (int q = 0; q < 16; ++q) v[h][q] += so_far[h][q];
+                        }
+                        if (!last) {
+                            store_piece(t_lanes + kI8SumCol0 + c, v);
+                            continue;
+                        }
+                        if (split > 1) {          // the cluster's one tile, stored further down
+                            parts.leave(parts.at(quarter, c / kGrChunk, lane), v);
+                            continue;
+                        }
+                        piece_to_floats(v, unit);
+                    }
+                    if (p.out_fmt != 0)
+                        store.step<true, true>(v, out + c * p.out_ld, t.rows - c, p.scale_r + row0 + c);
+                    else
+                        store.step<false, true>(v, out + c * p.out_ld, t.rows - c, p.scale_r + row0 + c);
                 }
-                joins = true;
-                break;
             }
-            for (int32_t c = 0; c < t.n_mma[0]; c += kGrChunk) {
-                uint32_t v[2][16];
-                load_piece(t_row + c, v);
-                if (c + kGrChunk >= t.n_mma[0]) {
-                    ptx::tc_fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(accempty_bar(sub & 1u));
-                }
-                if (p.out_fmt != 0)
-                    store.step<true, true>(v, out + c * p.out_ld, t.rows - c, p.scale_r + row0 + c);
-                else
-                    store.step<false, true>(v, out + c * p.out_ld, t.rows - c, p.scale_r + row0 + c);
-            }
-            ++sub;
+            if (!ok) break;
+            joins = split > 1;
+            if (joins) break;
         }
     } else {
         // ------------------------------------------------ widening (warps 6..13)
@@ -389,8 +503,8 @@ __global__ void __launch_bounds__(kI8Threads, 1) tn_i8_kernel(const __grid_const
                 if (!parts.mine(quarter, s)) continue;
                 const int32_t c = s * kGrChunk;
                 uint32_t v[2][16];
-                load_piece(tmem_base + (static_cast<uint32_t>(32 * quarter) << 16) + c, v);
-                parts.add_others(parts.at(quarter, s, lane), v);
+                join_piece(parts, parts.at(quarter, s, lane), v);
+                piece_to_floats(v, unit);
                 if (p.out_fmt != 0)
                     store.step<true, true>(v, out + c * p.out_ld, t.rows - c, p.scale_r + row0 + c);
                 else
@@ -416,8 +530,8 @@ __global__ void __launch_bounds__(kI8Threads, 1) tn_i8_kernel(const __grid_const
 // The weights are again widened on the way, each CTA's 128 rows into its own
 // tensor memory; the tokens come widened to f16 (widen_rows_kernel; T x K, where
 // widening the weights as well would move five bytes for each of them first).
-// Bound by the tensor cores: 8192 x 4096 x 8192 333 us with the widening (1650 TFLOP/s;
-// the f16 rate under the power cap is 1715).
+// Bound by the tensor cores and the widening that feeds them: 8192 x 4096 x 8192 345 us
+// with the tokens' widening (1590 TFLOP/s; the f16 rate under the power cap is 1715).
 //
 // Tiles of 256 (L) x up to 192 (R) rows: two accumulators of 192 columns and two
 // stages of widened weights of 64 fill the 512 TMEM columns.  A stage is 128
@@ -430,24 +544,32 @@ constexpr int kIpLBytes = 128 * 128;
 constexpr int kIpAtomBytes = kIpRowsR * 128;                 // 64 terms of a CTA's tokens
 constexpr int kIpStageBytes = kIpLBytes + 2 * kIpAtomBytes;
 constexpr int kIpStages = 4;                                 // (an even number: a team's stages are every other one)
+// Warps: two teams of four that widen, eight of the epilogue, one for the TMA and one
+// for the MMAs (and two that only wait).  The epilogue's sums of 96 columns a thread
+// want more registers than an even share, which the others give up.
+constexpr int kIpThreads = 640, kIpLaunchRegs = 96;
+constexpr int kIpEpiWarps = 8, kIpFirstEpi = 8, kIpTmaWarp = 16, kIpMmaWarp = 17;
+constexpr int kIpRegsLead = 64, kIpRegsWiden = 72, kIpRegsEpi = 136;
+static_assert(128 * kIpRegsLead + 256 * kIpRegsWiden + 256 * kIpRegsEpi <= kIpThreads * kIpLaunchRegs,
+              "no more registers than the block is launched with");
 constexpr uint32_t kIpACol0 = 2 * kIpRows;
 constexpr uint32_t kIpTmemCols = 512;
 static_assert(kIpACol0 + 2 * kI8ACols == kIpTmemCols, "the TMEM columns are all used");
 static_assert(kIpAtomBytes % 1024 == 0, "blocks start on the swizzle's 1024 bytes");
 // full8[S], fullr[S], empty[S], fulla[2], emptya[2], accfull[2], accempty[2], drain, never
 constexpr int kIpBarriers = 3 * kIpStages + 10;
-constexpr int kIpSmemBytes = 1024 /* alignment slack */ + kIpStages * kIpStageBytes + kI8EpiWarps * kGrStageBytes +
+constexpr int kIpSmemBytes = 1024 /* alignment slack */ + kIpStages * kIpStageBytes + kIpEpiWarps * kGrStageBytes +
                              kIpBarriers * 8 + 32 + kIpStages * 4 + 2 * (kGrMaxExperts + 8) * 4;
 static_assert(kIpSmemBytes <= 232448, "exceeds the 227 KiB shared memory of one CTA");
 
-__global__ void __launch_bounds__(kI8Threads, 1) tn_i8_pair_kernel(const __grid_constant__ GroupedParams p)
+__global__ void __launch_bounds__(kIpThreads, 1) tn_i8_pair_kernel(const __grid_constant__ GroupedParams p)
 {
     constexpr int kS = kIpStages;
 
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t s_ring = ptx::smem_addr(smem), s_staging = s_ring + kS * kIpStageBytes;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kS * kIpStageBytes + kI8EpiWarps * kGrStageBytes);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kS * kIpStageBytes + kIpEpiWarps * kGrStageBytes);
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + kIpBarriers);
     volatile uint32_t *abort_flag = tmem_holder + 1;
     volatile uint32_t *issued_count = tmem_holder + 2;    // fills this CTA's producer issued
@@ -485,7 +607,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) tn_i8_pair_kernel(const __grid_
             ptx::mbar_init(fulla_bar(b), 2 * kI8TeamWarps);
             ptx::mbar_init(emptya_bar(b), 1);
             ptx::mbar_init(accfull_bar(b), 1);
-            ptx::mbar_init(accempty_bar(b), 2 * kI8EpiWarps);
+            ptx::mbar_init(accempty_bar(b), 2 * kIpEpiWarps);
         }
         ptx::mbar_init(drain_bar, 1);
         ptx::mbar_init(never_bar, 1);
@@ -499,7 +621,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) tn_i8_pair_kernel(const __grid_
         ptx::prefetch_tensormap(&p.tmap_l);
         ptx::prefetch_tensormap(&p.tmap_r[kIpRowsR / 16 - 1]);
     }
-    if (warp == 1) {
+    if (warp == kIpMmaWarp) {
         ptx::tmem_alloc<2>(ptx::smem_addr(tmem_holder), kIpTmemCols);
         ptx::tmem_relinquish_alloc_permit<2>();
     }
@@ -511,185 +633,149 @@ __global__ void __launch_bounds__(kI8Threads, 1) tn_i8_pair_kernel(const __grid_
 
     ptx::griddep_wait();                      // every thread's first global access is behind this wait
     const int32_t l_tiles = (p.l_extent + 255) / 256;
-    grouped_tables<kGrI8, kIpRows, kI8Threads>(p, l_tiles, start, before);
+    grouped_tables<kGrI8, kIpRows, kIpThreads>(p, l_tiles, start, before);
     const int32_t total = before[p.E];
     const int32_t slot = static_cast<int32_t>(blockIdx.x) / 2, slots = static_cast<int32_t>(gridDim.x) / 2;
     GroupedWalk<kGrI8, kIpRows, kIpRows, 256, 32> walk{start, before, l_tiles, 0, p.red, 0};
     const int32_t blocks = (p.red + kI8Block - 1) / kI8Block;       // stages of a tile
 
-    if (warp == 0) {
-        // ------------------------------------------------ TMA producer (both CTAs)
-        int stage = 0;
-        uint32_t phase = 0, n_issued = 0;
-        bool ok = true;
-        if (p.flags & (pos == 0 ? kFlagStallProducer0 : kFlagStallProducer1)) ok = wait_warp(w, never_bar, 0u, kSiteStall);
-        for (int32_t u = slot; ok && u < total; u += slots) {
-            const GroupedTile t = walk.at(u);
-            const int32_t cols = t.n_mma[0] / 2;                 // this CTA's tokens
-            const CUtensorMap *map_r = p.tmap_r + cols / 16 - 1;
-            const int32_t l0 = t.l0 + static_cast<int32_t>(pos) * 128;
-            const int32_t r0 = start[t.e] + t.r0 + static_cast<int32_t>(pos) * cols;
-            for (int32_t i = 0; i < blocks; ++i) {
-                if (!wait_warp(w, empty_bar(stage), phase ^ 1u, kSiteEmpty)) {
-                    ok = false;
-                    break;
-                }
-                ++n_issued;
-                if (ptx::elect_one()) {
-                    const uint32_t s_l = s_ring + stage * kIpStageBytes, s_r = s_l + kIpLBytes;
-                    const uint32_t bar_r = ptx::mapa_shared(fullr_bar(stage), 0);
-                    const uint32_t bytes = 2u * cols * 128u;
-                    fill_bytes[stage] = bytes;
-                    ptx::mbar_arrive_expect_tx(full8_bar(stage), kIpLBytes);
-                    tma_load_3d(s_l, &p.tmap_l, full8_bar(stage), i * kI8Block, l0, t.e);
-                    if (pos == 0) ptx::mbar_arrive_expect_tx(fullr_bar(stage), 2 * bytes);
-                    ptx::tma_load_2d_pair(s_r, map_r, bar_r, i * kI8Block, r0);
-                    ptx::tma_load_2d_pair(s_r + kIpAtomBytes, map_r, bar_r, i * kI8Block + kGrBlock, r0);
-                    *issued_count = n_issued;
-                }
-                __syncwarp();
-                if (++stage == kS) {
-                    stage = 0;
-                    phase ^= 1u;
-                }
-            }
-        }
-        if (lane == 0) ptx::griddep_launch_dependents();
-        if (ptx::elect_one()) {
-            auto fills = [](uint32_t n, int s) { return n / kS + (static_cast<uint32_t>(s) < n % kS ? 1u : 0u); };
-            // this CTA's weights: every issued load lands before the CTA can exit
-            for (int s = 0; s < kS; ++s)
-                if (const uint32_t passes = fills(n_issued, s)) w.drain(full8_bar(s), (passes - 1) & 1u);
-            ptx::st_release_cluster_u32(ptx::mapa_shared(done_addr, pos), 1u);
-            if (pos == 0) {
-                // the pair's tokens, as in tn_grouped_kernel
-                uint32_t peer = n_issued;
-                const uint64_t t0 = ptx::globaltimer();
-                bool stopped = true;
-                while (ptx::ld_acquire_cluster_u32(ptx::mapa_shared(done_addr, 1)) == 0u) {
-                    if (ptx::globaltimer() - t0 > w.limit) {
-                        atomicCAS(&g_tn_status, 0, 4 | (kSitePeerDone << 8));
-                        stopped = false;
-                        break;
-                    }
-                }
-                if (stopped) peer = ptx::ld_relaxed_cluster_u32(ptx::mapa_shared(count_addr, 1));
-                for (int s = 0; s < kS; ++s) {
-                    const uint32_t mine = fills(n_issued, s), theirs = fills(peer, s);
-                    const uint32_t last = mine > theirs ? mine : theirs;
-                    if (last == 0) continue;
-                    if (mine > theirs + 1 || theirs > mine + 1) {      // cannot happen; never guess
-                        atomicCAS(&g_tn_status, 0, 4 | (kSiteReconcile << 8));
-                        continue;
-                    }
-                    if (mine > theirs)
-                        ptx::mbar_complete_tx(fullr_bar(s), fill_bytes[s]);
-                    else if (theirs > mine)
-                        ptx::mbar_arrive_expect_tx(fullr_bar(s),
-                                                   ptx::ld_relaxed_cluster_u32(ptx::mapa_shared(fill_addr + 4u * s, 1)));
-                    w.drain(fullr_bar(s), (last - 1) & 1u);
-                }
-            }
-        }
-    } else if (warp == 1) {
-        if (pos == 0) {
-            // ------------------------------------------------ MMA issuer (even CTA)
+    if (warp >= kIpTmaWarp) {
+        ptx::setmaxnreg_dec<kIpRegsLead>();
+        if (warp == kIpTmaWarp) {
+            // ------------------------------------------------ TMA producer (both CTAs)
             int stage = 0;
-            uint32_t phase = 0, sub = 0, n = 0;               // n: stages so far
-            bool ok = true, issued_any = false;
-            if (p.flags & kFlagStallMma) ok = wait_warp(w, never_bar, 0u, kSiteStall);
-            for (int32_t u = slot; ok && p.red > 0 && u < total; u += slots, ++sub) {
+            uint32_t phase = 0, n_issued = 0;
+            bool ok = true;
+            if (p.flags & (pos == 0 ? kFlagStallProducer0 : kFlagStallProducer1)) ok = wait_warp(w, never_bar, 0u, kSiteStall);
+            for (int32_t u = slot; ok && u < total; u += slots) {
                 const GroupedTile t = walk.at(u);
-                const uint32_t idesc = ptx::idesc_f32acc(256, static_cast<uint32_t>(t.n_mma[0]), 0u, 0u);
-                const uint32_t d_tmem = tmem_base + (sub & 1u) * kIpRows;
-                if (!wait_warp(w, accempty_bar(sub & 1u), ((sub >> 1) & 1u) ^ 1u, kSiteAccEmpty)) break;
-                for (int32_t i = 0; i < blocks; ++i, ++n) {
-                    const uint32_t team = n & 1u;
-                    if (!wait_warp(w, fullr_bar(stage), phase, kSiteLoaded) ||
-                        !wait_warp(w, fulla_bar(team), (n >> 1) & 1u, kSiteLoaded)) {
+                const int32_t cols = t.n_mma[0] / 2;                 // this CTA's tokens
+                const CUtensorMap *map_r = p.tmap_r + cols / 16 - 1;
+                const int32_t l0 = t.l0 + static_cast<int32_t>(pos) * 128;
+                const int32_t r0 = start[t.e] + t.r0 + static_cast<int32_t>(pos) * cols;
+                for (int32_t i = 0; i < blocks; ++i) {
+                    if (!wait_warp(w, empty_bar(stage), phase ^ 1u, kSiteEmpty)) {
                         ok = false;
                         break;
                     }
-                    ptx::tc_fence_after_sync();
-                    const int32_t left = p.red - i * kI8Block;
+                    ++n_issued;
                     if (ptx::elect_one()) {
-#pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            const uint64_t desc_r = ptx::desc_kmajor_sw128(s_ring + stage * kIpStageBytes + kIpLBytes +
-                                                                           half * kIpAtomBytes);
-                            const uint32_t a_tmem = tmem_base + kIpACol0 + team * kI8ACols + half * (kI8ACols / 2);
-#pragma unroll
-                            for (int j = 0; j < kGrBlock / 16; ++j)
-                                if (left > half * kGrBlock + 16 * j)
-                                    ptx::mma_f16_ts<2>(d_tmem, a_tmem + 8 * j, desc_r + 2u * j, idesc,
-                                                       (i | half | j) != 0 ? 1u : 0u);
-                        }
-                        ptx::mma_commit<2>(emptya_bar(team), 3);
-                        ptx::mma_commit<2>(empty_bar(stage), 3);
-                        if (i + 1 == blocks) ptx::mma_commit<2>(accfull_bar(sub & 1u), 3);
+                        const uint32_t s_l = s_ring + stage * kIpStageBytes, s_r = s_l + kIpLBytes;
+                        const uint32_t bar_r = ptx::mapa_shared(fullr_bar(stage), 0);
+                        const uint32_t bytes = 2u * cols * 128u;
+                        fill_bytes[stage] = bytes;
+                        ptx::mbar_arrive_expect_tx(full8_bar(stage), kIpLBytes);
+                        tma_load_3d(s_l, &p.tmap_l, full8_bar(stage), i * kI8Block, l0, t.e);
+                        if (pos == 0) ptx::mbar_arrive_expect_tx(fullr_bar(stage), 2 * bytes);
+                        ptx::tma_load_2d_pair(s_r, map_r, bar_r, i * kI8Block, r0);
+                        ptx::tma_load_2d_pair(s_r + kIpAtomBytes, map_r, bar_r, i * kI8Block + kGrBlock, r0);
+                        *issued_count = n_issued;
                     }
                     __syncwarp();
-                    issued_any = true;
                     if (++stage == kS) {
                         stage = 0;
                         phase ^= 1u;
                     }
                 }
             }
-            if (issued_any && ptx::elect_one()) {             // every MMA issued completes before TMEM is freed
-                ptx::mma_commit<2>(drain_bar, 1);
-                w.drain(drain_bar, 0u);
-            }
-        }
-    } else if (warp < 2 + kI8EpiWarps) {
-        // ------------------------------------------------ epilogue (warps 2..5, both CTAs)
-        const int quarter = warp & 3;
-        GroupedStore store;
-        store.init(s_staging + (warp - 2) * kGrStageBytes, lane);
-        store.ld = p.out_ld;
-        uint32_t sub = 0;
-        for (int32_t u = slot; u < total; u += slots) {
-            const GroupedTile t = walk.at(u);
-            const int32_t l0 = t.l0 + static_cast<int32_t>(pos) * 128 + 32 * quarter;
-            const int64_t row0 = static_cast<int64_t>(start[t.e]) + t.r0;
-            uint16_t *out = p.out + row0 * p.out_ld + l0;
-            store.wide = p.l_extent - l0 < 32 ? p.l_extent - l0 : 32;
-            store.vec = p.out_vec != 0 && store.wide == 32;
-            if (p.red == 0) {                     // an empty sum
-                if (lane < store.wide)
-                    for (int32_t r = 0; r < t.rows; ++r) out[r * p.out_ld + lane] = 0;
-                continue;
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                store.scale_l[i] = 8 * i + (lane >> 2) < store.wide
-                                       ? __ldg(p.scale_l + static_cast<int64_t>(t.e) * p.l_extent + l0 + 8 * i + (lane >> 2))
-                                       : 0.0f;
-            if (!wait_warp(w, accfull_bar(sub & 1u), (sub >> 1) & 1u, kSiteAccFull)) break;
-            ptx::tc_fence_after_sync();
-            const uint32_t t_row = tmem_base + (static_cast<uint32_t>(32 * quarter) << 16) + (sub & 1u) * kIpRows;
-            for (int32_t c = 0; c < t.n_mma[0]; c += kGrChunk) {
-                uint32_t v[2][16];
-                ptx::tmem_ld_16x256b_x4(t_row + c, v[0]);
-                ptx::tmem_ld_16x256b_x4(t_row + (16u << 16) + c, v[1]);
-                ptx::tmem_ld_wait_all();
-                ptx::reg_dependency(v[0]);
-                ptx::reg_dependency(v[1]);
-                if (c + kGrChunk >= t.n_mma[0]) {
-                    ptx::tc_fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive_remote(ptx::mapa_shared(accempty_bar(sub & 1u), 0));
+            if (lane == 0) ptx::griddep_launch_dependents();
+            if (ptx::elect_one()) {
+                auto fills = [](uint32_t n, int s) { return n / kS + (static_cast<uint32_t>(s) < n % kS ? 1u : 0u); };
+                // this CTA's weights: every issued load lands before the CTA can exit
+                for (int s = 0; s < kS; ++s)
+                    if (const uint32_t passes = fills(n_issued, s)) w.drain(full8_bar(s), (passes - 1) & 1u);
+                ptx::st_release_cluster_u32(ptx::mapa_shared(done_addr, pos), 1u);
+                if (pos == 0) {
+                    // the pair's tokens, as in tn_grouped_kernel
+                    uint32_t peer = n_issued;
+                    const uint64_t t0 = ptx::globaltimer();
+                    bool stopped = true;
+                    while (ptx::ld_acquire_cluster_u32(ptx::mapa_shared(done_addr, 1)) == 0u) {
+                        if (ptx::globaltimer() - t0 > w.limit) {
+                            atomicCAS(&g_tn_status, 0, 4 | (kSitePeerDone << 8));
+                            stopped = false;
+                            break;
+                        }
+                    }
+                    if (stopped) peer = ptx::ld_relaxed_cluster_u32(ptx::mapa_shared(count_addr, 1));
+                    for (int s = 0; s < kS; ++s) {
+                        const uint32_t mine = fills(n_issued, s), theirs = fills(peer, s);
+                        const uint32_t last = mine > theirs ? mine : theirs;
+                        if (last == 0) continue;
+                        if (mine > theirs + 1 || theirs > mine + 1) {      // cannot happen; never guess
+                            atomicCAS(&g_tn_status, 0, 4 | (kSiteReconcile << 8));
+                            continue;
+                        }
+                        if (mine > theirs)
+                            ptx::mbar_complete_tx(fullr_bar(s), fill_bytes[s]);
+                        else if (theirs > mine)
+                            ptx::mbar_arrive_expect_tx(fullr_bar(s),
+                                                       ptx::ld_relaxed_cluster_u32(ptx::mapa_shared(fill_addr + 4u * s, 1)));
+                        w.drain(fullr_bar(s), (last - 1) & 1u);
+                    }
                 }
-                if (p.out_fmt != 0)
-                    store.step<true, true>(v, out + c * p.out_ld, t.rows - c, p.scale_r + row0 + c);
-                else
-                    store.step<false, true>(v, out + c * p.out_ld, t.rows - c, p.scale_r + row0 + c);
             }
-            ++sub;
+        } else if (warp == kIpMmaWarp) {
+            if (pos == 0) {
+                // ------------------------------------------------ MMA issuer (even CTA)
+                int stage = 0;
+                uint32_t phase = 0, sub = 0, n = 0;               // runs (run `sub` uses accumulator sub % 2) and stages so far
+                bool ok = true, issued_any = false;
+                if (p.flags & kFlagStallMma) ok = wait_warp(w, never_bar, 0u, kSiteStall);
+                for (int32_t u = slot; ok && p.red > 0 && u < total; u += slots) {
+                    const GroupedTile t = walk.at(u);
+                    const uint32_t idesc = ptx::idesc_f32acc(256, static_cast<uint32_t>(t.n_mma[0]), 0u, 0u);
+                    for (int32_t i = 0, run = 0; i < blocks; ++i, ++n) {      // run: stages of the run so far
+                        const uint32_t team = n & 1u;
+                        const uint32_t d_tmem = tmem_base + (sub & 1u) * kIpRows;
+                        if ((run == 0 && !wait_warp(w, accempty_bar(sub & 1u), ((sub >> 1) & 1u) ^ 1u, kSiteAccEmpty)) ||
+                            !wait_warp(w, fullr_bar(stage), phase, kSiteLoaded) ||
+                            !wait_warp(w, fulla_bar(team), (n >> 1) & 1u, kSiteLoaded)) {
+                            ok = false;
+                            break;
+                        }
+                        ptx::tc_fence_after_sync();
+                        const int32_t left = p.red - i * kI8Block;
+                        const bool last = i + 1 == blocks || run + 1 == kI8Run;
+                        if (ptx::elect_one()) {
+#pragma unroll
+                            for (int half = 0; half < 2; ++half) {
+                                const uint64_t desc_r = ptx::desc_kmajor_sw128(s_ring + stage * kIpStageBytes + kIpLBytes +
+                                                                               half * kIpAtomBytes);
+                                const uint32_t a_tmem = tmem_base + kIpACol0 + team * kI8ACols + half * (kI8ACols / 2);
+#pragma unroll
+                                for (int j = 0; j < kGrBlock / 16; ++j)
+                                    if (left > half * kGrBlock + 16 * j)
+                                        ptx::mma_f16_ts<2>(d_tmem, a_tmem + 8 * j, desc_r + 2u * j, idesc,
+                                                           (run | half | j) != 0 ? 1u : 0u);
+                            }
+                            ptx::mma_commit<2>(emptya_bar(team), 3);
+                            ptx::mma_commit<2>(empty_bar(stage), 3);
+                            if (last) ptx::mma_commit<2>(accfull_bar(sub & 1u), 3);
+                        }
+                        __syncwarp();
+                        issued_any = true;
+                        ++run;
+                        if (last) {
+                            run = 0;
+                            ++sub;
+                        }
+                        if (++stage == kS) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
+                    }
+                }
+                if (issued_any && ptx::elect_one()) {             // every MMA issued completes before TMEM is freed
+                    ptx::mma_commit<2>(drain_bar, 1);
+                    w.drain(drain_bar, 0u);
+                }
+            }
         }
-    } else {
-        // ------------------------------------------------ widening (warps 6..13, both CTAs)
-        const int team = (warp - 2 - kI8EpiWarps) / kI8TeamWarps;
+    } else if (warp < kIpFirstEpi) {
+        // ------------------------------------------------ widening (both CTAs)
+        ptx::setmaxnreg_dec<kIpRegsWiden>();
+        const int team = warp / kI8TeamWarps;
         static_assert(kS % 2 == 0, "a team's stages are every other one");
         const int quarter = warp & 3;
         const uint32_t row_l = static_cast<uint32_t>(32 * quarter + lane) * 128u;
@@ -710,7 +796,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) tn_i8_pair_kernel(const __grid_
                 ok = wait_warp(w, emptya_bar(team), phase_a ^ 1u, kSiteEmpty);
                 if (!ok) break;
                 ptx::tc_fence_after_sync();                   // the MMAs that read this TMEM stage are done
-                widen_row_to_tmem(src, lane, v, t_a);
+                widen_row_to_tmem<2>(src, lane, v, t_a);
                 ptx::tmem_st_wait();
                 ptx::tc_fence_before_sync();
                 __syncwarp();
@@ -726,12 +812,102 @@ __global__ void __launch_bounds__(kI8Threads, 1) tn_i8_pair_kernel(const __grid_
                 }
             }
         }
+    } else {
+        // ------------------------------------------------ epilogue (both CTAs)
+        // Two warps to a quarter of the lanes, which take every other 32 columns.  Sums of
+        // one run are stored out of their accumulator; those of several gather in
+        // registers, and go back as floats to where the last run was.
+        ptx::setmaxnreg_inc<kIpRegsEpi>();
+        constexpr int kPieces = kIpRows / kGrChunk / 2;
+        const int quarter = warp & 3, turn = (warp - kIpFirstEpi) >> 2;
+        const uint32_t t_lanes = tmem_base + (static_cast<uint32_t>(32 * quarter) << 16);
+        const float unit = sum_unit(p.red);
+        GroupedStore store;
+        store.init(s_staging + (warp - kIpFirstEpi) * kGrStageBytes, lane);
+        store.ld = p.out_ld;
+        uint32_t sub = 0;                                     // runs so far
+        auto acc_full = [&]() {
+            const bool ok = wait_warp(w, accfull_bar(sub & 1u), (sub >> 1) & 1u, kSiteAccFull);
+            if (ok) ptx::tc_fence_after_sync();
+            return ok;
+        };
+        auto hand_back = [&]() {                              // this warp has read its part of the accumulator
+            ptx::tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive_remote(ptx::mapa_shared(accempty_bar(sub & 1u), 0));
+        };
+        for (int32_t u = slot; u < total; u += slots) {
+            if (blocks > kI8Run) {
+                const int32_t n_mma = walk.at(u).n_mma[0];
+                uint32_t sum[kPieces][2][16];
+#pragma unroll
+                for (int s = 0; s < kPieces; ++s)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int q = 0; q < 16; ++q) sum[s][h][q] = 0u;
+                bool ok;
+                int32_t i = 0;
+                while (true) {
+                    ok = acc_full();
+                    if (!ok) break;
+#pragma unroll
+                    for (int s = 0; s < kPieces; ++s) {
+                        const int32_t c = (2 * s + turn) * kGrChunk;
+                        if (c >= n_mma) break;
+                        uint32_t v[2][16];
+                        load_piece(t_lanes + (sub & 1u) * kIpRows + c, v);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+#pragma unroll
+                            for (int q = 0; q < 16; ++q)
+                                sum[s][h][q] += static_cast<uint32_t>(__float2int_rn(__uint_as_float(v[h][q]) * unit));
+                    }
+                    i += kI8Run;
+                    if (i >= blocks) break;
+                    hand_back();
+                    ++sub;
+                }
+                if (!ok) break;
+#pragma unroll
+                for (int s = 0; s < kPieces; ++s) {
+                    const int32_t c = (2 * s + turn) * kGrChunk;
+                    if (c >= n_mma) break;
+                    piece_to_floats(sum[s], unit);
+                    store_piece(t_lanes + (sub & 1u) * kIpRows + c, sum[s]);
+                }
+            }
+            const GroupedTile t = walk.at(u);
+            const int32_t l0 = t.l0 + static_cast<int32_t>(pos) * 128 + 32 * quarter;
+            const int64_t row0 = static_cast<int64_t>(start[t.e]) + t.r0;
+            uint16_t *out = p.out + row0 * p.out_ld + l0;
+            store.wide = p.l_extent - l0 < 32 ? p.l_extent - l0 : 32;
+            store.vec = p.out_vec != 0 && store.wide == 32;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                store.scale_l[i] = 8 * i + (lane >> 2) < store.wide
+                                       ? __ldg(p.scale_l + static_cast<int64_t>(t.e) * p.l_extent + l0 + 8 * i + (lane >> 2))
+                                       : 0.0f;
+            if (blocks <= kI8Run && !acc_full()) break;
+#pragma unroll 1
+            for (int32_t c = turn * kGrChunk; c < t.n_mma[0]; c += 2 * kGrChunk) {
+                uint32_t v[2][16];
+                load_piece(t_lanes + (sub & 1u) * kIpRows + c, v);
+                if (c + 2 * kGrChunk >= t.n_mma[0]) hand_back();
+                if (p.out_fmt != 0)
+                    store.step<true, true>(v, out + c * p.out_ld, t.rows - c, p.scale_r + row0 + c);
+                else
+                    store.step<false, true>(v, out + c * p.out_ld, t.rows - c, p.scale_r + row0 + c);
+            }
+            if (turn * kGrChunk >= t.n_mma[0]) hand_back();   // (no columns of its own)
+            ++sub;
+        }
     }
 
     __syncwarp();                // .aligned barriers below need converged warps
     ptx::tc_fence_before_sync();
     ptx::cluster_sync();         // no CTA leaves while the other may still touch its shared memory
-    if (warp == 1) {
+    if (warp == kIpMmaWarp) {
         __syncwarp();
         ptx::tc_fence_after_sync();
         ptx::tmem_dealloc<2>(tmem_base, kIpTmemCols);

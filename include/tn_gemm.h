@@ -322,9 +322,12 @@ gemm_status_t gemm_tn_grouped_grad_a(int type, int64_t E, int64_t M, int64_t K, 
  * A, B: signed 8-bit integers, all 256 values; C: N (or T) rows of M, out_type
  * GEMM_IN_F16 or GEMM_IN_BF16.  scale_a, scale_b: fp32 in device memory, 4-byte
  * aligned.  GB300's tensor cores multiply 8-bit integers far below their FP16
- * rate, so the integers are widened to FP16, which holds each of them exactly;
- * products are exact and S is an FP32 sum, exact while it stays below 2^24.
- * The result is rounded once.  The workspace (op GEMM_GROUPED_I8) also holds
+ * rate, so the integers are widened to FP16, which holds each of them exactly, and
+ * FP32 sums of 1024 products, which are exact too, are added up as integers.  S is
+ * the exact sum, rounded once to FP32, for K up to 131071; beyond, every 1024 terms
+ * are first rounded to a multiple of a power of two below K / 32768.  The two
+ * scalings are FP32 products, in the order above, and the last is rounded to out_type.
+ * The workspace (op GEMM_GROUPED_I8) also holds
  * the tokens widened to FP16 where there are many rows per expert and tiles; an
  * operand that the TMA cannot address is copied into it as it is.  Everything
  * else (offsets, rows of no expert, errors) is as for gemm_tn_grouped.

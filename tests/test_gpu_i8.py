@@ -89,6 +89,81 @@ def test_extreme_codes_and_long_sums():
             assert_scaled(C, Bt.double() @ A.double().t(), sa[None, :], sb[:, None], K, torch.bfloat16)
 
 
+def long_codes(kind, M, N, K, seed):
+    """Codes whose sums are about 0 (mixed), pass 2^24 many times over (same), or pass it
+    and come back to a small number (cancel)."""
+    A, Bt = codes(M, K, seed=seed), codes(N, K, seed=seed + 1)
+    if kind == "mixed":
+        return A, Bt
+    A, Bt = (t.int().abs().clamp(64, 127).to(torch.int8) for t in (A, Bt))
+    if kind == "cancel":
+        half = K // 2
+        A[:, K - half:] = -A[:, :half]
+        Bt[:, K - half:] = Bt[:, :half]
+        A[:, ::997] = codes(M, (K + 996) // 997, seed=seed + 2)
+    return A, Bt
+
+
+def scaled_once(sums, sa, sb, dtype):
+    """The exact sums rounded to FP32, scaled in FP32 by the channel and then by the token,
+    and rounded to the type: each step as the operator's definition has it."""
+    return ((sums.float() * sa) * sb).to(dtype)
+
+
+@pytest.mark.parametrize("kind", ["mixed", "same", "cancel"])
+@pytest.mark.parametrize("M,N,K", [(1, 1, 1024), (1, 1, 1025), (64, 65, 2049), (129, 16, 3000), (100, 5, 16384), (300, 200, 12300),
+                                   (832, 32, 12160), (20000, 40, 4096), (33, 64, 100000), (16, 3, 131071),
+                                   # CTA pairs
+                                   (2000, 1000, 1025), (520, 4097, 2064), (1290, 1537, 8191), (4096, 600, 16384), (8192, 257, 3001)])
+def test_i8_sums_are_exact(M, N, K, kind):
+    A, Bt = long_codes(kind, M, N, K, seed=K)
+    sa, sb = scales(M, seed=3), scales(N, seed=4) / 64
+    sums = Bt.double() @ A.double().t()
+    for dtype in TYPES:
+        C = g.i8_tn(A, Bt, sa, sb, dtype=dtype)
+        g.gemm_poll_device_status()
+        assert torch.equal(C, scaled_once(sums, sa[None, :], sb[:, None], dtype))
+
+
+@pytest.mark.parametrize("kind", ["same", "cancel"])
+@pytest.mark.parametrize("counts,M,K", [([3, 0, 70, 1], 200, 5000), ([200, 9], 129, 2049), ([1], 96, 20000),
+                                        ([2192, 1930, 1000, 2], 520, 2080), ([3000, 0, 2600, 193], 520, 4001), ([40] * 40, 1000, 1500)])
+def test_i8_grouped_sums_are_exact(counts, M, K, kind):
+    E, T, off = len(counts), sum(counts), offsets_of(counts)
+    A, Bt = long_codes(kind, E * M, T, K, seed=K)
+    A, sa, sb = A.view(E, M, K), scales(E, M, seed=3), scales(T, seed=4) / 64
+    b = off.tolist()
+    rows = torch.cat([sa[e].expand(b[e + 1] - b[e], M) for e in range(E)])
+    C = g.i8_tn_grouped(A, Bt, sa, sb, off)
+    g.gemm_poll_device_status()
+    assert torch.equal(C, scaled_once(grouped_sums(A, Bt, b), rows, sb[:, None], torch.float16))
+
+
+@pytest.mark.parametrize("M,N", [(16, 3), (300, 5000)])
+@pytest.mark.parametrize("K", [131071, 131072, 140001])
+def test_i8_sums_at_the_end_of_32_bits(M, N, K):
+    """Of 131071 terms the largest sum is 2^31 - 2^14; longer ones are FP32 sums of exact
+    runs of 1024 terms: one rounding for each run, and for each part of a split sum."""
+    one = torch.ones(M, device="cuda") * 2.0 ** -16
+    A, Bt = (torch.full((n, K), -128, dtype=torch.int8, device="cuda") for n in (M, N))
+    C = g.i8_tn(A, Bt, one, torch.ones(N, device="cuda"))
+    assert bool((C == torch.tensor(float(K) / 4, device="cuda").half()).all())
+    C = g.i8_tn(A, -(Bt + 1), one, torch.ones(N, device="cuda"))              # 127 * -128
+    assert bool((C == torch.tensor(-float(K) * 127 / 512, device="cuda").half()).all())
+    A, Bt = long_codes("cancel", M, N, K, seed=5)
+    sa, sb = scales(M, seed=3), scales(N, seed=4) / 64
+    C = g.i8_tn(A, Bt, sa, sb)
+    g.gemm_poll_device_status()
+    sums = Bt.double() @ A.double().t()
+    if K <= 131071:
+        assert torch.equal(C, scaled_once(sums, sa[None, :], sb[:, None], torch.float16))
+    else:
+        size = Bt.double().abs() @ A.double().abs().t()
+        scale = sa.double()[None, :] * sb.double()[:, None]
+        bound = ((K + 1023) // 1024 + 8) * 2.0 ** -24 * size * scale + (sums * scale).abs() * (2.0 ** -11 * 1.001 + 2.0 ** -22) + 2.0 ** -24
+        assert bool(((C.double() - sums * scale).abs() <= bound).all())
+
+
 @pytest.mark.parametrize("N", [5, 64, 600, 20000])
 def test_every_code_widens_exactly(N):
     """A's rows hold all 256 values, Bt picks one term per row."""
