@@ -72,22 +72,25 @@ GroupedOperand grouped_operand(const void *base, int64_t rows, int64_t blocks, i
     return o;
 }
 
-// Sizes the copy, if there is one.
-void grouped_copy(GroupedOperand &o, bool i8, bool widen)
+// Sizes the copy, if there is one; false where 63 bits do not hold its bytes.
+bool grouped_copy(GroupedOperand &o, bool i8, bool widen)
 {
     o.widen = widen;
     o.copy |= widen;
     if (o.copy) {
         const int64_t rows = o.rows, blocks = o.blocks, inner = o.inner;
         o.copy_ld = (inner + 63) / 64 * 64;
+        if (rows * blocks > (int64_t(1) << 60) / o.copy_ld) return false;
         o.copy_bytes = size_t(rows) * size_t(blocks) * size_t(o.copy_ld) * (i8 && !widen ? 1 : 2);
         o.copy_bytes = (o.copy_bytes + 255) & ~size_t(255);
     }
+    return true;
 }
 
 struct GroupedPlan {
     GroupedOperand x, y;
     size_t map_bytes;             // grad_a: two tensor maps per expert
+    bool fits;                    // the bytes are a number of 63 bits
     size_t bytes() const { return x.copy_bytes + y.copy_bytes + map_bytes; }
 };
 
@@ -104,6 +107,7 @@ GroupedPlan grouped_plan(int op, int64_t E, int64_t M, int64_t K, int64_t T, con
                          int64_t stride_x, const void *Y, int64_t ldy)
 {
     GroupedPlan g{};
+    g.fits = true;
     if (grouped_idle(E, M, K, T)) return g;
     const bool i8 = op == GEMM_GROUPED_I8;
     if (op == GEMM_GROUPED_GRAD_A) {
@@ -115,8 +119,7 @@ GroupedPlan grouped_plan(int op, int64_t E, int64_t M, int64_t K, int64_t T, con
         g.x = grouped_operand(X, M, E, K, ldx, stride_x, !grad_b, i8);
         g.y = grouped_operand(Y, T, 1, grad_b ? M : K, ldy, 0, true, i8);
     }
-    grouped_copy(g.x, i8, false);
-    grouped_copy(g.y, i8, i8 && !i8_direct(M, T, E));
+    g.fits = grouped_copy(g.x, i8, false) && grouped_copy(g.y, i8, i8 && !i8_direct(M, T, E));
     return g;
 }
 
@@ -126,7 +129,10 @@ int64_t grouped_workspace(int op, int64_t E, int64_t M, int64_t K, int64_t T, co
     if (op < GEMM_GROUPED_PRODUCT || op > GEMM_GROUPED_I8 || E < 0 || M < 0 || K < 0 || T < 0 || ldx < 0 || ldy < 0 ||
         stride_x < 0 || !grouped_sizes_fit(E, M, K, T, ldx, ldy, stride_x))
         return -1;
-    return static_cast<int64_t>(grouped_plan(op, E, M, K, T, X, ldx, stride_x, Y, ldy).bytes());
+    const int64_t inner_x = op == GEMM_GROUPED_GRAD_A ? M : K, inner_y = op == GEMM_GROUPED_GRAD_B ? M : K;
+    if (ldx < 1 || ldx < inner_x || ldy < 1 || ldy < inner_y) return -1;
+    const GroupedPlan plan = grouped_plan(op, E, M, K, T, X, ldx, stride_x, Y, ldy);
+    return plan.fits ? static_cast<int64_t>(plan.bytes()) : -1;
 }
 
 // Copies the operands that the plan says into the workspace, in one launch.
@@ -510,6 +516,7 @@ gemm_status_t run_grouped(const GroupedCall &c)
             return fail(GEMM_ERR_INVALID_ARG, "%s: a scale pointer is not 4-byte aligned", name);
     }
     const GroupedPlan plan = grouped_plan(c.op, c.E, c.M, c.K, c.T, c.X, c.ldx, c.stride_x, c.Y, c.ldy);
+    if (!plan.fits) return fail(GEMM_ERR_UNSUPPORTED, "%s: the operands' copies are too large", name);
     if (plan.bytes() > 0) {
         if (!c.workspace || c.workspace_bytes < static_cast<int64_t>(plan.bytes()))
             return fail(GEMM_ERR_INVALID_ARG, "%s: the workspace has %lld bytes, %zu are needed (gemm_grouped_workspace)", name,

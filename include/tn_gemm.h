@@ -290,7 +290,8 @@ typedef enum {
     GEMM_GROUPED_I8 = 3         /* X = A,  Y = B; gemm_i8_tn has E = 1 */
 } gemm_grouped_op_t;
 
-/* Workspace bytes of a call, -1 for arguments that it would refuse. */
+/* Workspace bytes of a call, -1 for an op, size, stride or leading dimension that
+ * it would refuse.  X and Y are looked at for their alignment alone. */
 int64_t gemm_grouped_workspace(int op, int64_t E, int64_t M, int64_t K, int64_t T,
                                const void *X, int64_t ldx, int64_t stride_x,
                                const void *Y, int64_t ldy);

@@ -193,3 +193,23 @@ def test_weight_gradients_that_overlap_are_refused(lib, E, M, K, ldda, stride, f
         assert status == g.GEMM_ERR_CUDA           # (past the checks: there is no device)
     else:
         assert status == g.GEMM_ERR_INVALID_ARG and "overlap" in g.last_error()
+
+
+BIG = 2 ** 31 - 256
+
+
+@pytest.mark.parametrize("lib", BINDINGS, ids=lambda b: getattr(b, "__name__", "ctypes"))
+@pytest.mark.parametrize("op,E,M,K,T,ldx,stride,ldy", [
+    (0, 2, 16, 8, 4, 7, 128, 8), (0, 2, 16, 8, 4, 8, 128, 7), (0, 2, 16, 8, 4, 1, 128, 8), (0, 2, 16, 0, 4, 0, 0, 1),
+    (1, 2, 16, 8, 4, 7, 128, 16), (1, 2, 16, 8, 4, 8, 128, 15), (2, 2, 16, 8, 4, 15, 0, 8), (2, 2, 16, 8, 4, 16, 0, 7),
+    (3, 1, 16, 16, 4, 15, 0, 16), (3, 1, 16, 16, 4, 16, 0, 15), (3, 1, 16, 16, 4, 16, 0, 0),
+    (0, 1024, BIG, BIG - 1, 4, BIG, 0, BIG), (0, 1024, BIG, BIG, 4, BIG, 8, BIG), (2, 1, BIG, 8, BIG, BIG + 8, 0, 8)])
+def test_workspace_of_a_call_that_is_refused(lib, op, E, M, K, T, ldx, stride, ldy):
+    """Leading dimensions below the rows they hold, and copies of more than 2^63 bytes."""
+    assert lib.gemm_grouped_workspace(op, E, M, K, T, P, ldx, stride, 2 * P, ldy) == -1
+
+
+def test_copies_past_63_bits_are_refused():
+    big = dict(E=1024, M=BIG, K=BIG - 1, lda=BIG, ldb=BIG, ldc=BIG, stride_a=0, ws=5 * P, n=2 ** 62)
+    assert product(g.lib, **big) == g.GEMM_ERR_UNSUPPORTED and "copies" in g.last_error()
+    assert g.gemm_grouped_workspace(0, 1, 1 << 20, BIG - 1, 4, P, BIG, 0, 2 * P, BIG) > 2 ** 51
