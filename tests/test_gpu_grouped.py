@@ -401,6 +401,82 @@ def test_the_workspace_belongs_to_the_calls_stream(kind):
     assert again.data_ptr() == at
 
 
+def helper_calls(T, M, K, E):
+    """Each helper of the grouped and 8-bit products with operands that are contiguous (its
+    short way) and the same with an output given (its long way); small integers."""
+    counts = [T // E] * (E - 1) + [T - T // E * (E - 1)]
+    off = offsets_of(counts)
+    A, Bt, dCt = (small_ints(*s, seed=i, dtype=torch.float16) for i, s in enumerate([(E, M, K), (T, K), (T, M)], 1))
+    qa, qb, sa, sb = A.to(torch.int8), Bt.to(torch.int8), torch.full((E, M), 0.5, device="cuda"), torch.ones(T, device="cuda")
+    new = lambda *s: torch.full(s, 9.0, dtype=torch.float16, device="cuda")  # noqa: E731
+    return {
+        "tn_grouped": (lambda **kw: g.tn_grouped(A, Bt, off, **kw), dict(C=new(T, M))),
+        "tn_grouped_grad_b": (lambda **kw: g.tn_grouped_grad_b(A, dCt, off, **kw), dict(dBt=new(T, K))),
+        "tn_grouped_grad_a": (lambda **kw: g.tn_grouped_grad_a(dCt, Bt, off, **kw), dict(dA=new(E, M, K))),
+        "i8_tn": (lambda **kw: g.i8_tn(qa[0], qb, sa[0], sb, **kw), dict(C=new(T, M))),
+        "i8_tn_grouped": (lambda **kw: g.i8_tn_grouped(qa, qb, sa, sb, off, **kw), dict(C=new(T, M))),
+    }
+
+
+@pytest.mark.parametrize("name", ["tn_grouped", "tn_grouped_grad_b", "tn_grouped_grad_a", "i8_tn", "i8_tn_grouped"])
+@pytest.mark.parametrize("T,M,K,E", [(70, 40, 24, 3), (70, 40, 23, 3), (1, 1, 1, 1), (0, 8, 8, 2), (5, 0, 8, 2), (5, 8, 0, 2),
+                                     (5, 1, 9, 2), (5, 9, 1, 2)])
+def test_both_ways_through_a_helper_agree(name, T, M, K, E):
+    call, out = helper_calls(T, M, K, E)[name]
+    short, longer = call(), call(**out)
+    g.gemm_poll_device_status()
+    given = next(iter(out.values()))
+    assert longer.data_ptr() == given.data_ptr() and short.dtype == longer.dtype
+    assert short.shape == longer.shape and torch.equal(short, longer)
+
+
+def wrong_arguments():
+    f16, i8 = dict(dtype=torch.float16, device="cuda"), dict(dtype=torch.int8, device="cuda")
+    off = torch.tensor([0, 2, 5], dtype=torch.int32, device="cuda")
+    A, Bt, dCt = torch.zeros(2, 16, 8, **f16), torch.zeros(5, 8, **f16), torch.zeros(5, 16, **f16)
+    qa, qb, sa, sb = torch.zeros(2, 16, 8, **i8), torch.zeros(5, 8, **i8), torch.ones(2, 16, device="cuda"), torch.ones(5, device="cuda")
+    for o in (off.long(), off[:2], off.cpu(), off[None]):
+        yield lambda o=o: g.tn_grouped(A, Bt, o)
+        yield lambda o=o: g.tn_grouped_grad_b(A, dCt, o)
+        yield lambda o=o: g.i8_tn_grouped(qa, qb, sa, sb, o)
+        if o.numel() == 3:
+            yield lambda o=o: g.tn_grouped_grad_a(dCt, Bt, o)
+    for b in (Bt.bfloat16(), Bt[:, :4].contiguous(), Bt.cpu(), Bt[0], Bt.float()):
+        yield lambda b=b: g.tn_grouped(A, b, off)
+        yield lambda b=b: g.tn_grouped_grad_b(A, b, off)
+        if b.dtype != torch.float16 or b.shape[0] != 5 or not b.is_cuda:
+            yield lambda b=b: g.tn_grouped_grad_a(dCt, b, off)
+    for a in (A.bfloat16(), A[0], A.cpu(), A.float()):
+        yield lambda a=a: g.tn_grouped(a, Bt, off)
+        yield lambda a=a: g.tn_grouped_grad_b(a, dCt, off)
+    yield lambda: g.tn_grouped_grad_a(dCt[:4], Bt, off)
+    for s in (sb[:4], sb.double(), sb.cpu(), sb[None], torch.ones(10, device="cuda")[::2]):
+        yield lambda s=s: g.i8_tn(qa[0], qb, sa[0], s)
+        yield lambda s=s: g.i8_tn_grouped(qa, qb, sa, s, off)
+    for s in (sa[0], sa.half(), sa.cpu(), sa.t(), sa[:1]):
+        yield lambda s=s: g.i8_tn_grouped(qa, qb, s, sb, off)
+    yield lambda: g.i8_tn(qa[0], qb, sa, sb)
+    for q in (qb.to(torch.uint8), qb[:, :4].contiguous(), qb.cpu(), qb[0]):
+        yield lambda q=q: g.i8_tn(qa[0], q, sa[0], sb)
+        yield lambda q=q: g.i8_tn_grouped(qa, q, sa, sb, off)
+    yield lambda: g.i8_tn(qa[0], qb, sa[0], sb, dtype=torch.float32)
+    yield lambda: g.i8_tn(qa[0], qb, sa[0], sb, C=torch.zeros(5, 16, **f16), dtype=torch.bfloat16)
+    yield lambda: g.tn_grouped(A, Bt, off, C=torch.zeros(5, 16, **f16).bfloat16())
+    yield lambda: g.tn_grouped(A, Bt, off, C=torch.zeros(5, 15, **f16))
+    yield lambda: g.tn_grouped_grad_a(dCt, Bt, off, dA=torch.zeros(1, 16, 8, **f16).expand(2, 16, 8))
+
+
+def test_helpers_refuse_what_does_not_fit_on_a_gpu():
+    """Nothing slips past the checks on a helper's short way."""
+    for i, call in enumerate(wrong_arguments()):
+        try:
+            call()
+        except (ValueError, g.GemmError):
+            continue
+        raise AssertionError(f"call {i} was not refused")
+    g.gemm_poll_device_status()
+
+
 def test_captured_replayed_and_two_graphs_at_once():
     cases = [small_case(1), small_case(50)]
     for c in cases:

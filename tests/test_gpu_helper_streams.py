@@ -87,3 +87,25 @@ def test_results_on_another_stream(name, as_handle):
     assert same(copies, want)
     del junk
     g.gemm_poll_device_status()
+
+
+def test_a_captured_call_on_a_forked_stream():
+    """The same calls with a stream argument inside a graph's capture, replayed."""
+    made, side = calls(), torch.cuda.Stream()
+    want = {name: tensors(made[name](None)) for name in NAMES}
+    torch.cuda.synchronize()
+    graph, got = torch.cuda.CUDAGraph(), {}
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        for name in NAMES[5:]:
+            got[name] = made[name](side)
+        torch.cuda.current_stream().wait_stream(side)
+    for _ in range(3):
+        for name in got:
+            for t in tensors(got[name]):
+                t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for name in got:
+            assert same(got[name], want[name]), name
+    g.gemm_poll_device_status()
