@@ -39,7 +39,10 @@ int64_t grouped_tiles(int64_t l_extent, int64_t l, int64_t T, int64_t E, int64_t
 // so it asks no device.  Measured on GB300, single CTAs / pairs: 1024 x 200 x 4096
 // (32 tiles) 11.9 / 19.7 us, 1024 x 1024 x 1024 (136) 8.7 / 11.9, 320 x 4178 x 2560
 // (198) 21.0 / 25.2, 4096 x 512 x 4096 (288) 30.3 / 24.8, 2048 x 2048 x 2048 (528)
-// 31.2 / 24.0.
+// 31.2 / 24.0.  The host knows the mean over all experts alone.  Where it is near the
+// bound and the rows go to few of them, pairs would be faster: 16 experts of 4096 x 2048
+// and 2000 rows 55.1 / 48.4 spread evenly, 53.9 / 38.9 over four, 53.1 / 36.1 over one;
+// 64 of 2048 x 2048 and 8000 rows 103.9 / 85.0, 102.5 / 62.5 over four.
 constexpr int64_t kI8DirectRows = 128, kI8DirectTiles = 228;
 
 bool i8_direct(int64_t M, int64_t T, int64_t E)
@@ -195,7 +198,7 @@ int co_resident(const void *kernel, const cudaLaunchConfig_t &cfg, int fallback)
 // won back.  slots: the device's co-resident clusters of 2, 4 and 8 (0 = not queried).
 // Measured on GB300, whole sums -> split: 1024 x 16 x 8192 in 8 bits (8 tiles)
 // 22.3 -> 10.3 us, 4096 x 16 x 4096 (32 tiles) 13.4 -> 9.7, 2048 x 16 x 1536 7.8 -> 7.5,
-// 2048 x 16 x 1024 6.8 -> 7.0; weight gradient of 8 experts of 8192 x 512 with 256 rows
+// 2048 x 16 x 1024 6.8 -> 7.0; token gradient of 8 experts of 8192 x 512 with 256 rows
 // 28.2 -> 19.1; and with more clusters of 8 than are resident, 2048 x 16 x 4096 14.0 -> 17.6.
 int grouped_split(const void *kernel, int threads, int smem, int64_t tiles, int64_t stages, int sms, int (&slots)[3])
 {
@@ -417,6 +420,9 @@ gemm_status_t launch_grouped_op(const GroupedCall &c, DeviceState &dev, tn::Grou
     // 35.8 / 28.6.  By tiles: 8 of 1024 x 4096 with 512 rows in all (128) 18.1 / 20.8,
     // 5 of 200 x 5240 with 2020 (72, the sum split) 17.8 / 34.9; 4 of 2048 x 2048 with
     // 400 (160) 10.8 / 10.4, 8 of 1024 x 1024 with 1024 (192) 11.2 / 8.6.
+    // The rows per expert are the mean over all, also where few experts get them; pairs
+    // would then be faster: 64 experts of 2048 x 2048 and 2000 rows 85.7 / 90.4 spread
+    // evenly, but 37.2 / 31.6 over 16 of them, 34.4 / 18.4 over four, 31.0 / 16.3 over one.
     const bool few = kOp != tn::kGrGradA &&
                      (c.T <= 32 * c.E || grouped_tiles(prm.l_extent, 128, c.T, c.E, 64) <= dev.sms);
     gemm_status_t st;
@@ -463,7 +469,9 @@ gemm_status_t launch_grouped_op(const GroupedCall &c, DeviceState &dev, tn::Grou
         // Short sums are bound by what surrounds them and by the stores: tiles of two
         // halves, half as many.  Measured on GB300, 256 -> 512 rows: 32 experts of 1024 x 2048
         // and 3008 rows 51.6 -> 44.5 us; but 8 of 8192 x 4096 and 8192 rows 324 -> 340 us, of
-        // 4096 x 4096 and 16384 rows 342 -> 343.
+        // 4096 x 4096 and 16384 rows 342 -> 343.  By the mean over all experts: near the bound,
+        // 32 of 1024 x 2048 and 8000 rows, 41.3 -> 43.6 spread evenly, 51.1 -> 57.1 where eight
+        // of them get the rows, 79.8 -> 105.6 where one does.
         if (c.M >= 512 && c.T <= 256 * c.E) return launch_grouped<kOp, 2, 512>(c, dev, prm, 2);
     }
     return launch_grouped<kOp, 2, 256>(c, dev, prm, 1);

@@ -1042,7 +1042,8 @@ __device__ __forceinline__ uint32_t f16x2_minus_1152(uint32_t v)
     return r;
 }
 
-// In the order 0, 2, 1, 3: what bounds the widening is the integer pipe, and a
+// (An integer in the low bits of a float whose exponent makes them its units is a known
+// trick.)  In the order 0, 2, 1, 3: what bounds the widening is the integer pipe, and a
 // mask is cheaper than byte permutations.  All operands are widened alike, so
 // each product still pairs a term with its own.
 __device__ __forceinline__ uint2 i8x4_to_f16x4(uint32_t w)

@@ -18,10 +18,12 @@
 // Schedule, ragged ends, bounded waits, split sums and the epilogue's steps are the
 // grouped kernel's.
 //
-// Measured on GB300: 16 experts of 4096 x 2048, 515 rows 32.0 us (4.4 TB/s; 512 tiles are
-// 3.4 waves and take the time of 4); 8192 x 16 x 2048 9.0 us replayed from a graph, where
-// start, epilogue and the join of two half sums are some 6 of them (11.0 us called from
-// Python, whose host time bounds it); 1024 x 16 x 8192 10.3 us on 64 CTAs.
+// Measured on GB300: 16 experts of 4096 x 2048, 515 rows 32.5 us (4.3 TB/s).  512 tiles are
+// 3.4 waves and take the time of 4; and between a tile's ends a stage takes 0.43 us from
+// memory (8192 x 16 on 128 CTAs, K = 4096 -> 8192: 11.6 -> 18.4 us, 4.9 TB/s; out of L2 0.33
+// us a stage).  8192 x 16 x 2048 9.0 us replayed from a graph, where start, epilogue and the
+// join of two half sums are some 6 of them (10.7 us called from Python, whose host time
+// bounds it); 1024 x 16 x 8192 10.3 us on 64 CTAs.
 #pragma once
 
 #include "grouped_kernel.cuh"
@@ -59,8 +61,8 @@ static_assert(kI8SmemBytes <= 232448, "exceeds the 227 KiB shared memory of one 
 // stay in 32 bits.  The runs of a longer sum are rounded to whole units of 2^s, s > 0,
 // so that it does, 2^s being less than a 32768th of the number of terms.
 //
-// Measured on GB300 against one accumulator for the whole sum, which was off by hundreds
-// where large parts cancel: single CTAs 8192 x 16 x 2048 and 1024 x 16 x 8192 no
+// Measured on GB300 against one accumulator for the whole sum, which was off by 1100 in
+// sums of 10000 whose halves of 16384 terms cancel: single CTAs 8192 x 16 x 2048 and 1024 x 16 x 8192 no
 // difference, 4096 x 192 x 8192 29.8 -> 30.9 us; pairs 8192 x 4096 x 8192 312 -> 323,
 // 8 experts of 4096 x 2048 with 4096 rows 57.4 -> 62.2, sums of one run (K = 1024)
 // 51.1 -> 53.2.  What it costs there is the widening warps' share of the SM, which
@@ -530,8 +532,8 @@ __global__ void __launch_bounds__(kI8Threads, 1) tn_i8_kernel(const __grid_const
 // The weights are again widened on the way, each CTA's 128 rows into its own
 // tensor memory; the tokens come widened to f16 (widen_rows_kernel; T x K, where
 // widening the weights as well would move five bytes for each of them first).
-// Bound by the tensor cores and the widening that feeds them: 8192 x 4096 x 8192 345 us
-// with the tokens' widening (1590 TFLOP/s; the f16 rate under the power cap is 1715).
+// Bound by the tensor cores and the widening that feeds them: 8192 x 4096 x 8192 340 us
+// with the tokens' widening (1620 TFLOP/s; the f16 rate under the power cap is 1715).
 //
 // Tiles of 256 (L) x up to 192 (R) rows: two accumulators of 192 columns and two
 // stages of widened weights of 64 fill the 512 TMEM columns.  A stage is 128
