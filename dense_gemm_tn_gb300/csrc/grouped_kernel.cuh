@@ -42,6 +42,7 @@
 // gradients 1390 (8192 rows, 14336 x 4096) and 1490 (16384 rows, 4096 x 4096).
 #pragma once
 
+#include "grouped_ptx.cuh"
 #include "repack_kernel.cuh"
 #include "tn_gemm_kernel.cuh"
 

@@ -126,3 +126,11 @@ def test_roofline_bound_peak_and_kernel_name():
     assert rf["bound"] == "hbm" and rf["algorithmic_bytes"] == alg
     assert abs(rf["achieved"] - alg / 0.01e-3 / 1e9) < 1e-6 and rf["peak"] == 6800.0
     assert rf["kernel"] == "tn_skinny_kernel<KindF16>"
+
+
+@pytest.mark.parametrize("workload", ["sq_8192", "e4m3_8192"])
+def test_traffic_records_of_the_bench_are_of_the_current_code(workload):
+    """The bench's roofline reports DRAM bytes only where the record was taken on the
+    kernel's present code; what other kernels alone use belongs in headers of theirs."""
+    import bench
+    assert bench.measured_traffic(workload) is not None
