@@ -342,9 +342,11 @@ gemm_status_t launch_i8(const GroupedCall &c, DeviceState &dev, tn::GroupedParam
 }
 
 // x as for launch_i8; tokens: the widened copy, ld_tokens elements a row.
+template <bool kRuns>
 gemm_status_t launch_i8_pair(const GroupedCall &c, DeviceState &dev, tn::GroupedParams &prm, const void *x, int64_t ldx,
                              int64_t stride_x, int64_t inner_x, const void *tokens, int64_t ld_tokens)
 {
+    using Cfg = tn::I8PairCfg<kRuns>;
     gemm_status_t st;
     const uint64_t apart = c.E > 1 ? uint64_t(stride_x) : uint64_t(16);
     if (prm.red > 0) {
@@ -357,7 +359,7 @@ gemm_status_t launch_i8_pair(const GroupedCall &c, DeviceState &dev, tn::Grouped
                                 16 * (i + 1), "rows")) != GEMM_OK)
                 return st;
     }
-    auto kernel = tn::tn_i8_pair_kernel;
+    auto kernel = tn::tn_i8_pair_kernel<kRuns>;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -366,19 +368,19 @@ gemm_status_t launch_i8_pair(const GroupedCall &c, DeviceState &dev, tn::Grouped
     attr[1].val.clusterDim.x = 2;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
-    cfg.blockDim = dim3(tn::kIpThreads, 1, 1);
-    cfg.dynamicSmemBytes = tn::kIpSmemBytes;
+    cfg.blockDim = dim3(Cfg::kThreads, 1, 1);
+    cfg.dynamicSmemBytes = Cfg::kSmemBytes;
     int slots;
     {
         std::lock_guard<std::mutex> lock(g_mutex);
-        int &n = dev.i8_pair_slots;
+        int &n = dev.i8_pair_slots[kRuns];
         if (n == 0) {
-            cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, tn::kIpSmemBytes);
+            cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmemBytes);
             if (e != cudaSuccess) return fail(GEMM_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
             // (with fewer registers its epilogue would wait for more than there are)
             cudaFuncAttributes fa;
             e = cudaFuncGetAttributes(&fa, kernel);
-            if (e != cudaSuccess || fa.numRegs < tn::kIpLaunchRegs)
+            if (e != cudaSuccess || (kRuns && fa.numRegs < tn::kIpLaunchRegs))
                 return fail(GEMM_ERR_CUDA, "%s: the kernel was compiled for fewer registers than it shares out", c.name);
             cfg.attrs = attr + 1;
             cfg.numAttrs = 1;
@@ -580,7 +582,8 @@ gemm_status_t run_grouped(const GroupedCall &c)
     prm.flags = stall_flags(g_inject_stall.load());
     prm.wait_limit_ns = g_wait_limit_ns.load();
     if (i8 && plan.y.widen)
-        st = launch_i8_pair(c, *dev, prm, x, ldx, stride_x, in_x, y, ldy);
+        st = red > tn::kI8Run * tn::kI8Block ? launch_i8_pair<true>(c, *dev, prm, x, ldx, stride_x, in_x, y, ldy)
+                                             : launch_i8_pair<false>(c, *dev, prm, x, ldx, stride_x, in_x, y, ldy);
     else if (i8)
         st = launch_i8(c, *dev, prm, x, y, ldx, stride_x, ldy, in_x, in_y);
     else if (grad_a)

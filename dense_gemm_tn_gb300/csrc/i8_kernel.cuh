@@ -62,12 +62,12 @@ static_assert(kI8SmemBytes <= 232448, "exceeds the 227 KiB shared memory of one 
 // so that it does, 2^s being less than a 32768th of the number of terms.
 //
 // Measured on GB300 against one accumulator for the whole sum, which was off by 1100 in
-// sums of 10000 whose halves of 16384 terms cancel: single CTAs 8192 x 16 x 2048 and 1024 x 16 x 8192 no
-// difference, 4096 x 192 x 8192 29.8 -> 30.9 us; pairs 8192 x 4096 x 8192 312 -> 323,
-// 8 experts of 4096 x 2048 with 4096 rows 57.4 -> 62.2, sums of one run (K = 1024)
-// 51.1 -> 53.2.  What it costs there is the widening warps' share of the SM, which
-// have no time to spare.  (Sums kept in floats until one comes to 2^24, read with
-// 32-lane loads, or held by twelve warps instead of eight were all slower.)
+// sums of 10000 whose halves of 16384 terms cancel: single CTAs 8192 x 16 x 2048 and
+// 1024 x 16 x 8192 no difference, 4096 x 192 x 8192 29.8 -> 30.9 us; pairs, K up to 1024,
+// no difference, 8192 x 4096 x 8192 313 -> 325, 8 experts of 4096 x 2048 with 4096 rows
+// 57.9 -> 62.5.  What it costs there is the widening warps' share of the SM, which have no
+// time to spare.  (Sums kept in floats until one comes to 2^24, read with 32-lane loads,
+// or held by twelve warps instead of eight were all slower.)
 constexpr int kI8Run = 1024 / kI8Block;                      // stages
 constexpr int32_t kI8MaxExact = 131071;                      // * 2^14 < 2^31
 
@@ -546,33 +546,42 @@ constexpr int kIpLBytes = 128 * 128;
 constexpr int kIpAtomBytes = kIpRowsR * 128;                 // 64 terms of a CTA's tokens
 constexpr int kIpStageBytes = kIpLBytes + 2 * kIpAtomBytes;
 constexpr int kIpStages = 4;                                 // (an even number: a team's stages are every other one)
-// Warps: two teams of four that widen, eight of the epilogue, one for the TMA and one
-// for the MMAs (and two that only wait).  The epilogue's sums of 96 columns a thread
-// want more registers than an even share, which the others give up.
-constexpr int kIpThreads = 640, kIpLaunchRegs = 96;
-constexpr int kIpEpiWarps = 8, kIpFirstEpi = 8, kIpTmaWarp = 16, kIpMmaWarp = 17;
-constexpr int kIpRegsLead = 64, kIpRegsWiden = 72, kIpRegsEpi = 136;
-static_assert(128 * kIpRegsLead + 256 * kIpRegsWiden + 256 * kIpRegsEpi <= kIpThreads * kIpLaunchRegs,
+// kRuns: sums of more than one run.  Warps: two teams of four that widen, four of the
+// epilogue (kRuns: eight), one for the TMA and one for the MMAs (kRuns: and two that only
+// wait, so that warps come in fours).  The sums of 96 columns a thread want more registers
+// than an even share, which the others give up.
+template <bool kRuns>
+struct I8PairCfg {
+    static constexpr int kEpiWarps = kRuns ? 8 : 4;
+    static constexpr int kTurns = kEpiWarps / 4;             // warps to a quarter of the lanes, which take steps in turn
+    static constexpr int kPieces = kIpRows / kGrChunk / kTurns;
+    static constexpr int kFirstEpi = 8, kTmaWarp = kFirstEpi + kEpiWarps, kMmaWarp = kTmaWarp + 1;
+    static constexpr int kThreads = 32 * (kTmaWarp + (kRuns ? 4 : 2));
+    // full8[S], fullr[S], empty[S], fulla[2], emptya[2], accfull[2], accempty[2], drain, never
+    static constexpr int kBarriers = 3 * kIpStages + 10;
+    static constexpr int kSmemBytes = 1024 /* alignment slack */ + kIpStages * kIpStageBytes + kEpiWarps * kGrStageBytes +
+                                      kBarriers * 8 + 32 + kIpStages * 4 + 2 * (kGrMaxExperts + 8) * 4;
+    static_assert(kSmemBytes <= 232448, "exceeds the 227 KiB shared memory of one CTA");
+};
+constexpr int kIpLaunchRegs = 96, kIpRegsLead = 64, kIpRegsWiden = 72, kIpRegsEpi = 136;
+static_assert(128 * kIpRegsLead + 256 * kIpRegsWiden + 256 * kIpRegsEpi <= I8PairCfg<true>::kThreads * kIpLaunchRegs,
               "no more registers than the block is launched with");
 constexpr uint32_t kIpACol0 = 2 * kIpRows;
 constexpr uint32_t kIpTmemCols = 512;
 static_assert(kIpACol0 + 2 * kI8ACols == kIpTmemCols, "the TMEM columns are all used");
 static_assert(kIpAtomBytes % 1024 == 0, "blocks start on the swizzle's 1024 bytes");
-// full8[S], fullr[S], empty[S], fulla[2], emptya[2], accfull[2], accempty[2], drain, never
-constexpr int kIpBarriers = 3 * kIpStages + 10;
-constexpr int kIpSmemBytes = 1024 /* alignment slack */ + kIpStages * kIpStageBytes + kIpEpiWarps * kGrStageBytes +
-                             kIpBarriers * 8 + 32 + kIpStages * 4 + 2 * (kGrMaxExperts + 8) * 4;
-static_assert(kIpSmemBytes <= 232448, "exceeds the 227 KiB shared memory of one CTA");
 
-__global__ void __launch_bounds__(kIpThreads, 1) tn_i8_pair_kernel(const __grid_constant__ GroupedParams p)
+template <bool kRuns>
+__global__ void __launch_bounds__(I8PairCfg<kRuns>::kThreads, 1) tn_i8_pair_kernel(const __grid_constant__ GroupedParams p)
 {
+    using Cfg = I8PairCfg<kRuns>;
     constexpr int kS = kIpStages;
 
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t s_ring = ptx::smem_addr(smem), s_staging = s_ring + kS * kIpStageBytes;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kS * kIpStageBytes + kIpEpiWarps * kGrStageBytes);
-    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + kIpBarriers);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kS * kIpStageBytes + Cfg::kEpiWarps * kGrStageBytes);
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + Cfg::kBarriers);
     volatile uint32_t *abort_flag = tmem_holder + 1;
     volatile uint32_t *issued_count = tmem_holder + 2;    // fills this CTA's producer issued
     volatile uint32_t *producer_done = tmem_holder + 3;   // set once this CTA's producer issues no more
@@ -609,7 +618,7 @@ __global__ void __launch_bounds__(kIpThreads, 1) tn_i8_pair_kernel(const __grid_
             ptx::mbar_init(fulla_bar(b), 2 * kI8TeamWarps);
             ptx::mbar_init(emptya_bar(b), 1);
             ptx::mbar_init(accfull_bar(b), 1);
-            ptx::mbar_init(accempty_bar(b), 2 * kIpEpiWarps);
+            ptx::mbar_init(accempty_bar(b), 2 * Cfg::kEpiWarps);
         }
         ptx::mbar_init(drain_bar, 1);
         ptx::mbar_init(never_bar, 1);
@@ -623,7 +632,7 @@ __global__ void __launch_bounds__(kIpThreads, 1) tn_i8_pair_kernel(const __grid_
         ptx::prefetch_tensormap(&p.tmap_l);
         ptx::prefetch_tensormap(&p.tmap_r[kIpRowsR / 16 - 1]);
     }
-    if (warp == kIpMmaWarp) {
+    if (warp == Cfg::kMmaWarp) {
         ptx::tmem_alloc<2>(ptx::smem_addr(tmem_holder), kIpTmemCols);
         ptx::tmem_relinquish_alloc_permit<2>();
     }
@@ -635,15 +644,15 @@ __global__ void __launch_bounds__(kIpThreads, 1) tn_i8_pair_kernel(const __grid_
 
     ptx::griddep_wait();                      // every thread's first global access is behind this wait
     const int32_t l_tiles = (p.l_extent + 255) / 256;
-    grouped_tables<kGrI8, kIpRows, kIpThreads>(p, l_tiles, start, before);
+    grouped_tables<kGrI8, kIpRows, Cfg::kThreads>(p, l_tiles, start, before);
     const int32_t total = before[p.E];
     const int32_t slot = static_cast<int32_t>(blockIdx.x) / 2, slots = static_cast<int32_t>(gridDim.x) / 2;
     GroupedWalk<kGrI8, kIpRows, kIpRows, 256, 32> walk{start, before, l_tiles, 0, p.red, 0};
     const int32_t blocks = (p.red + kI8Block - 1) / kI8Block;       // stages of a tile
 
-    if (warp >= kIpTmaWarp) {
-        ptx::setmaxnreg_dec<kIpRegsLead>();
-        if (warp == kIpTmaWarp) {
+    if (warp >= Cfg::kTmaWarp) {
+        if constexpr (kRuns) ptx::setmaxnreg_dec<kIpRegsLead>();
+        if (warp == Cfg::kTmaWarp) {
             // ------------------------------------------------ TMA producer (both CTAs)
             int stage = 0;
             uint32_t phase = 0, n_issued = 0;
@@ -717,7 +726,7 @@ __global__ void __launch_bounds__(kIpThreads, 1) tn_i8_pair_kernel(const __grid_
                     }
                 }
             }
-        } else if (warp == kIpMmaWarp) {
+        } else if (warp == Cfg::kMmaWarp) {
             if (pos == 0) {
                 // ------------------------------------------------ MMA issuer (even CTA)
                 int stage = 0;
@@ -738,7 +747,7 @@ __global__ void __launch_bounds__(kIpThreads, 1) tn_i8_pair_kernel(const __grid_
                         }
                         ptx::tc_fence_after_sync();
                         const int32_t left = p.red - i * kI8Block;
-                        const bool last = i + 1 == blocks || run + 1 == kI8Run;
+                        const bool last = i + 1 == blocks || (kRuns && run + 1 == kI8Run);
                         if (ptx::elect_one()) {
 #pragma unroll
                             for (int half = 0; half < 2; ++half) {
@@ -774,9 +783,9 @@ __global__ void __launch_bounds__(kIpThreads, 1) tn_i8_pair_kernel(const __grid_
                 }
             }
         }
-    } else if (warp < kIpFirstEpi) {
+    } else if (warp < Cfg::kFirstEpi) {
         // ------------------------------------------------ widening (both CTAs)
-        ptx::setmaxnreg_dec<kIpRegsWiden>();
+        if constexpr (kRuns) ptx::setmaxnreg_dec<kIpRegsWiden>();
         const int team = warp / kI8TeamWarps;
         static_assert(kS % 2 == 0, "a team's stages are every other one");
         const int quarter = warp & 3;
@@ -798,7 +807,7 @@ __global__ void __launch_bounds__(kIpThreads, 1) tn_i8_pair_kernel(const __grid_
                 ok = wait_warp(w, emptya_bar(team), phase_a ^ 1u, kSiteEmpty);
                 if (!ok) break;
                 ptx::tc_fence_after_sync();                   // the MMAs that read this TMEM stage are done
-                widen_row_to_tmem<2>(src, lane, v, t_a);
+                widen_row_to_tmem<kRuns ? 2 : 4>(src, lane, v, t_a);
                 ptx::tmem_st_wait();
                 ptx::tc_fence_before_sync();
                 __syncwarp();
@@ -816,16 +825,15 @@ __global__ void __launch_bounds__(kIpThreads, 1) tn_i8_pair_kernel(const __grid_
         }
     } else {
         // ------------------------------------------------ epilogue (both CTAs)
-        // Two warps to a quarter of the lanes, which take every other 32 columns.  Sums of
-        // one run are stored out of their accumulator; those of several gather in
-        // registers, and go back as floats to where the last run was.
-        ptx::setmaxnreg_inc<kIpRegsEpi>();
-        constexpr int kPieces = kIpRows / kGrChunk / 2;
-        const int quarter = warp & 3, turn = (warp - kIpFirstEpi) >> 2;
+        // The sums of several runs gather in registers, and go back as floats to the
+        // accumulator of the last one, out of which a tile is stored.
+        if constexpr (kRuns) ptx::setmaxnreg_inc<kIpRegsEpi>();
+        constexpr int kTurns = Cfg::kTurns, kPieces = Cfg::kPieces;
+        const int quarter = warp & 3, turn = (warp - Cfg::kFirstEpi) >> 2;
         const uint32_t t_lanes = tmem_base + (static_cast<uint32_t>(32 * quarter) << 16);
         const float unit = sum_unit(p.red);
         GroupedStore store;
-        store.init(s_staging + (warp - kIpFirstEpi) * kGrStageBytes, lane);
+        store.init(s_staging + (warp - Cfg::kFirstEpi) * kGrStageBytes, lane);
         store.ld = p.out_ld;
         uint32_t sub = 0;                                     // runs so far
         auto acc_full = [&]() {
@@ -839,7 +847,7 @@ __global__ void __launch_bounds__(kIpThreads, 1) tn_i8_pair_kernel(const __grid_
             if (lane == 0) ptx::mbar_arrive_remote(ptx::mapa_shared(accempty_bar(sub & 1u), 0));
         };
         for (int32_t u = slot; u < total; u += slots) {
-            if (blocks > kI8Run) {
+            if constexpr (kRuns) {
                 const int32_t n_mma = walk.at(u).n_mma[0];
                 uint32_t sum[kPieces][2][16];
 #pragma unroll
@@ -855,7 +863,7 @@ __global__ void __launch_bounds__(kIpThreads, 1) tn_i8_pair_kernel(const __grid_
                     if (!ok) break;
 #pragma unroll
                     for (int s = 0; s < kPieces; ++s) {
-                        const int32_t c = (2 * s + turn) * kGrChunk;
+                        const int32_t c = (kTurns * s + turn) * kGrChunk;
                         if (c >= n_mma) break;
                         uint32_t v[2][16];
                         load_piece(t_lanes + (sub & 1u) * kIpRows + c, v);
@@ -873,7 +881,7 @@ __global__ void __launch_bounds__(kIpThreads, 1) tn_i8_pair_kernel(const __grid_
                 if (!ok) break;
 #pragma unroll
                 for (int s = 0; s < kPieces; ++s) {
-                    const int32_t c = (2 * s + turn) * kGrChunk;
+                    const int32_t c = (kTurns * s + turn) * kGrChunk;
                     if (c >= n_mma) break;
                     piece_to_floats(sum[s], unit);
                     store_piece(t_lanes + (sub & 1u) * kIpRows + c, sum[s]);
@@ -890,12 +898,14 @@ __global__ void __launch_bounds__(kIpThreads, 1) tn_i8_pair_kernel(const __grid_
                 store.scale_l[i] = 8 * i + (lane >> 2) < store.wide
                                        ? __ldg(p.scale_l + static_cast<int64_t>(t.e) * p.l_extent + l0 + 8 * i + (lane >> 2))
                                        : 0.0f;
-            if (blocks <= kI8Run && !acc_full()) break;
+            if constexpr (!kRuns) {
+                if (!acc_full()) break;
+            }
 #pragma unroll 1
-            for (int32_t c = turn * kGrChunk; c < t.n_mma[0]; c += 2 * kGrChunk) {
+            for (int32_t c = turn * kGrChunk; c < t.n_mma[0]; c += kTurns * kGrChunk) {
                 uint32_t v[2][16];
                 load_piece(t_lanes + (sub & 1u) * kIpRows + c, v);
-                if (c + 2 * kGrChunk >= t.n_mma[0]) hand_back();
+                if (c + kTurns * kGrChunk >= t.n_mma[0]) hand_back();
                 if (p.out_fmt != 0)
                     store.step<true, true>(v, out + c * p.out_ld, t.rows - c, p.scale_r + row0 + c);
                 else
@@ -909,7 +919,7 @@ __global__ void __launch_bounds__(kIpThreads, 1) tn_i8_pair_kernel(const __grid_
     __syncwarp();                // .aligned barriers below need converged warps
     ptx::tc_fence_before_sync();
     ptx::cluster_sync();         // no CTA leaves while the other may still touch its shared memory
-    if (warp == kIpMmaWarp) {
+    if (warp == Cfg::kMmaWarp) {
         __syncwarp();
         ptx::tc_fence_after_sync();
         ptx::tmem_dealloc<2>(tmem_base, kIpTmemCols);

@@ -99,7 +99,7 @@ struct DeviceState {
     int grouped_slots[3][3] = {};     // co-resident tn_grouped_kernel CTAs or pairs, by operation and variant (0 = not queried)
     int split_slots[3][3] = {};       // co-resident clusters of 2, 4 and 8 single CTAs: product, its gradient by B, 8-bit
     bool i8_attr = false;             // tn_i8_kernel's shared-memory attribute set
-    int i8_pair_slots = 0;            // co-resident pairs of tn_i8_pair_kernel (0 = not queried)
+    int i8_pair_slots[2] = {};        // co-resident pairs of tn_i8_pair_kernel, by its kRuns (0 = not queried)
     // One lock per stream, held by a call from its first buffer lookup through
     // its last launch: a call is several launches (row copy, GEMM, reduce),
     // and two host threads' calls on one stream must not interleave them.

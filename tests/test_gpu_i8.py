@@ -114,7 +114,7 @@ def scaled_once(sums, sa, sb, dtype):
 @pytest.mark.parametrize("M,N,K", [(1, 1, 1024), (1, 1, 1025), (64, 65, 2049), (129, 16, 3000), (100, 5, 16384), (300, 200, 12300),
                                    (832, 32, 12160), (20000, 40, 4096), (33, 64, 100000), (16, 3, 131071),
                                    # CTA pairs
-                                   (2000, 1000, 1025), (520, 4097, 2064), (1290, 1537, 8191), (4096, 600, 16384), (8192, 257, 3001)])
+                                   (2000, 1000, 1024), (2000, 1000, 1025), (520, 4097, 2064), (1290, 1537, 8191), (4096, 600, 16384), (8192, 257, 3001)])
 def test_i8_sums_are_exact(M, N, K, kind):
     A, Bt = long_codes(kind, M, N, K, seed=K)
     sa, sb = scales(M, seed=3), scales(N, seed=4) / 64
