@@ -13,6 +13,8 @@ The same names as the C ABI:
     gemm_f16_tn_softmax_stats(M, N, K, A, lda, B, ldb, C, ldc, scale, row_max, row_sum, stream=None)
     gemm_tn_grouped / gemm_tn_grouped_grad_b / gemm_tn_grouped_grad_a / gemm_i8_tn / gemm_i8_tn_grouped /
         gemm_quantize_i8_rows: products grouped by expert with their gradients, 8-bit integer products, row quantiser
+    gemm_tn_gated / gemm_tn_gated_grad: gated projections act(gate) * up, dense and by expert, and their backward pass
+    gemm_tn_cross_entropy / gemm_tn_cross_entropy_grad: softmax cross entropy of a projection onto a vocabulary
     gemm_poll_device_status(stream=None)
 
 A, B and C are device pointers given as ints or as CUDA torch tensors (their
@@ -32,6 +34,8 @@ Convenience wrappers over torch tensors in TN storage:
     tn_grouped(A (E,M,K), Bt (T,K), offsets (E+1,) int32, C=None) -> (T, M); tn_grouped_grad_b, tn_grouped_grad_a
     i8_tn(A (M,K) int8, Bt (N,K) int8, scale_a (M,), scale_b (N,), C=None) -> (N, M); i8_tn_grouped
     quantize_i8_rows(x (rows, cols)) -> (int8 codes, scale (rows,))
+    tn_gated(A (2M,K) or (E,2M,K), Bt (T,K), offsets=None) -> (T, M); tn_gated_grad
+    tn_cross_entropy(A (M,K), Bt (N,K), targets (N,) int64) -> (loss (N,), lse (N,)); tn_cross_entropy_grad
 The (N, M) row-major result IS the column-major M x N matrix C with ldc = M.
 With a `stream`, new results are that stream's memory, as under torch.cuda.stream.
 """
@@ -62,6 +66,8 @@ EXPORTS = (
     "gemm_f8e4m3_tn_dscale", "gemm_quantize_e4m3", "gemm_f16_tn_softmax_stats",
     "gemm_grouped_workspace", "gemm_tn_grouped", "gemm_tn_grouped_grad_b", "gemm_tn_grouped_grad_a",
     "gemm_i8_tn", "gemm_i8_tn_grouped", "gemm_quantize_i8_rows",
+    "gemm_gated_workspace", "gemm_tn_gated", "gemm_tn_gated_grad",
+    "gemm_cross_entropy_workspace", "gemm_tn_cross_entropy", "gemm_tn_cross_entropy_grad",
 )
 
 GEMM_IN_F32 = 0
@@ -72,6 +78,12 @@ GEMM_GROUPED_PRODUCT = 0
 GEMM_GROUPED_GRAD_B = 1
 GEMM_GROUPED_GRAD_A = 2
 GEMM_GROUPED_I8 = 3
+
+GEMM_ACT_SILU = 0
+GEMM_ACT_GELU = 1
+GEMM_ACT_GELU_TANH = 2
+#: Activations of tn_gated by name.
+ACTIVATIONS = {"silu": GEMM_ACT_SILU, "gelu": GEMM_ACT_GELU, "gelu_tanh": GEMM_ACT_GELU_TANH}
 
 
 class GemmError(RuntimeError):
@@ -114,6 +126,19 @@ def _load() -> ctypes.CDLL:
     lib.gemm_i8_tn_grouped.restype = st
     lib.gemm_quantize_i8_rows.argtypes = [vp, st, i64, i64, i64, vp, i64, vp, vp]
     lib.gemm_quantize_i8_rows.restype = st
+    lib.gemm_gated_workspace.argtypes = [st, st, i64, i64, i64, i64, vp, i64, i64, vp, i64]
+    lib.gemm_gated_workspace.restype = i64
+    lib.gemm_tn_gated.argtypes = [st, st, i64, i64, i64, i64, vp, i64, i64, vp, i64, vp, vp, i64, vp, i64, vp, i64, vp]
+    lib.gemm_tn_gated.restype = st
+    lib.gemm_tn_gated_grad.argtypes = [st, st, i64, i64, i64, i64, vp, i64, i64, vp, i64, vp, vp, i64, vp, i64, vp, i64, i64,
+                                       vp, i64, vp, i64, vp]
+    lib.gemm_tn_gated_grad.restype = st
+    lib.gemm_cross_entropy_workspace.argtypes = [st, i64, i64, i64, vp, i64, vp, i64]
+    lib.gemm_cross_entropy_workspace.restype = i64
+    lib.gemm_tn_cross_entropy.argtypes = [st, i64, i64, i64, vp, i64, vp, i64, vp, vp, vp, vp, i64, vp]
+    lib.gemm_tn_cross_entropy.restype = st
+    lib.gemm_tn_cross_entropy_grad.argtypes = [st, i64, i64, i64, vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, i64, vp, i64, vp]
+    lib.gemm_tn_cross_entropy_grad.restype = st
     lib.gemm_status_string.argtypes = [st]
     lib.gemm_status_string.restype = ctypes.c_char_p
     lib.gemm_last_error.argtypes = []
@@ -278,6 +303,48 @@ def gemm_quantize_i8_rows(x, x_type, rows, cols, ldx, q, ldq, scale, stream=None
     """8-bit quantisation with a scale per row: codes into q, amax / 127 of each row into scale."""
     return _check(calls.gemm_quantize_i8_rows(_ptr(x), int(x_type), rows, cols, ldx, _ptr(q), ldq, _ptr(scale),
                                               _stream(stream)))
+
+
+def gemm_gated_workspace(grad, dense, E, M, K, T, A, lda, stride_a, B, ldb) -> int:
+    """Workspace bytes of gemm_tn_gated (grad 0) or gemm_tn_gated_grad (grad 1); dense: without offsets."""
+    n = calls.gemm_gated_workspace(int(grad), int(dense), E, M, K, T, _ptr(A), lda, stride_a, _ptr(B), ldb)
+    if n < 0:
+        raise ValueError("gemm_gated_workspace: argument out of range")
+    return n
+
+
+def gemm_tn_gated(type, act, E, M, K, T, A, lda, stride_a, B, ldb, offsets, H, ldh, P=None, ldp=0, workspace=None,
+                  workspace_bytes=0, stream=None) -> int:
+    return _check(calls.gemm_tn_gated(int(type), int(act), E, M, K, T, _ptr(A), lda, stride_a, _ptr(B), ldb, _ptr(offsets),
+                                      _ptr(H), ldh, _ptr(P), ldp, _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def gemm_tn_gated_grad(type, act, E, M, K, T, A, lda, stride_a, B, ldb, offsets, P, ldp, dH, lddh, dA, ldda, stride_da, dB,
+                       lddb, workspace=None, workspace_bytes=0, stream=None) -> int:
+    return _check(calls.gemm_tn_gated_grad(int(type), int(act), E, M, K, T, _ptr(A), lda, stride_a, _ptr(B), ldb,
+                                           _ptr(offsets), _ptr(P), ldp, _ptr(dH), lddh, _ptr(dA), ldda, stride_da, _ptr(dB),
+                                           lddb, _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def gemm_cross_entropy_workspace(grad, M, N, K, A, lda, B, ldb) -> int:
+    """Workspace bytes of gemm_tn_cross_entropy (grad 0) or gemm_tn_cross_entropy_grad (grad 1)."""
+    n = calls.gemm_cross_entropy_workspace(int(grad), M, N, K, _ptr(A), lda, _ptr(B), ldb)
+    if n < 0:
+        raise ValueError("gemm_cross_entropy_workspace: argument out of range")
+    return n
+
+
+def gemm_tn_cross_entropy(type, M, N, K, A, lda, B, ldb, targets, loss, lse, workspace=None, workspace_bytes=0,
+                          stream=None) -> int:
+    return _check(calls.gemm_tn_cross_entropy(int(type), M, N, K, _ptr(A), lda, _ptr(B), ldb, _ptr(targets), _ptr(loss),
+                                              _ptr(lse), _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def gemm_tn_cross_entropy_grad(type, M, N, K, A, lda, B, ldb, targets, lse, dloss, dA, ldda, dB, lddb, workspace=None,
+                               workspace_bytes=0, stream=None) -> int:
+    return _check(calls.gemm_tn_cross_entropy_grad(int(type), M, N, K, _ptr(A), lda, _ptr(B), ldb, _ptr(targets), _ptr(lse),
+                                                   _ptr(dloss), _ptr(dA), ldda, _ptr(dB), lddb, _ptr(workspace),
+                                                   workspace_bytes, _stream(stream)))
 
 
 def gemm_f16_tn_noalloc(M, N, K, A, lda, B, ldb, C, ldc, stream=None) -> int:
@@ -817,3 +884,163 @@ def quantize_i8_rows(x, stream=None):
     _check(calls.gemm_quantize_i8_rows(x.data_ptr(), kind, rows, cols, ldx, q.data_ptr(), max(cols, 1), scale.data_ptr(),
                                        _launch_stream(device.index, stream)))
     return q, scale
+
+
+# ---------------------------------------------------------------- gated projections and the vocabulary's loss
+def _gated_weights(A, dtype, offsets):
+    """(E, M, K, lda, stride_a) of gate and up rows: (E, 2 M, K) with offsets, (2 M, K) without."""
+    if offsets is None:
+        lda, stride_a = _rows(A, dtype, "A", cuda=False), 0
+        E, (rows, K) = 1, A.shape
+    else:
+        lda, stride_a = _experts(A, dtype, "A")
+        E, rows, K = A.shape
+        _vector(offsets, _torch.int32, E + 1, "offsets")
+    if rows % 2:
+        raise ValueError(f"A must have an even number of rows (gate rows, then up rows), not {rows}")
+    return E, rows // 2, K, lda, stride_a
+
+
+def _activation(act):
+    kind = ACTIVATIONS.get(act)
+    if kind is None:
+        raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}, not {act!r}")
+    return kind
+
+
+def tn_gated(A, Bt, offsets=None, act="silu", keep=False, H=None, P=None, stream=None):
+    """Gated projections: P^T[t] = A Bt[t] for A's M gate and M up rows, H^T[t, m] =
+    act(P^T[t, m]) P^T[t, M + m].  A (2 M, K) and Bt (T, K), or A (E, 2 M, K) and
+    offsets (E + 1,) int32 as in tn_grouped; all fp16 or all bf16, rows contiguous ->
+    H (T, M).  keep: returns (H, P) with the fp32 products P (T, 2 M), which
+    tn_gated_grad takes.  act: "silu", "gelu" or "gelu_tanh"."""
+    torch = _torch or _load_torch()
+    _tensors(torch, A, Bt)
+    dtype, device = A.dtype, A.device
+    half, kind = _half_type(dtype, "A"), _activation(act)
+    E, M, K, lda, stride_a = _gated_weights(A, dtype, offsets)
+    ldb, T = _tokens(Bt, dtype, K, "Bt"), Bt.shape[0]
+    if offsets is None:
+        _same_device(device, Bt=Bt)
+    else:
+        _same_device(device, Bt=Bt, offsets=offsets)
+    if _elsewhere(device.index):
+        with torch.cuda.device(device):
+            return tn_gated(A, Bt, offsets, act, keep, H, P, stream)
+    H, ldh = _result(H, (T, M), dtype, device, stream, "H")
+    ldp = 0
+    if keep or P is not None:
+        P, ldp = _result(P, (T, 2 * M), torch.float32, device, stream, "P")
+    a, b = A.data_ptr(), Bt.data_ptr()
+    n = calls.gemm_gated_workspace(0, offsets is None, E, M, K, T, a, lda, stride_a, b, ldb)
+    held = _workspace(device, stream, n) if n > 0 else None
+    _check(calls.gemm_tn_gated(half, kind, E, M, K, T, a, lda, stride_a, b, ldb, _ptr(offsets), H.data_ptr(), ldh, _ptr(P),
+                               ldp, held.data_ptr() if n > 0 else None, n, _launch_stream(device.index, stream)))
+    return H if P is None else (H, P)
+
+
+def tn_gated_grad(A, Bt, P, dHt, offsets=None, act="silu", dA=None, dBt=None, want_a=True, want_b=True, stream=None):
+    """The gradients of tn_gated: from its operands, its products P and the gradient
+    dHt (T, M) of its result -> (dA of A's shape, dBt (T, K)).  want_a, want_b: a
+    gradient that is not wanted is not computed, and None.  Rows of dBt that belong to
+    no expert are not written; an expert without rows has zeros in dA."""
+    torch = _torch or _load_torch()
+    _tensors(torch, A, Bt, P, dHt)
+    dtype, device = A.dtype, A.device
+    half, kind = _half_type(dtype, "A"), _activation(act)
+    E, M, K, lda, stride_a = _gated_weights(A, dtype, offsets)
+    ldb, T = _tokens(Bt, dtype, K, "Bt"), Bt.shape[0]
+    ldp = _rows(P, torch.float32, "P", (T, 2 * M), cuda=False)
+    lddh = _rows(dHt, dtype, "dHt", (T, M), cuda=False)
+    if offsets is None:
+        _same_device(device, Bt=Bt, P=P, dHt=dHt)
+    else:
+        _same_device(device, Bt=Bt, P=P, dHt=dHt, offsets=offsets)
+    if _elsewhere(device.index):
+        with torch.cuda.device(device):
+            return tn_gated_grad(A, Bt, P, dHt, offsets, act, dA, dBt, want_a, want_b, stream)
+    ldda = stride_da = lddb = 0
+    if want_a:
+        if dA is None:
+            dA = _empty(tuple(A.shape), dtype, device, stream)
+        if offsets is None:
+            ldda = _rows(dA, dtype, "dA", tuple(A.shape))
+        else:
+            ldda, stride_da = _experts(dA, dtype, "dA", tuple(A.shape))
+        _same_device(device, dA=dA)
+    if want_b:
+        dBt, lddb = _result(dBt, (T, K), dtype, device, stream, "dBt")
+    a, b = A.data_ptr(), Bt.data_ptr()
+    n = calls.gemm_gated_workspace(1, offsets is None, E, M, K, T, a, lda, stride_a, b, ldb)
+    held = _workspace(device, stream, n) if n > 0 else None
+    _check(calls.gemm_tn_gated_grad(half, kind, E, M, K, T, a, lda, stride_a, b, ldb, _ptr(offsets), P.data_ptr(), ldp,
+                                    dHt.data_ptr(), lddh, dA.data_ptr() if want_a else None, ldda, stride_da,
+                                    dBt.data_ptr() if want_b else None, lddb, held.data_ptr() if n > 0 else None, n,
+                                    _launch_stream(device.index, stream)))
+    return (dA if want_a else None), (dBt if want_b else None)
+
+
+def _result(t, shape, dtype, device, stream, name):
+    """(t, its row stride): a new tensor on the call's stream, or the caller's."""
+    if t is None:
+        return _empty(shape, dtype, device, stream), max(shape[1], 1)
+    ld = _rows(t, dtype, name, shape)
+    _same_device(device, **{name: t})
+    return t, ld
+
+
+def _loss_operands(A, Bt, **vectors):
+    """(GEMM_IN_..., M, N, K, lda, ldb) of a vocabulary A (M, K), tokens Bt (N, K) and what belongs to the tokens."""
+    torch = _torch or _load_torch()
+    _tensors(torch, A, Bt, *vectors.values())
+    half = _half_type(A.dtype, "A")
+    M, N, K, lda, ldb = _operands(A, Bt, A.dtype)
+    if M == 0 and N > 0:
+        raise ValueError("A has no rows: there are no classes")
+    for name, t in vectors.items():
+        _vector(t, torch.int64 if name == "targets" else torch.float32, N, name)
+    _same_device(A.device, **vectors)
+    return half, M, N, K, lda, ldb
+
+
+def tn_cross_entropy(A, Bt, targets, stream=None):
+    """Softmax cross entropy of Bt's rows against the classes A: A (M, K) and Bt (N, K),
+    both fp16 or both bf16, targets (N,) int64 -> (loss (N,), lse (N,)), fp32: lse[n] =
+    log sum_m exp(A[m] . Bt[n]), loss[n] = lse[n] - A[targets[n]] . Bt[n]; 0 for a
+    negative target, NaN for one of M or more.  The logits are never held."""
+    half, M, N, K, lda, ldb = _loss_operands(A, Bt, targets=targets)
+    torch, device = _torch, A.device
+    if _elsewhere(device.index):
+        with torch.cuda.device(device):
+            return tn_cross_entropy(A, Bt, targets, stream)
+    loss, lse = (_empty((N,), torch.float32, device, stream) for _ in range(2))
+    a, b = A.data_ptr(), Bt.data_ptr()
+    n = calls.gemm_cross_entropy_workspace(0, M, N, K, a, lda, b, ldb)
+    held = _workspace(device, stream, n) if n > 0 else None
+    _check(calls.gemm_tn_cross_entropy(half, M, N, K, a, lda, b, ldb, targets.data_ptr(), loss.data_ptr(), lse.data_ptr(),
+                                       held.data_ptr() if n > 0 else None, n, _launch_stream(device.index, stream)))
+    return loss, lse
+
+
+def tn_cross_entropy_grad(A, Bt, targets, lse, dloss, dA=None, dBt=None, want_a=True, want_b=True, stream=None):
+    """The gradients of tn_cross_entropy's loss: from its operands, its lse and the
+    gradient dloss (N,) fp32 of the loss -> (dA (M, K), dBt (N, K)).  want_a, want_b: a
+    gradient that is not wanted is not computed, and None."""
+    half, M, N, K, lda, ldb = _loss_operands(A, Bt, targets=targets, lse=lse, dloss=dloss)
+    torch, device = _torch, A.device
+    if _elsewhere(device.index):
+        with torch.cuda.device(device):
+            return tn_cross_entropy_grad(A, Bt, targets, lse, dloss, dA, dBt, want_a, want_b, stream)
+    ldda = lddb = 0
+    if want_a:
+        dA, ldda = _result(dA, (M, K), A.dtype, device, stream, "dA")
+    if want_b:
+        dBt, lddb = _result(dBt, (N, K), A.dtype, device, stream, "dBt")
+    a, b = A.data_ptr(), Bt.data_ptr()
+    n = calls.gemm_cross_entropy_workspace(1, M, N, K, a, lda, b, ldb)
+    held = _workspace(device, stream, n) if n > 0 else None
+    _check(calls.gemm_tn_cross_entropy_grad(half, M, N, K, a, lda, b, ldb, targets.data_ptr(), lse.data_ptr(),
+                                            dloss.data_ptr(), dA.data_ptr() if want_a else None, ldda,
+                                            dBt.data_ptr() if want_b else None, lddb, held.data_ptr() if n > 0 else None, n,
+                                            _launch_stream(device.index, stream)))
+    return (dA if want_a else None), (dBt if want_b else None)

@@ -17,7 +17,7 @@ LIB = os.path.join(PKG, "libdense_gemm_tn.so")
 SOURCES = [os.path.join(CSRC, "tn_gemm.cu")]
 DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in ("tn_gemm_kernel.cuh", "sm103_ptx.cuh", "quant_e4m3_kernel.cuh", "repack_kernel.cuh",
                                                      "aux_kernels.cuh", "skinny_kernel.cuh", "grouped_kernel.cuh", "grouped_ptx.cuh", "grouped_host.cuh", "i8_kernel.cuh",
-                                                     "quant_i8_kernel.cuh")] + [
+                                                     "quant_i8_kernel.cuh", "grouped_sinks.cuh", "sinks_host.cuh")] + [
     os.path.join(INCLUDE, "tn_gemm.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -28,7 +28,7 @@ def nvcc() -> str:
 
 
 def build_cmd(verbose_ptxas: bool = False) -> list[str]:
-    cmd = [nvcc(), "-std=c++17", "-O3", *ARCH, "-lineinfo", "-Xcompiler", "-fPIC", "-shared",
+    cmd = [nvcc(), "-std=c++17", "-O3", *ARCH, "-lineinfo", "--split-compile=0", "-Xcompiler", "-fPIC", "-shared",
            "-diag-suppress", "1160", "-I", INCLUDE, "-o", LIB, *SOURCES]
     if verbose_ptxas:
         cmd.insert(1, "-Xptxas=-v")

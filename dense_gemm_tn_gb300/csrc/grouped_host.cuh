@@ -258,8 +258,9 @@ gemm_status_t launch_grouped(const GroupedCall &c, DeviceState &dev, tn::Grouped
         }
         slots = n;
     }
-    const int64_t l_tiles = (int64_t(prm.l_extent) + Cfg::kTileL - 1) / Cfg::kTileL;
-    const int64_t r_tiles = kOp == tn::kGrGradA ? c.E * ((c.M + kRows - 1) / kRows)
+    constexpr int kReads = tn::grouped_reads(kOp), kSpan = kOp == tn::kGrGated ? Cfg::kTileL / 2 : Cfg::kTileL;
+    const int64_t l_tiles = (int64_t(prm.l_extent) + kSpan - 1) / kSpan;
+    const int64_t r_tiles = kReads == tn::kGrGradA ? c.E * ((c.M + kRows - 1) / kRows)
                                                 : c.T / kRows + (c.E < c.T ? c.E : c.T);   // an upper bound
     if (r_tiles > (int64_t(1) << 30) / l_tiles) return fail(GEMM_ERR_UNSUPPORTED, "%s: too many output tiles", c.name);
     const int64_t tiles = r_tiles * l_tiles;
@@ -425,13 +426,18 @@ gemm_status_t launch_grouped_op(const GroupedCall &c, DeviceState &dev, tn::Grou
     // The rows per expert are the mean over all, also where few experts get them; pairs
     // would then be faster: 64 experts of 2048 x 2048 and 2000 rows 85.7 / 90.4 spread
     // evenly, but 37.2 / 31.6 over 16 of them, 34.4 / 18.4 over four, 31.0 / 16.3 over one.
-    const bool few = kOp != tn::kGrGradA &&
-                     (c.T <= 32 * c.E || grouped_tiles(prm.l_extent, 128, c.T, c.E, 64) <= dev.sms);
+    constexpr int kReads = tn::grouped_reads(kOp);
+    const bool few = kReads != tn::kGrGradA &&
+                     (c.T <= 32 * c.E ||
+                      grouped_tiles(prm.l_extent, kOp == tn::kGrGated ? 64 : 128, c.T, c.E, 64) <= dev.sms);
     gemm_status_t st;
     if (prm.red > 0) {
         const CUtensorMapDataType type =
             prm.fmt ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-        if constexpr (kOp == tn::kGrGradA) {
+        if constexpr (kOp == tn::kGrGradAOne) {
+            if ((st = encode_2d(&prm.tmap_r[0], type, x, inner_x, c.T, ldx * 2, 64, tn::kGrBlock, "dC")) != GEMM_OK) return st;
+            if ((st = encode_2d(&prm.tmap_l, type, y, inner_y, c.T, ldy * 2, 64, tn::kGrBlock, "B")) != GEMM_OK) return st;
+        } else if constexpr (kOp == tn::kGrGradA) {
             tn::GroupedMapsParams m;
             memset(&m, 0, sizeof(m));
             if ((st = encode_2d(&m.dc, type, x, inner_x, c.T, ldx * 2, 64, tn::kGrBlock, "dC")) != GEMM_OK) return st;
@@ -456,16 +462,18 @@ gemm_status_t launch_grouped_op(const GroupedCall &c, DeviceState &dev, tn::Grou
             cudaError_t e = cudaLaunchKernelEx(&cfg, tn::grouped_maps_kernel, m);
             if (e != cudaSuccess) return fail(GEMM_ERR_CUDA, "%s: launch (tensor maps): %s", c.name, cudaGetErrorString(e));
         } else {
-            const uint32_t box_l = kOp == tn::kGrGradB ? 64 : 128;
+            const uint32_t box_l = kOp == tn::kGrGated ? 16 : kReads == tn::kGrGradB ? 64 : 128;
             const uint64_t apart = c.E > 1 ? uint64_t(stride_x) * 2 : uint64_t(16);
-            if ((st = encode_map(&prm.tmap_l, type, x, inner_x, c.M, ldx * 2, c.E, apart, 64, box_l, "A")) != GEMM_OK)
+            const uint64_t gate_to_up = kOp == tn::kGrGated ? uint64_t(c.M) * uint64_t(ldx) * 2 : 0;
+            if ((st = encode_map(&prm.tmap_l, type, x, inner_x, c.M, ldx * 2, c.E, apart, 64, box_l, "A", gate_to_up)) !=
+                GEMM_OK)
                 return st;
             for (uint32_t i = 0; i < (few ? 4 : 8); ++i)
                 if ((st = encode_2d(&prm.tmap_r[i], type, y, inner_y, c.T, ldy * 2, 64, 16 * (i + 1), "rows")) != GEMM_OK)
                     return st;
         }
     }
-    if constexpr (kOp != tn::kGrGradA) {
+    if constexpr (kReads != tn::kGrGradA) {
         if (few) return launch_grouped<kOp, 1, 64>(c, dev, prm, 0);
     } else {
         // Short sums are bound by what surrounds them and by the stores: tiles of two

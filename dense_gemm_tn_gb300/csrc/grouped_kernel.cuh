@@ -43,6 +43,7 @@
 #pragma once
 
 #include "grouped_ptx.cuh"
+#include "grouped_sinks.cuh"
 #include "repack_kernel.cuh"
 #include "tn_gemm_kernel.cuh"
 
@@ -54,8 +55,24 @@ constexpr int kGrRaster = 8;                 // R tiles per raster group
 constexpr int kGrChunk = 32;                 // accumulator columns per epilogue step
 constexpr int kGrStageBytes = kGrChunk * 64; // one epilogue warp's staging: 32 rows of 32 16-bit results
 
-// (kGrI8: the 8-bit kernels' product; tn_grouped_kernel has no such form.)
-enum GroupedOp : int { kGrProduct = 0, kGrGradB = 1, kGrGradA = 2, kGrI8 = 3 };
+// (kGrI8: the 8-bit kernels' product; tn_grouped_kernel has no such form.)  The
+// others read what one of the first three reads and end otherwise (grouped_sinks.cuh).
+enum GroupedOp : int {
+    kGrProduct = 0, kGrGradB = 1, kGrGradA = 2, kGrI8 = 3,
+    kGrGated = 4,            // a product of gate and up rows, act(gate) * up stored
+    kGrLossStats = 5,        // a product whose columns' softmax statistics are stored
+    kGrLossGrad = 6,         // a product whose softmax's loss gradient is stored
+    kGrGradBAdd = 7,         // a token gradient in parts, added up in FP32
+    kGrGradAOne = 8          // a weight gradient of one group, times a scale
+};
+constexpr int kGrOps = 9;
+
+// The one of the first three that an operation reads its operands as.
+__host__ __device__ constexpr int grouped_reads(int op)
+{
+    return op == kGrGated || op == kGrLossStats || op == kGrLossGrad ? kGrProduct
+           : op == kGrGradBAdd ? kGrGradB : op == kGrGradAOne ? kGrGradA : op;
+}
 
 constexpr int kGrEpiWarps = 8;               // epilogue warps: two per quarter of the TMEM lanes
 constexpr int kGrThreads = 64 + 32 * kGrEpiWarps;
@@ -113,6 +130,7 @@ struct GroupedParams {
     const float *scale_r;
     uint32_t flags;                  // kFlagStall* (test hooks)
     uint64_t wait_limit_ns;
+    SinkParams sink;                 // the operations from kGrGated on
 };
 
 // Waiter::wait by a converged warp, with one answer for all its lanes.
@@ -149,6 +167,8 @@ static_assert(row_tiles(0x7FFFFF00, 512) == 0x400000 && row_tiles(512, 512) == 1
 
 template <int kOp, int kRows, int kHalfRows, int kTileL, int kGran>
 struct GroupedWalk {
+    static constexpr int kReads = grouped_reads(kOp);
+    static constexpr int kSpan = kOp == kGrGated ? kTileL / 2 : kTileL;    // a gated tile holds gate and up rows
     const int32_t *start, *before;      // shared memory
     int32_t l_tiles, r_extent, red;
     int32_t e;
@@ -159,21 +179,21 @@ struct GroupedWalk {
         while (before[e + 1] <= u) ++e;
         GroupedTile t;
         const int32_t group_rows = start[e + 1] - start[e];
-        const int32_t rows = kOp == kGrGradA ? r_extent : group_rows;
+        const int32_t rows = kReads == kGrGradA ? r_extent : group_rows;
         const int32_t tiles = row_tiles(rows, kRows);
         // the rows in steps of kGran, spread evenly: the first `more` tiles have one more
         const int32_t steps = (rows + kGran - 1) / kGran, each = steps / tiles, more = steps - each * tiles;
         int64_t tr, tl;
         tile_coord(u - before[e], tiles, l_tiles, kGrRaster, tr, tl);
         t.e = e;
-        t.l0 = static_cast<int32_t>(tl) * kTileL;
+        t.l0 = static_cast<int32_t>(tl) * kSpan;
         const int32_t r = static_cast<int32_t>(tr);
         t.r0 = (r * each + (r < more ? r : more)) * kGran;
         const int32_t padded = (each + (r < more ? 1 : 0)) * kGran;
         t.rows = rows - t.r0 < padded ? rows - t.r0 : padded;
         t.n_mma[0] = padded < kHalfRows ? padded : kHalfRows;
         t.n_mma[1] = padded - t.n_mma[0];
-        t.red = kOp == kGrGradA ? group_rows : red;
+        t.red = kReads == kGrGradA ? group_rows : red;
         return t;
     }
 };
@@ -213,6 +233,26 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap
         : "memory");
 }
 
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int32_t x, int32_t y,
+                                            int32_t z, int32_t q)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::
+            "r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(q)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_4d_pair(uint32_t dst, const CUtensorMap *map, uint32_t bar, int32_t x,
+                                                 int32_t y, int32_t z, int32_t q)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(q)
+        : "memory");
+}
+
 // Makes a tensor map that another kernel wrote usable by this thread's TMA
 // instructions.
 __device__ __forceinline__ void acquire_tensormap(const CUtensorMap *map)
@@ -225,6 +265,7 @@ __device__ __forceinline__ void acquire_tensormap(const CUtensorMap *map)
 template <int kOp, int kRows, int kCtaThreads = kGrThreads>
 __device__ __forceinline__ void grouped_tables(const GroupedParams &p, int32_t l_tiles, int32_t *start, int32_t *before)
 {
+    constexpr int kReads = grouped_reads(kOp);
     const int32_t E = p.E, T = p.T;
     for (int32_t i = threadIdx.x; i <= E; i += kCtaThreads) {
         const int32_t o = p.offsets ? p.offsets[i] : (i == 0 ? 0 : T);
@@ -254,7 +295,7 @@ __device__ __forceinline__ void grouped_tables(const GroupedParams &p, int32_t l
         __syncwarp();
         int32_t sum = 0;
         for (int32_t i = i0; i < i1 && i < E; ++i) {
-            const int32_t rows = kOp == kGrGradA ? p.r_extent : start[i + 1] - start[i];
+            const int32_t rows = kReads == kGrGradA ? p.r_extent : start[i + 1] - start[i];
             sum += row_tiles(rows, kRows) * l_tiles;
         }
         int32_t acc = sum;
@@ -266,7 +307,7 @@ __device__ __forceinline__ void grouped_tables(const GroupedParams &p, int32_t l
         for (int32_t i = i0; i < i1; ++i) {
             before[i] = acc;
             if (i < E) {
-                const int32_t rows = kOp == kGrGradA ? p.r_extent : start[i + 1] - start[i];
+                const int32_t rows = kReads == kGrGradA ? p.r_extent : start[i + 1] - start[i];
                 acc += row_tiles(rows, kRows) * l_tiles;
             }
         }
@@ -370,6 +411,17 @@ struct GroupedStore {
     __device__ __forceinline__ void half(uint32_t t_row, int32_t first, int32_t steps, uint16_t *out, int32_t rows,
                                          const float *scale_r, ReadAll read_all) const
     {
+        each_step(t_row, first, steps, read_all, [&](int32_t s, const uint32_t (&v)[2][16]) {
+            const int32_t c = s * kGrChunk;
+            step<kBf16, kScaled>(v, out + c * ld, rows - c, kScaled ? scale_r + c : nullptr);
+        });
+    }
+
+    // The same, store(s, columns of step s) for each.
+    template <class ReadAll, class Store>
+    static __device__ __forceinline__ void each_step(uint32_t t_row, int32_t first, int32_t steps, ReadAll read_all,
+                                                     Store store)
+    {
         auto load = [&](int32_t s, uint32_t (&v)[2][16]) {
             ptx::tmem_ld_16x256b_x4(t_row + s * kGrChunk, v[0]);
             ptx::tmem_ld_16x256b_x4(t_row + (16u << 16) + s * kGrChunk, v[1]);
@@ -378,10 +430,6 @@ struct GroupedStore {
             ptx::tmem_ld_wait_all();
             ptx::reg_dependency(v[0]);
             ptx::reg_dependency(v[1]);
-        };
-        auto store = [&](int32_t s, const uint32_t (&v)[2][16]) {
-            const int32_t c = s * kGrChunk;
-            step<kBf16, kScaled>(v, out + c * ld, rows - c, kScaled ? scale_r + c : nullptr);
         };
         uint32_t va[2][16], vb[2][16];
         int32_t s = first;
@@ -494,7 +542,9 @@ __global__ void __launch_bounds__(kGrThreads, 1) tn_grouped_kernel(const __grid_
 {
     using Cfg = GroupedCfg<kGroup, kRows>;
     constexpr int kStages = Cfg::kStages, kAtoms = Cfg::kAtoms;
-    constexpr bool kLMajorK = kOp == kGrProduct, kRMajorK = kOp != kGrGradA;
+    constexpr int kReads = grouped_reads(kOp);
+    constexpr bool kLMajorK = kReads == kGrProduct, kRMajorK = kReads != kGrGradA;
+    constexpr bool kSinks = kOp >= kGrGated;      // the epilogue is one of grouped_sinks.cuh's
 
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -548,7 +598,7 @@ __global__ void __launch_bounds__(kGrThreads, 1) tn_grouped_kernel(const __grid_
     }
     if (kOp != kGrGradA && threadIdx.x == 32 && p.red > 0) {
         ptx::prefetch_tensormap(&p.tmap_l);
-        ptx::prefetch_tensormap(&p.tmap_r[Cfg::kRowsR / 16 - 1]);
+        ptx::prefetch_tensormap(&p.tmap_r[kReads == kGrGradA ? 0 : Cfg::kRowsR / 16 - 1]);
     }
     if (warp == 1) {
         ptx::tmem_alloc<kGroup>(ptx::smem_addr(tmem_holder), Cfg::kTmemCols);
@@ -566,11 +616,12 @@ __global__ void __launch_bounds__(kGrThreads, 1) tn_grouped_kernel(const __grid_
     // Every thread's first global access is behind this wait: the offsets, and
     // in grad_a the maps, may be the previous kernel's.
     ptx::griddep_wait();
-    const int32_t l_tiles = (p.l_extent + Cfg::kTileL - 1) / Cfg::kTileL;
+    constexpr int kSpan = kOp == kGrGated ? Cfg::kTileL / 2 : Cfg::kTileL, kCtaSpan = kSpan / kGroup;
+    const int32_t l_tiles = (p.l_extent + kSpan - 1) / kSpan;
     grouped_tables<kOp, kRows>(p, l_tiles, start, before);
     const int32_t total = before[p.E];
     // (grad_a's sums are the groups' own rows: not split)
-    constexpr bool kMaySplit = kGroup == 1 && kOp != kGrGradA;
+    constexpr bool kMaySplit = kGroup == 1 && kReads != kGrGradA;
     static_assert(!kMaySplit || kRows <= 2 * kGrChunk, "the pieces of a split sum are four by two at most");
     const int32_t split = kMaySplit ? p.split : 1;
     const int32_t ctas = kGroup * split;
@@ -600,18 +651,19 @@ __global__ void __launch_bounds__(kGrThreads, 1) tn_grouped_kernel(const __grid_
             int32_t mapped = -1;
             for (int32_t u = slot; ok && u < total; u += slots) {
                 const GroupedTile t = walk.at(u);
-                const int32_t l0 = t.l0 + static_cast<int32_t>(pos) * Cfg::kRowsL;
+                const int32_t l0 = t.l0 + static_cast<int32_t>(pos) * kCtaSpan;
                 int32_t cols[2], r0[2];       // this CTA's R elements of either half, and the first
                 uint32_t r_bytes = 0;
 #pragma unroll
                 for (int h = 0; h < Cfg::kHalves; ++h) {
                     cols[h] = t.n_mma[h] / kGroup;
-                    r0[h] = (kOp == kGrGradA ? 0 : start[t.e]) + t.r0 + h * Cfg::kHalfRows +
+                    r0[h] = (kReads == kGrGradA ? 0 : start[t.e]) + t.r0 + h * Cfg::kHalfRows +
                             static_cast<int32_t>(pos) * cols[h];
                     r_bytes += kRMajorK ? cols[h] * 128u
                                         : static_cast<uint32_t>((cols[h] + 63) / 64) * (kGrBlock * 128u);
                 }
                 const uint32_t fill = Cfg::kLBytes + r_bytes;
+                // (a weight gradient of one group: the call's own two maps)
                 const CUtensorMap *map_l = &p.tmap_l, *map_r = p.tmap_r;
                 if constexpr (kOp == kGrGradA) {
                     map_r = p.group_maps + 2 * t.e;
@@ -657,9 +709,18 @@ __global__ void __launch_bounds__(kGrThreads, 1) tn_grouped_kernel(const __grid_
                             else
                                 tma_load_3d(dst, map, bar, x, y, z);
                         };
-                        if constexpr (kLMajorK) {
+                        if constexpr (kOp == kGrGated) {
+                            // 16 gate rows, then the 16 up rows beside them, four times
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                if constexpr (kGroup == 2)
+                                    tma_load_4d_pair(s_l + q * 4096u, map_l, bar, k0, l0 + 16 * q, 0, t.e);
+                                else
+                                    tma_load_4d(s_l + q * 4096u, map_l, bar, k0, l0 + 16 * q, 0, t.e);
+                            }
+                        } else if constexpr (kLMajorK) {
                             load3(s_l, map_l, k0, l0, t.e);
-                        } else if constexpr (kOp == kGrGradB) {
+                        } else if constexpr (kReads == kGrGradB) {
                             load3(s_l, map_l, l0, k0, t.e);
                             load3(s_l + kGrBlock * 128, map_l, l0 + 64, k0, t.e);
                         } else {
@@ -882,14 +943,19 @@ __global__ void __launch_bounds__(kGrThreads, 1) tn_grouped_kernel(const __grid_
                 }
                 break;
             }
-            const int32_t l0 = t.l0 + static_cast<int32_t>(pos) * Cfg::kRowsL + 32 * quarter;   // this warp's 32
-            const int64_t row0 = static_cast<int64_t>(kOp == kGrGradA ? 0 : start[t.e]) + t.r0;
+            const int32_t l0 = t.l0 + static_cast<int32_t>(pos) * kCtaSpan + kCtaSpan / 4 * quarter;   // this warp's part
+            const int64_t row0 = static_cast<int64_t>(kReads == kGrGradA ? 0 : start[t.e]) + t.r0;
             uint16_t *out = p.out + t.e * p.out_stride + row0 * p.out_ld + l0;
             store.wide = p.l_extent - l0 < 32 ? p.l_extent - l0 : 32;
             store.vec = p.out_vec != 0 && store.wide == 32;
             if (t.red == 0) {                     // an empty sum
-                if (lane < store.wide)
+                if constexpr (kSinks) {
+                    const uint32_t zero[2][16] = {};
+                    for (int32_t c = turn * kGrChunk; c < t.rows; c += 2 * kGrChunk)
+                        Sink<kOp>::step(p, store, zero, l0, row0 + c, t.rows - c);
+                } else if (lane < store.wide) {
                     for (int32_t r = turn; r < t.rows; r += 2) out[r * p.out_ld + lane] = 0;
+                }
                 continue;
             }
 #pragma unroll 1
@@ -915,7 +981,12 @@ __global__ void __launch_bounds__(kGrThreads, 1) tn_grouped_kernel(const __grid_
                 };
                 uint16_t *dst = out + first * p.out_ld;
                 const int32_t rows = t.rows - first;
-                if (out_bf16)
+                if constexpr (kSinks)
+                    GroupedStore::each_step(t_row, turn, steps, hand_back, [&](int32_t s, const uint32_t (&v)[2][16]) {
+                        const int32_t c = s * kGrChunk;
+                        Sink<kOp>::step(p, store, v, l0, row0 + first + c, rows - c);
+                    });
+                else if (out_bf16)
                     store.half<true, false>(t_row, turn, steps, dst, rows, nullptr, hand_back);
                 else
                     store.half<false, false>(t_row, turn, steps, dst, rows, nullptr, hand_back);
@@ -931,20 +1002,23 @@ __global__ void __launch_bounds__(kGrThreads, 1) tn_grouped_kernel(const __grid_
             if (joins) {
                 const int quarter = warp & 3;
                 const GroupedTile t = walk.at(slot);
-                const int32_t l0 = t.l0 + 32 * quarter;
+                const int32_t l0 = t.l0 + kCtaSpan / 4 * quarter;
                 GroupedStore store;
                 store.init(s_staging + (warp - 2) * kGrStageBytes, lane);
                 store.ld = p.out_ld;
                 store.wide = p.l_extent - l0 < 32 ? p.l_extent - l0 : 32;
                 store.vec = p.out_vec != 0 && store.wide == 32;
-                uint16_t *out = p.out + (static_cast<int64_t>(start[t.e]) + t.r0) * p.out_ld + l0;
+                const int64_t row0 = static_cast<int64_t>(start[t.e]) + t.r0;
+                uint16_t *out = p.out + row0 * p.out_ld + l0;
                 for (int s = (warp - 2) >> 2; s * kGrChunk < t.n_mma[0]; s += 2) {
                     if (!parts.mine(quarter, s)) continue;
                     uint32_t v[2][16];
                     load_piece(tmem_base + (static_cast<uint32_t>(32 * quarter) << 16) + s * kGrChunk, v);
                     parts.add_others(parts.at(quarter, s, lane), v);
                     const int32_t c = s * kGrChunk;
-                    if (p.out_fmt != 0)
+                    if constexpr (kSinks)
+                        Sink<kOp>::step(p, store, v, l0, row0 + c, t.rows - c);
+                    else if (p.out_fmt != 0)
                         store.step<true, false>(v, out + c * p.out_ld, t.rows - c, nullptr);
                     else
                         store.step<false, false>(v, out + c * p.out_ld, t.rows - c, nullptr);

@@ -1,0 +1,536 @@
+// What the products of a language model's layers do with their accumulators
+// (tn_grouped_kernel's operations from kGrGated on), and the small kernels that
+// belong to them.
+//
+// A sink gets a warp's 32 x 32 piece of the accumulator as the kernel's epilogue
+// reads it: register v[q][4 i + 2 h + c] of lane t is column 8 i + 2 (t % 4) + c
+// and lane 16 q + 8 h + t / 4 of the piece.  Columns are the result's rows
+// (tokens), lanes its contiguous index.
+#pragma once
+
+#include <cstdint>
+#include <cuda_fp16.h>
+#include <cuda_bf16.h>
+
+#include "grouped_ptx.cuh"
+
+namespace tn {
+
+// (gemm_act_t of the C ABI)
+enum Act : int { kActSilu = 0, kActGelu = 1, kActGeluTanh = 2 };
+
+struct SinkParams {
+    int32_t act;                     // gated: Act
+    float *pre;                      // gated: the products themselves, T rows of [gate | up], or NULL
+    int64_t pre_ld;
+    const int64_t *targets;          // loss: a class per token; negative: ignored
+    float2 *stats;                   // loss: [ceil(classes / 32)][T] maximum, sum of exp(z - maximum)
+    float *z_target;                 // loss: [T] the target's logit
+    const float2 *rows;              // loss gradient: [T] (log-sum-exp, factor)
+    int32_t first, classes;          // loss gradient: the piece's first class, and how many
+    float *sum;                      // parts added up: FP32 sums
+    int64_t sum_ld;
+    int32_t add;                     // parts added up: AddPart
+    const float *out_scale;          // the result's factor (one float), or NULL
+};
+
+enum AddPart : int { kAddOnly = 0, kAddFirst = 1, kAddMore = 2, kAddLast = 3 };
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 1 / (1 + exp(-x)) (relative error about 2^-21).  exp overflows to an infinity
+// below -88, where the quotient is 0.
+__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.0f, 1.0f + ex2(-x * kLog2e)); }
+
+// y(x) with act(x) = x y(x):
+//   silu       sigmoid(x)
+//   gelu       the normal distribution function, erfc(-x / sqrt 2) / 2
+//   gelu_tanh  (1 + tanh z) / 2 = sigmoid(2 z), z = sqrt(2 / pi) (x + 0.044715 x^3)
+template <int kAct>
+__device__ __forceinline__ float act_factor(float x)
+{
+    if constexpr (kAct == kActSilu) return sigmoid(x);
+    if constexpr (kAct == kActGelu) return 0.5f * erfcf(-0.7071067811865476f * x);
+    return sigmoid(1.5957691216057308f * x * fmaf(0.044715f * x, x, 1.0f));
+}
+
+// act'(x) = y + x y'(x), y = act_factor(x).
+template <int kAct>
+__device__ __forceinline__ float act_slope(float x, float y)
+{
+    if constexpr (kAct == kActSilu) return fmaf(x * y, 1.0f - y, y);
+    if constexpr (kAct == kActGelu)
+        return fmaf(x, 0.3989422804014327f * ex2(-0.5f * kLog2e * x * x), y);
+    return fmaf(x * y * (1.0f - y), 1.5957691216057308f * fmaf(0.134145f * x, x, 1.0f), y);
+}
+
+template <int kOp>
+struct Sink;
+
+// ------------------------------------------------------------------ gated projections
+// The L operand's rows alternate, 16 gate rows and the 16 up rows beside them, so
+// a thread's v[0] and v[1] hold the gate and the up product of the same 16 results.
+template <>
+struct Sink<4 /* kGrGated */> {
+    template <int kAct, bool kBf16, class Store>
+    static __device__ __forceinline__ void store_h(const SinkParams &k, const Store &store, const uint32_t (&v)[2][16],
+                                                   uint16_t *out, int32_t wide, bool vec, int32_t rows)
+    {
+        const int lane = store.lane;
+        uint32_t h[4][2];                         // [8 columns][8 lanes]
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+            float x[2];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const float g = __uint_as_float(v[0][2 * r + c]), u = __uint_as_float(v[1][2 * r + c]);
+                x[c] = g * act_factor<kAct>(g) * u;
+            }
+            h[r >> 1][r & 1] = kBf16 ? ptx::pack_bf16x2(x[0], x[1]) : ptx::pack_f16x2(x[0], x[1]);
+        }
+        // Staging rows of 16 results (32 bytes), their two 16-byte pieces exchanged in
+        // every other four rows, so that eight rows' pieces meet no bank twice.
+        auto piece = [&](int row, int c) { return store.base + row * 32 + ((c ^ ((row >> 2) & 1)) << 4); };
+        __syncwarp();                             // the last step's pieces have been read
+#pragma unroll
+        for (int i = 0; i < 4; i += 2)
+            ptx::stmatrix_x4_trans(piece(8 * i + 8 * (lane >> 4) + (lane & 7), (lane >> 3) & 1), h[i][0], h[i][1],
+                                   h[i + 1][0], h[i + 1][1]);
+        __syncwarp();
+        if (vec) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int32_t r = 16 * q + (lane >> 1);
+                if (r < rows)
+                    *reinterpret_cast<uint4 *>(out + r * store.ld + 8 * (lane & 1)) = ptx::ld_shared_v4(piece(r, lane & 1));
+            }
+        } else {
+            const int32_t m = lane & 15, n = rows < 32 ? rows : 32;
+            if (m < wide)
+                for (int32_t r = lane >> 4; r < n; r += 2)
+                    out[r * store.ld + m] = ptx::ld_shared_u16(piece(r, m >> 3) + 2 * (m & 7));
+        }
+    }
+
+    template <class Params, class Store>
+    static __device__ __forceinline__ void step(const Params &p, const Store &store, const uint32_t (&v)[2][16],
+                                                int32_t l0, int64_t row, int32_t rows)
+    {
+        const SinkParams &k = p.sink;
+        const int lane = store.lane;
+        const int32_t wide = p.l_extent - l0 < 16 ? p.l_extent - l0 : 16;
+        if (k.pre) {
+            // Eight lanes hold eight neighbouring results of a row: whole sectors.
+            const int32_t c0 = 2 * (lane & 3), m0 = lane >> 2;
+            float *gate = k.pre + (row + c0) * k.pre_ld + l0 + m0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float *at = gate + (8 * i + c) * k.pre_ld;
+                    if (8 * i + c0 + c < rows) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            if (m0 + 8 * h < wide) {
+                                at[8 * h] = __uint_as_float(v[0][4 * i + 2 * h + c]);
+                                at[p.l_extent + 8 * h] = __uint_as_float(v[1][4 * i + 2 * h + c]);
+                            }
+                    }
+                }
+        }
+        uint16_t *out = p.out + row * p.out_ld + l0;
+        const bool vec = p.out_vec != 0 && wide == 16;
+        auto all = [&](auto bf16) {
+            constexpr bool kBf16 = decltype(bf16)::value;
+            switch (k.act) {
+            case kActSilu: return store_h<kActSilu, kBf16>(k, store, v, out, wide, vec, rows);
+            case kActGelu: return store_h<kActGelu, kBf16>(k, store, v, out, wide, vec, rows);
+            default: return store_h<kActGeluTanh, kBf16>(k, store, v, out, wide, vec, rows);
+            }
+        };
+        if (p.out_fmt != 0)
+            all(Flag<true>{});
+        else
+            all(Flag<false>{});
+    }
+
+    template <bool kValue>
+    struct Flag {
+        static constexpr bool value = kValue;
+    };
+};
+
+// ------------------------------------------------------------------ loss
+// A token's 32 logits of the piece become their maximum and the sum of their
+// exponentials above it, both in FP32; cross_entropy_join_kernel adds up the
+// pieces.  A thread's four logits of a column first give its own pair; pairs are
+// then merged over the eight lanes that share the columns, half of the columns
+// passed on each time: 7 exchanges of a pair for 8 columns.
+template <>
+struct Sink<5 /* kGrLossStats */> {
+    static __device__ __forceinline__ void merge(float &m, float &s, float om, float os)
+    {
+        const float top = fmaxf(m, om);
+        // (a piece without a logit above -inf: nothing to scale)
+        const float a = m == top ? s : s * ex2((m - top) * kLog2e), b = om == top ? os : os * ex2((om - top) * kLog2e);
+        m = top;
+        s = a + b;
+    }
+
+    template <class Params, class Store>
+    static __device__ __forceinline__ void step(const Params &p, const Store &store, const uint32_t (&v)[2][16],
+                                                int32_t l0, int64_t row, int32_t rows)
+    {
+        if (l0 >= p.l_extent) return;             // (past the last class: no piece)
+        const SinkParams &k = p.sink;
+        const int lane = store.lane;
+        const int32_t m0 = l0 + (lane >> 2);
+        const float none = __int_as_float(0xff800000);
+        float m[8], s[8];                         // [2 i + c]
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float z[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    z[q] = m0 + 8 * q < p.l_extent ? __uint_as_float(v[q >> 1][4 * i + 2 * (q & 1) + c]) : none;
+                const float top = fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3]));
+                // a maximum of -inf: of classes past the end alone, or of logits that are
+                const float from = top == none ? 0.0f : top;
+                float sum = 0.0f;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) sum += ex2((z[q] - from) * kLog2e);
+                m[2 * i + c] = top;
+                s[2 * i + c] = sum;
+            }
+        // after the three turns a lane holds column 8 (2 b4 + b3) + 2 (lane % 4) + b2 (bn: bit n of it)
+#pragma unroll
+        for (int d = 4, bit = 16; d >= 1; d /= 2, bit /= 2) {
+            const bool upper = lane & bit;
+#pragma unroll
+            for (int j = 0; j < d; ++j) {
+                const float om = __shfl_xor_sync(0xffffffffu, upper ? m[j] : m[j + d], bit);
+                const float os = __shfl_xor_sync(0xffffffffu, upper ? s[j] : s[j + d], bit);
+                float mm = upper ? m[j + d] : m[j], ss = upper ? s[j + d] : s[j];
+                merge(mm, ss, om, os);
+                m[j] = mm;
+                s[j] = ss;
+            }
+        }
+        const int32_t col = 8 * (2 * (lane >> 4 & 1) + (lane >> 3 & 1)) + 2 * (lane & 3) + (lane >> 2 & 1);
+        if (col < rows) k.stats[static_cast<int64_t>(l0 >> 5) * p.T + row + col] = make_float2(m[0], s[0]);
+        // the target's logit, where this piece has it
+        int64_t at = -1;
+        if (lane < rows) at = __ldg(k.targets + row + lane) - l0;
+        uint32_t hits = __ballot_sync(0xffffffffu, at >= 0 && at < 32 && l0 + at < p.l_extent);
+        while (hits) {
+            const int32_t c = __ffs(hits) - 1;
+            hits &= hits - 1;
+            const int32_t q = __shfl_sync(0xffffffffu, static_cast<int32_t>(at), c);
+            if ((lane & 3) == ((c & 7) >> 1) && lane >> 2 == (q & 7)) {
+                const int32_t want = 16 * (q >> 4) + 4 * (c >> 3) + 2 * (q >> 3 & 1) + (c & 1);
+#pragma unroll
+                for (int r = 0; r < 32; ++r)
+                    if (r == want) k.z_target[row + c] = __uint_as_float(v[r >> 4][r & 15]);
+            }
+        }
+    }
+};
+
+// d = (exp(z - lse) - [m = target]) factor, rounded to the operands' type: what the
+// tensor cores multiply in both gradients.  (fp16: the factors are scaled up so that
+// the largest is near 2^13, see cross_entropy_rows_kernel; d then keeps its relative
+// precision down to 2^-27 of it.)  Classes past the piece's end are zeros: the
+// products over the piece read them.
+template <>
+struct Sink<6 /* kGrLossGrad */> {
+    template <class Params, class Store>
+    static __device__ __forceinline__ void step(const Params &p, const Store &store, const uint32_t (&v)[2][16],
+                                                int32_t l0, int64_t row, int32_t rows)
+    {
+        const SinkParams &k = p.sink;
+        const int lane = store.lane;
+        const int32_t m0 = l0 + (lane >> 2);
+        uint32_t d[2][16];
+        int64_t at = -1;
+        if (lane < rows) at = __ldg(k.targets + row + lane) - k.first - l0;
+        const uint32_t hits = __ballot_sync(0xffffffffu, at >= 0 && at < 32);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int32_t col = 8 * i + 2 * (lane & 3) + c;
+                float2 r = make_float2(0.0f, 0.0f);
+                if (col < rows) r = __ldg(k.rows + row + col);
+                int32_t hit = -1;
+                if (hits) {                       // (the whole warp: the exchange is every lane's)
+                    hit = __shfl_sync(0xffffffffu, static_cast<int32_t>(at), col);
+                    if (!(hits >> col & 1)) hit = -1;
+                }
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int b = 4 * i + 2 * (q & 1) + c;
+                    float x = ex2((__uint_as_float(v[q >> 1][b]) - r.x) * kLog2e);
+                    if (hit == (lane >> 2) + 8 * q) x -= 1.0f;
+                    // (an ignored token's logits may be anything)
+                    x = r.y == 0.0f || m0 + 8 * q >= k.classes ? 0.0f : x * r.y;
+                    d[q >> 1][b] = __float_as_uint(x);
+                }
+            }
+        uint16_t *out = p.out + row * p.out_ld + l0;
+        if (p.out_fmt != 0)
+            store.template step<true, false>(d, out, rows, nullptr);
+        else
+            store.template step<false, false>(d, out, rows, nullptr);
+    }
+};
+
+// ------------------------------------------------------------------ sums in parts
+// A sum over parts of the vocabulary, one launch each: the first leaves FP32 sums,
+// the next ones add theirs (each element once a launch, so the order is the
+// launches'), and the last one's result is rounded once.
+template <>
+struct Sink<7 /* kGrGradBAdd */> {
+    template <class Params, class Store>
+    static __device__ __forceinline__ void step(const Params &p, const Store &store, const uint32_t (&v)[2][16],
+                                                int32_t l0, int64_t row, int32_t rows)
+    {
+        const SinkParams &k = p.sink;
+        const int lane = store.lane;
+        const int32_t c0 = 2 * (lane & 3), m0 = lane >> 2;
+        float *sum = k.sum + (row + c0) * k.sum_ld + l0 + m0;
+        uint32_t x[2][16];
+        const float scale = k.out_scale ? __ldg(k.out_scale) : 1.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float *at = sum + (8 * i + c) * k.sum_ld;
+                const bool inside = k.add != kAddOnly && 8 * i + c0 + c < rows;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int b = 4 * i + 2 * (q & 1) + c;
+                    float y = __uint_as_float(v[q >> 1][b]);
+                    if (inside && m0 + 8 * q < store.wide) {
+                        if (k.add == kAddFirst)
+                            at[8 * q] = y;
+                        else if (k.add == kAddMore)
+                            asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(at + 8 * q), "f"(y) : "memory");
+                        else
+                            y += at[8 * q];
+                    }
+                    x[q >> 1][b] = __float_as_uint(y * scale);
+                }
+            }
+        if (k.add == kAddFirst || k.add == kAddMore) return;
+        uint16_t *out = p.out + row * p.out_ld + l0;
+        if (p.out_fmt != 0)
+            store.template step<true, false>(x, out, rows, nullptr);
+        else
+            store.template step<false, false>(x, out, rows, nullptr);
+    }
+};
+
+template <>
+struct Sink<8 /* kGrGradAOne */> {
+    template <class Params, class Store>
+    static __device__ __forceinline__ void step(const Params &p, const Store &store, const uint32_t (&v)[2][16],
+                                                int32_t l0, int64_t row, int32_t rows)
+    {
+        const float scale = p.sink.out_scale ? __ldg(p.sink.out_scale) : 1.0f;
+        uint32_t x[2][16];
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int b = 0; b < 16; ++b) x[q][b] = __float_as_uint(__uint_as_float(v[q][b]) * scale);
+        uint16_t *out = p.out + row * p.out_ld + l0;
+        if (p.out_fmt != 0)
+            store.template step<true, false>(x, out, rows, nullptr);
+        else
+            store.template step<false, false>(x, out, rows, nullptr);
+    }
+};
+
+// ------------------------------------------------------------------ loss: joins
+// The pieces' pairs of each token, in the order of the classes within a slice and of
+// the slices (so results repeat): `lanes` tokens a CTA (a power of two), 512 / lanes
+// slices.  Reads 8 bytes per token and 32 classes.
+constexpr int kJoinThreads = 512;
+
+struct JoinParams {
+    const float2 *stats;
+    const float *z_target;
+    const int64_t *targets;
+    float *loss, *lse;
+    int64_t N, classes;
+    int32_t pieces, lanes;
+};
+
+__global__ void __launch_bounds__(kJoinThreads) cross_entropy_join_kernel(const JoinParams p)
+{
+    __shared__ float2 part[kJoinThreads];
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    const int32_t lane = threadIdx.x & (p.lanes - 1), slice = threadIdx.x / p.lanes, slices = kJoinThreads / p.lanes;
+    const int64_t n = static_cast<int64_t>(blockIdx.x) * p.lanes + lane;
+    const float none = __int_as_float(0xff800000);
+    float m = none, s = 0.0f;
+    if (n < p.N) {
+        const int32_t per = (p.pieces + slices - 1) / slices;
+        const int32_t q0 = slice * per, q1 = min(q0 + per, p.pieces);
+#pragma unroll 8
+        for (int32_t q = q0; q < q1; ++q) {
+            const float2 x = p.stats[static_cast<int64_t>(q) * p.N + n];
+            Sink<5>::merge(m, s, x.x, x.y);
+        }
+    }
+    part[threadIdx.x] = make_float2(m, s);
+    for (int32_t half = slices / 2; half >= 1; half /= 2) {
+        __syncthreads();
+        if (slice < half) {
+            const float2 x = part[threadIdx.x + half * p.lanes];
+            Sink<5>::merge(m, s, x.x, x.y);
+            part[threadIdx.x] = make_float2(m, s);
+        }
+    }
+    if (slice == 0 && n < p.N) {
+        const float lse = m + logf(s);
+        p.lse[n] = lse;
+        const int64_t t = p.targets[n];
+        p.loss[n] = t < 0 ? 0.0f : t < p.classes ? lse - p.z_target[n] : __int_as_float(0x7fffffff);
+    }
+}
+
+// The loss gradient's factor of each token: the loss's own gradient, 0 where the
+// target is negative, NaN where it is no class; for fp16 times a power of two that
+// takes the largest into [2^13, 2^14), which `scale` undoes.  One CTA.
+constexpr int kRowsThreads = 1024;
+
+struct LossRowsParams {
+    const int64_t *targets;
+    const float *lse, *dloss;
+    float2 *rows;
+    float *scale;
+    int64_t N, classes;
+    bool half;
+};
+
+__global__ void __launch_bounds__(kRowsThreads) cross_entropy_rows_kernel(const LossRowsParams p)
+{
+    __shared__ float tops[kRowsThreads / 32];
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    auto factor = [&p](int64_t n) {
+        const int64_t t = p.targets[n];
+        return t < 0 ? 0.0f : t < p.classes ? p.dloss[n] : __int_as_float(0x7fffffff);
+    };
+    float up = 1.0f;
+    if (p.half) {
+        float top = 0.0f;
+        for (int64_t n = threadIdx.x; n < p.N; n += kRowsThreads) top = fmaxf(top, fabsf(factor(n)));
+        for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = top;
+        __syncthreads();
+        for (int i = 0; i < kRowsThreads / 32; ++i) top = fmaxf(top, tops[i]);
+        // (0, an infinity or a NaN: as they are; the power and its inverse stay normal numbers)
+        if (top > 0.0f && top < __int_as_float(0x7f800000)) {
+            int e = 13 - ilogbf(top);
+            e = e > 120 ? 120 : e < -120 ? -120 : e;
+            up = ldexpf(1.0f, e);
+        }
+    }
+    for (int64_t n = threadIdx.x; n < p.N; n += kRowsThreads) p.rows[n] = make_float2(p.lse[n], factor(n) * up);
+    if (threadIdx.x == 0) *p.scale = 1.0f / up;
+}
+
+// ------------------------------------------------------------------ gated: backward
+// d_gate = dH u act'(g) and d_up = dH act(g) from the kept products, rounded to the
+// operands' type: 8 bytes of products and 2 of dH read, 4 written an element, nothing
+// else.  kVec: 4 elements a thread (rows on 16- and 8-byte boundaries).
+constexpr int kGatedGradThreads = 256;
+
+struct GatedGradParams {
+    const float *pre;
+    int64_t pre_ld;
+    const uint16_t *dh;
+    int64_t dh_ld;
+    uint16_t *dp;                    // T rows of [gate | up], then zeros to dp_ld
+    int64_t dp_ld;
+    const int32_t *offsets;          // rows before the first and from the last on are left out; or NULL
+    int32_t E, T, M;
+};
+
+template <int kAct, bool kBf16, bool kVec>
+__global__ void __launch_bounds__(kGatedGradThreads) gated_grad_kernel(const GatedGradParams p)
+{
+    constexpr int kN = kVec ? 4 : 1;
+    __shared__ int32_t ends[kGatedGradThreads / 32];
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    int32_t begin = 0, end = p.T;
+    if (p.offsets) {                              // read as the products read them
+        auto clamped = [&](int32_t i) {
+            const int32_t o = p.offsets[i];
+            return o < 0 ? 0 : (o > p.T ? p.T : o);
+        };
+        int32_t top = 0;
+        for (int32_t i = threadIdx.x; i <= p.E; i += kGatedGradThreads) top = max(top, clamped(i));
+        top = __reduce_max_sync(0xffffffffu, top);
+        if ((threadIdx.x & 31) == 0) ends[threadIdx.x >> 5] = top;
+        __syncthreads();
+        end = 0;
+        for (int i = 0; i < kGatedGradThreads / 32; ++i) end = max(end, ends[i]);
+        begin = clamped(0);
+    }
+    auto value = [](uint16_t b) {
+        return kBf16 ? __uint_as_float(static_cast<uint32_t>(b) << 16) : __half2float(__ushort_as_half(b));
+    };
+    auto round2 = [](float a, float b) { return kBf16 ? ptx::pack_bf16x2(a, b) : ptx::pack_f16x2(a, b); };
+    const int32_t units = (p.M + kN - 1) / kN;
+    for (int64_t row = begin + blockIdx.y; row < end; row += gridDim.y) {
+        const float *gate = p.pre + row * p.pre_ld, *up = gate + p.M;
+        const uint16_t *dh = p.dh + row * p.dh_ld;
+        uint16_t *dp = p.dp + row * p.dp_ld;
+        for (int32_t i = blockIdx.x * kGatedGradThreads + threadIdx.x; i < units; i += gridDim.x * kGatedGradThreads) {
+            float g[kN], u[kN], d[kN], dg[kN], du[kN];
+            if constexpr (kVec) {
+                const float4 a = __ldcs(reinterpret_cast<const float4 *>(gate) + i);
+                const float4 b = __ldcs(reinterpret_cast<const float4 *>(up) + i);
+                const uint2 c = __ldcs(reinterpret_cast<const uint2 *>(dh) + i);
+                g[0] = a.x, g[1] = a.y, g[2] = a.z, g[3] = a.w;
+                u[0] = b.x, u[1] = b.y, u[2] = b.z, u[3] = b.w;
+                d[0] = value(c.x), d[1] = value(c.x >> 16), d[2] = value(c.y), d[3] = value(c.y >> 16);
+            } else {
+                g[0] = gate[i];
+                u[0] = up[i];
+                d[0] = value(dh[i]);
+            }
+#pragma unroll
+            for (int q = 0; q < kN; ++q) {
+                const float y = act_factor<kAct>(g[q]);
+                dg[q] = d[q] * u[q] * act_slope<kAct>(g[q], y);
+                du[q] = d[q] * (g[q] * y);
+            }
+            if constexpr (kVec) {
+                reinterpret_cast<uint2 *>(dp)[i] = make_uint2(round2(dg[0], dg[1]), round2(dg[2], dg[3]));
+                reinterpret_cast<uint2 *>(dp + p.M)[i] = make_uint2(round2(du[0], du[1]), round2(du[2], du[3]));
+            } else {
+                const uint32_t x = round2(dg[0], du[0]);
+                dp[i] = static_cast<uint16_t>(x);
+                dp[p.M + i] = static_cast<uint16_t>(x >> 16);
+            }
+        }
+        if (blockIdx.x == 0)                      // the products read whole 16-byte units of a row
+            for (int64_t c = 2 * static_cast<int64_t>(p.M) + threadIdx.x; c < p.dp_ld; c += kGatedGradThreads) dp[c] = 0;
+    }
+}
+
+}  // namespace tn

@@ -252,6 +252,71 @@ static PyObject *py_gemm_quantize_i8_rows(PyObject *self, PyObject *const *args,
                                                        (float *)v[7].p, v[8].p));
 }
 
+/* (grad, dense, E, M, K, T, A, lda, stride_a, B, ldb) -> bytes */
+static PyObject *py_gemm_gated_workspace(PyObject *self, PyObject *const *args, Py_ssize_t nargs)
+{
+    (void)self;
+    arg_value v[11];
+    if (!read_args("gemm_gated_workspace", "iillllpllpl", args, nargs, v)) return NULL;
+    return PyLong_FromLongLong(gemm_gated_workspace(v[0].i, v[1].i, v[2].l, v[3].l, v[4].l, v[5].l, v[6].p, v[7].l, v[8].l,
+                                                    v[9].p, v[10].l));
+}
+
+/* (type, act, E, M, K, T, A, lda, stride_a, B, ldb, offsets, H, ldh, P, ldp, workspace, workspace_bytes, stream) */
+static PyObject *py_gemm_tn_gated(PyObject *self, PyObject *const *args, Py_ssize_t nargs)
+{
+    (void)self;
+    arg_value v[19];
+    if (!read_args("gemm_tn_gated", "iillllpllplpplplplp", args, nargs, v)) return NULL;
+    return PyLong_FromLong((long)gemm_tn_gated(v[0].i, v[1].i, v[2].l, v[3].l, v[4].l, v[5].l, v[6].p, v[7].l, v[8].l,
+                                               v[9].p, v[10].l, (const int32_t *)v[11].p, v[12].p, v[13].l,
+                                               (float *)v[14].p, v[15].l, v[16].p, v[17].l, v[18].p));
+}
+
+/* (type, act, E, M, K, T, A, lda, stride_a, B, ldb, offsets, P, ldp, dH, lddh, dA, ldda, stride_da, dB, lddb, workspace,
+ * workspace_bytes, stream) */
+static PyObject *py_gemm_tn_gated_grad(PyObject *self, PyObject *const *args, Py_ssize_t nargs)
+{
+    (void)self;
+    arg_value v[24];
+    if (!read_args("gemm_tn_gated_grad", "iillllpllplpplplpllplplp", args, nargs, v)) return NULL;
+    return PyLong_FromLong((long)gemm_tn_gated_grad(
+        v[0].i, v[1].i, v[2].l, v[3].l, v[4].l, v[5].l, v[6].p, v[7].l, v[8].l, v[9].p, v[10].l, (const int32_t *)v[11].p,
+        (const float *)v[12].p, v[13].l, v[14].p, v[15].l, v[16].p, v[17].l, v[18].l, v[19].p, v[20].l, v[21].p, v[22].l,
+        v[23].p));
+}
+
+/* (grad, M, N, K, A, lda, B, ldb) -> bytes */
+static PyObject *py_gemm_cross_entropy_workspace(PyObject *self, PyObject *const *args, Py_ssize_t nargs)
+{
+    (void)self;
+    arg_value v[8];
+    if (!read_args("gemm_cross_entropy_workspace", "illlplpl", args, nargs, v)) return NULL;
+    return PyLong_FromLongLong(gemm_cross_entropy_workspace(v[0].i, v[1].l, v[2].l, v[3].l, v[4].p, v[5].l, v[6].p, v[7].l));
+}
+
+/* (type, M, N, K, A, lda, B, ldb, targets, loss, lse, workspace, workspace_bytes, stream) */
+static PyObject *py_gemm_tn_cross_entropy(PyObject *self, PyObject *const *args, Py_ssize_t nargs)
+{
+    (void)self;
+    arg_value v[14];
+    if (!read_args("gemm_tn_cross_entropy", "illlplplpppplp", args, nargs, v)) return NULL;
+    return PyLong_FromLong((long)gemm_tn_cross_entropy(v[0].i, v[1].l, v[2].l, v[3].l, v[4].p, v[5].l, v[6].p, v[7].l,
+                                                       (const int64_t *)v[8].p, (float *)v[9].p, (float *)v[10].p, v[11].p,
+                                                       v[12].l, v[13].p));
+}
+
+/* (type, M, N, K, A, lda, B, ldb, targets, lse, dloss, dA, ldda, dB, lddb, workspace, workspace_bytes, stream) */
+static PyObject *py_gemm_tn_cross_entropy_grad(PyObject *self, PyObject *const *args, Py_ssize_t nargs)
+{
+    (void)self;
+    arg_value v[18];
+    if (!read_args("gemm_tn_cross_entropy_grad", "illlplplpppplplplp", args, nargs, v)) return NULL;
+    return PyLong_FromLong((long)gemm_tn_cross_entropy_grad(
+        v[0].i, v[1].l, v[2].l, v[3].l, v[4].p, v[5].l, v[6].p, v[7].l, (const int64_t *)v[8].p, (const float *)v[9].p,
+        (const float *)v[10].p, v[11].p, v[12].l, v[13].p, v[14].l, v[15].p, v[16].l, v[17].p));
+}
+
 static PyMethodDef methods[] = {
     {"gemm_f16_tn", (PyCFunction)(void (*)(void))py_gemm_f16_tn, METH_FASTCALL,
      "gemm_f16_tn(M, N, K, A, lda, B, ldb, C, ldc, stream) -> status"},
@@ -284,6 +349,22 @@ static PyMethodDef methods[] = {
      "workspace_bytes, stream) -> status"},
     {"gemm_quantize_i8_rows", (PyCFunction)(void (*)(void))py_gemm_quantize_i8_rows, METH_FASTCALL,
      "gemm_quantize_i8_rows(x, x_type, rows, cols, ldx, q, ldq, scale, stream) -> status"},
+    {"gemm_gated_workspace", (PyCFunction)(void (*)(void))py_gemm_gated_workspace, METH_FASTCALL,
+     "gemm_gated_workspace(grad, dense, E, M, K, T, A, lda, stride_a, B, ldb) -> bytes"},
+    {"gemm_tn_gated", (PyCFunction)(void (*)(void))py_gemm_tn_gated, METH_FASTCALL,
+     "gemm_tn_gated(type, act, E, M, K, T, A, lda, stride_a, B, ldb, offsets, H, ldh, P, ldp, workspace, workspace_bytes, "
+     "stream) -> status"},
+    {"gemm_tn_gated_grad", (PyCFunction)(void (*)(void))py_gemm_tn_gated_grad, METH_FASTCALL,
+     "gemm_tn_gated_grad(type, act, E, M, K, T, A, lda, stride_a, B, ldb, offsets, P, ldp, dH, lddh, dA, ldda, stride_da, "
+     "dB, lddb, workspace, workspace_bytes, stream) -> status"},
+    {"gemm_cross_entropy_workspace", (PyCFunction)(void (*)(void))py_gemm_cross_entropy_workspace, METH_FASTCALL,
+     "gemm_cross_entropy_workspace(grad, M, N, K, A, lda, B, ldb) -> bytes"},
+    {"gemm_tn_cross_entropy", (PyCFunction)(void (*)(void))py_gemm_tn_cross_entropy, METH_FASTCALL,
+     "gemm_tn_cross_entropy(type, M, N, K, A, lda, B, ldb, targets, loss, lse, workspace, workspace_bytes, stream) -> "
+     "status"},
+    {"gemm_tn_cross_entropy_grad", (PyCFunction)(void (*)(void))py_gemm_tn_cross_entropy_grad, METH_FASTCALL,
+     "gemm_tn_cross_entropy_grad(type, M, N, K, A, lda, B, ldb, targets, lse, dloss, dA, ldda, dB, lddb, workspace, "
+     "workspace_bytes, stream) -> status"},
     {NULL, NULL, 0, NULL},
 };
 

@@ -1,0 +1,492 @@
+// Host side of the gated projections and of the vocabulary's loss (included by
+// tn_gemm.cu, inside its anonymous namespace).  Like the grouped products these
+// calls keep nothing in the library: all their buffers are the caller's workspace.
+
+// Sections of a workspace, each from a 256-byte boundary on.
+struct Sections {
+    uint8_t *base;
+    size_t at = 0;
+    template <typename T>
+    T *take(size_t n)
+    {
+        T *p = reinterpret_cast<T *>(base + at);
+        at += (n * sizeof(T) + 255) & ~size_t(255);
+        return p;
+    }
+};
+
+gemm_status_t check_workspace(const char *name, const void *workspace, int64_t bytes, size_t need, const char *query)
+{
+    if (need == 0) return GEMM_OK;
+    if (!workspace || bytes < static_cast<int64_t>(need))
+        return fail(GEMM_ERR_INVALID_ARG, "%s: the workspace has %lld bytes, %zu are needed (%s)", name,
+                    (long long)(workspace ? bytes : 0), need, query);
+    if (reinterpret_cast<uintptr_t>(workspace) % 256)
+        return fail(GEMM_ERR_INVALID_ARG, "%s: the workspace is not 256-byte aligned", name);
+    return GEMM_OK;
+}
+
+bool aligned_to(const void *p, uintptr_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+
+tn::GroupedParams sink_params(const GroupedCall &c, int64_t l_extent, int64_t red, void *out, int64_t ldo)
+{
+    tn::GroupedParams prm;
+    memset(&prm, 0, sizeof(prm));
+    prm.offsets = c.offsets;
+    prm.out = static_cast<uint16_t *>(out);
+    prm.out_ld = ldo;
+    prm.E = static_cast<int32_t>(c.E);
+    prm.T = static_cast<int32_t>(c.T);
+    prm.l_extent = static_cast<int32_t>(l_extent);
+    prm.red = static_cast<int32_t>(red);
+    prm.fmt = prm.out_fmt = c.type == GEMM_IN_BF16 ? 1u : 0u;
+    prm.out_vec = aligned_to(out, 16) && ldo % 8 == 0;
+    prm.split = 1;
+    prm.flags = stall_flags(g_inject_stall.load());
+    prm.wait_limit_ns = g_wait_limit_ns.load();
+    return prm;
+}
+
+// The operands of a call as the TMA reads them: in place, or copied into the workspace.
+struct SinkOperands {
+    const void *x, *y;
+    int64_t ldx, stride_x, ldy, in_x, in_y;
+};
+
+gemm_status_t place_operands(const char *name, DeviceState &dev, const GroupedPlan &plan, Sections &ws,
+                             const int32_t *offsets, cudaStream_t stream, SinkOperands &o)
+{
+    o = {plan.x.base, plan.y.base, plan.x.ld, plan.x.stride, plan.y.ld, plan.x.inner, plan.y.inner};
+    if (plan.x.copy) {
+        o.x = ws.take<uint8_t>(plan.x.copy_bytes);
+        o.ldx = o.in_x = plan.x.copy_ld;
+        o.stride_x = plan.x.rows * o.ldx;
+    }
+    if (plan.y.copy) {
+        o.y = ws.take<uint8_t>(plan.y.copy_bytes);
+        o.ldy = o.in_y = plan.y.copy_ld;
+    }
+    if (!plan.x.copy && !plan.y.copy) return GEMM_OK;
+    return launch_widen<uint16_t>(name, dev, plan, const_cast<void *>(o.x), const_cast<void *>(o.y), offsets, stream);
+}
+
+template <typename... Args>
+gemm_status_t launch_plain(const char *name, void (*kernel)(Args...), dim3 grid, int threads, size_t smem,
+                           cudaStream_t stream, Args... args)
+{
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+    if (e != cudaSuccess) return fail(GEMM_ERR_CUDA, "%s: launch: %s", name, cudaGetErrorString(e));
+    return GEMM_OK;
+}
+
+// ------------------------------------------------------------------ gated projections
+bool gated_sizes_fit(int64_t E, int64_t M, int64_t K, int64_t T, int64_t lda, int64_t ldb, int64_t stride)
+{
+    return M <= kMaxDim / 2 && grouped_sizes_fit(E, 2 * M, K, T, lda, ldb, stride);
+}
+
+struct GatedPlan {
+    GroupedPlan g;               // the copies (and the backward pass's tensor maps)
+    int64_t ldd;                 // the backward pass's rows of 2 M gradients, padded
+    size_t bytes;
+    bool fits;
+};
+
+// A is read along its rows in the forward pass and across them in the backward pass.
+GatedPlan gated_plan(bool grad, bool dense, int64_t E, int64_t M, int64_t K, int64_t T, const void *A, int64_t lda,
+                     int64_t stride_a, const void *B, int64_t ldb)
+{
+    GatedPlan p{};
+    p.fits = true;
+    p.ldd = (2 * M + 63) / 64 * 64;
+    if (grouped_idle(E, M, K, T)) return p;
+    if (!grad) {
+        p.g = grouped_plan(GEMM_GROUPED_PRODUCT, E, 2 * M, K, T, A, lda, stride_a, B, ldb);
+        p.bytes = p.g.bytes();
+        p.fits = p.g.fits;
+        return p;
+    }
+    p.g.x = grouped_operand(A, 2 * M, E, K, lda, stride_a, false, false);
+    p.g.y = grouped_operand(B, T, 1, K, ldb, 0, false, false);
+    p.g.map_bytes = dense ? 0 : size_t(E) * 2 * sizeof(CUtensorMap);
+    p.fits = grouped_copy(p.g.x, false, false) && grouped_copy(p.g.y, false, false) && T <= (int64_t(1) << 60) / p.ldd;
+    p.bytes = p.g.bytes() + ((size_t(T) * size_t(p.ldd) * 2 + 255) & ~size_t(255));
+    return p;
+}
+
+int64_t gated_workspace(int grad, int dense, int64_t E, int64_t M, int64_t K, int64_t T, const void *A, int64_t lda,
+                        int64_t stride_a, const void *B, int64_t ldb)
+{
+    if (E < 0 || M < 0 || K < 0 || T < 0 || lda < 1 || ldb < 1 || lda < K || ldb < K || stride_a < 0 || (dense && E != 1) ||
+        !gated_sizes_fit(E, M, K, T, lda, ldb, stride_a))
+        return -1;
+    const GatedPlan p = gated_plan(grad != 0, dense != 0, E, M, K, T, A, lda, stride_a, B, ldb);
+    return p.fits ? static_cast<int64_t>(p.bytes) : -1;
+}
+
+// What the forward and the backward call check alike.
+gemm_status_t check_gated(const char *name, int type, int act, int64_t E, int64_t M, int64_t K, int64_t T, int64_t lda,
+                          int64_t stride_a, int64_t ldb, const int32_t *offsets)
+{
+    if (type != GEMM_IN_F16 && type != GEMM_IN_BF16)
+        return fail(GEMM_ERR_INVALID_ARG, "%s: unknown or unsupported type %d (GEMM_IN_F16 or GEMM_IN_BF16)", name, type);
+    if (act < GEMM_ACT_SILU || act > GEMM_ACT_GELU_TANH)
+        return fail(GEMM_ERR_INVALID_ARG, "%s: unknown activation %d", name, act);
+    if (E < 0 || M < 0 || K < 0 || T < 0)
+        return fail(GEMM_ERR_INVALID_ARG, "%s: negative size (E=%lld M=%lld K=%lld rows=%lld)", name, (long long)E,
+                    (long long)M, (long long)K, (long long)T);
+    if (lda < 1 || lda < K || ldb < 1 || ldb < K)
+        return fail(GEMM_ERR_INVALID_ARG, "%s: a leading dimension is below its row's length", name);
+    if (stride_a < 0) return fail(GEMM_ERR_INVALID_ARG, "%s: negative stride", name);
+    if (!offsets && E != 1) return fail(GEMM_ERR_INVALID_ARG, "%s: offsets is NULL, and there is not one expert", name);
+    if (!aligned_to(offsets, 4)) return fail(GEMM_ERR_INVALID_ARG, "%s: offsets is not 4-byte aligned", name);
+    if (!gated_sizes_fit(E, M, K, T, lda, ldb, stride_a))
+        return fail(GEMM_ERR_UNSUPPORTED, "%s: more than %d experts, or a size, leading dimension or stride too large", name,
+                    tn::kGrMaxExperts);
+    return GEMM_OK;
+}
+
+gemm_status_t run_gated(int type, int act, int64_t E, int64_t M, int64_t K, int64_t T, const void *A, int64_t lda,
+                        int64_t stride_a, const void *B, int64_t ldb, const int32_t *offsets, void *H, int64_t ldh, float *P,
+                        int64_t ldp, void *workspace, int64_t workspace_bytes, cudaStream_t stream)
+{
+    const char *name = "gemm_tn_gated";
+    gemm_status_t st = check_gated(name, type, act, E, M, K, T, lda, stride_a, ldb, offsets);
+    if (st != GEMM_OK) return st;
+    if (ldh < 1 || ldh < M || (P && (ldp < 1 || ldp < 2 * M)))
+        return fail(GEMM_ERR_INVALID_ARG, "%s: a leading dimension is below its row's length", name);
+    if (ldh > kMaxDim || (P && ldp > kMaxDim))
+        return fail(GEMM_ERR_UNSUPPORTED, "%s: a leading dimension is too large", name);
+    if (E == 0 || M == 0 || T == 0) return GEMM_OK;
+    if (!H) return fail(GEMM_ERR_INVALID_ARG, "%s: the result is NULL", name);
+    if (!aligned_to(H, 2) || !aligned_to(P, 4))
+        return fail(GEMM_ERR_INVALID_ARG, "%s: a result is not aligned to its element size", name);
+    if (K > 0 && (!A || !B)) return fail(GEMM_ERR_INVALID_ARG, "%s: an operand is NULL", name);
+    if (K > 0 && (!aligned_to(A, 2) || !aligned_to(B, 2)))
+        return fail(GEMM_ERR_INVALID_ARG, "%s: an operand is not aligned to its element size", name);
+    const GatedPlan plan = gated_plan(false, !offsets, E, M, K, T, A, lda, stride_a, B, ldb);
+    if (!plan.fits) return fail(GEMM_ERR_UNSUPPORTED, "%s: the operands' copies are too large", name);
+    if ((st = check_workspace(name, workspace, workspace_bytes, plan.bytes, "gemm_gated_workspace")) != GEMM_OK) return st;
+    DeviceState *dev = nullptr;
+    if ((st = device_state(&dev, nullptr)) != GEMM_OK) return st;
+
+    Sections ws{static_cast<uint8_t *>(workspace)};
+    SinkOperands o{};
+    if (K > 0 && (st = place_operands(name, *dev, plan.g, ws, offsets, stream, o)) != GEMM_OK) return st;
+    GroupedCall c{name, GEMM_GROUPED_PRODUCT, type, type, E, M, K, T};
+    c.offsets = offsets;
+    c.stream = stream;
+    tn::GroupedParams prm = sink_params(c, M, K, H, ldh);
+    prm.sink.act = act;
+    prm.sink.pre = P;
+    prm.sink.pre_ld = ldp;
+    st = launch_grouped_op<tn::kGrGated>(c, *dev, prm, o.x, o.y, o.ldx, o.stride_x, o.ldy, o.in_x, o.in_y);
+    t_rec.copied = (plan.g.x.copy ? 1 : 0) | (plan.g.y.copy ? 2 : 0);
+    return st;
+}
+
+template <int kAct>
+gemm_status_t launch_gated_grad(const char *name, DeviceState &dev, const tn::GatedGradParams &p, bool bf16,
+                                cudaStream_t stream)
+{
+    const bool vec = p.M % 4 == 0 && p.pre_ld % 4 == 0 && p.dh_ld % 4 == 0 && aligned_to(p.pre, 16) && aligned_to(p.dh, 8);
+    const int64_t units = (int64_t(p.M) + (vec ? 3 : 0)) / (vec ? 4 : 1);
+    const int64_t across = (units + tn::kGatedGradThreads - 1) / tn::kGatedGradThreads;
+    // about eight CTAs an SM, whole rows of them
+    const int64_t want = int64_t(dev.sms) * 8;
+    const int64_t gx = across < want ? across : want;
+    int64_t gy = (want + gx - 1) / gx;
+    if (gy > p.T) gy = p.T;
+    if (gy > 65535) gy = 65535;
+    const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(gy), 1);
+    auto kernel = bf16 ? (vec ? tn::gated_grad_kernel<kAct, true, true> : tn::gated_grad_kernel<kAct, true, false>)
+                       : (vec ? tn::gated_grad_kernel<kAct, false, true> : tn::gated_grad_kernel<kAct, false, false>);
+    return launch_plain(name, kernel, grid, tn::kGatedGradThreads, 0, stream, p);
+}
+
+gemm_status_t run_gated_grad(int type, int act, int64_t E, int64_t M, int64_t K, int64_t T, const void *A, int64_t lda,
+                             int64_t stride_a, const void *B, int64_t ldb, const int32_t *offsets, const float *P,
+                             int64_t ldp, const void *dH, int64_t lddh, void *dA, int64_t ldda, int64_t stride_da, void *dB,
+                             int64_t lddb, void *workspace, int64_t workspace_bytes, cudaStream_t stream)
+{
+    const char *name = "gemm_tn_gated_grad";
+    gemm_status_t st = check_gated(name, type, act, E, M, K, T, lda, stride_a, ldb, offsets);
+    if (st != GEMM_OK) return st;
+    if (ldp < 1 || ldp < 2 * M || lddh < 1 || lddh < M || (dA && (ldda < 1 || ldda < K)) || (dB && (lddb < 1 || lddb < K)))
+        return fail(GEMM_ERR_INVALID_ARG, "%s: a leading dimension is below its row's length", name);
+    if (dA && stride_da < 0) return fail(GEMM_ERR_INVALID_ARG, "%s: negative stride", name);
+    if (ldp > kMaxDim || lddh > kMaxDim || (dA && (ldda > kMaxDim || stride_da > (int64_t(1) << 38))) ||
+        (dB && lddb > kMaxDim))
+        return fail(GEMM_ERR_UNSUPPORTED, "%s: a leading dimension or stride is too large", name);
+    if (E == 0 || K == 0) return GEMM_OK;         // no gradient has an element
+    if (M == 0) dA = nullptr;
+    if (T == 0) dB = nullptr;
+    if (!dA && !dB) return GEMM_OK;
+    if (!aligned_to(dA, 2) || !aligned_to(dB, 2))
+        return fail(GEMM_ERR_INVALID_ARG, "%s: a result is not 2-byte aligned", name);
+    if (dA && E > 1 && stride_da < (2 * M - 1) * ldda + K && (stride_da < K || ldda < (E - 1) * stride_da + K))
+        return fail(GEMM_ERR_INVALID_ARG, "%s: the experts' results overlap", name);
+    const bool idle = M == 0 || T == 0;
+    if (!idle) {
+        if (!A || !B || !P || !dH) return fail(GEMM_ERR_INVALID_ARG, "%s: an operand is NULL", name);
+        if (!aligned_to(A, 2) || !aligned_to(B, 2) || !aligned_to(dH, 2) || !aligned_to(P, 4))
+            return fail(GEMM_ERR_INVALID_ARG, "%s: an operand is not aligned to its element size", name);
+    }
+    GatedPlan plan = gated_plan(true, !offsets, E, M, K, T, A, lda, stride_a, B, ldb);
+    if (!plan.fits) return fail(GEMM_ERR_UNSUPPORTED, "%s: the operands' copies are too large", name);
+    if ((st = check_workspace(name, workspace, workspace_bytes, plan.bytes, "gemm_gated_workspace")) != GEMM_OK) return st;
+    DeviceState *dev = nullptr;
+    if ((st = device_state(&dev, nullptr)) != GEMM_OK) return st;
+
+    Sections ws{static_cast<uint8_t *>(workspace)};
+    plan.g.x.copy &= dB != nullptr;               // (each gradient reads one of them)
+    plan.g.y.copy &= dA != nullptr;
+    SinkOperands o{};
+    uint16_t *dP = nullptr;
+    if (!idle) {
+        if ((st = place_operands(name, *dev, plan.g, ws, offsets, stream, o)) != GEMM_OK) return st;
+        dP = ws.take<uint16_t>(size_t(T) * size_t(plan.ldd));
+        const tn::GatedGradParams p{P, ldp, static_cast<const uint16_t *>(dH), lddh, dP, plan.ldd, offsets,
+                                    static_cast<int32_t>(E), static_cast<int32_t>(T), static_cast<int32_t>(M)};
+        const bool bf16 = type == GEMM_IN_BF16;
+        st = act == GEMM_ACT_SILU   ? launch_gated_grad<tn::kActSilu>(name, *dev, p, bf16, stream)
+             : act == GEMM_ACT_GELU ? launch_gated_grad<tn::kActGelu>(name, *dev, p, bf16, stream)
+                                    : launch_gated_grad<tn::kActGeluTanh>(name, *dev, p, bf16, stream);
+        if (st != GEMM_OK) return st;
+    }
+    GroupedCall c{name, GEMM_GROUPED_GRAD_B, type, type, E, 2 * M, K, T};
+    c.offsets = offsets;
+    c.stream = stream;
+    const int copied = (plan.g.x.copy ? 1 : 0) | (plan.g.y.copy ? 2 : 0);
+    if (dB) {
+        tn::GroupedParams prm = sink_params(c, K, 2 * M, dB, lddb);
+        st = launch_grouped_op<tn::kGrGradB>(c, *dev, prm, o.x, dP, o.ldx, o.stride_x, plan.ldd, o.in_x, plan.ldd);
+        t_rec.copied = copied;
+        if (st != GEMM_OK) return st;
+    }
+    if (dA) {
+        tn::GroupedParams prm = sink_params(c, K, T, dA, ldda);
+        prm.out_stride = stride_da;
+        prm.out_vec = prm.out_vec && (E == 1 || stride_da % 8 == 0);
+        prm.r_extent = static_cast<int32_t>(2 * M);
+        if (offsets) {
+            prm.group_maps = idle ? nullptr : ws.take<CUtensorMap>(size_t(E) * 2);
+            st = launch_grouped_op<tn::kGrGradA>(c, *dev, prm, dP, o.y, plan.ldd, 0, o.ldy, plan.ldd, o.in_y);
+        } else {
+            st = launch_grouped_op<tn::kGrGradAOne>(c, *dev, prm, dP, o.y, plan.ldd, 0, o.ldy, plan.ldd, o.in_y);
+        }
+        t_rec.copied = copied;
+    }
+    return st;
+}
+
+// ------------------------------------------------------------------ loss
+// The gradient goes through the vocabulary in pieces of about this many bytes of
+// the logits' gradients, which both products then read again: as large as the L2
+// keeps, and of at least kLossMinPiece classes, so that the FP32 sums of the token
+// gradient (read and written once a piece) stay small beside the products.
+constexpr int64_t kLossPieceBytes = int64_t(1) << 27, kLossMinPiece = 1024;
+
+struct LossPlan {
+    GroupedPlan g;
+    int64_t pieces, piece;       // classes of a piece (the last may have fewer)
+    int64_t blocks;              // forward: 32 classes each
+    size_t bytes;
+    bool fits;
+};
+
+LossPlan loss_plan(bool grad, int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, const void *B, int64_t ldb)
+{
+    LossPlan p{};
+    p.fits = true;
+    if (M == 0 || N == 0) return p;
+    p.g = grouped_plan(GEMM_GROUPED_PRODUCT, 1, M, K, N, A, lda, 0, B, ldb);
+    p.fits = K == 0 || p.g.fits;
+    size_t bytes = 0;
+    auto add = [&](int64_t rows, int64_t row_bytes) {
+        if (rows > (int64_t(1) << 60) / row_bytes) p.fits = false;
+        else bytes += (size_t(rows) * size_t(row_bytes) + 255) & ~size_t(255);
+    };
+    if (!grad) {
+        p.blocks = (M + 31) / 32;
+        add(N, p.blocks * int64_t(sizeof(float2)));
+        add(N, sizeof(float));
+    } else {
+        int64_t piece = kLossPieceBytes / (2 * N) / 256 * 256;
+        if (piece < kLossMinPiece) piece = kLossMinPiece;
+        p.pieces = (M + piece - 1) / piece;
+        piece = (M + p.pieces - 1) / p.pieces;
+        p.piece = (piece + 255) / 256 * 256;
+        p.pieces = (M + p.piece - 1) / p.piece;
+        add(N, p.piece * 2);
+        add(N, sizeof(float2));
+        add(1, sizeof(float));
+        if (p.pieces > 1 && K > 0) add(N, K * int64_t(sizeof(float)));
+    }
+    p.bytes = p.g.bytes() + bytes;
+    return p;
+}
+
+int64_t loss_workspace(int grad, int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, const void *B, int64_t ldb)
+{
+    if (M < 0 || N < 0 || K < 0 || lda < 1 || ldb < 1 || lda < K || ldb < K || !grouped_sizes_fit(1, M, K, N, lda, ldb, 0))
+        return -1;
+    const LossPlan p = loss_plan(grad != 0, M, N, K, A, lda, B, ldb);
+    return p.fits ? static_cast<int64_t>(p.bytes) : -1;
+}
+
+gemm_status_t check_loss(const char *name, int type, int64_t M, int64_t N, int64_t K, const void *A, int64_t lda,
+                         const void *B, int64_t ldb, const int64_t *targets)
+{
+    if (type != GEMM_IN_F16 && type != GEMM_IN_BF16)
+        return fail(GEMM_ERR_INVALID_ARG, "%s: unknown or unsupported type %d (GEMM_IN_F16 or GEMM_IN_BF16)", name, type);
+    if (M < 0 || N < 0 || K < 0)
+        return fail(GEMM_ERR_INVALID_ARG, "%s: negative size (M=%lld N=%lld K=%lld)", name, (long long)M, (long long)N,
+                    (long long)K);
+    if (lda < 1 || lda < K || ldb < 1 || ldb < K)
+        return fail(GEMM_ERR_INVALID_ARG, "%s: a leading dimension is below its row's length", name);
+    if (!grouped_sizes_fit(1, M, K, N, lda, ldb, 0))
+        return fail(GEMM_ERR_UNSUPPORTED, "%s: a size or leading dimension is too large", name);
+    if (M == 0 && N > 0) return fail(GEMM_ERR_INVALID_ARG, "%s: there are no classes", name);
+    if (N == 0) return GEMM_OK;
+    if (!targets) return fail(GEMM_ERR_INVALID_ARG, "%s: targets is NULL", name);
+    if (!aligned_to(targets, 8)) return fail(GEMM_ERR_INVALID_ARG, "%s: targets is not 8-byte aligned", name);
+    if (K > 0 && (!A || !B)) return fail(GEMM_ERR_INVALID_ARG, "%s: an operand is NULL", name);
+    if (K > 0 && (!aligned_to(A, 2) || !aligned_to(B, 2)))
+        return fail(GEMM_ERR_INVALID_ARG, "%s: an operand is not aligned to its element size", name);
+    return GEMM_OK;
+}
+
+gemm_status_t run_loss(int type, int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, const void *B, int64_t ldb,
+                       const int64_t *targets, float *loss, float *lse, void *workspace, int64_t workspace_bytes,
+                       cudaStream_t stream)
+{
+    const char *name = "gemm_tn_cross_entropy";
+    gemm_status_t st = check_loss(name, type, M, N, K, A, lda, B, ldb, targets);
+    if (st != GEMM_OK || N == 0) return st;
+    if (!loss || !lse) return fail(GEMM_ERR_INVALID_ARG, "%s: a result is NULL", name);
+    if (!aligned_to(loss, 4) || !aligned_to(lse, 4))
+        return fail(GEMM_ERR_INVALID_ARG, "%s: a result is not 4-byte aligned", name);
+    const LossPlan plan = loss_plan(false, M, N, K, A, lda, B, ldb);
+    if (!plan.fits) return fail(GEMM_ERR_UNSUPPORTED, "%s: the workspace would be too large", name);
+    if ((st = check_workspace(name, workspace, workspace_bytes, plan.bytes, "gemm_cross_entropy_workspace")) != GEMM_OK)
+        return st;
+    DeviceState *dev = nullptr;
+    if ((st = device_state(&dev, nullptr)) != GEMM_OK) return st;
+
+    Sections ws{static_cast<uint8_t *>(workspace)};
+    SinkOperands o{};
+    if (K > 0 && (st = place_operands(name, *dev, plan.g, ws, nullptr, stream, o)) != GEMM_OK) return st;
+    float2 *stats = ws.take<float2>(size_t(plan.blocks) * size_t(N));
+    float *z_target = ws.take<float>(size_t(N));
+    GroupedCall c{name, GEMM_GROUPED_PRODUCT, type, type, 1, M, K, N};
+    c.stream = stream;
+    tn::GroupedParams prm = sink_params(c, M, K, nullptr, 0);
+    prm.sink.targets = targets;
+    prm.sink.stats = stats;
+    prm.sink.z_target = z_target;
+    st = launch_grouped_op<tn::kGrLossStats>(c, *dev, prm, o.x, o.y, o.ldx, o.stride_x, o.ldy, o.in_x, o.in_y);
+    t_rec.copied = (plan.g.x.copy ? 1 : 0) | (plan.g.y.copy ? 2 : 0);
+    if (st != GEMM_OK) return st;
+    // tokens of a CTA: as many as a sector's 32 bytes of pairs at least, and no more than give every SM a CTA
+    int32_t lanes = 32;
+    while (lanes > 1 && (lanes / 2 >= N || (lanes > 4 && (N + lanes - 1) / lanes < dev->sms))) lanes /= 2;
+    const tn::JoinParams jp{stats, z_target, targets, loss, lse, N, M, static_cast<int32_t>(plan.blocks), lanes};
+    return launch_plain(name, tn::cross_entropy_join_kernel, dim3(static_cast<unsigned>((N + lanes - 1) / lanes), 1, 1),
+                        tn::kJoinThreads, 0, stream, jp);
+}
+
+gemm_status_t run_loss_grad(int type, int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, const void *B, int64_t ldb,
+                            const int64_t *targets, const float *lse, const float *dloss, void *dA, int64_t ldda, void *dB,
+                            int64_t lddb, void *workspace, int64_t workspace_bytes, cudaStream_t stream)
+{
+    const char *name = "gemm_tn_cross_entropy_grad";
+    gemm_status_t st = check_loss(name, type, M, N, K, A, lda, B, ldb, targets);
+    if (st != GEMM_OK) return st;
+    if ((dA && (ldda < 1 || ldda < K)) || (dB && (lddb < 1 || lddb < K)))
+        return fail(GEMM_ERR_INVALID_ARG, "%s: a leading dimension is below its row's length", name);
+    if ((dA && ldda > kMaxDim) || (dB && lddb > kMaxDim))
+        return fail(GEMM_ERR_UNSUPPORTED, "%s: a leading dimension is too large", name);
+    if (K == 0 || M == 0) return GEMM_OK;         // no gradient has an element
+    if (N == 0) dB = nullptr;
+    if (!dA && !dB) return GEMM_OK;
+    if (!aligned_to(dA, 2) || !aligned_to(dB, 2))
+        return fail(GEMM_ERR_INVALID_ARG, "%s: a result is not 2-byte aligned", name);
+    if (N > 0) {
+        if (!lse || !dloss) return fail(GEMM_ERR_INVALID_ARG, "%s: lse or dloss is NULL", name);
+        if (!aligned_to(lse, 4) || !aligned_to(dloss, 4))
+            return fail(GEMM_ERR_INVALID_ARG, "%s: lse or dloss is not 4-byte aligned", name);
+    }
+    const LossPlan plan = loss_plan(true, M, N, K, A, lda, B, ldb);
+    if (!plan.fits) return fail(GEMM_ERR_UNSUPPORTED, "%s: the workspace would be too large", name);
+    if ((st = check_workspace(name, workspace, workspace_bytes, plan.bytes, "gemm_cross_entropy_workspace")) != GEMM_OK)
+        return st;
+    DeviceState *dev = nullptr;
+    if ((st = device_state(&dev, nullptr)) != GEMM_OK) return st;
+    auto call = [&](int64_t classes) {
+        GroupedCall c{name, GEMM_GROUPED_PRODUCT, type, type, 1, classes, K, N};
+        c.stream = stream;
+        return c;
+    };
+    if (N == 0) {                                 // zeros
+        const GroupedCall c = call(M);
+        tn::GroupedParams prm = sink_params(c, K, 0, dA, ldda);
+        prm.r_extent = static_cast<int32_t>(M);
+        return launch_grouped_op<tn::kGrGradAOne>(c, *dev, prm, nullptr, nullptr, 0, 0, 0, 0, 0);
+    }
+
+    Sections ws{static_cast<uint8_t *>(workspace)};
+    SinkOperands o{};
+    if ((st = place_operands(name, *dev, plan.g, ws, nullptr, stream, o)) != GEMM_OK) return st;
+    const int copied = (plan.g.x.copy ? 1 : 0) | (plan.g.y.copy ? 2 : 0);
+    const int64_t ldd = plan.piece;
+    uint16_t *d = ws.take<uint16_t>(size_t(N) * size_t(ldd));
+    float2 *rows = ws.take<float2>(size_t(N));
+    float *scale = ws.take<float>(1);
+    float *sum = plan.pieces > 1 ? ws.take<float>(size_t(N) * size_t(K)) : nullptr;
+    const tn::LossRowsParams rp{targets, lse, dloss, rows, scale, N, M, type == GEMM_IN_F16};
+    if ((st = launch_plain(name, tn::cross_entropy_rows_kernel, dim3(1, 1, 1), tn::kRowsThreads, 0, stream, rp)) != GEMM_OK)
+        return st;
+    for (int64_t i = 0; i < plan.pieces; ++i) {
+        const int64_t first = i * plan.piece, classes = M - first < plan.piece ? M - first : plan.piece;
+        const int64_t padded = (classes + 7) / 8 * 8;      // the products read whole 16-byte units
+        const GroupedCall c = call(classes);
+        const uint16_t *x = static_cast<const uint16_t *>(o.x) + first * o.ldx;
+        tn::GroupedParams prm = sink_params(c, padded, K, d, ldd);
+        prm.sink.targets = targets;
+        prm.sink.rows = rows;
+        prm.sink.first = static_cast<int32_t>(first);
+        prm.sink.classes = static_cast<int32_t>(classes);
+        st = launch_grouped_op<tn::kGrLossGrad>(c, *dev, prm, x, o.y, o.ldx, 0, o.ldy, o.in_x, o.in_y);
+        if (st == GEMM_OK && dB) {
+            prm = sink_params(c, K, padded, dB, lddb);
+            prm.sink.sum = sum;
+            prm.sink.sum_ld = K;
+            prm.sink.add = plan.pieces == 1         ? tn::kAddOnly
+                           : i == 0                 ? tn::kAddFirst
+                           : i + 1 < plan.pieces    ? tn::kAddMore
+                                                    : tn::kAddLast;
+            prm.sink.out_scale = scale;
+            st = launch_grouped_op<tn::kGrGradBAdd>(c, *dev, prm, x, d, o.ldx, 0, ldd, o.in_x, padded);
+        }
+        if (st == GEMM_OK && dA) {
+            prm = sink_params(c, K, N, static_cast<uint16_t *>(dA) + first * ldda, ldda);
+            prm.r_extent = static_cast<int32_t>(classes);
+            prm.sink.out_scale = scale;
+            st = launch_grouped_op<tn::kGrGradAOne>(c, *dev, prm, d, o.y, ldd, 0, o.ldy, padded, o.in_y);
+        }
+        t_rec.copied = copied;
+        if (st != GEMM_OK) return st;
+    }
+    return GEMM_OK;
+}

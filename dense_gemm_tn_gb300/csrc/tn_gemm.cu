@@ -96,8 +96,8 @@ struct DeviceState {
     std::unordered_map<cudaStream_t, Split> stats;
     int quant_blocks[3] = {};         // co-resident quantiser CTAs per SM, by input type (0 = not queried)
     bool skinny_attr[2] = {};         // tn_skinny_kernel's shared-memory attribute set, by kind
-    int grouped_slots[3][3] = {};     // co-resident tn_grouped_kernel CTAs or pairs, by operation and variant (0 = not queried)
-    int split_slots[3][3] = {};       // co-resident clusters of 2, 4 and 8 single CTAs: product, its gradient by B, 8-bit
+    int grouped_slots[tn::kGrOps][3] = {};   // co-resident tn_grouped_kernel CTAs or pairs, by operation and variant (0 = not queried)
+    int split_slots[tn::kGrOps][3] = {};     // co-resident clusters of 2, 4 and 8 single CTAs, by operation (8-bit: 2)
     bool i8_attr = false;             // tn_i8_kernel's shared-memory attribute set
     int i8_pair_slots[2] = {};        // co-resident pairs of tn_i8_pair_kernel, by its kRuns (0 = not queried)
     // One lock per stream, held by a call from its first buffer lookup through
@@ -287,11 +287,12 @@ struct MapKey {
     uint32_t box_inner, box_outer;
     int type;
     uint64_t depth, depth_bytes;      // third dimension; depth 0: a 2-D map
+    uint64_t mid_bytes;               // not 0: two such matrices, so far apart, between the second and the last dimension
     bool operator==(const MapKey &o) const
     {
         return base == o.base && inner == o.inner && outer == o.outer && row_bytes == o.row_bytes &&
                box_inner == o.box_inner && box_outer == o.box_outer && type == o.type && depth == o.depth &&
-               depth_bytes == o.depth_bytes;
+               depth_bytes == o.depth_bytes && mid_bytes == o.mid_bytes;
     }
 };
 
@@ -300,9 +301,10 @@ struct MapKeyHash {
     {
         // 64-bit multiplicative mixing of the fields
         uint64_t h = 0x9E3779B97F4A7C15ull;
-        const uint64_t f[7] = {static_cast<uint64_t>(k.base), k.inner, k.outer, k.row_bytes,
+        const uint64_t f[8] = {static_cast<uint64_t>(k.base), k.inner, k.outer, k.row_bytes,
                                (static_cast<uint64_t>(k.box_inner) << 32) | k.box_outer,
-                               static_cast<uint64_t>(static_cast<uint32_t>(k.type)) | (k.depth << 32), k.depth_bytes};
+                               static_cast<uint64_t>(static_cast<uint32_t>(k.type)) | (k.depth << 32), k.depth_bytes,
+                               k.mid_bytes};
         for (uint64_t x : f) {
             h ^= x + 0x9E3779B97F4A7C15ull + (h << 6) + (h >> 2);
             h *= 0xBF58476D1CE4E5B9ull;
@@ -324,13 +326,14 @@ struct MapCache {
 MapCache g_maps;
 
 // depth > 0: a 3-D map of `depth` such matrices, depth_bytes apart, with boxes
-// of one matrix.
+// of one matrix; with mid_bytes > 0 a 4-D map of `depth` pairs of them, a pair's
+// matrices mid_bytes apart, with boxes of one pair.
 gemm_status_t encode_map(CUtensorMap *map, CUtensorMapDataType type, const void *base, uint64_t inner,
                          uint64_t outer, uint64_t row_bytes, uint64_t depth, uint64_t depth_bytes,
-                         uint32_t box_inner, uint32_t box_outer, const char *what)
+                         uint32_t box_inner, uint32_t box_outer, const char *what, uint64_t mid_bytes = 0)
 {
     const MapKey key{reinterpret_cast<uintptr_t>(base), inner, outer, row_bytes, box_inner, box_outer,
-                     static_cast<int>(type), depth, depth_bytes};
+                     static_cast<int>(type), depth, depth_bytes, mid_bytes};
     {
         std::lock_guard<std::mutex> lock(g_maps.mutex);
         auto it = g_maps.entries.find(key);
@@ -342,11 +345,12 @@ gemm_status_t encode_map(CUtensorMap *map, CUtensorMapDataType type, const void 
     }
     EncodeTiledFn fn = encode_fn();
     if (!fn) return fail(GEMM_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
-    const cuuint64_t dims[3] = {inner, outer, depth};
-    const cuuint64_t strides[2] = {row_bytes, depth_bytes};
-    const cuuint32_t box[3] = {box_inner, box_outer, 1};
-    const cuuint32_t elem_strides[3] = {1, 1, 1};
-    CUresult r = fn(map, type, depth ? 3 : 2, const_cast<void *>(base), dims, strides, box, elem_strides,
+    const bool pairs = mid_bytes > 0;
+    const cuuint64_t dims[4] = {inner, outer, pairs ? 2 : depth, depth};
+    const cuuint64_t strides[3] = {row_bytes, pairs ? mid_bytes : depth_bytes, depth_bytes};
+    const cuuint32_t box[4] = {box_inner, box_outer, pairs ? 2u : 1u, 1};
+    const cuuint32_t elem_strides[4] = {1, 1, 1, 1};
+    CUresult r = fn(map, type, pairs ? 4 : depth ? 3 : 2, const_cast<void *>(base), dims, strides, box, elem_strides,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(GEMM_ERR_CUDA, "cuTensorMapEncodeTiled(%s) failed with %d", what, (int)r);
@@ -1137,6 +1141,7 @@ gemm_status_t run_quant(const void *x, int x_type, int64_t rows, int64_t cols, i
 }
 
 #include "grouped_host.cuh"
+#include "sinks_host.cuh"
 
 }  // namespace
 
@@ -1259,6 +1264,56 @@ gemm_status_t gemm_quantize_i8_rows(const void *x, int x_type, int64_t rows, int
 {
     t_last_error[0] = '\0';
     return run_quant_rows(x, x_type, rows, cols, ldx, q, ldq, scale, static_cast<cudaStream_t>(stream));
+}
+
+int64_t gemm_gated_workspace(int grad, int dense, int64_t E, int64_t M, int64_t K, int64_t T, const void *A, int64_t lda,
+                             int64_t stride_a, const void *B, int64_t ldb)
+{
+    return gated_workspace(grad, dense, E, M, K, T, A, lda, stride_a, B, ldb);
+}
+
+gemm_status_t gemm_tn_gated(int type, int act, int64_t E, int64_t M, int64_t K, int64_t T, const void *A, int64_t lda,
+                            int64_t stride_a, const void *B, int64_t ldb, const int32_t *offsets, void *H, int64_t ldh,
+                            float *P, int64_t ldp, void *workspace, int64_t workspace_bytes, void *stream)
+{
+    t_last_error[0] = '\0';
+    return run_gated(type, act, E, M, K, T, A, lda, stride_a, B, ldb, offsets, H, ldh, P, ldp, workspace, workspace_bytes,
+                     static_cast<cudaStream_t>(stream));
+}
+
+gemm_status_t gemm_tn_gated_grad(int type, int act, int64_t E, int64_t M, int64_t K, int64_t T, const void *A, int64_t lda,
+                                 int64_t stride_a, const void *B, int64_t ldb, const int32_t *offsets, const float *P,
+                                 int64_t ldp, const void *dH, int64_t lddh, void *dA, int64_t ldda, int64_t stride_da,
+                                 void *dB, int64_t lddb, void *workspace, int64_t workspace_bytes, void *stream)
+{
+    t_last_error[0] = '\0';
+    return run_gated_grad(type, act, E, M, K, T, A, lda, stride_a, B, ldb, offsets, P, ldp, dH, lddh, dA, ldda, stride_da, dB,
+                          lddb, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
+}
+
+int64_t gemm_cross_entropy_workspace(int grad, int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, const void *B,
+                                     int64_t ldb)
+{
+    return loss_workspace(grad, M, N, K, A, lda, B, ldb);
+}
+
+gemm_status_t gemm_tn_cross_entropy(int type, int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, const void *B,
+                                    int64_t ldb, const int64_t *targets, float *loss, float *lse, void *workspace,
+                                    int64_t workspace_bytes, void *stream)
+{
+    t_last_error[0] = '\0';
+    return run_loss(type, M, N, K, A, lda, B, ldb, targets, loss, lse, workspace, workspace_bytes,
+                    static_cast<cudaStream_t>(stream));
+}
+
+gemm_status_t gemm_tn_cross_entropy_grad(int type, int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, const void *B,
+                                         int64_t ldb, const int64_t *targets, const float *lse, const float *dloss, void *dA,
+                                         int64_t ldda, void *dB, int64_t lddb, void *workspace, int64_t workspace_bytes,
+                                         void *stream)
+{
+    t_last_error[0] = '\0';
+    return run_loss_grad(type, M, N, K, A, lda, B, ldb, targets, lse, dloss, dA, ldda, dB, lddb, workspace, workspace_bytes,
+                         static_cast<cudaStream_t>(stream));
 }
 
 const char *gemm_status_string(gemm_status_t s)

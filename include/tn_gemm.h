@@ -362,6 +362,112 @@ gemm_status_t gemm_i8_tn_grouped(int out_type, int64_t E, int64_t M, int64_t K, 
 gemm_status_t gemm_quantize_i8_rows(const void *x, int x_type, int64_t rows, int64_t cols, int64_t ldx,
                                     int8_t *q, int64_t ldq, float *scale, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Gated projections: the first half of a gated feed-forward block, and its
+ * backward pass.
+ *
+ * A_e holds 2 M rows of K: M gate rows, then M up rows (element (m,k) of the gate
+ * at A[e*stride_a + m*lda + k], of the up rows at A[e*stride_a + (M+m)*lda + k]).
+ * For every row t of expert e:
+ *
+ *     P[t,j] = sum_k A_e[j,k] B[t,k]                 0 <= j < 2 M
+ *     H[t,m] = act(P[t,m]) * P[t,M+m]                0 <= m < M
+ *
+ * and, with dH the gradient of H:
+ *
+ *     dP[t,m]   = dH[t,m] P[t,M+m] act'(P[t,m])
+ *     dP[t,M+m] = dH[t,m] act(P[t,m])
+ *     dB[t,k]   = sum_j dP[t,j] A_e[j,k]             dA_e[j,k] = sum_{t of e} dP[t,j] B[t,k]
+ *
+ * Operands and results are of `type` (GEMM_IN_F16 or GEMM_IN_BF16); P is FP32.
+ * gemm_tn_gated is one kernel: P goes to memory only where the caller passes it
+ * (T rows of 2 M with leading dimension ldp), to be kept for the backward pass.
+ * gemm_tn_gated_grad rounds dP to `type` before the two products.  dA or dB may be
+ * NULL: that gradient is not computed.
+ *
+ * offsets as for gemm_tn_grouped (rows of no expert are neither read nor written,
+ * an expert without rows has a dA of zeros); or NULL with E == 1: all T rows.
+ *
+ * Workspace: gemm_gated_workspace returns the bytes that a call needs (grad: 0 for
+ * gemm_tn_gated, else 1; dense: not 0 where offsets is NULL), -1 for sizes it would
+ * refuse.  The forward call needs none where the TMA reads the operands in place
+ * (base, lda, ldb, stride_a and K multiples of 16 bytes); the backward call holds dP
+ * there (4 M T bytes).  Ownership and alignment as for gemm_tn_grouped.
+ *
+ * Errors: as for gemm_tn_grouped, and GEMM_ERR_INVALID_ARG for an unknown
+ * activation, or offsets NULL with E != 1.
+ */
+typedef enum {
+    GEMM_ACT_SILU = 0,       /* x / (1 + exp(-x)) */
+    GEMM_ACT_GELU = 1,       /* x (1 + erf(x / sqrt 2)) / 2 */
+    GEMM_ACT_GELU_TANH = 2   /* x (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))) / 2 */
+} gemm_act_t;
+
+int64_t gemm_gated_workspace(int grad, int dense, int64_t E, int64_t M, int64_t K, int64_t T,
+                             const void *A, int64_t lda, int64_t stride_a,
+                             const void *B, int64_t ldb);
+
+gemm_status_t gemm_tn_gated(int type, int act, int64_t E, int64_t M, int64_t K, int64_t T,
+                            const void *A, int64_t lda, int64_t stride_a,
+                            const void *B, int64_t ldb, const int32_t *offsets,
+                            void *H, int64_t ldh, float *P, int64_t ldp,
+                            void *workspace, int64_t workspace_bytes, void *stream);
+
+gemm_status_t gemm_tn_gated_grad(int type, int act, int64_t E, int64_t M, int64_t K, int64_t T,
+                                 const void *A, int64_t lda, int64_t stride_a,
+                                 const void *B, int64_t ldb, const int32_t *offsets,
+                                 const float *P, int64_t ldp, const void *dH, int64_t lddh,
+                                 void *dA, int64_t ldda, int64_t stride_da,
+                                 void *dB, int64_t lddb,
+                                 void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * Softmax cross entropy of a projection onto M classes (a vocabulary), and its
+ * gradients, without the N x M logits ever being held:
+ *
+ *     Z[n,m]  = sum_k A[m,k] B[n,k]
+ *     lse[n]  = log sum_m exp(Z[n,m])
+ *     loss[n] = lse[n] - Z[n,targets[n]]
+ *     d[n,m]  = dloss[n] (exp(Z[n,m] - lse[n]) - (m == targets[n] ? 1 : 0))
+ *     dB[n,k] = sum_m d[n,m] A[m,k]                  dA[m,k] = sum_n d[n,m] B[n,k]
+ *
+ * A (M x K), B (N x K) and the gradients are of `type` (GEMM_IN_F16 or
+ * GEMM_IN_BF16); targets are 64-bit integers, loss, lse and dloss N floats, all in
+ * device memory.  A token whose target is negative is ignored: its loss is 0 and its
+ * d is 0 (its lse is written; its row of B still takes part in dA as 0 * B, so it
+ * must be finite).  A target of M or more has a loss of NaN, and NaN gradients.
+ * Logits and statistics are FP32.
+ *
+ * gemm_tn_cross_entropy_grad takes the lse that the forward call left.  It computes
+ * the logits again, a piece of the vocabulary at a time; d is rounded to `type`
+ * there, and dB is summed over the pieces in FP32, in a fixed order.  dA or dB may
+ * be NULL: that gradient is not computed.  N == 0 writes zeros to dA.
+ *
+ * Workspace: gemm_cross_entropy_workspace returns the bytes that a call needs (grad:
+ * 0 for gemm_tn_cross_entropy, else 1), -1 for sizes it would refuse: forward N M / 4
+ * + 4 N, gradient about 128 MiB (2048 N beyond 65536 tokens; 2 N M where that is
+ * less) + 4 N K, and copies of operands that the TMA cannot read in place (as for
+ * gemm_tn_grouped).  Ownership and alignment as there.
+ *
+ * Errors: GEMM_ERR_INVALID_ARG for an unknown type, a negative size, M == 0 with
+ * N > 0, a leading dimension below its row's length, NULL or misaligned pointers
+ * with work to do (targets: 8 bytes), or a workspace that is too small;
+ * GEMM_ERR_UNSUPPORTED and GEMM_ERR_CUDA as for gemm_tn_grouped.
+ */
+int64_t gemm_cross_entropy_workspace(int grad, int64_t M, int64_t N, int64_t K,
+                                     const void *A, int64_t lda, const void *B, int64_t ldb);
+
+gemm_status_t gemm_tn_cross_entropy(int type, int64_t M, int64_t N, int64_t K,
+                                    const void *A, int64_t lda, const void *B, int64_t ldb,
+                                    const int64_t *targets, float *loss, float *lse,
+                                    void *workspace, int64_t workspace_bytes, void *stream);
+
+gemm_status_t gemm_tn_cross_entropy_grad(int type, int64_t M, int64_t N, int64_t K,
+                                         const void *A, int64_t lda, const void *B, int64_t ldb,
+                                         const int64_t *targets, const float *lse, const float *dloss,
+                                         void *dA, int64_t ldda, void *dB, int64_t lddb,
+                                         void *workspace, int64_t workspace_bytes, void *stream);
+
 /* Human-readable name of a status code (static storage). */
 const char *gemm_status_string(gemm_status_t status);
 
