@@ -15,6 +15,7 @@ The same names as the C ABI:
         gemm_quantize_i8_rows: products grouped by expert with their gradients, 8-bit integer products, row quantiser
     gemm_tn_gated / gemm_tn_gated_grad: gated projections act(gate) * up, dense and by expert, and their backward pass
     gemm_tn_cross_entropy / gemm_tn_cross_entropy_grad: softmax cross entropy of a projection onto a vocabulary
+    gemm_w4_tn / gemm_quantize_w4_rows: products with 4-bit weights and group scales for few tokens, their quantiser
     gemm_poll_device_status(stream=None)
 
 A, B and C are device pointers given as ints or as CUDA torch tensors (their
@@ -36,6 +37,7 @@ Convenience wrappers over torch tensors in TN storage:
     quantize_i8_rows(x (rows, cols)) -> (int8 codes, scale (rows,))
     tn_gated(A (2M,K) or (E,2M,K), Bt (T,K), offsets=None) -> (T, M); tn_gated_grad
     tn_cross_entropy(A (M,K), Bt (N,K), targets (N,) int64) -> (loss (N,), lse (N,)); tn_cross_entropy_grad
+    w4_tn(A (M,ceil(K/2)) uint8, Bt (N,K), scale_a (M,groups), group) -> (N, M); quantize_w4_rows
 The (N, M) row-major result IS the column-major M x N matrix C with ldc = M.
 With a `stream`, new results are that stream's memory, as under torch.cuda.stream.
 """
@@ -68,6 +70,7 @@ EXPORTS = (
     "gemm_i8_tn", "gemm_i8_tn_grouped", "gemm_quantize_i8_rows",
     "gemm_gated_workspace", "gemm_tn_gated", "gemm_tn_gated_grad",
     "gemm_cross_entropy_workspace", "gemm_tn_cross_entropy", "gemm_tn_cross_entropy_grad",
+    "gemm_w4_tn", "gemm_quantize_w4_rows",
 )
 
 GEMM_IN_F32 = 0
@@ -139,6 +142,10 @@ def _load() -> ctypes.CDLL:
     lib.gemm_tn_cross_entropy.restype = st
     lib.gemm_tn_cross_entropy_grad.argtypes = [st, i64, i64, i64, vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, i64, vp, i64, vp]
     lib.gemm_tn_cross_entropy_grad.restype = st
+    lib.gemm_w4_tn.argtypes = [st, i64, i64, i64, vp, i64, vp, i64, i64, vp, i64, vp, i64, vp]
+    lib.gemm_w4_tn.restype = st
+    lib.gemm_quantize_w4_rows.argtypes = [vp, st, i64, i64, i64, i64, vp, i64, st, vp, i64, vp]
+    lib.gemm_quantize_w4_rows.restype = st
     lib.gemm_status_string.argtypes = [st]
     lib.gemm_status_string.restype = ctypes.c_char_p
     lib.gemm_last_error.argtypes = []
@@ -345,6 +352,17 @@ def gemm_tn_cross_entropy_grad(type, M, N, K, A, lda, B, ldb, targets, lse, dlos
     return _check(calls.gemm_tn_cross_entropy_grad(int(type), M, N, K, _ptr(A), lda, _ptr(B), ldb, _ptr(targets), _ptr(lse),
                                                    _ptr(dloss), _ptr(dA), ldda, _ptr(dB), lddb, _ptr(workspace),
                                                    workspace_bytes, _stream(stream)))
+
+
+def gemm_w4_tn(type, M, N, K, A, lda, scale_a, ld_scale, group, B, ldb, C, ldc, stream=None) -> int:
+    return _check(calls.gemm_w4_tn(int(type), M, N, K, _ptr(A), lda, _ptr(scale_a), ld_scale, group, _ptr(B), ldb, _ptr(C),
+                                   ldc, _stream(stream)))
+
+
+def gemm_quantize_w4_rows(x, x_type, rows, cols, ldx, group, q, ldq, scale_type, scale, ld_scale, stream=None) -> int:
+    """4-bit quantisation with a scale per group of a row's terms: two codes a byte into q."""
+    return _check(calls.gemm_quantize_w4_rows(_ptr(x), int(x_type), rows, cols, ldx, group, _ptr(q), ldq, int(scale_type),
+                                              _ptr(scale), ld_scale, _stream(stream)))
 
 
 def gemm_f16_tn_noalloc(M, N, K, A, lda, B, ldb, C, ldc, stream=None) -> int:
@@ -1044,3 +1062,63 @@ def tn_cross_entropy_grad(A, Bt, targets, lse, dloss, dA=None, dBt=None, want_a=
                                             dBt.data_ptr() if want_b else None, lddb, held.data_ptr() if n > 0 else None, n,
                                             _launch_stream(device.index, stream)))
     return (dA if want_a else None), (dBt if want_b else None)
+
+
+# ---------------------------------------------------------------- 4-bit weights
+def w4_tn(A, Bt, scale_a, group, C=None, stream=None):
+    """C^T[n, m] = sum over groups g of scale_a[m, g] (sum over k in g of q[m, k] Bt[n, k]):
+    A (M, ceil(K / 2)) uint8, two signed 4-bit integers a byte, the even k in the low
+    half; Bt (N, K) and scale_a (M, ceil(K / group)) both fp16 or both bf16; group 32, 64,
+    128 or 256 terms -> (N, M) of their type.  For the few tokens of a decode step."""
+    torch = _torch or _load_torch()
+    _tensors(torch, A, Bt, scale_a)
+    dtype, device = Bt.dtype, A.device
+    half = _half_type(dtype, "Bt")
+    lda = _rows(A, torch.uint8, "A", cuda=False)
+    ldb = _rows(Bt, dtype, "Bt", cuda=False)
+    M, (N, K) = A.shape[0], Bt.shape
+    if group not in (32, 64, 128, 256):
+        raise ValueError(f"group must be 32, 64, 128 or 256, not {group!r}")
+    if A.shape[1] != (K + 1) // 2:
+        raise ValueError(f"A has {A.shape[1]} bytes a row, {(K + 1) // 2} hold {K} terms")
+    lds = _rows(scale_a, dtype, "scale_a", (M, -(-K // group)), cuda=False)
+    _same_device(device, Bt=Bt, scale_a=scale_a)
+    if _elsewhere(device.index):
+        with torch.cuda.device(device):
+            return w4_tn(A, Bt, scale_a, group, C, stream)
+    C, ldc = _result(C, (N, M), dtype, device, stream, "C")
+    _check(calls.gemm_w4_tn(half, M, N, K, A.data_ptr(), lda, scale_a.data_ptr(), lds, group, Bt.data_ptr(), ldb,
+                            C.data_ptr(), ldc, _launch_stream(device.index, stream)))
+    return C
+
+
+def quantize_w4_rows(x, group, dtype=None, stream=None):
+    """x: a 2-D float32 / float16 / bfloat16 CUDA tensor with unit column stride.  Returns
+    (codes (rows, ceil(cols / 2)) uint8, scale (rows, ceil(cols / group)) of `dtype`):
+    w4_tn's A and scale_a.  dtype: torch.float16 or torch.bfloat16 (x's own, unless it
+    is float32).  The codes' rows start on 16-byte boundaries."""
+    torch = _torch or _load_torch()
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError("x must be a 2-D float32/float16/bfloat16 tensor")
+    kind = GEMM_IN_F32 if x.dtype is torch.float32 else _half_kinds.get(x.dtype)
+    if kind is None:
+        raise ValueError("x must be a 2-D float32/float16/bfloat16 tensor")
+    if dtype is None and x.dtype is torch.float32:
+        raise ValueError("dtype must say which 16-bit type the scales of a float32 tensor have")
+    dtype = dtype or x.dtype
+    half = _half_type(dtype, "dtype")
+    if group not in (32, 64, 128, 256):
+        raise ValueError(f"group must be 32, 64, 128 or 256, not {group!r}")
+    device = x.device
+    ldx = _rows(x, x.dtype, "x")
+    if _elsewhere(device.index):
+        with torch.cuda.device(device):
+            return quantize_w4_rows(x, group, dtype, stream)
+    rows, cols = x.shape
+    row_bytes, groups = (cols + 1) // 2, -(-cols // group)
+    ldq = max(-(-row_bytes // 16) * 16, 1)
+    q = _empty((rows, ldq), torch.uint8, device, stream)[:, :row_bytes]
+    scale = _empty((rows, groups), dtype, device, stream)
+    _check(calls.gemm_quantize_w4_rows(x.data_ptr(), kind, rows, cols, ldx, group, q.data_ptr(), ldq, half, scale.data_ptr(),
+                                       max(groups, 1), _launch_stream(device.index, stream)))
+    return q, scale

@@ -317,6 +317,26 @@ static PyObject *py_gemm_tn_cross_entropy_grad(PyObject *self, PyObject *const *
         (const float *)v[10].p, v[11].p, v[12].l, v[13].p, v[14].l, v[15].p, v[16].l, v[17].p));
 }
 
+/* (type, M, N, K, A, lda, scale_a, ld_scale, group, B, ldb, C, ldc, stream) */
+static PyObject *py_gemm_w4_tn(PyObject *self, PyObject *const *args, Py_ssize_t nargs)
+{
+    (void)self;
+    arg_value v[14];
+    if (!read_args("gemm_w4_tn", "illlplpllplplp", args, nargs, v)) return NULL;
+    return PyLong_FromLong((long)gemm_w4_tn(v[0].i, v[1].l, v[2].l, v[3].l, v[4].p, v[5].l, v[6].p, v[7].l, v[8].l, v[9].p,
+                                            v[10].l, v[11].p, v[12].l, v[13].p));
+}
+
+/* (x, x_type, rows, cols, ldx, group, q, ldq, scale_type, scale, ld_scale, stream) */
+static PyObject *py_gemm_quantize_w4_rows(PyObject *self, PyObject *const *args, Py_ssize_t nargs)
+{
+    (void)self;
+    arg_value v[12];
+    if (!read_args("gemm_quantize_w4_rows", "pillllpliplp", args, nargs, v)) return NULL;
+    return PyLong_FromLong((long)gemm_quantize_w4_rows(v[0].p, v[1].i, v[2].l, v[3].l, v[4].l, v[5].l, v[6].p, v[7].l,
+                                                       v[8].i, v[9].p, v[10].l, v[11].p));
+}
+
 static PyMethodDef methods[] = {
     {"gemm_f16_tn", (PyCFunction)(void (*)(void))py_gemm_f16_tn, METH_FASTCALL,
      "gemm_f16_tn(M, N, K, A, lda, B, ldb, C, ldc, stream) -> status"},
@@ -365,6 +385,10 @@ static PyMethodDef methods[] = {
     {"gemm_tn_cross_entropy_grad", (PyCFunction)(void (*)(void))py_gemm_tn_cross_entropy_grad, METH_FASTCALL,
      "gemm_tn_cross_entropy_grad(type, M, N, K, A, lda, B, ldb, targets, lse, dloss, dA, ldda, dB, lddb, workspace, "
      "workspace_bytes, stream) -> status"},
+    {"gemm_w4_tn", (PyCFunction)(void (*)(void))py_gemm_w4_tn, METH_FASTCALL,
+     "gemm_w4_tn(type, M, N, K, A, lda, scale_a, ld_scale, group, B, ldb, C, ldc, stream) -> status"},
+    {"gemm_quantize_w4_rows", (PyCFunction)(void (*)(void))py_gemm_quantize_w4_rows, METH_FASTCALL,
+     "gemm_quantize_w4_rows(x, x_type, rows, cols, ldx, group, q, ldq, scale_type, scale, ld_scale, stream) -> status"},
     {NULL, NULL, 0, NULL},
 };
 

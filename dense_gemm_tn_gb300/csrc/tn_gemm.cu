@@ -27,6 +27,7 @@
 #include "grouped_kernel.cuh"
 #include "i8_kernel.cuh"
 #include "quant_i8_kernel.cuh"
+#include "w4_kernel.cuh"
 
 namespace {
 
@@ -1142,6 +1143,7 @@ gemm_status_t run_quant(const void *x, int x_type, int64_t rows, int64_t cols, i
 
 #include "grouped_host.cuh"
 #include "sinks_host.cuh"
+#include "w4_host.cuh"
 
 }  // namespace
 
@@ -1314,6 +1316,21 @@ gemm_status_t gemm_tn_cross_entropy_grad(int type, int64_t M, int64_t N, int64_t
     t_last_error[0] = '\0';
     return run_loss_grad(type, M, N, K, A, lda, B, ldb, targets, lse, dloss, dA, ldda, dB, lddb, workspace, workspace_bytes,
                          static_cast<cudaStream_t>(stream));
+}
+
+gemm_status_t gemm_w4_tn(int type, int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, const void *scale_a,
+                         int64_t ld_scale, int64_t group, const void *B, int64_t ldb, void *C, int64_t ldc, void *stream)
+{
+    t_last_error[0] = '\0';
+    return run_w4(type, M, N, K, A, lda, scale_a, ld_scale, group, B, ldb, C, ldc, static_cast<cudaStream_t>(stream));
+}
+
+gemm_status_t gemm_quantize_w4_rows(const void *x, int x_type, int64_t rows, int64_t cols, int64_t ldx, int64_t group, void *q,
+                                    int64_t ldq, int scale_type, void *scale, int64_t ld_scale, void *stream)
+{
+    t_last_error[0] = '\0';
+    return run_quant_w4(x, x_type, rows, cols, ldx, group, q, ldq, scale_type, scale, ld_scale,
+                        static_cast<cudaStream_t>(stream));
 }
 
 const char *gemm_status_string(gemm_status_t s)

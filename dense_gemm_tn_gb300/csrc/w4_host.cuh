@@ -1,0 +1,143 @@
+// Host side of the products with 4-bit weights and of their quantiser (included by
+// tn_gemm.cu, inside its anonymous namespace).
+
+bool w4_group_ok(int64_t group) { return group == 32 || group == 64 || group == 128 || group == 256; }
+
+template <bool kBf16, int kTilesM, int kTilesN>
+gemm_status_t launch_w4(const char *name, DeviceState &dev, w4::ProductParams &p, bool aligned, cudaStream_t stream)
+{
+    const bool whole = p.group % w4::kBlock == 0;
+    auto kernel = whole ? (aligned ? w4::product_kernel<kBf16, kTilesM, kTilesN, true, true>
+                                   : w4::product_kernel<kBf16, kTilesM, kTilesN, true, false>)
+                        : (aligned ? w4::product_kernel<kBf16, kTilesM, kTilesN, false, true>
+                                   : w4::product_kernel<kBf16, kTilesM, kTilesN, false, false>);
+    const int64_t blocks = (int64_t(p.K) + w4::kBlock - 1) / w4::kBlock;
+    p.token_tiles = static_cast<int32_t>((int64_t(p.N) + 8 * kTilesN - 1) / (8 * kTilesN));
+    const int64_t tiles = (int64_t(p.M) + 16 * kTilesM - 1) / (16 * kTilesM) * p.token_tiles;
+    if (tiles > INT32_MAX) return fail(GEMM_ERR_UNSUPPORTED, "%s: too many tiles", name);
+    // warps that share a tile's sum: eight, and sixteen where that still leaves SMs without a CTA of their own
+    int warps = tiles < 2 * int64_t(dev.sms) ? 16 : 8;
+    while (warps > 1 && warps / 2 >= blocks) warps /= 2;
+    const size_t smem = size_t(warps) * w4::part_floats(kTilesM, kTilesN) * sizeof(float);
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 96 * 1024);
+        if (e != cudaSuccess) return fail(GEMM_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+    }
+    t_rec = LaunchRecord{};
+    t_rec.name = name;
+    t_rec.grouped = 1;
+    t_rec.cluster = 1;
+    t_rec.grid = static_cast<int>(tiles);
+    t_rec.slots = dev.sms;
+    t_rec.tiles = static_cast<int>(tiles);
+    return launch_plain(name, kernel, dim3(static_cast<unsigned>(tiles), 1, 1), 32 * warps, smem, stream, p);
+}
+
+template <bool kBf16>
+gemm_status_t launch_w4_tokens(const char *name, DeviceState &dev, w4::ProductParams &p, bool aligned, cudaStream_t stream)
+{
+    const bool many = int64_t(p.M) >= 64 * int64_t(dev.sms);
+    if (p.N <= 8)
+        return many ? launch_w4<kBf16, 2, 1>(name, dev, p, aligned, stream) : launch_w4<kBf16, 1, 1>(name, dev, p, aligned, stream);
+    if (p.N <= 16)
+        return many ? launch_w4<kBf16, 2, 2>(name, dev, p, aligned, stream) : launch_w4<kBf16, 1, 2>(name, dev, p, aligned, stream);
+    return launch_w4<kBf16, 2, 4>(name, dev, p, aligned, stream);
+}
+
+gemm_status_t run_w4(int type, int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, const void *scale, int64_t lds,
+                     int64_t group, const void *B, int64_t ldb, void *C, int64_t ldc, cudaStream_t stream)
+{
+    const char *name = "gemm_w4_tn";
+    if (type != GEMM_IN_F16 && type != GEMM_IN_BF16)
+        return fail(GEMM_ERR_INVALID_ARG, "%s: unknown or unsupported type %d (GEMM_IN_F16 or GEMM_IN_BF16)", name, type);
+    if (M < 0 || N < 0 || K < 0)
+        return fail(GEMM_ERR_INVALID_ARG, "%s: negative size (M=%lld N=%lld K=%lld)", name, (long long)M, (long long)N,
+                    (long long)K);
+    if (!w4_group_ok(group)) return fail(GEMM_ERR_INVALID_ARG, "%s: the group is not 32, 64, 128 or 256 terms", name);
+    const int64_t bytes = (K + 1) / 2, groups = (K + group - 1) / group;
+    if (lda < 1 || lda < bytes || lds < 1 || lds < groups || ldb < 1 || ldb < K || ldc < 1 || ldc < M)
+        return fail(GEMM_ERR_INVALID_ARG, "%s: a leading dimension is below its row's length", name);
+    if (M > kMaxDim || N > kMaxDim || K > kMaxDim || lda > kMaxDim || lds > kMaxDim || ldb > kMaxDim || ldc > kMaxDim)
+        return fail(GEMM_ERR_UNSUPPORTED, "%s: a size or leading dimension is too large", name);
+    if (M == 0 || N == 0) return GEMM_OK;
+    if (!C) return fail(GEMM_ERR_INVALID_ARG, "%s: the result is NULL", name);
+    if (!aligned_to(C, 2)) return fail(GEMM_ERR_INVALID_ARG, "%s: the result is not 2-byte aligned", name);
+    if (K > 0) {
+        if (!A || !scale || !B) return fail(GEMM_ERR_INVALID_ARG, "%s: an operand is NULL", name);
+        if (!aligned_to(scale, 2) || !aligned_to(B, 2))
+            return fail(GEMM_ERR_INVALID_ARG, "%s: an operand is not aligned to its element size", name);
+    }
+    DeviceState *dev = nullptr;
+    gemm_status_t st = device_state(&dev, nullptr);
+    if (st != GEMM_OK) return st;
+    w4::ProductParams p;
+    memset(&p, 0, sizeof(p));
+    p.a = static_cast<const uint8_t *>(A);
+    p.lda = lda;
+    p.scale = static_cast<const uint16_t *>(scale);
+    p.lds = lds;
+    p.b = static_cast<const uint16_t *>(B);
+    p.ldb = ldb;
+    p.c = static_cast<uint16_t *>(C);
+    p.ldc = ldc;
+    p.M = static_cast<int32_t>(M);
+    p.N = static_cast<int32_t>(N);
+    p.K = static_cast<int32_t>(K);
+    p.group = static_cast<int32_t>(group);
+    p.groups = static_cast<int32_t>(groups);
+    p.words = aligned_to(A, 4) && aligned_to(B, 4);
+    const bool aligned = aligned_to(A, 16) && (M == 1 || lda % 16 == 0) && aligned_to(B, 16) && (N == 1 || ldb % 8 == 0);
+    return type == GEMM_IN_BF16 ? launch_w4_tokens<true>(name, *dev, p, aligned, stream)
+                                : launch_w4_tokens<false>(name, *dev, p, aligned, stream);
+}
+
+gemm_status_t run_quant_w4(const void *x, int x_type, int64_t rows, int64_t cols, int64_t ldx, int64_t group, void *q,
+                           int64_t ldq, int scale_type, void *scale, int64_t lds, cudaStream_t stream)
+{
+    const char *name = "gemm_quantize_w4_rows";
+    if (x_type < w4::kF32 || x_type > w4::kBF16)
+        return fail(GEMM_ERR_INVALID_ARG, "%s: unknown input type %d", name, x_type);
+    if (scale_type != GEMM_IN_F16 && scale_type != GEMM_IN_BF16)
+        return fail(GEMM_ERR_INVALID_ARG, "%s: unknown or unsupported scale type %d (GEMM_IN_F16 or GEMM_IN_BF16)", name,
+                    scale_type);
+    if (rows < 0 || cols < 0) return fail(GEMM_ERR_INVALID_ARG, "%s: negative size", name);
+    if (!w4_group_ok(group)) return fail(GEMM_ERR_INVALID_ARG, "%s: the group is not 32, 64, 128 or 256 terms", name);
+    if (ldx < 1 || ldx < cols || ldq < 1 || ldq < (cols + 1) / 2 || lds < 1 || lds < (cols + group - 1) / group)
+        return fail(GEMM_ERR_INVALID_ARG, "%s: a leading dimension is below its row's length", name);
+    if (cols > kMaxDim || rows > (int64_t(1) << 40) / (cols > 1 ? cols : 1))
+        return fail(GEMM_ERR_UNSUPPORTED, "%s: more than 2^40 elements", name);
+    if (rows == 0 || cols == 0) return GEMM_OK;
+    if (!x || !q || !scale) return fail(GEMM_ERR_INVALID_ARG, "%s: x, q or scale is NULL", name);
+    const int64_t esz = x_type == w4::kF32 ? 4 : 2;
+    if (!aligned_to(x, esz)) return fail(GEMM_ERR_INVALID_ARG, "%s: x is not aligned to its element size", name);
+    if (!aligned_to(scale, 2)) return fail(GEMM_ERR_INVALID_ARG, "%s: scale is not 2-byte aligned", name);
+    DeviceState *dev = nullptr;
+    gemm_status_t st = device_state(&dev, nullptr);
+    if (st != GEMM_OK) return st;
+    w4::QuantParams p;
+    memset(&p, 0, sizeof(p));
+    p.x = x;
+    p.ldx = ldx;
+    p.q = static_cast<uint8_t *>(q);
+    p.ldq = ldq;
+    p.scale = static_cast<uint16_t *>(scale);
+    p.lds = lds;
+    p.rows = rows;
+    p.cols = static_cast<int32_t>(cols);
+    p.group = static_cast<int32_t>(group);
+    p.segs = static_cast<int32_t>((cols + w4::kQuantSeg - 1) / w4::kQuantSeg);
+    p.bf16 = scale_type == GEMM_IN_BF16;
+    p.vec = aligned_to(x, 16) && aligned_to(q, 4) && (rows == 1 || (ldx * esz % 16 == 0 && ldq % 4 == 0));
+    const int64_t per = w4::kQuantThreads / 32;
+    int64_t grid = (rows * p.segs + per - 1) / per;
+    if (grid > int64_t(dev->sms) * 64) grid = int64_t(dev->sms) * 64;
+    t_rec = LaunchRecord{};
+    t_rec.name = name;
+    t_rec.quant = true;
+    t_rec.qgrid = grid;
+    t_rec.qunits = rows * p.segs;
+    t_rec.vec = p.vec;
+    auto kernel = x_type == w4::kF32 ? w4::quant_kernel<w4::kF32>
+                  : x_type == w4::kF16 ? w4::quant_kernel<w4::kF16> : w4::quant_kernel<w4::kBF16>;
+    return launch_plain(name, kernel, dim3(static_cast<unsigned>(grid), 1, 1), w4::kQuantThreads, 0, stream, p);
+}

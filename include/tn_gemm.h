@@ -468,6 +468,46 @@ gemm_status_t gemm_tn_cross_entropy_grad(int type, int64_t M, int64_t N, int64_t
                                          void *dA, int64_t ldda, void *dB, int64_t lddb,
                                          void *workspace, int64_t workspace_bytes, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Products with 4-bit weights and a scale per group of terms, for the few tokens of
+ * a decode step:
+ *
+ *     C[n,m] = sum_g scale_a[m,g] (sum_{k in group g} q[m,k] B[n,k])
+ *
+ * q: signed 4-bit integers (-8 .. 7, two's complement), row m at A + m*lda bytes, term
+ * k in byte k / 2: the low four bits for even k, the high four for odd k (lda >=
+ * (K + 1) / 2; the last half of an odd row is not used).  Group g holds the terms
+ * g*group .. g*group + group - 1, the last one what is left; group is 32, 64, 128 or
+ * 256.  scale_a[m,g] at scale_a[m*ld_scale + g], ld_scale >= ceil(K / group).  B
+ * (N x K), C (N rows of M) and the scales are of `type` (GEMM_IN_F16 or GEMM_IN_BF16).
+ * A group's sum is FP32 of exact products, the scale is applied to it in FP32, and the
+ * result is rounded once.  Any N is accepted; the codes are read once for every 32
+ * tokens, so for hundreds of them a product of widened weights is faster.  One launch,
+ * no buffer.
+ *
+ * gemm_quantize_w4_rows makes such weights of x (rows x cols; x_type and ldx as for
+ * gemm_quantize_e4m3):
+ *
+ *     scale[r,g] = max_{c in g} |x[r,c]| * (1/7)   fp32 (1/7 as an fp32 number), rounded to scale_type (16 bits)
+ *     q[r,c]     = round(x[r,c] / scale[r,g])      of the exact quotient, ties to even, within -8 .. 7
+ *
+ * A group of zeros, or whose scale rounds to 0, has codes 0; one with an infinity or a
+ * NaN, or whose scale is beyond the type, has scale NaN and codes 0.  The unused half
+ * of an odd row's last byte is 0.  rows == 0 or cols == 0 writes nothing.  One launch.
+ *
+ * Errors of both: GEMM_ERR_INVALID_ARG for an unknown type or group, a negative size,
+ * a leading dimension below its row's length, or NULL or misaligned pointers with work
+ * to do (codes need no alignment; rows on 16-byte boundaries are fastest);
+ * GEMM_ERR_UNSUPPORTED off sm_103 or for sizes beyond 2^31 - 256 (the quantiser: 2^40
+ * elements); GEMM_ERR_CUDA on a failed launch.
+ */
+gemm_status_t gemm_w4_tn(int type, int64_t M, int64_t N, int64_t K,
+                         const void *A, int64_t lda, const void *scale_a, int64_t ld_scale, int64_t group,
+                         const void *B, int64_t ldb, void *C, int64_t ldc, void *stream);
+
+gemm_status_t gemm_quantize_w4_rows(const void *x, int x_type, int64_t rows, int64_t cols, int64_t ldx, int64_t group,
+                                    void *q, int64_t ldq, int scale_type, void *scale, int64_t ld_scale, void *stream);
+
 /* Human-readable name of a status code (static storage). */
 const char *gemm_status_string(gemm_status_t status);
 
