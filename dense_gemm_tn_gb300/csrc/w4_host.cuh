@@ -6,21 +6,18 @@ bool w4_group_ok(int64_t group) { return group == 32 || group == 64 || group == 
 template <bool kBf16, int kTilesM, int kTilesN>
 gemm_status_t launch_w4(const char *name, DeviceState &dev, w4::ProductParams &p, bool aligned, cudaStream_t stream)
 {
-    const bool whole = p.group % w4::kBlock == 0;
+    const bool whole = p.group_shift >= 7;
     auto kernel = whole ? (aligned ? w4::product_kernel<kBf16, kTilesM, kTilesN, true, true>
                                    : w4::product_kernel<kBf16, kTilesM, kTilesN, true, false>)
                         : (aligned ? w4::product_kernel<kBf16, kTilesM, kTilesN, false, true>
                                    : w4::product_kernel<kBf16, kTilesM, kTilesN, false, false>);
-    const int64_t blocks = (int64_t(p.K) + w4::kBlock - 1) / w4::kBlock;
     p.token_tiles = static_cast<int32_t>((int64_t(p.N) + 8 * kTilesN - 1) / (8 * kTilesN));
     const int64_t tiles = (int64_t(p.M) + 16 * kTilesM - 1) / (16 * kTilesM) * p.token_tiles;
     if (tiles > INT32_MAX) return fail(GEMM_ERR_UNSUPPORTED, "%s: too many tiles", name);
-    // warps that share a tile's sum: eight, and sixteen where that still leaves SMs without a CTA of their own
-    int warps = tiles < 2 * int64_t(dev.sms) ? 16 : 8;
-    while (warps > 1 && warps / 2 >= blocks) warps /= 2;
-    const size_t smem = size_t(warps) * w4::part_floats(kTilesM, kTilesN) * sizeof(float);
+    const int part = w4::part_floats(kTilesM, kTilesN), ring = aligned ? w4::ring_floats(kTilesM) : 0;
+    const size_t smem = size_t(w4::kWarps) * (part > ring ? part : ring) * sizeof(float);
     if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 96 * 1024);
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
         if (e != cudaSuccess) return fail(GEMM_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
     }
     t_rec = LaunchRecord{};
@@ -30,13 +27,13 @@ gemm_status_t launch_w4(const char *name, DeviceState &dev, w4::ProductParams &p
     t_rec.grid = static_cast<int>(tiles);
     t_rec.slots = dev.sms;
     t_rec.tiles = static_cast<int>(tiles);
-    return launch_plain(name, kernel, dim3(static_cast<unsigned>(tiles), 1, 1), 32 * warps, smem, stream, p);
+    return launch_plain(name, kernel, dim3(static_cast<unsigned>(tiles), 1, 1), w4::kThreads, smem, stream, p);
 }
 
 template <bool kBf16>
 gemm_status_t launch_w4_tokens(const char *name, DeviceState &dev, w4::ProductParams &p, bool aligned, cudaStream_t stream)
 {
-    const bool many = int64_t(p.M) >= 64 * int64_t(dev.sms);
+    const bool many = int64_t(p.M) >= 24 * int64_t(dev.sms);
     if (p.N <= 8)
         return many ? launch_w4<kBf16, 2, 1>(name, dev, p, aligned, stream) : launch_w4<kBf16, 1, 1>(name, dev, p, aligned, stream);
     if (p.N <= 16)
@@ -83,7 +80,7 @@ gemm_status_t run_w4(int type, int64_t M, int64_t N, int64_t K, const void *A, i
     p.M = static_cast<int32_t>(M);
     p.N = static_cast<int32_t>(N);
     p.K = static_cast<int32_t>(K);
-    p.group = static_cast<int32_t>(group);
+    while ((int64_t(1) << p.group_shift) < group) ++p.group_shift;
     p.groups = static_cast<int32_t>(groups);
     p.words = aligned_to(A, 4) && aligned_to(B, 4);
     const bool aligned = aligned_to(A, 16) && (M == 1 || lda % 16 == 0) && aligned_to(B, 16) && (N == 1 || ldb % 8 == 0);
@@ -125,19 +122,23 @@ gemm_status_t run_quant_w4(const void *x, int x_type, int64_t rows, int64_t cols
     p.rows = rows;
     p.cols = static_cast<int32_t>(cols);
     p.group = static_cast<int32_t>(group);
-    p.segs = static_cast<int32_t>((cols + w4::kQuantSeg - 1) / w4::kQuantSeg);
     p.bf16 = scale_type == GEMM_IN_BF16;
-    p.vec = aligned_to(x, 16) && aligned_to(q, 4) && (rows == 1 || (ldx * esz % 16 == 0 && ldq % 4 == 0));
+    p.vec = aligned_to(x, 16) && aligned_to(q, 8) && (rows == 1 || (ldx * esz % 16 == 0 && ldq % 8 == 0));
     const int64_t per = w4::kQuantThreads / 32;
-    int64_t grid = (rows * p.segs + per - 1) / per;
-    if (grid > int64_t(dev->sms) * 64) grid = int64_t(dev->sms) * 64;
+    const int64_t seg = x_type == w4::kF32 ? w4::QuantCfg<w4::kF32>::kSeg : w4::QuantCfg<w4::kF16>::kSeg;
+    const int64_t segs = (cols + seg - 1) / seg;
+    if (segs > 65535) return fail(GEMM_ERR_UNSUPPORTED, "%s: too many columns", name);
+    int64_t grid = (rows + per - 1) / per;
+    const int64_t most = (int64_t(dev->sms) * 64 + segs - 1) / segs;
+    if (grid > most) grid = most;
     t_rec = LaunchRecord{};
     t_rec.name = name;
     t_rec.quant = true;
-    t_rec.qgrid = grid;
-    t_rec.qunits = rows * p.segs;
+    t_rec.qgrid = grid * segs;
+    t_rec.qunits = rows * segs;
     t_rec.vec = p.vec;
     auto kernel = x_type == w4::kF32 ? w4::quant_kernel<w4::kF32>
                   : x_type == w4::kF16 ? w4::quant_kernel<w4::kF16> : w4::quant_kernel<w4::kBF16>;
-    return launch_plain(name, kernel, dim3(static_cast<unsigned>(grid), 1, 1), w4::kQuantThreads, 0, stream, p);
+    return launch_plain(name, kernel, dim3(static_cast<unsigned>(grid), static_cast<unsigned>(segs), 1), w4::kQuantThreads, 0,
+                        stream, p);
 }

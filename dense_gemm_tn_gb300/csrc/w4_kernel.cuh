@@ -46,7 +46,7 @@ struct ProductParams {
     uint16_t *c;                     // N rows of M
     int64_t ldc;
     int32_t M, N, K;
-    int32_t group;                   // terms per scale: 32, 64, 128 or 256
+    int32_t group_shift;             // terms per scale: 32, 64, 128 or 256, as a power of two
     int32_t groups;                  // scales of a row
     int32_t token_tiles;             // tiles of 8 kTilesN tokens
     bool words;                      // (rows not on 16-byte boundaries) the operands start on 4-byte ones
@@ -83,19 +83,30 @@ __device__ __noinline__ uint4 load_part(const uint8_t *p, int32_t valid)
 
 // The eight codes of a word as four pairs of 16-bit floats: (0, 4), (1, 5), (2, 6), (3, 7).
 // A code's four bits, the top one flipped, are q + 8 in the low bits of 1024 (fp16)
-// or 128 (bf16), whose steps are 1 there.
+// or 128 (bf16), whose steps are 1 there.  fp16 has room for them four bits further up
+// as well, as 1024 + 16 (q + 8), which a sixteenth of takes back exactly; bf16 takes a
+// shift for that.
 template <bool kBf16>
 __device__ __forceinline__ void widen(uint32_t w, uint32_t (&h)[4])
 {
-    constexpr uint32_t kMagic = kBf16 ? 0x43084308u : 0x64086408u;      // (xor 8: the flip)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    auto pick = [](uint32_t v, uint32_t mask, uint32_t magic) {        // (v & mask) ^ magic
         uint32_t x;
-        asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(x) : "r"(w >> (4 * i)), "r"(0x000F000Fu), "r"(kMagic));
-        if constexpr (kBf16)
-            asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(h[i]) : "r"(x), "r"(0x43084308u));
-        else
-            asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(h[i]) : "r"(x), "r"(0x64086408u));
+        asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(x) : "r"(v), "r"(mask), "r"(magic));
+        return x;
+    };
+    if constexpr (kBf16) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(h[i]) : "r"(pick(w >> (4 * i), 0x000F000Fu, 0x43084308u)), "r"(0x43084308u));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t v = w >> (8 * i);
+            asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(h[2 * i]) : "r"(pick(v, 0x000F000Fu, 0x64086408u)), "r"(0x64086408u));
+            asm("fma.rn.f16x2 %0, %1, %2, %3;"
+                : "=r"(h[2 * i + 1])
+                : "r"(pick(v, 0x00F000F0u, 0x64806480u)), "r"(0x2C002C00u), "r"(0xD480D480u));     // / 16 - 72
+        }
     }
 }
 
@@ -112,6 +123,23 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
                      "{%0, %1, %2, %3};"
                      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The first of a sum's.
+template <bool kBf16>
+__device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1)
+{
+    if constexpr (kBf16)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%10, %10, %10, %10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%10, %10, %10, %10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
 template <bool kBf16>
@@ -150,12 +178,24 @@ __device__ __forceinline__ void exchange(uint4 &v, int t)
 // 16 kTilesM rows, four apart so that a fragment's stores meet no bank twice.
 __host__ __device__ constexpr int part_floats(int tiles_m, int tiles_n) { return 8 * tiles_n * (16 * tiles_m + 4); }
 
+constexpr int kWarps = 8, kThreads = 32 * kWarps;
+constexpr int kDepth = 4;                        // blocks of a warp's ring
+__host__ __device__ constexpr int ring_floats(int tiles_m) { return kDepth * tiles_m * 2 * 32 * 4; }
+
+__device__ __forceinline__ uint4 ld_shared(uint32_t addr)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr)
+                 : "memory");
+    return v;
+}
+
 template <bool kBf16, int kTilesM, int kTilesN, bool kWhole, bool kAligned>
-__global__ void __launch_bounds__(512) product_kernel(const __grid_constant__ ProductParams p)
+__global__ void __launch_bounds__(kThreads) product_kernel(const __grid_constant__ ProductParams p)
 {
     extern __shared__ float parts[];
     constexpr int kRows = 16 * kTilesM, kTokens = 8 * kTilesN, kLd = kRows + 4;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
     const int32_t tile = static_cast<int32_t>(blockIdx.x) / p.token_tiles;
     const int32_t n0 = (static_cast<int32_t>(blockIdx.x) - tile * p.token_tiles) * kTokens;
@@ -165,6 +205,10 @@ __global__ void __launch_bounds__(512) product_kernel(const __grid_constant__ Pr
     ptx::griddep_launch_dependents();
 
     const int32_t blocks = (p.K + kBlock - 1) / kBlock, row_bytes = (p.K + 1) / 2;
+    // Blocks that are read without a look at their ends: all of one is there, and where
+    // words are cut, so are the bytes that the last one takes along (the next block's,
+    // or the next row's).
+    const int32_t plain = kAligned ? p.K / kBlock : p.words ? max(blocks - (m0 + kRows >= p.M ? 2 : 1), 0) : 0;
     const uint8_t *a_row[kTilesM][2];
     const uint16_t *s_row[kTilesM][2];
 #pragma unroll
@@ -184,61 +228,45 @@ __global__ void __launch_bounds__(512) product_kernel(const __grid_constant__ Pr
         b_row[i] = p.b + (held[i] ? n : 0) * p.ldb + (kWhole ? 32 : 8) * t;
     }
 
-    struct Step {
-        uint4 code[kTilesM][2];
+    float acc[kTilesM][kTilesN][4] = {};
+
+    // What a block's multiplication needs beside its codes: the scales, and the tokens where
+    // there are few enough to be held.
+    constexpr bool kAhead = kTilesN <= 2;
+    struct Beside {
         uint16_t scale[kTilesM][2];
+        uint4 tokens[kAhead ? 4 : 1][kTilesN];
     };
-    // A block that can be read without a look at its ends: the whole of it is there, and
-    // where words are cut, the bytes that the last one takes along are (the next block's,
-    // or the next row's).
-    const bool last_tile = m0 + kRows >= p.M;
-    auto plain = [&](int32_t b) {
-        if (kAligned) return (b + 1) * kBlock <= p.K;
-        return p.words && b + (last_tile ? 2 : 1) < blocks;
-    };
-    auto load = [&](int32_t b, Step &s) {
-        const bool whole = plain(b);
-        const int32_t off = b * (kBlock / 2), valid = row_bytes - off - 16 * t;
-        const int32_t grp = (b * kBlock + 32 * t) / p.group;
+    auto load = [&](Beside &s, int32_t b, bool whole, auto token) {
+        const int32_t grp = kWhole ? b >> (p.group_shift - 7) : (b * kBlock + 32 * t) >> p.group_shift;
 #pragma unroll
         for (int i = 0; i < kTilesM; ++i)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint8_t *at = a_row[i][h] + off;
-                if (whole)
-                    s.code[i][h] = kAligned ? __ldg(reinterpret_cast<const uint4 *>(at)) : load_words(at);
-                else
-                    s.code[i][h] = load_part(at, valid);
-                s.scale[i][h] = grp < p.groups ? __ldg(s_row[i][h] + grp) : uint16_t(0);
-            }
+            for (int h = 0; h < 2; ++h) s.scale[i][h] = whole || grp < p.groups ? __ldg(s_row[i][h] + grp) : uint16_t(0);
+        if constexpr (kAhead)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < kTilesN; ++i) s.tokens[j][i] = token(j, i);
     };
-    float acc[kTilesM][kTilesN][4] = {};
-
-    auto compute = [&](int32_t b, Step &s) {
-        const bool whole = plain(b);
+    // The multiplication.  token(j, i): the tokens' terms of word j, tile i; codes(v): the
+    // block's codes, as soon as they are there.
+    auto compute = [&](const Beside &s, auto token, auto codes) {
+        uint4 code[kTilesM][2];
+        codes(code);
         if constexpr (!kWhole) {
 #pragma unroll
             for (int i = 0; i < kTilesM; ++i)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) exchange(s.code[i][h], t);
+                for (int h = 0; h < 2; ++h) exchange(code[i][h], t);
         }
         float part[kTilesM][kTilesN][4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            // the tokens' eight terms of this word
-            uint32_t x[kTilesN][4];
-            const int32_t k = b * kBlock + (kWhole ? 32 * t + 8 * j : 32 * j + 8 * t);
+            uint32_t x[kTilesN][4];              // the tokens' eight terms of this word
 #pragma unroll
             for (int i = 0; i < kTilesN; ++i) {
-                const uint16_t *at = b_row[i] + b * kBlock + (kWhole ? 8 : 32) * j;
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (held[i]) {
-                    if (whole)
-                        v = kAligned ? __ldg(reinterpret_cast<const uint4 *>(at))
-                                     : load_words(reinterpret_cast<const uint8_t *>(at));
-                    else
-                        v = load_part(reinterpret_cast<const uint8_t *>(at), 2 * min(p.K - k, 8));
-                }
+                const uint4 v = kAhead ? s.tokens[kAhead ? j : 0][i] : token(j, i);
                 x[i][0] = __byte_perm(v.x, v.z, 0x5410);
                 x[i][1] = __byte_perm(v.x, v.z, 0x7632);
                 x[i][2] = __byte_perm(v.y, v.w, 0x5410);
@@ -246,19 +274,19 @@ __global__ void __launch_bounds__(512) product_kernel(const __grid_constant__ Pr
             }
 #pragma unroll
             for (int i = 0; i < kTilesM; ++i) {
-                const uint4 lo = s.code[i][0], hi = s.code[i][1];
+                const uint4 lo = code[i][0], hi = code[i][1];
                 uint32_t u[4], v[4];
                 widen<kBf16>(j == 0 ? lo.x : j == 1 ? lo.y : j == 2 ? lo.z : lo.w, u);
                 widen<kBf16>(j == 0 ? hi.x : j == 1 ? hi.y : j == 2 ? hi.z : hi.w, v);
-                const bool begin = !kWhole || j == 0, end = !kWhole || j == 3;
 #pragma unroll
                 for (int n = 0; n < kTilesN; ++n) {
-                    float(&d)[4] = part[i][n];
-                    if (begin) d[0] = d[1] = d[2] = d[3] = 0.0f;
-                    mma<kBf16>(d, u[0], v[0], u[1], v[1], x[n][0], x[n][1]);
-                    mma<kBf16>(d, u[2], v[2], u[3], v[3], x[n][2], x[n][3]);
+                    if (!kWhole || j == 0)
+                        mma_first<kBf16>(part[i][n], u[0], v[0], u[1], v[1], x[n][0], x[n][1]);
+                    else
+                        mma<kBf16>(part[i][n], u[0], v[0], u[1], v[1], x[n][0], x[n][1]);
+                    mma<kBf16>(part[i][n], u[2], v[2], u[3], v[3], x[n][2], x[n][3]);
                 }
-                if (end) {
+                if (!kWhole || j == 3) {
                     float s0 = to_float<kBf16>(s.scale[i][0]), s1 = to_float<kBf16>(s.scale[i][1]);
                     if constexpr (!kWhole) {     // lane j of the four has the scales of these 32 terms
                         s0 = __shfl_sync(0xffffffffu, s0, (lane & ~3) | j);
@@ -276,20 +304,97 @@ __global__ void __launch_bounds__(512) product_kernel(const __grid_constant__ Pr
         }
     };
 
-    // one block's codes on their way while another's are multiplied
-    Step s0, s1;
+    // The blocks warp, warp + kWarps, ...: the plain ones kDepth at a time, so that all
+    // addresses are a pointer and a constant.
+    constexpr int kCodeStep = kWarps * kBlock / 2, kTokenStep = kWarps * kBlock;
     int32_t b = warp;
-    if (b < blocks) load(b, s0);
-    while (b < blocks) {
-        if (b + warps < blocks) load(b + warps, s1);
-        compute(b, s0);
-        b += warps;
-        if (b >= blocks) break;
-        if (b + warps < blocks) load(b + warps, s0);
-        compute(b, s1);
-        b += warps;
+#pragma unroll
+    for (int i = 0; i < kTilesM; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) a_row[i][h] += warp * (kBlock / 2);
+#pragma unroll
+    for (int i = 0; i < kTilesN; ++i) b_row[i] += warp * kBlock;
+    // Aligned: each lane copies its own pieces kDepth - 1 blocks ahead into a ring of its
+    // own in shared memory: many bytes in flight, few registers, nothing to synchronise.
+    const uint32_t ring = ptx::smem_addr(parts) + (warp * kDepth * kTilesM * 2 * 32 + lane) * 16;
+    auto copy = [&](int32_t left, int ahead, int stage) {        // the block `ahead` turns on, if there is one
+        if (left > ahead * kWarps) {
+#pragma unroll
+            for (int i = 0; i < kTilesM; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(
+                                     ring + ((stage * kTilesM + i) * 2 + h) * 512),
+                                 "l"(a_row[i][h] + ahead * kCodeStep)
+                                 : "memory");
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    if constexpr (kAligned)
+#pragma unroll
+        for (int s = 0; s < kDepth - 1; ++s) copy(plain - b, s, s);
+    auto token_at = [&](int turn) {
+        return [&, turn](int j, int i) {
+            const uint16_t *at = b_row[i] + turn * kTokenStep + (kWhole ? 8 : 32) * j;
+            if (!held[i]) return make_uint4(0, 0, 0, 0);
+            if constexpr (kAligned) return __ldg(reinterpret_cast<const uint4 *>(at));
+            return load_words(reinterpret_cast<const uint8_t *>(at));
+        };
+    };
+    Beside beside[2];                            // this turn's and the next one's
+    static_assert(kDepth % 2 == 0, "which is which does not depend on the round");
+    if (b < plain) load(beside[0], b, true, token_at(0));
+#pragma unroll 1
+    while (b < plain) {
+        const int32_t left = plain - b;
+#pragma unroll
+        for (int s = 0; s < kDepth; ++s) {
+            if (s > 0 && left <= s * kWarps) break;
+            if constexpr (kAligned) copy(left, s + kDepth - 1, (s + kDepth - 1) % kDepth);
+            if (left > (s + 1) * kWarps) load(beside[(s + 1) & 1], b + (s + 1) * kWarps, true, token_at(s + 1));
+            compute(beside[s & 1], token_at(s), [&](uint4(&code)[kTilesM][2]) {
+                if constexpr (kAligned) asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
+#pragma unroll
+                for (int i = 0; i < kTilesM; ++i)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        code[i][h] = kAligned ? ld_shared(ring + ((s * kTilesM + i) * 2 + h) * 512)
+                                              : load_words(a_row[i][h] + s * kCodeStep);
+            });
+        }
+        const int32_t turns = min((left + kWarps - 1) / kWarps, kDepth);
+        b += turns * kWarps;
+#pragma unroll
+        for (int i = 0; i < kTilesM; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) a_row[i][h] += turns * kCodeStep;
+#pragma unroll
+        for (int i = 0; i < kTilesN; ++i) b_row[i] += turns * kTokenStep;
     }
+#pragma unroll 1
+    for (; b < blocks; b += kWarps) {            // what is left is read byte by byte
+        auto token = [&](int j, int i) {
+            const int32_t k = (kWhole ? 32 * t + 8 * j : 32 * j + 8 * t);
+            return load_part(reinterpret_cast<const uint8_t *>(b_row[i] + (kWhole ? 8 : 32) * j),
+                             held[i] ? 2 * min(p.K - b * kBlock - k, 8) : 0);
+        };
+        load(beside[0], b, false, token);
+        compute(beside[0], token, [&](uint4(&code)[kTilesM][2]) {
+#pragma unroll
+            for (int i = 0; i < kTilesM; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) code[i][h] = load_part(a_row[i][h], row_bytes - b * (kBlock / 2) - 16 * t);
+        });
+#pragma unroll
+        for (int i = 0; i < kTilesM; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) a_row[i][h] += kCodeStep;
+#pragma unroll
+        for (int i = 0; i < kTilesN; ++i) b_row[i] += kTokenStep;
+    }
+    if constexpr (kAligned) asm volatile("cp.async.wait_all;" ::: "memory");
 
+    __syncthreads();                             // every ring is done with
     float *mine = parts + warp * part_floats(kTilesM, kTilesN);
 #pragma unroll
     for (int i = 0; i < kTilesM; ++i)
@@ -298,11 +403,11 @@ __global__ void __launch_bounds__(512) product_kernel(const __grid_constant__ Pr
 #pragma unroll
             for (int r = 0; r < 4; ++r) mine[(8 * n + 2 * t + (r & 1)) * kLd + 16 * i + 8 * (r >> 1) + g] = acc[i][n][r];
     __syncthreads();
-    for (int32_t i = threadIdx.x; i < kRows * kTokens; i += blockDim.x) {
+    for (int32_t i = threadIdx.x; i < kRows * kTokens; i += kThreads) {
         const int32_t n = i / kRows, m = i - n * kRows;
         if (n0 + n >= p.N || m0 + m >= p.M) continue;
         float sum = 0.0f;
-        for (int w = 0; w < warps; ++w) sum += parts[w * part_floats(kTilesM, kTilesN) + n * kLd + m];
+        for (int w = 0; w < kWarps; ++w) sum += parts[w * part_floats(kTilesM, kTilesN) + n * kLd + m];
         p.c[(n0 + n) * p.ldc + m0 + m] = from_float<kBf16>(sum);
     }
 }
@@ -310,9 +415,9 @@ __global__ void __launch_bounds__(512) product_kernel(const __grid_constant__ Pr
 // ------------------------------------------------------------------ quantiser
 //     scale[r, g] = amax times the float next to 1 / 7, in FP32, rounded to 16 bits
 //     q[r, c]     = round(x / scale) of the exact quotient, ties to even, within -8 .. 7
-// A warp takes 256 terms of a row at a time, eight a lane, so a group's maximum is
-// one of up to 32 neighbouring lanes.  Bound by the read of x.
-constexpr int kQuantThreads = 256, kQuantSeg = 256;
+// A warp takes 512 terms of a row at a time (FP32: 256), 16 a lane (8), so a group's
+// maximum is one of up to 32 neighbouring lanes.  Bound by the read of x.
+constexpr int kQuantThreads = 256;
 
 struct QuantParams {
     const void *x;
@@ -323,16 +428,15 @@ struct QuantParams {
     int64_t lds;
     int64_t rows;
     int32_t cols, group;
-    int32_t segs;                    // of a row
     bool bf16;                       // the scales' type
-    bool vec;                        // x's rows on 16-byte boundaries, q's on 4-byte ones
+    bool vec;                        // x's rows on 16-byte boundaries, q's on 8-byte ones
 };
 
 enum In : int { kF32 = 0, kF16 = 1, kBF16 = 2 };
 
-// round(x / s) for s > 0: the quotient by a reciprocal, put right by the exact rest
-// x - q s (q s has at most 15 bits, and the rest is below s: no bit is lost).
-__device__ __forceinline__ int32_t code(float x, float s, float inverse)
+// round(x / s) for s > 0 and any x: the quotient by a reciprocal, put right by the
+// exact rest x - q s (q s has at most 15 bits, and the rest is below s: no bit is lost).
+__device__ __forceinline__ uint32_t code(float x, float s, float inverse)
 {
     float q = rintf(x * inverse);
     q = fminf(fmaxf(q, -16.0f), 16.0f);
@@ -340,24 +444,28 @@ __device__ __forceinline__ int32_t code(float x, float s, float inverse)
     const bool odd = static_cast<int32_t>(q) & 1;
     if (rest2 > s || (rest2 == s && odd)) q += 1.0f;
     if (rest2 < -s || (rest2 == -s && odd)) q -= 1.0f;
-    const int32_t i = static_cast<int32_t>(q);
-    return i < -8 ? -8 : i > 7 ? 7 : i;
+    return static_cast<uint32_t>(static_cast<int32_t>(fminf(fmaxf(q, -8.0f), 7.0f))) & 15u;
 }
+
+// A lane's terms at a time: 16 of a 16-bit type, 8 of FP32; a warp's are kSeg.
+template <int kIn>
+struct QuantCfg {
+    static constexpr int kTerms = kIn == kF32 ? 8 : 16, kSeg = 32 * kTerms;
+};
 
 template <int kIn>
 __global__ void __launch_bounds__(kQuantThreads) quant_kernel(const QuantParams p)
 {
-    constexpr int kElem = kIn == kF32 ? 4 : 2;
+    constexpr int kTerms = QuantCfg<kIn>::kTerms, kSeg = QuantCfg<kIn>::kSeg, kElem = kIn == kF32 ? 4 : 2;
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     const int lane = threadIdx.x & 31;
-    const int64_t units = p.rows * p.segs, step = static_cast<int64_t>(gridDim.x) * (kQuantThreads / 32);
-    for (int64_t u = static_cast<int64_t>(blockIdx.x) * (kQuantThreads / 32) + (threadIdx.x >> 5); u < units; u += step) {
-        const int64_t r = u / p.segs;
-        const int32_t c = static_cast<int32_t>(u - r * p.segs) * kQuantSeg + 8 * lane;
+    const int64_t row_step = static_cast<int64_t>(gridDim.x) * (kQuantThreads / 32);
+    const int32_t c = static_cast<int32_t>(blockIdx.y) * kSeg + kTerms * lane;
+    for (int64_t r = static_cast<int64_t>(blockIdx.x) * (kQuantThreads / 32) + (threadIdx.x >> 5); r < p.rows; r += row_step) {
         const uint8_t *src = static_cast<const uint8_t *>(p.x) + (r * p.ldx + c) * kElem;
-        float x[8];
-        if (p.vec && c + 8 <= p.cols) {
+        float x[kTerms];
+        if (p.vec && c + kTerms <= p.cols) {
             if constexpr (kIn == kF32) {
                 const float4 a = __ldcs(reinterpret_cast<const float4 *>(src));
                 const float4 b = __ldcs(reinterpret_cast<const float4 *>(src) + 1);
@@ -365,16 +473,17 @@ __global__ void __launch_bounds__(kQuantThreads) quant_kernel(const QuantParams 
                 x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
             } else {
                 const uint4 a = __ldcs(reinterpret_cast<const uint4 *>(src));
-                const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+                const uint4 b = __ldcs(reinterpret_cast<const uint4 *>(src) + 1);
+                const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < kTerms / 2; ++i) {
                     x[2 * i] = to_float<kIn == kBF16>(static_cast<uint16_t>(w[i]));
                     x[2 * i + 1] = to_float<kIn == kBF16>(static_cast<uint16_t>(w[i] >> 16));
                 }
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < kTerms; ++i) {
                 x[i] = 0.0f;
                 if (c + i < p.cols) {
                     if constexpr (kIn == kF32)
@@ -384,30 +493,58 @@ __global__ void __launch_bounds__(kQuantThreads) quant_kernel(const QuantParams 
                 }
             }
         }
-        uint32_t top = 0;                        // as bits: a NaN is above all others
+        float top = 0.0f;                        // (a NaN stays)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-        for (int d = p.group / 16; d >= 1; d /= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-        float s = __fmul_rn(__uint_as_float(top), 1.0f / 7.0f);
-        const uint16_t s16 = p.bf16 ? from_float<true>(s) : from_float<false>(s);
-        s = p.bf16 ? to_float<true>(s16) : to_float<false>(s16);
+        for (int i = 0; i < kTerms; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(top) : "f"(fabsf(x[i])));
+        for (int d = p.group / (2 * kTerms); d >= 1; d /= 2)
+            asm("max.NaN.f32 %0, %0, %1;" : "+f"(top) : "f"(__shfl_xor_sync(0xffffffffu, top, d)));
+        const float s32 = __fmul_rn(top, 1.0f / 7.0f);
+        const uint16_t s16 = p.bf16 ? from_float<true>(s32) : from_float<false>(s32);
+        const float s = p.bf16 ? to_float<true>(s16) : to_float<false>(s16);
         const bool finite = s < __int_as_float(0x7f800000);
-        uint32_t word = 0;
-        if (finite && s > 0.0f) {
+        uint32_t word[kTerms / 8];
+        // The usual way, for 16-bit x: a quotient is a tie or at least 2^-12 off every tie
+        // (x and s have 11 bits at most, and x is not below s / 2 there), so x / s rounded to
+        // 2^-14 is on the tie or on its own side of it, and rounding that to a whole number is
+        // rounding the exact quotient.  The sums' last bits are the code, one step 2^-14 and
+        // then 1.  A scale below the type's normal numbers has less than 11 bits of precision and may
+        // leave codes beyond 7: the other way, as for FP32.
+        if (kIn != kF32 && s >= (p.bf16 ? 0x1p-96f : 0x1p-14f) && finite) {
+            const float inverse = __fdividef(1.0f, s);
+#pragma unroll
+            for (int i = 0; i < kTerms / 8; ++i) {
+                // 0x4B400000 is 1.5 2^23 as bits; the codes' top bits come out flipped
+                uint32_t w = 0u - 0x4B400000u * 0x11111111u;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const float fine = fmaf(x[8 * i + q], inverse, 768.0f) - 768.0f;
+                    w += __float_as_uint(fine + (12582912.0f + 8.0f)) << (4 * q);
+                }
+                word[i] = w ^ 0x88888888u;
+            }
+        } else {
             // (a scale whose reciprocal is no normal number: both times 2^96)
             const float up = s < 0x1p-96f ? 0x1p96f : 1.0f;
             const float su = s * up, inverse = __fdividef(1.0f, su);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) word |= (static_cast<uint32_t>(code(x[i] * up, su, inverse)) & 15u) << (4 * i);
+            for (int i = 0; i < kTerms / 8; ++i) {
+                word[i] = 0;
+                if (finite && s > 0.0f)
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) word[i] |= code(x[8 * i + q] * up, su, inverse) << (4 * q);
+            }
         }
         if (c < p.cols) {
             uint8_t *dst = p.q + r * p.ldq + c / 2;
-            if (p.vec && c + 7 <= p.cols) {
-                *reinterpret_cast<uint32_t *>(dst) = word;
+            if (p.vec && c + kTerms - 1 <= p.cols) {
+                if constexpr (kTerms == 16)
+                    *reinterpret_cast<uint2 *>(dst) = make_uint2(word[0], word[1]);
+                else
+                    *reinterpret_cast<uint32_t *>(dst) = word[0];
             } else {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (c + 2 * i < p.cols) dst[i] = static_cast<uint8_t>(word >> (8 * i));
+                for (int i = 0; i < kTerms / 2; ++i)
+                    if (c + 2 * i < p.cols) dst[i] = static_cast<uint8_t>(word[i / 4] >> (8 * (i % 4)));
             }
             if (c % p.group == 0) p.scale[r * p.lds + c / p.group] = finite ? s16 : uint16_t(0x7FFF);
         }
