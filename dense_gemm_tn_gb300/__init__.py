@@ -936,16 +936,24 @@ def tn_gated(A, Bt, offsets=None, act="silu", keep=False, H=None, P=None, stream
     _tensors(torch, A, Bt)
     dtype, device = A.dtype, A.device
     half, kind = _half_type(dtype, "A"), _activation(act)
-    E, M, K, lda, stride_a = _gated_weights(A, dtype, offsets)
-    ldb, T = _tokens(Bt, dtype, K, "Bt"), Bt.shape[0]
-    if offsets is None:
-        _same_device(device, Bt=Bt)
+    sa, sb = A.shape, Bt.shape
+    if (H is None and offsets is None and Bt.dtype is dtype and len(sa) == 2 == len(sb) and sa[1] == sb[1] > 0
+            and sa[0] % 2 == 0 < sa[0] and _plain(torch, A, Bt)):
+        E, M, K, T = 1, sa[0] // 2, sa[1], sb[0]
+        lda = ldb = K
+        stride_a = 0
+        H, ldh = _empty((T, M), dtype, device, stream), M
     else:
-        _same_device(device, Bt=Bt, offsets=offsets)
-    if _elsewhere(device.index):
-        with torch.cuda.device(device):
-            return tn_gated(A, Bt, offsets, act, keep, H, P, stream)
-    H, ldh = _result(H, (T, M), dtype, device, stream, "H")
+        E, M, K, lda, stride_a = _gated_weights(A, dtype, offsets)
+        ldb, T = _tokens(Bt, dtype, K, "Bt"), Bt.shape[0]
+        if offsets is None:
+            _same_device(device, Bt=Bt)
+        else:
+            _same_device(device, Bt=Bt, offsets=offsets)
+        if _elsewhere(device.index):
+            with torch.cuda.device(device):
+                return tn_gated(A, Bt, offsets, act, keep, H, P, stream)
+        H, ldh = _result(H, (T, M), dtype, device, stream, "H")
     ldp = 0
     if keep or P is not None:
         P, ldp = _result(P, (T, 2 * M), torch.float32, device, stream, "P")
@@ -1072,21 +1080,28 @@ def w4_tn(A, Bt, scale_a, group, C=None, stream=None):
     128 or 256 terms -> (N, M) of their type.  For the few tokens of a decode step."""
     torch = _torch or _load_torch()
     _tensors(torch, A, Bt, scale_a)
-    dtype, device = Bt.dtype, A.device
+    dtype, device, sa, sb, ss = Bt.dtype, A.device, A.shape, Bt.shape, scale_a.shape
     half = _half_type(dtype, "Bt")
-    lda = _rows(A, torch.uint8, "A", cuda=False)
-    ldb = _rows(Bt, dtype, "Bt", cuda=False)
-    M, (N, K) = A.shape[0], Bt.shape
     if group not in (32, 64, 128, 256):
         raise ValueError(f"group must be 32, 64, 128 or 256, not {group!r}")
-    if A.shape[1] != (K + 1) // 2:
-        raise ValueError(f"A has {A.shape[1]} bytes a row, {(K + 1) // 2} hold {K} terms")
-    lds = _rows(scale_a, dtype, "scale_a", (M, -(-K // group)), cuda=False)
-    _same_device(device, Bt=Bt, scale_a=scale_a)
-    if _elsewhere(device.index):
-        with torch.cuda.device(device):
-            return w4_tn(A, Bt, scale_a, group, C, stream)
-    C, ldc = _result(C, (N, M), dtype, device, stream, "C")
+    if (C is None and A.dtype is torch.uint8 and scale_a.dtype is dtype and len(sa) == 2 == len(sb) and len(ss) == 2
+            and 0 < sa[1] == (sb[1] + 1) // 2 and sa[0] == ss[0] and ss[1] == -(-sb[1] // group)
+            and A.stride(1) == 1 and sa[0] > 1 and A.get_device() == Bt.get_device() and _plain(torch, Bt, scale_a)):
+        M, (N, K) = sa[0], sb
+        lda, ldb, lds = A.stride(0), K, ss[1]
+        C, ldc = _empty((N, M), dtype, device, stream), M
+    else:
+        lda = _rows(A, torch.uint8, "A", cuda=False)
+        ldb = _rows(Bt, dtype, "Bt", cuda=False)
+        M, (N, K) = A.shape[0], Bt.shape
+        if A.shape[1] != (K + 1) // 2:
+            raise ValueError(f"A has {A.shape[1]} bytes a row, {(K + 1) // 2} hold {K} terms")
+        lds = _rows(scale_a, dtype, "scale_a", (M, -(-K // group)), cuda=False)
+        _same_device(device, Bt=Bt, scale_a=scale_a)
+        if _elsewhere(device.index):
+            with torch.cuda.device(device):
+                return w4_tn(A, Bt, scale_a, group, C, stream)
+        C, ldc = _result(C, (N, M), dtype, device, stream, "C")
     _check(calls.gemm_w4_tn(half, M, N, K, A.data_ptr(), lda, scale_a.data_ptr(), lds, group, Bt.data_ptr(), ldb,
                             C.data_ptr(), ldc, _launch_stream(device.index, stream)))
     return C

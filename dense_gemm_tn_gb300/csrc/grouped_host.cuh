@@ -225,6 +225,42 @@ int grouped_split(const void *kernel, int threads, int smem, int64_t tiles, int6
     return split;
 }
 
+// How one group's product is cut: the rows of a tile, at most, and the parts of the sum
+// (more than one only where may_part says so), so that the last wave of tiles is
+// nearly full.  An estimate in cycles decides: a block of 64 terms takes a CTA pair 2
+// cycles a row of the tile, or the 64 bytes a cycle that its 128 + rows / 2 rows come in
+// at; a tile some 2500 more; and parts are written and read again in FP32.
+// (The rule is the workspace query's too, so it asks no device: 152 SMs.)
+struct ProductCut {
+    int32_t rows, parts;
+};
+
+constexpr int64_t kCutSms = 152, kSumFewRows = 64;
+
+ProductCut cut_product(int group, int64_t rows, int64_t l_tiles, int64_t blocks, int64_t out_elems, bool may_part)
+{
+    const int64_t most = group == 2 ? 256 : 64, gran = 16 * group, slots = kCutSms / group;
+    ProductCut best{static_cast<int32_t>(most), 1};
+    if (rows <= 0 || blocks <= 0) return best;
+    int64_t least = INT64_MAX;
+    for (int64_t h = most; h >= most / 2; h -= gran) {
+        const int64_t r_tiles = (rows + h - 1) / h, steps = (rows + gran - 1) / gran;
+        const int64_t tall = (steps + r_tiles - 1) / r_tiles * gran;          // the rows are spread evenly
+        const int64_t block = group == 2 ? (2 * tall > 256 + tall ? 2 * tall : 256 + tall) : 500;
+        for (int64_t parts = 1; parts <= (may_part ? 16 : 1); ++parts) {
+            if (parts > 1 && parts * 16 > blocks) break;
+            const int64_t waves = (r_tiles * l_tiles * parts + slots - 1) / slots;
+            int64_t cost = waves * ((blocks + parts - 1) / parts * block + 2500);
+            if (parts > 1) cost += 8000 + parts * (out_elems / 256);
+            if (cost < least) {
+                least = cost;
+                best = {static_cast<int32_t>(h), static_cast<int32_t>(parts)};
+            }
+        }
+    }
+    return best;
+}
+
 template <int kOp, int kGroup, int kRows>
 gemm_status_t launch_grouped(const GroupedCall &c, DeviceState &dev, tn::GroupedParams &prm, int variant)
 {
@@ -238,7 +274,7 @@ gemm_status_t launch_grouped(const GroupedCall &c, DeviceState &dev, tn::Grouped
     attr[1].val.clusterDim.x = kGroup;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
-    cfg.blockDim = dim3(tn::kGrThreads, 1, 1);
+    cfg.blockDim = dim3(tn::GroupedWarps<kOp>::kThreads, 1, 1);
     cfg.dynamicSmemBytes = Cfg::kSmemBytes;
     int slots;
     {
@@ -247,6 +283,12 @@ gemm_status_t launch_grouped(const GroupedCall &c, DeviceState &dev, tn::Grouped
         if (n == 0) {
             cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmemBytes);
             if (e != cudaSuccess) return fail(GEMM_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+            if (tn::GroupedWarps<kOp>::kSegmented && kRows > 64) {
+                cudaFuncAttributes fa;
+                e = cudaFuncGetAttributes(&fa, kernel);
+                if (e != cudaSuccess || fa.numRegs < tn::GroupedWarps<kOp>::kRegs)
+                    return fail(GEMM_ERR_CUDA, "%s: the kernel was compiled for fewer registers than it shares out", c.name);
+            }
             int found = dev.sms;
             if (kGroup == 2) {
                 cfg.attrs = attr + 1;
@@ -260,13 +302,21 @@ gemm_status_t launch_grouped(const GroupedCall &c, DeviceState &dev, tn::Grouped
     }
     constexpr int kReads = tn::grouped_reads(kOp), kSpan = kOp == tn::kGrGated ? Cfg::kTileL / 2 : Cfg::kTileL;
     const int64_t l_tiles = (int64_t(prm.l_extent) + kSpan - 1) / kSpan;
-    const int64_t r_tiles = kReads == tn::kGrGradA ? c.E * ((c.M + kRows - 1) / kRows)
-                                                : c.T / kRows + (c.E < c.T ? c.E : c.T);   // an upper bound
+    const int64_t rows = kReads == tn::kGrGradA ? prm.r_extent : c.T;
+    if (kOp >= tn::kGrGated) {
+        if (kOp != tn::kGrGradBAdd)               // (there the call has cut it already)
+            prm.tile_rows = prm.offsets || kRows > 256
+                                ? kRows
+                                : cut_product(kGroup, rows, l_tiles, (int64_t(prm.red) + 63) / 64, 0, false).rows;
+    }
+    const int64_t most = kOp >= tn::kGrGated ? prm.tile_rows : kRows;
+    const int64_t r_tiles = kReads == tn::kGrGradA ? c.E * ((rows + most - 1) / most)
+                                                : c.T / most + (c.E < c.T ? c.E : c.T);   // an upper bound
     if (r_tiles > (int64_t(1) << 30) / l_tiles) return fail(GEMM_ERR_UNSUPPORTED, "%s: too many output tiles", c.name);
-    const int64_t tiles = r_tiles * l_tiles;
+    const int64_t tiles = r_tiles * l_tiles * (kOp == tn::kGrGradBAdd ? prm.parts : 1);
     constexpr int64_t kStageTerms = Cfg::kAtoms * tn::kGrBlock;
-    if constexpr (kGroup == 1)
-        prm.split = grouped_split(reinterpret_cast<const void *>(kernel), tn::kGrThreads, Cfg::kSmemBytes, tiles,
+    if constexpr (kGroup == 1 && kOp != tn::kGrGradBAdd)
+        prm.split = grouped_split(reinterpret_cast<const void *>(kernel), tn::GroupedWarps<kOp>::kThreads, Cfg::kSmemBytes, tiles,
                                   (int64_t(prm.red) + kStageTerms - 1) / kStageTerms, dev.sms, dev.split_slots[kOp]);
     const int cluster = kGroup * prm.split;
     const int grid = static_cast<int>(tiles < slots ? tiles : slots) * cluster;
@@ -427,7 +477,8 @@ gemm_status_t launch_grouped_op(const GroupedCall &c, DeviceState &dev, tn::Grou
     // would then be faster: 64 experts of 2048 x 2048 and 2000 rows 85.7 / 90.4 spread
     // evenly, but 37.2 / 31.6 over 16 of them, 34.4 / 18.4 over four, 31.0 / 16.3 over one.
     constexpr int kReads = tn::grouped_reads(kOp);
-    const bool few = kReads != tn::kGrGradA &&
+    // (A sum in parts has tiles enough: there the rows alone decide.)
+    const bool few = kOp == tn::kGrGradBAdd ? c.T <= kSumFewRows : kReads != tn::kGrGradA &&
                      (c.T <= 32 * c.E ||
                       grouped_tiles(prm.l_extent, kOp == tn::kGrGated ? 64 : 128, c.T, c.E, 64) <= dev.sms);
     gemm_status_t st;

@@ -77,6 +77,25 @@ __host__ __device__ constexpr int grouped_reads(int op)
 constexpr int kGrEpiWarps = 8;               // epilogue warps: two per quarter of the TMEM lanes
 constexpr int kGrThreads = 64 + 32 * kGrEpiWarps;
 
+// The loss's statistics hold sums in their epilogue, whose warps therefore get most of
+// the registers: they are whole warpgroups (two warps before them are idle).  Sums
+// of more than kGrSegment blocks are cut: the tensor cores' running sum drops what is
+// below its last bit, towards zero, at every step of 16 terms, so a long sum is short
+// by some 8e-10 of itself a term (measured: 3.3e-6 at 4096 terms, and 1024 at a time
+// 0.9e-6), all logits alike, which the loss keeps.  The segments' sums are added in FP32,
+// rounded to nearest.
+template <int kOp>
+struct GroupedWarps {
+    static constexpr bool kSegmented = kOp == kGrLossStats;
+    static constexpr int kEpi = kGrEpiWarps, kFirst = kSegmented ? 4 : 2;
+    static constexpr int kThreads = 32 * (kFirst + kEpi), kTurns = kEpi / 4;
+    // (the block's registers, shared out anew: the launch is refused where it was compiled for fewer)
+    static constexpr int kRegs = 168, kRegsLead = 56, kRegsEpi = 224;
+    static_assert(!kSegmented || 32 * (kFirst * kRegsLead + kEpi * kRegsEpi) <= kThreads * kRegs,
+                  "no more registers than the block is launched with");
+};
+constexpr int kGrSegment = 16;
+
 // kGroup CTAs compute a tile of 128 * kGroup (L) x kRows (R).  Its rows are one
 // MMA N side up to 256, or (kRows = 512) two halves that share the L operand,
 // the first of 256 rows: a quarter fewer bytes per MMA out of L2.  A half's
@@ -130,7 +149,10 @@ struct GroupedParams {
     const float *scale_r;
     uint32_t flags;                  // kFlagStall* (test hooks)
     uint64_t wait_limit_ns;
-    SinkParams sink;                 // the operations from kGrGated on
+    // The operations from kGrGated on:
+    int32_t tile_rows;               // rows of the result in a tile at most
+    int32_t parts;                   // kGrGradBAdd: the sum's parts, each a result of its own
+    SinkParams sink;
 };
 
 // Waiter::wait by a converged warp, with one answer for all its lanes.
@@ -172,15 +194,16 @@ struct GroupedWalk {
     const int32_t *start, *before;      // shared memory
     int32_t l_tiles, r_extent, red;
     int32_t e;
+    int32_t most = kRows;               // rows of a tile, at most
 
-    // Tile u (u never decreases over the calls).
+    // Tile u (u never decreases over the calls, or there is one group).
     __device__ __forceinline__ GroupedTile at(int32_t u)
     {
         while (before[e + 1] <= u) ++e;
         GroupedTile t;
         const int32_t group_rows = start[e + 1] - start[e];
         const int32_t rows = kReads == kGrGradA ? r_extent : group_rows;
-        const int32_t tiles = row_tiles(rows, kRows);
+        const int32_t tiles = row_tiles(rows, kOp >= kGrGated ? most : kRows);
         // the rows in steps of kGran, spread evenly: the first `more` tiles have one more
         const int32_t steps = (rows + kGran - 1) / kGran, each = steps / tiles, more = steps - each * tiles;
         int64_t tr, tl;
@@ -262,11 +285,11 @@ __device__ __forceinline__ void acquire_tensormap(const CUtensorMap *map)
 }
 
 // The group tables in shared memory, by all threads of the CTA.
-template <int kOp, int kRows, int kCtaThreads = kGrThreads>
+template <int kOp, int kRows, int kCtaThreads = GroupedWarps<kOp>::kThreads>
 __device__ __forceinline__ void grouped_tables(const GroupedParams &p, int32_t l_tiles, int32_t *start, int32_t *before)
 {
     constexpr int kReads = grouped_reads(kOp);
-    const int32_t E = p.E, T = p.T;
+    const int32_t E = p.E, T = p.T, most = kOp >= kGrGated ? p.tile_rows : kRows;
     for (int32_t i = threadIdx.x; i <= E; i += kCtaThreads) {
         const int32_t o = p.offsets ? p.offsets[i] : (i == 0 ? 0 : T);
         start[i] = o < 0 ? 0 : (o > T ? T : o);
@@ -296,7 +319,7 @@ __device__ __forceinline__ void grouped_tables(const GroupedParams &p, int32_t l
         int32_t sum = 0;
         for (int32_t i = i0; i < i1 && i < E; ++i) {
             const int32_t rows = kReads == kGrGradA ? p.r_extent : start[i + 1] - start[i];
-            sum += row_tiles(rows, kRows) * l_tiles;
+            sum += row_tiles(rows, most) * l_tiles;
         }
         int32_t acc = sum;
         for (int d = 1; d < 32; d *= 2) {
@@ -308,7 +331,7 @@ __device__ __forceinline__ void grouped_tables(const GroupedParams &p, int32_t l
             before[i] = acc;
             if (i < E) {
                 const int32_t rows = kReads == kGrGradA ? p.r_extent : start[i + 1] - start[i];
-                acc += row_tiles(rows, kRows) * l_tiles;
+                acc += row_tiles(rows, most) * l_tiles;
             }
         }
     }
@@ -538,9 +561,12 @@ __device__ __forceinline__ void load_piece(uint32_t t_addr, uint32_t (&v)[2][16]
 }
 
 template <int kOp, int kGroup, int kRows>
-__global__ void __launch_bounds__(kGrThreads, 1) tn_grouped_kernel(const __grid_constant__ GroupedParams p)
+__global__ void __launch_bounds__(GroupedWarps<kOp>::kThreads, 1) tn_grouped_kernel(const __grid_constant__ GroupedParams p)
 {
     using Cfg = GroupedCfg<kGroup, kRows>;
+    using Warps = GroupedWarps<kOp>;
+    constexpr bool kSegmented = Warps::kSegmented, kShareRegs = kSegmented && kRows > 64;
+    static_assert(!kSegmented || (Cfg::kHalves == 1 && kGrSegment % Cfg::kAtoms == 0), "segments are whole stages");
     constexpr int kStages = Cfg::kStages, kAtoms = Cfg::kAtoms;
     constexpr int kReads = grouped_reads(kOp);
     constexpr bool kLMajorK = kReads == kGrProduct, kRMajorK = kReads != kGrGradA;
@@ -586,7 +612,7 @@ __global__ void __launch_bounds__(kGrThreads, 1) tn_grouped_kernel(const __grid_
         }
         for (int b = 0; b < 2; ++b) {
             ptx::mbar_init(accfull_bar(b), 1);
-            ptx::mbar_init(accempty_bar(b), kGrEpiWarps * kGroup);
+            ptx::mbar_init(accempty_bar(b), Warps::kEpi * kGroup);
         }
         ptx::mbar_init(drain_bar, 1);
         ptx::mbar_init(never_bar, 1);
@@ -619,24 +645,37 @@ __global__ void __launch_bounds__(kGrThreads, 1) tn_grouped_kernel(const __grid_
     constexpr int kSpan = kOp == kGrGated ? Cfg::kTileL / 2 : Cfg::kTileL, kCtaSpan = kSpan / kGroup;
     const int32_t l_tiles = (p.l_extent + kSpan - 1) / kSpan;
     grouped_tables<kOp, kRows>(p, l_tiles, start, before);
-    const int32_t total = before[p.E];
+    constexpr bool kParts = kOp == kGrGradBAdd;
+    const int32_t tiles = before[p.E], total = kParts ? tiles * p.parts : tiles;
     // (grad_a's sums are the groups' own rows: not split)
-    constexpr bool kMaySplit = kGroup == 1 && kReads != kGrGradA;
+    constexpr bool kMaySplit = kGroup == 1 && kReads != kGrGradA && !kParts;
     static_assert(!kMaySplit || kRows <= 2 * kGrChunk, "the pieces of a split sum are four by two at most");
     const int32_t split = kMaySplit ? p.split : 1;
     const int32_t ctas = kGroup * split;
     const int32_t slot = static_cast<int32_t>(blockIdx.x) / ctas, slots = static_cast<int32_t>(gridDim.x) / ctas;
     const SplitSum parts{s_ring, split, split > 1 ? static_cast<int32_t>(ptx::cluster_ctarank()) : 0};
-    // the blocks of a sum of `blocks` that are this CTA's: whole stages
+    // of the blocks of a sum of `blocks`, those before the `rank`th CTA's of the cluster, or
+    // before the `rank`th part: whole stages
     auto part = [&](int32_t blocks, int32_t rank) {
-        if (!kMaySplit) return rank == 0 ? 0 : blocks;
-        const int32_t stages = (blocks + kAtoms - 1) / kAtoms, to = stages * rank / split * kAtoms;
+        if (!kMaySplit && !kParts) return rank == 0 ? 0 : blocks;
+        const int32_t stages = (blocks + kAtoms - 1) / kAtoms;
+        const int32_t to = static_cast<int32_t>(static_cast<int64_t>(stages) * rank / (kParts ? p.parts : split)) * kAtoms;
         return to < blocks ? to : blocks;
     };
     GroupedWalk<kOp, kRows, Cfg::kHalfRows, Cfg::kTileL, Cfg::kGran> walk{start, before, l_tiles, p.r_extent, p.red, 0};
+    if constexpr (kSinks) walk.most = p.tile_rows;
+    auto tile_at = [&](int32_t u) { return walk.at(kParts ? u % tiles : u); };
+    auto rank_of = [&](int32_t u) { return kParts ? u / tiles : parts.rank; };
     auto blocks_of = [](int32_t red) { return (red + kGrBlock - 1) / kGrBlock; };
+    // a part of a sum that is too short for all of them
+    auto no_terms = [&](const GroupedTile &t, int32_t u) {
+        return kParts && part(blocks_of(t.red), rank_of(u)) == part(blocks_of(t.red), rank_of(u) + 1);
+    };
 
     bool joins = false;                           // an epilogue warp whose tile's split sum is complete here
+    uint32_t kept[2][16];                         // ... of segments: its own part of its piece
+    if (warp < Warps::kFirst) {
+    if constexpr (kShareRegs) ptx::setmaxnreg_dec<Warps::kRegsLead>();
     if (warp == 0) {
         // ------------------------------------------------ TMA producer (every CTA)
         // A pair's loads all complete on the even CTA's full[s][a], which its own
@@ -650,7 +689,7 @@ __global__ void __launch_bounds__(kGrThreads, 1) tn_grouped_kernel(const __grid_
                 ok = wait_warp(w, never_bar, 0u, kSiteStall);
             int32_t mapped = -1;
             for (int32_t u = slot; ok && u < total; u += slots) {
-                const GroupedTile t = walk.at(u);
+                const GroupedTile t = tile_at(u);
                 const int32_t l0 = t.l0 + static_cast<int32_t>(pos) * kCtaSpan;
                 int32_t cols[2], r0[2];       // this CTA's R elements of either half, and the first
                 uint32_t r_bytes = 0;
@@ -678,7 +717,7 @@ __global__ void __launch_bounds__(kGrThreads, 1) tn_grouped_kernel(const __grid_
                     }
                 }
                 const int32_t sum_blocks = blocks_of(t.red);
-                const int32_t begin = part(sum_blocks, parts.rank), blocks = part(sum_blocks, parts.rank + 1);
+                const int32_t begin = part(sum_blocks, rank_of(u)), blocks = part(sum_blocks, rank_of(u) + 1);
                 for (int32_t i = begin; i < blocks; i += kAtoms) {
                     if (!wait_warp(w, empty_bar(stage), phase ^ 1u, kSiteEmpty)) {
                         ok = false;
@@ -813,8 +852,8 @@ __global__ void __launch_bounds__(kGrThreads, 1) tn_grouped_kernel(const __grid_
             constexpr uint32_t kStepL = kLMajorK ? 2 : 128, kStepR = kRMajorK ? 2 : 128;   // 16 terms on, in 16-byte units
             if (p.flags & kFlagStallMma) ok = wait_warp(w, never_bar, 0u, kSiteStall);
             for (int32_t u = slot; ok && u < total; u += slots) {
-                const GroupedTile t = walk.at(u);
-                if (t.red == 0) continue;
+                const GroupedTile t = tile_at(u);
+                if (t.red == 0 || no_terms(t, u)) continue;
                 const int halves = Cfg::kHalves == 2 && t.n_mma[1] > 0 ? 2 : 1;
                 uint32_t idesc[2], d_tmem[2];
 #pragma unroll
@@ -826,7 +865,7 @@ __global__ void __launch_bounds__(kGrThreads, 1) tn_grouped_kernel(const __grid_
                 if (!wait_warp(w, accempty_bar(sub & 1u), ((sub >> 1) & 1u) ^ 1u, kSiteAccEmpty)) break;
                 ptx::tc_fence_after_sync();
                 const int32_t sum_blocks = blocks_of(t.red);
-                const int32_t begin = part(sum_blocks, parts.rank), blocks = part(sum_blocks, parts.rank + 1);
+                const int32_t begin = part(sum_blocks, rank_of(u)), blocks = part(sum_blocks, rank_of(u) + 1);
                 // The MMAs of block i, in atom a of stage s, for half h.  Terms past the end
                 // of the sum are zeros: whole steps of them are left out.
                 auto issue = [&](int s, int a, int32_t i, int h) {
@@ -839,7 +878,7 @@ __global__ void __launch_bounds__(kGrThreads, 1) tn_grouped_kernel(const __grid_
                     for (int j = 0; j < kGrBlock / 16; ++j)
                         if (left > 16 * j)
                             ptx::mma_f16<kGroup>(d_tmem[h], desc_l + kStepL * j, desc_r + kStepR * j, idesc[h],
-                                                 (i - begin) | j ? 1u : 0u);
+                                                 (kSegmented ? (i - begin) % kGrSegment : i - begin) | j ? 1u : 0u);
                 };
                 // A tile's second half may have to wait for the epilogue to read its
                 // accumulator.  Until then stages are held with only their first half's MMAs
@@ -861,6 +900,19 @@ __global__ void __launch_bounds__(kGrThreads, 1) tn_grouped_kernel(const __grid_
                     }
                 };
                 for (int32_t i = begin; ok && i < blocks; i += kAtoms) {
+                    if constexpr (kSegmented) {
+                        if (i > begin && (i - begin) % kGrSegment == 0) {      // on to the other accumulator
+                            if (ptx::elect_one()) ptx::mma_commit<kGroup>(accfull_bar(sub & 1u), kMask);
+                            __syncwarp();
+                            ++sub;
+                            d_tmem[0] = tmem_base + (sub & 1u) * Cfg::kAccCols;
+                            if (!wait_warp(w, accempty_bar(sub & 1u), ((sub >> 1) & 1u) ^ 1u, kSiteAccEmpty)) {
+                                ok = false;
+                                break;
+                            }
+                            ptx::tc_fence_after_sync();
+                        }
+                    }
 #pragma unroll
                     for (int a = 0; a < kAtoms; ++a) {
                         if (!wait_warp(w, full_bar(stage, a), phase, kSiteLoaded)) {
@@ -919,18 +971,50 @@ __global__ void __launch_bounds__(kGrThreads, 1) tn_grouped_kernel(const __grid_
                 w.drain(drain_bar, 0u);
             }
         }
+    }
     } else {
-        // ------------------------------------------------ epilogue (warps 2..9, every CTA)
+        // ------------------------------------------------ epilogue (warps 2..9, or 4..11, every CTA)
+        if constexpr (kShareRegs) ptx::setmaxnreg_inc<Warps::kRegsEpi>();
         const int quarter = warp & 3;             // TMEM lanes 32*quarter .. +31 are this warp's
-        const int turn = (warp - 2) >> 2;         // of the columns' steps, the quarter's two warps take every other one
+        const int turn = (warp - Warps::kFirst) >> 2;        // of the columns' steps, the quarter's two warps take every other one
         GroupedStore store;
-        store.init(s_staging + (warp - 2) * kGrStageBytes, lane);
+        store.init(s_staging + (warp - Warps::kFirst) * kGrStageBytes, lane);
         store.ld = p.out_ld;
         uint32_t sub = 0;                         // halves so far
         bool ok = true;
         const bool out_bf16 = p.out_fmt != 0;
         for (int32_t u = slot; ok && u < total; u += slots) {
-            const GroupedTile t = walk.at(u);
+            const GroupedTile t = tile_at(u);
+            if constexpr (kSegmented && kMaySplit) {
+                if (split > 1) {                  // as below, its segments' sums in registers
+                    const int32_t sum_blocks = blocks_of(t.red);
+                    const int32_t n = part(sum_blocks, parts.rank + 1) - part(sum_blocks, parts.rank);
+                    bool got = true;
+                    for (int32_t i = 0; got && i < n; i += kGrSegment, ++sub) {
+                        got = wait_warp(w, accfull_bar(sub & 1u), (sub >> 1) & 1u, kSiteAccFull);
+                        if (!got) break;
+                        ptx::tc_fence_after_sync();
+                        if (turn * kGrChunk < t.n_mma[0]) {
+                            uint32_t v[2][16];
+                            load_piece(tmem_base + (static_cast<uint32_t>(32 * quarter) << 16) + (sub & 1u) * Cfg::kAccCols +
+                                           turn * kGrChunk, v);
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                                for (int x = 0; x < 16; ++x)
+                                    kept[h][x] = i == 0 ? v[h][x]
+                                                        : __float_as_uint(__uint_as_float(kept[h][x]) + __uint_as_float(v[h][x]));
+                        }
+                        ptx::tc_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(accempty_bar(sub & 1u));
+                    }
+                    joins = got;
+                    if (got && turn * kGrChunk < t.n_mma[0] && !parts.mine(quarter, turn))
+                        parts.leave(parts.at(quarter, turn, lane), kept);
+                    break;
+                }
+            }
             if (split > 1) {                      // the cluster's one tile, stored further down
                 ok = joins = wait_warp(w, accfull_bar(0), 0u, kSiteAccFull);
                 if (!ok) break;
@@ -948,14 +1032,78 @@ __global__ void __launch_bounds__(kGrThreads, 1) tn_grouped_kernel(const __grid_
             uint16_t *out = p.out + t.e * p.out_stride + row0 * p.out_ld + l0;
             store.wide = p.l_extent - l0 < 32 ? p.l_extent - l0 : 32;
             store.vec = p.out_vec != 0 && store.wide == 32;
-            if (t.red == 0) {                     // an empty sum
+            if (t.red == 0 || no_terms(t, u)) {   // an empty sum
                 if constexpr (kSinks) {
                     const uint32_t zero[2][16] = {};
-                    for (int32_t c = turn * kGrChunk; c < t.rows; c += 2 * kGrChunk)
-                        Sink<kOp>::step(p, store, zero, l0, row0 + c, t.rows - c);
+                    for (int32_t c = turn * kGrChunk; c < t.rows; c += Warps::kTurns * kGrChunk)
+                        Sink<kOp>::step(p, store, zero, l0, row0 + c, t.rows - c, kParts ? rank_of(u) : 0);
                 } else if (lane < store.wide) {
                     for (int32_t r = turn; r < t.rows; r += 2) out[r * p.out_ld + lane] = 0;
                 }
+                continue;
+            }
+            if constexpr (kSegmented) {
+                constexpr int kSteps = Cfg::kHalfRows / kGrChunk / Warps::kTurns > 0
+                                           ? Cfg::kHalfRows / kGrChunk / Warps::kTurns : 1;
+                const int32_t sum_blocks = blocks_of(t.red), steps = (t.n_mma[0] + kGrChunk - 1) / kGrChunk;
+                const uint32_t t_lanes = tmem_base + (static_cast<uint32_t>(32 * quarter) << 16);
+                auto hand_back = [&]() {
+                    ptx::tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if constexpr (kGroup == 2)
+                            ptx::mbar_arrive_remote(ptx::mapa_shared(accempty_bar(sub & 1u), 0));
+                        else
+                            ptx::mbar_arrive(accempty_bar(sub & 1u));
+                    }
+                };
+                float sum[kSteps][2][16];
+                for (int32_t i = 0; i < sum_blocks; i += kGrSegment, ++sub) {
+                    ok = wait_warp(w, accfull_bar(sub & 1u), (sub >> 1) & 1u, kSiteAccFull);
+                    if (!ok) break;
+                    ptx::tc_fence_after_sync();
+                    const uint32_t t_acc = t_lanes + (sub & 1u) * Cfg::kAccCols;
+                    const bool last = i + kGrSegment >= sum_blocks;
+                    // (a sum of one segment stays where it is)
+                    if (!last || i > 0) {
+#pragma unroll
+                        for (int q = 0; q < kSteps; ++q) {
+                            const int32_t s = turn + q * Warps::kTurns;
+                            if (s >= steps) break;
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const uint32_t addr = t_acc + (static_cast<uint32_t>(16 * h) << 16) + s * kGrChunk;
+                                uint32_t v[16];
+                                ptx::tmem_ld_16x256b_x4(addr, v);
+                                ptx::tmem_ld_wait_all();
+                                ptx::reg_dependency(v);
+#pragma unroll
+                                for (int x = 0; x < 16; ++x)
+                                    sum[q][h][x] = i == 0 ? __uint_as_float(v[x]) : sum[q][h][x] + __uint_as_float(v[x]);
+                                if (last) {       // back to where the last segment was
+#pragma unroll
+                                    for (int x = 0; x < 16; ++x) v[x] = __float_as_uint(sum[q][h][x]);
+                                    ptx::tmem_st_16x256b_x4(addr, v);
+                                }
+                            }
+                        }
+                        if (!last) {
+                            hand_back();
+                            continue;
+                        }
+                        ptx::tmem_st_wait();
+                    }
+#pragma unroll 1
+                    for (int32_t s = turn; s < steps; s += Warps::kTurns) {
+                        const int32_t c = s * kGrChunk;
+                        uint32_t v[2][16];
+                        load_piece(t_acc + c, v);
+                        if (s + Warps::kTurns >= steps) hand_back();
+                        Sink<kOp>::step(p, store, v, l0, row0 + c, t.rows - c, 0);
+                    }
+                    if (turn >= steps) hand_back();
+                }
+                if (!ok) break;
                 continue;
             }
 #pragma unroll 1
@@ -984,7 +1132,7 @@ __global__ void __launch_bounds__(kGrThreads, 1) tn_grouped_kernel(const __grid_
                 if constexpr (kSinks)
                     GroupedStore::each_step(t_row, turn, steps, hand_back, [&](int32_t s, const uint32_t (&v)[2][16]) {
                         const int32_t c = s * kGrChunk;
-                        Sink<kOp>::step(p, store, v, l0, row0 + first + c, rows - c);
+                        Sink<kOp>::step(p, store, v, l0, row0 + first + c, rows - c, kParts ? rank_of(u) : 0);
                     });
                 else if (out_bf16)
                     store.half<true, false>(t_row, turn, steps, dst, rows, nullptr, hand_back);
@@ -1004,20 +1152,27 @@ __global__ void __launch_bounds__(kGrThreads, 1) tn_grouped_kernel(const __grid_
                 const GroupedTile t = walk.at(slot);
                 const int32_t l0 = t.l0 + kCtaSpan / 4 * quarter;
                 GroupedStore store;
-                store.init(s_staging + (warp - 2) * kGrStageBytes, lane);
+                store.init(s_staging + (warp - Warps::kFirst) * kGrStageBytes, lane);
                 store.ld = p.out_ld;
                 store.wide = p.l_extent - l0 < 32 ? p.l_extent - l0 : 32;
                 store.vec = p.out_vec != 0 && store.wide == 32;
                 const int64_t row0 = static_cast<int64_t>(start[t.e]) + t.r0;
                 uint16_t *out = p.out + row0 * p.out_ld + l0;
-                for (int s = (warp - 2) >> 2; s * kGrChunk < t.n_mma[0]; s += 2) {
+                for (int s = (warp - Warps::kFirst) >> 2; s * kGrChunk < t.n_mma[0]; s += Warps::kTurns) {
                     if (!parts.mine(quarter, s)) continue;
                     uint32_t v[2][16];
-                    load_piece(tmem_base + (static_cast<uint32_t>(32 * quarter) << 16) + s * kGrChunk, v);
+                    if constexpr (kSegmented) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+#pragma unroll
+                            for (int x = 0; x < 16; ++x) v[h][x] = kept[h][x];
+                    } else {
+                        load_piece(tmem_base + (static_cast<uint32_t>(32 * quarter) << 16) + s * kGrChunk, v);
+                    }
                     parts.add_others(parts.at(quarter, s, lane), v);
                     const int32_t c = s * kGrChunk;
                     if constexpr (kSinks)
-                        Sink<kOp>::step(p, store, v, l0, row0 + c, t.rows - c);
+                        Sink<kOp>::step(p, store, v, l0, row0 + c, t.rows - c, 0);
                     else if (p.out_fmt != 0)
                         store.step<true, false>(v, out + c * p.out_ld, t.rows - c, nullptr);
                     else

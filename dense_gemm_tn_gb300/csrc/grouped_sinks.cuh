@@ -28,8 +28,8 @@ struct SinkParams {
     float *z_target;                 // loss: [T] the target's logit
     const float2 *rows;              // loss gradient: [T] (log-sum-exp, factor)
     int32_t first, classes;          // loss gradient: the piece's first class, and how many
-    float *sum;                      // parts added up: FP32 sums
-    int64_t sum_ld;
+    float *sum;                      // parts added up: FP32 sums, one result for each part
+    int64_t sum_ld, sum_stride;
     int32_t add;                     // parts added up: AddPart
     const float *out_scale;          // the result's factor (one float), or NULL
 };
@@ -121,7 +121,7 @@ struct Sink<4 /* kGrGated */> {
 
     template <class Params, class Store>
     static __device__ __forceinline__ void step(const Params &p, const Store &store, const uint32_t (&v)[2][16],
-                                                int32_t l0, int64_t row, int32_t rows)
+                                                int32_t l0, int64_t row, int32_t rows, int32_t part)
     {
         const SinkParams &k = p.sink;
         const int lane = store.lane;
@@ -170,9 +170,10 @@ struct Sink<4 /* kGrGated */> {
 // ------------------------------------------------------------------ loss
 // A token's 32 logits of the piece become their maximum and the sum of their
 // exponentials above it, both in FP32; cross_entropy_join_kernel adds up the
-// pieces.  A thread's four logits of a column first give its own pair; pairs are
-// then merged over the eight lanes that share the columns, half of the columns
-// passed on each time: 7 exchanges of a pair for 8 columns.
+// pieces.  A column's logits lie in eight lanes, four in each, and a lane has four of
+// eight columns.  So the columns' maxima and sums are merged by halving: each turn a
+// lane passes on half of its columns, 7 exchanges for 8 columns, and 7 more take the
+// maxima back to all lanes before the exponentials.
 template <>
 struct Sink<5 /* kGrLossStats */> {
     static __device__ __forceinline__ void merge(float &m, float &s, float om, float os)
@@ -184,49 +185,62 @@ struct Sink<5 /* kGrLossStats */> {
         s = a + b;
     }
 
-    template <class Params, class Store>
-    static __device__ __forceinline__ void step(const Params &p, const Store &store, const uint32_t (&v)[2][16],
-                                                int32_t l0, int64_t row, int32_t rows)
+    // x[j]: the lane's share of column 2 i + c = j; leaves the whole of its own column, 4 b4 +
+    // 2 b3 + b2 (bn: bit n of the lane), in x[0].
+    template <class Op>
+    static __device__ __forceinline__ void halve(float (&x)[8], int lane, Op op)
     {
-        if (l0 >= p.l_extent) return;             // (past the last class: no piece)
-        const SinkParams &k = p.sink;
-        const int lane = store.lane;
-        const int32_t m0 = l0 + (lane >> 2);
-        const float none = __int_as_float(0xff800000);
-        float m[8], s[8];                         // [2 i + c]
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                float z[4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    z[q] = m0 + 8 * q < p.l_extent ? __uint_as_float(v[q >> 1][4 * i + 2 * (q & 1) + c]) : none;
-                const float top = fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3]));
-                // a maximum of -inf: of classes past the end alone, or of logits that are
-                const float from = top == none ? 0.0f : top;
-                float sum = 0.0f;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) sum += ex2((z[q] - from) * kLog2e);
-                m[2 * i + c] = top;
-                s[2 * i + c] = sum;
-            }
-        // after the three turns a lane holds column 8 (2 b4 + b3) + 2 (lane % 4) + b2 (bn: bit n of it)
 #pragma unroll
         for (int d = 4, bit = 16; d >= 1; d /= 2, bit /= 2) {
             const bool upper = lane & bit;
 #pragma unroll
             for (int j = 0; j < d; ++j) {
-                const float om = __shfl_xor_sync(0xffffffffu, upper ? m[j] : m[j + d], bit);
-                const float os = __shfl_xor_sync(0xffffffffu, upper ? s[j] : s[j + d], bit);
-                float mm = upper ? m[j + d] : m[j], ss = upper ? s[j + d] : s[j];
-                merge(mm, ss, om, os);
-                m[j] = mm;
-                s[j] = ss;
+                const float other = __shfl_xor_sync(0xffffffffu, upper ? x[j] : x[j + d], bit);
+                x[j] = op(upper ? x[j + d] : x[j], other);
             }
         }
-        const int32_t col = 8 * (2 * (lane >> 4 & 1) + (lane >> 3 & 1)) + 2 * (lane & 3) + (lane >> 2 & 1);
-        if (col < rows) k.stats[static_cast<int64_t>(l0 >> 5) * p.T + row + col] = make_float2(m[0], s[0]);
+    }
+
+    template <class Params, class Store>
+    static __device__ __forceinline__ void step(const Params &p, const Store &store, const uint32_t (&v)[2][16],
+                                                int32_t l0, int64_t row, int32_t rows, int32_t part)
+    {
+        if (l0 >= p.l_extent) return;             // (past the last class: no piece)
+        const SinkParams &k = p.sink;
+        const int lane = store.lane;
+        const float none = __int_as_float(0xff800000);
+        const int32_t left = p.l_extent - l0 - (lane >> 2);     // of the lane's classes 0, 8, 16 and 24
+        auto logit = [&](int j, int q) {
+            const float z = __uint_as_float(v[q >> 1][4 * (j >> 1) + 2 * (q & 1) + (j & 1)]);
+            return 8 * q < left ? z : none;
+        };
+        float x[8], m[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m[j] = fmaxf(fmaxf(logit(j, 0), logit(j, 1)), fmaxf(logit(j, 2), logit(j, 3)));
+        halve(m, lane, [](float a, float b) { return fmaxf(a, b); });
+        const float top = m[0];
+#pragma unroll
+        for (int d = 1, bit = 4; d <= 4; d *= 2, bit *= 2) {
+            const bool upper = lane & bit;
+#pragma unroll
+            for (int j = 0; j < d; ++j) {
+                const float other = __shfl_xor_sync(0xffffffffu, m[j], bit);
+                const float mine = m[j];
+                m[j] = upper ? other : mine;
+                m[j + d] = upper ? mine : other;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            // (a maximum of -inf: of logits that all are)
+            const float from = m[j] == none ? 0.0f : m[j];
+            x[j] = (ex2((logit(j, 0) - from) * kLog2e) + ex2((logit(j, 1) - from) * kLog2e)) +
+                   (ex2((logit(j, 2) - from) * kLog2e) + ex2((logit(j, 3) - from) * kLog2e));
+        }
+        halve(x, lane, [](float a, float b) { return a + b; });
+        const int32_t own = 4 * (lane >> 4 & 1) + 2 * (lane >> 3 & 1) + (lane >> 2 & 1);
+        const int32_t col = 8 * (own >> 1) + 2 * (lane & 3) + (own & 1);
+        if (col < rows) k.stats[static_cast<int64_t>(l0 >> 5) * p.T + row + col] = make_float2(top, x[0]);
         // the target's logit, where this piece has it
         int64_t at = -1;
         if (lane < rows) at = __ldg(k.targets + row + lane) - l0;
@@ -254,7 +268,7 @@ template <>
 struct Sink<6 /* kGrLossGrad */> {
     template <class Params, class Store>
     static __device__ __forceinline__ void step(const Params &p, const Store &store, const uint32_t (&v)[2][16],
-                                                int32_t l0, int64_t row, int32_t rows)
+                                                int32_t l0, int64_t row, int32_t rows, int32_t part)
     {
         const SinkParams &k = p.sink;
         const int lane = store.lane;
@@ -294,19 +308,21 @@ struct Sink<6 /* kGrLossGrad */> {
 };
 
 // ------------------------------------------------------------------ sums in parts
-// A sum over parts of the vocabulary, one launch each: the first leaves FP32 sums,
-// the next ones add theirs (each element once a launch, so the order is the
-// launches'), and the last one's result is rounded once.
+// A token gradient's sum may be cut twice.  Pieces of the vocabulary are launches: the
+// first leaves FP32 sums, the next ones add theirs (each element once a launch, so the
+// order is the launches'), and the last one's result is rounded once.  And where a
+// launch's tiles are few, parts of its sum are tiles of their own, each part with
+// sums of its own; parts_join_kernel adds them up in their order.
 template <>
 struct Sink<7 /* kGrGradBAdd */> {
     template <class Params, class Store>
     static __device__ __forceinline__ void step(const Params &p, const Store &store, const uint32_t (&v)[2][16],
-                                                int32_t l0, int64_t row, int32_t rows)
+                                                int32_t l0, int64_t row, int32_t rows, int32_t part)
     {
         const SinkParams &k = p.sink;
         const int lane = store.lane;
         const int32_t c0 = 2 * (lane & 3), m0 = lane >> 2;
-        float *sum = k.sum + (row + c0) * k.sum_ld + l0 + m0;
+        float *sum = k.sum + part * k.sum_stride + (row + c0) * k.sum_ld + l0 + m0;
         uint32_t x[2][16];
         const float scale = k.out_scale ? __ldg(k.out_scale) : 1.0f;
 #pragma unroll
@@ -343,7 +359,7 @@ template <>
 struct Sink<8 /* kGrGradAOne */> {
     template <class Params, class Store>
     static __device__ __forceinline__ void step(const Params &p, const Store &store, const uint32_t (&v)[2][16],
-                                                int32_t l0, int64_t row, int32_t rows)
+                                                int32_t l0, int64_t row, int32_t rows, int32_t part)
     {
         const float scale = p.sink.out_scale ? __ldg(p.sink.out_scale) : 1.0f;
         uint32_t x[2][16];
@@ -449,6 +465,53 @@ __global__ void __launch_bounds__(kRowsThreads) cross_entropy_rows_kernel(const 
     }
     for (int64_t n = threadIdx.x; n < p.N; n += kRowsThreads) p.rows[n] = make_float2(p.lse[n], factor(n) * up);
     if (threadIdx.x == 0) *p.scale = 1.0f / up;
+}
+
+// ------------------------------------------------------------------ parts of a sum, joined
+// out = scale (sum of the parts, in their order), rounded once.  Reads 4 bytes an
+// element and part, writes 2.
+constexpr int kPartsThreads = 256;
+
+struct PartsParams {
+    const float *sum;                // parts of rows x cols, sum_ld floats a row
+    int64_t sum_ld, sum_stride;
+    uint16_t *out;
+    int64_t ld;
+    const float *scale;              // one float, or NULL
+    int64_t rows;
+    int32_t cols, parts;
+    bool bf16;
+    bool vec;                        // four elements a thread: rows on 16-byte (out: 8-byte) boundaries
+};
+
+__global__ void __launch_bounds__(kPartsThreads) parts_join_kernel(const PartsParams p)
+{
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    const float scale = p.scale ? __ldg(p.scale) : 1.0f;
+    const int32_t per = p.vec ? 4 : 1, units = (p.cols + per - 1) / per;
+    const int32_t c = static_cast<int32_t>(blockIdx.x) * kPartsThreads + static_cast<int32_t>(threadIdx.x);
+    if (c >= units) return;
+    for (int64_t r = blockIdx.y; r < p.rows; r += gridDim.y) {
+        const float *from = p.sum + r * p.sum_ld + c * per;
+        uint16_t *out = p.out + r * p.ld + c * per;
+        float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+        for (int32_t q = 0; q < p.parts; ++q, from += p.sum_stride) {
+            if (p.vec) {
+                const float4 v = __ldcs(reinterpret_cast<const float4 *>(from));
+                x[0] += v.x, x[1] += v.y, x[2] += v.z, x[3] += v.w;
+            } else {
+                x[0] += *from;
+            }
+        }
+        const uint32_t lo = p.bf16 ? ptx::pack_bf16x2(x[0] * scale, x[1] * scale) : ptx::pack_f16x2(x[0] * scale, x[1] * scale);
+        const uint32_t hi = p.bf16 ? ptx::pack_bf16x2(x[2] * scale, x[3] * scale) : ptx::pack_f16x2(x[2] * scale, x[3] * scale);
+        if (p.vec)
+            *reinterpret_cast<uint2 *>(out) = make_uint2(lo, hi);
+        else
+            *out = static_cast<uint16_t>(lo);
+    }
 }
 
 // ------------------------------------------------------------------ gated: backward

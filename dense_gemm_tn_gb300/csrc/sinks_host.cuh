@@ -89,6 +89,49 @@ gemm_status_t launch_plain(const char *name, void (*kernel)(Args...), dim3 grid,
     return GEMM_OK;
 }
 
+// ------------------------------------------------------------------ token gradients in parts
+// The cut of one group's token gradient: T rows of K, sums of `red` terms.
+ProductCut token_grad_cut(int64_t T, int64_t K, int64_t red)
+{
+    const int group = T <= kSumFewRows ? 1 : 2;
+    return cut_product(group, T, (K + 128 * group - 1) / (128 * group), (red + 63) / 64, T * K, true);
+}
+
+// Floats of the parts' sums: none where a tile's sum is whole when it is stored.
+size_t token_grad_floats(const ProductCut &cut, int64_t pieces, int64_t T, int64_t K)
+{
+    return cut.parts > 1 || pieces > 1 ? size_t(cut.parts) * size_t(T) * size_t(K) : 0;
+}
+
+// Piece i of `pieces` of dB = scale (d A): A's `c.M` rows (x), d's rows of `red` gradients.
+gemm_status_t launch_token_grad(const GroupedCall &c, DeviceState &dev, const ProductCut &cut, const void *x, int64_t ldx,
+                                int64_t in_x, const uint16_t *d, int64_t ldd, int64_t red, void *dB, int64_t lddb,
+                                const float *scale, float *sum, int64_t i, int64_t pieces)
+{
+    tn::GroupedParams prm = sink_params(c, c.K, red, dB, lddb);
+    prm.tile_rows = cut.rows;
+    prm.parts = cut.parts;
+    prm.sink.sum = sum;
+    prm.sink.sum_ld = c.K;
+    prm.sink.sum_stride = c.T * c.K;
+    prm.sink.out_scale = scale;
+    prm.sink.add = cut.parts == 1 && pieces == 1         ? tn::kAddOnly
+                   : i == 0                              ? tn::kAddFirst
+                   : cut.parts == 1 && i + 1 == pieces   ? tn::kAddLast
+                                                         : tn::kAddMore;
+    gemm_status_t st = launch_grouped_op<tn::kGrGradBAdd>(c, dev, prm, x, d, ldx, 0, ldd, in_x, (red + 7) / 8 * 8);
+    if (st != GEMM_OK || cut.parts == 1 || i + 1 < pieces) return st;
+    tn::PartsParams p{sum, c.K, c.T * c.K, static_cast<uint16_t *>(dB), lddb, scale, c.T, static_cast<int32_t>(c.K), cut.parts,
+                      c.type == GEMM_IN_BF16, c.K % 4 == 0 && lddb % 4 == 0 && aligned_to(dB, 8)};
+    const int64_t units = p.vec ? c.K / 4 : c.K;
+    const int64_t gx = (units + tn::kPartsThreads - 1) / tn::kPartsThreads;
+    int64_t gy = (int64_t(dev.sms) * 16 + gx - 1) / gx;
+    if (gy > c.T) gy = c.T;
+    if (gy > 65535) gy = 65535;
+    return launch_plain(c.name, tn::parts_join_kernel, dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy), 1),
+                        tn::kPartsThreads, 0, c.stream, p);
+}
+
 // ------------------------------------------------------------------ gated projections
 bool gated_sizes_fit(int64_t E, int64_t M, int64_t K, int64_t T, int64_t lda, int64_t ldb, int64_t stride)
 {
@@ -98,6 +141,8 @@ bool gated_sizes_fit(int64_t E, int64_t M, int64_t K, int64_t T, int64_t lda, in
 struct GatedPlan {
     GroupedPlan g;               // the copies (and the backward pass's tensor maps)
     int64_t ldd;                 // the backward pass's rows of 2 M gradients, padded
+    ProductCut cut;              // without experts: of the token gradient
+    size_t floats;               // ... and its parts' sums
     size_t bytes;
     bool fits;
 };
@@ -121,6 +166,11 @@ GatedPlan gated_plan(bool grad, bool dense, int64_t E, int64_t M, int64_t K, int
     p.g.map_bytes = dense ? 0 : size_t(E) * 2 * sizeof(CUtensorMap);
     p.fits = grouped_copy(p.g.x, false, false) && grouped_copy(p.g.y, false, false) && T <= (int64_t(1) << 60) / p.ldd;
     p.bytes = p.g.bytes() + ((size_t(T) * size_t(p.ldd) * 2 + 255) & ~size_t(255));
+    if (dense) {
+        p.cut = token_grad_cut(T, K, 2 * M);
+        p.floats = token_grad_floats(p.cut, 1, T, K);
+        p.bytes += (p.floats * sizeof(float) + 255) & ~size_t(255);
+    }
     return p;
 }
 
@@ -156,6 +206,36 @@ gemm_status_t check_gated(const char *name, int type, int act, int64_t E, int64_
     return GEMM_OK;
 }
 
+// A decode step's tokens go to a kernel of their own (where the general one would read
+// the operands in place).
+int64_t few_rows_limit() { return getenv("GFEW") ? atoi(getenv("GFEW")) : 16; }
+#define kGatedFewRows few_rows_limit()
+
+template <bool kBf16, int kTilesN>
+gemm_status_t launch_gated_few(const char *name, DeviceState &dev, const tn::GatedFewParams &p, cudaStream_t stream)
+{
+    auto kernel = tn::gated_few_kernel<kBf16, kTilesN>;
+    const int64_t ctas = int64_t(p.tiles) * (p.offsets ? (p.E < p.T ? p.E : p.T) : 1);
+    if (ctas > INT32_MAX) return fail(GEMM_ERR_UNSUPPORTED, "%s: too many output tiles", name);
+    {
+        std::lock_guard<std::mutex> lock(g_mutex);
+        bool &set = dev.few_attr[kBf16][kTilesN - 1];
+        if (!set) {
+            const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, tn::kFewRingBytes);
+            if (e != cudaSuccess) return fail(GEMM_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+            set = true;
+        }
+    }
+    t_rec = LaunchRecord{};
+    t_rec.name = name;
+    t_rec.grouped = 1;
+    t_rec.cluster = 1;
+    t_rec.grid = static_cast<int>(ctas);
+    t_rec.slots = dev.sms;
+    t_rec.tiles = static_cast<int>(ctas);
+    return launch_plain(name, kernel, dim3(static_cast<unsigned>(ctas), 1, 1), tn::kFewThreads, tn::kFewRingBytes, stream, p);
+}
+
 gemm_status_t run_gated(int type, int act, int64_t E, int64_t M, int64_t K, int64_t T, const void *A, int64_t lda,
                         int64_t stride_a, const void *B, int64_t ldb, const int32_t *offsets, void *H, int64_t ldh, float *P,
                         int64_t ldp, void *workspace, int64_t workspace_bytes, cudaStream_t stream)
@@ -179,6 +259,14 @@ gemm_status_t run_gated(int type, int act, int64_t E, int64_t M, int64_t K, int6
     if ((st = check_workspace(name, workspace, workspace_bytes, plan.bytes, "gemm_gated_workspace")) != GEMM_OK) return st;
     DeviceState *dev = nullptr;
     if ((st = device_state(&dev, nullptr)) != GEMM_OK) return st;
+    if (K > 0 && T <= kGatedFewRows && !plan.g.x.copy && !plan.g.y.copy) {
+        const tn::GatedFewParams p{static_cast<const uint16_t *>(A), lda, stride_a, static_cast<const uint16_t *>(B), ldb, offsets,
+                                   static_cast<uint16_t *>(H), ldh, P, ldp, static_cast<int32_t>(E), static_cast<int32_t>(T),
+                                   static_cast<int32_t>(M), static_cast<int32_t>(K), static_cast<int32_t>((M + 15) / 16), act};
+        if (type == GEMM_IN_BF16)
+            return T <= 8 ? launch_gated_few<true, 1>(name, *dev, p, stream) : launch_gated_few<true, 2>(name, *dev, p, stream);
+        return T <= 8 ? launch_gated_few<false, 1>(name, *dev, p, stream) : launch_gated_few<false, 2>(name, *dev, p, stream);
+    }
 
     Sections ws{static_cast<uint8_t *>(workspace)};
     SinkOperands o{};
@@ -253,9 +341,11 @@ gemm_status_t run_gated_grad(int type, int act, int64_t E, int64_t M, int64_t K,
     plan.g.y.copy &= dA != nullptr;
     SinkOperands o{};
     uint16_t *dP = nullptr;
+    float *sum = nullptr;
     if (!idle) {
         if ((st = place_operands(name, *dev, plan.g, ws, offsets, stream, o)) != GEMM_OK) return st;
         dP = ws.take<uint16_t>(size_t(T) * size_t(plan.ldd));
+        if (plan.floats) sum = ws.take<float>(plan.floats);
         const tn::GatedGradParams p{P, ldp, static_cast<const uint16_t *>(dH), lddh, dP, plan.ldd, offsets,
                                     static_cast<int32_t>(E), static_cast<int32_t>(T), static_cast<int32_t>(M)};
         const bool bf16 = type == GEMM_IN_BF16;
@@ -269,8 +359,12 @@ gemm_status_t run_gated_grad(int type, int act, int64_t E, int64_t M, int64_t K,
     c.stream = stream;
     const int copied = (plan.g.x.copy ? 1 : 0) | (plan.g.y.copy ? 2 : 0);
     if (dB) {
-        tn::GroupedParams prm = sink_params(c, K, 2 * M, dB, lddb);
-        st = launch_grouped_op<tn::kGrGradB>(c, *dev, prm, o.x, dP, o.ldx, o.stride_x, plan.ldd, o.in_x, plan.ldd);
+        if (!offsets && !idle) {
+            st = launch_token_grad(c, *dev, plan.cut, o.x, o.ldx, o.in_x, dP, plan.ldd, 2 * M, dB, lddb, nullptr, sum, 0, 1);
+        } else {
+            tn::GroupedParams prm = sink_params(c, K, 2 * M, dB, lddb);
+            st = launch_grouped_op<tn::kGrGradB>(c, *dev, prm, o.x, dP, o.ldx, o.stride_x, plan.ldd, o.in_x, plan.ldd);
+        }
         t_rec.copied = copied;
         if (st != GEMM_OK) return st;
     }
@@ -300,6 +394,8 @@ constexpr int64_t kLossPieceBytes = int64_t(1) << 27, kLossMinPiece = 1024;
 struct LossPlan {
     GroupedPlan g;
     int64_t pieces, piece;       // classes of a piece (the last may have fewer)
+    ProductCut cut;              // of the token gradient over a piece
+    size_t floats;               // ... and its parts' sums
     int64_t blocks;              // forward: 32 classes each
     size_t bytes;
     bool fits;
@@ -331,7 +427,9 @@ LossPlan loss_plan(bool grad, int64_t M, int64_t N, int64_t K, const void *A, in
         add(N, p.piece * 2);
         add(N, sizeof(float2));
         add(1, sizeof(float));
-        if (p.pieces > 1 && K > 0) add(N, K * int64_t(sizeof(float)));
+        p.cut = token_grad_cut(N, K, p.piece);
+        p.floats = token_grad_floats(p.cut, p.pieces, N, K);
+        if (p.floats) add(N, p.cut.parts * K * int64_t(sizeof(float)));
     }
     p.bytes = p.g.bytes() + bytes;
     return p;
@@ -453,7 +551,7 @@ gemm_status_t run_loss_grad(int type, int64_t M, int64_t N, int64_t K, const voi
     uint16_t *d = ws.take<uint16_t>(size_t(N) * size_t(ldd));
     float2 *rows = ws.take<float2>(size_t(N));
     float *scale = ws.take<float>(1);
-    float *sum = plan.pieces > 1 ? ws.take<float>(size_t(N) * size_t(K)) : nullptr;
+    float *sum = plan.floats ? ws.take<float>(plan.floats) : nullptr;
     const tn::LossRowsParams rp{targets, lse, dloss, rows, scale, N, M, type == GEMM_IN_F16};
     if ((st = launch_plain(name, tn::cross_entropy_rows_kernel, dim3(1, 1, 1), tn::kRowsThreads, 0, stream, rp)) != GEMM_OK)
         return st;
@@ -468,17 +566,8 @@ gemm_status_t run_loss_grad(int type, int64_t M, int64_t N, int64_t K, const voi
         prm.sink.first = static_cast<int32_t>(first);
         prm.sink.classes = static_cast<int32_t>(classes);
         st = launch_grouped_op<tn::kGrLossGrad>(c, *dev, prm, x, o.y, o.ldx, 0, o.ldy, o.in_x, o.in_y);
-        if (st == GEMM_OK && dB) {
-            prm = sink_params(c, K, padded, dB, lddb);
-            prm.sink.sum = sum;
-            prm.sink.sum_ld = K;
-            prm.sink.add = plan.pieces == 1         ? tn::kAddOnly
-                           : i == 0                 ? tn::kAddFirst
-                           : i + 1 < plan.pieces    ? tn::kAddMore
-                                                    : tn::kAddLast;
-            prm.sink.out_scale = scale;
-            st = launch_grouped_op<tn::kGrGradBAdd>(c, *dev, prm, x, d, o.ldx, 0, ldd, o.in_x, padded);
-        }
+        if (st == GEMM_OK && dB)
+            st = launch_token_grad(c, *dev, plan.cut, x, o.ldx, o.in_x, d, ldd, classes, dB, lddb, scale, sum, i, plan.pieces);
         if (st == GEMM_OK && dA) {
             prm = sink_params(c, K, N, static_cast<uint16_t *>(dA) + first * ldda, ldda);
             prm.r_extent = static_cast<int32_t>(classes);

@@ -28,6 +28,7 @@
 #include "i8_kernel.cuh"
 #include "quant_i8_kernel.cuh"
 #include "w4_kernel.cuh"
+#include "gated_few_kernel.cuh"
 
 namespace {
 
@@ -99,6 +100,7 @@ struct DeviceState {
     bool skinny_attr[2] = {};         // tn_skinny_kernel's shared-memory attribute set, by kind
     int grouped_slots[tn::kGrOps][3] = {};   // co-resident tn_grouped_kernel CTAs or pairs, by operation and variant (0 = not queried)
     int split_slots[tn::kGrOps][3] = {};     // co-resident clusters of 2, 4 and 8 single CTAs, by operation (8-bit: 2)
+    bool few_attr[2][2] = {};         // gated_few_kernel's shared-memory attribute set, by type and token tiles
     bool i8_attr = false;             // tn_i8_kernel's shared-memory attribute set
     int i8_pair_slots[2] = {};        // co-resident pairs of tn_i8_pair_kernel, by its kRuns (0 = not queried)
     // One lock per stream, held by a call from its first buffer lookup through

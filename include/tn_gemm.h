@@ -392,7 +392,7 @@ gemm_status_t gemm_quantize_i8_rows(const void *x, int x_type, int64_t rows, int
  * gemm_tn_gated, else 1; dense: not 0 where offsets is NULL), -1 for sizes it would
  * refuse.  The forward call needs none where the TMA reads the operands in place
  * (base, lda, ldb, stride_a and K multiples of 16 bytes); the backward call holds dP
- * there (4 M T bytes).  Ownership and alignment as for gemm_tn_grouped.
+ * there (4 M T bytes) and, without offsets, up to 16 FP32 sums of dB (64 K T bytes).  Ownership and alignment as for gemm_tn_grouped.
  *
  * Errors: as for gemm_tn_grouped, and GEMM_ERR_INVALID_ARG for an unknown
  * activation, or offsets NULL with E != 1.
@@ -446,7 +446,7 @@ gemm_status_t gemm_tn_gated_grad(int type, int act, int64_t E, int64_t M, int64_
  * Workspace: gemm_cross_entropy_workspace returns the bytes that a call needs (grad:
  * 0 for gemm_tn_cross_entropy, else 1), -1 for sizes it would refuse: forward N M / 4
  * + 4 N, gradient about 128 MiB (2048 N beyond 65536 tokens; 2 N M where that is
- * less) + 4 N K, and copies of operands that the TMA cannot read in place (as for
+ * less) + up to 64 N K, and copies of operands that the TMA cannot read in place (as for
  * gemm_tn_grouped).  Ownership and alignment as there.
  *
  * Errors: GEMM_ERR_INVALID_ARG for an unknown type, a negative size, M == 0 with

@@ -35,20 +35,32 @@ def check(A, Bt, targets, dloss, dtype, stream=None):
 
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("N,M,K", [(1, 1, 1), (1, 2, 8), (2, 33, 17), (31, 32, 64), (1, 5000, 256), (33, 257, 100), (64, 1000, 136),
-                                   (130, 4099, 72), (257, 3001, 264), (1000, 700, 40), (7, 70001, 64)])
+                                   (130, 4099, 72), (257, 3001, 264), (1000, 700, 40), (7, 70001, 64),
+                                   (5, 900, 4104), (64, 3000, 1096), (300, 2100, 2048), (257, 40000, 1100)])
 def test_loss_and_gradients(N, M, K, dtype):
     A, Bt, targets, dloss = operands(N, M, K, dtype)
     check(A, Bt, targets, dloss, dtype)
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("N,M", [(40000, 3500), (20000, 7777)])
-def test_pieces_of_the_vocabulary(N, M, dtype):
-    """Several pieces: sums that go on from one to the next, targets in each of them, a short last one."""
-    A, Bt, targets, dloss = operands(N, M, 48, dtype)
-    assert tn.gemm_cross_entropy_workspace(1, M, N, 48, A, 48, Bt, 48) < 2 * N * M
-    targets[:M] = torch.arange(M, device="cuda")
+@pytest.mark.parametrize("N,M,K", [(40000, 3500, 48), (20000, 7777, 48), (4000, 40000, 72), (65537, 9217, 24)])
+def test_pieces_of_the_vocabulary(N, M, K, dtype):
+    """Several pieces: sums that go on from one to the next (also in parts), targets in each of them, a last one of one class."""
+    A, Bt, targets, dloss = operands(N, M, K, dtype)
+    assert tn.gemm_cross_entropy_workspace(1, M, N, K, A, K, Bt, K) < 2 * N * M
+    n = min(N, M)
+    targets[:n] = torch.arange(M - n, M, device="cuda")
     check(A, Bt, targets, dloss, dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("N,M,K", [(1, 20000, 200), (64, 30000, 136), (65, 30001, 64), (500, 20011, 264), (1021, 9000, 520), (2500, 4100, 1000)])
+def test_sums_in_parts(N, M, K, dtype):
+    """Few tokens and many classes: the token gradient's sums in parts."""
+    A, Bt, targets, dloss = operands(N, M, K, dtype)
+    first = check(A, Bt, targets, dloss, dtype)
+    again = tn.tn_cross_entropy_grad(A, Bt, targets, first[1], dloss)
+    assert torch.equal(first[2], again[0]) and torch.equal(first[3], again[1])
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
@@ -65,6 +77,18 @@ def test_ignored_tokens(dtype):
     loss, lse = tn.tn_cross_entropy(A, Bt, targets)
     dA, dB = tn.tn_cross_entropy_grad(A, Bt, targets, lse, dloss)
     assert not bool(loss.any()) and not bool(dA.any()) and not bool(dB.any())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("N,M", [(40, 1000), (600, 2000)])
+def test_long_sums_lose_nothing(N, M, dtype):
+    """8192 terms: sums of 1024, each short by 64 steps' truncations at most (2^-24 of the running sum each, half of
+    that on average, and the running sum half of the whole), all logits alike: the loss within 2^-18 of itself."""
+    A, Bt, targets, dloss = operands(N, M, 8192, dtype)
+    loss, lse = tn.tn_cross_entropy(A, Bt, targets)
+    ref, lse_ref, _, _, _, _ = loss64(A, Bt, targets)
+    assert float((loss.double() - ref).norm() / ref.norm()) < 2.0 ** -18
+    assert float((lse.double() - lse_ref).norm() / lse_ref.norm()) < 2.0 ** -19
 
 
 def test_targets_that_are_no_class():

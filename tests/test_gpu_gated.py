@@ -37,7 +37,8 @@ def check(A, Bt, dH, offsets, bounds, act, dtype, stream=None):
 
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("T,M,K", [(1, 1, 1), (1, 64, 64), (3, 17, 33), (1, 1000, 520), (33, 16, 8), (65, 200, 136), (130, 129, 72),
-                                   (300, 513, 264), (777, 1000, 1000), (2048, 512, 256), (1, 4096, 2048), (16, 2048, 4096)])
+                                   (300, 513, 264), (777, 1000, 1000), (2048, 512, 256), (1, 4096, 2048), (16, 2048, 4096),
+                                   (300, 5000, 256), (64, 6000, 100), (65, 6001, 128), (1000, 3000, 520)])
 def test_dense(T, M, K, dtype):
     A, Bt, dH = operands(1, T, M, K, dtype)
     check(A, Bt, dH, None, [0, T], ACTS[(T + M + K) % 3], dtype)
