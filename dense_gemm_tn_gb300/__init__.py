@@ -1019,13 +1019,22 @@ def _loss_operands(A, Bt, **vectors):
     """(GEMM_IN_..., M, N, K, lda, ldb) of a vocabulary A (M, K), tokens Bt (N, K) and what belongs to the tokens."""
     torch = _torch or _load_torch()
     _tensors(torch, A, Bt, *vectors.values())
-    half = _half_type(A.dtype, "A")
-    M, N, K, lda, ldb = _operands(A, Bt, A.dtype)
+    half, sa, sb = _half_type(A.dtype, "A"), A.shape, Bt.shape
+    if len(sa) == 2 == len(sb) and sa[1] == sb[1] > 0 < sa[0] and Bt.dtype is A.dtype and _plain(torch, A, Bt, *vectors.values()):
+        for name, t in vectors.items():
+            if t.dim() != 1 or t.shape[0] != sb[0] or t.dtype is not (torch.int64 if name == "targets" else torch.float32):
+                break
+        else:
+            return half, sa[0], sb[0], sa[1], sa[1], sa[1]
+    lda, ldb = _rows(A, A.dtype, "A", cuda=False), _rows(Bt, A.dtype, "Bt", cuda=False)
+    (M, K), N = A.shape, Bt.shape[0]
+    if Bt.shape[1] != K:
+        raise ValueError(f"A is {tuple(A.shape)} and Bt {tuple(Bt.shape)}: their second dimensions (K) differ")
     if M == 0 and N > 0:
         raise ValueError("A has no rows: there are no classes")
     for name, t in vectors.items():
         _vector(t, torch.int64 if name == "targets" else torch.float32, N, name)
-    _same_device(A.device, **vectors)
+    _same_device(A.device, Bt=Bt, **vectors)
     return half, M, N, K, lda, ldb
 
 
@@ -1115,24 +1124,30 @@ def quantize_w4_rows(x, group, dtype=None, stream=None):
     torch = _torch or _load_torch()
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise ValueError("x must be a 2-D float32/float16/bfloat16 tensor")
-    kind = GEMM_IN_F32 if x.dtype is torch.float32 else _half_kinds.get(x.dtype)
+    xtype, device = x.dtype, x.device
+    kind = GEMM_IN_F32 if xtype is torch.float32 else _half_kinds.get(xtype)
     if kind is None:
         raise ValueError("x must be a 2-D float32/float16/bfloat16 tensor")
-    if dtype is None and x.dtype is torch.float32:
-        raise ValueError("dtype must say which 16-bit type the scales of a float32 tensor have")
-    dtype = dtype or x.dtype
+    if dtype is None:
+        if xtype is torch.float32:
+            raise ValueError("dtype must say which 16-bit type the scales of a float32 tensor have")
+        dtype = xtype
     half = _half_type(dtype, "dtype")
     if group not in (32, 64, 128, 256):
         raise ValueError(f"group must be 32, 64, 128 or 256, not {group!r}")
-    device = x.device
-    ldx = _rows(x, x.dtype, "x")
-    if _elsewhere(device.index):
-        with torch.cuda.device(device):
-            return quantize_w4_rows(x, group, dtype, stream)
     rows, cols = x.shape
+    if cols > 0 and _plain(torch, x):
+        ldx = cols
+    else:
+        ldx = _rows(x, xtype, "x")
+        if _elsewhere(device.index):
+            with torch.cuda.device(device):
+                return quantize_w4_rows(x, group, dtype, stream)
     row_bytes, groups = (cols + 1) // 2, -(-cols // group)
     ldq = max(-(-row_bytes // 16) * 16, 1)
-    q = _empty((rows, ldq), torch.uint8, device, stream)[:, :row_bytes]
+    q = _empty((rows, ldq), torch.uint8, device, stream)
+    if ldq != row_bytes:
+        q = q[:, :row_bytes]
     scale = _empty((rows, groups), dtype, device, stream)
     _check(calls.gemm_quantize_w4_rows(x.data_ptr(), kind, rows, cols, ldx, group, q.data_ptr(), ldq, half, scale.data_ptr(),
                                        max(groups, 1), _launch_stream(device.index, stream)))

@@ -3,6 +3,16 @@
 
 bool w4_group_ok(int64_t group) { return group == 32 || group == 64 || group == 128 || group == 256; }
 
+void record_w4(const char *name, const DeviceState &dev, int64_t tiles)
+{
+    t_rec = LaunchRecord{};
+    t_rec.name = name;
+    t_rec.grouped = 1;
+    t_rec.cluster = 1;
+    t_rec.grid = t_rec.tiles = static_cast<int>(tiles);
+    t_rec.slots = dev.sms;
+}
+
 template <bool kBf16, int kTilesM, int kTilesN>
 gemm_status_t launch_w4(const char *name, DeviceState &dev, w4::ProductParams &p, bool aligned, cudaStream_t stream)
 {
@@ -20,20 +30,47 @@ gemm_status_t launch_w4(const char *name, DeviceState &dev, w4::ProductParams &p
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
         if (e != cudaSuccess) return fail(GEMM_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
     }
-    t_rec = LaunchRecord{};
-    t_rec.name = name;
-    t_rec.grouped = 1;
-    t_rec.cluster = 1;
-    t_rec.grid = static_cast<int>(tiles);
-    t_rec.slots = dev.sms;
-    t_rec.tiles = static_cast<int>(tiles);
+    record_w4(name, dev, tiles);
     return launch_plain(name, kernel, dim3(static_cast<unsigned>(tiles), 1, 1), w4::kThreads, smem, stream, p);
 }
 
+template <bool kBf16, int kTilesM, int kTilesN, bool kWhole>
+gemm_status_t launch_w4_wide(const char *name, DeviceState &dev, w4::ProductParams &p, cudaStream_t stream)
+{
+    using Cfg = w4::WideCfg<kTilesM, kTilesN, kWhole>;
+    auto kernel = w4::wide_kernel<kBf16, kTilesM, kTilesN, kWhole>;
+    p.token_tiles = static_cast<int32_t>((int64_t(p.N) + Cfg::kTokens - 1) / Cfg::kTokens);
+    const int64_t tiles = (int64_t(p.M) + Cfg::kRows - 1) / Cfg::kRows * p.token_tiles;
+    if (tiles > INT32_MAX) return fail(GEMM_ERR_UNSUPPORTED, "%s: too many tiles", name);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kBytes);
+    if (e != cudaSuccess) return fail(GEMM_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+    record_w4(name, dev, tiles);
+    return launch_plain(name, kernel, dim3(static_cast<unsigned>(tiles), 1, 1), w4::kThreads, Cfg::kBytes, stream, p);
+}
+
+template <bool kBf16, int kTilesM, int kTilesN>
+gemm_status_t launch_w4_wide(const char *name, DeviceState &dev, w4::ProductParams &p, cudaStream_t stream)
+{
+    return p.group_shift >= 7 ? launch_w4_wide<kBf16, kTilesM, kTilesN, true>(name, dev, p, stream)
+                              : launch_w4_wide<kBf16, kTilesM, kTilesN, false>(name, dev, p, stream);
+}
+
+// Up to 8 tokens, few rows and rows that are not aligned: warps split the sum (two tiles
+// of 16 rows each where that still leaves 1.5 CTAs an SM: 8192 x 8192 and one token
+// 12.3 us, one tile 14.1; 1024 x 4096 4.3 and 3.4).  More tokens over rows that give nearly every SM
+// a tile of 64: warps share the tokens.  Measured on GB300 at K = 4096, groups of 128,
+// split / shared: 16 tokens, 4096 rows 7.3 / 11.3 us, 8192 13.0 / 11.8, 28672 35.1 / 26.5; 64 tokens
+// 17.7 / 24.4, 33.1 / 25.0, 96.4 / 72.4.
 template <bool kBf16>
 gemm_status_t launch_w4_tokens(const char *name, DeviceState &dev, w4::ProductParams &p, bool aligned, cudaStream_t stream)
 {
-    const bool many = int64_t(p.M) >= 24 * int64_t(dev.sms);
+    const int64_t M = p.M, sms = dev.sms;
+    if (aligned && p.N > 8 && M >= 53 * sms) {
+        if (p.N <= 16) return launch_w4_wide<kBf16, 1, 2>(name, dev, p, stream);
+        if (p.N <= 32) return launch_w4_wide<kBf16, 1, 4>(name, dev, p, stream);
+        return launch_w4_wide<kBf16, 1, 8>(name, dev, p, stream);
+    }
+    const bool many = M >= 24 * sms;
     if (p.N <= 8)
         return many ? launch_w4<kBf16, 2, 1>(name, dev, p, aligned, stream) : launch_w4<kBf16, 1, 1>(name, dev, p, aligned, stream);
     if (p.N <= 16)
@@ -103,6 +140,9 @@ gemm_status_t run_quant_w4(const void *x, int x_type, int64_t rows, int64_t cols
         return fail(GEMM_ERR_INVALID_ARG, "%s: a leading dimension is below its row's length", name);
     if (cols > kMaxDim || rows > (int64_t(1) << 40) / (cols > 1 ? cols : 1))
         return fail(GEMM_ERR_UNSUPPORTED, "%s: more than 2^40 elements", name);
+    const int64_t seg = x_type == w4::kF32 ? w4::QuantCfg<w4::kF32>::kSeg : w4::QuantCfg<w4::kF16>::kSeg;
+    const int64_t segs = (cols + seg - 1) / seg;  // a launch's second index
+    if (segs > 65535) return fail(GEMM_ERR_UNSUPPORTED, "%s: too many columns", name);
     if (rows == 0 || cols == 0) return GEMM_OK;
     if (!x || !q || !scale) return fail(GEMM_ERR_INVALID_ARG, "%s: x, q or scale is NULL", name);
     const int64_t esz = x_type == w4::kF32 ? 4 : 2;
@@ -125,9 +165,6 @@ gemm_status_t run_quant_w4(const void *x, int x_type, int64_t rows, int64_t cols
     p.bf16 = scale_type == GEMM_IN_BF16;
     p.vec = aligned_to(x, 16) && aligned_to(q, 8) && (rows == 1 || (ldx * esz % 16 == 0 && ldq % 8 == 0));
     const int64_t per = w4::kQuantThreads / 32;
-    const int64_t seg = x_type == w4::kF32 ? w4::QuantCfg<w4::kF32>::kSeg : w4::QuantCfg<w4::kF16>::kSeg;
-    const int64_t segs = (cols + seg - 1) / seg;
-    if (segs > 65535) return fail(GEMM_ERR_UNSUPPORTED, "%s: too many columns", name);
     int64_t grid = (rows + per - 1) / per;
     const int64_t most = (int64_t(dev->sms) * 64 + segs - 1) / segs;
     if (grid > most) grid = most;

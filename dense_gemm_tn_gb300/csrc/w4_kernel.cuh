@@ -412,6 +412,226 @@ __global__ void __launch_bounds__(kThreads) product_kernel(const __grid_constant
     }
 }
 
+// ------------------------------------------------------------------ more than 8 tokens
+// Tokens weigh as much as codes from here on, so warps share them: a CTA's warps are
+// kWideRows (rows of 16 kTilesM each) by kWideSums (parts of the sum), and step
+// through the sum together, kWideSums blocks of 128 terms a stage, codes and tokens copied
+// to shared memory kDepth - 1 stages ahead.  Aligned rows only; what a row or the tokens
+// lack of the last block arrives as zeros.
+constexpr int kWideRows = 4, kWideSums = 2;
+static_assert(kWideRows * kWideSums == kWarps, "all of them");
+
+template <int kTilesM, int kTilesN, bool kWhole>
+struct WideCfg {
+    static constexpr int kRows = 16 * kTilesM * kWideRows, kTokens = 8 * kTilesN;
+    // A token's block of 16 pieces (16 bytes).  kWhole: lane t reads piece 4 t + j, which the
+    // swizzle and a pitch of 9 banks of 32 bytes keep from meeting; else piece 4 j + t.
+    static constexpr int kTokenPitch = kWhole ? 256 + 32 : 256 + 64;
+    static constexpr int kCodeBytes = kRows * kWideSums * 64, kTokenBytes = kTokens * kWideSums * kTokenPitch;
+    static constexpr int kStageBytes = kCodeBytes + kTokenBytes;
+    static constexpr int kDepth = kTilesN <= 2 ? 4 : kTilesN <= 4 ? 3 : 2;
+    static constexpr int kSumFloats = kTokens * (kRows + 4);
+    static constexpr int kBytes = kDepth * kStageBytes > 4 * kWideSums * kSumFloats ? kDepth * kStageBytes
+                                                                                      : 4 * kWideSums * kSumFloats;
+};
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, int32_t bytes)
+{
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr)
+{
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+template <bool kBf16, int kTilesM, int kTilesN, bool kWhole>
+__global__ void __launch_bounds__(kThreads) wide_kernel(const __grid_constant__ ProductParams p)
+{
+    using Cfg = WideCfg<kTilesM, kTilesN, kWhole>;
+    extern __shared__ __align__(16) float wide_smem[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    const int part = warp % kWideSums, row0 = warp / kWideSums * 16 * kTilesM;    // this warp's share of the sum, its rows
+    const int32_t tile = static_cast<int32_t>(blockIdx.x) / p.token_tiles;
+    const int32_t n0 = (static_cast<int32_t>(blockIdx.x) - tile * p.token_tiles) * Cfg::kTokens;
+    const int32_t m0 = tile * Cfg::kRows;
+
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+
+    constexpr int kStep = kWideSums * kBlock;                // terms of a stage
+    const int32_t stages = (p.K + kStep - 1) / kStep, row_bytes = (p.K + 1) / 2;
+    const uint32_t smem = ptx::smem_addr(wide_smem);
+
+    // What this thread copies of every stage: codes, 16 bytes of a row each (4 kWideSums to a
+    // row), then tokens (16 kWideSums to a token).
+    constexpr int kCodePieces = Cfg::kCodeBytes / 16, kTokenPieces = Cfg::kTokens * kWideSums * 16;
+    constexpr int kCodeTurns = (kCodePieces + kThreads - 1) / kThreads, kTokenTurns = (kTokenPieces + kThreads - 1) / kThreads;
+    const uint8_t *code_src[kCodeTurns];
+    const uint16_t *token_src[kTokenTurns];
+    uint32_t code_dst[kCodeTurns], token_dst[kTokenTurns];
+    int32_t code_at[kCodeTurns], token_at[kTokenTurns], token_bytes[kTokenTurns];      // first byte, first term
+#pragma unroll
+    for (int i = 0; i < kCodeTurns; ++i) {
+        const int x = threadIdx.x + i * kThreads, r = x / (4 * kWideSums), c = x % (4 * kWideSums);
+        code_at[i] = 16 * c;
+        code_src[i] = p.a + min(m0 + r, p.M - 1) * p.lda + 16 * c;
+        // (not kWhole: the four lanes of a row read a word each of the same piece)
+        const int piece = kWhole ? c & 3 : (c & 3) ^ (r >> 1 & 3);
+        code_dst[i] = ((c >> 2) * Cfg::kRows + r) * 64 + 16 * piece;
+    }
+#pragma unroll
+    for (int i = 0; i < kTokenTurns; ++i) {
+        const int x = threadIdx.x + i * kThreads, n = x / (16 * kWideSums), c = x % (16 * kWideSums);
+        token_at[i] = 8 * c;
+        token_bytes[i] = n0 + n < p.N && n < Cfg::kTokens ? 16 : 0;      // (no such token: zeros)
+        token_src[i] = p.b + min(n0 + n, p.N - 1) * p.ldb + 8 * c;
+        const int piece = kWhole ? (c & 15) ^ (c >> 3 & 1) : c & 15;
+        token_dst[i] = Cfg::kCodeBytes + ((c >> 4) * Cfg::kTokens + n) * Cfg::kTokenPitch + 16 * piece;
+    }
+    // The copies of a stage into ring slot `slot`, the pointers on to the next one's.  A whole
+    // stage's are all 16 bytes; of the last one's what the rows and tokens lack arrives as zeros.
+    const int32_t whole = p.K / kStep;
+    auto copy = [&](int32_t stage, int slot) {
+        if (stage < stages) {
+            const uint32_t to = smem + slot * Cfg::kStageBytes;
+            const int32_t k0 = stage * kStep;
+#pragma unroll
+            for (int i = 0; i < kCodeTurns; ++i) {
+                if (kCodePieces % kThreads && static_cast<int>(threadIdx.x) + i * kThreads >= kCodePieces) break;
+                int32_t bytes = 16;
+                if (stage >= whole) bytes = max(min(row_bytes - k0 / 2 - code_at[i], 16), 0);
+                copy16(to + code_dst[i], bytes ? code_src[i] : p.a, bytes);
+                code_src[i] += kStep / 2;
+            }
+#pragma unroll
+            for (int i = 0; i < kTokenTurns; ++i) {
+                if (kTokenPieces % kThreads && static_cast<int>(threadIdx.x) + i * kThreads >= kTokenPieces) break;
+                int32_t bytes = token_bytes[i];
+                if (stage >= whole) bytes = max(min(2 * min(p.K - k0 - token_at[i], 8), bytes), 0);
+                copy16(to + token_dst[i], bytes ? token_src[i] : p.b, bytes);
+                token_src[i] += kStep;
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    const uint16_t *s_row[kTilesM][2];
+#pragma unroll
+    for (int i = 0; i < kTilesM; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) s_row[i][h] = p.scale + min(m0 + row0 + 16 * i + 8 * h + g, p.M - 1) * p.lds;
+    struct Scales {
+        uint16_t v[kTilesM][2];
+    };
+    auto load_scales = [&](int32_t stage, Scales &s) {
+        const int32_t grp = (stage * kStep + part * kBlock + (kWhole ? 0 : 32 * t)) >> p.group_shift;
+#pragma unroll
+        for (int i = 0; i < kTilesM; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) s.v[i][h] = grp < p.groups ? __ldg(s_row[i][h] + grp) : uint16_t(0);
+    };
+
+    float acc[kTilesM][kTilesN][4] = {};
+#pragma unroll
+    for (int s = 0; s < Cfg::kDepth - 1; ++s) copy(s, s);
+    Scales next;
+    load_scales(0, next);
+#pragma unroll 1
+    for (int32_t first = 0; first < stages; first += Cfg::kDepth) {
+#pragma unroll
+    for (int slot = 0; slot < Cfg::kDepth; ++slot) {
+        const int32_t stage = first + slot;
+        if (slot > 0 && stage >= stages) break;
+        asm volatile("cp.async.wait_group %0;" ::"n"(Cfg::kDepth - 2) : "memory");
+        __syncthreads();                         // the stage is whole, and the one before it done with
+        copy(stage + Cfg::kDepth - 1, (slot + Cfg::kDepth - 1) % Cfg::kDepth);
+        const Scales now = next;
+        load_scales(stage + 1, next);
+        const uint32_t from = smem + slot * Cfg::kStageBytes;
+        const uint32_t codes = from + (part * Cfg::kRows + row0 + g) * 64;
+        const uint32_t tokens = from + Cfg::kCodeBytes + (part * Cfg::kTokens + g) * Cfg::kTokenPitch;
+        uint4 code[kTilesM][2];
+#pragma unroll
+        for (int i = 0; i < kTilesM; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t at = codes + (16 * i + 8 * h) * 64;
+                if constexpr (kWhole) {
+                    code[i][h] = ld_shared(at + 16 * t);
+                } else {
+                    const uint32_t x = g >> 1 & 3;           // (row0, 16 i and 8 h leave these bits of the row)
+                    code[i][h] = make_uint4(ld_shared_u32(at + 16 * x + 4 * t), ld_shared_u32(at + 16 * (1 ^ x) + 4 * t),
+                                            ld_shared_u32(at + 16 * (2 ^ x) + 4 * t), ld_shared_u32(at + 16 * (3 ^ x) + 4 * t));
+                }
+            }
+        float sum[kTilesM][kTilesN][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint32_t x[kTilesN][4];
+#pragma unroll
+            for (int n = 0; n < kTilesN; ++n) {
+                const int piece = kWhole ? (4 * t + j) ^ (t >> 1) : 4 * j + t;
+                const uint4 v = ld_shared(tokens + 8 * n * Cfg::kTokenPitch + 16 * piece);
+                x[n][0] = __byte_perm(v.x, v.z, 0x5410);
+                x[n][1] = __byte_perm(v.x, v.z, 0x7632);
+                x[n][2] = __byte_perm(v.y, v.w, 0x5410);
+                x[n][3] = __byte_perm(v.y, v.w, 0x7632);
+            }
+#pragma unroll
+            for (int i = 0; i < kTilesM; ++i) {
+                const uint4 lo = code[i][0], hi = code[i][1];
+                uint32_t u[4], v[4];
+                widen<kBf16>(j == 0 ? lo.x : j == 1 ? lo.y : j == 2 ? lo.z : lo.w, u);
+                widen<kBf16>(j == 0 ? hi.x : j == 1 ? hi.y : j == 2 ? hi.z : hi.w, v);
+#pragma unroll
+                for (int n = 0; n < kTilesN; ++n) {
+                    if (!kWhole || j == 0)
+                        mma_first<kBf16>(sum[i][n], u[0], v[0], u[1], v[1], x[n][0], x[n][1]);
+                    else
+                        mma<kBf16>(sum[i][n], u[0], v[0], u[1], v[1], x[n][0], x[n][1]);
+                    mma<kBf16>(sum[i][n], u[2], v[2], u[3], v[3], x[n][2], x[n][3]);
+                }
+                if (!kWhole || j == 3) {
+                    float s0 = to_float<kBf16>(now.v[i][0]), s1 = to_float<kBf16>(now.v[i][1]);
+                    if constexpr (!kWhole) {     // lane j of the four has the scales of these 32 terms
+                        s0 = __shfl_sync(0xffffffffu, s0, (lane & ~3) | j);
+                        s1 = __shfl_sync(0xffffffffu, s1, (lane & ~3) | j);
+                    }
+#pragma unroll
+                    for (int n = 0; n < kTilesN; ++n) {
+                        acc[i][n][0] = fmaf(s0, sum[i][n][0], acc[i][n][0]);
+                        acc[i][n][1] = fmaf(s0, sum[i][n][1], acc[i][n][1]);
+                        acc[i][n][2] = fmaf(s1, sum[i][n][2], acc[i][n][2]);
+                        acc[i][n][3] = fmaf(s1, sum[i][n][3], acc[i][n][3]);
+                    }
+                }
+            }
+        }
+    }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+    constexpr int kLd = Cfg::kRows + 4;
+    float *mine = wide_smem + part * Cfg::kSumFloats + row0;
+#pragma unroll
+    for (int i = 0; i < kTilesM; ++i)
+#pragma unroll
+        for (int n = 0; n < kTilesN; ++n)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) mine[(8 * n + 2 * t + (r & 1)) * kLd + 16 * i + 8 * (r >> 1) + g] = acc[i][n][r];
+    __syncthreads();
+    for (int32_t i = threadIdx.x; i < Cfg::kRows * Cfg::kTokens; i += kThreads) {
+        const int32_t n = i / Cfg::kRows, m = i - n * Cfg::kRows;
+        if (n0 + n >= p.N || m0 + m >= p.M) continue;
+        float all = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWideSums; ++w) all += wide_smem[w * Cfg::kSumFloats + n * kLd + m];
+        p.c[(n0 + n) * p.ldc + m0 + m] = from_float<kBf16>(all);
+    }
+}
+
 // ------------------------------------------------------------------ quantiser
 //     scale[r, g] = amax times the float next to 1 / 7, in FP32, rounded to 16 bits
 //     q[r, c]     = round(x / scale) of the exact quotient, ties to even, within -8 .. 7

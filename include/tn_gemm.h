@@ -499,7 +499,8 @@ gemm_status_t gemm_tn_cross_entropy_grad(int type, int64_t M, int64_t N, int64_t
  * a leading dimension below its row's length, or NULL or misaligned pointers with work
  * to do (codes need no alignment; rows on 16-byte boundaries are fastest);
  * GEMM_ERR_UNSUPPORTED off sm_103 or for sizes beyond 2^31 - 256 (the quantiser: 2^40
- * elements, 16776960 columns); GEMM_ERR_CUDA on a failed launch.
+ * elements, 16776960 columns of FP32,
+ * twice that of 16 bits); GEMM_ERR_CUDA on a failed launch.
  */
 gemm_status_t gemm_w4_tn(int type, int64_t M, int64_t N, int64_t K,
                          const void *A, int64_t lda, const void *scale_a, int64_t ld_scale, int64_t group,
