@@ -29,7 +29,7 @@ def nvcc() -> str:
 
 
 def build_cmd(verbose_ptxas: bool = False) -> list[str]:
-    cmd = [nvcc(), "-std=c++17", "-O3", *ARCH, "-lineinfo", "--split-compile=0", "-Xcompiler", "-fPIC", "-shared",
+    cmd = [nvcc(), "-std=c++17", "-O3", *ARCH, "-lineinfo", "-Xcompiler", "-fPIC", "-shared",
            "-diag-suppress", "1160", "-I", INCLUDE, "-o", LIB, *SOURCES]
     if verbose_ptxas:
         cmd.insert(1, "-Xptxas=-v")
