@@ -74,6 +74,7 @@ __host__ __device__ constexpr int grouped_reads(int op)
            : op == kGrGradBAdd ? kGrGradB : op == kGrGradAOne ? kGrGradA : op;
 }
 
+constexpr int kI8RowsL = 128, kI8Rows = 64;  // the 8-bit kernel's tile (i8_kernel.cuh)
 constexpr int kGrEpiWarps = 8;               // epilogue warps: two per quarter of the TMEM lanes
 constexpr int kGrThreads = 64 + 32 * kGrEpiWarps;
 
@@ -1103,9 +1104,7 @@ __global__ void __launch_bounds__(GroupedWarps<kOp>::kThreads, 1) tn_grouped_ker
                     }
                     if (turn >= steps) hand_back();
                 }
-                if (!ok) break;
-                continue;
-            }
+            } else {
 #pragma unroll 1
             for (int half = 0; half < Cfg::kHalves; ++half) {
                 const int32_t first = half * Cfg::kHalfRows;       // the half's first row within the tile
@@ -1139,6 +1138,7 @@ __global__ void __launch_bounds__(GroupedWarps<kOp>::kThreads, 1) tn_grouped_ker
                 else
                     store.half<false, false>(t_row, turn, steps, dst, rows, nullptr, hand_back);
                 ++sub;
+            }
             }
         }
     }
@@ -1207,7 +1207,7 @@ struct GroupedMapsParams {
     int32_t E, T;
 };
 
-__global__ void __launch_bounds__(32) grouped_maps_kernel(const __grid_constant__ GroupedMapsParams p)
+[[maybe_unused]] static __global__ void __launch_bounds__(32) grouped_maps_kernel(const __grid_constant__ GroupedMapsParams p)
 {
     __shared__ __align__(128) CUtensorMap map;
     ptx::griddep_wait();

@@ -36,7 +36,6 @@ constexpr int kI8TeamWarps = kI8WidenWarps / 2;
 constexpr int kI8Threads = 32 * (2 + kI8EpiWarps + kI8WidenWarps);
 constexpr int kI8Block = 128;                                // terms per 8-bit stage: 128 bytes
 
-constexpr int kI8RowsL = 128, kI8Rows = 64;
 constexpr int kI8Stage8Bytes = (kI8RowsL + kI8Rows) * 128;   // 8-bit stage: L, then R
 constexpr int kI8Stages8 = 6;
 constexpr int kI8HalfBytes = kI8Rows * 128;                  // 64 terms of R as f16

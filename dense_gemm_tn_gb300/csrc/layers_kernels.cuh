@@ -1,0 +1,232 @@
+// The small kernels around the gated projections' and the loss's products: the joins
+// of a token's statistics and of a sum's parts, the loss gradient's factors, and the
+// gated projections' elementwise backward pass.  All are bound by what they read and
+// write.
+#pragma once
+
+#include "grouped_sinks.cuh"
+
+namespace tn {
+
+// ------------------------------------------------------------------ loss: joins
+// The pieces' pairs of each token, in the order of the classes within a slice and of
+// the slices (so results repeat): `lanes` tokens a CTA (a power of two), 512 / lanes
+// slices.  Reads 8 bytes per token and 32 classes.
+constexpr int kJoinThreads = 512;
+
+struct JoinParams {
+    const float2 *stats;
+    const float *z_target;
+    const int64_t *targets;
+    float *loss, *lse;
+    int64_t N, classes;
+    int32_t pieces, lanes;
+};
+
+__global__ void __launch_bounds__(kJoinThreads) cross_entropy_join_kernel(const JoinParams p)
+{
+    __shared__ float2 part[kJoinThreads];
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    const int32_t lane = threadIdx.x & (p.lanes - 1), slice = threadIdx.x / p.lanes, slices = kJoinThreads / p.lanes;
+    const int64_t n = static_cast<int64_t>(blockIdx.x) * p.lanes + lane;
+    const float none = __int_as_float(0xff800000);
+    float m = none, s = 0.0f;
+    if (n < p.N) {
+        const int32_t per = (p.pieces + slices - 1) / slices;
+        const int32_t q0 = slice * per, q1 = min(q0 + per, p.pieces);
+#pragma unroll 8
+        for (int32_t q = q0; q < q1; ++q) {
+            const float2 x = p.stats[static_cast<int64_t>(q) * p.N + n];
+            Sink<5>::merge(m, s, x.x, x.y);
+        }
+    }
+    part[threadIdx.x] = make_float2(m, s);
+    for (int32_t half = slices / 2; half >= 1; half /= 2) {
+        __syncthreads();
+        if (slice < half) {
+            const float2 x = part[threadIdx.x + half * p.lanes];
+            Sink<5>::merge(m, s, x.x, x.y);
+            part[threadIdx.x] = make_float2(m, s);
+        }
+    }
+    if (slice == 0 && n < p.N) {
+        const float lse = m + logf(s);
+        p.lse[n] = lse;
+        const int64_t t = p.targets[n];
+        p.loss[n] = t < 0 ? 0.0f : t < p.classes ? lse - p.z_target[n] : __int_as_float(0x7fffffff);
+    }
+}
+
+// The loss gradient's factor of each token: the loss's own gradient, 0 where the
+// target is negative, NaN where it is no class; for fp16 times a power of two that
+// takes the largest into [2^13, 2^14), which `scale` undoes.  One CTA.
+constexpr int kRowsThreads = 1024;
+
+struct LossRowsParams {
+    const int64_t *targets;
+    const float *lse, *dloss;
+    float2 *rows;
+    float *scale;
+    int64_t N, classes;
+    bool half;
+};
+
+__global__ void __launch_bounds__(kRowsThreads) cross_entropy_rows_kernel(const LossRowsParams p)
+{
+    __shared__ float tops[kRowsThreads / 32];
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    auto factor = [&p](int64_t n) {
+        const int64_t t = p.targets[n];
+        return t < 0 ? 0.0f : t < p.classes ? p.dloss[n] : __int_as_float(0x7fffffff);
+    };
+    float up = 1.0f;
+    if (p.half) {
+        float top = 0.0f;
+        for (int64_t n = threadIdx.x; n < p.N; n += kRowsThreads) top = fmaxf(top, fabsf(factor(n)));
+        for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = top;
+        __syncthreads();
+        for (int i = 0; i < kRowsThreads / 32; ++i) top = fmaxf(top, tops[i]);
+        // (0, an infinity or a NaN: as they are; the power and its inverse stay normal numbers)
+        if (top > 0.0f && top < __int_as_float(0x7f800000)) {
+            int e = 13 - ilogbf(top);
+            e = e > 120 ? 120 : e < -120 ? -120 : e;
+            up = ldexpf(1.0f, e);
+        }
+    }
+    for (int64_t n = threadIdx.x; n < p.N; n += kRowsThreads) p.rows[n] = make_float2(p.lse[n], factor(n) * up);
+    if (threadIdx.x == 0) *p.scale = 1.0f / up;
+}
+
+// ------------------------------------------------------------------ parts of a sum, joined
+// out = scale (sum of the parts, in their order), rounded once.  Reads 4 bytes an
+// element and part, writes 2.
+constexpr int kPartsThreads = 256;
+
+struct PartsParams {
+    const float *sum;                // parts of rows x cols, sum_ld floats a row
+    int64_t sum_ld, sum_stride;
+    uint16_t *out;
+    int64_t ld;
+    const float *scale;              // one float, or NULL
+    int64_t rows;
+    int32_t cols, parts;
+    bool bf16;
+    bool vec;                        // four elements a thread: rows on 16-byte (out: 8-byte) boundaries
+};
+
+__global__ void __launch_bounds__(kPartsThreads) parts_join_kernel(const PartsParams p)
+{
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    const float scale = p.scale ? __ldg(p.scale) : 1.0f;
+    const int32_t per = p.vec ? 4 : 1, units = (p.cols + per - 1) / per;
+    const int32_t c = static_cast<int32_t>(blockIdx.x) * kPartsThreads + static_cast<int32_t>(threadIdx.x);
+    if (c >= units) return;
+    for (int64_t r = blockIdx.y; r < p.rows; r += gridDim.y) {
+        const float *from = p.sum + r * p.sum_ld + c * per;
+        uint16_t *out = p.out + r * p.ld + c * per;
+        float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+        for (int32_t q = 0; q < p.parts; ++q, from += p.sum_stride) {
+            if (p.vec) {
+                const float4 v = __ldcs(reinterpret_cast<const float4 *>(from));
+                x[0] += v.x, x[1] += v.y, x[2] += v.z, x[3] += v.w;
+            } else {
+                x[0] += *from;
+            }
+        }
+        const uint32_t lo = p.bf16 ? ptx::pack_bf16x2(x[0] * scale, x[1] * scale) : ptx::pack_f16x2(x[0] * scale, x[1] * scale);
+        const uint32_t hi = p.bf16 ? ptx::pack_bf16x2(x[2] * scale, x[3] * scale) : ptx::pack_f16x2(x[2] * scale, x[3] * scale);
+        if (p.vec)
+            *reinterpret_cast<uint2 *>(out) = make_uint2(lo, hi);
+        else
+            *out = static_cast<uint16_t>(lo);
+    }
+}
+
+// ------------------------------------------------------------------ gated: backward
+// d_gate = dH u act'(g) and d_up = dH act(g) from the kept products, rounded to the
+// operands' type: 8 bytes of products and 2 of dH read, 4 written an element, nothing
+// else.  kVec: 4 elements a thread (rows on 16- and 8-byte boundaries).
+constexpr int kGatedGradThreads = 256;
+
+struct GatedGradParams {
+    const float *pre;
+    int64_t pre_ld;
+    const uint16_t *dh;
+    int64_t dh_ld;
+    uint16_t *dp;                    // T rows of [gate | up], then zeros to dp_ld
+    int64_t dp_ld;
+    const int32_t *offsets;          // rows before the first and from the last on are left out; or NULL
+    int32_t E, T, M;
+};
+
+template <int kAct, bool kBf16, bool kVec>
+__global__ void __launch_bounds__(kGatedGradThreads) gated_grad_kernel(const GatedGradParams p)
+{
+    constexpr int kN = kVec ? 4 : 1;
+    __shared__ int32_t ends[kGatedGradThreads / 32];
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    int32_t begin = 0, end = p.T;
+    if (p.offsets) {                              // read as the products read them
+        auto clamped = [&](int32_t i) {
+            const int32_t o = p.offsets[i];
+            return o < 0 ? 0 : (o > p.T ? p.T : o);
+        };
+        int32_t top = 0;
+        for (int32_t i = threadIdx.x; i <= p.E; i += kGatedGradThreads) top = max(top, clamped(i));
+        top = __reduce_max_sync(0xffffffffu, top);
+        if ((threadIdx.x & 31) == 0) ends[threadIdx.x >> 5] = top;
+        __syncthreads();
+        end = 0;
+        for (int i = 0; i < kGatedGradThreads / 32; ++i) end = max(end, ends[i]);
+        begin = clamped(0);
+    }
+    auto value = [](uint16_t b) {
+        return kBf16 ? __uint_as_float(static_cast<uint32_t>(b) << 16) : __half2float(__ushort_as_half(b));
+    };
+    auto round2 = [](float a, float b) { return kBf16 ? ptx::pack_bf16x2(a, b) : ptx::pack_f16x2(a, b); };
+    const int32_t units = (p.M + kN - 1) / kN;
+    for (int64_t row = begin + blockIdx.y; row < end; row += gridDim.y) {
+        const float *gate = p.pre + row * p.pre_ld, *up = gate + p.M;
+        const uint16_t *dh = p.dh + row * p.dh_ld;
+        uint16_t *dp = p.dp + row * p.dp_ld;
+        for (int32_t i = blockIdx.x * kGatedGradThreads + threadIdx.x; i < units; i += gridDim.x * kGatedGradThreads) {
+            float g[kN], u[kN], d[kN], dg[kN], du[kN];
+            if constexpr (kVec) {
+                const float4 a = __ldcs(reinterpret_cast<const float4 *>(gate) + i);
+                const float4 b = __ldcs(reinterpret_cast<const float4 *>(up) + i);
+                const uint2 c = __ldcs(reinterpret_cast<const uint2 *>(dh) + i);
+                g[0] = a.x, g[1] = a.y, g[2] = a.z, g[3] = a.w;
+                u[0] = b.x, u[1] = b.y, u[2] = b.z, u[3] = b.w;
+                d[0] = value(c.x), d[1] = value(c.x >> 16), d[2] = value(c.y), d[3] = value(c.y >> 16);
+            } else {
+                g[0] = gate[i];
+                u[0] = up[i];
+                d[0] = value(dh[i]);
+            }
+#pragma unroll
+            for (int q = 0; q < kN; ++q) {
+                const float y = act_factor<kAct>(g[q]);
+                dg[q] = d[q] * u[q] * act_slope<kAct>(g[q], y);
+                du[q] = d[q] * (g[q] * y);
+            }
+            if constexpr (kVec) {
+                reinterpret_cast<uint2 *>(dp)[i] = make_uint2(round2(dg[0], dg[1]), round2(dg[2], dg[3]));
+                reinterpret_cast<uint2 *>(dp + p.M)[i] = make_uint2(round2(du[0], du[1]), round2(du[2], du[3]));
+            } else {
+                const uint32_t x = round2(dg[0], du[0]);
+                dp[i] = static_cast<uint16_t>(x);
+                dp[p.M + i] = static_cast<uint16_t>(x >> 16);
+            }
+        }
+        if (blockIdx.x == 0)                      // the products read whole 16-byte units of a row
+            for (int64_t c = 2 * static_cast<int64_t>(p.M) + threadIdx.x; c < p.dp_ld; c += kGatedGradThreads) dp[c] = 0;
+    }
+}
+
+}  // namespace tn

@@ -1,5 +1,5 @@
 // Host side of the gated projections and of the vocabulary's loss (included by
-// tn_gemm.cu, inside its anonymous namespace).  Like the grouped products these
+// layers.cu, inside its anonymous namespace).  Like the grouped products these
 // calls keep nothing in the library: all their buffers are the caller's workspace.
 
 // Sections of a workspace, each from a 256-byte boundary on.
@@ -25,8 +25,6 @@ gemm_status_t check_workspace(const char *name, const void *workspace, int64_t b
         return fail(GEMM_ERR_INVALID_ARG, "%s: the workspace is not 256-byte aligned", name);
     return GEMM_OK;
 }
-
-bool aligned_to(const void *p, uintptr_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 
 tn::GroupedParams sink_params(const GroupedCall &c, int64_t l_extent, int64_t red, void *out, int64_t ldo)
 {
@@ -68,25 +66,6 @@ gemm_status_t place_operands(const char *name, DeviceState &dev, const GroupedPl
     }
     if (!plan.x.copy && !plan.y.copy) return GEMM_OK;
     return launch_widen<uint16_t>(name, dev, plan, const_cast<void *>(o.x), const_cast<void *>(o.y), offsets, stream);
-}
-
-template <typename... Args>
-gemm_status_t launch_plain(const char *name, void (*kernel)(Args...), dim3 grid, int threads, size_t smem,
-                           cudaStream_t stream, Args... args)
-{
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads, 1, 1);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
-    if (e != cudaSuccess) return fail(GEMM_ERR_CUDA, "%s: launch: %s", name, cudaGetErrorString(e));
-    return GEMM_OK;
 }
 
 // ------------------------------------------------------------------ token gradients in parts
@@ -364,7 +343,7 @@ gemm_status_t run_gated_grad(int type, int act, int64_t E, int64_t M, int64_t K,
             st = launch_token_grad(c, *dev, plan.cut, o.x, o.ldx, o.in_x, dP, plan.ldd, 2 * M, dB, lddb, nullptr, sum, 0, 1);
         } else {
             tn::GroupedParams prm = sink_params(c, K, 2 * M, dB, lddb);
-            st = launch_grouped_op<tn::kGrGradB>(c, *dev, prm, o.x, dP, o.ldx, o.stride_x, plan.ldd, o.in_x, plan.ldd);
+            st = launch_grad_b(c, *dev, prm, o.x, dP, o.ldx, o.stride_x, plan.ldd, o.in_x, plan.ldd);
         }
         t_rec.copied = copied;
         if (st != GEMM_OK) return st;
@@ -376,7 +355,7 @@ gemm_status_t run_gated_grad(int type, int act, int64_t E, int64_t M, int64_t K,
         prm.r_extent = static_cast<int32_t>(2 * M);
         if (offsets) {
             prm.group_maps = idle ? nullptr : ws.take<CUtensorMap>(size_t(E) * 2);
-            st = launch_grouped_op<tn::kGrGradA>(c, *dev, prm, dP, o.y, plan.ldd, 0, o.ldy, plan.ldd, o.in_y);
+            st = launch_grad_a(c, *dev, prm, dP, o.y, plan.ldd, 0, o.ldy, plan.ldd, o.in_y);
         } else {
             st = launch_grouped_op<tn::kGrGradAOne>(c, *dev, prm, dP, o.y, plan.ldd, 0, o.ldy, plan.ldd, o.in_y);
         }

@@ -19,6 +19,7 @@
 #include <vector>
 
 #include "tn_gemm.h"
+#include "host_common.cuh"
 #include "tn_gemm_kernel.cuh"
 #include "skinny_kernel.cuh"
 #include "aux_kernels.cuh"
@@ -27,12 +28,9 @@
 #include "grouped_kernel.cuh"
 #include "i8_kernel.cuh"
 #include "quant_i8_kernel.cuh"
-#include "w4_kernel.cuh"
-#include "gated_few_kernel.cuh"
 
 namespace {
 
-constexpr int64_t kMaxDim = (int64_t(1) << 31) - 256;   // TMA coordinates are signed 32-bit
 constexpr int kMaxDevices = 64;
 constexpr int kGroupM = 8;                               // tile rows per raster group
 // The lean configuration (two CTAs per SM) for launches of m-part units
@@ -62,54 +60,6 @@ constexpr bool kAltKDefault = true;
 
 thread_local char t_last_error[512] = "";
 
-gemm_status_t fail(gemm_status_t s, const char *fmt, ...)
-{
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(t_last_error, sizeof(t_last_error), fmt, ap);
-    va_end(ap);
-    return s;
-}
-
-struct DeviceState {
-    bool ready = false;
-    int sms = 0, major = 0, minor = 0;
-    // per kernel, indexed [kind: f16, e4m3][1: one CTA, 2: CTA pairs, 3: CTA pairs with 256 x 512 tiles,
-    // 4 / 5: one CTA / CTA pairs in k-range clusters]
-    bool smem_attr[2][10] = {};
-    int max_clusters[2][10] = {};     // co-resident clusters of the kernel's own size (0 = not queried yet)
-    // co-resident clusters of S single CTAs or S CTA pairs (kClusterReduce), by kind, CTAs per tile and S
-    // (0 = not queried, -1 = none)
-    int cluster_slots[2][3][5] = {};
-    // Split-K partial sums of the last wave, one buffer per stream (calls on
-    // one stream are ordered, so they may share it): [tickets | partials].
-    struct Split {
-        void *ptr = nullptr;
-        size_t bytes = 0, ticket_bytes = 0;
-        bool dirty = false;      // a launch may have stopped part-way (timeout): clear the tickets first
-    };
-    std::unordered_map<cudaStream_t, Split> split;
-    // Per-CTA maxima of the quantiser, one array per stream.
-    std::unordered_map<cudaStream_t, Split> quant;
-    // Row copies of operands the TMA cannot address in place, one workspace
-    // per stream, so calls on different streams may copy at the same time.
-    std::unordered_map<cudaStream_t, Split> repack;
-    // Softmax statistics: [tickets per tile row | parts], one buffer per stream.
-    std::unordered_map<cudaStream_t, Split> stats;
-    int quant_blocks[3] = {};         // co-resident quantiser CTAs per SM, by input type (0 = not queried)
-    bool skinny_attr[2] = {};         // tn_skinny_kernel's shared-memory attribute set, by kind
-    int grouped_slots[tn::kGrOps][3] = {};   // co-resident tn_grouped_kernel CTAs or pairs, by operation and variant (0 = not queried)
-    int split_slots[tn::kGrOps][3] = {};     // co-resident clusters of 2, 4 and 8 single CTAs, by operation (8-bit: 2)
-    bool few_attr[2][2] = {};         // gated_few_kernel's shared-memory attribute set, by type and token tiles
-    bool i8_attr = false;             // tn_i8_kernel's shared-memory attribute set
-    int i8_pair_slots[2] = {};        // co-resident pairs of tn_i8_pair_kernel, by its kRuns (0 = not queried)
-    // One lock per stream, held by a call from its first buffer lookup through
-    // its last launch: a call is several launches (row copy, GEMM, reduce),
-    // and two host threads' calls on one stream must not interleave them.
-    std::unordered_map<cudaStream_t, std::unique_ptr<std::mutex>> stream_locks;
-};
-
-std::mutex g_mutex;
 // Held shared by every call from its first workspace lookup through its last
 // launch, and exclusively by gemm_release_workspace: the buffers a call looked
 // up stay allocated until its kernels are enqueued.
@@ -118,8 +68,6 @@ std::shared_mutex g_workspace_lock;
 // The calling call's lock of `stream` on device state d (see stream_locks).
 std::unique_lock<std::mutex> lock_stream(DeviceState &d, cudaStream_t stream);
 DeviceState g_devices[kMaxDevices];
-std::atomic<uint64_t> g_wait_limit_ns{2000000000ull};
-std::atomic<int> g_inject_stall{0};
 std::atomic<int> g_force_cta_group{0};
 std::atomic<int> g_force_wide{0};       // 0: the cost estimate decides; 1: always; -1: never
 std::atomic<int> g_raster_group{0};     // tile rows per raster group; 0: kGroupM
@@ -128,19 +76,6 @@ std::atomic<unsigned long long *> g_clock_probe{nullptr};   // gemm_debug_set_cl
 std::atomic<int> g_long_k{0};           // small grids with a long K: 0 the library's choice; 1 split-reduce; 2 cluster
 std::atomic<int> g_lean{0};             // m-part launches: 0 the library's choice; 1 never lean; 2 lean where units allow
 std::atomic<int> g_skinny{0};           // N <= 64: 0 the library's choice; 1 never the skinny kernel; 2 always
-// The last launch on this host thread, for gemm_debug_last_launch: the
-// numbers are kept and formatted only when asked for (formatting every call
-// cost host time on the path of back-to-back small GEMMs).
-struct LaunchRecord {
-    const char *name = nullptr;     // nullptr: nothing launched yet
-    bool quant = false;
-    int G = 0, wide = 0, grid = 0, clusters = 0, slots = 0;
-    int tiles = 0, units = 0, tail_start = 0, tail_mode = 0, split_parts = 0, vec = 0, cluster = 0, lean = 0;
-    int skinny = 0;
-    int grouped = 0, copied = 0;    // a product grouped by expert (tiles: an upper bound); operands copied (1: first, 2: second)
-    long long qgrid = 0, qunits = 0;
-};
-thread_local LaunchRecord t_rec;
 thread_local char t_last_launch[256] = "";
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
@@ -162,42 +97,6 @@ EncodeTiledFn encode_fn()
     });
     return fn;
 }
-
-// Current device's state, initialised on first use (caller holds no lock).
-// The device whose primary context this host thread has made current.
-thread_local int t_context_dev = -1;
-
-gemm_status_t device_state(DeviceState **out, int *dev_out)
-{
-    int dev = -1;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return fail(GEMM_ERR_CUDA, "cudaGetDevice: %s", cudaGetErrorString(e));
-    if (dev < 0 || dev >= kMaxDevices) return fail(GEMM_ERR_UNSUPPORTED, "device ordinal %d out of range", dev);
-    if (t_context_dev != dev) {
-        // A host thread that has made no runtime call yet has no current
-        // context, and the driver calls made here (tensor-map encoding) need
-        // one: make the device's primary context current, once per thread.
-        if ((e = cudaSetDevice(dev)) != cudaSuccess)
-            return fail(GEMM_ERR_CUDA, "cudaSetDevice(%d): %s", dev, cudaGetErrorString(e));
-        t_context_dev = dev;
-    }
-    std::lock_guard<std::mutex> lock(g_mutex);
-    DeviceState &d = g_devices[dev];
-    if (!d.ready) {
-        if ((e = cudaDeviceGetAttribute(&d.major, cudaDevAttrComputeCapabilityMajor, dev)) != cudaSuccess ||
-            (e = cudaDeviceGetAttribute(&d.minor, cudaDevAttrComputeCapabilityMinor, dev)) != cudaSuccess ||
-            (e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
-            return fail(GEMM_ERR_CUDA, "cudaDeviceGetAttribute: %s", cudaGetErrorString(e));
-        d.ready = true;
-    }
-    if (d.major != 10 || d.minor != 3)
-        return fail(GEMM_ERR_UNSUPPORTED, "device %d is sm_%d%d; this library is built for sm_103a only", dev,
-                    d.major, d.minor);
-    *out = &d;
-    if (dev_out) *dev_out = dev;
-    return GEMM_OK;
-}
-
 
 // The key of a stream's buffers.  cudaStreamPerThread is one handle value
 // that names a different stream on every host thread, so it is keyed per
@@ -328,12 +227,63 @@ struct MapCache {
 };
 MapCache g_maps;
 
-// depth > 0: a 3-D map of `depth` such matrices, depth_bytes apart, with boxes
-// of one matrix; with mid_bytes > 0 a 4-D map of `depth` pairs of them, a pair's
-// matrices mid_bytes apart, with boxes of one pair.
+}  // namespace
+
+namespace tn_host {
+
+gemm_status_t fail(gemm_status_t s, const char *fmt, ...)
+{
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(t_last_error, sizeof(t_last_error), fmt, ap);
+    va_end(ap);
+    return s;
+}
+
+void clear_error() { t_last_error[0] = '\0'; }
+
+std::mutex g_mutex;
+std::atomic<uint64_t> g_wait_limit_ns{2000000000ull};
+std::atomic<int> g_inject_stall{0};
+thread_local LaunchRecord t_rec;
+
+// The device whose primary context this host thread has made current.
+thread_local int t_context_dev = -1;
+
+gemm_status_t device_state(DeviceState **out, int *dev_out)
+{
+    int dev = -1;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return fail(GEMM_ERR_CUDA, "cudaGetDevice: %s", cudaGetErrorString(e));
+    if (dev < 0 || dev >= kMaxDevices) return fail(GEMM_ERR_UNSUPPORTED, "device ordinal %d out of range", dev);
+    if (t_context_dev != dev) {
+        // A host thread that has made no runtime call yet has no current
+        // context, and the driver calls made here (tensor-map encoding) need
+        // one: make the device's primary context current, once per thread.
+        if ((e = cudaSetDevice(dev)) != cudaSuccess)
+            return fail(GEMM_ERR_CUDA, "cudaSetDevice(%d): %s", dev, cudaGetErrorString(e));
+        t_context_dev = dev;
+    }
+    std::lock_guard<std::mutex> lock(g_mutex);
+    DeviceState &d = g_devices[dev];
+    if (!d.ready) {
+        if ((e = cudaDeviceGetAttribute(&d.major, cudaDevAttrComputeCapabilityMajor, dev)) != cudaSuccess ||
+            (e = cudaDeviceGetAttribute(&d.minor, cudaDevAttrComputeCapabilityMinor, dev)) != cudaSuccess ||
+            (e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
+            return fail(GEMM_ERR_CUDA, "cudaDeviceGetAttribute: %s", cudaGetErrorString(e));
+        d.ready = true;
+    }
+    if (d.major != 10 || d.minor != 3)
+        return fail(GEMM_ERR_UNSUPPORTED, "device %d is sm_%d%d; this library is built for sm_103a only", dev,
+                    d.major, d.minor);
+    *out = &d;
+    if (dev_out) *dev_out = dev;
+    return GEMM_OK;
+}
+
 gemm_status_t encode_map(CUtensorMap *map, CUtensorMapDataType type, const void *base, uint64_t inner,
                          uint64_t outer, uint64_t row_bytes, uint64_t depth, uint64_t depth_bytes,
-                         uint32_t box_inner, uint32_t box_outer, const char *what, uint64_t mid_bytes = 0)
+                         uint32_t box_inner, uint32_t box_outer, const char *what, uint64_t mid_bytes)
 {
     const MapKey key{reinterpret_cast<uintptr_t>(base), inner, outer, row_bytes, box_inner, box_outer,
                      static_cast<int>(type), depth, depth_bytes, mid_bytes};
@@ -388,6 +338,10 @@ uint32_t stall_flags(int mode)
     default: return 0u;
     }
 }
+
+}  // namespace tn_host
+
+namespace {
 
 // Launches repack_rows_kernel for one or two operands (a job with 0 rows is
 // skipped); ld_dst, common to both, is a multiple of 16 bytes.
@@ -1144,10 +1098,25 @@ gemm_status_t run_quant(const void *x, int x_type, int64_t rows, int64_t cols, i
 }
 
 #include "grouped_host.cuh"
-#include "sinks_host.cuh"
-#include "w4_host.cuh"
+#include "grouped_calls.cuh"
 
 }  // namespace
+
+namespace tn_host {
+
+gemm_status_t launch_grad_b(const GroupedCall &c, DeviceState &dev, tn::GroupedParams &prm, const void *x, const void *y,
+                            int64_t ldx, int64_t stride_x, int64_t ldy, int64_t inner_x, int64_t inner_y)
+{
+    return launch_grouped_op<tn::kGrGradB>(c, dev, prm, x, y, ldx, stride_x, ldy, inner_x, inner_y);
+}
+
+gemm_status_t launch_grad_a(const GroupedCall &c, DeviceState &dev, tn::GroupedParams &prm, const void *x, const void *y,
+                            int64_t ldx, int64_t stride_x, int64_t ldy, int64_t inner_x, int64_t inner_y)
+{
+    return launch_grouped_op<tn::kGrGradA>(c, dev, prm, x, y, ldx, stride_x, ldy, inner_x, inner_y);
+}
+
+}  // namespace tn_host
 
 extern "C" {
 
@@ -1270,71 +1239,6 @@ gemm_status_t gemm_quantize_i8_rows(const void *x, int x_type, int64_t rows, int
     return run_quant_rows(x, x_type, rows, cols, ldx, q, ldq, scale, static_cast<cudaStream_t>(stream));
 }
 
-int64_t gemm_gated_workspace(int grad, int dense, int64_t E, int64_t M, int64_t K, int64_t T, const void *A, int64_t lda,
-                             int64_t stride_a, const void *B, int64_t ldb)
-{
-    return gated_workspace(grad, dense, E, M, K, T, A, lda, stride_a, B, ldb);
-}
-
-gemm_status_t gemm_tn_gated(int type, int act, int64_t E, int64_t M, int64_t K, int64_t T, const void *A, int64_t lda,
-                            int64_t stride_a, const void *B, int64_t ldb, const int32_t *offsets, void *H, int64_t ldh,
-                            float *P, int64_t ldp, void *workspace, int64_t workspace_bytes, void *stream)
-{
-    t_last_error[0] = '\0';
-    return run_gated(type, act, E, M, K, T, A, lda, stride_a, B, ldb, offsets, H, ldh, P, ldp, workspace, workspace_bytes,
-                     static_cast<cudaStream_t>(stream));
-}
-
-gemm_status_t gemm_tn_gated_grad(int type, int act, int64_t E, int64_t M, int64_t K, int64_t T, const void *A, int64_t lda,
-                                 int64_t stride_a, const void *B, int64_t ldb, const int32_t *offsets, const float *P,
-                                 int64_t ldp, const void *dH, int64_t lddh, void *dA, int64_t ldda, int64_t stride_da,
-                                 void *dB, int64_t lddb, void *workspace, int64_t workspace_bytes, void *stream)
-{
-    t_last_error[0] = '\0';
-    return run_gated_grad(type, act, E, M, K, T, A, lda, stride_a, B, ldb, offsets, P, ldp, dH, lddh, dA, ldda, stride_da, dB,
-                          lddb, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
-}
-
-int64_t gemm_cross_entropy_workspace(int grad, int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, const void *B,
-                                     int64_t ldb)
-{
-    return loss_workspace(grad, M, N, K, A, lda, B, ldb);
-}
-
-gemm_status_t gemm_tn_cross_entropy(int type, int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, const void *B,
-                                    int64_t ldb, const int64_t *targets, float *loss, float *lse, void *workspace,
-                                    int64_t workspace_bytes, void *stream)
-{
-    t_last_error[0] = '\0';
-    return run_loss(type, M, N, K, A, lda, B, ldb, targets, loss, lse, workspace, workspace_bytes,
-                    static_cast<cudaStream_t>(stream));
-}
-
-gemm_status_t gemm_tn_cross_entropy_grad(int type, int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, const void *B,
-                                         int64_t ldb, const int64_t *targets, const float *lse, const float *dloss, void *dA,
-                                         int64_t ldda, void *dB, int64_t lddb, void *workspace, int64_t workspace_bytes,
-                                         void *stream)
-{
-    t_last_error[0] = '\0';
-    return run_loss_grad(type, M, N, K, A, lda, B, ldb, targets, lse, dloss, dA, ldda, dB, lddb, workspace, workspace_bytes,
-                         static_cast<cudaStream_t>(stream));
-}
-
-gemm_status_t gemm_w4_tn(int type, int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, const void *scale_a,
-                         int64_t ld_scale, int64_t group, const void *B, int64_t ldb, void *C, int64_t ldc, void *stream)
-{
-    t_last_error[0] = '\0';
-    return run_w4(type, M, N, K, A, lda, scale_a, ld_scale, group, B, ldb, C, ldc, static_cast<cudaStream_t>(stream));
-}
-
-gemm_status_t gemm_quantize_w4_rows(const void *x, int x_type, int64_t rows, int64_t cols, int64_t ldx, int64_t group, void *q,
-                                    int64_t ldq, int scale_type, void *scale, int64_t ld_scale, void *stream)
-{
-    t_last_error[0] = '\0';
-    return run_quant_w4(x, x_type, rows, cols, ldx, group, q, ldq, scale_type, scale, ld_scale,
-                        static_cast<cudaStream_t>(stream));
-}
-
 const char *gemm_status_string(gemm_status_t s)
 {
     switch (s) {
@@ -1356,10 +1260,13 @@ gemm_status_t gemm_poll_device_status(void *stream)
     if (e != cudaSuccess) return fail(GEMM_ERR_CUDA, "cudaStreamSynchronize: %s", cudaGetErrorString(e));
     int v = 0;
     e = cudaMemcpyFromSymbol(&v, tn::g_tn_status, sizeof(int));
+    int layers = 0;
+    if (e == cudaSuccess) e = take_layers_status(&layers);
     if (e != cudaSuccess) return fail(GEMM_ERR_CUDA, "reading the status word: %s", cudaGetErrorString(e));
-    if (v != 0) {
+    if (v != 0 || layers != 0) {
         const int zero = 0;
-        cudaMemcpyToSymbol(tn::g_tn_status, &zero, sizeof(int));
+        if (v != 0) cudaMemcpyToSymbol(tn::g_tn_status, &zero, sizeof(int));
+        else v = layers;
         // A kernel that gave up may have left ticket counts part-way: the next
         // call on each stream clears them before use.
         int dev = -1;

@@ -1,5 +1,5 @@
 // Host side of the products with 4-bit weights and of their quantiser (included by
-// tn_gemm.cu, inside its anonymous namespace).
+// w4.cu, inside its anonymous namespace).
 
 bool w4_group_ok(int64_t group) { return group == 32 || group == 64 || group == 128 || group == 256; }
 

@@ -68,7 +68,7 @@ __device__ __forceinline__ uint4 load_words(const uint8_t *p)
 
 // 16 bytes from p on, of which the first `valid` count, the rest zeros; nothing else
 // is read.
-__device__ __noinline__ uint4 load_part(const uint8_t *p, int32_t valid)
+[[maybe_unused]] static __device__ __noinline__ uint4 load_part(const uint8_t *p, int32_t valid)
 {
     uint32_t r[4];
 #pragma unroll
