@@ -25,7 +25,7 @@ struct SinkParams {
     const int64_t *targets;          // loss: a class per token; negative: ignored
     float2 *stats;                   // loss: [ceil(classes / 32)][T] maximum, sum of exp(z - maximum)
     float *z_target;                 // loss: [T] the target's logit
-    const float2 *rows;              // loss gradient: [T] (log-sum-exp, factor)
+    const float2 *rows;              // loss gradient: [T] (-log-sum-exp / log 2, factor)
     int32_t first, classes;          // loss gradient: the piece's first class, and how many
     float *sum;                      // parts added up: FP32 sums, one result for each part
     int64_t sum_ld, sum_stride;
@@ -208,14 +208,23 @@ struct Sink<5 /* kGrLossStats */> {
         const SinkParams &k = p.sink;
         const int lane = store.lane;
         const float none = __int_as_float(0xff800000);
+        // (classes past the last are left out)
         const int32_t left = p.l_extent - l0 - (lane >> 2);     // of the lane's classes 0, 8, 16 and 24
-        auto logit = [&](int j, int q) {
-            const float z = __uint_as_float(v[q >> 1][4 * (j >> 1) + 2 * (q & 1) + (j & 1)]);
-            return 8 * q < left ? z : none;
-        };
+        const bool whole = p.l_extent - l0 >= 32;
+        auto logit = [&](int j, int q) { return __uint_as_float(v[q >> 1][4 * (j >> 1) + 2 * (q & 1) + (j & 1)]); };
         float x[8], m[8];
+        if (whole) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) m[j] = fmaxf(fmaxf(logit(j, 0), logit(j, 1)), fmaxf(logit(j, 2), logit(j, 3)));
+            for (int j = 0; j < 8; ++j) m[j] = fmaxf(fmaxf(logit(j, 0), logit(j, 1)), fmaxf(logit(j, 2), logit(j, 3)));
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                m[j] = none;
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (8 * q < left) m[j] = fmaxf(m[j], logit(j, q));
+            }
+        }
         halve(m, lane, [](float a, float b) { return fmaxf(a, b); });
         const float top = m[0];
 #pragma unroll
@@ -232,9 +241,15 @@ struct Sink<5 /* kGrLossStats */> {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             // (a maximum of -inf: of logits that all are)
-            const float from = m[j] == none ? 0.0f : m[j];
-            x[j] = (ex2((logit(j, 0) - from) * kLog2e) + ex2((logit(j, 1) - from) * kLog2e)) +
-                   (ex2((logit(j, 2) - from) * kLog2e) + ex2((logit(j, 3) - from) * kLog2e));
+            const float from = m[j] == none ? 0.0f : -m[j] * kLog2e;
+            float e[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) e[q] = ex2(fmaf(logit(j, q), kLog2e, from));
+            if (!whole)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (8 * q >= left) e[q] = 0.0f;
+            x[j] = (e[0] + e[1]) + (e[2] + e[3]);
         }
         halve(x, lane, [](float a, float b) { return a + b; });
         const int32_t own = 4 * (lane >> 4 & 1) + 2 * (lane >> 3 & 1) + (lane >> 2 & 1);
@@ -259,9 +274,9 @@ struct Sink<5 /* kGrLossStats */> {
 };
 
 // d = (exp(z - lse) - [m = target]) factor, rounded to the operands' type: what the
-// tensor cores multiply in both gradients.  (fp16: the factors are scaled up so that
-// the largest is near 2^13, see cross_entropy_rows_kernel; d then keeps its relative
-// precision down to 2^-27 of it.)  Classes past the piece's end are zeros: the
+// tensor cores multiply in both gradients.  (The factors are shares of the largest, in
+// fp16 times 2^13, see cross_entropy_rows_kernel; d then keeps its relative precision
+// down to 2^-27 of it.)  Classes past the piece's end are zeros: the
 // products over the piece read them.
 template <>
 struct Sink<6 /* kGrLossGrad */> {
@@ -271,38 +286,58 @@ struct Sink<6 /* kGrLossGrad */> {
     {
         const SinkParams &k = p.sink;
         const int lane = store.lane;
-        const int32_t m0 = l0 + (lane >> 2);
-        uint32_t d[2][16];
+        float d[2][16];
         int64_t at = -1;
         if (lane < rows) at = __ldg(k.targets + row + lane) - k.first - l0;
-        const uint32_t hits = __ballot_sync(0xffffffffu, at >= 0 && at < 32);
+        uint32_t hits = __ballot_sync(0xffffffffu, at >= 0 && at < 32);
+        float2 r[8];                              // of the lane's columns: -lse / log 2, factor
+        bool some = false;                        // a token that is ignored among them
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int j = 0; j < 8; ++j) {
+            const int32_t col = 8 * (j >> 1) + 2 * (lane & 3) + (j & 1);
+            r[j] = col < rows ? __ldg(k.rows + row + col) : make_float2(0.0f, 1.0f);
+            some |= r[j].y == 0.0f;
+        }
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const int32_t col = 8 * i + 2 * (lane & 3) + c;
-                float2 r = make_float2(0.0f, 0.0f);
-                if (col < rows) r = __ldg(k.rows + row + col);
-                int32_t hit = -1;
-                if (hits) {                       // (the whole warp: the exchange is every lane's)
-                    hit = __shfl_sync(0xffffffffu, static_cast<int32_t>(at), col);
-                    if (!(hits >> col & 1)) hit = -1;
-                }
+        for (int j = 0; j < 8; ++j)
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int b = 4 * i + 2 * (q & 1) + c;
-                    float x = ex2((__uint_as_float(v[q >> 1][b]) - r.x) * kLog2e);
-                    if (hit == (lane >> 2) + 8 * q) x -= 1.0f;
-                    // (an ignored token's logits may be anything)
-                    x = r.y == 0.0f || m0 + 8 * q >= k.classes ? 0.0f : x * r.y;
-                    d[q >> 1][b] = __float_as_uint(x);
-                }
+            for (int q = 0; q < 4; ++q) {
+                const int b = 4 * (j >> 1) + 2 * (q & 1) + (j & 1);
+                d[q >> 1][b] = ex2(fmaf(__uint_as_float(v[q >> 1][b]), kLog2e, r[j].x));
             }
+        while (hits) {                            // the targets among these classes
+            const int32_t c = __ffs(hits) - 1;
+            hits &= hits - 1;
+            const int32_t q = __shfl_sync(0xffffffffu, static_cast<int32_t>(at), c);
+            const bool own = (lane & 3) == ((c & 7) >> 1) && lane >> 2 == (q & 7);
+            const int32_t want = own ? 16 * (q >> 4) + 4 * (c >> 3) + 2 * (q >> 3 & 1) + (c & 1) : -1;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (i == want) d[i >> 4][i & 15] -= 1.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) d[q >> 1][4 * (j >> 1) + 2 * (q & 1) + (j & 1)] *= r[j].y;
+        const int32_t left = k.classes - l0 - (lane >> 2);
+        if (__any_sync(0xffffffffu, some || left < 25)) {
+            // an ignored token's logits may be anything; and what the classes leave of the last 32
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (r[j].y == 0.0f || 8 * q >= left) d[q >> 1][4 * (j >> 1) + 2 * (q & 1) + (j & 1)] = 0.0f;
+        }
+        uint32_t bits[2][16];
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) bits[q][i] = __float_as_uint(d[q][i]);
         uint16_t *out = p.out + row * p.out_ld + l0;
         if (p.out_fmt != 0)
-            store.template step<true, false>(d, out, rows, nullptr);
+            store.template step<true, false>(bits, out, rows, nullptr);
         else
-            store.template step<false, false>(d, out, rows, nullptr);
+            store.template step<false, false>(bits, out, rows, nullptr);
     }
 };
 

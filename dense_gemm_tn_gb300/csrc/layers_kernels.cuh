@@ -59,8 +59,11 @@ __global__ void __launch_bounds__(kJoinThreads) cross_entropy_join_kernel(const 
 }
 
 // The loss gradient's factor of each token: the loss's own gradient, 0 where the
-// target is negative, NaN where it is no class; for fp16 times a power of two that
-// takes the largest into [2^13, 2^14), which `scale` undoes.  One CTA.
+// target is negative, NaN where it is no class, as a share of the largest (times 2^13 for
+// fp16, whose small numbers end early); `scale` undoes that in the products' FP32 sums.
+// Where all tokens weigh alike, as in a mean, the factor is thus a power of two, and the
+// rounding of d = factor (p - 1) at the targets does not add the same error to all of
+// them (1 / 3900 is 0.2 % off in bf16).  One CTA.
 constexpr int kRowsThreads = 1024;
 
 struct LossRowsParams {
@@ -81,23 +84,18 @@ __global__ void __launch_bounds__(kRowsThreads) cross_entropy_rows_kernel(const 
         const int64_t t = p.targets[n];
         return t < 0 ? 0.0f : t < p.classes ? p.dloss[n] : __int_as_float(0x7fffffff);
     };
-    float up = 1.0f;
-    if (p.half) {
-        float top = 0.0f;
-        for (int64_t n = threadIdx.x; n < p.N; n += kRowsThreads) top = fmaxf(top, fabsf(factor(n)));
-        for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-        if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = top;
-        __syncthreads();
-        for (int i = 0; i < kRowsThreads / 32; ++i) top = fmaxf(top, tops[i]);
-        // (0, an infinity or a NaN: as they are; the power and its inverse stay normal numbers)
-        if (top > 0.0f && top < __int_as_float(0x7f800000)) {
-            int e = 13 - ilogbf(top);
-            e = e > 120 ? 120 : e < -120 ? -120 : e;
-            up = ldexpf(1.0f, e);
-        }
-    }
-    for (int64_t n = threadIdx.x; n < p.N; n += kRowsThreads) p.rows[n] = make_float2(p.lse[n], factor(n) * up);
-    if (threadIdx.x == 0) *p.scale = 1.0f / up;
+    float top = 0.0f;
+    for (int64_t n = threadIdx.x; n < p.N; n += kRowsThreads) top = fmaxf(top, fabsf(factor(n)));
+    for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = top;
+    __syncthreads();
+    for (int i = 0; i < kRowsThreads / 32; ++i) top = fmaxf(top, tops[i]);
+    // (all 0, or an infinity among them: as they are)
+    if (!(top > 0.0f && top < __int_as_float(0x7f800000))) top = 1.0f;
+    const float up = p.half ? 8192.0f : 1.0f;
+    for (int64_t n = threadIdx.x; n < p.N; n += kRowsThreads)
+        p.rows[n] = make_float2(-p.lse[n] * kLog2e, __fdiv_rn(factor(n), top) * up);
+    if (threadIdx.x == 0) *p.scale = top / up;
 }
 
 // ------------------------------------------------------------------ parts of a sum, joined
@@ -150,7 +148,7 @@ __global__ void __launch_bounds__(kPartsThreads) parts_join_kernel(const PartsPa
 // ------------------------------------------------------------------ gated: backward
 // d_gate = dH u act'(g) and d_up = dH act(g) from the kept products, rounded to the
 // operands' type: 8 bytes of products and 2 of dH read, 4 written an element, nothing
-// else.  kVec: 4 elements a thread (rows on 16- and 8-byte boundaries).
+// else.  kVec: 8 elements a thread (rows on 16-byte boundaries).
 constexpr int kGatedGradThreads = 256;
 
 struct GatedGradParams {
@@ -167,7 +165,7 @@ struct GatedGradParams {
 template <int kAct, bool kBf16, bool kVec>
 __global__ void __launch_bounds__(kGatedGradThreads) gated_grad_kernel(const GatedGradParams p)
 {
-    constexpr int kN = kVec ? 4 : 1;
+    constexpr int kN = kVec ? 8 : 1;
     __shared__ int32_t ends[kGatedGradThreads / 32];
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
@@ -198,12 +196,20 @@ __global__ void __launch_bounds__(kGatedGradThreads) gated_grad_kernel(const Gat
         for (int32_t i = blockIdx.x * kGatedGradThreads + threadIdx.x; i < units; i += gridDim.x * kGatedGradThreads) {
             float g[kN], u[kN], d[kN], dg[kN], du[kN];
             if constexpr (kVec) {
-                const float4 a = __ldcs(reinterpret_cast<const float4 *>(gate) + i);
-                const float4 b = __ldcs(reinterpret_cast<const float4 *>(up) + i);
-                const uint2 c = __ldcs(reinterpret_cast<const uint2 *>(dh) + i);
-                g[0] = a.x, g[1] = a.y, g[2] = a.z, g[3] = a.w;
-                u[0] = b.x, u[1] = b.y, u[2] = b.z, u[3] = b.w;
-                d[0] = value(c.x), d[1] = value(c.x >> 16), d[2] = value(c.y), d[3] = value(c.y >> 16);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float4 a = __ldcs(reinterpret_cast<const float4 *>(gate) + 2 * i + h);
+                    const float4 b = __ldcs(reinterpret_cast<const float4 *>(up) + 2 * i + h);
+                    g[4 * h] = a.x, g[4 * h + 1] = a.y, g[4 * h + 2] = a.z, g[4 * h + 3] = a.w;
+                    u[4 * h] = b.x, u[4 * h + 1] = b.y, u[4 * h + 2] = b.z, u[4 * h + 3] = b.w;
+                }
+                const uint4 c = __ldcs(reinterpret_cast<const uint4 *>(dh) + i);
+                const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    d[2 * q] = value(w[q]);
+                    d[2 * q + 1] = value(w[q] >> 16);
+                }
             } else {
                 g[0] = gate[i];
                 u[0] = up[i];
@@ -216,8 +222,10 @@ __global__ void __launch_bounds__(kGatedGradThreads) gated_grad_kernel(const Gat
                 du[q] = d[q] * (g[q] * y);
             }
             if constexpr (kVec) {
-                reinterpret_cast<uint2 *>(dp)[i] = make_uint2(round2(dg[0], dg[1]), round2(dg[2], dg[3]));
-                reinterpret_cast<uint2 *>(dp + p.M)[i] = make_uint2(round2(du[0], du[1]), round2(du[2], du[3]));
+                reinterpret_cast<uint4 *>(dp)[i] =
+                    make_uint4(round2(dg[0], dg[1]), round2(dg[2], dg[3]), round2(dg[4], dg[5]), round2(dg[6], dg[7]));
+                reinterpret_cast<uint4 *>(dp + p.M)[i] =
+                    make_uint4(round2(du[0], du[1]), round2(du[2], du[3]), round2(du[4], du[5]), round2(du[6], du[7]));
             } else {
                 const uint32_t x = round2(dg[0], du[0]);
                 dp[i] = static_cast<uint16_t>(x);

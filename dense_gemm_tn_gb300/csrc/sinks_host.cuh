@@ -267,8 +267,8 @@ template <int kAct>
 gemm_status_t launch_gated_grad(const char *name, DeviceState &dev, const tn::GatedGradParams &p, bool bf16,
                                 cudaStream_t stream)
 {
-    const bool vec = p.M % 4 == 0 && p.pre_ld % 4 == 0 && p.dh_ld % 4 == 0 && aligned_to(p.pre, 16) && aligned_to(p.dh, 8);
-    const int64_t units = (int64_t(p.M) + (vec ? 3 : 0)) / (vec ? 4 : 1);
+    const bool vec = p.M % 8 == 0 && p.pre_ld % 4 == 0 && p.dh_ld % 8 == 0 && aligned_to(p.pre, 16) && aligned_to(p.dh, 16);
+    const int64_t units = vec ? int64_t(p.M) / 8 : p.M;
     const int64_t across = (units + tn::kGatedGradThreads - 1) / tn::kGatedGradThreads;
     // about eight CTAs an SM, whole rows of them
     const int64_t want = int64_t(dev.sms) * 8;

@@ -91,6 +91,22 @@ def test_long_sums_lose_nothing(N, M, dtype):
     assert float((lse.double() - lse_ref).norm() / lse_ref.norm()) < 2.0 ** -19
 
 
+@pytest.mark.parametrize("N", [3900, 3000, 1537])
+def test_a_mean_loss_rounds_no_gradient_alike(N):
+    """dloss = 1 / N for all tokens: not a number of 8 bits, and the targets' d = -1 / N nearly.  Rounded itself it would be
+    off by the same 0.2 % everywhere; the 2-norm of the error stays that of random roundings, at most 2^-9 each
+    (d's and the result's: 1.5 x 2^-9 in the norm, were all at their largest 2^-8.5)."""
+    A, Bt, targets, _ = operands(N, 5000, 64, torch.bfloat16, spread=0.5)
+    dloss = torch.full((N,), 1 / N, device="cuda")
+    loss, lse = tn.tn_cross_entropy(A, Bt, targets)
+    dA, dB = tn.tn_cross_entropy_grad(A, Bt, targets, lse, dloss)
+    rA, rB, _, _ = loss_grad64(A, Bt, targets, dloss, torch.bfloat16, lse)
+    for got, ref in ((dA, rA), (dB, rB)):
+        assert float((got.double() - ref).norm() / ref.norm()) < 2.0 ** -8.5
+        along = float((got.double() * ref).sum() / (ref * ref).sum()) - 1       # the error they share
+        assert abs(along) < 2.0 ** -11
+
+
 def test_targets_that_are_no_class():
     A, Bt, targets, dloss = operands(70, 100, 64, torch.bfloat16)
     targets[3], targets[40] = 100, 1 << 40
