@@ -166,7 +166,9 @@ gemm_status_t run_quant_w4(const void *x, int x_type, int64_t rows, int64_t cols
     p.vec = aligned_to(x, 16) && aligned_to(q, 8) && (rows == 1 || (ldx * esz % 16 == 0 && ldq % 8 == 0));
     const int64_t per = w4::kQuantThreads / 32;
     int64_t grid = (rows + per - 1) / per;
-    const int64_t most = (int64_t(dev->sms) * 64 + segs - 1) / segs;
+    // CTAs that stay, a row ahead in their reads: about four an SM.  Measured on GB300, 8192 x
+    // 8192 bf16: 51.4 us with a CTA for every 8 rows and 512 terms, 43.6 with these.
+    const int64_t most = (int64_t(dev->sms) * 4 + segs - 1) / segs;
     if (grid > most) grid = most;
     t_rec = LaunchRecord{};
     t_rec.name = name;
