@@ -691,8 +691,7 @@ def _plain(torch, *tensors):
 
 def _elsewhere(index):
     """Whether device `index` is not the calling thread's current one (which the C ABI works on)."""
-    import torch
-    return torch.cuda.current_device() != index
+    return _torch._C._cuda_getDevice() != index
 
 
 def tn_grouped(A, Bt, offsets, C=None, stream=None):
@@ -905,18 +904,37 @@ def quantize_i8_rows(x, stream=None):
 
 
 # ---------------------------------------------------------------- gated projections and the vocabulary's loss
-def _gated_weights(A, dtype, offsets):
-    """(E, M, K, lda, stride_a) of gate and up rows: (E, 2 M, K) with offsets, (2 M, K) without."""
+def _gated_operands(A, Bt, offsets, P=None, dHt=None):
+    """(E, M, K, T, lda, stride_a, ldb, ldp, lddh) of gate and up rows A, (E, 2 M, K) with offsets and (2 M, K)
+    without, of tokens Bt (T, K) and, for the gradient, of products P (T, 2 M) and gradients dHt (T, M)."""
+    torch, dtype, sa, sb = _torch, A.dtype, A.shape, Bt.shape
+    if (len(sa) == (2 if offsets is None else 3) and len(sb) == 2 and sa[-1] == sb[1] > 0 and sa[-2] % 2 == 0 < sa[-2]
+            and Bt.dtype is dtype and _plain(torch, A, Bt)):
+        T, K, rows, E = sb[0], sb[1], sa[-2], 1 if offsets is None else sa[0]
+        M = rows // 2
+        if ((offsets is None or (isinstance(offsets, torch.Tensor) and offsets.dtype is torch.int32
+                                 and offsets.shape == (E + 1,) and _plain(torch, offsets)))
+                and (P is None or (P.dtype is torch.float32 and P.shape == (T, rows) and dHt.dtype is dtype
+                                   and dHt.shape == (T, M) and _plain(torch, P, dHt)))):
+            return E, M, K, T, K, (rows * K if E > 1 else 0), K, rows, M
+    stride_a = ldp = lddh = 0
     if offsets is None:
-        lda, stride_a = _rows(A, dtype, "A", cuda=False), 0
+        lda = _rows(A, dtype, "A", cuda=False)
         E, (rows, K) = 1, A.shape
     else:
         lda, stride_a = _experts(A, dtype, "A")
         E, rows, K = A.shape
-        _vector(offsets, _torch.int32, E + 1, "offsets")
+        _vector(offsets, torch.int32, E + 1, "offsets")
     if rows % 2:
         raise ValueError(f"A must have an even number of rows (gate rows, then up rows), not {rows}")
-    return E, rows // 2, K, lda, stride_a
+    ldb, T, M = _tokens(Bt, dtype, K, "Bt"), Bt.shape[0], rows // 2
+    if P is not None:
+        ldp = _rows(P, torch.float32, "P", (T, rows), cuda=False)
+    if dHt is not None:
+        lddh = _rows(dHt, dtype, "dHt", (T, M), cuda=False)
+    others = {"Bt": Bt, "P": P, "dHt": dHt, "offsets": offsets}
+    _same_device(A.device, **{name: t for name, t in others.items() if t is not None})
+    return E, M, K, T, lda, stride_a, ldb, ldp, lddh
 
 
 def _activation(act):
@@ -936,24 +954,11 @@ def tn_gated(A, Bt, offsets=None, act="silu", keep=False, H=None, P=None, stream
     _tensors(torch, A, Bt)
     dtype, device = A.dtype, A.device
     half, kind = _half_type(dtype, "A"), _activation(act)
-    sa, sb = A.shape, Bt.shape
-    if (H is None and offsets is None and Bt.dtype is dtype and len(sa) == 2 == len(sb) and sa[1] == sb[1] > 0
-            and sa[0] % 2 == 0 < sa[0] and _plain(torch, A, Bt)):
-        E, M, K, T = 1, sa[0] // 2, sa[1], sb[0]
-        lda = ldb = K
-        stride_a = 0
-        H, ldh = _empty((T, M), dtype, device, stream), M
-    else:
-        E, M, K, lda, stride_a = _gated_weights(A, dtype, offsets)
-        ldb, T = _tokens(Bt, dtype, K, "Bt"), Bt.shape[0]
-        if offsets is None:
-            _same_device(device, Bt=Bt)
-        else:
-            _same_device(device, Bt=Bt, offsets=offsets)
-        if _elsewhere(device.index):
-            with torch.cuda.device(device):
-                return tn_gated(A, Bt, offsets, act, keep, H, P, stream)
-        H, ldh = _result(H, (T, M), dtype, device, stream, "H")
+    E, M, K, T, lda, stride_a, ldb, _, _ = _gated_operands(A, Bt, offsets)
+    if _elsewhere(device.index):
+        with torch.cuda.device(device):
+            return tn_gated(A, Bt, offsets, act, keep, H, P, stream)
+    H, ldh = _result(H, (T, M), dtype, device, stream, "H")
     ldp = 0
     if keep or P is not None:
         P, ldp = _result(P, (T, 2 * M), torch.float32, device, stream, "P")
@@ -974,22 +979,16 @@ def tn_gated_grad(A, Bt, P, dHt, offsets=None, act="silu", dA=None, dBt=None, wa
     _tensors(torch, A, Bt, P, dHt)
     dtype, device = A.dtype, A.device
     half, kind = _half_type(dtype, "A"), _activation(act)
-    E, M, K, lda, stride_a = _gated_weights(A, dtype, offsets)
-    ldb, T = _tokens(Bt, dtype, K, "Bt"), Bt.shape[0]
-    ldp = _rows(P, torch.float32, "P", (T, 2 * M), cuda=False)
-    lddh = _rows(dHt, dtype, "dHt", (T, M), cuda=False)
-    if offsets is None:
-        _same_device(device, Bt=Bt, P=P, dHt=dHt)
-    else:
-        _same_device(device, Bt=Bt, P=P, dHt=dHt, offsets=offsets)
+    E, M, K, T, lda, stride_a, ldb, ldp, lddh = _gated_operands(A, Bt, offsets, P, dHt)
     if _elsewhere(device.index):
         with torch.cuda.device(device):
             return tn_gated_grad(A, Bt, P, dHt, offsets, act, dA, dBt, want_a, want_b, stream)
     ldda = stride_da = lddb = 0
     if want_a:
         if dA is None:
-            dA = _empty(tuple(A.shape), dtype, device, stream)
-        if offsets is None:
+            dA = _empty(A.shape, dtype, device, stream)
+            ldda, stride_da = max(K, 1), 2 * M * K if E > 1 else 0
+        elif offsets is None:
             ldda = _rows(dA, dtype, "dA", tuple(A.shape))
         else:
             ldda, stride_da = _experts(dA, dtype, "dA", tuple(A.shape))

@@ -58,6 +58,9 @@ struct DeviceState {
     int grouped_slots[kGroupedOps][3] = {};   // co-resident tn_grouped_kernel CTAs or pairs, by operation and variant (0 = not queried)
     int split_slots[kGroupedOps][3] = {};     // co-resident clusters of 2, 4 and 8 single CTAs, by operation (8-bit: 2)
     bool few_attr[2][2] = {};         // gated_few_kernel's shared-memory attribute set, by type and token tiles
+    // 4-bit products' shared-memory attribute set, by kernel (warps split the sum, warps share the
+    // tokens), type, whole blocks a group, row tiles and token tiles
+    bool w4_attr[2][2][2][3][9] = {};
     bool i8_attr = false;             // tn_i8_kernel's shared-memory attribute set
     int i8_pair_slots[2] = {};        // co-resident pairs of tn_i8_pair_kernel, by its kRuns (0 = not queried)
     // One lock per stream, held by a call from its first buffer lookup through

@@ -13,6 +13,18 @@ void record_w4(const char *name, const DeviceState &dev, int64_t tiles)
     t_rec.slots = dev.sms;
 }
 
+template <typename Kernel>
+gemm_status_t allow_smem(Kernel *kernel, size_t bytes, bool &set)
+{
+    std::lock_guard<std::mutex> lock(g_mutex);
+    if (!set) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+        if (e != cudaSuccess) return fail(GEMM_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+        set = true;
+    }
+    return GEMM_OK;
+}
+
 template <bool kBf16, int kTilesM, int kTilesN>
 gemm_status_t launch_w4(const char *name, DeviceState &dev, w4::ProductParams &p, bool aligned, cudaStream_t stream)
 {
@@ -26,9 +38,9 @@ gemm_status_t launch_w4(const char *name, DeviceState &dev, w4::ProductParams &p
     if (tiles > INT32_MAX) return fail(GEMM_ERR_UNSUPPORTED, "%s: too many tiles", name);
     const int part = w4::part_floats(kTilesM, kTilesN), ring = aligned ? w4::ring_floats(kTilesM) : 0;
     const size_t smem = size_t(w4::kWarps) * (part > ring ? part : ring) * sizeof(float);
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-        if (e != cudaSuccess) return fail(GEMM_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+    if (smem > 48 * 1024) {                       // (only an aligned kernel's ring)
+        const gemm_status_t st = allow_smem(kernel, smem, dev.w4_attr[0][kBf16][whole][kTilesM][kTilesN]);
+        if (st != GEMM_OK) return st;
     }
     record_w4(name, dev, tiles);
     return launch_plain(name, kernel, dim3(static_cast<unsigned>(tiles), 1, 1), w4::kThreads, smem, stream, p);
@@ -42,8 +54,8 @@ gemm_status_t launch_w4_wide(const char *name, DeviceState &dev, w4::ProductPara
     p.token_tiles = static_cast<int32_t>((int64_t(p.N) + Cfg::kTokens - 1) / Cfg::kTokens);
     const int64_t tiles = (int64_t(p.M) + Cfg::kRows - 1) / Cfg::kRows * p.token_tiles;
     if (tiles > INT32_MAX) return fail(GEMM_ERR_UNSUPPORTED, "%s: too many tiles", name);
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kBytes);
-    if (e != cudaSuccess) return fail(GEMM_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+    const gemm_status_t st = allow_smem(kernel, Cfg::kBytes, dev.w4_attr[1][kBf16][kWhole][kTilesM][kTilesN]);
+    if (st != GEMM_OK) return st;
     record_w4(name, dev, tiles);
     return launch_plain(name, kernel, dim3(static_cast<unsigned>(tiles), 1, 1), w4::kThreads, Cfg::kBytes, stream, p);
 }
