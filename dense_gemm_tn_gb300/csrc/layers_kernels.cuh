@@ -85,13 +85,15 @@ __global__ void __launch_bounds__(kRowsThreads) cross_entropy_rows_kernel(const 
         return t < 0 ? 0.0f : t < p.classes ? p.dloss[n] : __int_as_float(0x7fffffff);
     };
     float top = 0.0f;
-    for (int64_t n = threadIdx.x; n < p.N; n += kRowsThreads) top = fmaxf(top, fabsf(factor(n)));
+    for (int64_t n = threadIdx.x; n < p.N; n += kRowsThreads) {
+        const float f = fabsf(factor(n));
+        if (f < __int_as_float(0x7f800000)) top = fmaxf(top, f);     // (no infinity and no NaN)
+    }
     for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
     if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = top;
     __syncthreads();
     for (int i = 0; i < kRowsThreads / 32; ++i) top = fmaxf(top, tops[i]);
-    // (all 0, or an infinity among them: as they are)
-    if (!(top > 0.0f && top < __int_as_float(0x7f800000))) top = 1.0f;
+    if (top == 0.0f) top = 1.0f;
     const float up = p.half ? 8192.0f : 1.0f;
     for (int64_t n = threadIdx.x; n < p.N; n += kRowsThreads)
         p.rows[n] = make_float2(-p.lse[n] * kLog2e, __fdiv_rn(factor(n), top) * up);

@@ -107,6 +107,23 @@ def test_a_mean_loss_rounds_no_gradient_alike(N):
         assert abs(along) < 2.0 ** -11
 
 
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_a_loss_gradient_that_is_not_finite(dtype, bad):
+    """One token's; the others' rows stay what they are, gradients in the hundreds among them."""
+    A, Bt, targets, dloss = operands(70, 100, 64, dtype)
+    dloss *= 70 * 900
+    lse = tn.tn_cross_entropy(A, Bt, targets)[1]
+    kept = dloss.clone()
+    kept[7] = 0
+    _, rB, _, eB = loss_grad64(A, Bt, targets, kept, dtype, lse)
+    dloss[7] = bad
+    dA, dB = tn.tn_cross_entropy_grad(A, Bt, targets, lse, dloss)
+    others = torch.arange(70, device="cuda") != 7
+    assert_within(dB[others], rB[others], eB[others], "dB")
+    assert not bool(torch.isfinite(dB[7]).any()) and not bool(torch.isfinite(dA).any())
+
+
 def test_targets_that_are_no_class():
     A, Bt, targets, dloss = operands(70, 100, 64, torch.bfloat16)
     targets[3], targets[40] = 100, 1 << 40
