@@ -1,8 +1,8 @@
 // gated_few_kernel: the gated projections (grouped_sinks.cuh) of up to 16 tokens, a
-// decode step's.  What bounds them is the read of the weights, once, and for few
-// tokens the general kernel's tiles are too coarse for it: at 14336 x 4096 its 224
-// tiles of 128 rows make one and a half waves of SMs, 55 us; here 896 tiles of 16
-// gate and 16 up rows are three CTAs an SM and more.
+// decode step's, over weights of a few megabytes.  What bounds them is the read of the weights,
+// once, and the general kernel's tiles are too coarse for it: 2048 x 2048 are 32 tiles of
+// 64 gate and 64 up rows (split four ways, 9.8 us); here they are 128 of 16 and 16, 6.0 us
+// with one token (2.8 TB/s; the kernel's start and its join are most of the rest).
 //
 // A CTA's warps share a tile's rows and split the sum by blocks of 64 terms (128
 // bytes of a row).  Each lane copies its own 16-byte pieces of its rows kDepth - 1

@@ -186,17 +186,21 @@ gemm_status_t check_gated(const char *name, int type, int act, int64_t E, int64_
 }
 
 // A decode step's tokens go to a kernel of their own (where the general one would read
-// the operands in place).  Measured on GB300, general -> this: 14336 x 4096 with one token
-// 57.5 -> 45.6 us, with 16 57.7 -> 48.9; 2048 x 2048 with one 11.5 -> 5.8; 512 x 1024 10.0 -> 3.1; by
-// expert, 8 of 4096 x 2048 with 16 tokens 59.8 -> 57.1, 8 of 32 of 1024 x 2048 21.4 -> 18.9.
+// the operands in place) up to two of its CTAs an SM: there the general kernel's tiles are
+// too few, beyond it their wider loads win.  Measured on GB300, general / this: 512 x 1024
+// with one token 6.8 / 3.0 us, 2048 x 2048 9.8 / 6.0, with 16 tokens 10.0 / 6.7, 4096 x 2048 11.3 / 10.5
+// and 11.6 / 9.3, 4096 x 4096 16.7 / 18.3 and 16.9 / 16.2 (256 CTAs); 8192 x 2048 15.4 / 17.2,
+// 14336 x 4096 42.5 / 44.9 (896).  By expert: 2 of 8 of 1024 x 2048 10.5 / 7.2, 8 of 8 (512
+// CTAs) 15.8 / 18.4.
 constexpr int64_t kGatedFewRows = 16;
+
+int64_t gated_few_ctas(bool dense, int64_t E, int64_t M, int64_t T) { return (M + 15) / 16 * (dense || E < T ? E : T); }
 
 template <bool kBf16, int kTilesN>
 gemm_status_t launch_gated_few(const char *name, DeviceState &dev, const tn::GatedFewParams &p, cudaStream_t stream)
 {
     auto kernel = tn::gated_few_kernel<kBf16, kTilesN>;
-    const int64_t ctas = int64_t(p.tiles) * (p.offsets ? (p.E < p.T ? p.E : p.T) : 1);
-    if (ctas > INT32_MAX) return fail(GEMM_ERR_UNSUPPORTED, "%s: too many output tiles", name);
+    const int64_t ctas = gated_few_ctas(!p.offsets, p.E, p.M, p.T);
     {
         std::lock_guard<std::mutex> lock(g_mutex);
         bool &set = dev.few_attr[kBf16][kTilesN - 1];
@@ -239,7 +243,7 @@ gemm_status_t run_gated(int type, int act, int64_t E, int64_t M, int64_t K, int6
     if ((st = check_workspace(name, workspace, workspace_bytes, plan.bytes, "gemm_gated_workspace")) != GEMM_OK) return st;
     DeviceState *dev = nullptr;
     if ((st = device_state(&dev, nullptr)) != GEMM_OK) return st;
-    if (K > 0 && T <= kGatedFewRows && !plan.g.x.copy && !plan.g.y.copy) {
+    if (K > 0 && T <= kGatedFewRows && !plan.g.x.copy && !plan.g.y.copy && gated_few_ctas(!offsets, E, M, T) <= 2 * dev->sms) {
         const tn::GatedFewParams p{static_cast<const uint16_t *>(A), lda, stride_a, static_cast<const uint16_t *>(B), ldb, offsets,
                                    static_cast<uint16_t *>(H), ldh, P, ldp, static_cast<int32_t>(E), static_cast<int32_t>(T),
                                    static_cast<int32_t>(M), static_cast<int32_t>(K), static_cast<int32_t>((M + 15) / 16), act};

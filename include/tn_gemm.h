@@ -392,7 +392,8 @@ gemm_status_t gemm_quantize_i8_rows(const void *x, int x_type, int64_t rows, int
  * gemm_tn_gated, else 1; dense: not 0 where offsets is NULL), -1 for sizes it would
  * refuse.  The forward call needs none where the TMA reads the operands in place
  * (base, lda, ldb, stride_a and K multiples of 16 bytes); the backward call holds dP
- * there (4 M T bytes) and, without offsets, up to 16 FP32 sums of dB (64 K T bytes).  Ownership and alignment as for gemm_tn_grouped.
+ * there (4 M T bytes) and, without offsets, up to 16 FP32 sums of dB (64 K T bytes).
+ * Ownership and alignment as for gemm_tn_grouped.
  *
  * Errors: as for gemm_tn_grouped, and GEMM_ERR_INVALID_ARG for an unknown
  * activation, or offsets NULL with E != 1.
@@ -439,9 +440,11 @@ gemm_status_t gemm_tn_gated_grad(int type, int act, int64_t E, int64_t M, int64_
  * Logits and statistics are FP32.
  *
  * gemm_tn_cross_entropy_grad takes the lse that the forward call left.  It computes
- * the logits again, a piece of the vocabulary at a time; d is rounded to `type`
- * there, and dB is summed over the pieces in FP32, in a fixed order.  dA or dB may
- * be NULL: that gradient is not computed.  N == 0 writes zeros to dA.
+ * the logits again, a piece of the vocabulary at a time.  There d, as a share of the
+ * largest finite |dloss|, is rounded to `type` (in fp16 a share below 2^-27 loses bits,
+ * and one below 2^-38 is 0); the products' FP32 sums are scaled back before they are
+ * rounded.  dB is summed over the pieces in FP32, in a fixed order.  dA or dB may be
+ * NULL: that gradient is not computed.  N == 0 writes zeros to dA.
  *
  * Workspace: gemm_cross_entropy_workspace returns the bytes that a call needs (grad:
  * 0 for gemm_tn_cross_entropy, else 1), -1 for sizes it would refuse: forward N M / 4
@@ -481,14 +484,14 @@ gemm_status_t gemm_tn_cross_entropy_grad(int type, int64_t M, int64_t N, int64_t
  * 256.  scale_a[m,g] at scale_a[m*ld_scale + g], ld_scale >= ceil(K / group).  B
  * (N x K), C (N rows of M) and the scales are of `type` (GEMM_IN_F16 or GEMM_IN_BF16).
  * A group's sum is FP32 of exact products, the scale is applied to it in FP32, and the
- * result is rounded once.  Any N is accepted; the codes are read once for every 32
- * tokens, so for hundreds of them a product of widened weights is faster.  One launch,
- * no buffer.
+ * result is rounded once.  Any N is accepted; the codes are read and widened once for
+ * every 32 to 64 tokens, so for hundreds of them a product of widened weights is
+ * faster.  One launch, no buffer.
  *
  * gemm_quantize_w4_rows makes such weights of x (rows x cols; x_type and ldx as for
  * gemm_quantize_e4m3):
  *
- *     scale[r,g] = max_{c in g} |x[r,c]| * (1/7)   fp32 (1/7 as an fp32 number), rounded to scale_type (16 bits)
+ *     scale[r,g] = max_{c in g} |x[r,c]| * (1/7)   in fp32, 1/7 as an fp32 number; rounded to scale_type
  *     q[r,c]     = round(x[r,c] / scale[r,g])      of the exact quotient, ties to even, within -8 .. 7
  *
  * A group of zeros, or whose scale rounds to 0, has codes 0; one with an infinity or a
@@ -499,8 +502,8 @@ gemm_status_t gemm_tn_cross_entropy_grad(int type, int64_t M, int64_t N, int64_t
  * a leading dimension below its row's length, or NULL or misaligned pointers with work
  * to do (codes need no alignment; rows on 16-byte boundaries are fastest);
  * GEMM_ERR_UNSUPPORTED off sm_103 or for sizes beyond 2^31 - 256 (the quantiser: 2^40
- * elements, 16776960 columns of FP32,
- * twice that of 16 bits); GEMM_ERR_CUDA on a failed launch.
+ * elements, 16776960 columns of FP32, twice that of 16 bits); GEMM_ERR_CUDA on a
+ * failed launch.
  */
 gemm_status_t gemm_w4_tn(int type, int64_t M, int64_t N, int64_t K,
                          const void *A, int64_t lda, const void *scale_a, int64_t ld_scale, int64_t group,

@@ -69,6 +69,40 @@ def test_experts(counts, M, K, lead, dtype, act):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("counts,M,K,lead", [([0, 0, 3, 0, 1], 40, 64, 0), ([1] * 13, 24, 136, 0), ([0] * 40 + [2] + [0] * 30 + [5], 17, 72, 3),
+                                             ([0] * 31 + [1, 1, 9], 33, 200, 1), ([14, 0], 100, 512, 0), ([0, 0, 0], 24, 64, 5),
+                                             ([3, 1, 0, 2], 1600, 136, 0), ([1, 4, 0, 0, 5], 900, 520, 4)])
+def test_few_tokens_by_expert(counts, M, K, lead, dtype):
+    """At most 16 rows: experts found among many without, and tiles for two CTAs an SM and for more."""
+    offsets = offsets_of(counts, lead)
+    bounds = offsets.tolist()
+    T = bounds[-1] + 2
+    assert T <= 16
+    A, Bt, dH = operands(len(counts), T, M, K, dtype)
+    rows = slice(lead, bounds[-1])
+    Bt[:lead] = float("nan")
+    Bt[bounds[-1]:] = float("inf")
+    H, P = torch.full((T, M), 7.0, device="cuda", dtype=dtype), torch.full((T, 2 * M), 7.0, device="cuda")
+    act = ACTS[len(counts) % 3]
+    tn.tn_gated(A, Bt, offsets, act=act, H=H, P=P)
+    tn.gemm_poll_device_status()
+    H64, P64, off = gated64(A, Bt, bounds, act)
+    assert_within(P[rows], P64[rows], (off + 2.0 ** -126)[rows], "P")
+    assert_within(H[rows], H64[rows], gated_bound(P64, off, act, dtype)[rows], "H")
+    for t in (H, P):
+        assert bool((t[:lead] == 7).all()) and bool((t[bounds[-1]:] == 7).all())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T", [1, 8, 9, 16])
+@pytest.mark.parametrize("M", [4864, 4865])
+def test_few_tokens_and_many_rows(T, M, dtype):
+    """16 rows a CTA: 304 of them, and one more."""
+    A, Bt, dH = operands(1, T, M, 72, dtype)
+    check(A, Bt, dH, None, [0, T], "silu", dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("lda,ldb,ldh", [(72, 80, 56), (65, 67, 51), (64, 65, 50)])
 def test_strides(lda, ldb, ldh, dtype):
     E, T, M, K = 3, 150, 50, 64
