@@ -268,17 +268,18 @@ gemm_status_t run_gated(int type, int act, int64_t E, int64_t M, int64_t K, int6
 }
 
 template <int kAct>
-gemm_status_t launch_gated_grad(const char *name, DeviceState &dev, const tn::GatedGradParams &p, bool bf16,
-                                cudaStream_t stream)
+gemm_status_t launch_gated_grad(const char *name, DeviceState &dev, tn::GatedGradParams p, bool bf16, cudaStream_t stream)
 {
     const bool vec = p.M % 8 == 0 && p.pre_ld % 4 == 0 && p.dh_ld % 8 == 0 && aligned_to(p.pre, 16) && aligned_to(p.dh, 16);
     const int64_t units = vec ? int64_t(p.M) / 8 : p.M;
-    const int64_t across = (units + tn::kGatedGradThreads - 1) / tn::kGatedGradThreads;
+    p.lanes = 32;
+    while (p.lanes < tn::kGatedGradThreads && p.lanes < units) p.lanes *= 2;
+    const int64_t across = (units + p.lanes - 1) / p.lanes, rows = tn::kGatedGradThreads / p.lanes;
     // about eight CTAs an SM, whole rows of them
     const int64_t want = int64_t(dev.sms) * 8;
     const int64_t gx = across < want ? across : want;
     int64_t gy = (want + gx - 1) / gx;
-    if (gy > p.T) gy = p.T;
+    if (gy > (p.T + rows - 1) / rows) gy = (p.T + rows - 1) / rows;
     if (gy > 65535) gy = 65535;
     const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(gy), 1);
     auto kernel = bf16 ? (vec ? tn::gated_grad_kernel<kAct, true, true> : tn::gated_grad_kernel<kAct, true, false>)
@@ -331,7 +332,7 @@ gemm_status_t run_gated_grad(int type, int act, int64_t E, int64_t M, int64_t K,
         dP = ws.take<uint16_t>(size_t(T) * size_t(plan.ldd));
         if (plan.floats) sum = ws.take<float>(plan.floats);
         const tn::GatedGradParams p{P, ldp, static_cast<const uint16_t *>(dH), lddh, dP, plan.ldd, offsets,
-                                    static_cast<int32_t>(E), static_cast<int32_t>(T), static_cast<int32_t>(M)};
+                                    static_cast<int32_t>(E), static_cast<int32_t>(T), static_cast<int32_t>(M), 0};
         const bool bf16 = type == GEMM_IN_BF16;
         st = act == GEMM_ACT_SILU   ? launch_gated_grad<tn::kActSilu>(name, *dev, p, bf16, stream)
              : act == GEMM_ACT_GELU ? launch_gated_grad<tn::kActGelu>(name, *dev, p, bf16, stream)
