@@ -75,7 +75,12 @@ struct Sink;
 
 // ------------------------------------------------------------------ gated projections
 // The L operand's rows alternate, 16 gate rows and the 16 up rows beside them, so
-// a thread's v[0] and v[1] hold the gate and the up product of the same 16 results.
+// a thread's v[0] and v[1] hold the gate and the up product of the same 16 results, and
+// the products need not go to memory.  On GB300 the activation hides behind the next tile's
+// products: 3001 rows over 8 experts of 1024 x 2048 take 26.0 us with silu, 26.5 with gelu_tanh
+// (the plain product of as many rows 25.7), 31.1 with gelu, whose erfc is the longest; the
+// products' 25 MB in FP32 cost 4 to 5 more.  4096 tokens over 14336 x 4096: 549 us, 0.91 of the
+// measured burst rate.
 template <>
 struct Sink<4 /* kGrGated */> {
     template <int kAct, bool kBf16, class Store>
@@ -172,7 +177,9 @@ struct Sink<4 /* kGrGated */> {
 // pieces.  A column's logits lie in eight lanes, four in each, and a lane has four of
 // eight columns.  So the columns' maxima and sums are merged by halving: each turn a
 // lane passes on half of its columns, 7 exchanges for 8 columns, and 7 more take the
-// maxima back to all lanes before the exponentials.
+// maxima back to all lanes before the exponentials.  4096 tokens over 8192 classes of 4096 take
+// 153 us on GB300 (0.93 of the measured burst rate); 1021 over 32003 of 1024 52.1, of which the
+// products alone would take 35: over short sums the epilogue is longer than a tile's products.
 template <>
 struct Sink<5 /* kGrLossStats */> {
     static __device__ __forceinline__ void merge(float &m, float &s, float om, float os)
@@ -277,7 +284,8 @@ struct Sink<5 /* kGrLossStats */> {
 // tensor cores multiply in both gradients.  (The factors are shares of the largest, in
 // fp16 times 2^13, see cross_entropy_rows_kernel; d then keeps its relative precision
 // down to 2^-27 of it.)  Classes past the piece's end are zeros: the
-// products over the piece read them.
+// products over the piece read them.  A piece of 16384 classes of 4096 for 4096 tokens
+// takes 306 us on GB300, 0.93 of the measured burst rate.
 template <>
 struct Sink<6 /* kGrLossGrad */> {
     template <class Params, class Store>
@@ -346,7 +354,9 @@ struct Sink<6 /* kGrLossGrad */> {
 // first leaves FP32 sums, the next ones add theirs (each element once a launch, so the
 // order is the launches'), and the last one's result is rounded once.  And where a
 // launch's tiles are few, parts of its sum are tiles of their own, each part with
-// sums of its own; parts_join_kernel adds them up in their order.
+// sums of its own; parts_join_kernel adds them up in their order.  A piece of 16384 classes
+// for 4096 tokens of 4096: 347 us on GB300, of which the FP32 sums (64 MiB, read and written
+// once) take some 30.
 template <>
 struct Sink<7 /* kGrGradBAdd */> {
     template <class Params, class Store>
@@ -389,6 +399,8 @@ struct Sink<7 /* kGrGradBAdd */> {
     }
 };
 
+// A weight gradient whose sums carry the loss gradient's scale.  Nothing else is added
+// to the plain one: 16384 classes of 4096, 4096 tokens, 316 us on GB300 (0.90 of the burst rate).
 template <>
 struct Sink<8 /* kGrGradAOne */> {
     template <class Params, class Store>

@@ -67,12 +67,13 @@ gemm_status_t launch_w4_wide(const char *name, DeviceState &dev, w4::ProductPara
                               : launch_w4_wide<kBf16, kTilesM, kTilesN, false>(name, dev, p, stream);
 }
 
-// Up to 8 tokens, few rows and rows that are not aligned: warps split the sum (two tiles
-// of 16 rows each where that still leaves 1.5 CTAs an SM: 8192 x 8192 and one token
-// 12.3 us, one tile 14.1; 1024 x 4096 4.3 and 3.4).  More tokens over rows that give nearly every SM
-// a tile of 64: warps share the tokens.  Measured on GB300 at K = 4096, groups of 128,
-// split / shared: 16 tokens, 4096 rows 7.3 / 11.3 us, 8192 13.0 / 11.8, 28672 35.1 / 26.5; 64 tokens
-// 17.7 / 24.4, 33.1 / 25.0, 96.4 / 72.4.
+// Up to 8 tokens, few rows and rows that are not aligned: warps split the sum, each with two
+// tiles of 16 rows where these still make three CTAs for four SMs.  Measured on GB300, groups of
+// 128, one tile / two: 8192 x 8192 and one token 13.7 / 11.8 us, 28672 x 4096 19.0 / 19.0, with
+// eight 23.9 / 20.2, 4096 x 4096 with one 5.9 / 5.2, 1024 x 4096 3.0 / 3.9.  More tokens over rows
+// that give nearly every SM a tile of 64: warps share the tokens.  At K = 4096, split / shared:
+// 16 tokens, 4096 rows 7.0 / 10.6 us, 8192 12.6 / 11.0, 28672 34.6 / 24.1; 64 tokens 17.7 / 25.4,
+// 33.2 / 25.8, 96.3 / 74.5.
 template <bool kBf16>
 gemm_status_t launch_w4_tokens(const char *name, DeviceState &dev, w4::ProductParams &p, bool aligned, cudaStream_t stream)
 {

@@ -448,7 +448,7 @@ gemm_status_t gemm_tn_gated_grad(int type, int act, int64_t E, int64_t M, int64_
  *
  * Workspace: gemm_cross_entropy_workspace returns the bytes that a call needs (grad:
  * 0 for gemm_tn_cross_entropy, else 1), -1 for sizes it would refuse: forward N M / 4
- * + 4 N, gradient about 128 MiB (2048 N beyond 65536 tokens; 2 N M where that is
+ * + 4 N, gradient about 256 MiB (2048 N beyond 131072 tokens; 2 N M where that is
  * less) + up to 64 N K, and copies of operands that the TMA cannot read in place (as for
  * gemm_tn_grouped).  Ownership and alignment as there.
  *

@@ -142,7 +142,7 @@ def test_workspace_queries():
     assert ws(0, 1000, 300, 64, P, 64, 2 * P, 64) == up(300 * 32 * 8) + up(300 * 4)
     assert ws(1, 1000, 300, 64, P, 64, 2 * P, 64) == up(300 * 1024 * 2) + up(300 * 8) + 256
     for N in (1, 1000, 4096, 100000, 1 << 20):             # it does not grow with the vocabulary
-        most = max(1 << 27, 2048 * N) + 64 * N * 512 + 16 * N + 4096
+        most = max(1 << 28, 2048 * N) + 64 * N * 512 + 16 * N + 4096
         assert ws(1, 262144, N, 512, P, 512, 2 * P, 512) <= most
     with pytest.raises(ValueError):
         ws(0, 1000, 300, 64, P, 63, 2 * P, 64)
