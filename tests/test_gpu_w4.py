@@ -176,6 +176,17 @@ def test_quantiser(rows, cols, group, dtype, source):
 
 
 @pytest.mark.parametrize("source", [torch.float32, torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("rows,cols,ld", [(20001, 40, 40), (15001, 257, 257), (6001, 1029, 1032), (100003, 8, 24)])
+def test_quantiser_of_many_rows(rows, cols, ld, source):
+    """Several rows to a warp, each read while the one before it is worked on."""
+    x = padded(normals(rows, cols, seed=rows, dtype=torch.float32).mul_(torch.arange(rows, device="cuda")[:, None] % 7).to(source), ld, float("inf"))
+    for dtype, group in ((torch.float16, 32), (torch.bfloat16, 256)):
+        q, scale = tn.quantize_w4_rows(x, group, dtype=dtype)
+        q64, s64 = quant64(x, group, dtype)
+        assert torch.equal(unpack(q, cols), q64) and torch.equal(scale, s64)
+
+
+@pytest.mark.parametrize("source", [torch.float32, torch.float16, torch.bfloat16])
 def test_quantiser_at_borders(source):
     """Quotients at and next to a half, and scales at the ends of their types."""
     dtype = torch.bfloat16 if source == torch.bfloat16 else torch.float16
