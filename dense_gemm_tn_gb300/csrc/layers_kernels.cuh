@@ -164,8 +164,10 @@ __global__ void __launch_bounds__(kPartsThreads) parts_join_kernel(const PartsPa
 // ------------------------------------------------------------------ gated: backward
 // d_gate = dH u act'(g) and d_up = dH act(g) from the kept products, rounded to the
 // operands' type: 8 bytes of products and 2 of dH read, 4 written an element, nothing
-// else.  kVec: 8 elements a thread (rows on 16-byte boundaries); short rows share a CTA (3001
-// rows of 1024: a gradient of 71.3 us in all with a CTA a row, 69.9 with half a one).
+// else.  4096 rows of 14336 take 154 us on GB300 (5.3 TB/s; 171 with loads marked as read once),
+// 3001 of 1024 6.4 out of the L2.  kVec: 8 elements a thread (rows on 16-byte boundaries);
+// short rows share a CTA (3001 rows of 1024, the whole gradient: 71.3 us with a CTA a row, 69.9
+// with half a one).
 constexpr int kGatedGradThreads = 256;
 
 struct GatedGradParams {
@@ -217,12 +219,12 @@ __global__ void __launch_bounds__(kGatedGradThreads) gated_grad_kernel(const Gat
             if constexpr (kVec) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const float4 a = __ldcs(reinterpret_cast<const float4 *>(gate) + 2 * i + h);
-                    const float4 b = __ldcs(reinterpret_cast<const float4 *>(up) + 2 * i + h);
+                    const float4 a = __ldg(reinterpret_cast<const float4 *>(gate) + 2 * i + h);
+                    const float4 b = __ldg(reinterpret_cast<const float4 *>(up) + 2 * i + h);
                     g[4 * h] = a.x, g[4 * h + 1] = a.y, g[4 * h + 2] = a.z, g[4 * h + 3] = a.w;
                     u[4 * h] = b.x, u[4 * h + 1] = b.y, u[4 * h + 2] = b.z, u[4 * h + 3] = b.w;
                 }
-                const uint4 c = __ldcs(reinterpret_cast<const uint4 *>(dh) + i);
+                const uint4 c = __ldg(reinterpret_cast<const uint4 *>(dh) + i);
                 const uint32_t w[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
