@@ -108,3 +108,16 @@ def test_captured_calls_on_a_forked_stream():
         for name in got:
             assert same(got[name], want[name]), name
     g.gemm_poll_device_status()
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_both_bindings(name, monkeypatch):
+    """The same results through ctypes as through the CPython-API binding."""
+    if g.fast is None:
+        pytest.skip("the CPython-API binding was not built (no Python.h)")
+    results = []
+    for binding in (g.fast, g.lib):
+        monkeypatch.setattr(g, "calls", binding)
+        results.append(tensors(calls()[name](None)))
+    g.gemm_poll_device_status()
+    assert same(*results)
