@@ -115,9 +115,9 @@ def test_both_bindings(name, monkeypatch):
     """The same results through ctypes as through the CPython-API binding."""
     if g.fast is None:
         pytest.skip("the CPython-API binding was not built (no Python.h)")
-    results = []
+    call, results = calls()[name], []
     for binding in (g.fast, g.lib):
         monkeypatch.setattr(g, "calls", binding)
-        results.append(tensors(calls()[name](None)))
+        results.append(tensors(call(None)))
     g.gemm_poll_device_status()
     assert same(*results)
