@@ -491,7 +491,7 @@ gemm_status_t gemm_tn_cross_entropy_grad(int type, int64_t M, int64_t N, int64_t
  * gemm_quantize_w4_rows makes such weights of x (rows x cols; x_type and ldx as for
  * gemm_quantize_e4m3):
  *
- *     scale[r,g] = max_{c in g} |x[r,c]| * (1/7)   in fp32, 1/7 as an fp32 number; rounded to scale_type
+ *     scale[r,g] = max_{c in g} |x[r,c]| / 7       in fp32, rounded to scale_type
  *     q[r,c]     = round(x[r,c] / scale[r,g])      of the exact quotient, ties to even, within -8 .. 7
  *
  * A group of zeros, or whose scale rounds to 0, has codes 0; one with an infinity or a
