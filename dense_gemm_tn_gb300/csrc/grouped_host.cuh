@@ -353,7 +353,7 @@ gemm_status_t launch_grouped_op(const GroupedCall &c, DeviceState &dev, tn::Grou
         if constexpr (kOp == tn::kGrGradAOne) {
             if ((st = encode_2d(&prm.tmap_r[0], type, x, inner_x, c.T, ldx * 2, 64, tn::kGrBlock, "dC")) != GEMM_OK) return st;
             if ((st = encode_2d(&prm.tmap_l, type, y, inner_y, c.T, ldy * 2, 64, tn::kGrBlock, "B")) != GEMM_OK) return st;
-        } else if constexpr (kOp == tn::kGrGradA) {
+        } else if constexpr (tn::grouped_has_maps(kOp)) {
             tn::GroupedMapsParams m;
             memset(&m, 0, sizeof(m));
             if ((st = encode_2d(&m.dc, type, x, inner_x, c.T, ldx * 2, 64, tn::kGrBlock, "dC")) != GEMM_OK) return st;

@@ -63,16 +63,22 @@ enum GroupedOp : int {
     kGrLossStats = 5,        // a product whose columns' softmax statistics are stored
     kGrLossGrad = 6,         // a product whose softmax's loss gradient is stored
     kGrGradBAdd = 7,         // a token gradient in parts, added up in FP32
-    kGrGradAOne = 8          // a weight gradient of one group, times a scale
+    kGrGradAOne = 8,         // a weight gradient of one group, times a scale
+    kGrGradBScaled = 9,      // the first two gradients, times a scale
+    kGrGradAScaled = 10
 };
-constexpr int kGrOps = 9;
+constexpr int kGrOps = 11;
 
 // The one of the first three that an operation reads its operands as.
 __host__ __device__ constexpr int grouped_reads(int op)
 {
     return op == kGrGated || op == kGrLossStats || op == kGrLossGrad ? kGrProduct
-           : op == kGrGradBAdd ? kGrGradB : op == kGrGradAOne ? kGrGradA : op;
+           : op == kGrGradBAdd || op == kGrGradBScaled ? kGrGradB
+           : op == kGrGradAOne || op == kGrGradAScaled ? kGrGradA : op;
 }
+
+// Weight gradients by expert: the groups' rows have tensor maps of their own.
+__host__ __device__ constexpr bool grouped_has_maps(int op) { return op == kGrGradA || op == kGrGradAScaled; }
 
 constexpr int kI8RowsL = 128, kI8Rows = 64;  // the 8-bit kernel's tile (i8_kernel.cuh)
 constexpr int kGrEpiWarps = 8;               // epilogue warps: two per quarter of the TMEM lanes
@@ -623,7 +629,7 @@ __global__ void __launch_bounds__(GroupedWarps<kOp>::kThreads, 1) tn_grouped_ker
         ptx::fence_mbar_init();
         ptx::fence_proxy_async_smem();
     }
-    if (kOp != kGrGradA && threadIdx.x == 32 && p.red > 0) {
+    if (!grouped_has_maps(kOp) && threadIdx.x == 32 && p.red > 0) {
         ptx::prefetch_tensormap(&p.tmap_l);
         ptx::prefetch_tensormap(&p.tmap_r[kReads == kGrGradA ? 0 : Cfg::kRowsR / 16 - 1]);
     }
@@ -668,6 +674,8 @@ __global__ void __launch_bounds__(GroupedWarps<kOp>::kThreads, 1) tn_grouped_ker
     auto tile_at = [&](int32_t u) { return walk.at(kParts ? u % tiles : u); };
     auto rank_of = [&](int32_t u) { return kParts ? u / tiles : parts.rank; };
     auto blocks_of = [](int32_t red) { return (red + kGrBlock - 1) / kGrBlock; };
+    // what a sink is told beside the place: the part of the sum, or the group
+    auto which = [&](const GroupedTile &t, int32_t u) { return kParts ? rank_of(u) : grouped_has_maps(kOp) ? t.e : 0; };
     // a part of a sum that is too short for all of them
     auto no_terms = [&](const GroupedTile &t, int32_t u) {
         return kParts && part(blocks_of(t.red), rank_of(u)) == part(blocks_of(t.red), rank_of(u) + 1);
@@ -705,7 +713,7 @@ __global__ void __launch_bounds__(GroupedWarps<kOp>::kThreads, 1) tn_grouped_ker
                 const uint32_t fill = Cfg::kLBytes + r_bytes;
                 // (a weight gradient of one group: the call's own two maps)
                 const CUtensorMap *map_l = &p.tmap_l, *map_r = p.tmap_r;
-                if constexpr (kOp == kGrGradA) {
+                if constexpr (grouped_has_maps(kOp)) {
                     map_r = p.group_maps + 2 * t.e;
                     map_l = map_r + 1;
                     if (t.e != mapped && t.red > 0) {
@@ -1037,7 +1045,7 @@ __global__ void __launch_bounds__(GroupedWarps<kOp>::kThreads, 1) tn_grouped_ker
                 if constexpr (kSinks) {
                     const uint32_t zero[2][16] = {};
                     for (int32_t c = turn * kGrChunk; c < t.rows; c += Warps::kTurns * kGrChunk)
-                        Sink<kOp>::step(p, store, zero, l0, row0 + c, t.rows - c, kParts ? rank_of(u) : 0);
+                        Sink<kOp>::step(p, store, zero, l0, row0 + c, t.rows - c, which(t, u));
                 } else if (lane < store.wide) {
                     for (int32_t r = turn; r < t.rows; r += 2) out[r * p.out_ld + lane] = 0;
                 }
@@ -1131,7 +1139,7 @@ __global__ void __launch_bounds__(GroupedWarps<kOp>::kThreads, 1) tn_grouped_ker
                 if constexpr (kSinks)
                     GroupedStore::each_step(t_row, turn, steps, hand_back, [&](int32_t s, const uint32_t (&v)[2][16]) {
                         const int32_t c = s * kGrChunk;
-                        Sink<kOp>::step(p, store, v, l0, row0 + first + c, rows - c, kParts ? rank_of(u) : 0);
+                        Sink<kOp>::step(p, store, v, l0, row0 + first + c, rows - c, which(t, u));
                     });
                 else if (out_bf16)
                     store.half<true, false>(t_row, turn, steps, dst, rows, nullptr, hand_back);

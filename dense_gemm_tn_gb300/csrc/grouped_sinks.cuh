@@ -417,13 +417,13 @@ struct Sink<7 /* kGrGradBAdd */> {
     }
 };
 
-// A weight gradient whose sums carry the loss gradient's scale.  Nothing else is added
-// to the plain one: 16384 classes of 4096, 4096 tokens, 316 us on GB300 (0.90 of the burst rate).
-template <>
-struct Sink<8 /* kGrGradAOne */> {
+// Gradients whose sums carry a scale: the loss gradient's (one group), or that of fp16's
+// gated dP.  Nothing else is added to the plain ones: 16384 classes of 4096, 4096 tokens, 316 us
+// on GB300 (0.90 of the burst rate).
+struct ScaledSink {
     template <class Params, class Store>
     static __device__ __forceinline__ void step(const Params &p, const Store &store, const uint32_t (&v)[2][16],
-                                                int32_t l0, int64_t row, int32_t rows, int32_t part)
+                                                int32_t l0, int64_t row, int32_t rows, int32_t group)
     {
         const float scale = p.sink.out_scale ? __ldg(p.sink.out_scale) : 1.0f;
         uint32_t x[2][16];
@@ -431,12 +431,18 @@ struct Sink<8 /* kGrGradAOne */> {
         for (int q = 0; q < 2; ++q)
 #pragma unroll
             for (int b = 0; b < 16; ++b) x[q][b] = __float_as_uint(__uint_as_float(v[q][b]) * scale);
-        uint16_t *out = p.out + row * p.out_ld + l0;
+        uint16_t *out = p.out + group * p.out_stride + row * p.out_ld + l0;
         if (p.out_fmt != 0)
             store.template step<true, false>(x, out, rows, nullptr);
         else
             store.template step<false, false>(x, out, rows, nullptr);
     }
 };
+template <>
+struct Sink<8 /* kGrGradAOne */> : ScaledSink {};
+template <>
+struct Sink<9 /* kGrGradBScaled */> : ScaledSink {};
+template <>
+struct Sink<10 /* kGrGradAScaled */> : ScaledSink {};
 
 }  // namespace tn

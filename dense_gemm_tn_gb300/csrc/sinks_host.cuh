@@ -119,9 +119,10 @@ bool gated_sizes_fit(int64_t E, int64_t M, int64_t K, int64_t T, int64_t lda, in
 
 struct GatedPlan {
     GroupedPlan g;               // the copies (and the backward pass's tensor maps)
-    int64_t ldd;                 // the backward pass's rows of 2 M gradients, padded
+    int64_t ldd, units;          // the backward pass's rows of 2 M gradients: padded, and up to a whole 16-byte unit
     ProductCut cut;              // without experts: of the token gradient
     size_t floats;               // ... and its parts' sums
+    size_t entries;              // ... of the room (layers_kernels.cuh) where dP's rows have none to spare
     size_t bytes;
     bool fits;
 };
@@ -132,6 +133,7 @@ GatedPlan gated_plan(bool grad, bool dense, int64_t E, int64_t M, int64_t K, int
 {
     GatedPlan p{};
     p.fits = true;
+    p.units = (2 * M + 7) / 8 * 8;
     p.ldd = (2 * M + 63) / 64 * 64;
     if (grouped_idle(E, M, K, T)) return p;
     if (!grad) {
@@ -149,6 +151,10 @@ GatedPlan gated_plan(bool grad, bool dense, int64_t E, int64_t M, int64_t K, int
         p.cut = token_grad_cut(T, K, 2 * M);
         p.floats = token_grad_floats(p.cut, 1, T, K);
         p.bytes += (p.floats * sizeof(float) + 255) & ~size_t(255);
+    }
+    if ((p.ldd - p.units) * 2 < int64_t(tn::kGatedEntry * sizeof(float))) {
+        p.entries = size_t(T < tn::kGatedTops ? T : tn::kGatedTops);
+        p.bytes += (p.entries * tn::kGatedEntry * sizeof(float) + 255) & ~size_t(255);
     }
     return p;
 }
@@ -284,7 +290,19 @@ gemm_status_t launch_gated_grad(const char *name, DeviceState &dev, tn::GatedGra
     const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(gy), 1);
     auto kernel = bf16 ? (vec ? tn::gated_grad_kernel<kAct, true, true> : tn::gated_grad_kernel<kAct, true, false>)
                        : (vec ? tn::gated_grad_kernel<kAct, false, true> : tn::gated_grad_kernel<kAct, false, false>);
-    return launch_plain(name, kernel, grid, tn::kGatedGradThreads, 0, stream, p);
+    if (bf16) return launch_plain(name, kernel, grid, tn::kGatedGradThreads, 0, stream, p);
+    // fp16: the size of dH first, and the pass once more where dP's is another
+    p.tops = p.T < tn::kGatedTops ? p.T : tn::kGatedTops;
+    p.top_vec = p.dh_ld % 8 == 0 && aligned_to(p.dh, 16);
+    p.top_lanes = tn::kGatedTopThreads;           // (short rows share a CTA, and all where there are more than CTAs)
+    while (p.top_lanes > 32 && (p.top_lanes / 2 >= p.M / 8 || int64_t(p.tops) * (tn::kGatedTopThreads / p.top_lanes) < p.T))
+        p.top_lanes /= 2;
+    gemm_status_t st = launch_plain(name, tn::gated_top_kernel, dim3(static_cast<unsigned>(p.tops), 1, 1), tn::kGatedTopThreads, 0,
+                                    stream, p);
+    if (st == GEMM_OK) st = launch_plain(name, kernel, grid, tn::kGatedGradThreads, 0, stream, p);
+    p.again = true;
+    if (st == GEMM_OK) st = launch_plain(name, kernel, grid, tn::kGatedGradThreads, 0, stream, p);
+    return st;
 }
 
 gemm_status_t run_gated_grad(int type, int act, int64_t E, int64_t M, int64_t K, int64_t T, const void *A, int64_t lda,
@@ -327,13 +345,19 @@ gemm_status_t run_gated_grad(int type, int act, int64_t E, int64_t M, int64_t K,
     SinkOperands o{};
     uint16_t *dP = nullptr;
     float *sum = nullptr;
+    CUtensorMap *maps = nullptr;
+    const float *undo = nullptr;                  // fp16: dP's factor, taken back
+    const bool bf16 = type == GEMM_IN_BF16;
     if (!idle) {
         if ((st = place_operands(name, *dev, plan.g, ws, offsets, stream, o)) != GEMM_OK) return st;
+        if (offsets) maps = ws.take<CUtensorMap>(size_t(E) * 2);
         dP = ws.take<uint16_t>(size_t(T) * size_t(plan.ldd));
         if (plan.floats) sum = ws.take<float>(plan.floats);
-        const tn::GatedGradParams p{P, ldp, static_cast<const uint16_t *>(dH), lddh, dP, plan.ldd, offsets,
-                                    static_cast<int32_t>(E), static_cast<int32_t>(T), static_cast<int32_t>(M), 0};
-        const bool bf16 = type == GEMM_IN_BF16;
+        float *room = plan.entries ? ws.take<float>(plan.entries * tn::kGatedEntry) : reinterpret_cast<float *>(dP + plan.units);
+        if (!bf16) undo = room + 2;
+        const tn::GatedGradParams p{P, ldp, static_cast<const uint16_t *>(dH), lddh, dP, plan.ldd, plan.units, room,
+                                    plan.entries ? tn::kGatedEntry : plan.ldd / 2, offsets, static_cast<int32_t>(E),
+                                    static_cast<int32_t>(T), static_cast<int32_t>(M), 0, 0, 0, false, false};
         st = act == GEMM_ACT_SILU   ? launch_gated_grad<tn::kActSilu>(name, *dev, p, bf16, stream)
              : act == GEMM_ACT_GELU ? launch_gated_grad<tn::kActGelu>(name, *dev, p, bf16, stream)
                                     : launch_gated_grad<tn::kActGeluTanh>(name, *dev, p, bf16, stream);
@@ -345,10 +369,12 @@ gemm_status_t run_gated_grad(int type, int act, int64_t E, int64_t M, int64_t K,
     const int copied = (plan.g.x.copy ? 1 : 0) | (plan.g.y.copy ? 2 : 0);
     if (dB) {
         if (!offsets && !idle) {
-            st = launch_token_grad(c, *dev, plan.cut, o.x, o.ldx, o.in_x, dP, plan.ldd, 2 * M, dB, lddb, nullptr, sum, 0, 1);
+            st = launch_token_grad(c, *dev, plan.cut, o.x, o.ldx, o.in_x, dP, plan.ldd, 2 * M, dB, lddb, undo, sum, 0, 1);
         } else {
             tn::GroupedParams prm = sink_params(c, K, 2 * M, dB, lddb);
-            st = launch_grad_b(c, *dev, prm, o.x, dP, o.ldx, o.stride_x, plan.ldd, o.in_x, plan.ldd);
+            prm.sink.out_scale = undo;
+            st = bf16 ? launch_grad_b(c, *dev, prm, o.x, dP, o.ldx, o.stride_x, plan.ldd, o.in_x, plan.units)
+                      : launch_grouped_op<tn::kGrGradBScaled>(c, *dev, prm, o.x, dP, o.ldx, o.stride_x, plan.ldd, o.in_x, plan.units);
         }
         t_rec.copied = copied;
         if (st != GEMM_OK) return st;
@@ -358,11 +384,13 @@ gemm_status_t run_gated_grad(int type, int act, int64_t E, int64_t M, int64_t K,
         prm.out_stride = stride_da;
         prm.out_vec = prm.out_vec && (E == 1 || stride_da % 8 == 0);
         prm.r_extent = static_cast<int32_t>(2 * M);
+        prm.sink.out_scale = undo;
         if (offsets) {
-            prm.group_maps = idle ? nullptr : ws.take<CUtensorMap>(size_t(E) * 2);
-            st = launch_grad_a(c, *dev, prm, dP, o.y, plan.ldd, 0, o.ldy, plan.ldd, o.in_y);
+            prm.group_maps = maps;
+            st = bf16 ? launch_grad_a(c, *dev, prm, dP, o.y, plan.ldd, 0, o.ldy, plan.units, o.in_y)
+                      : launch_grouped_op<tn::kGrGradAScaled>(c, *dev, prm, dP, o.y, plan.ldd, 0, o.ldy, plan.units, o.in_y);
         } else {
-            st = launch_grouped_op<tn::kGrGradAOne>(c, *dev, prm, dP, o.y, plan.ldd, 0, o.ldy, plan.ldd, o.in_y);
+            st = launch_grouped_op<tn::kGrGradAOne>(c, *dev, prm, dP, o.y, plan.ldd, 0, o.ldy, plan.units, o.in_y);
         }
         t_rec.copied = copied;
     }

@@ -382,8 +382,10 @@ gemm_status_t gemm_quantize_i8_rows(const void *x, int x_type, int64_t rows, int
  * Operands and results are of `type` (GEMM_IN_F16 or GEMM_IN_BF16); P is FP32.
  * gemm_tn_gated is one kernel: P goes to memory only where the caller passes it
  * (T rows of 2 M with leading dimension ldp), to be kept for the backward pass.
- * gemm_tn_gated_grad rounds dP to `type` before the two products.  dA or dB may be
- * NULL: that gradient is not computed.
+ * gemm_tn_gated_grad rounds dP to `type` before the two products; in fp16 times a power of
+ * two that the largest finite number of dP decides (over all experts), which the products'
+ * FP32 sums take back: of numbers below 2^-18 of the largest bits are lost, and those below
+ * 2^-29 are 0.  dA or dB may be NULL: that gradient is not computed.
  *
  * offsets as for gemm_tn_grouped (rows of no expert are neither read nor written,
  * an expert without rows has a dA of zeros); or NULL with E == 1: all T rows.
@@ -392,7 +394,8 @@ gemm_status_t gemm_quantize_i8_rows(const void *x, int x_type, int64_t rows, int
  * gemm_tn_gated, else 1; dense: not 0 where offsets is NULL), -1 for sizes it would
  * refuse.  The forward call needs none where the TMA reads the operands in place
  * (base, lda, ldb, stride_a and K multiples of 16 bytes); the backward call holds dP
- * there (4 M T bytes) and, without offsets, up to 16 FP32 sums of dB (64 K T bytes).
+ * there (4 M T bytes, and up to 4864 for its factor) and, without offsets, up to 16 FP32
+ * sums of dB (64 K T bytes).
  * Ownership and alignment as for gemm_tn_grouped.
  *
  * Errors: as for gemm_tn_grouped, and GEMM_ERR_INVALID_ARG for an unknown
