@@ -65,14 +65,15 @@ enum GroupedOp : int {
     kGrGradBAdd = 7,         // a token gradient in parts, added up in FP32
     kGrGradAOne = 8,         // a weight gradient of one group, times a scale
     kGrGradBScaled = 9,      // the first two gradients, times a scale
-    kGrGradAScaled = 10
+    kGrGradAScaled = 10,
+    kGrLossGradLong = 11     // kGrLossGrad for sums of several segments (below)
 };
-constexpr int kGrOps = 11;
+constexpr int kGrOps = 12;
 
 // The one of the first three that an operation reads its operands as.
 __host__ __device__ constexpr int grouped_reads(int op)
 {
-    return op == kGrGated || op == kGrLossStats || op == kGrLossGrad ? kGrProduct
+    return op == kGrGated || op == kGrLossStats || op == kGrLossGrad || op == kGrLossGradLong ? kGrProduct
            : op == kGrGradBAdd || op == kGrGradBScaled ? kGrGradB
            : op == kGrGradAOne || op == kGrGradAScaled ? kGrGradA : op;
 }
@@ -90,10 +91,14 @@ constexpr int kGrThreads = 64 + 32 * kGrEpiWarps;
 // below its last bit, towards zero, at every step of 16 terms, so a long sum is short
 // by some 8e-10 of itself a term (measured: 3.3e-6 at 4096 terms, and 1024 at a time
 // 0.9e-6), all logits alike, which the loss keeps.  The segments' sums are added in FP32,
-// rounded to nearest.
+// rounded to nearest.  The loss's gradient cuts its logits alike: it takes them against the log-sum-exp
+// of the statistics' logits, and a token whose target has all but 1e-4 of the mass has a gradient of
+// 1e-4, of which a logit of 30 that is 3e-6 of itself off on one side alone would leave nothing.  (Sums
+// of one segment are the same in the kernel without, which is shorter: 1021 tokens over 32003 classes of 1024
+// with gradients take 3.6 us less.)
 template <int kOp>
 struct GroupedWarps {
-    static constexpr bool kSegmented = kOp == kGrLossStats;
+    static constexpr bool kSegmented = kOp == kGrLossStats || kOp == kGrLossGradLong;
     static constexpr int kEpi = kGrEpiWarps, kFirst = kSegmented ? 4 : 2;
     static constexpr int kThreads = 32 * (kFirst + kEpi), kTurns = kEpi / 4;
     // (the block's registers, shared out anew: the launch is refused where it was compiled for fewer)

@@ -26,6 +26,7 @@ struct SinkParams {
     float2 *stats;                   // loss: [ceil(classes / 32)][T] maximum, sum of exp(z - maximum)
     float *z_target;                 // loss: [T] the target's logit
     const float2 *rows;              // loss gradient: [T] (-log-sum-exp / log 2, factor)
+    const float *lse;                // loss gradient: [T] the log-sum-exps
     int32_t first, classes;          // loss gradient: the piece's first class, and how many
     float *sum;                      // parts added up: FP32 sums, one result for each part
     int64_t sum_ld, sum_stride;
@@ -35,13 +36,24 @@ struct SinkParams {
 
 enum AddPart : int { kAddOnly = 0, kAddFirst = 1, kAddMore = 2, kAddLast = 3 };
 
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float ex2(float x)
 {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// exp(x) - 1, for small x by the exponential's series (six terms: below 1/4 the seventh is 2^-24 of it).
+__device__ __forceinline__ float exp_less_one(float x)
+{
+    float y = fmaf(x, 1.0f / 6.0f, 1.0f);
+    y = fmaf(x * 0.2f, y, 1.0f);
+    y = fmaf(x * 0.25f, y, 1.0f);
+    y = fmaf(x * (1.0f / 3.0f), y, 1.0f);
+    y = fmaf(x * 0.5f, y, 1.0f);
+    return fabsf(x) < 0.25f ? x * y : ex2(x * kLog2e) - 1.0f;
 }
 
 // 1 / (1 + exp(-x)) (relative error about 2^-21).  exp overflows to an infinity
@@ -279,6 +291,8 @@ struct Sink<5 /* kGrLossStats */> {
         halve(x, lane, [](float a, float b) { return a + b; });
         const int32_t own = 4 * (lane >> 4 & 1) + 2 * (lane >> 3 & 1) + (lane >> 2 & 1);
         const int32_t col = 8 * (own >> 1) + 2 * (lane & 3) + (own & 1);
+        // (top / log 2 was rounded: by 2^-19 at a top of 30, which all of the column's exponentials share)
+        if (top != none) x[0] *= fmaf(-kLn2, fmaf(top, kLog2e, -top * kLog2e), 1.0f);
         if (col < rows) k.stats[static_cast<int64_t>(l0 >> 5) * p.T + row + col] = make_float2(top, x[0]);
         // the target's logit, where this piece has it
         int64_t at = -1;
@@ -299,7 +313,8 @@ struct Sink<5 /* kGrLossStats */> {
 };
 
 // d = (exp(z - lse) - [m = target]) factor, rounded to the operands' type: what the
-// tensor cores multiply in both gradients.  (The factors are shares of the largest, in
+// tensor cores multiply in both gradients.  At the target exp(x) - 1 is taken as such, which keeps what is left of
+// a probability near one.  (The factors are shares of the largest, in
 // fp16 times 2^13, see cross_entropy_rows_kernel; d then keeps its relative precision
 // down to 2^-27 of it.)  Classes past the piece's end are zeros: the
 // products over the piece read them.  A piece of 16384 classes of 4096 for 4096 tokens
@@ -315,7 +330,7 @@ struct Sink<6 /* kGrLossGrad */> {
         float d[2][16];
         int64_t at = -1;
         if (lane < rows) at = __ldg(k.targets + row + lane) - k.first - l0;
-        uint32_t hits = __ballot_sync(0xffffffffu, at >= 0 && at < 32);
+        const bool hits = __any_sync(0xffffffffu, at >= 0 && at < 32);
         float2 r[8];                              // of the lane's columns: -lse / log 2, factor
         bool some = false;                        // a token that is ignored among them
 #pragma unroll
@@ -331,15 +346,23 @@ struct Sink<6 /* kGrLossGrad */> {
                 const int b = 4 * (j >> 1) + 2 * (q & 1) + (j & 1);
                 d[q >> 1][b] = ex2(fmaf(__uint_as_float(v[q >> 1][b]), kLog2e, r[j].x));
             }
-        while (hits) {                            // the targets among these classes
-            const int32_t c = __ffs(hits) - 1;
-            hits &= hits - 1;
-            const int32_t q = __shfl_sync(0xffffffffu, static_cast<int32_t>(at), c);
-            const bool own = (lane & 3) == ((c & 7) >> 1) && lane >> 2 == (q & 7);
-            const int32_t want = own ? 16 * (q >> 4) + 4 * (c >> 3) + 2 * (q >> 3 & 1) + (c & 1) : -1;
+        if (hits) {                               // targets among these classes: all at once
+            const int32_t own = at >= 0 && at < 32 ? static_cast<int32_t>(at) : -1;
+            const float own_lse = lane < rows ? __ldg(k.lse + row + lane) : 0.0f;
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (i == want) d[i >> 4][i & 15] -= 1.0f;
+            for (int j = 0; j < 8; ++j) {
+                const int32_t col = 8 * (j >> 1) + 2 * (lane & 3) + (j & 1);
+                const int32_t m = __shfl_sync(0xffffffffu, own, col) - (lane >> 2);       // 8 q: the lane's class q
+                const float lse = __shfl_sync(0xffffffffu, own_lse, col);
+                float z = 0.0f;
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (m == 8 * q) z = __uint_as_float(v[q >> 1][4 * (j >> 1) + 2 * (q & 1) + (j & 1)]);
+                const float left = exp_less_one(z - lse);
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (m == 8 * q) d[q >> 1][4 * (j >> 1) + 2 * (q & 1) + (j & 1)] = left;
+            }
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j)
@@ -366,6 +389,9 @@ struct Sink<6 /* kGrLossGrad */> {
             store.template step<false, false>(bits, out, rows, nullptr);
     }
 };
+
+template <>
+struct Sink<11 /* kGrLossGradLong */> : Sink<6> {};
 
 // ------------------------------------------------------------------ sums in parts
 // A token gradient's sum may be cut twice.  Pieces of the vocabulary are launches: the

@@ -22,7 +22,7 @@ struct GroupedParams;
 
 namespace __attribute__((visibility("hidden"))) tn_host {
 
-constexpr int kGroupedOps = 11;                          // tn::GroupedOp
+constexpr int kGroupedOps = 12;                          // tn::GroupedOp
 constexpr int64_t kMaxDim = (int64_t(1) << 31) - 256;   // TMA coordinates are signed 32-bit
 
 gemm_status_t fail(gemm_status_t s, const char *fmt, ...);

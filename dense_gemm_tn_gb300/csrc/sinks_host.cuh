@@ -579,9 +579,12 @@ gemm_status_t run_loss_grad(int type, int64_t M, int64_t N, int64_t K, const voi
         tn::GroupedParams prm = sink_params(c, padded, K, d, ldd);
         prm.sink.targets = targets;
         prm.sink.rows = rows;
+        prm.sink.lse = lse;
         prm.sink.first = static_cast<int32_t>(first);
         prm.sink.classes = static_cast<int32_t>(classes);
-        st = launch_grouped_op<tn::kGrLossGrad>(c, *dev, prm, x, o.y, o.ldx, 0, o.ldy, o.in_x, o.in_y);
+        st = K > tn::kGrSegment * tn::kGrBlock
+                 ? launch_grouped_op<tn::kGrLossGradLong>(c, *dev, prm, x, o.y, o.ldx, 0, o.ldy, o.in_x, o.in_y)
+                 : launch_grouped_op<tn::kGrLossGrad>(c, *dev, prm, x, o.y, o.ldx, 0, o.ldy, o.in_x, o.in_y);
         if (st == GEMM_OK && dB)
             st = launch_token_grad(c, *dev, plan.cut, x, o.ldx, o.in_x, d, ldd, classes, dB, lddb, scale, sum, i, plan.pieces);
         if (st == GEMM_OK && dA) {
