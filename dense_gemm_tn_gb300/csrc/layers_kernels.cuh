@@ -62,10 +62,11 @@ __global__ void __launch_bounds__(kJoinThreads) cross_entropy_join_kernel(const 
         }
     }
     if (slice == 0 && n < p.N) {
-        const float lse = m + logf(s);
-        p.lse[n] = lse;
+        const float above = logf(s);
+        p.lse[n] = m + above;
+        // (not lse less the logit: where the target is the maximum the lse's rounding is no part of the loss)
         const int64_t t = p.targets[n];
-        p.loss[n] = t < 0 ? 0.0f : t < p.classes ? lse - p.z_target[n] : __int_as_float(0x7fffffff);
+        p.loss[n] = t < 0 ? 0.0f : t < p.classes ? (m - p.z_target[n]) + above : __int_as_float(0x7fffffff);
     }
 }
 

@@ -112,3 +112,19 @@ def test_long_sums_repeat_and_share_their_segments(N, M, K, dtype):
     d *= torch.where(targets < 0, 0.0, dloss.double())[:, None]
     for got, want in ((dA, d.t() @ Bt.double()), (dB, d @ A.double())):
         assert float((got.double() - want).norm()) <= 1.5 * HALF_STEP[dtype] * float(want.norm()) + 1e-12
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("N,M,K", [(40, 3000, 512), (300, 2000, 1024), (1000, 3000, 64), (257, 40000, 136)])
+def test_small_losses(N, M, K, dtype):
+    """Losses of 1e-4 to 1e-2 where the lse is near 30: log(1 + rest), which the lse's rounding is no part of.  Off are the sum of
+    exponentials (2^-19, as in lse_error), the logarithm, and the rest by its logits' differences, each logit by a few steps of the
+    tensor cores' sum: K / 16 of 17 2^-24 of its terms' sizes, at most 60."""
+    A, Bt, targets = confident(N, M, K, dtype, 14.0, 15.0)
+    loss, lse = tn.tn_cross_entropy(A, Bt, targets)
+    tn.gemm_poll_device_status()
+    Z = Bt.double() @ A.double().t()
+    want = -torch.log_softmax(Z, 1)[torch.arange(N, device="cuda"), targets]
+    logits = (min(K, 1024) + 15) // 16 * 17 * 2.0 ** -24 * 60 * 2
+    assert bool(((loss.double() - want).abs() <= 2.0 ** -19 + want * (logits + 2.0 ** -20)).all())
+    assert float((loss.double() - want).norm() / want.norm()) < 1e-3
