@@ -10,6 +10,7 @@
 #include <atomic>
 #include <cstdint>
 #include <cstring>
+#include <initializer_list>
 #include <memory>
 #include <mutex>
 #include <unordered_map>
@@ -132,6 +133,69 @@ gemm_status_t launch_grad_a(const GroupedCall &c, DeviceState &dev, tn::GroupedP
 cudaError_t take_layers_status(int *value);
 
 inline bool aligned_to(const void *p, uintptr_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+
+// What a call reads or writes: `blocks` matrices of rows of `width` bytes, `pitch` bytes apart, the
+// matrices `stride` apart.  NULL, or no bytes: nothing.
+struct Span {
+    const void *base;
+    int64_t blocks, stride, rows, pitch, width;
+
+    Span(const void *p, int64_t bytes) : Span(p, 1, 0, 1, 0, bytes) {}
+    Span(const void *p, int64_t blocks_, int64_t stride_, int64_t rows_, int64_t pitch_, int64_t width_)
+        : base(p), blocks(blocks_), stride(stride_), rows(rows_), pitch(pitch_), width(width_)
+    {
+        if (!p || blocks_ < 1 || rows_ < 1 || width_ < 1) blocks = 0;
+        constexpr int64_t kMost = int64_t(1) << 56;          // (no address space holds more)
+        if (pitch > 0 && rows > kMost / pitch) rows = kMost / pitch;
+        if (blocks > 1 && stride == rows * pitch) rows *= blocks, blocks = 1;     // one after another
+    }
+    uintptr_t lo() const { return reinterpret_cast<uintptr_t>(base); }
+    uintptr_t hi() const { return lo() + (blocks - 1) * stride + (rows - 1) * pitch + width; }
+    bool dense() const { return blocks == 1 && (rows == 1 || pitch == width); }
+    Span block(int64_t i) const { return Span(static_cast<const char *>(base) + i * stride, 1, 0, rows, pitch, width); }
+};
+
+// Whether some row of x (one matrix) meets the bytes [lo, hi).
+inline bool rows_meet(const Span &x, uintptr_t lo, uintptr_t hi)
+{
+    if (x.hi() <= lo || hi <= x.lo()) return false;
+    const int64_t first = lo < x.lo() + x.width || x.pitch == 0 ? 0 : static_cast<int64_t>((lo - x.lo() - x.width) / x.pitch + 1);
+    return first < x.rows && x.lo() + first * x.pitch < hi;
+}
+
+// Whether a and b share a byte.  Two sets of rows with gaps of different pitches are not told
+// apart: taken as sharing none.
+inline bool share_bytes(const Span &a, const Span &b)
+{
+    if (a.blocks == 0 || b.blocks == 0 || a.hi() <= b.lo() || b.hi() <= a.lo()) return false;
+    if (a.blocks > 1 && b.blocks > 1 && a.stride == b.stride) {
+        for (int64_t i = 1 - a.blocks; i < b.blocks; ++i)    // (blocks as far apart meet alike)
+            if (share_bytes(a.block(0), b.block(i))) return true;
+        return false;
+    }
+    if (a.blocks > 1 || b.blocks > 1) {
+        for (int64_t i = 0; i < a.blocks; ++i)
+            for (int64_t j = 0; j < b.blocks; ++j)
+                if (share_bytes(a.block(i), b.block(j))) return true;
+        return false;
+    }
+    if (a.dense()) return rows_meet(b, a.lo(), a.hi());
+    if (b.dense()) return rows_meet(a, b.lo(), b.hi());
+    if (a.pitch != b.pitch) return false;
+    // both repeat alike, and their hulls meet: their columns do, or they lie side by side
+    const int64_t off = static_cast<int64_t>((b.lo() - a.lo()) % static_cast<uintptr_t>(a.pitch));
+    const int64_t from = a.lo() <= b.lo() ? off : (a.pitch - static_cast<int64_t>((a.lo() - b.lo()) % a.pitch)) % a.pitch;
+    return from < a.width || from + b.width > a.pitch;
+}
+
+// Refuses a call that writes `written` where one of the others is.
+inline gemm_status_t check_apart(const char *name, const char *what, const Span &written, std::initializer_list<Span> others)
+{
+    for (const Span &o : others)
+        if (share_bytes(written, o))
+            return fail(GEMM_ERR_INVALID_ARG, "%s: %s overlaps what the call reads, another result or the workspace", name, what);
+    return GEMM_OK;
+}
 
 // A launch that may begin its setup before the kernel before it has ended.
 template <typename... Args>

@@ -247,6 +247,12 @@ gemm_status_t run_gated(int type, int act, int64_t E, int64_t M, int64_t K, int6
     const GatedPlan plan = gated_plan(false, !offsets, E, M, K, T, A, lda, stride_a, B, ldb);
     if (!plan.fits) return fail(GEMM_ERR_UNSUPPORTED, "%s: the operands' copies are too large", name);
     if ((st = check_workspace(name, workspace, workspace_bytes, plan.bytes, "gemm_gated_workspace")) != GEMM_OK) return st;
+    const Span sA(A, E, stride_a * 2, 2 * M, lda * 2, K * 2), sB(B, 1, 0, T, ldb * 2, K * 2);
+    const Span sO(offsets, (E + 1) * 4), sW(workspace, static_cast<int64_t>(plan.bytes)), sH(H, 1, 0, T, ldh * 2, M * 2);
+    const Span sP(P, 1, 0, T, ldp * 4, 2 * M * 4);
+    if ((st = check_apart(name, "H", sH, {sA, sB, sO, sP, sW})) != GEMM_OK) return st;
+    if ((st = check_apart(name, "P", sP, {sA, sB, sO, sW})) != GEMM_OK) return st;
+    if ((st = check_apart(name, "the workspace", sW, {sA, sB, sO})) != GEMM_OK) return st;
     DeviceState *dev = nullptr;
     if ((st = device_state(&dev, nullptr)) != GEMM_OK) return st;
     if (K > 0 && T <= kGatedFewRows && !plan.g.x.copy && !plan.g.y.copy && gated_few_ctas(!offsets, E, M, T) <= 2 * dev->sms) {
@@ -336,6 +342,18 @@ gemm_status_t run_gated_grad(int type, int act, int64_t E, int64_t M, int64_t K,
     GatedPlan plan = gated_plan(true, !offsets, E, M, K, T, A, lda, stride_a, B, ldb);
     if (!plan.fits) return fail(GEMM_ERR_UNSUPPORTED, "%s: the operands' copies are too large", name);
     if ((st = check_workspace(name, workspace, workspace_bytes, plan.bytes, "gemm_gated_workspace")) != GEMM_OK) return st;
+    if (!idle) {
+        // (P and dH are read before a gradient is written, and A, for dB, before dA is)
+        const Span sA(A, E, stride_a * 2, 2 * M, lda * 2, K * 2), sB(B, 1, 0, T, ldb * 2, K * 2), sO(offsets, (E + 1) * 4);
+        const Span sdA(dA, E, stride_da * 2, 2 * M, ldda * 2, K * 2), sdB(dB, 1, 0, T, lddb * 2, K * 2), none(nullptr, 0);
+        const Span sW(workspace, static_cast<int64_t>(plan.bytes));
+        const bool in_place = dA == A && ldda == lda && (E == 1 || stride_da == stride_a);
+        if ((st = check_apart(name, "dA", sdA, {dB && !in_place ? sA : none, sB, sO, sdB, sW})) != GEMM_OK) return st;
+        if ((st = check_apart(name, "dB", sdB, {sA, dA ? sB : none, sO, sW})) != GEMM_OK) return st;
+        if ((st = check_apart(name, "the workspace", sW, {dB ? sA : none, dA ? sB : none, sO, Span(P, 1, 0, T, ldp * 4, 2 * M * 4),
+                                                          Span(dH, 1, 0, T, lddh * 2, M * 2)})) != GEMM_OK)
+            return st;
+    }
     DeviceState *dev = nullptr;
     if ((st = device_state(&dev, nullptr)) != GEMM_OK) return st;
 
@@ -495,6 +513,12 @@ gemm_status_t run_loss(int type, int64_t M, int64_t N, int64_t K, const void *A,
     if (!plan.fits) return fail(GEMM_ERR_UNSUPPORTED, "%s: the workspace would be too large", name);
     if ((st = check_workspace(name, workspace, workspace_bytes, plan.bytes, "gemm_cross_entropy_workspace")) != GEMM_OK)
         return st;
+    // (A and B are read before a result is written)
+    const Span sT(targets, N * 8), sL(loss, N * 4), sE(lse, N * 4), sW(workspace, static_cast<int64_t>(plan.bytes));
+    if ((st = check_apart(name, "the loss", sL, {sT, sE, sW})) != GEMM_OK) return st;
+    if ((st = check_apart(name, "lse", sE, {sT, sW})) != GEMM_OK) return st;
+    if ((st = check_apart(name, "the workspace", sW, {sT, Span(A, 1, 0, M, lda * 2, K * 2), Span(B, 1, 0, N, ldb * 2, K * 2)})) != GEMM_OK)
+        return st;
     DeviceState *dev = nullptr;
     if ((st = device_state(&dev, nullptr)) != GEMM_OK) return st;
 
@@ -545,6 +569,15 @@ gemm_status_t run_loss_grad(int type, int64_t M, int64_t N, int64_t K, const voi
     if (!plan.fits) return fail(GEMM_ERR_UNSUPPORTED, "%s: the workspace would be too large", name);
     if ((st = check_workspace(name, workspace, workspace_bytes, plan.bytes, "gemm_cross_entropy_workspace")) != GEMM_OK)
         return st;
+    if (N > 0) {
+        // (a piece's classes are read before their rows of dA are written, and B for the logits before dB is)
+        const Span sA(A, 1, 0, M, lda * 2, K * 2), sB(B, 1, 0, N, ldb * 2, K * 2), sT(targets, N * 8), sE(lse, N * 4), sD(dloss, N * 4);
+        const Span sdA(dA, 1, 0, M, ldda * 2, K * 2), sdB(dB, 1, 0, N, lddb * 2, K * 2), none(nullptr, 0);
+        const Span sW(workspace, static_cast<int64_t>(plan.bytes));
+        if ((st = check_apart(name, "dA", sdA, {dA == A && ldda == lda ? none : sA, sB, sT, sE, sD, sdB, sW})) != GEMM_OK) return st;
+        if ((st = check_apart(name, "dB", sdB, {sA, dA ? sB : none, sT, sE, sD, sW})) != GEMM_OK) return st;
+        if ((st = check_apart(name, "the workspace", sW, {sA, sB, sT, sE, sD})) != GEMM_OK) return st;
+    }
     DeviceState *dev = nullptr;
     if ((st = device_state(&dev, nullptr)) != GEMM_OK) return st;
     auto call = [&](int64_t classes) {

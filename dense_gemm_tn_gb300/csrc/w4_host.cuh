@@ -114,8 +114,12 @@ gemm_status_t run_w4(int type, int64_t M, int64_t N, int64_t K, const void *A, i
         if (!aligned_to(scale, 2) || !aligned_to(B, 2))
             return fail(GEMM_ERR_INVALID_ARG, "%s: an operand is not aligned to its element size", name);
     }
+    gemm_status_t st = check_apart(name, "C", Span(C, 1, 0, N, ldc * 2, M * 2),
+                                   {Span(A, 1, 0, M, lda, bytes), Span(scale, 1, 0, M, lds * 2, groups * 2),
+                                    Span(B, 1, 0, N, ldb * 2, K * 2)});
+    if (st != GEMM_OK) return st;
     DeviceState *dev = nullptr;
-    gemm_status_t st = device_state(&dev, nullptr);
+    st = device_state(&dev, nullptr);
     if (st != GEMM_OK) return st;
     w4::ProductParams p;
     memset(&p, 0, sizeof(p));
@@ -161,8 +165,13 @@ gemm_status_t run_quant_w4(const void *x, int x_type, int64_t rows, int64_t cols
     const int64_t esz = x_type == w4::kF32 ? 4 : 2;
     if (!aligned_to(x, esz)) return fail(GEMM_ERR_INVALID_ARG, "%s: x is not aligned to its element size", name);
     if (!aligned_to(scale, 2)) return fail(GEMM_ERR_INVALID_ARG, "%s: scale is not 2-byte aligned", name);
+    const Span sX(x, 1, 0, rows, ldx * esz, cols * esz), sQ(q, 1, 0, rows, ldq, (cols + 1) / 2);
+    const Span sS(scale, 1, 0, rows, lds * 2, (cols + group - 1) / group * 2);
+    gemm_status_t st = check_apart(name, "q", sQ, {sX, sS});
+    if (st == GEMM_OK) st = check_apart(name, "scale", sS, {sX});
+    if (st != GEMM_OK) return st;
     DeviceState *dev = nullptr;
-    gemm_status_t st = device_state(&dev, nullptr);
+    st = device_state(&dev, nullptr);
     if (st != GEMM_OK) return st;
     w4::QuantParams p;
     memset(&p, 0, sizeof(p));

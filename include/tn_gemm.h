@@ -398,8 +398,13 @@ gemm_status_t gemm_quantize_i8_rows(const void *x, int x_type, int64_t rows, int
  * sums of dB (64 K T bytes).
  * Ownership and alignment as for gemm_tn_grouped.
  *
+ * H, P, dA, dB and the workspace share no byte with one another or with what the call
+ * reads, except: dA and dB may lie in P and dH, which are read first; dA may be A itself; and
+ * dB may lie in B where dA is NULL.  Such calls are refused.  (Of two operands both of whose
+ * rows have gaps, of different pitches, the call cannot tell: it does not refuse them.)
+ *
  * Errors: as for gemm_tn_grouped, and GEMM_ERR_INVALID_ARG for an unknown
- * activation, or offsets NULL with E != 1.
+ * activation, offsets NULL with E != 1, or results that overlap as above.
  */
 typedef enum {
     GEMM_ACT_SILU = 0,       /* x / (1 + exp(-x)) */
@@ -455,7 +460,12 @@ gemm_status_t gemm_tn_gated_grad(int type, int act, int64_t E, int64_t M, int64_
  * less) + up to 64 N K, and copies of operands that the TMA cannot read in place (as for
  * gemm_tn_grouped).  Ownership and alignment as there.
  *
- * Errors: GEMM_ERR_INVALID_ARG for an unknown type, a negative size, M == 0 with
+ * loss, lse, dA, dB and the workspace share no byte with one another, with targets or, in
+ * the gradient, with lse and dloss; dA none with A (unless it is A itself) and B, dB none
+ * with A, nor with B unless dA is NULL; the workspace none with A and B.  Such calls are
+ * refused, as far as gemm_tn_gated's.
+ *
+ * Errors: GEMM_ERR_INVALID_ARG for such an overlap, an unknown type, a negative size, M == 0 with
  * N > 0, a leading dimension below its row's length, NULL or misaligned pointers
  * with work to do (targets: 8 bytes), or a workspace that is too small;
  * GEMM_ERR_UNSUPPORTED and GEMM_ERR_CUDA as for gemm_tn_grouped.
@@ -501,7 +511,10 @@ gemm_status_t gemm_tn_cross_entropy_grad(int type, int64_t M, int64_t N, int64_t
  * NaN, or whose scale is beyond the type, has scale NaN and codes 0.  The unused half
  * of an odd row's last byte is 0.  rows == 0 or cols == 0 writes nothing.  One launch.
  *
- * Errors of both: GEMM_ERR_INVALID_ARG for an unknown type or group, a negative size,
+ * C, q and scale share no byte with what the call reads, nor q with scale; such calls are
+ * refused, as far as gemm_tn_gated's.
+ *
+ * Errors of both: GEMM_ERR_INVALID_ARG for such an overlap, an unknown type or group, a negative size,
  * a leading dimension below its row's length, or NULL or misaligned pointers with work
  * to do (codes need no alignment; rows on 16-byte boundaries are fastest);
  * GEMM_ERR_UNSUPPORTED off sm_103 or for sizes beyond 2^31 - 256 (the quantiser: 2^40
