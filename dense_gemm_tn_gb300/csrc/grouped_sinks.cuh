@@ -56,13 +56,15 @@ __device__ __forceinline__ float exp_less_one(float x)
     return fabsf(x) < 0.25f ? x * y : ex2(x * kLog2e) - 1.0f;
 }
 
-// 1 / (1 + exp(-x)) (relative error about 2^-21).  exp overflows to an infinity
-// below -88, where the quotient is 0.
+// 1 / (1 + exp(-x)) (relative error about 2^-21 and |x| 2^-23, the argument's rounding).  Beyond
+// exp(-x) = 2^126 the quotient, less than FP32's smallest normal number, is 0.
 __device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.0f, 1.0f + ex2(-x * kLog2e)); }
 
 // The normal distribution function, erfc(-x / sqrt 2) / 2: for x < 0 t q(t) exp(-x^2 / 2) with t =
 // 1 / (1 + 0.3 |x|) (the form of Hastings' approximations, 1955; q's coefficients fitted here
-// for the least largest relative error, 1.7e-7), for x > 0 what that leaves of 1.  Shorter than
+// for the least largest relative error, 1.7e-7), for x > 0 what that leaves of 1.  In FP32 x^2 is rounded before
+// the exponential, which adds up to x^2 2^-25: 1.3e-6 in all at -5, 7e-6 at -13, where the function is 6e-39.  The results
+// have 16 bits, half a step of 2^-9 or 2^-12, so that is a hundredth of one at most.  Shorter than
 // erfcf: 3001 gated rows over 8 experts of 1024 x 2048 31.1 -> 27.4 us, their gradient 69.9 -> 66.0.
 __device__ __forceinline__ float normal_below(float x)
 {
