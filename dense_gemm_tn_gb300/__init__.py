@@ -673,6 +673,12 @@ def _workspace(device, stream, n):
         return torch.empty(n, dtype=torch.uint8, device=device)
 
 
+#: Bytes that a workspace with tensor maps goes on for behind what the call needs.  A call whose maps lay in the last
+#: 53 KiB before unmapped memory failed with an illegal address on a GB300, twice in the same place, and no access of the
+#: kernels leads there; with the same maps further from the end it never has.
+_BEHIND_MAPS = 1 << 16
+
+
 def _tensors(torch, *operands):
     for t in operands:
         if not isinstance(t, torch.Tensor):
@@ -791,7 +797,7 @@ def tn_grouped_grad_a(dCt, Bt, offsets, dA=None, stream=None):
         _same_device(device, dA=dA)
     d, b = dCt.data_ptr(), Bt.data_ptr()
     n = calls.gemm_grouped_workspace(GEMM_GROUPED_GRAD_A, E, M, K, T, d, ldd, 0, b, ldb)
-    held = _workspace(device, stream, n) if n > 0 else None
+    held = _workspace(device, stream, n + _BEHIND_MAPS) if n > 0 else None
     ws = held.data_ptr() if n > 0 else None
     _check(calls.gemm_tn_grouped_grad_a(kind, E, M, K, T, d, ldd, b, ldb, offsets.data_ptr(), dA.data_ptr(), ldda,
                                         stride_da, ws, n, _launch_stream(device.index, stream)))
@@ -997,7 +1003,7 @@ def tn_gated_grad(A, Bt, P, dHt, offsets=None, act="silu", dA=None, dBt=None, wa
         dBt, lddb = _result(dBt, (T, K), dtype, device, stream, "dBt")
     a, b = A.data_ptr(), Bt.data_ptr()
     n = calls.gemm_gated_workspace(1, offsets is None, E, M, K, T, a, lda, stride_a, b, ldb)
-    held = _workspace(device, stream, n) if n > 0 else None
+    held = _workspace(device, stream, n if offsets is None else n + _BEHIND_MAPS) if n > 0 else None
     _check(calls.gemm_tn_gated_grad(half, kind, E, M, K, T, a, lda, stride_a, b, ldb, _ptr(offsets), P.data_ptr(), ldp,
                                     dHt.data_ptr(), lddh, dA.data_ptr() if want_a else None, ldda, stride_da,
                                     dBt.data_ptr() if want_b else None, lddb, held.data_ptr() if n > 0 else None, n,

@@ -275,7 +275,9 @@ gemm_status_t gemm_f16_tn_noalloc(int64_t M, int64_t N, int64_t K,
  * the workspace (256-byte aligned); it may be used again, or freed in stream
  * order, once the call's kernels have run.  These calls keep no buffer of the
  * library's: calls and captured graphs that overlap need workspaces of their
- * own and nothing else.
+ * own and nothing else.  A workspace with tensor maps (grad_a's, and by expert that of
+ * gemm_tn_gated_grad) is best followed by 64 KiB of mapped memory: on a GB300 a call
+ * whose maps lay nearer to unmapped memory was seen to fail with an illegal address.
  *
  * Errors: GEMM_ERR_INVALID_ARG for an unknown type, a negative size or stride,
  * a leading dimension below its row's length, overlapping dA_e, NULL or
