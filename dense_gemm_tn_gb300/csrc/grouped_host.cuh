@@ -215,7 +215,8 @@ int grouped_split(const void *kernel, int threads, int smem, int64_t tiles, int6
 // tokens over 32003 classes of 1024 (8 tiles) 217.7 / 123.3 us in 4 (in 2 154.1, in 8 124.8), 300 over 32000
 // of 2048 181.4 / 103.8; 4096 over 8192 of 4096 316.9 / 311.4 in one part of other rows (in 2
 // 339.5).  Rows alone, the loss of 1021 over 32003: tiles of 256 57.2 us, as the rule says 57.1, of 192
-// 63.6.  (The rule is the workspace query's too, so it asks no device: 152 SMs.)
+// 63.6.  (The rule is the workspace query's too, so it asks no device: 152 SMs, a GB300's.  On another
+// count results are right, and the last wave is not as full as planned.)
 static_assert(kGroupedOps == tn::kGrOps, "every operation has its slots");
 
 struct ProductCut {

@@ -111,7 +111,7 @@ struct Sink;
 // the products need not go to memory.  On GB300 the activation hides behind the next tile's
 // products: 3001 rows over 8 experts of 1024 x 2048 take 26.1 us with silu, 26.6 with gelu_tanh
 // and 27.4 with gelu (the plain product of as many rows 25.7); the products' 25 MB in FP32 cost 4
-// more.  4096 tokens over 14336 x 4096: 549 us, 0.91 of the
+// more.  4096 tokens over 14336 x 4096: 546 to 570 us on different boxes, 0.91 to 0.87 of the
 // measured burst rate.
 template <>
 struct Sink<4 /* kGrGated */> {
@@ -320,7 +320,7 @@ struct Sink<5 /* kGrLossStats */> {
 // fp16 times 2^13, see cross_entropy_rows_kernel; d then keeps its relative precision
 // down to 2^-27 of it.)  Classes past the piece's end are zeros: the
 // products over the piece read them.  A piece of 16384 classes of 4096 for 4096 tokens
-// takes 306 us on GB300, 0.93 of the measured burst rate.
+// takes 336 us on GB300, 0.85 of the measured burst rate (306 as one sum a logit).
 template <>
 struct Sink<6 /* kGrLossGrad */> {
     template <class Params, class Store>

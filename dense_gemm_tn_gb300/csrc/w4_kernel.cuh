@@ -88,6 +88,7 @@ __device__ __forceinline__ uint4 load_words(const uint8_t *p)
 }
 
 // The eight codes of a word as four pairs of 16-bit floats: (0, 4), (1, 5), (2, 6), (3, 7).
+// (Integers widened by their place in a half's mantissa: Kim, Henry, Fahim and Awadalla, 2022.)
 // A code's four bits, the top one flipped, are q + 8 in the low bits of 1024 (fp16)
 // or 128 (bf16), whose steps are 1 there.  fp16 has room for them four bits further up
 // as well, as 1024 + 16 (q + 8), which a sixteenth of takes back exactly; bf16 takes a
